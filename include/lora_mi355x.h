@@ -651,6 +651,46 @@ int lora_fused_linear_e4m3(void *stream, const void *x, int64_t ldx, int32_t d_i
                            const lora_segments *seg, void *y, int64_t ldy,
                            void *ws, size_t ws_bytes);
 
+/* ------------------------------------------------------------------ gradients
+ * Training the adapters of many requests at once: the gradients of lora_sgmv's
+ * correction y[t] += s_i (x[t] A_i^T) B_i^T (s_i = alpha_i / r_i, i = a(t), A_i
+ * and B_i as stored), for dy = dL/dy, over the same segments.  With
+ *     u[t] = s_i dy[t] B_i  and  v[t] = s_i x[t] A_i^T    ([r_i] each)
+ * the call computes
+ *     dx[t] += u[t] A_i                        (accumulates, as y does in lora_sgmv)
+ *     dA_i   = sum over t with a(t) = i of u[t]^T x[t]     [r_i, d_in]
+ *     dB_i   = sum over t with a(t) = i of dy[t]^T v[t]    [d_out, r_i]
+ *   x, dy            the forward's input and the gradient of its output, of the
+ *                    call's dtype, any row pitch; 16-byte aligned rows of whole
+ *                    16-byte pieces take the fast loads
+ *   grad_A_dev,      device tables [n_adapters] of fp32 gradient addresses
+ *   grad_B_dev       (4-byte aligned; A's gradient contiguous [r_i, d_in], B's
+ *                    [d_out, r_i]); an entry of 0 leaves that gradient out, a
+ *                    NULL table all of its kind.  The gradients of adapters
+ *                    without a token in the batch are left as they were.  Two
+ *                    adapters of a batch must not share a gradient's memory.
+ *   flags            0: gradients are overwritten; LORA_GRAD_ACCUMULATE: added to
+ *   dx               NULL: not wanted.  Rows of tokens without an adapter are
+ *                    left as they were.  dx must not overlap x or dy.
+ *   x may be NULL when both tables are (only dx is wanted).
+ * Precision: u and v are fp32 sums of the dtype's products; bf16 calls feed them
+ * to the second products as bf16 parts (three for dA and dB, 24 significant
+ * bits; two for dx, 16 bits), with fp32 accumulation; dx is rounded once.
+ * Every sum has a fixed order: results are the same from run to run.
+ * Needs ws_bytes >= lora_workspace_bytes(LORA_OP_SGMV_BACKWARD, T, d_in, d_out,
+ * max_rank), T and max_rank as in lora_sgmv; the workspace needs no preparation.
+ * Two to four launches; capturable; calls that share a workspace must be ordered
+ * on one stream.
+ * Errors: LORA_ERR_ARG, LORA_ERR_DTYPE, LORA_ERR_ALIGN, LORA_ERR_PLAN,
+ * LORA_ERR_ADAPTER_ID (the segments use an adapter >= n_adapters),
+ * LORA_ERR_WORKSPACE, LORA_ERR_HIP. */
+#define LORA_GRAD_ACCUMULATE 1u
+
+int lora_sgmv_backward(void *stream, int dtype, const void *x, int64_t ldx, int32_t d_in, const void *dy,
+                       int64_t lddy, int32_t d_out, const lora_segments *seg, const uint64_t *grad_A_dev,
+                       const uint64_t *grad_B_dev, int32_t n_adapters, unsigned flags, void *dx, int64_t lddx,
+                       void *ws, size_t ws_bytes);
+
 /* ------------------------------------------------------------------ helpers */
 enum {
     LORA_OP_SGMV_SHRINK = 0,
@@ -659,7 +699,8 @@ enum {
     LORA_OP_BGMV_EXPAND = 3,
     LORA_OP_FUSED = 4,
     LORA_OP_SGMV = 5,
-    LORA_OP_BGMV = 6
+    LORA_OP_BGMV = 6,
+    LORA_OP_SGMV_BACKWARD = 7
 };
 
 /* Workspace bytes an op needs (0 = none; ws may then be NULL); -1 cast to

@@ -11,6 +11,7 @@ from .binding import (  # noqa: F401
     LORA_BF16,
     LORA_F32,
     DevicePool,
+    GradPool,
     LoraError,
     Plan,
     bgmv,
@@ -20,6 +21,7 @@ from .binding import (  # noqa: F401
     lib_path,
     load,
     sgmv,
+    sgmv_backward,
     sgmv_expand,
     sgmv_shrink,
     to_device,

@@ -29,6 +29,9 @@ LORA_OP_BGMV_EXPAND = 3
 LORA_OP_FUSED = 4
 LORA_OP_SGMV = 5
 LORA_OP_BGMV = 6
+LORA_OP_SGMV_BACKWARD = 7
+
+LORA_GRAD_ACCUMULATE = 1
 
 STATUS = {
     0: "LORA_OK", -1: "LORA_ERR_ARG", -2: "LORA_ERR_RANK", -3: "LORA_ERR_ADAPTER_ID",
@@ -48,6 +51,7 @@ EXPORTS = [
     "lora_page_alloc_give", "lora_page_alloc_free_count", "lora_pages_write", "lora_sgmv_paged", "lora_bgmv_paged",
     "lora_sgmv_grouped", "lora_sgmv_grouped_workspace_bytes", "lora_probe_empty", "lora_probe_stream",
     "lora_probe_chase", "lora_workspace_clear", "lora_debug_wait_limit", "lora_bgmv_noalloc",
+    "lora_sgmv_backward",
 ]
 LORA_CACHE_DRY = 1
 MAX_PROJ = 8
@@ -110,6 +114,8 @@ _SIGS = {
     "lora_debug_wait_limit": (ctypes.c_int, [_i32]),
     "lora_bgmv_noalloc": (ctypes.c_int, [_vp, ctypes.c_int, _i32, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _i32,
                                          _i32, _vp, _i64, _i32]),
+    "lora_sgmv_backward": (ctypes.c_int, [_vp, ctypes.c_int, _vp, _i64, _i32, _vp, _i64, _i32, _vp, _vp, _vp, _i32,
+                                          ctypes.c_uint, _vp, _i64, _vp, _sz]),
     "lora_probe_stream": (ctypes.c_int, [_vp, _vp, _i64, _vp, _i64, _vp, _i32]),
     "lora_probe_chase": (ctypes.c_int, [_vp, _vp, _i32, _vp]),
     "lora_page_alloc_create": (ctypes.c_int, [_i32, _vp]),
@@ -669,6 +675,54 @@ class PagedPool:
         return p
 
 
+@dataclass
+class GradPool:
+    """fp32 gradients of adapters: dA_i [r_i, d_in] and dB_i [d_out, r_i],
+    contiguous, reached through device tables of their addresses (0 = not
+    wanted)."""
+
+    storage: object  # the tensors that hold the gradients
+    A: list  # per adapter: a tensor of r_i * d_in fp32, or None
+    B: list
+    addr_A_dev: object
+    addr_B_dev: object
+
+    @property
+    def n_adapters(self) -> int:
+        return len(self.A)
+
+    @classmethod
+    def from_tensors(cls, A, B, device=None) -> "GradPool":
+        """A, B: one contiguous fp32 device tensor (or None) for each adapter."""
+        torch = _torch()
+        if len(A) != len(B):
+            raise ValueError("A and B list different numbers of adapters")
+        for t in (*A, *B):
+            if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or not t.is_cuda):
+                raise ValueError("gradients are contiguous fp32 device tensors")
+        device = device or next((t.device for t in (*A, *B) if t is not None), "cuda")
+
+        def table(ts):
+            a = np.array([0 if t is None else t.data_ptr() for t in ts], dtype=np.uint64)
+            return torch.from_numpy(a.view(np.int64)).to(device)
+
+        return cls(storage=None, A=list(A), B=list(B), addr_A_dev=table(A), addr_B_dev=table(B))
+
+    @classmethod
+    def like(cls, pool, device="cuda") -> "GradPool":
+        """Zero gradients for every adapter of a pool, in one buffer, 16-byte aligned."""
+        torch = _torch()
+        sizes = [int(r) * d for r in pool.rank for d in (pool.d_in, pool.d_out)]
+        starts = np.concatenate([[0], np.cumsum([(s + 3) // 4 * 4 for s in sizes])]).astype(np.int64)
+        storage = torch.zeros(max(int(starts[-1]), 4), device=device)
+        parts = [storage[int(o): int(o) + s] for o, s in zip(starts, sizes)]
+        A = [t.view(int(r), pool.d_in) for t, r in zip(parts[0::2], pool.rank)]
+        B = [t.view(pool.d_out, int(r)) for t, r in zip(parts[1::2], pool.rank)]
+        g = cls.from_tensors(A, B, device=device)
+        g.storage = storage
+        return g
+
+
 SEG_DESC = np.dtype([("A", "<u8"), ("B", "<u8"), ("start", "<i4"), ("len", "<i4"), ("rank", "<i4"),
                      ("adapter", "<i4"), ("scale", "<f4"), ("blk0", "<i4")])
 BLK_DESC = np.dtype([("A", "<u8"), ("B", "<u8"), ("scale", "<f4"), ("rank", "<i4"), ("n", "<i4"), ("p0", "<i4"),
@@ -997,6 +1051,21 @@ def fused_linear_e4m3(x, W0, w0_scale: float, plan: Plan, y, ws, stream=None):
                                   float(w0_scale), W0.shape[0], plan.seg, _ptr(y), y.stride(0),
                                   _ptr(ws), ws.numel() * ws.element_size()),
            "lora_fused_linear_e4m3")
+
+
+def sgmv_backward(x, dy, plan: Plan, grads: Optional[GradPool], dx, ws, dtype: str, accumulate: bool = False,
+                  stream=None):
+    """Gradients of sgmv: dx[perm] += u A (dx None: not wanted), grads.A = u^T x,
+    grads.B = dy^T v over each adapter's rows (added to them with accumulate;
+    grads None: not wanted)."""
+    d_in = (dx if x is None else x).shape[1]
+    _check(load().lora_sgmv_backward(_stream_handle(stream), DTYPES[dtype], _ptr(x), d_in if x is None else x.stride(0),
+                                     d_in, _ptr(dy), dy.stride(0), dy.shape[1], plan.seg,
+                                     _ptr(grads and grads.addr_A_dev), _ptr(grads and grads.addr_B_dev),
+                                     grads.n_adapters if grads else 0, LORA_GRAD_ACCUMULATE if accumulate else 0,
+                                     _ptr(dx), d_in if dx is None else dx.stride(0), _ptr(ws),
+                                     ws.numel() * ws.element_size()),
+           "lora_sgmv_backward")
 
 
 def v_pitch(max_rank: int) -> int:

@@ -231,7 +231,6 @@ size_t lora_segments_bytes(int32_t capacity)
 
 size_t lora_workspace_bytes(int op, int32_t T, int32_t d_in, int32_t d_out, int32_t max_rank)
 {
-    (void)d_out;
     switch (op) {
     case LORA_OP_SGMV_SHRINK:
     case LORA_OP_SGMV_EXPAND:
@@ -243,6 +242,9 @@ size_t lora_workspace_bytes(int op, int32_t T, int32_t d_in, int32_t d_out, int3
                3 * combined_workspace_bytes(T < 0 ? 0 : T, d_in < 1 ? 1 : d_in, max_rank < 1 ? 1 : max_rank);
     case LORA_OP_BGMV:
         return bgmv_workspace_bytes(T < 0 ? 0 : T, d_in < 1 ? 1 : d_in, max_rank < 1 ? 1 : max_rank);
+    case LORA_OP_SGMV_BACKWARD:
+        return sgmv_backward_workspace_bytes(T < 0 ? 0 : T, d_in < 1 ? 1 : d_in, d_out < 1 ? 1 : d_out,
+                                             max_rank < 1 ? 1 : max_rank);
     default: return size_t(-1);
     }
 }
@@ -814,6 +816,81 @@ int lora_bgmv_expand(void *stream, int dtype, int32_t T, const float *v, int64_t
     if ((st = make_expand_args(dtype, v, ldv, max_rank, y, ldy, d_out, true, &ea))) return st;
     return launch_bgmv_expand(static_cast<hipStream_t>(stream), ea, T, ids_dev, pool_B_dev, pool_rank_dev,
                               pool_alpha_dev, n_adapters, max_rank);
+}
+
+// Checks shared by the backward calls, for a plan with adapted tokens; fills b.
+static int make_backward_args(int dtype, const void *x, int64_t ldx, int32_t d_in, const void *dy, int64_t lddy,
+                              int32_t d_out, const lora_plan_header *h, const uint64_t *grad_A_dev,
+                              const uint64_t *grad_B_dev, int32_t n_adapters, unsigned flags, void *dx, int64_t lddx,
+                              BackwardArgs *b)
+{
+    const int es = esize_of(dtype);
+    if (flags & ~LORA_GRAD_ACCUMULATE) return fail(LORA_ERR_ARG, "unknown flags %#x", flags);
+    if (d_in < 1 || d_out < 1) return fail(LORA_ERR_ARG, "d_in %d or d_out %d < 1", d_in, d_out);
+    if (n_adapters < 0) return fail(LORA_ERR_ARG, "n_adapters %d < 0", n_adapters);
+    const bool grads = grad_A_dev || grad_B_dev;
+    if (!dy) return fail(LORA_ERR_ARG, "dy is NULL");
+    if (lddy < d_out) return fail(LORA_ERR_ARG, "lddy %lld < d_out %d", (long long)lddy, d_out);
+    if (!elem_aligned(dy, es)) return fail(LORA_ERR_ALIGN, "dy is not aligned to its element size");
+    if (grads) {
+        if (!x) return fail(LORA_ERR_ARG, "x is NULL");
+        if (ldx < d_in) return fail(LORA_ERR_ARG, "ldx %lld < d_in %d", (long long)ldx, d_in);
+        if (!elem_aligned(x, es)) return fail(LORA_ERR_ALIGN, "x is not aligned to its element size");
+        if ((reinterpret_cast<uintptr_t>(grad_A_dev) | reinterpret_cast<uintptr_t>(grad_B_dev)) & 7u)
+            return fail(LORA_ERR_ALIGN, "gradient tables are not 8-byte aligned");
+        // segments are in ascending adapter id
+        const auto *seg = reinterpret_cast<const lora_seg_desc *>(reinterpret_cast<const char *>(h) + h->seg_offset);
+        if (h->num_segments > 0 && seg[h->num_segments - 1].adapter >= n_adapters)
+            return fail(LORA_ERR_ADAPTER_ID, "the segments use adapter %d; the gradient tables have %d entries",
+                        seg[h->num_segments - 1].adapter, n_adapters);
+    }
+    if (dx) {
+        if (lddx < d_in) return fail(LORA_ERR_ARG, "lddx %lld < d_in %d", (long long)lddx, d_in);
+        if (!elem_aligned(dx, es)) return fail(LORA_ERR_ALIGN, "dx is not aligned to its element size");
+        if (dx == dy || (grads && dx == x)) return fail(LORA_ERR_ARG, "dx is x or dy");
+    }
+    auto whole = [es](const void *p, int64_t ld, int32_t d) {
+        return aligned16(p) && (ld * es) % 16 == 0 && (int64_t(d) * es) % 16 == 0;
+    };
+    b->dtype = dtype;
+    b->x = x;
+    b->ldx = ldx;
+    b->dy = dy;
+    b->lddy = lddy;
+    b->d_in = d_in;
+    b->d_out = d_out;
+    b->grad_A = grad_A_dev;
+    b->grad_B = grad_B_dev;
+    b->accumulate = flags & LORA_GRAD_ACCUMULATE;
+    b->dx = dx;
+    b->lddx = lddx;
+    b->vec_x = !grads || whole(x, ldx, d_in);
+    b->vec_dy = whole(dy, lddy, d_out);
+    b->vec_dx = dx && whole(dx, lddx, d_in);
+    return LORA_OK;
+}
+
+int lora_sgmv_backward(void *stream, int dtype, const void *x, int64_t ldx, int32_t d_in, const void *dy,
+                       int64_t lddy, int32_t d_out, const lora_segments *seg, const uint64_t *grad_A_dev,
+                       const uint64_t *grad_B_dev, int32_t n_adapters, unsigned flags, void *dx, int64_t lddx,
+                       void *ws, size_t ws_bytes)
+{
+    clear_error();
+    const lora_plan_header *h = nullptr;
+    const char *plan_dev = nullptr;
+    int st = check_segments(seg, &h, &plan_dev);
+    if (st) return st;
+    if ((st = check_dtype(dtype))) return st;
+    if (h->num_sorted == 0) return LORA_OK;
+    if (!plan_dev) return fail(LORA_ERR_ARG, "the segments' device buffer is NULL");
+    BackwardArgs b{};
+    if ((st = make_backward_args(dtype, x, ldx, d_in, dy, lddy, d_out, h, grad_A_dev, grad_B_dev, n_adapters, flags,
+                                 dx, lddx, &b)))
+        return st;
+    const size_t need = sgmv_backward_workspace_bytes(h->num_sorted, d_in, d_out, h->max_rank);
+    if (!ws || ws_bytes < need) return fail(LORA_ERR_WORKSPACE, "workspace %zu B < %zu B needed", ws_bytes, need);
+    if (!aligned16(ws)) return fail(LORA_ERR_ALIGN, "workspace is not 16-byte aligned");
+    return launch_sgmv_backward(static_cast<hipStream_t>(stream), b, PlanView{h, plan_dev}, ws);
 }
 
 // Checks and launch shared by the bf16 and E4M3 forms of the fused entry.

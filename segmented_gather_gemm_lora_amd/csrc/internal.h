@@ -133,6 +133,23 @@ int launch_fused_linear(hipStream_t s, const ShrinkArgs &sa, const void *W0, con
                         const PlanView &p, void *ws, bool w0_e4m3 = false, float w0_scale = 1.0f);
 size_t fused_workspace_bytes(int32_t T, int32_t d_in, int32_t max_rank);
 
+// Gradients of the segmented correction.  grad_A / grad_B: device tables of
+// fp32 gradient addresses by adapter (nullptr: none wanted); dx nullptr: not
+// wanted.
+struct BackwardArgs {
+    int dtype;
+    const void *x, *dy;
+    int64_t ldx, lddy;
+    int32_t d_in, d_out;
+    const uint64_t *grad_A, *grad_B;
+    bool accumulate;
+    void *dx;
+    int64_t lddx;
+    bool vec_x, vec_dy, vec_dx; // rows are whole aligned 16-byte pieces
+};
+size_t sgmv_backward_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out, int32_t max_rank);
+int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p, void *ws);
+
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Per-thread request to time the next launches (lora_profile_launches).

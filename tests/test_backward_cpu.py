@@ -1,0 +1,133 @@
+"""The backward calls on the CPU: refusals before any GPU call, workspace sizes,
+and the reference's own gradients against differences."""
+
+import ctypes
+
+import numpy as np
+import pytest
+
+from segmented_gather_gemm_lora_amd import binding as B
+from test_abi_cpu import FAKE_BASE, HostPlan, build, make_tables
+
+FX = FAKE_BASE + 0x40000000
+BIG = 1 << 40
+
+
+def plan_of(ids, n, ranks):
+    A, Bt, r, al = make_tables(n, np.random.default_rng(0), ranks)
+    st, plan = build(ids, n, A, Bt, r, al)
+    assert st == 0
+    return plan
+
+
+def run(plan, **kw):
+    a = dict(dtype=B.LORA_BF16, x=FX, ldx=64, d_in=64, dy=FX + 0x100000, lddy=128, d_out=128, gA=FX + 0x200000,
+             gB=FX + 0x300000, n=3, flags=0, dx=FX + 0x400000, lddx=64, ws=FX + 0x500000, ws_bytes=BIG, seg=None)
+    a.update(kw)
+    seg = plan.dev() if a["seg"] is None else a["seg"]
+    return B.load().lora_sgmv_backward(None, a["dtype"], a["x"], a["ldx"], a["d_in"], a["dy"], a["lddy"], a["d_out"], seg,
+                                       a["gA"], a["gB"], a["n"], a["flags"], a["dx"], a["lddx"], a["ws"], a["ws_bytes"])
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=7), "LORA_ERR_DTYPE"),
+    (dict(x=None), "LORA_ERR_ARG"),
+    (dict(dy=None), "LORA_ERR_ARG"),
+    (dict(d_in=0), "LORA_ERR_ARG"),
+    (dict(d_out=-1), "LORA_ERR_ARG"),
+    (dict(ldx=63), "LORA_ERR_ARG"),
+    (dict(lddy=127), "LORA_ERR_ARG"),
+    (dict(lddx=63), "LORA_ERR_ARG"),
+    (dict(flags=2), "LORA_ERR_ARG"),
+    (dict(n=-1), "LORA_ERR_ARG"),
+    (dict(n=2), "LORA_ERR_ADAPTER_ID"),
+    (dict(x=FX + 1), "LORA_ERR_ALIGN"),
+    (dict(dy=FX + 1), "LORA_ERR_ALIGN"),
+    (dict(dx=FX + 0x400001), "LORA_ERR_ALIGN"),
+    (dict(dtype=B.LORA_F32, x=FX + 2), "LORA_ERR_ALIGN"),
+    (dict(gA=FX + 4), "LORA_ERR_ALIGN"),
+    (dict(dx=FX), "LORA_ERR_ARG"),
+    (dict(dx=FX + 0x100000), "LORA_ERR_ARG"),
+    (dict(ws=None), "LORA_ERR_WORKSPACE"),
+    (dict(ws_bytes=16), "LORA_ERR_WORKSPACE"),
+    (dict(ws=FX + 0x500008), "LORA_ERR_ALIGN"),
+])
+def test_refusals(kw, status):
+    plan = plan_of([0, 2, 2, -1], 3, [16, 8, 4])
+    st = run(plan, **kw)
+    assert B.STATUS[st] == status, (kw, B.STATUS[st], B.last_error())
+    assert B.last_error()
+
+
+def test_refusals_of_segments():
+    plan = plan_of([0, 2], 3, [16, 8, 4])
+    L = B.load()
+    assert B.STATUS[L.lora_sgmv_backward(None, 1, FX, 64, 64, FX, 64, 64, None, FX, FX, 3, 0, FX, 64, FX, BIG)] == "LORA_ERR_ARG"
+    assert B.STATUS[run(plan, seg=plan.seg)] == "LORA_ERR_ARG"  # a host struct: never uploaded
+    assert B.STATUS[run(plan, seg=plan.dev(buf=0))] == "LORA_ERR_ARG"
+    blank = HostPlan(4)
+    d = plan.dev(host=blank.ptr)
+    assert B.STATUS[run(plan, seg=d)] == "LORA_ERR_PLAN"
+
+
+def test_no_adapted_rows_is_a_no_op():
+    for ids in ([], [-1, -1]):
+        assert run(plan_of(ids, 3, [16, 8, 4]), x=None, dy=None, ws=None, ws_bytes=0) == 0
+
+
+def test_nothing_wanted_is_a_no_op():
+    assert run(plan_of([0, 1], 3, [16, 8, 4]), x=None, gA=None, gB=None, dx=None) == 0
+
+
+def test_workspace_grows_with_every_size():
+    f = lambda T, i, o, r: B.lora_workspace_bytes(B.LORA_OP_SGMV_BACKWARD, T, i, o, r)  # noqa: E731
+    sizes = [f(T, 256, 512, 16) for T in range(0, 70000, 37)]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+    assert f(4096, 256, 512, 16) <= f(4096, 256, 512, 17) <= f(4096, 512, 512, 17) <= f(4096, 512, 1024, 17)
+    assert f(-1, 0, 0, 0) == f(0, 1, 1, 1)
+
+
+def test_reference_against_differences():
+    """The 64-bit reference's gradients are those of L = sum(dy y): y is linear in A, B and x each."""
+    import torch
+
+    from backward_ref import Problem
+
+    p = Problem("f32", [0, 1, -1, 1, 0, 0], [3, 2], 5, 4, seed=1)
+    p.dx_full.zero_()
+    (dx, dA, dB), _ = p.reference()
+    x = p.x.double().clone().requires_grad_()
+    A = [t.double().clone().requires_grad_() for t in p.A]
+    Bm = [t.double().clone().requires_grad_() for t in p.B]
+
+    def loss():
+        L = 0.0
+        for t, i in enumerate(p.ids):
+            if i >= 0:
+                L = L + (p.dy.double()[t] * (p.scale[i] * (x[t] @ A[i].t()) @ Bm[i].t())).sum()
+        return L
+
+    for t, g in ((x, dx), *zip(A, dA), *zip(Bm, dB)):
+        flat = t.data.view(-1)
+        for k in range(flat.numel()):
+            old = flat[k].item()
+            flat[k] = old + 0.5
+            up = loss().item()
+            flat[k] = old - 0.5
+            dn = loss().item()
+            flat[k] = old
+            assert abs((up - dn) - g.reshape(-1)[k]) <= 1e-12 * (1 + abs(g.reshape(-1)[k]))
+
+
+def test_gradient_pool_checks():
+    import torch
+
+    with pytest.raises(ValueError):
+        B.GradPool.from_tensors([torch.zeros(4)], [torch.zeros(4)])  # not on a device
+    with pytest.raises(ValueError):
+        B.GradPool.from_tensors([None], [])
+
+
+def test_header_and_binding_agree():
+    assert B.LORA_OP_SGMV_BACKWARD == 7 and B.LORA_GRAD_ACCUMULATE == 1
+    assert ctypes.sizeof(ctypes.c_uint) == 4
