@@ -691,6 +691,82 @@ int lora_sgmv_backward(void *stream, int dtype, const void *x, int64_t ldx, int3
                        const uint64_t *grad_B_dev, int32_t n_adapters, unsigned flags, void *dx, int64_t lddx,
                        void *ws, size_t ws_bytes);
 
+/* ------------------------------------------------------------------ optimizer
+ * AdamW (Loshchilov and Hutter, "Decoupled Weight Decay Regularization") over
+ * many tensors in one launch: the step that uses the gradients above, for the
+ * fp32 masters of every A_i and B_i of a pool.  Per element, in fp32:
+ *     g = grad_scale grad;  m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g g
+ *     p = p - lr (weight_decay p + (m / (1 - b1^step)) / (sqrt(v / (1 - b2^step)) + eps))
+ * and, where a copy is given, copy = bf16(p) rounded to nearest: the matrix that
+ * the bf16 calls read.  The numbers come from a device table with one entry for
+ * each group of tensors (an adapter of a tenant, say), so a captured step takes
+ * whatever the table holds at replay.  The caller counts the steps: 1 for the
+ * first; a group whose step is below 1 rests (its tensors are not touched).
+ *
+ * States: LORA_ADAM_F32, m and v fp32; or LORA_ADAM_8BIT, one byte each per
+ * element and one scale byte e for each LORA_ADAM_BLOCK consecutive elements of
+ * a tensor (the scale is 2^(e - 127)): m as OCP E4M3 codes, v as unsigned codes
+ * with 5 exponent bits of bias 15 and 3 mantissa bits (0xFF is NaN).  A state
+ * of all zero bytes is zero.  The 8-bit states are rounded stochastically, with
+ * random bits from a hash of the group's seed and step, the tensor's number in
+ * the plan and the element's index (the same inputs give the same state); a
+ * positive v is never rounded to 0.  A gradient that is not finite makes its own
+ * element's p, m and v NaN and touches no other element. */
+#define LORA_ADAM_F32 0
+#define LORA_ADAM_8BIT 1
+#define LORA_ADAM_BLOCK 256
+#define LORA_ADAM_MAX_ELEMENTS 0x7FFFFFFF /* elements of one tensor */
+
+typedef struct lora_adam_hyper { /* one group, in device memory */
+    float lr, beta1, beta2, eps, weight_decay;
+    float grad_scale; /* every gradient is multiplied by it (loss scaling, clipping); 1 for none */
+    int32_t step;     /* t, from 1; below 1 the group rests */
+    uint32_t seed;    /* of the 8-bit states' rounding */
+} lora_adam_hyper;    /* 32 bytes */
+
+typedef struct lora_adam_tensor { /* device addresses, 16-byte aligned (scales: any) */
+    uint64_t param;   /* fp32 [n] */
+    uint64_t grad;    /* fp32 or bf16 [n], read only */
+    uint64_t copy;    /* bf16 [n], or 0 */
+    uint64_t m, v;    /* fp32 [n], or one byte for each element */
+    uint64_t m_scale, v_scale; /* 8-bit states: bytes [ceil(n / LORA_ADAM_BLOCK)]; else 0 */
+    int64_t n;
+    int32_t group;    /* entry of the table of numbers */
+    int32_t reserved; /* 0 */
+} lora_adam_tensor;   /* 72 bytes */
+
+/* Bytes of the plan for these tensors (host array); 0 if the arguments are invalid. */
+size_t lora_adamw_plan_bytes(const lora_adam_tensor *tensors, int32_t n_tensors);
+
+/* Build the plan of a list of tensors in host memory (16-byte aligned; pinned
+ * for the upload).  grad_dtype: LORA_F32 or LORA_BF16, of every gradient.  No
+ * GPU call.
+ * Errors: LORA_ERR_ARG (also: two tensors share memory that the step writes),
+ * LORA_ERR_DTYPE, LORA_ERR_ALIGN, LORA_ERR_WORKSPACE. */
+int lora_adamw_plan(const lora_adam_tensor *tensors, int32_t n_tensors, int32_t n_groups, int state, int grad_dtype,
+                    void *plan_host, size_t plan_bytes);
+
+/* Enqueue the copy of a built plan to the device (16-byte aligned).
+ * Errors: LORA_ERR_ARG, LORA_ERR_ALIGN, LORA_ERR_PLAN, LORA_ERR_WORKSPACE, LORA_ERR_HIP. */
+int lora_adamw_upload(const void *plan_host, void *plan_dev, size_t dev_bytes, void *stream);
+
+/* One step of every tensor of the plan, one launch.
+ *   plan_host   the built plan (read for the launch geometry), unchanged since
+ *               the upload; plan_dev its uploaded copy
+ *   hyper_dev   device [n_groups], 16-byte aligned
+ * Calls that write the same tensors must be ordered on one stream.
+ * Errors: LORA_ERR_ARG (also: n_groups below the plan's), LORA_ERR_ALIGN,
+ * LORA_ERR_PLAN, LORA_ERR_HIP. */
+int lora_adamw(void *stream, const void *plan_host, const void *plan_dev, const lora_adam_hyper *hyper_dev,
+               int32_t n_groups);
+
+/* The values that 8-bit states stand for, as bf16 (exact): n elements of m and
+ * of v (either may be NULL), scales for each LORA_ADAM_BLOCK elements.  Codes and
+ * outputs 16-byte aligned.
+ * Errors: LORA_ERR_ARG, LORA_ERR_ALIGN, LORA_ERR_HIP. */
+int lora_adam_state_values(void *stream, int64_t n, const void *m, const void *m_scale, const void *v,
+                           const void *v_scale, void *m_out, void *v_out);
+
 /* ------------------------------------------------------------------ helpers */
 enum {
     LORA_OP_SGMV_SHRINK = 0,

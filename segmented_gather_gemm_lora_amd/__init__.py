@@ -10,10 +10,13 @@ from .binding import (  # noqa: F401
     DTYPES,
     LORA_BF16,
     LORA_F32,
+    AdamW,
     DevicePool,
     GradPool,
     LoraError,
     Plan,
+    adamw_hyper,
+    adamw_state_values,
     bgmv,
     bgmv_expand,
     bgmv_shrink,

@@ -32,6 +32,9 @@ LORA_OP_BGMV = 6
 LORA_OP_SGMV_BACKWARD = 7
 
 LORA_GRAD_ACCUMULATE = 1
+LORA_ADAM_F32 = 0
+LORA_ADAM_8BIT = 1
+ADAM_BLOCK = 256
 
 STATUS = {
     0: "LORA_OK", -1: "LORA_ERR_ARG", -2: "LORA_ERR_RANK", -3: "LORA_ERR_ADAPTER_ID",
@@ -51,7 +54,8 @@ EXPORTS = [
     "lora_page_alloc_give", "lora_page_alloc_free_count", "lora_pages_write", "lora_sgmv_paged", "lora_bgmv_paged",
     "lora_sgmv_grouped", "lora_sgmv_grouped_workspace_bytes", "lora_probe_empty", "lora_probe_stream",
     "lora_probe_chase", "lora_workspace_clear", "lora_debug_wait_limit", "lora_bgmv_noalloc",
-    "lora_sgmv_backward",
+    "lora_sgmv_backward", "lora_adamw_plan_bytes", "lora_adamw_plan", "lora_adamw_upload", "lora_adamw",
+    "lora_adam_state_values",
 ]
 LORA_CACHE_DRY = 1
 MAX_PROJ = 8
@@ -116,6 +120,11 @@ _SIGS = {
                                          _i32, _vp, _i64, _i32]),
     "lora_sgmv_backward": (ctypes.c_int, [_vp, ctypes.c_int, _vp, _i64, _i32, _vp, _i64, _i32, _vp, _vp, _vp, _i32,
                                           ctypes.c_uint, _vp, _i64, _vp, _sz]),
+    "lora_adamw_plan_bytes": (_sz, [_vp, _i32]),
+    "lora_adamw_plan": (ctypes.c_int, [_vp, _i32, _i32, ctypes.c_int, ctypes.c_int, _vp, _sz]),
+    "lora_adamw_upload": (ctypes.c_int, [_vp, _vp, _sz, _vp]),
+    "lora_adamw": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32]),
+    "lora_adam_state_values": (ctypes.c_int, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp]),
     "lora_probe_stream": (ctypes.c_int, [_vp, _vp, _i64, _vp, _i64, _vp, _i32]),
     "lora_probe_chase": (ctypes.c_int, [_vp, _vp, _i32, _vp]),
     "lora_page_alloc_create": (ctypes.c_int, [_i32, _vp]),
@@ -179,6 +188,16 @@ class LoraSgmvProj(ctypes.Structure):
 
 
 assert ctypes.sizeof(LoraSgmvProj) == 48
+
+
+class LoraAdamTensor(ctypes.Structure):
+    """struct lora_adam_tensor: one tensor of an AdamW plan."""
+
+    _fields_ = [("param", _u64), ("grad", _u64), ("copy", _u64), ("m", _u64), ("v", _u64), ("m_scale", _u64),
+                ("v_scale", _u64), ("n", _i64), ("group", _i32), ("reserved", _i32)]
+
+
+assert ctypes.sizeof(LoraAdamTensor) == 72
 
 
 def lib_path() -> str:
@@ -1066,6 +1085,92 @@ def sgmv_backward(x, dy, plan: Plan, grads: Optional[GradPool], dx, ws, dtype: s
                                      _ptr(dx), d_in if dx is None else dx.stride(0), _ptr(ws),
                                      ws.numel() * ws.element_size()),
            "lora_sgmv_backward")
+
+
+def adamw_hyper(n_groups: int, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, grad_scale=1.0, step=1,
+                seed=0, device="cuda"):
+    """The device table of lora_adamw, int32 [n_groups, 8] (columns 0 .. 5 hold
+    fp32 bits, 6 the step, 7 the seed).  Each argument is a number or one value
+    for each group.  `hyper[:, 6] += 1` counts a step on the device."""
+    torch = _torch()
+
+    def column(v, dtype):
+        t = torch.as_tensor(v, device=device)
+        t = (t.to(torch.int64) & 0xFFFFFFFF).to(torch.int32) if dtype is torch.int32 else t.to(dtype)
+        return t.expand(n_groups).contiguous().view(torch.int32)
+
+    floats = (lr, beta1, beta2, eps, weight_decay, grad_scale)
+    return torch.stack([*(column(v, torch.float32) for v in floats), column(step, torch.int32),
+                        column(seed, torch.int32)], 1)
+
+
+class AdamW:
+    """AdamW over many tensors in one launch (lora_adamw): params are fp32 device
+    tensors, grads fp32 or bf16 ones (all of one dtype), copies optional bf16
+    tensors that receive the rounded parameters.  groups[i] is the entry of
+    `hyper` (see adamw_hyper) that tensor i goes by.  state: "f32" or "8bit";
+    m, v (and m_scale, v_scale for 8-bit states) are lists of state tensors, made
+    here as zeros when not given."""
+
+    def __init__(self, params, grads, groups, hyper, state: str = "f32", copies=None, m=None, v=None, m_scale=None,
+                 v_scale=None, stream=None):
+        torch = _torch()
+        if state not in ("f32", "8bit"):
+            raise ValueError("state is 'f32' or '8bit'")
+        eight, device = state == "8bit", params[0].device if params else "cuda"
+        made = lambda given, size, dt: given if given is not None else [  # noqa: E731
+            torch.zeros(size(p.numel()), dtype=dt, device=p.device) for p in params]
+        blocks = lambda n: (n + ADAM_BLOCK - 1) // ADAM_BLOCK  # noqa: E731
+        self.params, self.grads, self.copies, self.hyper, self.state = list(params), list(grads), copies, hyper, state
+        self.m = made(m, lambda n: n, torch.uint8 if eight else torch.float32)
+        self.v = made(v, lambda n: n, torch.uint8 if eight else torch.float32)
+        self.m_scale = made(m_scale, blocks, torch.uint8) if eight else None
+        self.v_scale = made(v_scale, blocks, torch.uint8) if eight else None
+        gdt = self.grads[0].dtype if self.grads else torch.float32
+        if gdt not in (torch.float32, torch.bfloat16):
+            raise ValueError("gradients are fp32 or bf16")
+        if hyper.dtype != torch.int32 or hyper.dim() != 2 or hyper.shape[1] != 8 or not hyper.is_contiguous():
+            raise ValueError("hyper is the int32 [n_groups, 8] table of adamw_hyper")
+        n = len(self.params)
+        sdt = torch.uint8 if eight else torch.float32
+        lists = [("params", self.params, torch.float32, None), ("grads", self.grads, gdt, None),
+                 ("m", self.m, sdt, None), ("v", self.v, sdt, None)]
+        lists += [("copies", copies, torch.bfloat16, None)] if copies is not None else []
+        lists += [("m_scale", self.m_scale, sdt, blocks), ("v_scale", self.v_scale, sdt, blocks)] if eight else []
+        for name, ts, dt, size in lists:
+            if len(ts) != n or len(groups) != n:
+                raise ValueError(f"{name} and groups list one entry for each parameter")
+            for t, p in zip(ts, self.params):
+                want = size(p.numel()) if size else p.numel()
+                if t.dtype != dt or t.numel() != want or not t.is_contiguous() or t.device != p.device:
+                    raise ValueError(f"{name}: contiguous {dt} tensors of {want} elements on the parameter's device")
+        arr = (LoraAdamTensor * max(n, 1))()
+        for i, p in enumerate(self.params):
+            arr[i] = LoraAdamTensor(_ptr(p), _ptr(self.grads[i]), _ptr(copies[i]) if copies is not None else 0,
+                                    _ptr(self.m[i]), _ptr(self.v[i]), _ptr(self.m_scale[i]) if eight else 0,
+                                    _ptr(self.v_scale[i]) if eight else 0, p.numel(), int(groups[i]), 0)
+        lib = load()
+        nbytes = int(lib.lora_adamw_plan_bytes(arr, n))
+        self._host = torch.empty(max(nbytes, 16), dtype=torch.uint8, pin_memory=True)
+        self._dev = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+        _check(lib.lora_adamw_plan(arr, n, hyper.shape[0], LORA_ADAM_8BIT if eight else LORA_ADAM_F32,
+                                   LORA_BF16 if gdt == torch.bfloat16 else LORA_F32, _ptr(self._host), nbytes),
+               "lora_adamw_plan")
+        _check(lib.lora_adamw_upload(_ptr(self._host), _ptr(self._dev), nbytes, _stream_handle(stream)),
+               "lora_adamw_upload")
+
+    def step(self, stream=None):
+        """One step of every tensor, with the numbers that `hyper` holds on the device."""
+        _check(load().lora_adamw(_stream_handle(stream), _ptr(self._host), _ptr(self._dev), _ptr(self.hyper),
+                                 self.hyper.shape[0]), "lora_adamw")
+
+
+def adamw_state_values(m, m_scale, v, v_scale, m_out, v_out, stream=None):
+    """bf16 values of 8-bit states: flat code tensors (uint8), their scales (one
+    for each 256 elements) and bf16 outputs; m or v may be None."""
+    n = (v if m is None else m).numel()
+    _check(load().lora_adam_state_values(_stream_handle(stream), n, _ptr(m), _ptr(m_scale), _ptr(v), _ptr(v_scale),
+                                         _ptr(m_out), _ptr(v_out)), "lora_adam_state_values")
 
 
 def v_pitch(max_rank: int) -> int:

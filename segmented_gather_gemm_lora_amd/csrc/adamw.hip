@@ -1,0 +1,483 @@
+// AdamW over many tensors in one launch on gfx950, for the fp32 masters of the
+// adapters of a pool:
+//
+//     g = c grad;  m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g g
+//     p = p - lr (wd p + (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps))
+//
+// with lr, b1, b2, eps, wd, c, t of the tensor's group (an adapter: every
+// tenant's training run has its own), read from device memory, and optionally a
+// bf16 copy of p (the matrix that the forward reads).
+//
+// States are fp32 or 8 bits.  8 bits: a block of 256 elements has one scale
+// 2^(e - 127), e a byte, and a code per element: m as OCP E4M3, v (never
+// negative) as an unsigned float of 5 exponent bits (bias 15) and 3 mantissa
+// bits.  e is the least that keeps the block's largest magnitude below 1.75 2^8
+// (m) or 1.75 2^16 (v) scales.  Rounding is stochastic: v moves by 0.1% a step
+// (b2 = 0.999) and its codes are 6 to 12% apart, so rounding to nearest would
+// never move it; a value between two codes goes up with the probability of its
+// distance, so the stored state is right on average.  The 32 random bits of an
+// element (16 each for m and v) are a hash of the group's seed and step, the
+// tensor's number and the element's index.  A positive v never becomes 0, which
+// would make the next quotient arbitrary large.  A non-finite m or v is stored
+// as NaN and does not enter its block's scale.  The update of p uses m and v
+// before they are rounded.
+//
+// One workgroup takes one chunk, described by one record (addresses at the
+// chunk's start), and a wave 256 consecutive elements at a time, so that a
+// state block's maximum is a reduction over one wave.
+#include "internal.h"
+
+#include <algorithm>
+#include <cstring>
+#include <new>
+#include <vector>
+
+namespace lora {
+namespace {
+
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kBlock = LORA_ADAM_BLOCK; // elements of a state block: 4 per lane of a wave
+constexpr int kAdamThreads = 256;
+constexpr int kChunk = 4 * kAdamThreads; // elements of a workgroup
+constexpr uint32_t kAdamMagic = 0x4C6F4164u;
+
+struct AdamChunk {
+    uint64_t param, grad, copy, m, v, m_scale, v_scale; // at the chunk's first element
+    uint32_t e0;     // index of the first element in its tensor
+    int32_t n;       // elements, 1 .. kChunk
+    int32_t group;
+    uint32_t tensor; // the tensor's number
+    uint64_t reserved;
+};
+static_assert(sizeof(AdamChunk) == 80, "chunk record");
+
+struct AdamHeader {
+    uint32_t magic;
+    int32_t state, grad_dtype, n_groups;
+    int64_t n_chunks;
+    uint64_t bytes;
+};
+static_assert(sizeof(AdamHeader) == 32, "plan header");
+
+__device__ __forceinline__ uint32_t f32_to_bf16(float f) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f)); }
+__device__ __forceinline__ float bf16_to_f32(uint32_t h) { return __uint_as_float(h << 16); }
+
+// Multiply and xor-shift mixing of 32 bits (the fractions of sqrt 2 and sqrt 3
+// as odd multipliers): every input bit reaches every output bit.
+__device__ __forceinline__ uint32_t mix(uint32_t h)
+{
+    h ^= h >> 16;
+    h *= 0x6A09E667u;
+    h ^= h >> 15;
+    h *= 0xBB67AE85u;
+    return h ^ (h >> 16);
+}
+
+// Largest of 64 lanes' values.
+__device__ __forceinline__ uint32_t wave_max(uint32_t x)
+{
+#define LORA_MAX_DPP(ctrl, rows) x = max(x, uint32_t(__builtin_amdgcn_update_dpp(0, int(x), ctrl, rows, 0xf, false)))
+    LORA_MAX_DPP(0xB1, 0xf);  // lane ^ 1
+    LORA_MAX_DPP(0x4E, 0xf);  // lane ^ 2
+    LORA_MAX_DPP(0x124, 0xf); // rotations inside 16 lanes
+    LORA_MAX_DPP(0x128, 0xf);
+    LORA_MAX_DPP(0x142, 0xa); // lane 15 of rows 0 and 2 to rows 1 and 3
+    LORA_MAX_DPP(0x143, 0xc); // lane 31 to rows 2 and 3
+#undef LORA_MAX_DPP
+    return uint32_t(__builtin_amdgcn_readlane(int(x), 63));
+}
+
+// The 8-bit formats: BIAS of the exponent, TOP = exponent of the largest code.
+struct M8 {
+    static constexpr int kBias = 7, kTop = 8;
+    static constexpr uint32_t kMax = 0x7E, kNan = 0x7F;
+};
+struct V8 {
+    static constexpr int kBias = 15, kTop = 16;
+    static constexpr uint32_t kMax = 0xFE, kNan = 0xFF;
+};
+
+// Scale byte of a block whose largest magnitude has these bits.
+template <class Q> __device__ __forceinline__ int scale_of(uint32_t most)
+{
+    const int e = int(most >> 23) + ((most & 0x7fffffu) >= 0x600000u) - Q::kTop;
+    return min(max(e, 1), 254);
+}
+// |a| on the block's scale, as the code's magnitude: moved so that the code's
+// exponent field lies in the fp32 one (its subnormals are fp32 subnormals), the
+// code is the top bits; the noise is added below them.
+template <class Q> __device__ __forceinline__ uint32_t encode(float a, int e, uint32_t noise16)
+{
+    const uint32_t bits = __float_as_uint(__builtin_ldexpf(__builtin_fabsf(a), Q::kBias - e)) + (noise16 << 4);
+    const uint32_t c = min(bits >> 20, Q::kMax);
+    return __builtin_isfinite(a) ? c : Q::kNan;
+}
+template <class Q> __device__ __forceinline__ float decode(uint32_t mag, int e)
+{
+    const float f = __builtin_ldexpf(__uint_as_float(mag << 20), e - Q::kBias);
+    return mag == Q::kNan ? __builtin_nanf("") : f;
+}
+
+// 4 consecutive elements from a 16-byte (fp32) or 8-byte (bf16) aligned place; past n: 0.
+__device__ __forceinline__ floatx4 get4(const float *p, int n)
+{
+    if (n >= 4) return *reinterpret_cast<const floatx4 *>(p);
+    floatx4 f{};
+    for (int i = 0; i < n; ++i) f[i] = p[i];
+    return f;
+}
+__device__ __forceinline__ floatx4 get4(const uint16_t *p, int n)
+{
+    floatx4 f{};
+    if (n >= 4) {
+        const u32x2 w = *reinterpret_cast<const u32x2 *>(p);
+        return floatx4{bf16_to_f32(w[0] & 0xffffu), bf16_to_f32(w[0] >> 16), bf16_to_f32(w[1] & 0xffffu), bf16_to_f32(w[1] >> 16)};
+    }
+    for (int i = 0; i < n; ++i) f[i] = bf16_to_f32(p[i]);
+    return f;
+}
+__device__ __forceinline__ uint32_t get4(const uint8_t *p, int n)
+{
+    if (n >= 4) return *reinterpret_cast<const uint32_t *>(p);
+    uint32_t w = 0;
+    for (int i = 0; i < n; ++i) w |= uint32_t(p[i]) << (8 * i);
+    return w;
+}
+__device__ __forceinline__ void put4(float *p, floatx4 f, int n)
+{
+    if (n >= 4) *reinterpret_cast<floatx4 *>(p) = f;
+    else
+        for (int i = 0; i < n; ++i) p[i] = f[i];
+}
+__device__ __forceinline__ void put4(uint16_t *p, floatx4 f, int n)
+{
+    const u32x2 w = {f32_to_bf16(f[0]) | (f32_to_bf16(f[1]) << 16), f32_to_bf16(f[2]) | (f32_to_bf16(f[3]) << 16)};
+    if (n >= 4) *reinterpret_cast<u32x2 *>(p) = w;
+    else
+        for (int i = 0; i < n; ++i) p[i] = uint16_t(w[i >> 1] >> (16 * (i & 1)));
+}
+__device__ __forceinline__ void put4(uint8_t *p, uint32_t w, int n)
+{
+    if (n >= 4) *reinterpret_cast<uint32_t *>(p) = w;
+    else
+        for (int i = 0; i < n; ++i) p[i] = uint8_t(w >> (8 * i));
+}
+
+// 1 - b^t in 64 bits: with t in the thousands and b near 1 an fp32 power is off
+// by more than the fp32 quotient it goes into.
+__device__ __forceinline__ float one_minus_power(float b, int t)
+{
+    double p = 1.0, q = double(b);
+    for (uint32_t n = uint32_t(t); n; n >>= 1, q *= q)
+        if (n & 1) p *= q;
+    return float(1.0 - p);
+}
+
+template <bool BITS8, class G>
+__global__ __launch_bounds__(kAdamThreads) void adamw_kernel(const AdamChunk *__restrict__ chunks,
+                                                             const lora_adam_hyper *__restrict__ hyper)
+{
+#pragma clang fp contract(off)
+    const AdamChunk &c = chunks[blockIdx.x];
+    const int at = 4 * int(threadIdx.x); // this lane's first element in the chunk
+    const int n = c.n - at;              // elements from there, may be <= 0
+    const bool any = n > 0;
+    const int lat = any ? at : 0, ln = any ? n : 0;
+    floatx4 p = get4(reinterpret_cast<const float *>(c.param) + lat, ln);
+    floatx4 g = get4(reinterpret_cast<const G *>(c.grad) + lat, ln);
+    floatx4 m, v;
+    uint32_t mc = 0, vc = 0;
+    const int b = at / kBlock;            // state block (one per wave)
+    const bool live = b * kBlock < c.n;   // wave-uniform
+    int me = 0, ve = 0;
+    if constexpr (BITS8) {
+        mc = get4(reinterpret_cast<const uint8_t *>(c.m) + lat, ln);
+        vc = get4(reinterpret_cast<const uint8_t *>(c.v) + lat, ln);
+        me = reinterpret_cast<const uint8_t *>(c.m_scale)[live ? b : 0];
+        ve = reinterpret_cast<const uint8_t *>(c.v_scale)[live ? b : 0];
+    } else {
+        m = get4(reinterpret_cast<const float *>(c.m) + lat, ln);
+        v = get4(reinterpret_cast<const float *>(c.v) + lat, ln);
+    }
+    const lora_adam_hyper h = hyper[c.group];
+    if (h.step < 1 || !live) return; // a group that rests
+    const float bc1 = one_minus_power(h.beta1, h.step), bc2 = one_minus_power(h.beta2, h.step);
+    const float c1 = 1.0f - h.beta1, c2 = 1.0f - h.beta2;
+    if constexpr (BITS8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t q = (mc >> (8 * i)) & 0xffu;
+            const float f = decode<M8>(q & 0x7fu, me);
+            m[i] = q & 0x80u ? -f : f;
+            v[i] = decode<V8>((vc >> (8 * i)) & 0xffu, ve);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float gi = g[i] * h.grad_scale;
+        m[i] = h.beta1 * m[i] + c1 * gi;
+        v[i] = h.beta2 * v[i] + c2 * (gi * gi);
+        p[i] = p[i] - h.lr * (h.weight_decay * p[i] + (m[i] / bc1) / (__builtin_sqrtf(v[i] / bc2) + h.eps));
+    }
+    if constexpr (BITS8) {
+        uint32_t mm = 0, vm = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t ma = __float_as_uint(m[i]) & 0x7fffffffu, va = __float_as_uint(v[i]) & 0x7fffffffu;
+            if (i < n) {
+                mm = max(mm, ma < 0x7f800000u ? ma : 0u);
+                vm = max(vm, va < 0x7f800000u ? va : 0u);
+            }
+        }
+        me = scale_of<M8>(wave_max(mm));
+        ve = scale_of<V8>(wave_max(vm));
+        const uint32_t key = mix(mix(h.seed + uint32_t(h.step) * 0x9E3779B9u) + c.tensor * 0x510E527Fu);
+        mc = vc = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t rnd = mix((c.e0 + uint32_t(at + i)) * 0x9E3779B9u + key);
+            const uint32_t qm = encode<M8>(m[i], me, rnd & 0xffffu) | (m[i] < 0.f ? 0x80u : 0u);
+            uint32_t qv = encode<V8>(v[i], ve, rnd >> 16);
+            if (v[i] > 0.f && qv == 0) qv = 1;
+            mc |= qm << (8 * i);
+            vc |= qv << (8 * i);
+        }
+        if ((threadIdx.x & 63) == 0) {
+            reinterpret_cast<uint8_t *>(c.m_scale)[b] = uint8_t(me);
+            reinterpret_cast<uint8_t *>(c.v_scale)[b] = uint8_t(ve);
+        }
+    }
+    if (!any) return;
+    put4(reinterpret_cast<float *>(c.param) + at, p, n);
+    if (c.copy) put4(reinterpret_cast<uint16_t *>(c.copy) + at, p, n);
+    if constexpr (BITS8) {
+        put4(reinterpret_cast<uint8_t *>(c.m) + at, mc, n);
+        put4(reinterpret_cast<uint8_t *>(c.v) + at, vc, n);
+    } else {
+        put4(reinterpret_cast<float *>(c.m) + at, m, n);
+        put4(reinterpret_cast<float *>(c.v) + at, v, n);
+    }
+}
+
+// The values of 8-bit states; both formats' values are bf16 values (4
+// significant bits times a power of two in bf16's range).
+__global__ __launch_bounds__(256) void adam_values_kernel(int64_t n, const uint8_t *__restrict__ m,
+                                                          const uint8_t *__restrict__ ms, const uint8_t *__restrict__ v,
+                                                          const uint8_t *__restrict__ vs, uint16_t *__restrict__ mo,
+                                                          uint16_t *__restrict__ vo)
+{
+    const int64_t at = 4 * (int64_t(blockIdx.x) * 256 + threadIdx.x);
+    if (at >= n) return;
+    const int k = int(n - at < 4 ? n - at : 4);
+    if (m) {
+        const uint32_t w = get4(m + at, k);
+        const int e = ms[at / kBlock];
+        floatx4 f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t q = (w >> (8 * i)) & 0xffu;
+            const float a = decode<M8>(q & 0x7fu, e);
+            f[i] = q & 0x80u ? -a : a;
+        }
+        put4(mo + at, f, k);
+    }
+    if (v) {
+        const uint32_t w = get4(v + at, k);
+        const int e = vs[at / kBlock];
+        floatx4 f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = decode<V8>((w >> (8 * i)) & 0xffu, e);
+        put4(vo + at, f, k);
+    }
+}
+
+// The plan's header; nullptr with the error set.
+const AdamHeader *check_adam_plan(const void *plan)
+{
+    if (!plan) {
+        fail(LORA_ERR_ARG, "the plan's host buffer is NULL");
+        return nullptr;
+    }
+    if (reinterpret_cast<uintptr_t>(plan) & 15u) {
+        fail(LORA_ERR_ALIGN, "the plan's host buffer is not 16-byte aligned");
+        return nullptr;
+    }
+    const auto *h = static_cast<const AdamHeader *>(plan);
+    if (h->magic != kAdamMagic || h->n_chunks < 0) {
+        fail(LORA_ERR_PLAN, "buffer holds no built AdamW plan");
+        return nullptr;
+    }
+    return h;
+}
+int plan_status(const void *plan)
+{
+    return !plan ? LORA_ERR_ARG : (reinterpret_cast<uintptr_t>(plan) & 15u) ? LORA_ERR_ALIGN : LORA_ERR_PLAN;
+}
+
+bool sizes_ok(const lora_adam_tensor *t, int32_t n)
+{
+    if (n < 0 || (n > 0 && !t)) return false;
+    for (int32_t i = 0; i < n; ++i)
+        if (t[i].n < 0 || t[i].n > LORA_ADAM_MAX_ELEMENTS) return false;
+    return true;
+}
+
+int64_t chunks_of(const lora_adam_tensor *t, int32_t n)
+{
+    int64_t c = 0;
+    for (int32_t i = 0; i < n; ++i) c += (t[i].n + kChunk - 1) / kChunk;
+    return c;
+}
+
+} // namespace
+} // namespace lora
+
+using namespace lora;
+
+extern "C" {
+
+size_t lora_adamw_plan_bytes(const lora_adam_tensor *tensors, int32_t n_tensors)
+{
+    if (!sizes_ok(tensors, n_tensors)) return 0;
+    return sizeof(AdamHeader) + sizeof(AdamChunk) * size_t(chunks_of(tensors, n_tensors));
+}
+
+int lora_adamw_plan(const lora_adam_tensor *tensors, int32_t n_tensors, int32_t n_groups, int state, int grad_dtype,
+                    void *plan_host, size_t plan_bytes)
+{
+    clear_error();
+    if (n_tensors < 0) return fail(LORA_ERR_ARG, "n_tensors %d < 0", n_tensors);
+    if (n_tensors > 0 && !tensors) return fail(LORA_ERR_ARG, "tensors is NULL");
+    if (n_groups < 0) return fail(LORA_ERR_ARG, "n_groups %d < 0", n_groups);
+    if (state != LORA_ADAM_F32 && state != LORA_ADAM_8BIT) return fail(LORA_ERR_DTYPE, "unknown state format %d", state);
+    if (grad_dtype != LORA_F32 && grad_dtype != LORA_BF16) return fail(LORA_ERR_DTYPE, "unknown dtype %d", grad_dtype);
+    if (!plan_host) return fail(LORA_ERR_ARG, "plan_host is NULL");
+    if (!aligned16(plan_host)) return fail(LORA_ERR_ALIGN, "plan_host is not 16-byte aligned");
+    static_cast<AdamHeader *>(plan_host)->magic = 0;
+    // everything that is written, to find memory that two tensors share
+    struct Range {
+        uint64_t lo, hi;
+        int32_t tensor;
+    };
+    std::vector<Range> ranges;
+    try {
+        ranges.reserve(size_t(n_tensors) * 6);
+    } catch (const std::bad_alloc &) {
+        return fail(LORA_ERR_WORKSPACE, "no host memory for %d tensors", n_tensors);
+    }
+    const bool eight = state == LORA_ADAM_8BIT;
+    for (int32_t i = 0; i < n_tensors; ++i) {
+        const lora_adam_tensor &t = tensors[i];
+        if (t.n < 0 || t.n > LORA_ADAM_MAX_ELEMENTS)
+            return fail(LORA_ERR_ARG, "tensor %d: %lld elements outside [0, 2^31 - 1]", i, (long long)t.n);
+        if (t.group < 0 || t.group >= n_groups)
+            return fail(LORA_ERR_ARG, "tensor %d: group %d outside [0, %d)", i, t.group, n_groups);
+        if (t.n == 0) continue;
+        if (!t.param || !t.grad || !t.m || !t.v || (eight && (!t.m_scale || !t.v_scale)))
+            return fail(LORA_ERR_ARG, "tensor %d: a NULL address", i);
+        if ((t.param | t.grad | t.copy | t.m | t.v) & 15u)
+            return fail(LORA_ERR_ALIGN, "tensor %d: an address is not 16-byte aligned", i);
+        const uint64_t n = uint64_t(t.n), blocks = (n + kBlock - 1) / kBlock, es = eight ? 1 : 4;
+        ranges.push_back({t.param, t.param + 4 * n, i});
+        if (t.copy) ranges.push_back({t.copy, t.copy + 2 * n, i});
+        ranges.push_back({t.m, t.m + es * n, i});
+        ranges.push_back({t.v, t.v + es * n, i});
+        if (eight) {
+            ranges.push_back({t.m_scale, t.m_scale + blocks, i});
+            ranges.push_back({t.v_scale, t.v_scale + blocks, i});
+        }
+    }
+    std::sort(ranges.begin(), ranges.end(), [](const Range &a, const Range &b) { return a.lo < b.lo; });
+    for (size_t k = 1; k < ranges.size(); ++k)
+        if (ranges[k].lo < ranges[k - 1].hi)
+            return fail(LORA_ERR_ARG, "tensors %d and %d share memory that is written",
+                        std::min(ranges[k].tensor, ranges[k - 1].tensor), std::max(ranges[k].tensor, ranges[k - 1].tensor));
+    const size_t need = lora_adamw_plan_bytes(tensors, n_tensors);
+    if (plan_bytes < need) return fail(LORA_ERR_WORKSPACE, "plan buffer of %zu B < %zu B needed", plan_bytes, need);
+    auto *h = static_cast<AdamHeader *>(plan_host);
+    auto *ch = reinterpret_cast<AdamChunk *>(h + 1);
+    for (int32_t i = 0; i < n_tensors; ++i) {
+        const lora_adam_tensor &t = tensors[i];
+        const uint64_t gs = grad_dtype == LORA_BF16 ? 2 : 4, es = eight ? 1 : 4;
+        for (int64_t e = 0; e < t.n; e += kChunk, ++ch) {
+            std::memset(ch, 0, sizeof *ch);
+            ch->param = t.param + 4 * uint64_t(e);
+            ch->grad = t.grad + gs * uint64_t(e);
+            ch->copy = t.copy ? t.copy + 2 * uint64_t(e) : 0;
+            ch->m = t.m + es * uint64_t(e);
+            ch->v = t.v + es * uint64_t(e);
+            ch->m_scale = eight ? t.m_scale + uint64_t(e) / kBlock : 0;
+            ch->v_scale = eight ? t.v_scale + uint64_t(e) / kBlock : 0;
+            ch->e0 = uint32_t(e);
+            ch->n = int32_t(std::min<int64_t>(kChunk, t.n - e));
+            ch->group = t.group;
+            ch->tensor = uint32_t(i);
+        }
+    }
+    h->state = state;
+    h->grad_dtype = grad_dtype;
+    h->n_groups = n_groups;
+    h->n_chunks = chunks_of(tensors, n_tensors);
+    h->bytes = need;
+    h->magic = kAdamMagic;
+    return LORA_OK;
+}
+
+int lora_adamw_upload(const void *plan_host, void *plan_dev, size_t dev_bytes, void *stream)
+{
+    clear_error();
+    const AdamHeader *h = check_adam_plan(plan_host);
+    if (!h) return plan_status(plan_host);
+    if (!plan_dev) return fail(LORA_ERR_ARG, "plan_dev is NULL");
+    if (!aligned16(plan_dev)) return fail(LORA_ERR_ALIGN, "plan_dev is not 16-byte aligned");
+    if (dev_bytes < h->bytes) return fail(LORA_ERR_WORKSPACE, "plan_dev of %zu B < %zu B", dev_bytes, size_t(h->bytes));
+    const hipError_t e = hipMemcpyAsync(plan_dev, plan_host, h->bytes, hipMemcpyHostToDevice, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? LORA_OK : fail(LORA_ERR_HIP, "hipMemcpyAsync: %s", hipGetErrorString(e));
+}
+
+int lora_adamw(void *stream, const void *plan_host, const void *plan_dev, const lora_adam_hyper *hyper_dev,
+               int32_t n_groups)
+{
+    clear_error();
+    const AdamHeader *h = check_adam_plan(plan_host);
+    if (!h) return plan_status(plan_host);
+    if (n_groups < h->n_groups)
+        return fail(LORA_ERR_ARG, "%d groups of parameters; the plan's tensors use %d", n_groups, h->n_groups);
+    if (h->n_chunks == 0) return LORA_OK;
+    if (!plan_dev || !hyper_dev) return fail(LORA_ERR_ARG, "plan_dev or hyper_dev is NULL");
+    if (!aligned16(plan_dev) || !aligned16(hyper_dev))
+        return fail(LORA_ERR_ALIGN, "plan_dev or hyper_dev is not 16-byte aligned");
+    if (h->n_chunks > (int64_t(1) << 31) - 1) return fail(LORA_ERR_ARG, "too many chunks");
+    const auto *ch = reinterpret_cast<const AdamChunk *>(static_cast<const AdamHeader *>(plan_dev) + 1);
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const dim3 grid{unsigned(h->n_chunks)}, block(kAdamThreads);
+    const bool eight = h->state == LORA_ADAM_8BIT, gb = h->grad_dtype == LORA_BF16;
+    if (eight && gb) launch_kernel(adamw_kernel<true, uint16_t>, grid, block, 0, s, ch, hyper_dev);
+    else if (eight) launch_kernel(adamw_kernel<true, float>, grid, block, 0, s, ch, hyper_dev);
+    else if (gb) launch_kernel(adamw_kernel<false, uint16_t>, grid, block, 0, s, ch, hyper_dev);
+    else launch_kernel(adamw_kernel<false, float>, grid, block, 0, s, ch, hyper_dev);
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? LORA_OK : fail(LORA_ERR_HIP, "AdamW launch: %s", hipGetErrorString(e));
+}
+
+int lora_adam_state_values(void *stream, int64_t n, const void *m, const void *m_scale, const void *v,
+                           const void *v_scale, void *m_out, void *v_out)
+{
+    clear_error();
+    if (n < 0) return fail(LORA_ERR_ARG, "n %lld < 0", (long long)n);
+    if (n == 0 || (!m && !v)) return LORA_OK;
+    if ((m && (!m_scale || !m_out)) || (v && (!v_scale || !v_out))) return fail(LORA_ERR_ARG, "a scale or output is NULL");
+    if ((m && (!aligned16(m) || !aligned16(m_out))) || (v && (!aligned16(v) || !aligned16(v_out))))
+        return fail(LORA_ERR_ALIGN, "codes or outputs are not 16-byte aligned");
+    const int64_t nwg = (n + 1023) / 1024;
+    if (nwg > (int64_t(1) << 31) - 1) return fail(LORA_ERR_ARG, "n %lld is too large", (long long)n);
+    launch_kernel(adam_values_kernel, dim3(unsigned(nwg)), dim3(256), 0, static_cast<hipStream_t>(stream), n,
+                  static_cast<const uint8_t *>(m), static_cast<const uint8_t *>(m_scale), static_cast<const uint8_t *>(v),
+                  static_cast<const uint8_t *>(v_scale), static_cast<uint16_t *>(m_out), static_cast<uint16_t *>(v_out));
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? LORA_OK : fail(LORA_ERR_HIP, "state values launch: %s", hipGetErrorString(e));
+}
+
+} // extern "C"
