@@ -224,7 +224,8 @@ def _prepare_adamw(case, seed, gen):
     if own:
         from segmented_gather_gemm_lora_amd import binding as L
 
-        cut = lambda t: [t.view(-1)[int(a) : int(a) + int(k)] for a, k in zip(starts[:-1], sizes)]  # noqa: E731
+        # the buffers hold whole blocks of 256, and the plain form steps all of them: so do the tensors given here
+        cut = lambda t: [t.view(-1)[int(a) : int(a) + int(k) * BLOCK] for a, k in zip(starts[:-1], blocks)]  # noqa: E731
         per = lambda t: [t[int(a) // BLOCK : int(a) // BLOCK + int(k)] for a, k in zip(starts[:-1], blocks)]  # noqa: E731
         more = {"m_scale": per(s["m_scale"]), "v_scale": per(s["v_scale"])} if case["state"] == "8bit" else {}
         s["opt"] = L.AdamW(cut(s["p"]), cut(s["g"]), groups=[i // 2 for i in range(len(sizes))],
