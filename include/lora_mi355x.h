@@ -691,6 +691,22 @@ int lora_sgmv_backward(void *stream, int dtype, const void *x, int64_t ldx, int3
                        const uint64_t *grad_B_dev, int32_t n_adapters, unsigned flags, void *dx, int64_t lddx,
                        void *ws, size_t ws_bytes);
 
+/* Gradients of lora_fused_linear: as lora_sgmv_backward, with the shared base
+ * product's part of dx and overwriting it, for every token:
+ *     dx[t] = dy[t] W0 + u[t] A_i      (tokens without an adapter: dy[t] W0)
+ * The base weight is frozen: it gets no gradient.  bf16 only.  x, W0, dy, dx and
+ * the workspace must be 16-byte aligned, ldx, lddy and lddx multiples of 8
+ * elements and d_in a multiple of 8 (d_out is free).  dx is one fp32 sum over
+ * d_out and the ranks, rounded once.  Needs ws_bytes >=
+ * lora_workspace_bytes(LORA_OP_FUSED_BACKWARD, T, d_in, d_out, max_rank), T the
+ * batch's tokens.
+ * Errors: as lora_sgmv_backward; LORA_ERR_DTYPE for fp32; LORA_ERR_ARG also for
+ * dx NULL; LORA_ERR_ALIGN for the alignment rules above. */
+int lora_fused_linear_backward(void *stream, int dtype, const void *x, int64_t ldx, int32_t d_in, const void *W0,
+                               const void *dy, int64_t lddy, int32_t d_out, const lora_segments *seg,
+                               const uint64_t *grad_A_dev, const uint64_t *grad_B_dev, int32_t n_adapters,
+                               unsigned flags, void *dx, int64_t lddx, void *ws, size_t ws_bytes);
+
 /* ------------------------------------------------------------------ optimizer
  * AdamW (Loshchilov and Hutter, "Decoupled Weight Decay Regularization") over
  * many tensors in one launch: the step that uses the gradients above, for the
@@ -776,7 +792,8 @@ enum {
     LORA_OP_FUSED = 4,
     LORA_OP_SGMV = 5,
     LORA_OP_BGMV = 6,
-    LORA_OP_SGMV_BACKWARD = 7
+    LORA_OP_SGMV_BACKWARD = 7,
+    LORA_OP_FUSED_BACKWARD = 8
 };
 
 /* Workspace bytes an op needs (0 = none; ws may then be NULL); -1 cast to

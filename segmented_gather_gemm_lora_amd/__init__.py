@@ -21,6 +21,7 @@ from .binding import (  # noqa: F401
     bgmv_expand,
     bgmv_shrink,
     fused_linear,
+    fused_linear_backward,
     lib_path,
     load,
     sgmv,

@@ -30,6 +30,7 @@ LORA_OP_FUSED = 4
 LORA_OP_SGMV = 5
 LORA_OP_BGMV = 6
 LORA_OP_SGMV_BACKWARD = 7
+LORA_OP_FUSED_BACKWARD = 8
 
 LORA_GRAD_ACCUMULATE = 1
 LORA_ADAM_F32 = 0
@@ -54,7 +55,7 @@ EXPORTS = [
     "lora_page_alloc_give", "lora_page_alloc_free_count", "lora_pages_write", "lora_sgmv_paged", "lora_bgmv_paged",
     "lora_sgmv_grouped", "lora_sgmv_grouped_workspace_bytes", "lora_probe_empty", "lora_probe_stream",
     "lora_probe_chase", "lora_workspace_clear", "lora_debug_wait_limit", "lora_bgmv_noalloc",
-    "lora_sgmv_backward", "lora_adamw_plan_bytes", "lora_adamw_plan", "lora_adamw_upload", "lora_adamw",
+    "lora_sgmv_backward", "lora_fused_linear_backward", "lora_adamw_plan_bytes", "lora_adamw_plan", "lora_adamw_upload", "lora_adamw",
     "lora_adam_state_values",
 ]
 LORA_CACHE_DRY = 1
@@ -120,6 +121,8 @@ _SIGS = {
                                          _i32, _vp, _i64, _i32]),
     "lora_sgmv_backward": (ctypes.c_int, [_vp, ctypes.c_int, _vp, _i64, _i32, _vp, _i64, _i32, _vp, _vp, _vp, _i32,
                                           ctypes.c_uint, _vp, _i64, _vp, _sz]),
+    "lora_fused_linear_backward": (ctypes.c_int, [_vp, ctypes.c_int, _vp, _i64, _i32, _vp, _vp, _i64, _i32, _vp, _vp,
+                                                  _vp, _i32, ctypes.c_uint, _vp, _i64, _vp, _sz]),
     "lora_adamw_plan_bytes": (_sz, [_vp, _i32]),
     "lora_adamw_plan": (ctypes.c_int, [_vp, _i32, _i32, ctypes.c_int, ctypes.c_int, _vp, _sz]),
     "lora_adamw_upload": (ctypes.c_int, [_vp, _vp, _sz, _vp]),
@@ -1085,6 +1088,20 @@ def sgmv_backward(x, dy, plan: Plan, grads: Optional[GradPool], dx, ws, dtype: s
                                      _ptr(dx), d_in if dx is None else dx.stride(0), _ptr(ws),
                                      ws.numel() * ws.element_size()),
            "lora_sgmv_backward")
+
+
+def fused_linear_backward(x, W0, dy, plan: Plan, grads: Optional[GradPool], dx, ws, dtype: str = "bf16",
+                          accumulate: bool = False, stream=None):
+    """Gradients of fused_linear: dx = dy W0 + u A (overwritten, every row), and the
+    adapters' gradients as in sgmv_backward (grads None: not wanted; x may then be None)."""
+    d_in = W0.shape[1]
+    _check(load().lora_fused_linear_backward(_stream_handle(stream), DTYPES[dtype], _ptr(x),
+                                             d_in if x is None else x.stride(0), d_in, _ptr(W0), _ptr(dy), dy.stride(0),
+                                             dy.shape[1], plan.seg, _ptr(grads and grads.addr_A_dev),
+                                             _ptr(grads and grads.addr_B_dev), grads.n_adapters if grads else 0,
+                                             LORA_GRAD_ACCUMULATE if accumulate else 0, _ptr(dx), dx.stride(0),
+                                             _ptr(ws), ws.numel() * ws.element_size()),
+           "lora_fused_linear_backward")
 
 
 def adamw_hyper(n_groups: int, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, grad_scale=1.0, step=1,

@@ -245,6 +245,9 @@ size_t lora_workspace_bytes(int op, int32_t T, int32_t d_in, int32_t d_out, int3
     case LORA_OP_SGMV_BACKWARD:
         return sgmv_backward_workspace_bytes(T < 0 ? 0 : T, d_in < 1 ? 1 : d_in, d_out < 1 ? 1 : d_out,
                                              max_rank < 1 ? 1 : max_rank);
+    case LORA_OP_FUSED_BACKWARD:
+        return fused_backward_workspace_bytes(T < 0 ? 0 : T, d_in < 1 ? 1 : d_in, d_out < 1 ? 1 : d_out,
+                                              max_rank < 1 ? 1 : max_rank);
     default: return size_t(-1);
     }
 }
@@ -891,6 +894,35 @@ int lora_sgmv_backward(void *stream, int dtype, const void *x, int64_t ldx, int3
     if (!ws || ws_bytes < need) return fail(LORA_ERR_WORKSPACE, "workspace %zu B < %zu B needed", ws_bytes, need);
     if (!aligned16(ws)) return fail(LORA_ERR_ALIGN, "workspace is not 16-byte aligned");
     return launch_sgmv_backward(static_cast<hipStream_t>(stream), b, PlanView{h, plan_dev}, ws);
+}
+
+int lora_fused_linear_backward(void *stream, int dtype, const void *x, int64_t ldx, int32_t d_in, const void *W0,
+                               const void *dy, int64_t lddy, int32_t d_out, const lora_segments *seg,
+                               const uint64_t *grad_A_dev, const uint64_t *grad_B_dev, int32_t n_adapters,
+                               unsigned flags, void *dx, int64_t lddx, void *ws, size_t ws_bytes)
+{
+    clear_error();
+    const lora_plan_header *h = nullptr;
+    const char *plan_dev = nullptr;
+    int st = check_segments(seg, &h, &plan_dev);
+    if (st) return st;
+    if ((st = check_dtype(dtype))) return st;
+    if (dtype != LORA_BF16) return fail(LORA_ERR_DTYPE, "the fused entry takes bf16 only");
+    if (h->num_tokens == 0) return LORA_OK;
+    if (!plan_dev) return fail(LORA_ERR_ARG, "the segments' device buffer is NULL");
+    if (!W0 || !dx) return fail(LORA_ERR_ARG, "W0 or dx is NULL");
+    BackwardArgs b{};
+    if ((st = make_backward_args(dtype, x, ldx, d_in, dy, lddy, d_out, h, grad_A_dev, grad_B_dev, n_adapters, flags,
+                                 dx, lddx, &b)))
+        return st;
+    const bool grads = grad_A_dev || grad_B_dev;
+    if ((grads && (!aligned16(x) || ldx % 8)) || !aligned16(W0) || !aligned16(dy) || !aligned16(dx) || lddy % 8 ||
+        lddx % 8 || d_in % 8)
+        return fail(LORA_ERR_ALIGN, "fused entry needs 16-byte aligned x, W0, dy, dx rows and d_in %% 8 == 0");
+    const size_t need = fused_backward_workspace_bytes(h->num_tokens, d_in, d_out, h->max_rank < 1 ? 1 : h->max_rank);
+    if (!ws || ws_bytes < need) return fail(LORA_ERR_WORKSPACE, "workspace %zu B < %zu B needed", ws_bytes, need);
+    if (!aligned16(ws)) return fail(LORA_ERR_ALIGN, "workspace is not 16-byte aligned");
+    return launch_fused_backward(static_cast<hipStream_t>(stream), b, W0, PlanView{h, plan_dev}, ws);
 }
 
 // Checks and launch shared by the bf16 and E4M3 forms of the fused entry.

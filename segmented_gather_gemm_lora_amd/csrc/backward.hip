@@ -755,7 +755,8 @@ size_t sgmv_backward_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out, int
     return layout_of(T, d_in, d_out, max_rank).bytes;
 }
 
-int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p, void *ws)
+int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p, void *ws, const uint16_t **u_rows,
+                         int64_t *ldu)
 {
     const lora_plan_header *h = p.h;
     const Layout l = layout_of(h->num_sorted, b.d_in, b.d_out, h->max_rank);
@@ -788,7 +789,11 @@ int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p
     a.accumulate = b.accumulate;
     a.dx = b.dx;
     a.lddx = b.lddx;
-    a.sides = (b.grad_B ? 1 : 0) | (b.grad_A || b.dx ? 2 : 0);
+    a.sides = (b.grad_B ? 1 : 0) | (b.grad_A || b.dx || u_rows ? 2 : 0);
+    if (u_rows) {
+        *u_rows = reinterpret_cast<const uint16_t *>(a.ur);
+        *ldu = 2 * int64_t(a.r16);
+    }
     if (!a.sides) return LORA_OK;
     const lora_seg_desc *hs = reinterpret_cast<const lora_seg_desc *>(reinterpret_cast<const char *>(h) + h->seg_offset);
     for (int i = 0; i < h->num_segments; ++i) {

@@ -1,0 +1,445 @@
+// Input gradient of the fused adapted layer on gfx950:
+//
+//     dx[t] = dy[t] W0 + u[t] A_s          (W0 [d_out, d_in], A_s [r, d_in])
+//
+// for every token t, overwriting dx, with u = s dy B from the backward shrink
+// (backward.hip), in bf16 hi and lo halves.  One GEMM over the plan's rows: the
+// summed axis is d_out, and u A is appended to it as further steps (a step of 32
+// holds 16 ranks: u's hi halves, then its lo halves, against the same 16 rows
+// of A), so that the correction costs ceil(r / 16) steps per segment that meets a
+// tile and no code of its own.
+//
+// A workgroup computes 256 columns x ROWS plan rows with 8 waves.  The summed
+// axis advances 32 per stage through a ring of LDS stages filled by direct
+// global-to-LDS loads (16 bytes per lane) issued kStages - 1 stages ahead.
+// W0 (and A) are contiguous along the columns, not along the summed axis that
+// MFMA wants in a lane: their part of a stage holds 32 rows of 512 bytes, read
+// with ds_read_b64_tr_b16, which hands each lane one column of 4 rows.  Unit
+// (16 bytes) un of row q lies in slot un ^ 4 (q % 4): the 4 rows of a read fall in
+// distinct banks.  The dy (u) part holds rows of 64 bytes, unit un of row q in
+// slot un ^ (q / 2 % 4).
+// Units that lie outside (rows of another segment, ranks past r, the summed
+// axis past d_out) are loaded from a block of zeros.
+//
+// Few tiles (a narrow d_in) leave most CUs idle, so the summed axis is split:
+// each split writes fp32 sums to the workspace, and a last launch adds them in
+// split order.
+#include "internal.h"
+
+#include <algorithm>
+
+namespace lora {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kCols = 256;    // columns per workgroup
+constexpr int kBK = 32;       // summed axis per stage
+constexpr int kThreads = 512; // 8 waves
+constexpr int kStages = 4;
+constexpr int kWBytes = kBK * kCols * 2; // W0 part of a stage: 16 KB
+constexpr int kMaxSplits = 16;
+constexpr int kFill = 256; // workgroups that fill the chip
+
+__device__ const uint32_t g_zeros[4] = {0, 0, 0, 0};
+
+// WC column groups of waves (8 / WC row groups); a wave has TM row tiles and TN
+// column tiles of 16.
+template <int ROWS> struct Shape;
+template <> struct Shape<256> {
+    static constexpr int WC = 4, TM = 8, TN = 4;
+};
+template <> struct Shape<64> {
+    static constexpr int WC = 8, TM = 4, TN = 2;
+};
+
+constexpr int waitcnt_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
+
+// 16 bytes per lane to LDS at m0 + 16 lane (published by an explicit vmcnt wait
+// and a barrier; nothing else uses m0).
+__device__ __forceinline__ void dma16(const void *g, uint32_t lds_byte)
+{
+    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(lds_byte) : "memory");
+}
+__device__ __forceinline__ u32x2 read_tr(const char *lds)
+{
+    typedef __attribute__((address_space(3))) s16x4 lds4;
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(lds)));
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
+{
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    const bf16x2_t v = {static_cast<__bf16>(lo), static_cast<__bf16>(hi)};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+struct DgradArgs {
+    const uint16_t *dy;
+    int64_t lddy;
+    const uint16_t *W0;
+    const uint16_t *tail; // [T][8]: dy's last d_out % 8 columns and zeros, or null
+    int d_in, d_out;
+    const int32_t *perm;
+    const int32_t *segidx;
+    const lora_seg_desc *seg;
+    const uint16_t *ur; // u in rows: [position][per 16 ranks: 16 hi, 16 lo]
+    int64_t ldu;
+    int T, Tp;
+    uint16_t *dx;
+    int64_t lddx;
+    float *part; // [split][T][d_in] when splits > 1
+    int tiles_m, tiles_n, splits;
+};
+
+// Rows' columns d_out / 8 * 8 .. d_out - 1, padded with zeros to 8.
+__global__ __launch_bounds__(256) void dgrad_tail_kernel(const uint16_t *__restrict__ dy, int64_t lddy, int T, int d_out,
+                                                         uint16_t *__restrict__ tail)
+{
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= T * 8) return;
+    const int t = i >> 3, c = d_out / 8 * 8 + (i & 7);
+    tail[i] = c < d_out ? dy[int64_t(t) * lddy + c] : 0;
+}
+
+template <int ROWS>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void dgrad_kernel(DgradArgs a)
+{
+    typedef Shape<ROWS> G;
+    constexpr int kXBytes = ROWS * kBK * 2, kStageBytes = kWBytes + kXBytes;
+    constexpr int kWDma = kWBytes / 1024 / 8;                    // W0 loads of a wave per stage: 2
+    constexpr int kXDma = kXBytes / 1024 >= 8 ? kXBytes / 1024 / 8 : 1;
+    constexpr bool kXAll = kXBytes / 1024 >= 8;                  // every wave loads dy rows
+    static_assert(kStages * kStageBytes <= 160 * 1024, "LDS budget");
+    __shared__ __attribute__((aligned(1024))) char lds[kStages * kStageBytes];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int m = lane & 15, g = lane >> 4;
+    const int wr = wave / G::WC, wc = wave % G::WC;
+    const uint32_t lds0 = uint32_t(uintptr_t((__attribute__((address_space(3))) char *)(lds)));
+
+    // Row tiles fastest, then columns, then splits; a contiguous run per XCD.
+    const int nwg = a.tiles_m * a.tiles_n * a.splits;
+    int id = blockIdx.x;
+    if ((nwg & 7) == 0) id = (id & 7) * (nwg >> 3) + (id >> 3);
+    const int m0 = (id % a.tiles_m) * ROWS;
+    id /= a.tiles_m;
+    const int c0 = (id % a.tiles_n) * kCols, split = id / a.tiles_n;
+    const int nk = (a.d_out + kBK - 1) / kBK; // stages of the base product
+    const int k_begin = int(int64_t(nk) * split / a.splits), k_end = int(int64_t(nk) * (split + 1) / a.splits);
+
+    // correction steps of this tile (the last split has them)
+    int s0 = 0, s1 = -1, ncorr = 0;
+    if (split == a.splits - 1 && m0 < a.Tp) {
+        s0 = __builtin_amdgcn_readfirstlane(a.segidx[m0]);
+        s1 = __builtin_amdgcn_readfirstlane(a.segidx[min(m0 + ROWS, a.Tp) - 1]);
+        for (int s = s0; s <= s1; s += 64) {
+            int n = s + lane <= s1 ? (a.seg[s + lane].rank + 15) >> 4 : 0;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d);
+            ncorr += __builtin_amdgcn_readfirstlane(n);
+        }
+    }
+    const int nst = k_end - k_begin + ncorr;
+
+    // This lane's units.  W0 part: slot 64 i + lane of the stage, i = 2 wave + j:
+    // row slot / 32.  dy part: row slot / 4.
+    const char *zeros = reinterpret_cast<const char *>(g_zeros);
+    int wrow[kWDma], wcol[kWDma];
+    const char *wp[kWDma];
+#pragma unroll
+    for (int j = 0; j < kWDma; ++j) {
+        const int slot = (wave * kWDma + j) * 64 + lane;
+        wrow[j] = slot >> 5;
+        const int c = c0 + 8 * ((slot & 31) ^ ((wrow[j] & 3) << 2));
+        wcol[j] = c < a.d_in ? c : 0; // past d_in: columns that are not stored
+        wp[j] = reinterpret_cast<const char *>(a.W0 + int64_t(k_begin * kBK + wrow[j]) * a.d_in + wcol[j]);
+    }
+    const bool xw = kXAll || wave < kXBytes / 1024;
+    int xpos[kXDma], xk[kXDma], xtok[kXDma];
+    const char *xp[kXDma];
+#pragma unroll
+    for (int j = 0; j < kXDma; ++j) {
+        const int slot = ((xw ? wave : 0) * kXDma + j) * 64 + lane, row = slot >> 2;
+        xpos[j] = m0 + row;
+        xk[j] = 8 * ((slot & 3) ^ ((row >> 1) & 3));
+        xtok[j] = a.perm[xpos[j] < a.T ? xpos[j] : a.T - 1];
+        xp[j] = reinterpret_cast<const char *>(a.dy + int64_t(xtok[j]) * a.lddy + k_begin * kBK + xk[j]);
+    }
+
+    // Stage i of the list: base stages k_begin .. k_end - 1, then the correction.
+    int cs = s0, cj = 0; // next correction step: segment, first rank
+    auto issue = [&](int i) {
+        const uint32_t wbase = lds0 + uint32_t((i % kStages) * kStageBytes + wave * kWDma * 1024);
+        const uint32_t xbase = lds0 + uint32_t((i % kStages) * kStageBytes + kWBytes + wave * kXDma * 1024);
+        const int k0 = (k_begin + i) * kBK;
+        if (i < k_end - k_begin) {
+            if (k0 + kBK <= a.d_out) {
+#pragma unroll
+                for (int j = 0; j < kWDma; ++j) dma16(wp[j], wbase + j * 1024);
+                if (xw) {
+#pragma unroll
+                    for (int j = 0; j < kXDma; ++j) dma16(xp[j], xbase + j * 1024);
+                }
+#pragma unroll
+                for (int j = 0; j < kWDma; ++j) wp[j] += int64_t(kBK) * a.d_in * 2;
+#pragma unroll
+                for (int j = 0; j < kXDma; ++j) xp[j] += kBK * 2;
+            } else { // the last, partial stage
+#pragma unroll
+                for (int j = 0; j < kWDma; ++j) dma16(k0 + wrow[j] < a.d_out ? wp[j] : zeros, wbase + j * 1024);
+                if (xw) {
+#pragma unroll
+                    for (int j = 0; j < kXDma; ++j) {
+                        const int k = k0 + xk[j];
+                        const char *p = k + 8 <= a.d_out ? xp[j]
+                                        : k < a.d_out    ? reinterpret_cast<const char *>(a.tail + int64_t(xtok[j]) * 8)
+                                                         : zeros;
+                        dma16(p, xbase + j * 1024);
+                    }
+                }
+            }
+        } else if (i < nst) {
+            const lora_seg_desc *d = a.seg + cs;
+            const int r = d->rank, begin = d->start, end = begin + d->len;
+            const uint16_t *A = reinterpret_cast<const uint16_t *>(d->A);
+#pragma unroll
+            for (int j = 0; j < kWDma; ++j) {
+                const int rank = cj + (wrow[j] & 15);
+                const char *p = reinterpret_cast<const char *>(A + int64_t(rank) * a.d_in + wcol[j]);
+                dma16(rank < r ? p : zeros, wbase + j * 1024);
+            }
+            if (xw) {
+#pragma unroll
+                for (int j = 0; j < kXDma; ++j) {
+                    const char *p = reinterpret_cast<const char *>(a.ur + int64_t(xpos[j]) * a.ldu + 2 * cj + xk[j]);
+                    dma16(xpos[j] >= begin && xpos[j] < end ? p : zeros, xbase + j * 1024);
+                }
+            }
+            cj += 16;
+            if (cj >= r) {
+                cj = 0;
+                ++cs;
+            }
+        } else { // past the end: keeps the number of loads in flight
+#pragma unroll
+            for (int j = 0; j < kWDma; ++j) dma16(zeros, wbase + j * 1024);
+            if (xw) {
+#pragma unroll
+                for (int j = 0; j < kXDma; ++j) dma16(zeros, xbase + j * 1024);
+            }
+        }
+    };
+
+    // fragment places in a stage
+    uint32_t xoff[G::TM], woff[2]; // W0: tiles t and t + 1 are the halves of one unit, t / 2 moves 4 units
+#pragma unroll
+    for (int i = 0; i < G::TM; ++i) {
+        const int row = (wr * G::TM + i) * 16 + m;
+        xoff[i] = uint32_t(kWBytes + row * 64 + ((g ^ ((row >> 1) & 3)) << 4));
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int row = 8 * g + 4 * h + (m >> 2);
+        woff[h] = uint32_t(row * kCols * 2);
+    }
+    auto wunit = [&](int t) { // slot of this lane's unit of tile t (row % 4 = m / 4)
+        const int un = wc * 2 * G::TN + (t >> 1) * 4 + (m & 3);
+        return uint32_t(((un ^ ((m >> 2) << 2)) << 4) + 8 * (t & 1));
+    };
+
+    floatx4 acc[G::TN][G::TM];
+#pragma unroll
+    for (int t = 0; t < G::TN; ++t)
+#pragma unroll
+        for (int i = 0; i < G::TM; ++i) acc[t][i] = floatx4{};
+
+    // The fragments of stage i, once it is there; refills the ring.
+    auto stage = [&](int i, bf16x8(&wf)[G::TN], bf16x8(&xf)[G::TM]) {
+        // this wave's loads of stage i are done (later stages' may be in flight) ...
+        if (xw) __builtin_amdgcn_s_waitcnt(waitcnt_vm((kWDma + kXDma) * (kStages - 2)));
+        else __builtin_amdgcn_s_waitcnt(waitcnt_vm(kWDma * (kStages - 2)));
+        // ... and every wave's, and every wave has read stage i - 1
+        __builtin_amdgcn_s_barrier();
+        issue(i + kStages - 1);
+        const char *st = lds + (i % kStages) * kStageBytes;
+#pragma unroll
+        for (int t = 0; t < G::TN; ++t) {
+            const u32x2 lo = read_tr(st + woff[0] + wunit(t)), hi = read_tr(st + woff[1] + wunit(t));
+            wf[t] = __builtin_bit_cast(bf16x8, u32x4{lo[0], lo[1], hi[0], hi[1]});
+        }
+#pragma unroll
+        for (int k = 0; k < G::TM; ++k) xf[k] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(st + xoff[k]));
+    };
+    constexpr int kWaitLgkm0 = 15 | (3 << 14) | (7 << 4); // this wave's fragment reads are done before the next barrier
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
+    const int nbase = k_end - k_begin;
+    for (int i = 0; i < nbase; ++i) {
+        bf16x8 wf[G::TN], xf[G::TM];
+        stage(i, wf, xf);
+#pragma unroll
+        for (int k = 0; k < G::TM; ++k)
+#pragma unroll
+            for (int t = 0; t < G::TN; ++t)
+                acc[t][k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[t], xf[k], acc[t][k], 0, 0, 0);
+        __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+    }
+    // Correction: a step's products go to the rows of its segment alone, so that a
+    // NaN or infinity in one adapter (times the other rows' zeros) stays with it.
+    for (int i = nbase, s = s0, j = 0; i < nst; ++i) {
+        const lora_seg_desc *d = a.seg + s;
+        const int begin = d->start, end = begin + d->len;
+        bf16x8 wf[G::TN], xf[G::TM];
+        stage(i, wf, xf);
+#pragma unroll
+        for (int k = 0; k < G::TM; ++k) {
+            const int p0 = m0 + (wr * G::TM + k) * 16;
+            if (p0 + 16 <= begin || p0 >= end) continue; // wave-uniform
+            const bool mine = p0 + m >= begin && p0 + m < end;
+#pragma unroll
+            for (int t = 0; t < G::TN; ++t) {
+                const floatx4 v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[t], xf[k], floatx4{}, 0, 0, 0);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[t][k][q] += mine ? v[q] : 0.f;
+            }
+        }
+        __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+        j += 16;
+        if (j >= d->rank) {
+            j = 0;
+            ++s;
+        }
+    }
+    // no direct load may still be writing this workgroup's LDS when it ends
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+
+    // lane: 16 columns (8 for TN = 2) of each of its rows, as 16-byte pieces
+#pragma unroll
+    for (int k = 0; k < G::TM; ++k) {
+        const int p = m0 + (wr * G::TM + k) * 16 + m;
+        if (p >= a.T) continue;
+#pragma unroll
+        for (int h = 0; h < G::TN / 2; ++h) {
+            const int c = c0 + wc * 16 * G::TN + h * 32 + g * 8;
+            if (c >= a.d_in) continue; // d_in is a multiple of 8
+            const floatx4 lo = acc[2 * h][k], hi = acc[2 * h + 1][k];
+            if (a.splits > 1) {
+                float *o = a.part + (int64_t(split) * a.T + p) * a.d_in + c;
+                *reinterpret_cast<floatx4 *>(o) = lo;
+                *reinterpret_cast<floatx4 *>(o + 4) = hi;
+            } else {
+                *reinterpret_cast<u32x4 *>(a.dx + int64_t(a.perm[p]) * a.lddx + c) =
+                    u32x4{pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]), pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3])};
+            }
+        }
+    }
+}
+
+// dx row = sum of the splits' sums, in split order.
+__global__ __launch_bounds__(256) void dgrad_reduce_kernel(DgradArgs a)
+{
+    const int64_t u = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    const int upr = a.d_in / 8;
+    const int64_t p = u / upr;
+    if (p >= a.T) return;
+    const int c = int(u % upr) * 8;
+    const float *src = a.part + p * a.d_in + c;
+    const int64_t pitch = int64_t(a.T) * a.d_in;
+    floatx4 lo = floatx4{}, hi = floatx4{};
+    for (int s = 0; s < a.splits; ++s, src += pitch) {
+        lo += *reinterpret_cast<const floatx4 *>(src);
+        hi += *reinterpret_cast<const floatx4 *>(src + 4);
+    }
+    *reinterpret_cast<u32x4 *>(a.dx + int64_t(a.perm[p]) * a.lddx + c) =
+        u32x4{pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]), pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3])};
+}
+
+int rows_of(int32_t T) { return T <= 64 ? 64 : 256; }
+
+// Splits of the summed axis: as many as fill the chip in one round, with at
+// least 8 stages each.
+int splits_of(int64_t tiles, int32_t d_out)
+{
+    const int64_t stages = (int64_t(d_out) + kBK - 1) / kBK;
+    return int(std::max<int64_t>(1, std::min<int64_t>({kFill / tiles, stages / 8, kMaxSplits})));
+}
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+// dy's tail columns, and the splits' sums: splits x tiles <= kFill tiles of at most
+// 256 x 256, and at most kMaxSplits of T x d_in.
+size_t tail_bytes(int32_t T) { return up256(size_t(T) * 16); }
+size_t part_bytes(int32_t T, int32_t d_in)
+{
+    return std::min(size_t(kFill) * 256 * kCols * 4, up256(size_t(T) * size_t(d_in) * 4 * kMaxSplits));
+}
+
+} // namespace
+
+size_t fused_backward_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out, int32_t max_rank)
+{
+    return up256(sgmv_backward_workspace_bytes(T, d_in, d_out, max_rank)) + tail_bytes(T) + part_bytes(T, d_in);
+}
+
+int launch_fused_backward(hipStream_t s, const BackwardArgs &b, const void *W0, const PlanView &p, void *ws)
+{
+    const lora_plan_header *h = p.h;
+    const int T = h->num_tokens;
+    const int max_rank = h->max_rank < 1 ? 1 : h->max_rank;
+    DgradArgs a{};
+    const int rows = rows_of(T);
+    a.tiles_m = (T + rows - 1) / rows;
+    a.tiles_n = (b.d_in + kCols - 1) / kCols;
+    const int64_t tiles = int64_t(a.tiles_m) * a.tiles_n;
+    if (tiles > (int64_t(1) << 31) - 1) return fail(LORA_ERR_ARG, "fused backward: too many tiles");
+    a.splits = splits_of(tiles, b.d_out);
+    const int64_t units = int64_t(T) * (b.d_in / 8);
+    if ((units + 255) / 256 > (int64_t(1) << 31) - 1 || T > (1 << 27))
+        return fail(LORA_ERR_ARG, "fused backward: too many rows");
+    char *w = static_cast<char *>(ws) + up256(sgmv_backward_workspace_bytes(T, b.d_in, b.d_out, max_rank));
+    // the adapters' gradients, and u
+    if (h->num_sorted > 0) {
+        BackwardArgs q = b;
+        q.dx = nullptr;
+        const int st = launch_sgmv_backward(s, q, p, ws, &a.ur, &a.ldu);
+        if (st) return st;
+    }
+    a.dy = static_cast<const uint16_t *>(b.dy);
+    a.lddy = b.lddy;
+    a.W0 = static_cast<const uint16_t *>(W0);
+    a.d_in = b.d_in;
+    a.d_out = b.d_out;
+    a.perm = reinterpret_cast<const int32_t *>(p.dev + h->perm_offset);
+    a.segidx = reinterpret_cast<const int32_t *>(p.dev + h->segidx_offset);
+    a.seg = reinterpret_cast<const lora_seg_desc *>(p.dev + h->seg_offset);
+    a.T = T;
+    a.Tp = h->num_sorted;
+    a.dx = static_cast<uint16_t *>(b.dx);
+    a.lddx = b.lddx;
+    a.part = reinterpret_cast<float *>(w + tail_bytes(T));
+    hipError_t e = hipSuccess;
+    if (b.d_out % 8) {
+        uint16_t *tail = reinterpret_cast<uint16_t *>(w);
+        a.tail = tail;
+        launch_kernel(dgrad_tail_kernel, dim3(unsigned((int64_t(T) * 8 + 255) / 256)), dim3(256), 0, s, a.dy, a.lddy, T,
+                      a.d_out, tail);
+        if ((e = hipGetLastError()) != hipSuccess)
+            return fail(LORA_ERR_HIP, "fused backward tail launch: %s", hipGetErrorString(e));
+    }
+    const dim3 grid{unsigned(tiles * a.splits)};
+    if (rows == 64) launch_kernel(dgrad_kernel<64>, grid, dim3(kThreads), 0, s, a);
+    else launch_kernel(dgrad_kernel<256>, grid, dim3(kThreads), 0, s, a);
+    if ((e = hipGetLastError()) != hipSuccess) return fail(LORA_ERR_HIP, "fused backward launch: %s", hipGetErrorString(e));
+    if (a.splits > 1) {
+        launch_kernel(dgrad_reduce_kernel, dim3(unsigned((units + 255) / 256)), dim3(256), 0, s, a);
+        if ((e = hipGetLastError()) != hipSuccess)
+            return fail(LORA_ERR_HIP, "fused backward reduce launch: %s", hipGetErrorString(e));
+    }
+    return LORA_OK;
+}
+
+} // namespace lora

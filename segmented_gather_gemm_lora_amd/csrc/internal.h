@@ -148,7 +148,12 @@ struct BackwardArgs {
     bool vec_x, vec_dy, vec_dx; // rows are whole aligned 16-byte pieces
 };
 size_t sgmv_backward_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out, int32_t max_rank);
-int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p, void *ws);
+// u_rows / ldu: where the call leaves u in rows (bf16 calls: per position and 16
+// ranks, 16 hi then 16 lo halves), computed when asked for or needed.
+int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p, void *ws,
+                         const uint16_t **u_rows = nullptr, int64_t *ldu = nullptr);
+size_t fused_backward_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out, int32_t max_rank);
+int launch_fused_backward(hipStream_t s, const BackwardArgs &b, const void *W0, const PlanView &p, void *ws);
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

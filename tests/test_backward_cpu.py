@@ -59,6 +59,51 @@ def test_refusals(kw, status):
     assert B.last_error()
 
 
+def run_fused(plan, **kw):
+    a = dict(dtype=B.LORA_BF16, x=FX, ldx=64, d_in=64, W0=FX + 0x80000, dy=FX + 0x100000, lddy=128, d_out=128,
+             gA=FX + 0x200000, gB=FX + 0x300000, n=3, flags=0, dx=FX + 0x400000, lddx=64, ws=FX + 0x500000, ws_bytes=BIG)
+    a.update(kw)
+    return B.load().lora_fused_linear_backward(None, a["dtype"], a["x"], a["ldx"], a["d_in"], a["W0"], a["dy"], a["lddy"],
+                                               a["d_out"], plan.dev(), a["gA"], a["gB"], a["n"], a["flags"], a["dx"],
+                                               a["lddx"], a["ws"], a["ws_bytes"])
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=B.LORA_F32), "LORA_ERR_DTYPE"),
+    (dict(W0=None), "LORA_ERR_ARG"),
+    (dict(dx=None), "LORA_ERR_ARG"),
+    (dict(x=None), "LORA_ERR_ARG"),
+    (dict(dy=None), "LORA_ERR_ARG"),
+    (dict(lddy=127), "LORA_ERR_ARG"),
+    (dict(lddy=132), "LORA_ERR_ALIGN"),
+    (dict(ldx=68), "LORA_ERR_ALIGN"),
+    (dict(lddx=68), "LORA_ERR_ALIGN"),
+    (dict(x=FX + 8), "LORA_ERR_ALIGN"),
+    (dict(dy=FX + 0x100008), "LORA_ERR_ALIGN"),
+    (dict(dx=FX + 0x400008), "LORA_ERR_ALIGN"),
+    (dict(W0=FX + 0x80008), "LORA_ERR_ALIGN"),
+    (dict(d_in=60), "LORA_ERR_ALIGN"),
+    (dict(n=2), "LORA_ERR_ADAPTER_ID"),
+    (dict(flags=4), "LORA_ERR_ARG"),
+    (dict(ws_bytes=1000), "LORA_ERR_WORKSPACE"),
+    (dict(ws=FX + 0x500004), "LORA_ERR_ALIGN"),
+])
+def test_fused_refusals(kw, status):
+    st = run_fused(plan_of([0, 2, 2, -1], 3, [16, 8, 4]), **kw)
+    assert B.STATUS[st] == status, (kw, B.STATUS[st], B.last_error())
+
+
+def test_fused_without_tokens_is_a_no_op():
+    assert run_fused(plan_of([], 3, [16, 8, 4]), x=None, dy=None, dx=None, W0=None, ws=None, ws_bytes=0) == 0
+
+
+def test_fused_workspace_grows_with_every_size():
+    f = lambda T, i, o, r: B.lora_workspace_bytes(B.LORA_OP_FUSED_BACKWARD, T, i, o, r)  # noqa: E731
+    sizes = [f(T, 256, 512, 16) for T in range(0, 70000, 37)]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+    assert f(400, 256, 512, 16) <= f(400, 256, 512, 17) <= f(400, 512, 512, 17) <= f(400, 512, 1024, 17)
+
+
 def test_refusals_of_segments():
     plan = plan_of([0, 2], 3, [16, 8, 4])
     L = B.load()
