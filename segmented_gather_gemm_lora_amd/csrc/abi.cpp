@@ -852,8 +852,12 @@ static int make_backward_args(int dtype, const void *x, int64_t ldx, int32_t d_i
         if (!elem_aligned(dx, es)) return fail(LORA_ERR_ALIGN, "dx is not aligned to its element size");
         if (dx == dy || (grads && dx == x)) return fail(LORA_ERR_ARG, "dx is x or dy");
     }
-    auto whole = [es](const void *p, int64_t ld, int32_t d) {
-        return aligned16(p) && (ld * es) % 16 == 0 && (int64_t(d) * es) % 16 == 0;
+    // whole aligned 16-byte pieces; 32-bit byte offsets reach every row, and every
+    // row of A or B (at most 256 of d elements)
+    auto whole = [es, h](const void *p, int64_t ld, int32_t d) {
+        const int64_t most = int64_t(1) << 32;
+        return aligned16(p) && (ld * es) % 16 == 0 && (int64_t(d) * es) % 16 == 0 && ld < most / es / h->num_tokens &&
+               int64_t(d) * LORA_MAX_RANK * es < most;
     };
     b->dtype = dtype;
     b->x = x;

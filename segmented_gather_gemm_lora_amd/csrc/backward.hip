@@ -74,6 +74,14 @@ __device__ __forceinline__ bf16x8 join8(u32x2 a, u32x2 b)
     return __builtin_bit_cast(bf16x8, u32x4{a[0], a[1], b[0], b[1]});
 }
 
+// 16 bytes at a wave-uniform base (kept in scalar registers) plus a lane's 32-bit
+// byte offset: no 64-bit address per load in vector registers.
+__device__ __forceinline__ u32x4 load16(const void *base, uint32_t off)
+{
+    return *(gptr<u32x4>)(as_global<char>(base) + off);
+}
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 constexpr int kWin = 32; // sorted positions of one step over rows; u and v are stored in windows of it
 
 template <int DT> struct Elem;
@@ -116,10 +124,12 @@ template <int DT> __device__ __forceinline__ int col(int g, int v)
 }
 
 struct Item {
-    int32_t seg;
-    int32_t begin, end; // sorted positions
-    int32_t slot;       // partial sums' place, -1: the gradient itself
+    uint64_t grad_A, grad_B; // the adapter's gradients, 0: not wanted
+    int32_t begin, end;      // sorted positions
+    int32_t rank;
+    int32_t slot;            // partial sums' place, -1: the gradient itself
 };
+static_assert(sizeof(Item) == 32, "one record per item");
 struct Split { // a segment whose sums lie in `count` slots from slot0
     int32_t seg, slot0, count, reserved;
 };
@@ -196,11 +206,16 @@ __device__ void list_items(const BwdArgs &a, int *scan, int nthreads)
     int item0 = 0, slot0 = 0, split0 = 0;
     for (int s0 = 0; s0 < a.S; s0 += nthreads) {
         const int s = s0 + tid;
-        int start = 0, end = 0, n = 0;
+        int start = 0, end = 0, n = 0, r = 0;
+        uint64_t gA = 0, gB = 0;
         if (s < a.S) {
-            start = a.seg[s].start;
-            end = start + a.seg[s].len;
+            const lora_seg_desc &d = a.seg[s];
+            start = d.start;
+            end = start + d.len;
+            r = d.rank;
             n = (end - 1) / a.span - start / a.span + 1;
+            gA = a.grad_A ? a.grad_A[d.adapter] : 0;
+            gB = a.grad_B ? a.grad_B[d.adapter] : 0;
         }
         const int ns = n > 1 ? n : 0, nq = n > 1 ? 1 : 0;
         int *sc[3] = {scan, scan + nthreads, scan + 2 * nthreads};
@@ -218,7 +233,7 @@ __device__ void list_items(const BwdArgs &a, int *scan, int nthreads)
         for (int i = 0; i < n; ++i) {
             const int b = i == 0 ? start : (start / a.span + i) * a.span;
             const int e = i == n - 1 ? end : (start / a.span + i + 1) * a.span;
-            a.items[it + i] = Item{s, b, e, n > 1 ? sl + i : -1};
+            a.items[it + i] = Item{gA, gB, b, e, r, n > 1 ? sl + i : -1};
         }
         if (nq) a.splits[sp] = Split{s, sl, n, 0};
         item0 += sc[0][nthreads - 1];
@@ -230,136 +245,275 @@ __device__ void list_items(const BwdArgs &a, int *scan, int nthreads)
 
 constexpr int kShrinkWaves = 8;
 
-template <int DT, bool VEC, int RT>
-__global__ __launch_bounds__(kShrinkWaves * 64) void bwd_shrink_kernel(BwdArgs a)
+// The operands of NS steps of a wave: MB blocks of 16 rows of x (dy), RT rank
+// tiles of A (B).
+template <int DT, int RT, int MB, int NS> struct ShrinkOps {
+    typename Elem<DT>::F xf[NS][MB];
+    typename Elem<DT>::F wf[NS][RT];
+};
+
+// One side's operands of a workgroup: rows of x or dy, and A or B.
+struct ShrinkSide {
+    const void *src, *mat;
+    int64_t ld;
+    int K, r, rt0;
+    const int32_t *rows;
+    int n;
+};
+
+// A lane's rows: byte offsets of its first element of every row and of its part
+// of A or B (VEC; all below 4 GiB), or the rows' tokens.
+template <int RT, int MB> struct ShrinkOffs {
+    uint32_t x[MB], w[RT];
+};
+
+template <int DT, int SIDE, bool BVEC, int RT, int MB>
+__device__ __forceinline__ ShrinkOffs<RT, MB> shrink_offs(const ShrinkSide &sd, int lane)
+{
+    constexpr int es = int(sizeof(typename Elem<DT>::T));
+    const int m = lane & 15, g = lane >> 4;
+    ShrinkOffs<RT, MB> o;
+#pragma unroll
+    for (int b = 0; b < MB; ++b) // rows past n: never stored
+        o.x[b] = uint32_t(sd.rows[min(16 * b + m, sd.n - 1)]) * uint32_t(sd.ld * es) + 16 * g;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        if constexpr (BVEC) { // 32 rows x 2 RT pieces of 16 bytes a step, RT pieces a lane
+            const int q = lane + 64 * i, j = 16 * sd.rt0 + 8 * (q % (2 * RT));
+            o.w[i] = uint32_t((q / (2 * RT)) * sd.r + (j < sd.r ? j : 0)) * es;
+        } else {
+            const int j = 16 * (sd.rt0 + i) + m;
+            o.w[i] = uint32_t(j < sd.r ? j : sd.r - 1) * uint32_t(sd.K * es) + 16 * g;
+        }
+    }
+    return o;
+}
+
+// The operands of steps k .. (k wave-uniform).  VEC: rows by 16 bytes; W of side 0
+// by rank rows, of side 1 by 16-byte pieces (BVEC: ranks a multiple of 8); FULL:
+// every step inside K.  Else element by element.
+template <int DT, bool VEC, int SIDE, bool BVEC, bool FULL, int RT, int MB, int NS>
+__device__ __forceinline__ void shrink_load(ShrinkOps<DT, RT, MB, NS> &o, const ShrinkSide &sd,
+                                            const ShrinkOffs<RT, MB> &off, int k, int lane)
 {
     using E = Elem<DT>;
     using T = typename E::T;
     using F = typename E::F;
-    constexpr int W = kShrinkWaves, NS = RT >= 4 ? 2 : 4;
+    const int m = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+        const int ks = k + s * E::kStep;
+        if constexpr (VEC) {
+            // past K: the last units of a row, replaced by zero
+            const int kc = FULL || ks < sd.K ? ks : 0;
+            const bool in = FULL || ks + E::kVec * g < sd.K;
+            const uint32_t back = in ? 0 : uint32_t(16 * g); // the row's first unit
+            const char *xb = static_cast<const char *>(sd.src) + int64_t(kc) * int(sizeof(T));
+#pragma unroll
+            for (int b = 0; b < MB; ++b) {
+                u32x4 w = load16(xb, off.x[b] - back);
+                if (!in) w = u32x4{};
+                o.xf[s][b] = __builtin_bit_cast(F, w);
+            }
+        } else {
+#pragma unroll
+            for (int b = 0; b < MB; ++b)
+                o.xf[s][b] = load_row<DT, false>(
+                    as_global<T>(sd.src) + int64_t(off.x[b]) * sd.ld, ks + E::kVec * g, sd.K);
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            if constexpr (VEC && SIDE == 0) {
+                const int kc = FULL || ks < sd.K ? ks : 0;
+                const bool in = FULL || ks + E::kVec * g < sd.K;
+                u32x4 w = load16(static_cast<const char *>(sd.mat) + int64_t(kc) * int(sizeof(T)), off.w[i] - (in ? 0 : uint32_t(16 * g)));
+                if (!in) w = u32x4{};
+                o.wf[s][i] = __builtin_bit_cast(F, w);
+            } else if constexpr (BVEC) {
+                const int kr = ks + (lane + 64 * i) / (2 * RT);
+                const bool in = FULL || kr < sd.K;
+                const int kc = FULL || ks < sd.K ? ks : 0;
+                u32x4 w = load16(static_cast<const char *>(sd.mat) + int64_t(kc) * sd.r * 2, in ? off.w[i] : 0);
+                if (!in) w = u32x4{};
+                o.wf[s][i] = __builtin_bit_cast(F, w);
+            } else if constexpr (SIDE == 0) {
+                const int j = 16 * (sd.rt0 + i) + m;
+                o.wf[s][i] = load_row<DT, false>(as_global<T>(sd.mat) + int64_t(j < sd.r ? j : sd.r - 1) * sd.K, ks + E::kVec * g, sd.K);
+            } else {
+                o.wf[s][i] = load_col<DT>(as_global<T>(sd.mat), sd.r, 16 * (sd.rt0 + i) + m, ks + E::kVec * g, sd.K);
+            }
+        }
+    }
+}
+
+template <int DT, bool BVEC, int RT, int MB, int NS>
+__device__ __forceinline__ void shrink_mma(const ShrinkOps<DT, RT, MB, NS> &o, floatx4 (&acc)[MB][RT], char *tiles,
+                                           int lane)
+{
+    using F = typename Elem<DT>::F;
+    const int m = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+        F wf[RT];
+        if constexpr (BVEC) {
+            // 32-byte granules (one rank tile of a row), moved so that 4 rows of a
+            // tile fall in distinct banks
+            char *tile = tiles + (s & 1) * 1024 * RT;
+            auto gran = [](int kr, int t) { return kr * 32 * RT + (t ^ ((RT == 4 ? kr >> 1 : kr >> 2) & (RT - 1))) * 32; };
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                const int q = lane + 64 * i, kr = q / (2 * RT), pc = q % (2 * RT);
+                *reinterpret_cast<u32x4 *>(tile + gran(kr, pc >> 1) + (pc & 1) * 16) = __builtin_bit_cast(u32x4, o.wf[s][i]);
+            }
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                u32x2 h[2];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) h[b] = read_tr(tile + gran(8 * g + 4 * b + (m >> 2), i) + (m & 3) * 8);
+                wf[i] = __builtin_bit_cast(F, u32x4{h[0][0], h[0][1], h[1][0], h[1][1]});
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < RT; ++i) wf[i] = o.wf[s][i];
+        }
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+#pragma unroll
+            for (int i = 0; i < RT; ++i) acc[b][i] = mma<DT>(o.xf[s][b], wf[i], acc[b][i]);
+    }
+}
+
+// This wave's part of the sums: chunks of NS steps, the loads of the next chunk
+// issued before the products of the current one (PIPE).
+template <int DT, bool VEC, int SIDE, bool BVEC, bool PIPE, int RT, int MB, int NS>
+__device__ __forceinline__ void shrink_sum(floatx4 (&acc)[MB][RT], const ShrinkSide &sd, char *tiles, int wave, int lane)
+{
+    constexpr int kChunk = NS * Elem<DT>::kStep, kNext = kShrinkWaves * kChunk;
+    ShrinkOps<DT, RT, MB, NS> o0, o1;
+    ShrinkOffs<RT, MB> off{};
+    if constexpr (VEC) off = shrink_offs<DT, SIDE, BVEC, RT, MB>(sd, lane);
+    else
+        for (int b = 0; b < MB; ++b) off.x[b] = uint32_t(sd.rows[min(16 * b + (lane & 15), sd.n - 1)]);
+    int k = wave * kChunk;
+    if constexpr (VEC && PIPE) {
+        if (k + kChunk <= sd.K) {
+            shrink_load<DT, VEC, SIDE, BVEC, true>(o0, sd, off, k, lane);
+            for (;;) {
+                k += kNext;
+                const bool more0 = k + kChunk <= sd.K;
+                if (more0) shrink_load<DT, VEC, SIDE, BVEC, true>(o1, sd, off, k, lane);
+                shrink_mma<DT, BVEC>(o0, acc, tiles, lane);
+                if (!more0) break;
+                k += kNext;
+                const bool more1 = k + kChunk <= sd.K;
+                if (more1) shrink_load<DT, VEC, SIDE, BVEC, true>(o0, sd, off, k, lane);
+                shrink_mma<DT, BVEC>(o1, acc, tiles, lane);
+                if (!more1) break;
+            }
+        }
+    } else {
+        for (; VEC && k + kChunk <= sd.K; k += kNext) {
+            shrink_load<DT, VEC, SIDE, BVEC, true>(o0, sd, off, k, lane);
+            shrink_mma<DT, BVEC>(o0, acc, tiles, lane);
+        }
+    }
+    for (; k < sd.K; k += kNext) { // the last, partial chunk
+        shrink_load<DT, VEC, SIDE, BVEC, false>(o0, sd, off, k, lane);
+        shrink_mma<DT, BVEC>(o0, acc, tiles, lane);
+    }
+}
+
+// MB = 1: a workgroup takes a block of 16 rows; MB = 4: a chunk of up to 64, so
+// that A and B are read from L2 once for 64 rows.
+template <int DT, bool VEC, int RT, int MB>
+__global__ __launch_bounds__(kShrinkWaves * 64) void bwd_shrink_kernel(BwdArgs a)
+{
+    using E = Elem<DT>;
+    constexpr int W = kShrinkWaves, NS = RT * MB >= 4 ? 2 : 4;
+    constexpr bool kPipe = RT * MB > 1; // one rank tile of 16 rows: no gain
     constexpr int kTile = 1024 * RT; // LDS of one step's B tile: 32 rows of 16 RT ranks
     constexpr int kRed = W * RT * 1024, kTiles = W * 2 * kTile;
     constexpr int kScan = 3 * 4 * W * 64;
     constexpr int kLds = kRed > kTiles ? kRed : kTiles;
     __shared__ __attribute__((aligned(16))) char lds[kLds > kScan ? kLds : kScan];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int m = lane & 15, g = lane >> 4;
-    const int nside = a.sides == 3 ? 2 : 1;
-    if (int(blockIdx.x) == a.nblk * nside) {
-        list_items(a, reinterpret_cast<int *>(lds), W * 64);
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int units = MB == 1 ? a.nblk : a.nchunk;
+    // Workgroup b runs on XCD b % 8: an XCD takes a run of consecutive units, so
+    // that a segment's A and B are fetched into few L2s; the list of items first
+    // (one workgroup), then the longer side.
+    const int run = (units + 7) / 8, q = int(blockIdx.x >> 3) - 1;
+    if (q < 0) {
+        if (blockIdx.x == 0) list_items(a, reinterpret_cast<int *>(lds), W * 64);
         return;
     }
-    const int blk = blockIdx.x / nside;
-    const int side = a.sides == 3 ? int(blockIdx.x) % 2 : a.sides - 1;
-    const lora_blk_desc *d = a.blk + blk;
-    const int r = d->rank, n = d->n, p0 = d->p0;
-    const float scale = d->scale;
-    const int row = d->rows[m] >= 0 ? d->rows[m] : d->rows[0]; // past n: never stored
-    const int K = side ? a.d_out : a.d_in;
-    const gptr<T> src = as_global<T>(side ? a.dy : a.x) + int64_t(row) * (side ? a.lddy : a.ldx);
-    const gptr<T> mat = as_global<T>(reinterpret_cast<const void *>(side ? d->B : d->A));
+    const int unit = int(blockIdx.x % 8) * run + q % run;
+    if (unit >= units) return;
+    const int side = a.sides == 3 ? (q < run) == (a.d_out >= a.d_in) : a.sides - 1;
+    const void *pA, *pB;
+    int r, n, p0;
+    float scale;
+    const int32_t *rows;
+    if constexpr (MB == 1) {
+        const lora_blk_desc *d = a.blk + unit;
+        pA = reinterpret_cast<const void *>(d->A), pB = reinterpret_cast<const void *>(d->B);
+        r = d->rank, n = d->n, p0 = d->p0, scale = d->scale, rows = d->rows;
+    } else {
+        const lora_chunk_desc *d = a.chunk + unit;
+        pA = reinterpret_cast<const void *>(d->A), pB = reinterpret_cast<const void *>(d->B);
+        r = d->rank, n = d->n, p0 = d->p0, scale = d->scale, rows = d->rows;
+    }
+    ShrinkSide sd = side ? ShrinkSide{a.dy, pB, a.lddy, a.d_out, r, 0, rows, n} : ShrinkSide{a.x, pA, a.ldx, a.d_in, r, 0, rows, n};
     const int ntiles = (r + 15) >> 4;
     const bool bvec = VEC && DT == LORA_BF16 && (r & 7) == 0; // B rows are whole 16-byte pieces
+    char *tiles = lds + wave * 2 * kTile;
 
     for (int rt0 = 0; rt0 < ntiles; rt0 += RT) {
-        floatx4 acc[RT];
+        floatx4 acc[MB][RT];
 #pragma unroll
-        for (int i = 0; i < RT; ++i) acc[i] = floatx4{};
-        for (int kb = wave * NS * E::kStep; kb < K; kb += W * NS * E::kStep) {
-            F xf[NS];
+        for (int b = 0; b < MB; ++b)
 #pragma unroll
-            for (int s = 0; s < NS; ++s) xf[s] = load_row<DT, VEC>(src, kb + s * E::kStep + E::kVec * g, K);
-            if (side == 0) {
-                F wf[NS][RT];
-#pragma unroll
-                for (int s = 0; s < NS; ++s)
-#pragma unroll
-                    for (int i = 0; i < RT; ++i) {
-                        const int j = 16 * (rt0 + i) + m;
-                        wf[s][i] = load_row<DT, VEC>(mat + int64_t(j < r ? j : r - 1) * K, kb + s * E::kStep + E::kVec * g, K);
-                    }
-#pragma unroll
-                for (int s = 0; s < NS; ++s)
-#pragma unroll
-                    for (int i = 0; i < RT; ++i) acc[i] = mma<DT>(xf[s], wf[s][i], acc[i]);
-            } else if (bvec) {
-                if constexpr (DT == LORA_BF16) {
-                    // 32 rows x 2 RT pieces of 16 bytes, RT pieces a lane
-                    u32x4 w[NS][RT];
-#pragma unroll
-                    for (int s = 0; s < NS; ++s)
-#pragma unroll
-                        for (int i = 0; i < RT; ++i) {
-                            const int q = lane + 64 * i, kr = kb + 32 * s + q / (2 * RT), j = 16 * rt0 + 8 * (q % (2 * RT));
-                            w[s][i] = *(gptr<u32x4>)(mat + int64_t(kr < K ? kr : K - 1) * r + (j < r ? j : 0));
-                            if (kr >= K) w[s][i] = u32x4{};
-                        }
-#pragma unroll
-                    for (int s = 0; s < NS; ++s) {
-                        // 32-byte granules (one rank tile of a row), moved so that 4 rows of a
-                        // tile fall in distinct banks
-                        char *tile = lds + (wave * 2 + (s & 1)) * kTile;
-#pragma unroll
-                        for (int i = 0; i < RT; ++i) {
-                            const int q = lane + 64 * i, kr = q / (2 * RT), pc = q % (2 * RT);
-                            const int gran = (pc >> 1) ^ ((RT == 4 ? kr >> 1 : kr >> 2) & (RT - 1));
-                            *reinterpret_cast<u32x4 *>(tile + kr * 32 * RT + gran * 32 + (pc & 1) * 16) = w[s][i];
-                        }
-#pragma unroll
-                        for (int i = 0; i < RT; ++i) {
-                            u32x2 h[2];
-#pragma unroll
-                            for (int b = 0; b < 2; ++b) {
-                                const int kr = 8 * g + 4 * b + (m >> 2);
-                                const int gran = i ^ ((RT == 4 ? kr >> 1 : kr >> 2) & (RT - 1));
-                                h[b] = read_tr(tile + kr * 32 * RT + gran * 32 + (m & 3) * 8);
-                            }
-                            acc[i] = mma<DT>(xf[s], join8(h[0], h[1]), acc[i]);
-                        }
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int s = 0; s < NS; ++s)
-#pragma unroll
-                    for (int i = 0; i < RT; ++i)
-                        acc[i] = mma<DT>(xf[s], load_col<DT>(mat, r, 16 * (rt0 + i) + m, kb + s * E::kStep + E::kVec * g, K), acc[i]);
-            }
-        }
+            for (int i = 0; i < RT; ++i) acc[b][i] = floatx4{};
+        sd.rt0 = rt0;
+        if (side == 0) shrink_sum<DT, VEC, 0, false, kPipe, RT, MB, NS>(acc, sd, tiles, wave, lane);
+        else if (!bvec) shrink_sum<DT, VEC, 1, false, false, RT, MB, NS>(acc, sd, tiles, wave, lane);
+        else if constexpr (VEC && DT == LORA_BF16) shrink_sum<DT, VEC, 1, true, kPipe, RT, MB, NS>(acc, sd, tiles, wave, lane);
         // lane l of tile i holds D[row 4 (l / 16) + q][rank l % 16]
         float *red = reinterpret_cast<float *>(lds);
-        __syncthreads(); // the tiles of every wave are read
 #pragma unroll
-        for (int i = 0; i < RT; ++i) *reinterpret_cast<floatx4 *>(red + ((wave * RT + i) * 64 + lane) * 4) = acc[i];
-        __syncthreads();
-        for (int idx = tid; idx < RT * 256; idx += W * 64) {
-            const int i = idx >> 8, l2 = (idx >> 2) & 63, q = idx & 3;
-            float sum = 0.f;
+        for (int b = 0; b < MB; ++b) {
+            __syncthreads(); // every wave is past its tiles, and past the last sums
 #pragma unroll
-            for (int w = 0; w < W; ++w) sum += red[((w * RT + i) * 64 + l2) * 4 + q];
-            const int mm = 4 * (l2 >> 4) + q, j = 16 * (rt0 + i) + (l2 & 15);
-            if (mm >= n || rt0 + i >= ntiles) continue;
-            const int p = p0 + mm;
-            const float t = j < r ? sum * scale : 0.f;
-            char *win = (side ? a.ut : a.vt) + int64_t(p / kWin) * E::kParts * a.r16 * kWin * E::kPart;
-            const int at = j * kWin + p % kWin;
-            if constexpr (DT == LORA_BF16) {
-                const uint32_t h = f32_to_bf16(t);
-                const bool fin = (h & 0x7f80u) != 0x7f80u; // an infinity or NaN has no rest
-                const float rest = fin ? t - bf16_to_f32(h) : 0.f;
-                const uint32_t mid = f32_to_bf16(rest);
-                uint16_t *o = reinterpret_cast<uint16_t *>(win) + at;
-                o[0] = uint16_t(h);
-                o[a.r16 * kWin] = uint16_t(mid);
-                o[2 * a.r16 * kWin] = uint16_t(f32_to_bf16(rest - bf16_to_f32(mid)));
-                if (side) {
-                    uint16_t *u = reinterpret_cast<uint16_t *>(a.ur) + int64_t(p) * 2 * a.r16 + 32 * (j >> 4) + (j & 15);
-                    u[0] = uint16_t(h);
-                    u[16] = uint16_t(mid);
+            for (int i = 0; i < RT; ++i) *reinterpret_cast<floatx4 *>(red + ((wave * RT + i) * 64 + lane) * 4) = acc[b][i];
+            __syncthreads();
+            for (int idx = tid; idx < RT * 256; idx += W * 64) {
+                const int i = idx >> 8, l2 = (idx >> 2) & 63, q = idx & 3;
+                float sum = 0.f;
+#pragma unroll
+                for (int w = 0; w < W; ++w) sum += red[((w * RT + i) * 64 + l2) * 4 + q];
+                const int mm = 16 * b + 4 * (l2 >> 4) + q, j = 16 * (rt0 + i) + (l2 & 15);
+                if (mm >= n || rt0 + i >= ntiles) continue;
+                const int p = p0 + mm;
+                const float t = j < r ? sum * scale : 0.f;
+                char *win = (side ? a.ut : a.vt) + int64_t(p / kWin) * E::kParts * a.r16 * kWin * E::kPart;
+                const int at = j * kWin + p % kWin;
+                if constexpr (DT == LORA_BF16) {
+                    const uint32_t h = f32_to_bf16(t);
+                    const bool fin = (h & 0x7f80u) != 0x7f80u; // an infinity or NaN has no rest
+                    const float rest = fin ? t - bf16_to_f32(h) : 0.f;
+                    const uint32_t mid = f32_to_bf16(rest);
+                    uint16_t *o = reinterpret_cast<uint16_t *>(win) + at;
+                    o[0] = uint16_t(h);
+                    o[a.r16 * kWin] = uint16_t(mid);
+                    o[2 * a.r16 * kWin] = uint16_t(f32_to_bf16(rest - bf16_to_f32(mid)));
+                    if (side) {
+                        uint16_t *u = reinterpret_cast<uint16_t *>(a.ur) + int64_t(p) * 2 * a.r16 + 32 * (j >> 4) + (j & 15);
+                        u[0] = uint16_t(h);
+                        u[16] = uint16_t(mid);
+                    }
+                } else {
+                    reinterpret_cast<float *>(win)[at] = t;
+                    if (side) reinterpret_cast<float *>(a.ur)[int64_t(p) * a.r16 + j] = t;
                 }
-            } else {
-                reinterpret_cast<float *>(win)[at] = t;
-                if (side) reinterpret_cast<float *>(a.ur)[int64_t(p) * a.r16 + j] = t;
             }
         }
         __syncthreads();
@@ -371,19 +525,22 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void bwd_shrink_kernel(BwdArgs a
 // ranks in groups of 16 RT.
 // ----------------------------------------------------------------------------
 constexpr int kGradWaves = 4;
+#define LORA_GOCC (RT == 1 ? 5 : RT == 2 ? 4 : 2)
+#define LORA_DOCC 2
+
 constexpr int kMaxSpan = 2048;
 
 // The wave's column fragments of one window, from its LDS tile: 32 rows of 128
 // bytes, unit 16 bytes, unit un of row q in slot un ^ (4 if q & 2): 4 rows
 // of a fragment read then fall in distinct banks.
 __device__ __forceinline__ int tile_at(int q, int un) { return q * 128 + ((un ^ ((q & 2) << 1)) << 4); }
-__device__ __forceinline__ bf16x8 tile_frag(const char *tile, int t, int m, int g, int step)
+// Rows 8 g .. + 7 of the 4 columns in half `half` of unit `un` (this lane's piece, of
+// the 16 columns that 4 lanes name).
+__device__ __forceinline__ bf16x8 tile_frag(const char *tile, int un, int half, int m, int g)
 {
-    // rows step * g .. + 7, columns of tile t: 8-byte pieces of 4 columns
-    const int un = (t >> 1) * 4 + (m & 3);
     u32x2 h[2];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) h[b] = read_tr(tile + tile_at(step * g + 4 * b + (m >> 2), un) + (t & 1) * 8);
+    for (int b = 0; b < 2; ++b) h[b] = read_tr(tile + tile_at(8 * g + 4 * b + (m >> 2), un) + 8 * half);
     return join8(h[0], h[1]);
 }
 
@@ -400,167 +557,199 @@ __device__ __forceinline__ void put4(float *dst, floatx4 v, int n, bool vec, boo
     }
 }
 
+// Operands of one window.  bf16 rows by 16 bytes (VEC): row (lane / 8) + 8 i, column
+// 8 (lane % 8), to be turned through the tile; else the column fragments
+// themselves.  fp32 takes a window in two halves of 16 rows.
+template <int DT, bool VEC, int RT> struct GradOps {
+    static constexpr int kHalves = DT == LORA_BF16 ? 1 : 2;
+    typename Elem<DT>::F xf[kHalves][4];
+    typename Elem<DT>::F uf[kHalves][RT][Elem<DT>::kParts];
+};
+
+struct GradSide {
+    const void *src, *parts; // x and u (dA) or dy and v (dB)
+    int64_t ld;
+    int D;
+};
+
 template <int DT, bool VEC, int RT>
-__device__ __forceinline__ void grad_item(const BwdArgs &a, const Item &it, int side, int c0, int rt0, int r,
-                                          float *dst, bool add, const int32_t *tok, char *tile)
+__device__ __forceinline__ void grad_load(GradOps<DT, VEC, RT> &o, const BwdArgs &a, const GradSide &sd, int begin, int end,
+                                          int w, int c0, int rt0, const int32_t *tok, int lane)
 {
     using E = Elem<DT>;
     using T = typename E::T;
-    const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
-    const int D = side ? a.d_out : a.d_in;
-    const gptr<T> src = as_global<T>(side ? a.dy : a.x);
-    const int64_t ld = side ? a.lddy : a.ldx;
-    const char *ft = side ? a.vt : a.ut;
-    const int w0 = it.begin / kWin, w1 = (it.end - 1) / kWin;
+    const int m = lane & 15, g = lane >> 4;
+    const int base = w * kWin;
+    const char *win = static_cast<const char *>(sd.parts) + int64_t(w) * E::kParts * a.r16 * kWin * E::kPart;
+    const uint32_t uoff = uint32_t(m * kWin + E::kVec * g) * E::kPart;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        const int j = min(16 * (rt0 + i), a.r16 - 16); // ranks past r16: clamped, not stored
+#pragma unroll
+        for (int h = 0; h < o.kHalves; ++h)
+#pragma unroll
+            for (int q = 0; q < E::kParts; ++q)
+                o.uf[h][i][q] = __builtin_bit_cast(
+                    typename E::F, load16(win + ((q * a.r16 + j) * kWin + 16 * h) * E::kPart, uoff));
+    }
+    auto token = [&](int p) { return tok[min(max(p, begin), end - 1) - begin]; };
+    if constexpr (DT == LORA_BF16 && VEC) {
+        const char *src = static_cast<const char *>(sd.src) + int64_t(c0) * 2;
+        // past the row: columns that are not stored
+        const uint32_t cc = c0 + 8 * (lane & 7) < sd.D ? 16 * (lane & 7) : 0, pitch = uint32_t(sd.ld * 2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            o.xf[0][i] = __builtin_bit_cast(bf16x8, load16(src, uint32_t(token(base + (lane >> 3) + 8 * i)) * pitch + cc));
+    } else {
+        const gptr<T> src = as_global<T>(sd.src);
+#pragma unroll
+        for (int h = 0; h < o.kHalves; ++h)
+#pragma unroll
+            for (int e = 0; e < E::kVec; ++e) {
+                const gptr<T> row = src + int64_t(token(base + 16 * h + E::kVec * g + e)) * sd.ld;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const T f = row[min(c0 + 16 * t + m, sd.D - 1)];
+                    if constexpr (DT == LORA_BF16) o.xf[h][t][e] = __builtin_bit_cast(__bf16, f);
+                    else o.xf[h][t][e] = f;
+                }
+            }
+    }
+}
+
+template <int DT, bool VEC, int RT>
+__device__ __forceinline__ void grad_mma(GradOps<DT, VEC, RT> &o, floatx4 (&acc)[4][RT], int side, int begin, int end, int w,
+                                         char *tile, int lane)
+{
+    using E = Elem<DT>;
+    using F = typename E::F;
+    const int m = lane & 15, g = lane >> 4, base = w * kWin;
+    if (base < begin || base + kWin > end) { // rows outside: zero on both sides (wave-uniform)
+        auto in = [&](int p) { return p >= begin && p < end; };
+#pragma unroll
+        for (int h = 0; h < o.kHalves; ++h) {
+            u32x4 keep; // this lane's elements of the summed axis
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (DT == LORA_BF16)
+                    keep[e] = (in(base + 8 * g + 2 * e) ? 0xffffu : 0u) | (in(base + 8 * g + 2 * e + 1) ? 0xffff0000u : 0u);
+                else keep[e] = in(base + 16 * h + 4 * g + e) ? ~0u : 0u;
+            }
+            auto mask = [&](F &f) { f = __builtin_bit_cast(F, __builtin_bit_cast(u32x4, f) & keep); };
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int q = 0; q < E::kParts; ++q) mask(o.uf[h][i][q]);
+            if constexpr (DT == LORA_BF16 && VEC) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (!in(base + (lane >> 3) + 8 * i)) o.xf[0][i] = bf16x8{};
+            } else {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) mask(o.xf[h][t]);
+            }
+        }
+    }
+    if constexpr (DT == LORA_BF16 && VEC) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<u32x4 *>(tile + tile_at((lane >> 3) + 8 * i, lane & 7)) = __builtin_bit_cast(u32x4, o.xf[0][i]);
+    }
+#pragma unroll
+    for (int h = 0; h < o.kHalves; ++h) {
+        F xf[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            if constexpr (DT == LORA_BF16 && VEC) xf[t] = tile_frag(tile, 2 * t + ((m & 3) >> 1), m & 1, m, g);
+            else xf[t] = o.xf[h][t];
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int q = 0; q < E::kParts; ++q)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    acc[t][i] = side ? mma<DT>(o.uf[h][i][q], xf[t], acc[t][i]) : mma<DT>(xf[t], o.uf[h][i][q], acc[t][i]);
+    }
+}
+
+template <int DT, bool VEC, int RT>
+__device__ __forceinline__ void grad_item(const BwdArgs &a, const GradSide &sd, int side, int begin, int end, int c0, int rt0,
+                                          int r, float *dst, bool add, const int32_t *tok, char *tile, int lane)
+{
+    const int w1 = (end - 1) / kWin;
     floatx4 acc[4][RT];
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int i = 0; i < RT; ++i) acc[t][i] = floatx4{};
-
-    for (int w = w0; w <= w1; ++w) {
-        const int base = w * kWin;
-        const bool edge = base < it.begin || base + kWin > it.end; // wave-uniform
-        const char *win = ft + int64_t(w) * E::kParts * a.r16 * kWin * E::kPart;
-        if constexpr (DT == LORA_BF16) {
-            bf16x8 xf[4];
-            if constexpr (VEC) {
-                // row (lane / 8) + 8 i of the window, 16 bytes at column 8 (lane % 8)
-                int cc = c0 + 8 * (lane & 7);
-                cc = cc < D ? cc : 0; // past the row: columns that are not stored
-                u32x4 xr[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int p = base + (lane >> 3) + 8 * i;
-                    const int pc = min(max(p, it.begin), it.end - 1);
-                    xr[i] = *(gptr<u32x4>)(src + int64_t(tok[pc - it.begin]) * ld + cc);
-                    if (edge && p != pc) xr[i] = u32x4{};
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<u32x4 *>(tile + tile_at((lane >> 3) + 8 * i, lane & 7)) = xr[i];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) xf[t] = tile_frag(tile, t, m, g, 8);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int p = base + 8 * g + e;
-                    const int pc = min(max(p, it.begin), it.end - 1);
-                    const gptr<T> row = src + int64_t(tok[pc - it.begin]) * ld;
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const int cc = min(c0 + col<DT>(m >> 2, 4 * t + (m & 3)), D - 1);
-                        const uint16_t h = row[cc];
-                        xf[t][e] = __builtin_bit_cast(__bf16, uint16_t(p == pc ? h : 0));
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                // ranks past r16 (the last group): clamped, not stored
-                const int j = min(16 * (rt0 + i), a.r16 - 16) + m;
-#pragma unroll
-                for (int q = 0; q < E::kParts; ++q) {
-                    u32x4 uw = *(gptr<u32x4>)(as_global<uint16_t>(win) + (q * a.r16 + j) * kWin + 8 * g);
-                    if (edge) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int p = base + 8 * g + 2 * e;
-                            if (p < it.begin || p >= it.end) uw[e] &= 0xffff0000u;
-                            if (p + 1 < it.begin || p + 1 >= it.end) uw[e] &= 0x0000ffffu;
-                        }
-                    }
-                    const bf16x8 uf = __builtin_bit_cast(bf16x8, uw);
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        acc[t][i] = side ? mma<DT>(uf, xf[t], acc[t][i]) : mma<DT>(xf[t], uf, acc[t][i]);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                floatx4 xf[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int p = base + 16 * h + 4 * g + e;
-                    const int pc = min(max(p, it.begin), it.end - 1);
-                    const gptr<T> row = src + int64_t(tok[pc - it.begin]) * ld;
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const int cc = min(c0 + col<DT>(m >> 2, 4 * t + (m & 3)), D - 1);
-                        const float f = row[cc];
-                        xf[t][e] = p == pc ? f : 0.f;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < RT; ++i) {
-                    const int j = min(16 * (rt0 + i), a.r16 - 16) + m;
-                    floatx4 uf = *(gptr<floatx4>)(as_global<float>(win) + j * kWin + 16 * h + 4 * g);
-                    if (edge) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int p = base + 16 * h + 4 * g + e;
-                            if (p < it.begin || p >= it.end) uf[e] = 0.f;
-                        }
-                    }
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        acc[t][i] = side ? mma<DT>(uf, xf[t], acc[t][i]) : mma<DT>(xf[t], uf, acc[t][i]);
-                }
-            }
-        }
+    // Four rank tiles: the next window's loads are issued before the current one's
+    // products (16384 rows of rank 64: 106 us, 118 without).  Fewer: more waves fit
+    // instead (rank 16, 4096 rows: 17.2 us, 18.8 with).
+    GradOps<DT, VEC, RT> o0;
+    int w = begin / kWin;
+    grad_load(o0, a, sd, begin, end, w, c0, rt0, tok, lane);
+    for (;;) {
+        GradOps<DT, VEC, RT> o1;
+        if (RT == 4 && w < w1) grad_load(o1, a, sd, begin, end, w + 1, c0, rt0, tok, lane);
+        grad_mma(o0, acc, side, begin, end, w, tile, lane);
+        if (++w > w1) break;
+        if (RT == 4) o0 = o1;
+        else grad_load(o0, a, sd, begin, end, w, c0, rt0, tok, lane);
     }
     // dA (side 0): D rows are columns of x, D columns are ranks.  dB: D rows
     // are ranks, D columns are columns of dy (rows of dB).
-    const bool vec = (reinterpret_cast<uintptr_t>(dst) & 15) == 0 && ((side ? r : D) & 3) == 0;
+    const int m = lane & 15, g = lane >> 4;
+    const bool vec = (reinterpret_cast<uintptr_t>(dst) & 15) == 0 && ((side ? r : sd.D) & 3) == 0;
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             if (side == 0) {
-                const int j = 16 * (rt0 + i) + m, c = c0 + col<DT>(g, 4 * t);
-                if (j < r && c < D) put4(dst + int64_t(j) * D + c, acc[t][i], D - c, vec, add);
+                const int j = 16 * (rt0 + i) + m, c = c0 + 16 * t + 4 * g;
+                if (j < r && c < sd.D) put4(dst + int64_t(j) * sd.D + c, acc[t][i], sd.D - c, vec, add);
             } else {
-                const int c = c0 + col<DT>(m >> 2, 4 * t + (m & 3)), j = 16 * (rt0 + i) + 4 * g;
-                if (c < D && j < r) put4(dst + int64_t(c) * r + j, acc[t][i], r - j, vec, add);
+                const int c = c0 + 16 * t + m, j = 16 * (rt0 + i) + 4 * g;
+                if (c < sd.D && j < r) put4(dst + int64_t(c) * r + j, acc[t][i], r - j, vec, add);
             }
         }
 }
 
-template <int DT, bool VEC>
-__global__ __launch_bounds__(kGradWaves * 64) void bwd_grad_kernel(BwdArgs a, int tiles_A, int tiles)
+// RT: rank tiles that a wave holds at once (the plan's largest rank, at most 4).
+template <int DT, bool VEC, int RT>
+__global__ __launch_bounds__(kGradWaves * 64, LORA_GOCC) void bwd_grad_kernel(BwdArgs a, int tiles_A, int tiles)
 {
-    __shared__ __attribute__((aligned(16))) char tiles_lds[kGradWaves * 4096];
+    __shared__ __attribute__((aligned(16))) char tiles_lds[DT == LORA_BF16 && VEC ? kGradWaves * 4096 : 16];
     __shared__ int32_t tok[kMaxSpan];
-    const int item = blockIdx.x / tiles, tl = blockIdx.x % tiles;
-    const Item it = a.items[item];
+    const int tl = blockIdx.x % tiles;
+    const Item it = a.items[blockIdx.x / tiles];
     const int side = tl >= tiles_A;
-    const lora_seg_desc *sd = a.seg + it.seg;
-    const int r = sd->rank;
-    const uint64_t grad = (side ? a.grad_B : a.grad_A)[sd->adapter];
+    const uint64_t grad = side ? it.grad_B : it.grad_A;
     if (!grad) return; // this adapter's gradient is not wanted
     for (int i = threadIdx.x; i < it.end - it.begin; i += kGradWaves * 64) tok[i] = a.perm[it.begin + i];
     __syncthreads();
-    const int wave = threadIdx.x >> 6;
+    const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, r = it.rank;
+    const GradSide sd = side ? GradSide{a.dy, a.vt, a.lddy, a.d_out} : GradSide{a.x, a.ut, a.ldx, a.d_in};
     const int c0 = (side ? tl - tiles_A : tl) * (64 * kGradWaves) + 64 * wave;
-    if (c0 >= (side ? a.d_out : a.d_in)) return;
+    if (c0 >= sd.D) return;
     float *dst = reinterpret_cast<float *>(grad);
     bool add = a.accumulate;
     if (it.slot >= 0) {
         dst = a.part + it.slot * a.part_stride + (side ? int64_t(r) * a.d_in : 0);
         add = false;
     }
-    char *tile = tiles_lds + wave * 4096;
+    char *tile = tiles_lds + (DT == LORA_BF16 && VEC ? wave * 4096 : 0);
     for (int rt0 = 0; 16 * rt0 < r;) {
-        if (r - 16 * rt0 <= 16) {
-            grad_item<DT, VEC, 1>(a, it, side, c0, rt0, r, dst, add, tok, tile);
-            rt0 += 1;
-        } else if (r - 16 * rt0 <= 32) {
-            grad_item<DT, VEC, 2>(a, it, side, c0, rt0, r, dst, add, tok, tile);
+        const int left = r - 16 * rt0;
+        if (RT >= 4 && left > 32) {
+            grad_item<DT, VEC, RT >= 4 ? 4 : 1>(a, sd, side, it.begin, it.end, c0, rt0, r, dst, add, tok, tile, lane);
+            rt0 += 4;
+        } else if (RT >= 2 && left > 16) {
+            grad_item<DT, VEC, RT >= 2 ? 2 : 1>(a, sd, side, it.begin, it.end, c0, rt0, r, dst, add, tok, tile, lane);
             rt0 += 2;
         } else {
-            grad_item<DT, VEC, 4>(a, it, side, c0, rt0, r, dst, add, tok, tile);
-            rt0 += 4;
+            grad_item<DT, VEC, 1>(a, sd, side, it.begin, it.end, c0, rt0, r, dst, add, tok, tile, lane);
+            rt0 += 1;
         }
     }
 }
@@ -597,50 +786,41 @@ __global__ __launch_bounds__(256) void bwd_reduce_kernel(BwdArgs a)
 constexpr int kDxWaves = 4;
 
 template <int DT, bool VEC>
-__global__ __launch_bounds__(kDxWaves * 64) void bwd_dx_kernel(BwdArgs a, int tiles)
+__global__ __launch_bounds__(kDxWaves * 64, LORA_DOCC) void bwd_dx_kernel(BwdArgs a, int tiles)
 {
     using E = Elem<DT>;
     using T = typename E::T;
-    using F = typename E::F;
     __shared__ __attribute__((aligned(16))) char tiles_lds[kDxWaves * 2 * 2048];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, m = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), m = lane & 15, g = lane >> 4;
     const lora_chunk_desc *d = a.chunk + blockIdx.x / tiles;
     const int c0 = int(blockIdx.x % tiles) * (64 * kDxWaves) + 64 * wave;
     if (c0 >= a.d_in) return;
     const int r = d->rank, n = d->n, p0 = d->p0;
-    const gptr<T> A = as_global<T>(reinterpret_cast<const void *>(d->A));
+    [[maybe_unused]] const gptr<T> A = as_global<T>(reinterpret_cast<const void *>(d->A));
     char *tile = tiles_lds + wave * 4096;
-    floatx4 acc[4][4]; // column tile, row block
+    // operands of 16 ranks: u of 4 row blocks, and A by rows (bf16 VEC: rank
+    // (lane / 8) + 8 i, column 8 (lane % 8)) or by column fragments
+    struct Ops {
+        typename E::F uf[4], af[4];
+    };
+    constexpr int kU = DT == LORA_BF16 ? 4 : int(sizeof(float)); // bytes of u in rows per rank
+    uint32_t uoff[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int i = 0; i < 4; ++i) uoff[i] = uint32_t(min(16 * i + m, n - 1)) * uint32_t(a.r16 * kU) + 16 * g; // past n: not stored
+    const char *ur = a.ur + int64_t(p0) * a.r16 * kU;
+    const uint32_t acol = c0 + 8 * (lane & 7) < a.d_in ? 16 * (lane & 7) : 0;
+    auto load = [&](Ops &o, int j0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[t][i] = floatx4{};
-    for (int j0 = 0, s = 0; j0 < r; j0 += 16, ++s) {
-        F uf[4], af[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int p = p0 + min(16 * i + m, n - 1); // past n: not stored
-            if constexpr (DT == LORA_BF16)
-                uf[i] = __builtin_bit_cast(F, *(gptr<u32x4>)(as_global<uint16_t>(a.ur) + int64_t(p) * 2 * a.r16 + 2 * j0 + 8 * g));
-            else
-                uf[i] = *(gptr<floatx4>)(as_global<float>(a.ur) + int64_t(p) * a.r16 + j0 + 4 * g);
-        }
+        for (int i = 0; i < 4; ++i) o.uf[i] = __builtin_bit_cast(typename E::F, load16(ur + j0 * kU, uoff[i]));
         if constexpr (DT == LORA_BF16 && VEC) {
-            char *tl = tile + (s & 1) * 2048;
-            int cc = c0 + 8 * (lane & 7);
-            cc = cc < a.d_in ? cc : 0;
-            u32x4 w[2];
+            const char *base = reinterpret_cast<const char *>(d->A) + (int64_t(j0) * a.d_in + c0) * 2;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int j = j0 + (lane >> 3) + 8 * i;
-                w[i] = *(gptr<u32x4>)(A + int64_t(j < r ? j : r - 1) * a.d_in + cc);
-                if (j >= r) w[i] = u32x4{};
+                const int j = (lane >> 3) + 8 * i;
+                u32x4 w = load16(base, uint32_t(j0 + j < r ? j : 0) * uint32_t(a.d_in * 2) + acol);
+                if (j0 + j >= r) w = u32x4{};
+                o.af[i] = __builtin_bit_cast(bf16x8, w);
             }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4 *>(tl + tile_at((lane >> 3) + 8 * i, lane & 7)) = w[i];
-            // k slots of lane groups 0, 1 meet u's hi parts, 2, 3 its lo parts, of the same ranks
-#pragma unroll
-            for (int t = 0; t < 4; ++t) af[t] = tile_frag(tl, t, m, g & 1, 8);
         } else {
 #pragma unroll
             for (int e = 0; e < E::kVec; ++e) {
@@ -649,20 +829,67 @@ __global__ __launch_bounds__(kDxWaves * 64) void bwd_dx_kernel(BwdArgs a, int ti
                 for (int t = 0; t < 4; ++t) {
                     const int cc = min(c0 + col<DT>(m >> 2, 4 * t + (m & 3)), a.d_in - 1);
                     const T w = A[int64_t(j < r ? j : r - 1) * a.d_in + cc];
-                    if constexpr (DT == LORA_BF16) af[t][e] = __builtin_bit_cast(__bf16, uint16_t(j < r ? w : 0));
-                    else af[t][e] = j < r ? w : 0.f;
+                    if constexpr (DT == LORA_BF16) o.af[t][e] = __builtin_bit_cast(__bf16, uint16_t(j < r ? w : 0));
+                    else o.af[t][e] = j < r ? w : 0.f;
                 }
             }
+        }
+    };
+    floatx4 acc[4][4]; // column tile, row block
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][i] = floatx4{};
+    auto products = [&](const Ops &o, int s) {
+        typename E::F af[4];
+        if constexpr (DT == LORA_BF16 && VEC) {
+            char *tl = tile + (s & 1) * 2048;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                *reinterpret_cast<u32x4 *>(tl + tile_at((lane >> 3) + 8 * i, lane & 7)) = __builtin_bit_cast(u32x4, o.af[i]);
+            // k slots of lane groups 0, 1 meet u's hi parts, 2, 3 its lo parts, of the same ranks
+#pragma unroll
+            for (int t = 0; t < 4; ++t) af[t] = tile_frag(tl, (t >> 1) * 4 + (m & 3), t & 1, m, g & 1);
+        } else {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) af[t] = o.af[t];
         }
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[t][i] = mma<DT>(af[t], uf[i], acc[t][i]);
+            for (int i = 0; i < 4; ++i) acc[t][i] = mma<DT>(af[t], o.uf[i], acc[t][i]);
+    };
+    // the first operands, then dx's rows (needed last), then each next step's
+    // operands before the products of the current one
+    constexpr bool kPre = DT == LORA_BF16 && VEC;
+    Ops o0, o1;
+    load(o0, 0);
+    T *row[4];       // element by element
+    uint32_t yoff[4]; // VEC: byte offsets of the row's pieces of this lane
+    u32x4 y[4][2];
+    char *dxc = reinterpret_cast<char *>(static_cast<T *>(a.dx) + c0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = d->rows[min(16 * i + m, n - 1)];
+        row[i] = static_cast<T *>(a.dx) + int64_t(t) * a.lddx;
+        yoff[i] = uint32_t(t) * uint32_t(a.lddx * int(sizeof(T))) + 16 * g;
+        if constexpr (kPre) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) // past d_in: the row's first piece, not stored
+                y[i][h] = load16(dxc, c0 + col<DT>(g, 8 * h) < a.d_in ? yoff[i] + 64 * h : yoff[i] - 16 * g);
+        }
+    }
+    for (int j0 = 0;;) {
+        if (j0 + 16 < r) load(o1, j0 + 16);
+        products(o0, 0);
+        if ((j0 += 16) >= r) break;
+        if (j0 + 16 < r) load(o0, j0 + 16);
+        products(o1, 1);
+        if ((j0 += 16) >= r) break;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (16 * i + m >= n) continue;
-        T *row = static_cast<T *>(a.dx) + int64_t(d->rows[16 * i + m]) * a.lddx;
         if constexpr (DT == LORA_BF16) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -670,26 +897,25 @@ __global__ __launch_bounds__(kDxWaves * 64) void bwd_dx_kernel(BwdArgs a, int ti
                 const floatx4 lo = acc[2 * h][i], hi = acc[2 * h + 1][i];
                 if constexpr (VEC) {
                     if (c >= a.d_in) continue;
-                    const u32x4 y = *reinterpret_cast<const u32x4 *>(row + c);
                     u32x4 o;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float f0 = e < 2 ? lo[2 * e] : hi[2 * e - 4], f1 = e < 2 ? lo[2 * e + 1] : hi[2 * e - 3];
-                        o[e] = pack_bf16x2(bf16_to_f32(y[e] & 0xffffu) + f0, bf16_to_f32(y[e] >> 16) + f1);
+                        o[e] = pack_bf16x2(bf16_to_f32(y[i][h][e] & 0xffffu) + f0, bf16_to_f32(y[i][h][e] >> 16) + f1);
                     }
-                    *reinterpret_cast<u32x4 *>(row + c) = o;
+                    *reinterpret_cast<u32x4 *>(dxc + 64 * h + yoff[i]) = o;
                 } else {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         if (c + e < a.d_in)
-                            row[c + e] = uint16_t(f32_to_bf16(bf16_to_f32(row[c + e]) + (e < 4 ? lo[e & 3] : hi[e & 3])));
+                            row[i][c + e] = uint16_t(f32_to_bf16(bf16_to_f32(row[i][c + e]) + (e < 4 ? lo[e & 3] : hi[e & 3])));
                 }
             }
         } else {
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const int c = c0 + col<DT>(g, 4 * t);
-                if (c < a.d_in) put4(row + c, acc[t][i], a.d_in - c, VEC, true);
+                if (c < a.d_in) put4(row[i] + c, acc[t][i], a.d_in - c, VEC, true);
             }
         }
     }
@@ -734,12 +960,26 @@ Layout layout_of(int32_t rows, int32_t d_in, int32_t d_out, int32_t max_rank)
     return l;
 }
 
+template <int DT, bool VEC, int MB> void run_shrink_mb(hipStream_t s, const BwdArgs &a, unsigned units, unsigned nside)
+{
+    const dim3 grid((units + 7) / 8 * nside * 8 + 8), block(kShrinkWaves * 64);
+    if (a.r16 <= 16) launch_kernel(bwd_shrink_kernel<DT, VEC, 1, MB>, grid, block, 0, s, a);
+    else if (a.r16 <= 32) launch_kernel(bwd_shrink_kernel<DT, VEC, 2, MB>, grid, block, 0, s, a);
+    else launch_kernel(bwd_shrink_kernel<DT, VEC, 4, MB>, grid, block, 0, s, a);
+}
+// 64 rows per workgroup when that still gives every CU two of them.
 template <int DT, bool VEC> void run_shrink(hipStream_t s, const BwdArgs &a, int nside)
 {
-    const dim3 grid(unsigned(a.nblk) * nside + 1), block(kShrinkWaves * 64);
-    if (a.r16 <= 16) launch_kernel(bwd_shrink_kernel<DT, VEC, 1>, grid, block, 0, s, a);
-    else if (a.r16 <= 32) launch_kernel(bwd_shrink_kernel<DT, VEC, 2>, grid, block, 0, s, a);
-    else launch_kernel(bwd_shrink_kernel<DT, VEC, 4>, grid, block, 0, s, a);
+    if (VEC && DT == LORA_BF16 && int64_t(a.nchunk) * nside >= 512)
+        run_shrink_mb<DT, VEC, VEC && DT == LORA_BF16 ? 4 : 1>(s, a, unsigned(a.nchunk), unsigned(nside));
+    else run_shrink_mb<DT, VEC, 1>(s, a, unsigned(a.nblk), unsigned(nside));
+}
+template <int DT, bool VEC> void run_grad(hipStream_t s, const BwdArgs &a, dim3 grid, int tiles_A, int tiles)
+{
+    const dim3 block(kGradWaves * 64);
+    if (a.r16 <= 16) launch_kernel(bwd_grad_kernel<DT, VEC, 1>, grid, block, 0, s, a, tiles_A, tiles);
+    else if (a.r16 <= 32) launch_kernel(bwd_grad_kernel<DT, VEC, 2>, grid, block, 0, s, a, tiles_A, tiles);
+    else launch_kernel(bwd_grad_kernel<DT, VEC, 4>, grid, block, 0, s, a, tiles_A, tiles);
 }
 
 int checked(const char *what)
@@ -820,10 +1060,10 @@ int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p
     if (tiles) {
         const int64_t nwg = int64_t(a.nitems) * tiles;
         if (nwg > (int64_t(1) << 31) - 1) return fail(LORA_ERR_ARG, "backward: too many work items");
-        const dim3 grid{unsigned(nwg)}, block(kGradWaves * 64);
-        if (bf16 && vec) launch_kernel(bwd_grad_kernel<LORA_BF16, true>, grid, block, 0, s, a, tiles_A, tiles);
-        else if (bf16) launch_kernel(bwd_grad_kernel<LORA_BF16, false>, grid, block, 0, s, a, tiles_A, tiles);
-        else launch_kernel(bwd_grad_kernel<LORA_F32, false>, grid, block, 0, s, a, tiles_A, tiles);
+        const dim3 grid{unsigned(nwg)};
+        if (bf16 && vec) run_grad<LORA_BF16, true>(s, a, grid, tiles_A, tiles);
+        else if (bf16) run_grad<LORA_BF16, false>(s, a, grid, tiles_A, tiles);
+        else run_grad<LORA_F32, false>(s, a, grid, tiles_A, tiles);
         if ((st = checked("backward gradient"))) return st;
         if (a.nsplit) {
             const int64_t units = (l.part_stride / 4 + 255) / 256;
