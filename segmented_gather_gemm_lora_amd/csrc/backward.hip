@@ -37,6 +37,7 @@
 #include "internal.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace lora {
 namespace {
@@ -80,6 +81,9 @@ __device__ __forceinline__ u32x4 load16(const void *base, uint32_t off)
 {
     return *(gptr<u32x4>)(as_global<char>(base) + off);
 }
+// 16 bytes from or to a place that is aligned to its elements alone.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+template <class T> __device__ __forceinline__ u32x4 load16_any(gptr<T> p) { return *(gptr<u32x4_any>)(p); }
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 constexpr int kWin = 32; // sorted positions of one step over rows; u and v are stored in windows of it
@@ -163,22 +167,16 @@ struct BwdArgs {
 // Side 0: v, K = d_in, W = A (row j is rank j, contiguous along K).
 // Side 1: u, K = d_out, W = B (row k holds the ranks).
 // ----------------------------------------------------------------------------
-template <int DT, bool VEC>
-__device__ __forceinline__ typename Elem<DT>::F load_row(gptr<typename Elem<DT>::T> row, int k, int K)
+// Elements k .. of a row, 0 past K, one by one.
+template <int DT> __device__ __forceinline__ typename Elem<DT>::F load_row(gptr<typename Elem<DT>::T> row, int k, int K)
 {
     using E = Elem<DT>;
     typename E::F f;
-    if constexpr (VEC) { // K is a multiple of kVec
-        const int kk = k < K ? k : K - E::kVec;
-        f = __builtin_bit_cast(typename E::F, *(gptr<u32x4>)(row + kk));
-        if (k >= K) f = typename E::F{};
-    } else {
 #pragma unroll
-        for (int e = 0; e < E::kVec; ++e) {
-            const typename E::T w = row[k + e < K ? k + e : K - 1];
-            if constexpr (DT == LORA_BF16) f[e] = __builtin_bit_cast(__bf16, uint16_t(k + e < K ? w : 0));
-            else f[e] = k + e < K ? w : 0.f;
-        }
+    for (int e = 0; e < E::kVec; ++e) {
+        const typename E::T w = row[k + e < K ? k + e : K - 1];
+        if constexpr (DT == LORA_BF16) f[e] = __builtin_bit_cast(__bf16, uint16_t(k + e < K ? w : 0));
+        else f[e] = k + e < K ? w : 0.f;
     }
     return f;
 }
@@ -261,24 +259,29 @@ struct ShrinkSide {
     int n;
 };
 
-// A lane's rows: byte offsets of its first element of every row and of its part
-// of A or B (VEC; all below 4 GiB), or the rows' tokens.
+// How W is loaded: by elements, by 16 bytes at any alignment, by 16 aligned bytes.
+enum { kByElem = 0, kByAny = 1, kByVec = 2 };
+
+// A lane's rows: byte offsets of its first element of every row (VEC; all below
+// 4 GiB) or the rows' tokens, and the byte offset of its part of A or B.
 template <int RT, int MB> struct ShrinkOffs {
     uint32_t x[MB], w[RT];
 };
 
-template <int DT, int SIDE, bool BVEC, int RT, int MB>
+template <int DT, bool VEC, int SIDE, int RT, int MB>
 __device__ __forceinline__ ShrinkOffs<RT, MB> shrink_offs(const ShrinkSide &sd, int lane)
 {
     constexpr int es = int(sizeof(typename Elem<DT>::T));
     const int m = lane & 15, g = lane >> 4;
     ShrinkOffs<RT, MB> o;
 #pragma unroll
-    for (int b = 0; b < MB; ++b) // rows past n: never stored
-        o.x[b] = uint32_t(sd.rows[min(16 * b + m, sd.n - 1)]) * uint32_t(sd.ld * es) + 16 * g;
+    for (int b = 0; b < MB; ++b) { // rows past n: never stored
+        const uint32_t t = uint32_t(sd.rows[min(16 * b + m, sd.n - 1)]);
+        o.x[b] = VEC ? t * uint32_t(sd.ld * es) + 16 * g : t;
+    }
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-        if constexpr (BVEC) { // 32 rows x 2 RT pieces of 16 bytes a step, RT pieces a lane
+        if constexpr (SIDE == 1) { // 32 rows x 2 RT pieces of 16 bytes a step, RT pieces a lane
             const int q = lane + 64 * i, j = 16 * sd.rt0 + 8 * (q % (2 * RT));
             o.w[i] = uint32_t((q / (2 * RT)) * sd.r + (j < sd.r ? j : 0)) * es;
         } else {
@@ -289,10 +292,10 @@ __device__ __forceinline__ ShrinkOffs<RT, MB> shrink_offs(const ShrinkSide &sd, 
     return o;
 }
 
-// The operands of steps k .. (k wave-uniform).  VEC: rows by 16 bytes; W of side 0
-// by rank rows, of side 1 by 16-byte pieces (BVEC: ranks a multiple of 8); FULL:
-// every step inside K.  Else element by element.
-template <int DT, bool VEC, int SIDE, bool BVEC, bool FULL, int RT, int MB, int NS>
+// The operands of steps k .. (k wave-uniform).  Rows of x (dy) and of A by 16
+// bytes, B (WLOAD kByAny, kByVec) by pieces of 8 ranks; FULL: every element loaded
+// lies inside.  Else element by element (VEC rows: clamped to the row).
+template <int DT, bool VEC, int SIDE, int WLOAD, bool FULL, int RT, int MB, int NS>
 __device__ __forceinline__ void shrink_load(ShrinkOps<DT, RT, MB, NS> &o, const ShrinkSide &sd,
                                             const ShrinkOffs<RT, MB> &off, int k, int lane)
 {
@@ -303,42 +306,40 @@ __device__ __forceinline__ void shrink_load(ShrinkOps<DT, RT, MB, NS> &o, const 
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
         const int ks = k + s * E::kStep;
-        if constexpr (VEC) {
-            // past K: the last units of a row, replaced by zero
-            const int kc = FULL || ks < sd.K ? ks : 0;
-            const bool in = FULL || ks + E::kVec * g < sd.K;
-            const uint32_t back = in ? 0 : uint32_t(16 * g); // the row's first unit
-            const char *xb = static_cast<const char *>(sd.src) + int64_t(kc) * int(sizeof(T));
+        // VEC, past K: the row's first unit, replaced by zero
+        const int kc = FULL || ks < sd.K ? ks : 0;
+        const bool in = FULL || ks + E::kVec * g < sd.K;
+        const uint32_t back = in ? 0 : uint32_t(16 * g);
+        const char *xb = static_cast<const char *>(sd.src) + int64_t(kc) * int(sizeof(T));
+        const char *ab = static_cast<const char *>(sd.mat) + int64_t(kc) * int(sizeof(T));
 #pragma unroll
-            for (int b = 0; b < MB; ++b) {
+        for (int b = 0; b < MB; ++b) {
+            if constexpr (VEC) {
                 u32x4 w = load16(xb, off.x[b] - back);
                 if (!in) w = u32x4{};
                 o.xf[s][b] = __builtin_bit_cast(F, w);
+            } else {
+                const gptr<T> row = as_global<T>(sd.src) + int64_t(off.x[b]) * sd.ld;
+                if constexpr (FULL) o.xf[s][b] = __builtin_bit_cast(F, load16_any(row + (ks + E::kVec * g)));
+                else o.xf[s][b] = load_row<DT>(row, ks + E::kVec * g, sd.K);
             }
-        } else {
-#pragma unroll
-            for (int b = 0; b < MB; ++b)
-                o.xf[s][b] = load_row<DT, false>(
-                    as_global<T>(sd.src) + int64_t(off.x[b]) * sd.ld, ks + E::kVec * g, sd.K);
         }
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
-            if constexpr (VEC && SIDE == 0) {
-                const int kc = FULL || ks < sd.K ? ks : 0;
-                const bool in = FULL || ks + E::kVec * g < sd.K;
-                u32x4 w = load16(static_cast<const char *>(sd.mat) + int64_t(kc) * int(sizeof(T)), off.w[i] - (in ? 0 : uint32_t(16 * g)));
-                if (!in) w = u32x4{};
-                o.wf[s][i] = __builtin_bit_cast(F, w);
-            } else if constexpr (BVEC) {
-                const int kr = ks + (lane + 64 * i) / (2 * RT);
-                const bool in = FULL || kr < sd.K;
-                const int kc = FULL || ks < sd.K ? ks : 0;
-                u32x4 w = load16(static_cast<const char *>(sd.mat) + int64_t(kc) * sd.r * 2, in ? off.w[i] : 0);
+            if constexpr (SIDE == 0 && VEC) {
+                u32x4 w = load16(ab, off.w[i] - back);
                 if (!in) w = u32x4{};
                 o.wf[s][i] = __builtin_bit_cast(F, w);
             } else if constexpr (SIDE == 0) {
                 const int j = 16 * (sd.rt0 + i) + m;
-                o.wf[s][i] = load_row<DT, false>(as_global<T>(sd.mat) + int64_t(j < sd.r ? j : sd.r - 1) * sd.K, ks + E::kVec * g, sd.K);
+                const gptr<T> row = as_global<T>(sd.mat) + int64_t(j < sd.r ? j : sd.r - 1) * sd.K;
+                if constexpr (FULL) o.wf[s][i] = __builtin_bit_cast(F, load16_any(as_global<char>(ab) + off.w[i]));
+                else o.wf[s][i] = load_row<DT>(row, ks + E::kVec * g, sd.K);
+            } else if constexpr (WLOAD != kByElem) {
+                static_assert(FULL || WLOAD == kByElem, "pieces of whole chunks");
+                const char *bb = static_cast<const char *>(sd.mat) + int64_t(ks) * sd.r * 2;
+                if constexpr (WLOAD == kByVec) o.wf[s][i] = __builtin_bit_cast(F, load16(bb, off.w[i]));
+                else o.wf[s][i] = __builtin_bit_cast(F, load16_any(as_global<char>(bb) + off.w[i]));
             } else {
                 o.wf[s][i] = load_col<DT>(as_global<T>(sd.mat), sd.r, 16 * (sd.rt0 + i) + m, ks + E::kVec * g, sd.K);
             }
@@ -346,7 +347,8 @@ __device__ __forceinline__ void shrink_load(ShrinkOps<DT, RT, MB, NS> &o, const 
     }
 }
 
-template <int DT, bool BVEC, int RT, int MB, int NS>
+// PIECES: W is B by pieces, to be turned through the wave's LDS tile.
+template <int DT, bool PIECES, int RT, int MB, int NS>
 __device__ __forceinline__ void shrink_mma(const ShrinkOps<DT, RT, MB, NS> &o, floatx4 (&acc)[MB][RT], char *tiles,
                                            int lane)
 {
@@ -355,7 +357,7 @@ __device__ __forceinline__ void shrink_mma(const ShrinkOps<DT, RT, MB, NS> &o, f
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
         F wf[RT];
-        if constexpr (BVEC) {
+        if constexpr (PIECES) {
             // 32-byte granules (one rank tile of a row), moved so that 4 rows of a
             // tile fall in distinct banks
             char *tile = tiles + (s & 1) * 1024 * RT;
@@ -385,41 +387,42 @@ __device__ __forceinline__ void shrink_mma(const ShrinkOps<DT, RT, MB, NS> &o, f
 
 // This wave's part of the sums: chunks of NS steps, the loads of the next chunk
 // issued before the products of the current one (PIPE).
-template <int DT, bool VEC, int SIDE, bool BVEC, bool PIPE, int RT, int MB, int NS>
+template <int DT, bool VEC, int SIDE, int WLOAD, bool PIPE, int RT, int MB, int NS>
 __device__ __forceinline__ void shrink_sum(floatx4 (&acc)[MB][RT], const ShrinkSide &sd, char *tiles, int wave, int lane)
 {
     constexpr int kChunk = NS * Elem<DT>::kStep, kNext = kShrinkWaves * kChunk;
+    constexpr bool kPieces = SIDE == 1 && WLOAD != kByElem;
     ShrinkOps<DT, RT, MB, NS> o0, o1;
-    ShrinkOffs<RT, MB> off{};
-    if constexpr (VEC) off = shrink_offs<DT, SIDE, BVEC, RT, MB>(sd, lane);
-    else
-        for (int b = 0; b < MB; ++b) off.x[b] = uint32_t(sd.rows[min(16 * b + (lane & 15), sd.n - 1)]);
+    const ShrinkOffs<RT, MB> off = shrink_offs<DT, VEC, SIDE, RT, MB>(sd, lane);
+    // pieces of 8 ranks of rows that hold fewer or others reach up to 7 elements
+    // into the rows after, so they keep 8 rows from B's end
+    const int last = sd.K - kChunk - (WLOAD == kByAny && SIDE == 1 ? 8 : 0);
     int k = wave * kChunk;
-    if constexpr (VEC && PIPE) {
-        if (k + kChunk <= sd.K) {
-            shrink_load<DT, VEC, SIDE, BVEC, true>(o0, sd, off, k, lane);
+    if constexpr (PIPE) {
+        if (k <= last) {
+            shrink_load<DT, VEC, SIDE, WLOAD, true>(o0, sd, off, k, lane);
             for (;;) {
                 k += kNext;
-                const bool more0 = k + kChunk <= sd.K;
-                if (more0) shrink_load<DT, VEC, SIDE, BVEC, true>(o1, sd, off, k, lane);
-                shrink_mma<DT, BVEC>(o0, acc, tiles, lane);
+                const bool more0 = k <= last;
+                if (more0) shrink_load<DT, VEC, SIDE, WLOAD, true>(o1, sd, off, k, lane);
+                shrink_mma<DT, kPieces>(o0, acc, tiles, lane);
                 if (!more0) break;
                 k += kNext;
-                const bool more1 = k + kChunk <= sd.K;
-                if (more1) shrink_load<DT, VEC, SIDE, BVEC, true>(o0, sd, off, k, lane);
-                shrink_mma<DT, BVEC>(o1, acc, tiles, lane);
+                const bool more1 = k <= last;
+                if (more1) shrink_load<DT, VEC, SIDE, WLOAD, true>(o0, sd, off, k, lane);
+                shrink_mma<DT, kPieces>(o1, acc, tiles, lane);
                 if (!more1) break;
             }
         }
     } else {
-        for (; VEC && k + kChunk <= sd.K; k += kNext) {
-            shrink_load<DT, VEC, SIDE, BVEC, true>(o0, sd, off, k, lane);
-            shrink_mma<DT, BVEC>(o0, acc, tiles, lane);
+        for (; k <= last; k += kNext) {
+            shrink_load<DT, VEC, SIDE, WLOAD, true>(o0, sd, off, k, lane);
+            shrink_mma<DT, kPieces>(o0, acc, tiles, lane);
         }
     }
     for (; k < sd.K; k += kNext) { // the last, partial chunk
-        shrink_load<DT, VEC, SIDE, BVEC, false>(o0, sd, off, k, lane);
-        shrink_mma<DT, BVEC>(o0, acc, tiles, lane);
+        shrink_load<DT, VEC, SIDE, kByElem, false>(o0, sd, off, k, lane);
+        shrink_mma<DT, false>(o0, acc, tiles, lane);
     }
 }
 
@@ -464,7 +467,6 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void bwd_shrink_kernel(BwdArgs a
     }
     ShrinkSide sd = side ? ShrinkSide{a.dy, pB, a.lddy, a.d_out, r, 0, rows, n} : ShrinkSide{a.x, pA, a.ldx, a.d_in, r, 0, rows, n};
     const int ntiles = (r + 15) >> 4;
-    const bool bvec = VEC && DT == LORA_BF16 && (r & 7) == 0; // B rows are whole 16-byte pieces
     char *tiles = lds + wave * 2 * kTile;
 
     for (int rt0 = 0; rt0 < ntiles; rt0 += RT) {
@@ -474,9 +476,10 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void bwd_shrink_kernel(BwdArgs a
 #pragma unroll
             for (int i = 0; i < RT; ++i) acc[b][i] = floatx4{};
         sd.rt0 = rt0;
-        if (side == 0) shrink_sum<DT, VEC, 0, false, kPipe, RT, MB, NS>(acc, sd, tiles, wave, lane);
-        else if (!bvec) shrink_sum<DT, VEC, 1, false, false, RT, MB, NS>(acc, sd, tiles, wave, lane);
-        else if constexpr (VEC && DT == LORA_BF16) shrink_sum<DT, VEC, 1, true, kPipe, RT, MB, NS>(acc, sd, tiles, wave, lane);
+        if (side == 0) shrink_sum<DT, VEC, 0, kByElem, kPipe, RT, MB, NS>(acc, sd, tiles, wave, lane);
+        else if constexpr (DT == LORA_F32) shrink_sum<DT, VEC, 1, kByElem, false, RT, MB, NS>(acc, sd, tiles, wave, lane);
+        else if (r & 7) shrink_sum<DT, VEC, 1, kByAny, false, RT, MB, NS>(acc, sd, tiles, wave, lane);
+        else shrink_sum<DT, VEC, 1, kByVec, kPipe, RT, MB, NS>(acc, sd, tiles, wave, lane);
         // lane l of tile i holds D[row 4 (l / 16) + q][rank l % 16]
         float *red = reinterpret_cast<float *>(lds);
 #pragma unroll
@@ -557,10 +560,10 @@ __device__ __forceinline__ void put4(float *dst, floatx4 v, int n, bool vec, boo
     }
 }
 
-// Operands of one window.  bf16 rows by 16 bytes (VEC): row (lane / 8) + 8 i, column
-// 8 (lane % 8), to be turned through the tile; else the column fragments
-// themselves.  fp32 takes a window in two halves of 16 rows.
-template <int DT, bool VEC, int RT> struct GradOps {
+// Operands of one window.  bf16: rows by 16 bytes, row (lane / 8) + 8 i, column
+// 8 (lane % 8), to be turned through the tile; fp32: the column fragments
+// themselves, in two halves of 16 rows.
+template <int DT, int RT> struct GradOps {
     static constexpr int kHalves = DT == LORA_BF16 ? 1 : 2;
     typename Elem<DT>::F xf[kHalves][4];
     typename Elem<DT>::F uf[kHalves][RT][Elem<DT>::kParts];
@@ -572,8 +575,9 @@ struct GradSide {
     int D;
 };
 
-template <int DT, bool VEC, int RT>
-__device__ __forceinline__ void grad_load(GradOps<DT, VEC, RT> &o, const BwdArgs &a, const GradSide &sd, int begin, int end,
+// WHOLE: all 64 columns lie in the row (not asked for by VEC).
+template <int DT, bool VEC, bool WHOLE, int RT>
+__device__ __forceinline__ void grad_load(GradOps<DT, RT> &o, const BwdArgs &a, const GradSide &sd, int begin, int end,
                                           int w, int c0, int rt0, const int32_t *tok, int lane)
 {
     using E = Elem<DT>;
@@ -600,6 +604,15 @@ __device__ __forceinline__ void grad_load(GradOps<DT, VEC, RT> &o, const BwdArgs
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             o.xf[0][i] = __builtin_bit_cast(bf16x8, load16(src, uint32_t(token(base + (lane >> 3) + 8 * i)) * pitch + cc));
+    } else if constexpr (DT == LORA_BF16) {
+        const gptr<T> src = as_global<T>(sd.src);
+        const int c = c0 + 8 * (lane & 7);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const gptr<T> row = src + int64_t(token(base + (lane >> 3) + 8 * i)) * sd.ld;
+            if constexpr (WHOLE) o.xf[0][i] = __builtin_bit_cast(bf16x8, load16_any(row + c));
+            else o.xf[0][i] = load_row<DT>(row, c, sd.D);
+        }
     } else {
         const gptr<T> src = as_global<T>(sd.src);
 #pragma unroll
@@ -609,16 +622,14 @@ __device__ __forceinline__ void grad_load(GradOps<DT, VEC, RT> &o, const BwdArgs
                 const gptr<T> row = src + int64_t(token(base + 16 * h + E::kVec * g + e)) * sd.ld;
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    const T f = row[min(c0 + 16 * t + m, sd.D - 1)];
-                    if constexpr (DT == LORA_BF16) o.xf[h][t][e] = __builtin_bit_cast(__bf16, f);
-                    else o.xf[h][t][e] = f;
+                    o.xf[h][t][e] = row[min(c0 + 16 * t + m, sd.D - 1)];
                 }
             }
     }
 }
 
-template <int DT, bool VEC, int RT>
-__device__ __forceinline__ void grad_mma(GradOps<DT, VEC, RT> &o, floatx4 (&acc)[4][RT], int side, int begin, int end, int w,
+template <int DT, int RT>
+__device__ __forceinline__ void grad_mma(GradOps<DT, RT> &o, floatx4 (&acc)[4][RT], int side, int begin, int end, int w,
                                          char *tile, int lane)
 {
     using E = Elem<DT>;
@@ -640,7 +651,7 @@ __device__ __forceinline__ void grad_mma(GradOps<DT, VEC, RT> &o, floatx4 (&acc)
             for (int i = 0; i < RT; ++i)
 #pragma unroll
                 for (int q = 0; q < E::kParts; ++q) mask(o.uf[h][i][q]);
-            if constexpr (DT == LORA_BF16 && VEC) {
+            if constexpr (DT == LORA_BF16) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (!in(base + (lane >> 3) + 8 * i)) o.xf[0][i] = bf16x8{};
@@ -650,7 +661,7 @@ __device__ __forceinline__ void grad_mma(GradOps<DT, VEC, RT> &o, floatx4 (&acc)
             }
         }
     }
-    if constexpr (DT == LORA_BF16 && VEC) {
+    if constexpr (DT == LORA_BF16) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             *reinterpret_cast<u32x4 *>(tile + tile_at((lane >> 3) + 8 * i, lane & 7)) = __builtin_bit_cast(u32x4, o.xf[0][i]);
@@ -660,7 +671,7 @@ __device__ __forceinline__ void grad_mma(GradOps<DT, VEC, RT> &o, floatx4 (&acc)
         F xf[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            if constexpr (DT == LORA_BF16 && VEC) xf[t] = tile_frag(tile, 2 * t + ((m & 3) >> 1), m & 1, m, g);
+            if constexpr (DT == LORA_BF16) xf[t] = tile_frag(tile, 2 * t + ((m & 3) >> 1), m & 1, m, g);
             else xf[t] = o.xf[h][t];
         }
 #pragma unroll
@@ -673,7 +684,7 @@ __device__ __forceinline__ void grad_mma(GradOps<DT, VEC, RT> &o, floatx4 (&acc)
     }
 }
 
-template <int DT, bool VEC, int RT>
+template <int DT, bool VEC, bool WHOLE, int RT>
 __device__ __forceinline__ void grad_item(const BwdArgs &a, const GradSide &sd, int side, int begin, int end, int c0, int rt0,
                                           int r, float *dst, bool add, const int32_t *tok, char *tile, int lane)
 {
@@ -686,16 +697,16 @@ __device__ __forceinline__ void grad_item(const BwdArgs &a, const GradSide &sd, 
     // Four rank tiles: the next window's loads are issued before the current one's
     // products (16384 rows of rank 64: 106 us, 118 without).  Fewer: more waves fit
     // instead (rank 16, 4096 rows: 17.2 us, 18.8 with).
-    GradOps<DT, VEC, RT> o0;
+    GradOps<DT, RT> o0;
     int w = begin / kWin;
-    grad_load(o0, a, sd, begin, end, w, c0, rt0, tok, lane);
+    grad_load<DT, VEC, WHOLE>(o0, a, sd, begin, end, w, c0, rt0, tok, lane);
     for (;;) {
-        GradOps<DT, VEC, RT> o1;
-        if (RT == 4 && w < w1) grad_load(o1, a, sd, begin, end, w + 1, c0, rt0, tok, lane);
+        GradOps<DT, RT> o1;
+        if (RT == 4 && w < w1) grad_load<DT, VEC, WHOLE>(o1, a, sd, begin, end, w + 1, c0, rt0, tok, lane);
         grad_mma(o0, acc, side, begin, end, w, tile, lane);
         if (++w > w1) break;
         if (RT == 4) o0 = o1;
-        else grad_load(o0, a, sd, begin, end, w, c0, rt0, tok, lane);
+        else grad_load<DT, VEC, WHOLE>(o0, a, sd, begin, end, w, c0, rt0, tok, lane);
     }
     // dA (side 0): D rows are columns of x, D columns are ranks.  dB: D rows
     // are ranks, D columns are columns of dy (rows of dB).
@@ -715,14 +726,16 @@ __device__ __forceinline__ void grad_item(const BwdArgs &a, const GradSide &sd, 
         }
 }
 
-// RT: rank tiles that a wave holds at once (the plan's largest rank, at most 4).
+// RT: rank tiles that a wave holds (the plan's largest rank, at most 4: higher
+// ranks are `groups` of 64, a workgroup each).
 template <int DT, bool VEC, int RT>
-__global__ __launch_bounds__(kGradWaves * 64, LORA_GOCC) void bwd_grad_kernel(BwdArgs a, int tiles_A, int tiles)
+__global__ __launch_bounds__(kGradWaves * 64, LORA_GOCC) void bwd_grad_kernel(BwdArgs a, int tiles_A, int tiles, int groups)
 {
-    __shared__ __attribute__((aligned(16))) char tiles_lds[DT == LORA_BF16 && VEC ? kGradWaves * 4096 : 16];
+    __shared__ __attribute__((aligned(16))) char tiles_lds[DT == LORA_BF16 ? kGradWaves * 4096 : 16];
     __shared__ int32_t tok[kMaxSpan];
-    const int tl = blockIdx.x % tiles;
-    const Item it = a.items[blockIdx.x / tiles];
+    const int tl = blockIdx.x % tiles, group = blockIdx.x / tiles % groups;
+    const Item it = a.items[blockIdx.x / tiles / groups];
+    if (64 * group >= it.rank) return;
     const int side = tl >= tiles_A;
     const uint64_t grad = side ? it.grad_B : it.grad_A;
     if (!grad) return; // this adapter's gradient is not wanted
@@ -738,20 +751,19 @@ __global__ __launch_bounds__(kGradWaves * 64, LORA_GOCC) void bwd_grad_kernel(Bw
         dst = a.part + it.slot * a.part_stride + (side ? int64_t(r) * a.d_in : 0);
         add = false;
     }
-    char *tile = tiles_lds + (DT == LORA_BF16 && VEC ? wave * 4096 : 0);
-    for (int rt0 = 0; 16 * rt0 < r;) {
-        const int left = r - 16 * rt0;
-        if (RT >= 4 && left > 32) {
-            grad_item<DT, VEC, RT >= 4 ? 4 : 1>(a, sd, side, it.begin, it.end, c0, rt0, r, dst, add, tok, tile, lane);
-            rt0 += 4;
-        } else if (RT >= 2 && left > 16) {
-            grad_item<DT, VEC, RT >= 2 ? 2 : 1>(a, sd, side, it.begin, it.end, c0, rt0, r, dst, add, tok, tile, lane);
-            rt0 += 2;
-        } else {
-            grad_item<DT, VEC, 1>(a, sd, side, it.begin, it.end, c0, rt0, r, dst, add, tok, tile, lane);
-            rt0 += 1;
-        }
-    }
+    char *tile = tiles_lds + (DT == LORA_BF16 ? wave * 4096 : 0);
+    auto ranks = [&](auto whole) {
+        constexpr bool W = decltype(whole)::value;
+        const int left = r - 64 * group;
+        if (RT >= 4 && left > 32)
+            grad_item<DT, VEC, W, RT >= 4 ? 4 : 1>(a, sd, side, it.begin, it.end, c0, 4 * group, r, dst, add, tok, tile, lane);
+        else if (RT >= 2 && left > 16)
+            grad_item<DT, VEC, W, RT >= 2 ? 2 : 1>(a, sd, side, it.begin, it.end, c0, 4 * group, r, dst, add, tok, tile, lane);
+        else grad_item<DT, VEC, W, 1>(a, sd, side, it.begin, it.end, c0, 4 * group, r, dst, add, tok, tile, lane);
+    };
+    if constexpr (VEC || DT == LORA_F32) ranks(std::true_type{});
+    else if (c0 + 64 <= sd.D) ranks(std::true_type{});
+    else ranks(std::false_type{});
 }
 
 // Launch 3: gradient = sum of a split segment's slots, in slot order.
@@ -796,10 +808,9 @@ __global__ __launch_bounds__(kDxWaves * 64, LORA_DOCC) void bwd_dx_kernel(BwdArg
     const int c0 = int(blockIdx.x % tiles) * (64 * kDxWaves) + 64 * wave;
     if (c0 >= a.d_in) return;
     const int r = d->rank, n = d->n, p0 = d->p0;
-    [[maybe_unused]] const gptr<T> A = as_global<T>(reinterpret_cast<const void *>(d->A));
     char *tile = tiles_lds + wave * 4096;
-    // operands of 16 ranks: u of 4 row blocks, and A by rows (bf16 VEC: rank
-    // (lane / 8) + 8 i, column 8 (lane % 8)) or by column fragments
+    // operands of 16 ranks: u of 4 row blocks, and A by rows (bf16: rank
+    // (lane / 8) + 8 i, column 8 (lane % 8)) or by column fragments (fp32)
     struct Ops {
         typename E::F uf[4], af[4];
     };
@@ -808,29 +819,33 @@ __global__ __launch_bounds__(kDxWaves * 64, LORA_DOCC) void bwd_dx_kernel(BwdArg
 #pragma unroll
     for (int i = 0; i < 4; ++i) uoff[i] = uint32_t(min(16 * i + m, n - 1)) * uint32_t(a.r16 * kU) + 16 * g; // past n: not stored
     const char *ur = a.ur + int64_t(p0) * a.r16 * kU;
+    const bool whole = c0 + 64 <= a.d_in; // every piece of this wave lies in its row
     const uint32_t acol = c0 + 8 * (lane & 7) < a.d_in ? 16 * (lane & 7) : 0;
     auto load = [&](Ops &o, int j0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) o.uf[i] = __builtin_bit_cast(typename E::F, load16(ur + j0 * kU, uoff[i]));
-        if constexpr (DT == LORA_BF16 && VEC) {
+        if constexpr (DT == LORA_BF16) {
             const char *base = reinterpret_cast<const char *>(d->A) + (int64_t(j0) * a.d_in + c0) * 2;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int j = (lane >> 3) + 8 * i;
-                u32x4 w = load16(base, uint32_t(j0 + j < r ? j : 0) * uint32_t(a.d_in * 2) + acol);
+                const uint32_t row = uint32_t(j0 + j < r ? j : 0) * uint32_t(a.d_in * 2);
+                u32x4 w;
+                if constexpr (VEC) w = load16(base, row + acol);
+                else if (whole) w = load16_any(as_global<char>(base) + (row + acol)); // wave-uniform
+                else w = __builtin_bit_cast(u32x4, load_row<DT>(as_global<T>(base + row), 8 * (lane & 7), a.d_in - c0));
                 if (j0 + j >= r) w = u32x4{};
                 o.af[i] = __builtin_bit_cast(bf16x8, w);
             }
         } else {
+            const gptr<T> A = as_global<T>(reinterpret_cast<const void *>(d->A));
 #pragma unroll
             for (int e = 0; e < E::kVec; ++e) {
-                const int j = DT == LORA_BF16 ? j0 + 8 * (g & 1) + e : j0 + 4 * g + e;
+                const int j = j0 + 4 * g + e;
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    const int cc = min(c0 + col<DT>(m >> 2, 4 * t + (m & 3)), a.d_in - 1);
-                    const T w = A[int64_t(j < r ? j : r - 1) * a.d_in + cc];
-                    if constexpr (DT == LORA_BF16) o.af[t][e] = __builtin_bit_cast(__bf16, uint16_t(j < r ? w : 0));
-                    else o.af[t][e] = j < r ? w : 0.f;
+                    const T w = A[int64_t(j < r ? j : r - 1) * a.d_in + min(c0 + 16 * t + m, a.d_in - 1)];
+                    o.af[t][e] = j < r ? w : 0.f;
                 }
             }
         }
@@ -842,7 +857,7 @@ __global__ __launch_bounds__(kDxWaves * 64, LORA_DOCC) void bwd_dx_kernel(BwdArg
         for (int i = 0; i < 4; ++i) acc[t][i] = floatx4{};
     auto products = [&](const Ops &o, int s) {
         typename E::F af[4];
-        if constexpr (DT == LORA_BF16 && VEC) {
+        if constexpr (DT == LORA_BF16) {
             char *tl = tile + (s & 1) * 2048;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -861,7 +876,6 @@ __global__ __launch_bounds__(kDxWaves * 64, LORA_DOCC) void bwd_dx_kernel(BwdArg
     };
     // the first operands, then dx's rows (needed last), then each next step's
     // operands before the products of the current one
-    constexpr bool kPre = DT == LORA_BF16 && VEC;
     Ops o0, o1;
     load(o0, 0);
     T *row[4];       // element by element
@@ -873,10 +887,14 @@ __global__ __launch_bounds__(kDxWaves * 64, LORA_DOCC) void bwd_dx_kernel(BwdArg
         const int t = d->rows[min(16 * i + m, n - 1)];
         row[i] = static_cast<T *>(a.dx) + int64_t(t) * a.lddx;
         yoff[i] = uint32_t(t) * uint32_t(a.lddx * int(sizeof(T))) + 16 * g;
-        if constexpr (kPre) {
+        if constexpr (DT == LORA_BF16) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) // past d_in: the row's first piece, not stored
-                y[i][h] = load16(dxc, c0 + col<DT>(g, 8 * h) < a.d_in ? yoff[i] + 64 * h : yoff[i] - 16 * g);
+            for (int h = 0; h < 2; ++h) {
+                const int c = c0 + col<DT>(g, 8 * h);
+                if constexpr (VEC) y[i][h] = load16(dxc, c < a.d_in ? yoff[i] + 64 * h : yoff[i] - 16 * g); // past d_in: not stored
+                else if (whole) y[i][h] = load16_any(as_global<T>(row[i]) + c);
+                else y[i][h] = __builtin_bit_cast(u32x4, load_row<DT>(as_global<T>(row[i]), c, a.d_in));
+            }
         }
     }
     for (int j0 = 0;;) {
@@ -895,21 +913,19 @@ __global__ __launch_bounds__(kDxWaves * 64, LORA_DOCC) void bwd_dx_kernel(BwdArg
             for (int h = 0; h < 2; ++h) {
                 const int c = c0 + col<DT>(g, 8 * h);
                 const floatx4 lo = acc[2 * h][i], hi = acc[2 * h + 1][i];
-                if constexpr (VEC) {
-                    if (c >= a.d_in) continue;
-                    u32x4 o;
+                if (c >= a.d_in) continue;
+                u32x4 o;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float f0 = e < 2 ? lo[2 * e] : hi[2 * e - 4], f1 = e < 2 ? lo[2 * e + 1] : hi[2 * e - 3];
-                        o[e] = pack_bf16x2(bf16_to_f32(y[i][h][e] & 0xffffu) + f0, bf16_to_f32(y[i][h][e] >> 16) + f1);
-                    }
-                    *reinterpret_cast<u32x4 *>(dxc + 64 * h + yoff[i]) = o;
-                } else {
+                for (int e = 0; e < 4; ++e) {
+                    const float f0 = e < 2 ? lo[2 * e] : hi[2 * e - 4], f1 = e < 2 ? lo[2 * e + 1] : hi[2 * e - 3];
+                    o[e] = pack_bf16x2(bf16_to_f32(y[i][h][e] & 0xffffu) + f0, bf16_to_f32(y[i][h][e] >> 16) + f1);
+                }
+                if constexpr (VEC) *reinterpret_cast<u32x4 *>(dxc + 64 * h + yoff[i]) = o;
+                else if (whole) *reinterpret_cast<u32x4_any *>(row[i] + c) = o;
+                else
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        if (c + e < a.d_in)
-                            row[i][c + e] = uint16_t(f32_to_bf16(bf16_to_f32(row[i][c + e]) + (e < 4 ? lo[e & 3] : hi[e & 3])));
-                }
+                        if (c + e < a.d_in) row[i][c + e] = uint16_t(o[e >> 1] >> (16 * (e & 1)));
             }
         } else {
 #pragma unroll
@@ -924,11 +940,12 @@ __global__ __launch_bounds__(kDxWaves * 64, LORA_DOCC) void bwd_dx_kernel(BwdArg
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Sorted positions of one span, a whole number of windows: up to kSpans spans
-// for the rows, so that the bytes of partial sums stay bounded.
-constexpr int kMinSpan = 128, kSpans = 16;
+// for the rows, so that the bytes of partial sums stay bounded.  Few rows have
+// wide spans, since a segment over two of them costs a launch.
+constexpr int kMinSpan = 64, kSpans = 16;
 int span_of(int32_t rows)
 {
-    int span = kMinSpan;
+    int span = rows <= 256 ? 128 : kMinSpan;
     while (span < kMaxSpan && rows / span > kSpans) span *= 2;
     return span;
 }
@@ -974,12 +991,12 @@ template <int DT, bool VEC> void run_shrink(hipStream_t s, const BwdArgs &a, int
         run_shrink_mb<DT, VEC, VEC && DT == LORA_BF16 ? 4 : 1>(s, a, unsigned(a.nchunk), unsigned(nside));
     else run_shrink_mb<DT, VEC, 1>(s, a, unsigned(a.nblk), unsigned(nside));
 }
-template <int DT, bool VEC> void run_grad(hipStream_t s, const BwdArgs &a, dim3 grid, int tiles_A, int tiles)
+template <int DT, bool VEC> void run_grad(hipStream_t s, const BwdArgs &a, dim3 grid, int tiles_A, int tiles, int groups)
 {
     const dim3 block(kGradWaves * 64);
-    if (a.r16 <= 16) launch_kernel(bwd_grad_kernel<DT, VEC, 1>, grid, block, 0, s, a, tiles_A, tiles);
-    else if (a.r16 <= 32) launch_kernel(bwd_grad_kernel<DT, VEC, 2>, grid, block, 0, s, a, tiles_A, tiles);
-    else launch_kernel(bwd_grad_kernel<DT, VEC, 4>, grid, block, 0, s, a, tiles_A, tiles);
+    if (a.r16 <= 16) launch_kernel(bwd_grad_kernel<DT, VEC, 1>, grid, block, 0, s, a, tiles_A, tiles, groups);
+    else if (a.r16 <= 32) launch_kernel(bwd_grad_kernel<DT, VEC, 2>, grid, block, 0, s, a, tiles_A, tiles, groups);
+    else launch_kernel(bwd_grad_kernel<DT, VEC, 4>, grid, block, 0, s, a, tiles_A, tiles, groups);
 }
 
 int checked(const char *what)
@@ -1058,12 +1075,13 @@ int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p
     const int tiles_A = a.grad_A ? (a.d_in + kCols - 1) / kCols : 0;
     const int tiles = tiles_A + (a.grad_B ? (a.d_out + kCols - 1) / kCols : 0);
     if (tiles) {
-        const int64_t nwg = int64_t(a.nitems) * tiles;
+        const int groups = (a.r16 + 63) / 64;
+        const int64_t nwg = int64_t(a.nitems) * tiles * groups;
         if (nwg > (int64_t(1) << 31) - 1) return fail(LORA_ERR_ARG, "backward: too many work items");
         const dim3 grid{unsigned(nwg)};
-        if (bf16 && vec) run_grad<LORA_BF16, true>(s, a, grid, tiles_A, tiles);
-        else if (bf16) run_grad<LORA_BF16, false>(s, a, grid, tiles_A, tiles);
-        else run_grad<LORA_F32, false>(s, a, grid, tiles_A, tiles);
+        if (bf16 && vec) run_grad<LORA_BF16, true>(s, a, grid, tiles_A, tiles, groups);
+        else if (bf16) run_grad<LORA_BF16, false>(s, a, grid, tiles_A, tiles, groups);
+        else run_grad<LORA_F32, false>(s, a, grid, tiles_A, tiles, groups);
         if ((st = checked("backward gradient"))) return st;
         if (a.nsplit) {
             const int64_t units = (l.part_stride / 4 + 255) / 256;
