@@ -21,7 +21,7 @@
 // Units that lie outside (rows of another segment, ranks past r, the summed
 // axis past d_out) are loaded from a block of zeros.
 //
-// Few tiles (a narrow d_in) leave most CUs idle, so the summed axis is split:
+// Few tiles (a narrow d_in) leave most CUs idle, so the stages are split:
 // each split writes fp32 sums to the workspace, and a last launch adds them in
 // split order.
 #include "internal.h"
@@ -57,6 +57,21 @@ template <> struct Shape<64> {
     static constexpr int WC = 8, TM = 4, TN = 2;
 };
 
+// Read-only memory at a wave-uniform address: scalar loads, which wait for no
+// vector load in flight.
+template <typename T> using cptr = const __attribute__((address_space(4))) T *;
+template <typename T> __device__ __forceinline__ cptr<T> as_const(const T *p) { return (cptr<T>)(p); }
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int wave_sum(int v)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
+    return uniform(v);
+}
+
+// s_waitcnt immediates: vmcnt in bits 3:0 and 15:14, expcnt 6:4, lgkmcnt 11:8; the
+// others at their largest (no wait).
+constexpr int kWaitLgkm0 = ~(15 << 8);
 constexpr int waitcnt_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
 
 // 16 bytes per lane to LDS at m0 + 16 lane (published by an explicit vmcnt wait
@@ -129,21 +144,42 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     id /= a.tiles_m;
     const int c0 = (id % a.tiles_n) * kCols, split = id / a.tiles_n;
     const int nk = (a.d_out + kBK - 1) / kBK; // stages of the base product
-    const int k_begin = int(int64_t(nk) * split / a.splits), k_end = int(int64_t(nk) * (split + 1) / a.splits);
 
-    // correction steps of this tile (the last split has them)
+    // The tile's stages: those of the base product, then the correction steps of
+    // the segments s0 .. s1 that meet it; each split takes an equal run of them.
     int s0 = 0, s1 = -1, ncorr = 0;
-    if (split == a.splits - 1 && m0 < a.Tp) {
-        s0 = __builtin_amdgcn_readfirstlane(a.segidx[m0]);
-        s1 = __builtin_amdgcn_readfirstlane(a.segidx[min(m0 + ROWS, a.Tp) - 1]);
-        for (int s = s0; s <= s1; s += 64) {
-            int n = s + lane <= s1 ? (a.seg[s + lane].rank + 15) >> 4 : 0;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d);
-            ncorr += __builtin_amdgcn_readfirstlane(n);
-        }
+    if (m0 < a.Tp) {
+        s0 = uniform(a.segidx[m0]);
+        s1 = uniform(a.segidx[min(m0 + ROWS, a.Tp) - 1]);
+        for (int s = s0; s <= s1; s += 64) ncorr += wave_sum(s + lane <= s1 ? (a.seg[s + lane].rank + 15) >> 4 : 0);
     }
-    const int nst = k_end - k_begin + ncorr;
+    const int begin = int(int64_t(nk + ncorr) * split / a.splits), end = int(int64_t(nk + ncorr) * (split + 1) / a.splits);
+    const int k_begin = min(begin, nk);
+    const int nbase = min(end, nk) - k_begin, nst = end - begin;
+    // the first correction step of this run: segment cs, first rank cj
+    int cs = s0, cj = 0;
+    if (end > nk && begin > nk) {
+        int skip = begin - nk;
+        for (int s = s0; s <= s1; s += 64) {
+            const int n = s + lane <= s1 ? (a.seg[s + lane].rank + 15) >> 4 : 0;
+            int upto = n; // steps of this and the lanes before
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int v = __shfl_up(upto, d);
+                upto += lane >= d ? v : 0;
+            }
+            const int all = uniform(__shfl(upto, 63));
+            if (skip < all) {
+                const int at = __ffsll(__ballot(upto > skip)) - 1;
+                cs = s + at;
+                cj = 16 * (skip - uniform(__shfl(upto - n, at)));
+                break;
+            }
+            skip -= all;
+        }
+        cs = uniform(cs);
+        cj = uniform(cj);
+    }
 
     // This lane's units.  W0 part: slot 64 i + lane of the stage, i = 2 wave + j:
     // row slot / 32.  dy part: row slot / 4.
@@ -170,13 +206,15 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
         xp[j] = reinterpret_cast<const char *>(a.dy + int64_t(xtok[j]) * a.lddy + k_begin * kBK + xk[j]);
     }
 
-    // Stage i of the list: base stages k_begin .. k_end - 1, then the correction.
-    int cs = s0, cj = 0; // next correction step: segment, first rank
+    // Stage i of this run: nbase base stages, then the correction.
+    int is = cs, ij = cj; // the next correction step to load, and its segment (read ahead)
+    lora_seg_desc next{};
+    if (nst > nbase) next = *as_const(a.seg + is);
     auto issue = [&](int i) {
         const uint32_t wbase = lds0 + uint32_t((i % kStages) * kStageBytes + wave * kWDma * 1024);
         const uint32_t xbase = lds0 + uint32_t((i % kStages) * kStageBytes + kWBytes + wave * kXDma * 1024);
         const int k0 = (k_begin + i) * kBK;
-        if (i < k_end - k_begin) {
+        if (i < nbase) {
             if (k0 + kBK <= a.d_out) {
 #pragma unroll
                 for (int j = 0; j < kWDma; ++j) dma16(wp[j], wbase + j * 1024);
@@ -203,26 +241,26 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
                 }
             }
         } else if (i < nst) {
-            const lora_seg_desc *d = a.seg + cs;
-            const int r = d->rank, begin = d->start, end = begin + d->len;
-            const uint16_t *A = reinterpret_cast<const uint16_t *>(d->A);
+            const int r = next.rank, first = next.start, last = first + next.len;
+            const uint16_t *A = reinterpret_cast<const uint16_t *>(next.A);
 #pragma unroll
             for (int j = 0; j < kWDma; ++j) {
-                const int rank = cj + (wrow[j] & 15);
+                const int rank = ij + (wrow[j] & 15);
                 const char *p = reinterpret_cast<const char *>(A + int64_t(rank) * a.d_in + wcol[j]);
                 dma16(rank < r ? p : zeros, wbase + j * 1024);
             }
             if (xw) {
 #pragma unroll
                 for (int j = 0; j < kXDma; ++j) {
-                    const char *p = reinterpret_cast<const char *>(a.ur + int64_t(xpos[j]) * a.ldu + 2 * cj + xk[j]);
-                    dma16(xpos[j] >= begin && xpos[j] < end ? p : zeros, xbase + j * 1024);
+                    const char *p = reinterpret_cast<const char *>(a.ur + int64_t(xpos[j]) * a.ldu + 2 * ij + xk[j]);
+                    dma16(xpos[j] >= first && xpos[j] < last ? p : zeros, xbase + j * 1024);
                 }
             }
-            cj += 16;
-            if (cj >= r) {
-                cj = 0;
-                ++cs;
+            ij += 16;
+            if (ij >= r) {
+                ij = 0;
+                is = min(is + 1, s1);
+                next = *as_const(a.seg + is);
             }
         } else { // past the end: keeps the number of loads in flight
 #pragma unroll
@@ -234,21 +272,30 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
         }
     };
 
-    // fragment places in a stage
-    uint32_t xoff[G::TM], woff[2]; // W0: tiles t and t + 1 are the halves of one unit, t / 2 moves 4 units
+    // This lane's fragment places in a stage.  dy rows of a wave's row tiles are
+    // 1024 bytes apart; W0: tiles t and t + 1 are the halves of one unit, tiles t + 2
+    // lie 4 units on, the second 4 rows of a fragment 4 rows on.
+    const int xr = wr * G::TM * 16 + m;
+    const uint32_t xoff = uint32_t(kWBytes + xr * 64 + ((g ^ ((xr >> 1) & 3)) << 4));
+    uint32_t woff[G::TN / 2];
 #pragma unroll
-    for (int i = 0; i < G::TM; ++i) {
-        const int row = (wr * G::TM + i) * 16 + m;
-        xoff[i] = uint32_t(kWBytes + row * 64 + ((g ^ ((row >> 1) & 3)) << 4));
+    for (int t = 0; t < G::TN / 2; ++t) {
+        const int row = 8 * g + (m >> 2), un = wc * 2 * G::TN + t * 4 + (m & 3);
+        woff[t] = uint32_t(row * kCols * 2 + ((un ^ ((row & 3) << 2)) << 4));
     }
+    auto read_w = [&](const char *st, bf16x8(&wf)[G::TN]) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int row = 8 * g + 4 * h + (m >> 2);
-        woff[h] = uint32_t(row * kCols * 2);
-    }
-    auto wunit = [&](int t) { // slot of this lane's unit of tile t (row % 4 = m / 4)
-        const int un = wc * 2 * G::TN + (t >> 1) * 4 + (m & 3);
-        return uint32_t(((un ^ ((m >> 2) << 2)) << 4) + 8 * (t & 1));
+        for (int t = 0; t < G::TN; ++t) {
+            const char *p = st + woff[t >> 1] + 8 * (t & 1);
+            const u32x2 lo = read_tr(p), hi = read_tr(p + 4 * kCols * 2);
+            wf[t] = __builtin_bit_cast(bf16x8, u32x4{lo[0], lo[1], hi[0], hi[1]});
+        }
+    };
+    constexpr int kHalf = G::TM / 2; // row tiles are read and multiplied in two halves
+    auto read_x = [&](const char *st, int half, bf16x8(&xf)[kHalf]) {
+#pragma unroll
+        for (int k = 0; k < kHalf; ++k)
+            xf[k] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(st + xoff + (half * kHalf + k) * 1024));
     };
 
     floatx4 acc[G::TN][G::TM];
@@ -257,62 +304,81 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 #pragma unroll
         for (int i = 0; i < G::TM; ++i) acc[t][i] = floatx4{};
 
-    // The fragments of stage i, once it is there; refills the ring.
-    auto stage = [&](int i, bf16x8(&wf)[G::TN], bf16x8(&xf)[G::TM]) {
-        // this wave's loads of stage i are done (later stages' may be in flight) ...
-        if (xw) __builtin_amdgcn_s_waitcnt(waitcnt_vm((kWDma + kXDma) * (kStages - 2)));
-        else __builtin_amdgcn_s_waitcnt(waitcnt_vm(kWDma * (kStages - 2)));
-        // ... and every wave's, and every wave has read stage i - 1
+    // Stage i + 1 is there and stage i's slot free: this wave's reads of stage i and
+    // its loads of stage i + 1 are done (later ones may be in flight), and every
+    // wave's.  Refills the slot.
+    auto next_stage = [&](int i) {
+        asm volatile("" ::: "memory");
+        if (xw) __builtin_amdgcn_s_waitcnt(waitcnt_vm((kWDma + kXDma) * (kStages - 2)) & kWaitLgkm0);
+        else __builtin_amdgcn_s_waitcnt(waitcnt_vm(kWDma * (kStages - 2)) & kWaitLgkm0);
         __builtin_amdgcn_s_barrier();
-        issue(i + kStages - 1);
-        const char *st = lds + (i % kStages) * kStageBytes;
-#pragma unroll
-        for (int t = 0; t < G::TN; ++t) {
-            const u32x2 lo = read_tr(st + woff[0] + wunit(t)), hi = read_tr(st + woff[1] + wunit(t));
-            wf[t] = __builtin_bit_cast(bf16x8, u32x4{lo[0], lo[1], hi[0], hi[1]});
-        }
-#pragma unroll
-        for (int k = 0; k < G::TM; ++k) xf[k] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(st + xoff[k]));
+        asm volatile("" ::: "memory");
+        issue(i + kStages);
     };
-    constexpr int kWaitLgkm0 = 15 | (3 << 14) | (7 << 4); // this wave's fragment reads are done before the next barrier
+    // Base stage i: the second half of its rows is read while the first half's
+    // products run, and the next stage's columns and first half while the second
+    // half's do.  w0: its column fragments, w1: the next stage's.
+    bf16x8 wa[G::TN], wb[G::TN], xa[kHalf], xb[kHalf];
+    auto base_stage = [&](int i, bf16x8(&w0)[G::TN], bf16x8(&w1)[G::TN]) {
+        read_x(lds + (i % kStages) * kStageBytes, 1, xb);
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue(i);
-    const int nbase = k_end - k_begin;
-    for (int i = 0; i < nbase; ++i) {
-        bf16x8 wf[G::TN], xf[G::TM];
-        stage(i, wf, xf);
-#pragma unroll
-        for (int k = 0; k < G::TM; ++k)
+        for (int k = 0; k < kHalf; ++k)
 #pragma unroll
             for (int t = 0; t < G::TN; ++t)
-                acc[t][k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[t], xf[k], acc[t][k], 0, 0, 0);
-        __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+                acc[t][k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w0[t], xa[k], acc[t][k], 0, 0, 0);
+        next_stage(i);
+        const char *st = lds + ((i + 1) % kStages) * kStageBytes;
+        read_w(st, w1);
+        read_x(st, 0, xa);
+#pragma unroll
+        for (int k = 0; k < kHalf; ++k)
+#pragma unroll
+            for (int t = 0; t < G::TN; ++t)
+                acc[t][kHalf + k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w0[t], xb[k], acc[t][kHalf + k], 0, 0, 0);
+    };
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) issue(i);
+    if (xw) __builtin_amdgcn_s_waitcnt(waitcnt_vm((kWDma + kXDma) * (kStages - 1)));
+    else __builtin_amdgcn_s_waitcnt(waitcnt_vm(kWDma * (kStages - 1)));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    read_w(lds, wa);
+    read_x(lds, 0, xa);
+    int i = 0;
+    for (; i + 1 < nbase; i += 2) {
+        base_stage(i, wa, wb);
+        base_stage(i + 1, wb, wa);
     }
+    if (i < nbase) base_stage(i++, wa, wb);
     // Correction: a step's products go to the rows of its segment alone, so that a
     // NaN or infinity in one adapter (times the other rows' zeros) stays with it.
-    for (int i = nbase, s = s0, j = 0; i < nst; ++i) {
-        const lora_seg_desc *d = a.seg + s;
-        const int begin = d->start, end = begin + d->len;
-        bf16x8 wf[G::TN], xf[G::TM];
-        stage(i, wf, xf);
+    for (; i < nst; ++i) {
+        const cptr<lora_seg_desc> d = as_const(a.seg + cs);
+        const int first = d->start, last = first + d->len;
+        const char *st = lds + (i % kStages) * kStageBytes;
+        read_w(st, wa);
 #pragma unroll
-        for (int k = 0; k < G::TM; ++k) {
-            const int p0 = m0 + (wr * G::TM + k) * 16;
-            if (p0 + 16 <= begin || p0 >= end) continue; // wave-uniform
-            const bool mine = p0 + m >= begin && p0 + m < end;
+        for (int h = 0; h < 2; ++h) {
+            read_x(st, h, xa);
 #pragma unroll
-            for (int t = 0; t < G::TN; ++t) {
-                const floatx4 v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[t], xf[k], floatx4{}, 0, 0, 0);
+            for (int k = 0; k < kHalf; ++k) {
+                const int p0 = m0 + (wr * G::TM + h * kHalf + k) * 16;
+                if (p0 + 16 <= first || p0 >= last) continue; // wave-uniform
+                const bool mine = p0 + m >= first && p0 + m < last;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) acc[t][k][q] += mine ? v[q] : 0.f;
+                for (int t = 0; t < G::TN; ++t) {
+                    const floatx4 v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wa[t], xa[k], floatx4{}, 0, 0, 0);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) acc[t][h * kHalf + k][q] += mine ? v[q] : 0.f;
+                }
             }
         }
-        __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
-        j += 16;
-        if (j >= d->rank) {
-            j = 0;
-            ++s;
+        cj += 16;
+        if (cj >= d->rank) {
+            cj = 0;
+            ++cs;
         }
+        next_stage(i);
     }
     // no direct load may still be writing this workgroup's LDS when it ends
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
