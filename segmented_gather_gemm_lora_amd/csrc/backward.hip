@@ -151,7 +151,7 @@ struct BwdArgs {
     char *ut, *vt;  // u and v in windows: [window][part][rank][32 positions]
     char *ur;       // u in rows: bf16 [position][16 ranks hi, 16 ranks lo ...], fp32 [position][ranks]
     Item *items;
-    Split *splits;
+    Split *segsplits;
     float *part;
     int64_t part_stride;
     int span, nitems, nsplit;
@@ -160,6 +160,9 @@ struct BwdArgs {
     int sides; // bit 0: v is wanted, bit 1: u
     void *dx;
     int64_t lddx;
+    // JOIN: the sums of a base product in parts, [splits][T][d_in] by plan rows
+    const float *joins;
+    int splits, T, Tp;
 };
 
 // ----------------------------------------------------------------------------
@@ -233,7 +236,7 @@ __device__ void list_items(const BwdArgs &a, int *scan, int nthreads)
             const int e = i == n - 1 ? end : (start / a.span + i + 1) * a.span;
             a.items[it + i] = Item{gA, gB, b, e, r, n > 1 ? sl + i : -1};
         }
-        if (nq) a.splits[sp] = Split{s, sl, n, 0};
+        if (nq) a.segsplits[sp] = Split{s, sl, n, 0};
         item0 += sc[0][nthreads - 1];
         slot0 += sc[1][nthreads - 1];
         split0 += sc[2][nthreads - 1];
@@ -528,9 +531,6 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void bwd_shrink_kernel(BwdArgs a
 // ranks in groups of 16 RT.
 // ----------------------------------------------------------------------------
 constexpr int kGradWaves = 4;
-#define LORA_GOCC (RT == 1 ? 5 : RT == 2 ? 4 : 2)
-#define LORA_DOCC 2
-
 constexpr int kMaxSpan = 2048;
 
 // The wave's column fragments of one window, from its LDS tile: 32 rows of 128
@@ -729,7 +729,7 @@ __device__ __forceinline__ void grad_item(const BwdArgs &a, const GradSide &sd, 
 // RT: rank tiles that a wave holds (the plan's largest rank, at most 4: higher
 // ranks are `groups` of 64, a workgroup each).
 template <int DT, bool VEC, int RT>
-__global__ __launch_bounds__(kGradWaves * 64, LORA_GOCC) void bwd_grad_kernel(BwdArgs a, int tiles_A, int tiles, int groups)
+__global__ __launch_bounds__(kGradWaves * 64, RT == 1 ? 5 : RT == 2 ? 4 : 2) void bwd_grad_kernel(BwdArgs a, int tiles_A, int tiles, int groups)
 {
     __shared__ __attribute__((aligned(16))) char tiles_lds[DT == LORA_BF16 ? kGradWaves * 4096 : 16];
     __shared__ int32_t tok[kMaxSpan];
@@ -769,7 +769,7 @@ __global__ __launch_bounds__(kGradWaves * 64, LORA_GOCC) void bwd_grad_kernel(Bw
 // Launch 3: gradient = sum of a split segment's slots, in slot order.
 __global__ __launch_bounds__(256) void bwd_reduce_kernel(BwdArgs a)
 {
-    const Split sp = a.splits[blockIdx.y];
+    const Split sp = a.segsplits[blockIdx.y];
     const lora_seg_desc *sd = a.seg + sp.seg;
     const int64_t nA = int64_t(sd->rank) * a.d_in, n = nA + int64_t(sd->rank) * a.d_out;
     const uint64_t gA = a.grad_A ? a.grad_A[sd->adapter] : 0, gB = a.grad_B ? a.grad_B[sd->adapter] : 0;
@@ -797,35 +797,47 @@ __global__ __launch_bounds__(256) void bwd_reduce_kernel(BwdArgs a)
 // ----------------------------------------------------------------------------
 constexpr int kDxWaves = 4;
 
-template <int DT, bool VEC>
-__global__ __launch_bounds__(kDxWaves * 64, LORA_DOCC) void bwd_dx_kernel(BwdArgs a, int tiles)
+// JOIN: dx is not read but set, to the sum of the parts of a base product plus u A,
+// for every row of the plan, by blocks of 16 rows (those past the plan's: rows
+// without an adapter).
+template <int DT, bool VEC, bool JOIN>
+__global__ __launch_bounds__(kDxWaves * 64, JOIN ? 4 : 2) void bwd_dx_kernel(BwdArgs a, int tiles)
 {
     using E = Elem<DT>;
     using T = typename E::T;
     __shared__ __attribute__((aligned(16))) char tiles_lds[kDxWaves * 2 * 2048];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), m = lane & 15, g = lane >> 4;
-    const lora_chunk_desc *d = a.chunk + blockIdx.x / tiles;
+    const int unit = blockIdx.x / tiles;
     const int c0 = int(blockIdx.x % tiles) * (64 * kDxWaves) + 64 * wave;
     if (c0 >= a.d_in) return;
-    const int r = d->rank, n = d->n, p0 = d->p0;
+    constexpr int RB = JOIN ? 1 : 4; // row blocks
+    int r = 0, p0 = 0, n = 0;
+    const void *A = nullptr;
+    auto take = [&](const auto *d) {
+        r = d->rank, n = d->n, p0 = d->p0;
+        A = reinterpret_cast<const void *>(d->A);
+    };
+    if constexpr (!JOIN) take(a.chunk + unit);
+    else if (unit < a.nblk) take(a.blk + unit);
+    else p0 = a.Tp + 16 * (unit - a.nblk), n = min(16, a.T - p0);
     char *tile = tiles_lds + wave * 4096;
     // operands of 16 ranks: u of 4 row blocks, and A by rows (bf16: rank
     // (lane / 8) + 8 i, column 8 (lane % 8)) or by column fragments (fp32)
     struct Ops {
-        typename E::F uf[4], af[4];
+        typename E::F uf[RB], af[4];
     };
     constexpr int kU = DT == LORA_BF16 ? 4 : int(sizeof(float)); // bytes of u in rows per rank
-    uint32_t uoff[4];
+    uint32_t uoff[RB];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) uoff[i] = uint32_t(min(16 * i + m, n - 1)) * uint32_t(a.r16 * kU) + 16 * g; // past n: not stored
+    for (int i = 0; i < RB; ++i) uoff[i] = uint32_t(min(16 * i + m, n - 1)) * uint32_t(a.r16 * kU) + 16 * g; // past n: not stored
     const char *ur = a.ur + int64_t(p0) * a.r16 * kU;
     const bool whole = c0 + 64 <= a.d_in; // every piece of this wave lies in its row
     const uint32_t acol = c0 + 8 * (lane & 7) < a.d_in ? 16 * (lane & 7) : 0;
     auto load = [&](Ops &o, int j0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o.uf[i] = __builtin_bit_cast(typename E::F, load16(ur + j0 * kU, uoff[i]));
+        for (int i = 0; i < RB; ++i) o.uf[i] = __builtin_bit_cast(typename E::F, load16(ur + j0 * kU, uoff[i]));
         if constexpr (DT == LORA_BF16) {
-            const char *base = reinterpret_cast<const char *>(d->A) + (int64_t(j0) * a.d_in + c0) * 2;
+            const char *base = static_cast<const char *>(A) + (int64_t(j0) * a.d_in + c0) * 2;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int j = (lane >> 3) + 8 * i;
@@ -838,23 +850,23 @@ __global__ __launch_bounds__(kDxWaves * 64, LORA_DOCC) void bwd_dx_kernel(BwdArg
                 o.af[i] = __builtin_bit_cast(bf16x8, w);
             }
         } else {
-            const gptr<T> A = as_global<T>(reinterpret_cast<const void *>(d->A));
+            const gptr<T> Af = as_global<T>(A);
 #pragma unroll
             for (int e = 0; e < E::kVec; ++e) {
                 const int j = j0 + 4 * g + e;
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    const T w = A[int64_t(j < r ? j : r - 1) * a.d_in + min(c0 + 16 * t + m, a.d_in - 1)];
+                    const T w = Af[int64_t(j < r ? j : r - 1) * a.d_in + min(c0 + 16 * t + m, a.d_in - 1)];
                     o.af[t][e] = j < r ? w : 0.f;
                 }
             }
         }
     };
-    floatx4 acc[4][4]; // column tile, row block
+    floatx4 acc[4][RB]; // column tile, row block
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[t][i] = floatx4{};
+        for (int i = 0; i < RB; ++i) acc[t][i] = floatx4{};
     auto products = [&](const Ops &o, int s) {
         typename E::F af[4];
         if constexpr (DT == LORA_BF16) {
@@ -872,22 +884,22 @@ __global__ __launch_bounds__(kDxWaves * 64, LORA_DOCC) void bwd_dx_kernel(BwdArg
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[t][i] = mma<DT>(af[t], o.uf[i], acc[t][i]);
+            for (int i = 0; i < RB; ++i) acc[t][i] = mma<DT>(af[t], o.uf[i], acc[t][i]);
     };
     // the first operands, then dx's rows (needed last), then each next step's
     // operands before the products of the current one
     Ops o0, o1;
-    load(o0, 0);
-    T *row[4];       // element by element
-    uint32_t yoff[4]; // VEC: byte offsets of the row's pieces of this lane
-    u32x4 y[4][2];
+    if (!JOIN || r) load(o0, 0);
+    T *row[RB];      // element by element
+    uint32_t yoff[RB]; // VEC: byte offsets of the row's pieces of this lane
+    u32x4 y[RB][2];
     char *dxc = reinterpret_cast<char *>(static_cast<T *>(a.dx) + c0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = d->rows[min(16 * i + m, n - 1)];
+    for (int i = 0; i < RB; ++i) {
+        const int t = a.perm[p0 + min(16 * i + m, n - 1)];
         row[i] = static_cast<T *>(a.dx) + int64_t(t) * a.lddx;
         yoff[i] = uint32_t(t) * uint32_t(a.lddx * int(sizeof(T))) + 16 * g;
-        if constexpr (DT == LORA_BF16) {
+        if constexpr (!JOIN && DT == LORA_BF16) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int c = c0 + col<DT>(g, 8 * h);
@@ -897,7 +909,19 @@ __global__ __launch_bounds__(kDxWaves * 64, LORA_DOCC) void bwd_dx_kernel(BwdArg
             }
         }
     }
-    for (int j0 = 0;;) {
+    if constexpr (JOIN) {
+        const float *q = a.joins + int64_t(p0) * a.d_in + c0;
+        for (int k = 0; k < a.splits; ++k, q += int64_t(a.T) * a.d_in)
+#pragma unroll
+            for (int i = 0; i < RB; ++i)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const int c = col<DT>(g, 4 * t);
+                    acc[t][i] += *reinterpret_cast<const floatx4 *>(q + int64_t(min(16 * i + m, n - 1)) * a.d_in +
+                                                                    (c0 + c < a.d_in ? c : 0));
+                }
+    }
+    for (int j0 = 0; !JOIN || r;) {
         if (j0 + 16 < r) load(o1, j0 + 16);
         products(o0, 0);
         if ((j0 += 16) >= r) break;
@@ -906,7 +930,7 @@ __global__ __launch_bounds__(kDxWaves * 64, LORA_DOCC) void bwd_dx_kernel(BwdArg
         if ((j0 += 16) >= r) break;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RB; ++i) {
         if (16 * i + m >= n) continue;
         if constexpr (DT == LORA_BF16) {
 #pragma unroll
@@ -918,7 +942,8 @@ __global__ __launch_bounds__(kDxWaves * 64, LORA_DOCC) void bwd_dx_kernel(BwdArg
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float f0 = e < 2 ? lo[2 * e] : hi[2 * e - 4], f1 = e < 2 ? lo[2 * e + 1] : hi[2 * e - 3];
-                    o[e] = pack_bf16x2(bf16_to_f32(y[i][h][e] & 0xffffu) + f0, bf16_to_f32(y[i][h][e] >> 16) + f1);
+                    o[e] = JOIN ? pack_bf16x2(f0, f1)
+                                : pack_bf16x2(bf16_to_f32(y[i][h][e] & 0xffffu) + f0, bf16_to_f32(y[i][h][e] >> 16) + f1);
                 }
                 if constexpr (VEC) *reinterpret_cast<u32x4 *>(dxc + 64 * h + yoff[i]) = o;
                 else if (whole) *reinterpret_cast<u32x4_any *>(row[i] + c) = o;
@@ -1012,11 +1037,9 @@ size_t sgmv_backward_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out, int
     return layout_of(T, d_in, d_out, max_rank).bytes;
 }
 
-int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p, void *ws, const uint16_t **u_rows,
-                         int64_t *ldu)
+static BwdArgs make_args(const BackwardArgs &b, const PlanView &p, const Layout &l, void *ws)
 {
     const lora_plan_header *h = p.h;
-    const Layout l = layout_of(h->num_sorted, b.d_in, b.d_out, h->max_rank);
     char *w = static_cast<char *>(ws);
     BwdArgs a{};
     a.x = b.x;
@@ -1037,7 +1060,8 @@ int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p
     a.vt = w + l.vt;
     a.ur = w + l.ur;
     a.items = reinterpret_cast<Item *>(w + l.items);
-    a.splits = reinterpret_cast<Split *>(w + l.splits);
+    a.splits = 1;
+    a.segsplits = reinterpret_cast<Split *>(w + l.splits);
     a.part = reinterpret_cast<float *>(w + l.part);
     a.part_stride = l.part_stride;
     a.span = l.span;
@@ -1046,6 +1070,17 @@ int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p
     a.accumulate = b.accumulate;
     a.dx = b.dx;
     a.lddx = b.lddx;
+    a.T = h->num_tokens;
+    a.Tp = h->num_sorted;
+    return a;
+}
+
+int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p, void *ws, const uint16_t **u_rows,
+                         int64_t *ldu)
+{
+    const lora_plan_header *h = p.h;
+    const Layout l = layout_of(h->num_sorted, b.d_in, b.d_out, h->max_rank);
+    BwdArgs a = make_args(b, p, l, ws);
     a.sides = (b.grad_B ? 1 : 0) | (b.grad_A || b.dx || u_rows ? 2 : 0);
     if (u_rows) {
         *u_rows = reinterpret_cast<const uint16_t *>(a.ur);
@@ -1096,13 +1131,28 @@ int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p
         if (nwg > (int64_t(1) << 31) - 1) return fail(LORA_ERR_ARG, "backward: too many dx tiles");
         const dim3 grid{unsigned(nwg)}, block(kDxWaves * 64);
         const bool vx = vec && b.vec_dx;
-        if (bf16 && vx) launch_kernel(bwd_dx_kernel<LORA_BF16, true>, grid, block, 0, s, a, tx);
-        else if (bf16) launch_kernel(bwd_dx_kernel<LORA_BF16, false>, grid, block, 0, s, a, tx);
-        else if (vx) launch_kernel(bwd_dx_kernel<LORA_F32, true>, grid, block, 0, s, a, tx);
-        else launch_kernel(bwd_dx_kernel<LORA_F32, false>, grid, block, 0, s, a, tx);
+        if (bf16 && vx) launch_kernel(bwd_dx_kernel<LORA_BF16, true, false>, grid, block, 0, s, a, tx);
+        else if (bf16) launch_kernel(bwd_dx_kernel<LORA_BF16, false, false>, grid, block, 0, s, a, tx);
+        else if (vx) launch_kernel(bwd_dx_kernel<LORA_F32, true, false>, grid, block, 0, s, a, tx);
+        else launch_kernel(bwd_dx_kernel<LORA_F32, false, false>, grid, block, 0, s, a, tx);
         if ((st = checked("backward dx"))) return st;
     }
     return LORA_OK;
+}
+
+int launch_dx_join(hipStream_t s, const BackwardArgs &b, const PlanView &p, void *ws, const float *parts, int splits)
+{
+    const lora_plan_header *h = p.h;
+    BwdArgs a = make_args(b, p, layout_of(h->num_sorted, b.d_in, b.d_out, h->max_rank), ws);
+    a.joins = parts;
+    a.splits = splits;
+    const int tx = (a.d_in + 64 * kDxWaves - 1) / (64 * kDxWaves);
+    const int64_t nwg = (int64_t(a.nblk) + (a.T - a.Tp + 15) / 16) * tx;
+    if (nwg > (int64_t(1) << 31) - 1) return fail(LORA_ERR_ARG, "backward: too many dx tiles");
+    const dim3 grid{unsigned(nwg)}, block(kDxWaves * 64);
+    if (b.vec_dx) launch_kernel(bwd_dx_kernel<LORA_BF16, true, true>, grid, block, 0, s, a, tx);
+    else launch_kernel(bwd_dx_kernel<LORA_BF16, false, true>, grid, block, 0, s, a, tx);
+    return checked("backward join");
 }
 
 } // namespace lora

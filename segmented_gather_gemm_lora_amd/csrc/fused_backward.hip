@@ -21,9 +21,11 @@
 // Units that lie outside (rows of another segment, ranks past r, the summed
 // axis past d_out) are loaded from a block of zeros.
 //
-// Few tiles (a narrow d_in) leave most CUs idle, so the stages are split:
-// each split writes fp32 sums to the workspace, and a last launch adds them in
-// split order.
+// Few tiles (a narrow d_in, few rows) leave most CUs idle, so the stages are split:
+// each split writes fp32 sums to the workspace, and a last launch (the backward's
+// dx kernel) adds them in split order, and u A.  With 200 adapters over 1024
+// tokens the correction took 20 us as steps of the split GEMM (117 us, 96
+// without) and takes XX us in the last launch.
 #include "internal.h"
 
 #include <algorithm>
@@ -145,41 +147,16 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     const int c0 = (id % a.tiles_n) * kCols, split = id / a.tiles_n;
     const int nk = (a.d_out + kBK - 1) / kBK; // stages of the base product
 
-    // The tile's stages: those of the base product, then the correction steps of
-    // the segments s0 .. s1 that meet it; each split takes an equal run of them.
+    // The stages of the base product, shared by the splits, then (one split) the
+    // correction steps of the segments s0 .. s1 that meet the tile.
     int s0 = 0, s1 = -1, ncorr = 0;
-    if (m0 < a.Tp) {
+    if (a.splits == 1 && m0 < a.Tp) {
         s0 = uniform(a.segidx[m0]);
         s1 = uniform(a.segidx[min(m0 + ROWS, a.Tp) - 1]);
         for (int s = s0; s <= s1; s += 64) ncorr += wave_sum(s + lane <= s1 ? (a.seg[s + lane].rank + 15) >> 4 : 0);
     }
-    const int begin = int(int64_t(nk + ncorr) * split / a.splits), end = int(int64_t(nk + ncorr) * (split + 1) / a.splits);
-    const int k_begin = min(begin, nk);
-    const int nbase = min(end, nk) - k_begin, nst = end - begin;
-    // the first correction step of this run: segment cs, first rank cj
-    int cs = s0, cj = 0;
-    if (end > nk && begin > nk) {
-        int skip = begin - nk;
-        for (int s = s0; s <= s1; s += 64) {
-            const int n = s + lane <= s1 ? (a.seg[s + lane].rank + 15) >> 4 : 0;
-            int upto = n; // steps of this and the lanes before
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int v = __shfl_up(upto, d);
-                upto += lane >= d ? v : 0;
-            }
-            const int all = uniform(__shfl(upto, 63));
-            if (skip < all) {
-                const int at = __ffsll(__ballot(upto > skip)) - 1;
-                cs = s + at;
-                cj = 16 * (skip - uniform(__shfl(upto - n, at)));
-                break;
-            }
-            skip -= all;
-        }
-        cs = uniform(cs);
-        cj = uniform(cj);
-    }
+    const int k_begin = int(int64_t(nk) * split / a.splits);
+    const int nbase = int(int64_t(nk) * (split + 1) / a.splits) - k_begin, nst = nbase + ncorr;
 
     // This lane's units.  W0 part: slot 64 i + lane of the stage, i = 2 wave + j:
     // row slot / 32.  dy part: row slot / 4.
@@ -207,9 +184,14 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     }
 
     // Stage i of this run: nbase base stages, then the correction.
-    int is = cs, ij = cj; // the next correction step to load, and its segment (read ahead)
-    lora_seg_desc next{};
-    if (nst > nbase) next = *as_const(a.seg + is);
+    int is = s0, ij = 0; // the next correction step to load, and its segment (read ahead)
+    uint64_t nA = 0;
+    int nr = 0, nfirst = 0, nlen = 0;
+    auto read_seg = [&] {
+        const cptr<lora_seg_desc> d = as_const(a.seg + is);
+        nA = d->A, nr = d->rank, nfirst = d->start, nlen = d->len;
+    };
+    if (nst > nbase) read_seg();
     auto issue = [&](int i) {
         const uint32_t wbase = lds0 + uint32_t((i % kStages) * kStageBytes + wave * kWDma * 1024);
         const uint32_t xbase = lds0 + uint32_t((i % kStages) * kStageBytes + kWBytes + wave * kXDma * 1024);
@@ -241,8 +223,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
                 }
             }
         } else if (i < nst) {
-            const int r = next.rank, first = next.start, last = first + next.len;
-            const uint16_t *A = reinterpret_cast<const uint16_t *>(next.A);
+            const int r = nr, first = nfirst, last = nfirst + nlen;
+            const uint16_t *A = reinterpret_cast<const uint16_t *>(nA);
 #pragma unroll
             for (int j = 0; j < kWDma; ++j) {
                 const int rank = ij + (wrow[j] & 15);
@@ -260,7 +242,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
             if (ij >= r) {
                 ij = 0;
                 is = min(is + 1, s1);
-                next = *as_const(a.seg + is);
+                read_seg();
             }
         } else { // past the end: keeps the number of loads in flight
 #pragma unroll
@@ -352,7 +334,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     if (i < nbase) base_stage(i++, wa, wb);
     // Correction: a step's products go to the rows of its segment alone, so that a
     // NaN or infinity in one adapter (times the other rows' zeros) stays with it.
-    for (; i < nst; ++i) {
+    for (int cs = s0, cj = 0; i < nst; ++i) {
         const cptr<lora_seg_desc> d = as_const(a.seg + cs);
         const int first = d->start, last = first + d->len;
         const char *st = lds + (i % kStages) * kStageBytes;
@@ -405,25 +387,6 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     }
 }
 
-// dx row = sum of the splits' sums, in split order.
-__global__ __launch_bounds__(256) void dgrad_reduce_kernel(DgradArgs a)
-{
-    const int64_t u = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    const int upr = a.d_in / 8;
-    const int64_t p = u / upr;
-    if (p >= a.T) return;
-    const int c = int(u % upr) * 8;
-    const float *src = a.part + p * a.d_in + c;
-    const int64_t pitch = int64_t(a.T) * a.d_in;
-    floatx4 lo = floatx4{}, hi = floatx4{};
-    for (int s = 0; s < a.splits; ++s, src += pitch) {
-        lo += *reinterpret_cast<const floatx4 *>(src);
-        hi += *reinterpret_cast<const floatx4 *>(src + 4);
-    }
-    *reinterpret_cast<u32x4 *>(a.dx + int64_t(a.perm[p]) * a.lddx + c) =
-        u32x4{pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]), pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3])};
-}
-
 int rows_of(int32_t T) { return T <= 64 ? 64 : 256; }
 
 // Splits of the summed axis: as many as fill the chip in one round, with at
@@ -463,8 +426,7 @@ int launch_fused_backward(hipStream_t s, const BackwardArgs &b, const void *W0, 
     const int64_t tiles = int64_t(a.tiles_m) * a.tiles_n;
     if (tiles > (int64_t(1) << 31) - 1) return fail(LORA_ERR_ARG, "fused backward: too many tiles");
     a.splits = splits_of(tiles, b.d_out);
-    const int64_t units = int64_t(T) * (b.d_in / 8);
-    if ((units + 255) / 256 > (int64_t(1) << 31) - 1 || T > (1 << 27))
+    if (T > (1 << 27))
         return fail(LORA_ERR_ARG, "fused backward: too many rows");
     char *w = static_cast<char *>(ws) + up256(sgmv_backward_workspace_bytes(T, b.d_in, b.d_out, max_rank));
     // the adapters' gradients, and u
@@ -500,11 +462,7 @@ int launch_fused_backward(hipStream_t s, const BackwardArgs &b, const void *W0, 
     if (rows == 64) launch_kernel(dgrad_kernel<64>, grid, dim3(kThreads), 0, s, a);
     else launch_kernel(dgrad_kernel<256>, grid, dim3(kThreads), 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return fail(LORA_ERR_HIP, "fused backward launch: %s", hipGetErrorString(e));
-    if (a.splits > 1) {
-        launch_kernel(dgrad_reduce_kernel, dim3(unsigned((units + 255) / 256)), dim3(256), 0, s, a);
-        if ((e = hipGetLastError()) != hipSuccess)
-            return fail(LORA_ERR_HIP, "fused backward reduce launch: %s", hipGetErrorString(e));
-    }
+    if (a.splits > 1) return launch_dx_join(s, b, p, ws, a.part, a.splits);
     return LORA_OK;
 }
 
