@@ -964,21 +964,27 @@ __global__ __launch_bounds__(kDxWaves * 64, JOIN ? 4 : 2) void bwd_dx_kernel(Bwd
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Sorted positions of one span, a whole number of windows: up to kSpans spans
-// for the rows, so that the bytes of partial sums stay bounded.  Few rows have
-// wide spans, since a segment over two of them costs a launch.
-constexpr int kMinSpan = 64, kSpans = 16;
-int span_of(int32_t rows)
+// Sorted positions of one span, a power of two of windows.  Items of the whole
+// batch are wanted, since a segment over k spans costs k partial sums and a launch:
+// the widest span (up to kLong rows, 16 windows one after the other) that still
+// gives the chip kEnough workgroups.  At most kSpans spans, so that the bytes of
+// partial sums stay bounded, and none that a few rows would need.
+constexpr int kMinSpan = 64, kLong = 512, kSpans = 16, kEnough = 1024;
+int span_of(int64_t rows, int64_t segments, int64_t wgs_per_item)
 {
-    int span = rows <= 256 ? 128 : kMinSpan;
+    if (rows <= 256) return 256;
+    int span = kMinSpan;
     while (span < kMaxSpan && rows / span > kSpans) span *= 2;
+    while (span < kLong && (segments + rows / (2 * span)) * wgs_per_item >= kEnough) span *= 2;
     return span;
 }
+// Borders of spans inside `rows` sorted positions, at most, for any span that
+// span_of gives for them or for fewer.
+size_t most_borders(size_t rows) { return std::max(std::min(rows / kMinSpan, size_t(kSpans)), rows / kMaxSpan); }
 
 struct Layout {
     size_t ut, vt, ur, items, splits, part, bytes;
     int64_t part_stride;
-    int span;
 };
 
 // For up to `rows` adapted tokens; the partial sums of a segment cut into k
@@ -988,13 +994,11 @@ Layout layout_of(int32_t rows, int32_t d_in, int32_t d_out, int32_t max_rank)
     Layout l{};
     const size_t r16 = size_t(max_rank + 15) / 16 * 16, n = size_t(rows);
     const size_t windows = (n + kWin - 1) / kWin;
-    l.span = span_of(rows);
     l.ut = 0;
     l.vt = l.ut + up256(windows * kWin * r16 * 6); // three bf16 parts; fp32 takes 4 of the 6 bytes
     l.ur = l.vt + up256(windows * kWin * r16 * 6);
     l.items = l.ur + up256(n * r16 * 4);
-    // span borders inside rows / span of any fewer rows, too: the size grows with `rows`
-    const size_t borders = std::max(std::min(n / kMinSpan, size_t(kSpans)), n / kMaxSpan);
+    const size_t borders = most_borders(n);
     l.splits = l.items + up256((n + borders) * sizeof(Item));
     l.part = l.splits + up256(borders * sizeof(Split));
     l.part_stride = (int64_t(max_rank) * (int64_t(d_in) + d_out) + 3) / 4 * 4;
@@ -1064,7 +1068,6 @@ static BwdArgs make_args(const BackwardArgs &b, const PlanView &p, const Layout 
     a.segsplits = reinterpret_cast<Split *>(w + l.splits);
     a.part = reinterpret_cast<float *>(w + l.part);
     a.part_stride = l.part_stride;
-    a.span = l.span;
     a.grad_A = b.grad_A;
     a.grad_B = b.grad_B;
     a.accumulate = b.accumulate;
@@ -1087,6 +1090,10 @@ int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p
         *ldu = 2 * int64_t(a.r16);
     }
     if (!a.sides) return LORA_OK;
+    constexpr int kCols = 64 * kGradWaves;
+    const int tiles_A = a.grad_A ? (a.d_in + kCols - 1) / kCols : 0;
+    const int tiles = tiles_A + (a.grad_B ? (a.d_out + kCols - 1) / kCols : 0), groups = (a.r16 + 63) / 64;
+    a.span = span_of(h->num_sorted, h->num_segments, int64_t(tiles) * groups);
     const lora_seg_desc *hs = reinterpret_cast<const lora_seg_desc *>(reinterpret_cast<const char *>(h) + h->seg_offset);
     for (int i = 0; i < h->num_segments; ++i) {
         const int n = (hs[i].start + hs[i].len - 1) / a.span - hs[i].start / a.span + 1;
@@ -1106,11 +1113,7 @@ int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p
     int st = checked("backward shrink");
     if (st) return st;
 
-    constexpr int kCols = 64 * kGradWaves;
-    const int tiles_A = a.grad_A ? (a.d_in + kCols - 1) / kCols : 0;
-    const int tiles = tiles_A + (a.grad_B ? (a.d_out + kCols - 1) / kCols : 0);
     if (tiles) {
-        const int groups = (a.r16 + 63) / 64;
         const int64_t nwg = int64_t(a.nitems) * tiles * groups;
         if (nwg > (int64_t(1) << 31) - 1) return fail(LORA_ERR_ARG, "backward: too many work items");
         const dim3 grid{unsigned(nwg)};
