@@ -13,13 +13,13 @@
 //     block and side, its waves split the long axis and are summed in LDS in
 //     wave order), stored in the forms that the next launches multiply with;
 //     one more workgroup lists the work items of launch 2;
-//  2. bwd_grad_kernel: dA and dB.  An item is one segment's rows inside one
-//     span of `span` sorted positions; an item covers 256 columns of x or dy per
-//     workgroup.  A segment inside one span is written at once; the sums of a
-//     segment that crosses spans go to the workspace;
+//  2. bwd_out_kernel: dA, dB and dx.  An item of dA and dB is one segment's rows
+//     inside one span of `span` sorted positions; a workgroup takes 256 columns of
+//     x or dy of it.  A segment inside one span is written at once; the sums of a
+//     segment that crosses spans go to the workspace.  Further workgroups take 256
+//     columns of dx for a block of 16 rows (ranks up to 32) or a chunk of 64;
 //  3. bwd_reduce_kernel: adds those partial sums in span order (a fixed order:
-//     the gradients do not change from run to run);
-//  4. bwd_dx_kernel: dx, one workgroup per 64-row chunk and 256 columns.
+//     the gradients do not change from run to run).
 //
 // The transposed operands.  MFMA wants, in each lane, consecutive elements of
 // the summed axis.  x, dy (summed over rows for dA, dB), A (summed over its
@@ -158,6 +158,9 @@ struct BwdArgs {
     const uint64_t *grad_A, *grad_B;
     int accumulate;
     int sides; // bit 0: v is wanted, bit 1: u
+    // launch 2: column tiles of x and of both, groups of 64 ranks, gradient workgroups,
+    // column tiles of dx
+    int tiles_A, tiles, groups, ngrad, tiles_x;
     void *dx;
     int64_t lddx;
     // JOIN: the sums of a base product in parts, [splits][T][d_in] by plan rows
@@ -532,6 +535,11 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void bwd_shrink_kernel(BwdArgs a
 // ----------------------------------------------------------------------------
 constexpr int kGradWaves = 4;
 constexpr int kMaxSpan = 2048;
+constexpr int kTileCols = 64 * kGradWaves; // columns of a workgroup
+// Row blocks of a dx workgroup, by the rank tiles of a gradient one (which set the
+// registers that the launch has): with one rank tile, chunks of 64 rows would
+// take twice its registers (4096 rows of rank 16: 70 us against 29).
+constexpr int dx_blocks(int rank_tiles) { return rank_tiles >= 3 ? 4 : 1; }
 
 // The wave's column fragments of one window, from its LDS tile: 32 rows of 128
 // bytes, unit 16 bytes, unit un of row q in slot un ^ (4 if q & 2): 4 rows
@@ -729,21 +737,19 @@ __device__ __forceinline__ void grad_item(const BwdArgs &a, const GradSide &sd, 
 // RT: rank tiles that a wave holds (the plan's largest rank, at most 4: higher
 // ranks are `groups` of 64, a workgroup each).
 template <int DT, bool VEC, int RT>
-__global__ __launch_bounds__(kGradWaves * 64, RT == 1 ? 5 : RT == 2 ? 4 : 2) void bwd_grad_kernel(BwdArgs a, int tiles_A, int tiles, int groups)
+__device__ __forceinline__ void grad_unit(const BwdArgs &a, int id, char *tiles_lds, int32_t *tok)
 {
-    __shared__ __attribute__((aligned(16))) char tiles_lds[DT == LORA_BF16 ? kGradWaves * 4096 : 16];
-    __shared__ int32_t tok[kMaxSpan];
-    const int tl = blockIdx.x % tiles, group = blockIdx.x / tiles % groups;
-    const Item it = a.items[blockIdx.x / tiles / groups];
+    const int tl = id % a.tiles, group = id / a.tiles % a.groups;
+    const Item it = a.items[id / a.tiles / a.groups];
     if (64 * group >= it.rank) return;
-    const int side = tl >= tiles_A;
+    const int side = tl >= a.tiles_A;
     const uint64_t grad = side ? it.grad_B : it.grad_A;
     if (!grad) return; // this adapter's gradient is not wanted
     for (int i = threadIdx.x; i < it.end - it.begin; i += kGradWaves * 64) tok[i] = a.perm[it.begin + i];
     __syncthreads();
     const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, r = it.rank;
     const GradSide sd = side ? GradSide{a.dy, a.vt, a.lddy, a.d_out} : GradSide{a.x, a.ut, a.ldx, a.d_in};
-    const int c0 = (side ? tl - tiles_A : tl) * (64 * kGradWaves) + 64 * wave;
+    const int c0 = (side ? tl - a.tiles_A : tl) * (64 * kGradWaves) + 64 * wave;
     if (c0 >= sd.D) return;
     float *dst = reinterpret_cast<float *>(grad);
     bool add = a.accumulate;
@@ -766,59 +772,32 @@ __global__ __launch_bounds__(kGradWaves * 64, RT == 1 ? 5 : RT == 2 ? 4 : 2) voi
     else ranks(std::false_type{});
 }
 
-// Launch 3: gradient = sum of a split segment's slots, in slot order.
-__global__ __launch_bounds__(256) void bwd_reduce_kernel(BwdArgs a)
-{
-    const Split sp = a.segsplits[blockIdx.y];
-    const lora_seg_desc *sd = a.seg + sp.seg;
-    const int64_t nA = int64_t(sd->rank) * a.d_in, n = nA + int64_t(sd->rank) * a.d_out;
-    const uint64_t gA = a.grad_A ? a.grad_A[sd->adapter] : 0, gB = a.grad_B ? a.grad_B[sd->adapter] : 0;
-    for (int64_t e = 4 * (int64_t(blockIdx.x) * 256 + threadIdx.x); e < n; e += 4 * int64_t(gridDim.x) * 256) {
-        // slots start at multiples of 4; a group of 4 may reach from dA into dB
-        const bool wA = e < nA && gA, wB = e + 3 >= nA && gB;
-        if (!wA && !wB) continue;
-        const float *src = a.part + sp.slot0 * a.part_stride + e;
-        floatx4 sum = floatx4{};
-        for (int q = 0; q < sp.count; ++q) sum += *reinterpret_cast<const floatx4 *>(src + q * a.part_stride);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t k = e + i;
-            if (k >= n) break;
-            const uint64_t base = k < nA ? gA : gB;
-            if (!base) continue;
-            float *dst = reinterpret_cast<float *>(base) + (k < nA ? k : k - nA);
-            *dst = a.accumulate ? *dst + sum[i] : sum[i];
-        }
-    }
-}
-
 // ----------------------------------------------------------------------------
-// Launch 4.  A wave: 64 columns of dx, the up to 64 rows of one chunk.
+// dx.  A wave: 64 columns, the up to 16 RB rows of a block or a chunk.
 // ----------------------------------------------------------------------------
-constexpr int kDxWaves = 4;
+constexpr int kDxWaves = kGradWaves;
 
 // JOIN: dx is not read but set, to the sum of the parts of a base product plus u A,
 // for every row of the plan, by blocks of 16 rows (those past the plan's: rows
 // without an adapter).
-template <int DT, bool VEC, bool JOIN>
-__global__ __launch_bounds__(kDxWaves * 64, JOIN ? 4 : 2) void bwd_dx_kernel(BwdArgs a, int tiles)
+template <int DT, bool VEC, bool JOIN, int RB>
+__device__ __forceinline__ void dx_unit(const BwdArgs &a, int id, char *tiles_lds)
 {
+    static_assert(RB == 1 || (RB == 4 && !JOIN), "a block or a chunk");
     using E = Elem<DT>;
     using T = typename E::T;
-    __shared__ __attribute__((aligned(16))) char tiles_lds[kDxWaves * 2 * 2048];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), m = lane & 15, g = lane >> 4;
-    const int unit = blockIdx.x / tiles;
-    const int c0 = int(blockIdx.x % tiles) * (64 * kDxWaves) + 64 * wave;
+    const int unit = id / a.tiles_x;
+    const int c0 = int(id % a.tiles_x) * (64 * kDxWaves) + 64 * wave;
     if (c0 >= a.d_in) return;
-    constexpr int RB = JOIN ? 1 : 4; // row blocks
     int r = 0, p0 = 0, n = 0;
     const void *A = nullptr;
     auto take = [&](const auto *d) {
         r = d->rank, n = d->n, p0 = d->p0;
         A = reinterpret_cast<const void *>(d->A);
     };
-    if constexpr (!JOIN) take(a.chunk + unit);
-    else if (unit < a.nblk) take(a.blk + unit);
+    if constexpr (RB == 4) take(a.chunk + unit);
+    else if (!JOIN || unit < a.nblk) take(a.blk + unit);
     else p0 = a.Tp + 16 * (unit - a.nblk), n = min(16, a.T - p0);
     char *tile = tiles_lds + wave * 4096;
     // operands of 16 ranks: u of 4 row blocks, and A by rows (bf16: rank
@@ -962,6 +941,49 @@ __global__ __launch_bounds__(kDxWaves * 64, JOIN ? 4 : 2) void bwd_dx_kernel(Bwd
     }
 }
 
+// Launch 2: the gradients' workgroups, then dx's (they read the same u).
+template <int DT, bool VEC, int RT>
+__global__ __launch_bounds__(kGradWaves * 64, RT == 1 ? 5 : RT == 2 && DT == LORA_BF16 ? 4 : 2) void bwd_out_kernel(BwdArgs a)
+{
+    __shared__ __attribute__((aligned(16))) char tiles_lds[DT == LORA_BF16 ? kGradWaves * 4096 : 16];
+    __shared__ int32_t tok[kMaxSpan];
+    if (int(blockIdx.x) < a.ngrad) grad_unit<DT, VEC, RT>(a, blockIdx.x, tiles_lds, tok);
+    else dx_unit<DT, VEC, false, dx_blocks(RT)>(a, int(blockIdx.x) - a.ngrad, tiles_lds);
+}
+
+// Launch 3: gradient = sum of a split segment's slots, in slot order.
+__global__ __launch_bounds__(256) void bwd_reduce_kernel(BwdArgs a)
+{
+    const Split sp = a.segsplits[blockIdx.y];
+    const lora_seg_desc *sd = a.seg + sp.seg;
+    const int64_t nA = int64_t(sd->rank) * a.d_in, n = nA + int64_t(sd->rank) * a.d_out;
+    const uint64_t gA = a.grad_A ? a.grad_A[sd->adapter] : 0, gB = a.grad_B ? a.grad_B[sd->adapter] : 0;
+    for (int64_t e = 4 * (int64_t(blockIdx.x) * 256 + threadIdx.x); e < n; e += 4 * int64_t(gridDim.x) * 256) {
+        // slots start at multiples of 4; a group of 4 may reach from dA into dB
+        const bool wA = e < nA && gA, wB = e + 3 >= nA && gB;
+        if (!wA && !wB) continue;
+        const float *src = a.part + sp.slot0 * a.part_stride + e;
+        floatx4 sum = floatx4{};
+        for (int q = 0; q < sp.count; ++q) sum += *reinterpret_cast<const floatx4 *>(src + q * a.part_stride);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t k = e + i;
+            if (k >= n) break;
+            const uint64_t base = k < nA ? gA : gB;
+            if (!base) continue;
+            float *dst = reinterpret_cast<float *>(base) + (k < nA ? k : k - nA);
+            *dst = a.accumulate ? *dst + sum[i] : sum[i];
+        }
+    }
+}
+
+// The last launch of the fused layer's backward.
+template <bool VEC> __global__ __launch_bounds__(kDxWaves * 64, 4) void bwd_join_kernel(BwdArgs a)
+{
+    __shared__ __attribute__((aligned(16))) char tiles_lds[kDxWaves * 4096];
+    dx_unit<LORA_BF16, VEC, true, 1>(a, blockIdx.x, tiles_lds);
+}
+
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Sorted positions of one span, a power of two of windows.  Items of the whole
@@ -1020,12 +1042,12 @@ template <int DT, bool VEC> void run_shrink(hipStream_t s, const BwdArgs &a, int
         run_shrink_mb<DT, VEC, VEC && DT == LORA_BF16 ? 4 : 1>(s, a, unsigned(a.nchunk), unsigned(nside));
     else run_shrink_mb<DT, VEC, 1>(s, a, unsigned(a.nblk), unsigned(nside));
 }
-template <int DT, bool VEC> void run_grad(hipStream_t s, const BwdArgs &a, dim3 grid, int tiles_A, int tiles, int groups)
+template <int DT, bool VEC> void run_out(hipStream_t s, const BwdArgs &a, dim3 grid)
 {
     const dim3 block(kGradWaves * 64);
-    if (a.r16 <= 16) launch_kernel(bwd_grad_kernel<DT, VEC, 1>, grid, block, 0, s, a, tiles_A, tiles, groups);
-    else if (a.r16 <= 32) launch_kernel(bwd_grad_kernel<DT, VEC, 2>, grid, block, 0, s, a, tiles_A, tiles, groups);
-    else launch_kernel(bwd_grad_kernel<DT, VEC, 4>, grid, block, 0, s, a, tiles_A, tiles, groups);
+    if (a.r16 <= 16) launch_kernel(bwd_out_kernel<DT, VEC, 1>, grid, block, 0, s, a);
+    else if (a.r16 <= 32) launch_kernel(bwd_out_kernel<DT, VEC, 2>, grid, block, 0, s, a);
+    else launch_kernel(bwd_out_kernel<DT, VEC, 4>, grid, block, 0, s, a);
 }
 
 int checked(const char *what)
@@ -1073,6 +1095,7 @@ static BwdArgs make_args(const BackwardArgs &b, const PlanView &p, const Layout 
     a.accumulate = b.accumulate;
     a.dx = b.dx;
     a.lddx = b.lddx;
+    a.tiles_x = (a.d_in + kTileCols - 1) / kTileCols;
     a.T = h->num_tokens;
     a.Tp = h->num_sorted;
     return a;
@@ -1090,10 +1113,10 @@ int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p
         *ldu = 2 * int64_t(a.r16);
     }
     if (!a.sides) return LORA_OK;
-    constexpr int kCols = 64 * kGradWaves;
-    const int tiles_A = a.grad_A ? (a.d_in + kCols - 1) / kCols : 0;
-    const int tiles = tiles_A + (a.grad_B ? (a.d_out + kCols - 1) / kCols : 0), groups = (a.r16 + 63) / 64;
-    a.span = span_of(h->num_sorted, h->num_segments, int64_t(tiles) * groups);
+    a.tiles_A = a.grad_A ? (a.d_in + kTileCols - 1) / kTileCols : 0;
+    a.tiles = a.tiles_A + (a.grad_B ? (a.d_out + kTileCols - 1) / kTileCols : 0);
+    a.groups = (a.r16 + 63) / 64;
+    a.span = span_of(h->num_sorted, h->num_segments, int64_t(a.tiles) * a.groups);
     const lora_seg_desc *hs = reinterpret_cast<const lora_seg_desc *>(reinterpret_cast<const char *>(h) + h->seg_offset);
     for (int i = 0; i < h->num_segments; ++i) {
         const int n = (hs[i].start + hs[i].len - 1) / a.span - hs[i].start / a.span + 1;
@@ -1103,42 +1126,30 @@ int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p
 
     if (a.nsplit > 65535) return fail(LORA_ERR_ARG, "backward: %d segments over several spans (> 65535)", a.nsplit);
 
+    const int64_t ngrad = int64_t(a.nitems) * a.tiles * a.groups;
+    const int64_t ndx = a.dx ? int64_t(dx_blocks((a.r16 + 15) / 16) == 4 ? a.nchunk : a.nblk) * a.tiles_x : 0;
+    if (ngrad + ndx > (int64_t(1) << 31) - 1) return fail(LORA_ERR_ARG, "backward: too many work items");
+    a.ngrad = int(ngrad);
+
     const bool bf16 = b.dtype == LORA_BF16;
-    const bool vec = b.vec_x && b.vec_dy;
+    const bool vec = b.vec_x && b.vec_dy && (!a.dx || b.vec_dx);
     const int nside = a.sides == 3 ? 2 : 1;
     if (bf16 && vec) run_shrink<LORA_BF16, true>(s, a, nside);
     else if (bf16) run_shrink<LORA_BF16, false>(s, a, nside);
     else if (vec) run_shrink<LORA_F32, true>(s, a, nside);
     else run_shrink<LORA_F32, false>(s, a, nside);
     int st = checked("backward shrink");
-    if (st) return st;
-
-    if (tiles) {
-        const int64_t nwg = int64_t(a.nitems) * tiles * groups;
-        if (nwg > (int64_t(1) << 31) - 1) return fail(LORA_ERR_ARG, "backward: too many work items");
-        const dim3 grid{unsigned(nwg)};
-        if (bf16 && vec) run_grad<LORA_BF16, true>(s, a, grid, tiles_A, tiles, groups);
-        else if (bf16) run_grad<LORA_BF16, false>(s, a, grid, tiles_A, tiles, groups);
-        else run_grad<LORA_F32, false>(s, a, grid, tiles_A, tiles, groups);
-        if ((st = checked("backward gradient"))) return st;
-        if (a.nsplit) {
-            const int64_t units = (l.part_stride / 4 + 255) / 256;
-            launch_kernel(bwd_reduce_kernel, dim3(unsigned(std::min<int64_t>(units, 1024)), unsigned(a.nsplit)), dim3(256),
-                          0, s, a);
-            if ((st = checked("backward reduce"))) return st;
-        }
-    }
-    if (a.dx) {
-        const int tx = (a.d_in + 64 * kDxWaves - 1) / (64 * kDxWaves);
-        const int64_t nwg = int64_t(a.nchunk) * tx;
-        if (nwg > (int64_t(1) << 31) - 1) return fail(LORA_ERR_ARG, "backward: too many dx tiles");
-        const dim3 grid{unsigned(nwg)}, block(kDxWaves * 64);
-        const bool vx = vec && b.vec_dx;
-        if (bf16 && vx) launch_kernel(bwd_dx_kernel<LORA_BF16, true, false>, grid, block, 0, s, a, tx);
-        else if (bf16) launch_kernel(bwd_dx_kernel<LORA_BF16, false, false>, grid, block, 0, s, a, tx);
-        else if (vx) launch_kernel(bwd_dx_kernel<LORA_F32, true, false>, grid, block, 0, s, a, tx);
-        else launch_kernel(bwd_dx_kernel<LORA_F32, false, false>, grid, block, 0, s, a, tx);
-        if ((st = checked("backward dx"))) return st;
+    if (st || ngrad + ndx == 0) return st;
+    const dim3 grid{unsigned(ngrad + ndx)};
+    if (bf16 && vec) run_out<LORA_BF16, true>(s, a, grid);
+    else if (bf16) run_out<LORA_BF16, false>(s, a, grid);
+    else if (vec) run_out<LORA_F32, true>(s, a, grid);
+    else run_out<LORA_F32, false>(s, a, grid);
+    if ((st = checked("backward gradient"))) return st;
+    if (a.tiles && a.nsplit) {
+        const int64_t units = (l.part_stride / 4 + 255) / 256;
+        launch_kernel(bwd_reduce_kernel, dim3(unsigned(std::min<int64_t>(units, 1024)), unsigned(a.nsplit)), dim3(256), 0, s, a);
+        return checked("backward reduce");
     }
     return LORA_OK;
 }
@@ -1149,12 +1160,11 @@ int launch_dx_join(hipStream_t s, const BackwardArgs &b, const PlanView &p, void
     BwdArgs a = make_args(b, p, layout_of(h->num_sorted, b.d_in, b.d_out, h->max_rank), ws);
     a.joins = parts;
     a.splits = splits;
-    const int tx = (a.d_in + 64 * kDxWaves - 1) / (64 * kDxWaves);
-    const int64_t nwg = (int64_t(a.nblk) + (a.T - a.Tp + 15) / 16) * tx;
+    const int64_t nwg = (int64_t(a.nblk) + (a.T - a.Tp + 15) / 16) * a.tiles_x;
     if (nwg > (int64_t(1) << 31) - 1) return fail(LORA_ERR_ARG, "backward: too many dx tiles");
     const dim3 grid{unsigned(nwg)}, block(kDxWaves * 64);
-    if (b.vec_dx) launch_kernel(bwd_dx_kernel<LORA_BF16, true, true>, grid, block, 0, s, a, tx);
-    else launch_kernel(bwd_dx_kernel<LORA_BF16, false, true>, grid, block, 0, s, a, tx);
+    if (b.vec_dx) launch_kernel(bwd_join_kernel<true>, grid, block, 0, s, a);
+    else launch_kernel(bwd_join_kernel<false>, grid, block, 0, s, a);
     return checked("backward join");
 }
 
