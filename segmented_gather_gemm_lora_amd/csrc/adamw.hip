@@ -37,6 +37,7 @@ namespace {
 
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kBlock = LORA_ADAM_BLOCK; // elements of a state block: 4 per lane of a wave
 constexpr int kAdamThreads = 256;
@@ -114,16 +115,28 @@ template <class Q> __device__ __forceinline__ uint32_t encode(float a, int e, ui
     const uint32_t c = min(bits >> 20, Q::kMax);
     return __builtin_isfinite(a) ? c : Q::kNan;
 }
-template <class Q> __device__ __forceinline__ float decode(uint32_t mag, int e)
+// 4 codes of m: the hardware's E4M3 conversion, then the scale 2^(e - 127).
+__device__ __forceinline__ floatx4 decode_m(uint32_t w, int e)
 {
-    const float f = __builtin_ldexpf(__uint_as_float(mag << 20), e - Q::kBias);
-    return mag == Q::kNan ? __builtin_nanf("") : f;
+    typedef float floatx2 __attribute__((ext_vector_type(2)));
+    const floatx2 a = __builtin_amdgcn_cvt_pk_f32_fp8(int(w), false), b = __builtin_amdgcn_cvt_pk_f32_fp8(int(w), true);
+    const float scale = __uint_as_float(uint32_t(e) << 23);
+    return floatx4{a[0] * scale, a[1] * scale, b[0] * scale, b[1] * scale};
+}
+// A code of v: its bits in the fp32 exponent and mantissa, then the scale.
+__device__ __forceinline__ float decode_v(uint32_t c, int e)
+{
+    const float f = __builtin_ldexpf(__uint_as_float(c << 20), e - V8::kBias);
+    return c == V8::kNan ? __builtin_nanf("") : f;
 }
 
+// Everything of a step is touched once: fp32 accesses are non-temporal (128
+// adapters of rank 16, 503 MB: 96 us without, 80 us with).
+//
 // 4 consecutive elements from a 16-byte (fp32) or 8-byte (bf16) aligned place; past n: 0.
 __device__ __forceinline__ floatx4 get4(const float *p, int n)
 {
-    if (n >= 4) return *reinterpret_cast<const floatx4 *>(p);
+    if (n >= 4) return __builtin_nontemporal_load(reinterpret_cast<const floatx4 *>(p));
     floatx4 f{};
     for (int i = 0; i < n; ++i) f[i] = p[i];
     return f;
@@ -147,7 +160,7 @@ __device__ __forceinline__ uint32_t get4(const uint8_t *p, int n)
 }
 __device__ __forceinline__ void put4(float *p, floatx4 f, int n)
 {
-    if (n >= 4) *reinterpret_cast<floatx4 *>(p) = f;
+    if (n >= 4) __builtin_nontemporal_store(f, reinterpret_cast<floatx4 *>(p));
     else
         for (int i = 0; i < n; ++i) p[i] = f[i];
 }
@@ -205,21 +218,21 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(const AdamChunk *__
     if (h.step < 1 || !live) return; // a group that rests
     const float bc1 = one_minus_power(h.beta1, h.step), bc2 = one_minus_power(h.beta2, h.step);
     const float c1 = 1.0f - h.beta1, c2 = 1.0f - h.beta2;
+    const float ib1 = 1.0f / bc1, ib2 = 1.0f / bc2;
     if constexpr (BITS8) {
+        m = decode_m(mc, me);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t q = (mc >> (8 * i)) & 0xffu;
-            const float f = decode<M8>(q & 0x7fu, me);
-            m[i] = q & 0x80u ? -f : f;
-            v[i] = decode<V8>((vc >> (8 * i)) & 0xffu, ve);
-        }
+        for (int i = 0; i < 4; ++i) v[i] = decode_v((vc >> (8 * i)) & 0xffu, ve);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float gi = g[i] * h.grad_scale;
         m[i] = h.beta1 * m[i] + c1 * gi;
         v[i] = h.beta2 * v[i] + c2 * (gi * gi);
-        p[i] = p[i] - h.lr * (h.weight_decay * p[i] + (m[i] / bc1) / (__builtin_sqrtf(v[i] / bc2) + h.eps));
+        // root and quotient to 1 ulp each, of an update that is far below p: exact
+        // ones bound the 8-bit step by its arithmetic (478 us against 393 for 100 M
+        // elements)
+        p[i] = p[i] - h.lr * (h.weight_decay * p[i] + (m[i] * ib1) * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[i] * ib2) + h.eps));
     }
     if constexpr (BITS8) {
         uint32_t mm = 0, vm = 0;
@@ -262,35 +275,37 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(const AdamChunk *__
 }
 
 // The values of 8-bit states; both formats' values are bf16 values (4
-// significant bits times a power of two in bf16's range).
+// significant bits times a power of two in bf16's range).  16 elements a thread,
+// in accesses of 16 bytes where they are whole.
 __global__ __launch_bounds__(256) void adam_values_kernel(int64_t n, const uint8_t *__restrict__ m,
                                                           const uint8_t *__restrict__ ms, const uint8_t *__restrict__ v,
                                                           const uint8_t *__restrict__ vs, uint16_t *__restrict__ mo,
                                                           uint16_t *__restrict__ vo)
 {
-    const int64_t at = 4 * (int64_t(blockIdx.x) * 256 + threadIdx.x);
+    const int64_t at = 16 * (int64_t(blockIdx.x) * 256 + threadIdx.x);
     if (at >= n) return;
-    const int k = int(n - at < 4 ? n - at : 4);
-    if (m) {
-        const uint32_t w = get4(m + at, k);
-        const int e = ms[at / kBlock];
-        floatx4 f;
+    auto side = [&](const uint8_t *codes, const uint8_t *scales, uint16_t *out, auto values) {
+        const int e = scales[at / kBlock];
+        if (n - at >= 16) {
+            const u32x4 w = *reinterpret_cast<const u32x4 *>(codes + at);
+            u32x4 o[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t q = (w >> (8 * i)) & 0xffu;
-            const float a = decode<M8>(q & 0x7fu, e);
-            f[i] = q & 0x80u ? -a : a;
+            for (int q = 0; q < 4; ++q) {
+                const floatx4 f = values(w[q], e);
+                o[q >> 1][2 * (q & 1)] = f32_to_bf16(f[0]) | (f32_to_bf16(f[1]) << 16);
+                o[q >> 1][2 * (q & 1) + 1] = f32_to_bf16(f[2]) | (f32_to_bf16(f[3]) << 16);
+            }
+            *reinterpret_cast<u32x4 *>(out + at) = o[0];
+            *reinterpret_cast<u32x4 *>(out + at + 8) = o[1];
+        } else {
+            for (int64_t k = at; k < n; k += 4)
+                put4(out + k, values(get4(codes + k, int(n - k)), e), int(n - k));
         }
-        put4(mo + at, f, k);
-    }
-    if (v) {
-        const uint32_t w = get4(v + at, k);
-        const int e = vs[at / kBlock];
-        floatx4 f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = decode<V8>((w >> (8 * i)) & 0xffu, e);
-        put4(vo + at, f, k);
-    }
+    };
+    if (m) side(m, ms, mo, [](uint32_t w, int e) { return decode_m(w, e); });
+    if (v) side(v, vs, vo, [](uint32_t w, int e) {
+        return floatx4{decode_v(w & 0xffu, e), decode_v((w >> 8) & 0xffu, e), decode_v((w >> 16) & 0xffu, e), decode_v(w >> 24, e)};
+    });
 }
 
 // The plan's header; nullptr with the error set.
@@ -471,7 +486,7 @@ int lora_adam_state_values(void *stream, int64_t n, const void *m, const void *m
     if ((m && (!m_scale || !m_out)) || (v && (!v_scale || !v_out))) return fail(LORA_ERR_ARG, "a scale or output is NULL");
     if ((m && (!aligned16(m) || !aligned16(m_out))) || (v && (!aligned16(v) || !aligned16(v_out))))
         return fail(LORA_ERR_ALIGN, "codes or outputs are not 16-byte aligned");
-    const int64_t nwg = (n + 1023) / 1024;
+    const int64_t nwg = (n + 4095) / 4096;
     if (nwg > (int64_t(1) << 31) - 1) return fail(LORA_ERR_ARG, "n %lld is too large", (long long)n);
     launch_kernel(adam_values_kernel, dim3(unsigned(nwg)), dim3(256), 0, static_cast<hipStream_t>(stream), n,
                   static_cast<const uint8_t *>(m), static_cast<const uint8_t *>(m_scale), static_cast<const uint8_t *>(v),

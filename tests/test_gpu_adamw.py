@@ -138,6 +138,22 @@ def test_extreme_magnitudes(scale):
     c.check()
 
 
+@pytest.mark.parametrize("state", ["f32", "8bit"])
+def test_tiny_gradients_without_eps(state):
+    """eps = 0 and g g below fp32's normal range: the quotient m / sqrt(v) is still of order 1."""
+    r = np.random.default_rng(4)
+    h = dict(HYPER[0], eps=0.0, weight_decay=0.0)
+    g = ((np.sign(r.standard_normal(600)) * (1 + r.random(600))) * 2e-18).astype(np.float32)
+    p = torch.zeros(600, device="cuda")
+    o = B.AdamW([p], [torch.from_numpy(g).cuda()], [0], table_of([h]), state=state)
+    o.step()
+    torch.cuda.synchronize()
+    want, bound, _, v = R.step(np.zeros(600), g, np.zeros(600), np.zeros(600), h)
+    assert (v < 2.0**-126).sum() > 300 and (v > 2.0**-133).all()  # most of them subnormal
+    # v itself has as few as 2^-149 / v of relative accuracy here, on both sides alike
+    assert (np.abs(p.double().cpu().numpy() - want) <= bound).all()
+
+
 def test_rounding_has_no_bias():
     """The mean of many stochastic roundings of one value is the value: each is
     off by less than a code's gap, so the mean of N is off by at most
