@@ -41,13 +41,21 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kBlock = LORA_ADAM_BLOCK; // elements of a state block: 4 per lane of a wave
 constexpr int kAdamThreads = 256;
-constexpr int kChunk = 4 * kAdamThreads; // elements of a workgroup
+constexpr int kRow = 4 * kAdamThreads; // elements that a workgroup takes at a time
+// Elements of a chunk: two rows for many elements with 8-bit states, whose
+// arithmetic shows (the record, the group's numbers and its powers are read and
+// formed once for them: 100 M elements in 345 us, 407 with one row; four and
+// eight rows alike); one row where there are few (131072 elements: 3.5 us, 5.4
+// with four) and with fp32 states (16.8 M elements: 80 us, 88 with two).
+constexpr int64_t kFewElements = 1 << 22;
+int chunk_of(int64_t elements, bool eight) { return eight && elements > kFewElements ? 2 * kRow : kRow; }
+
 constexpr uint32_t kAdamMagic = 0x4C6F4164u;
 
 struct AdamChunk {
     uint64_t param, grad, copy, m, v, m_scale, v_scale; // at the chunk's first element
     uint32_t e0;     // index of the first element in its tensor
-    int32_t n;       // elements, 1 .. kChunk
+    int32_t n;       // elements
     int32_t group;
     uint32_t tensor; // the tensor's number
     uint64_t reserved;
@@ -188,89 +196,102 @@ __device__ __forceinline__ float one_minus_power(float b, int t)
     return float(1.0 - p);
 }
 
+// A lane's 4 elements of a row, as loaded.
+template <bool BITS8, class G> struct AdamRow {
+    floatx4 p, g, m, v;
+    uint32_t mc, vc;
+    int me, ve;
+    __device__ __forceinline__ void load(const AdamChunk &c, int at)
+    {
+        const int n = c.n - at, lat = n > 0 ? at : 0, ln = n > 0 ? n : 0; // past the end: nothing
+        p = get4(reinterpret_cast<const float *>(c.param) + lat, ln);
+        g = get4(reinterpret_cast<const G *>(c.grad) + lat, ln);
+        if constexpr (BITS8) {
+            mc = get4(reinterpret_cast<const uint8_t *>(c.m) + lat, ln);
+            vc = get4(reinterpret_cast<const uint8_t *>(c.v) + lat, ln);
+            const int b = at / kBlock * kBlock < c.n ? at / kBlock : 0; // state block (one per wave)
+            me = reinterpret_cast<const uint8_t *>(c.m_scale)[b];
+            ve = reinterpret_cast<const uint8_t *>(c.v_scale)[b];
+        } else {
+            m = get4(reinterpret_cast<const float *>(c.m) + lat, ln);
+            v = get4(reinterpret_cast<const float *>(c.v) + lat, ln);
+        }
+    }
+};
+
 template <bool BITS8, class G>
 __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(const AdamChunk *__restrict__ chunks,
                                                              const lora_adam_hyper *__restrict__ hyper)
 {
 #pragma clang fp contract(off)
     const AdamChunk &c = chunks[blockIdx.x];
-    const int at = 4 * int(threadIdx.x); // this lane's first element in the chunk
-    const int n = c.n - at;              // elements from there, may be <= 0
-    const bool any = n > 0;
-    const int lat = any ? at : 0, ln = any ? n : 0;
-    floatx4 p = get4(reinterpret_cast<const float *>(c.param) + lat, ln);
-    floatx4 g = get4(reinterpret_cast<const G *>(c.grad) + lat, ln);
-    floatx4 m, v;
-    uint32_t mc = 0, vc = 0;
-    const int b = at / kBlock;            // state block (one per wave)
-    const bool live = b * kBlock < c.n;   // wave-uniform
-    int me = 0, ve = 0;
-    if constexpr (BITS8) {
-        mc = get4(reinterpret_cast<const uint8_t *>(c.m) + lat, ln);
-        vc = get4(reinterpret_cast<const uint8_t *>(c.v) + lat, ln);
-        me = reinterpret_cast<const uint8_t *>(c.m_scale)[live ? b : 0];
-        ve = reinterpret_cast<const uint8_t *>(c.v_scale)[live ? b : 0];
-    } else {
-        m = get4(reinterpret_cast<const float *>(c.m) + lat, ln);
-        v = get4(reinterpret_cast<const float *>(c.v) + lat, ln);
-    }
+    int at = 4 * int(threadIdx.x); // this lane's first element of the row, in the chunk
+    AdamRow<BITS8, G> row;
+    row.load(c, at);
     const lora_adam_hyper h = hyper[c.group];
-    if (h.step < 1 || !live) return; // a group that rests
+    if (h.step < 1) return; // a group that rests
     const float bc1 = one_minus_power(h.beta1, h.step), bc2 = one_minus_power(h.beta2, h.step);
     const float c1 = 1.0f - h.beta1, c2 = 1.0f - h.beta2;
     const float ib1 = 1.0f / bc1, ib2 = 1.0f / bc2;
-    if constexpr (BITS8) {
-        m = decode_m(mc, me);
+    const uint32_t key = mix(mix(h.seed + uint32_t(h.step) * 0x9E3779B9u) + c.tensor * 0x510E527Fu);
+    while (at / kBlock * kBlock < c.n) { // wave-uniform
+        floatx4 p = row.p, g = row.g, m = row.m, v = row.v;
+        if constexpr (BITS8) {
+            m = decode_m(row.mc, row.me);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = decode_v((vc >> (8 * i)) & 0xffu, ve);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float gi = g[i] * h.grad_scale;
-        m[i] = h.beta1 * m[i] + c1 * gi;
-        v[i] = h.beta2 * v[i] + c2 * (gi * gi);
-        // root and quotient to 1 ulp each, of an update that is far below p: exact
-        // ones bound the 8-bit step by its arithmetic (478 us against 393 for 100 M
-        // elements)
-        p[i] = p[i] - h.lr * (h.weight_decay * p[i] + (m[i] * ib1) * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[i] * ib2) + h.eps));
-    }
-    if constexpr (BITS8) {
-        uint32_t mm = 0, vm = 0;
+            for (int i = 0; i < 4; ++i) v[i] = decode_v((row.vc >> (8 * i)) & 0xffu, row.ve);
+        }
+        const int here = at;
+        at += kRow;
+        if (at / kBlock * kBlock < c.n) row.load(c, at); // the next row's, while this one is computed
+        const int n = c.n - here, b = here / kBlock; // elements from here, may be <= 0; state block
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t ma = __float_as_uint(m[i]) & 0x7fffffffu, va = __float_as_uint(v[i]) & 0x7fffffffu;
-            if (i < n) {
-                mm = max(mm, ma < 0x7f800000u ? ma : 0u);
-                vm = max(vm, va < 0x7f800000u ? va : 0u);
+            const float gi = g[i] * h.grad_scale;
+            m[i] = h.beta1 * m[i] + c1 * gi;
+            v[i] = h.beta2 * v[i] + c2 * (gi * gi);
+            // root and quotient to 1 ulp each, of an update that is far below p: exact
+            // ones bound the 8-bit step by its arithmetic (478 us against 393 for 100 M
+            // elements)
+            p[i] = p[i] - h.lr * (h.weight_decay * p[i] + (m[i] * ib1) * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[i] * ib2) + h.eps));
+        }
+        uint32_t mc = 0, vc = 0;
+        if constexpr (BITS8) {
+            uint32_t mm = 0, vm = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t ma = __float_as_uint(m[i]) & 0x7fffffffu, va = __float_as_uint(v[i]) & 0x7fffffffu;
+                if (i < n) {
+                    mm = max(mm, ma < 0x7f800000u ? ma : 0u);
+                    vm = max(vm, va < 0x7f800000u ? va : 0u);
+                }
+            }
+            const int me = scale_of<M8>(wave_max(mm)), ve = scale_of<V8>(wave_max(vm));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t rnd = mix((c.e0 + uint32_t(here + i)) * 0x9E3779B9u + key);
+                const uint32_t qm = encode<M8>(m[i], me, rnd & 0xffffu) | (m[i] < 0.f ? 0x80u : 0u);
+                uint32_t qv = encode<V8>(v[i], ve, rnd >> 16);
+                if (v[i] > 0.f && qv == 0) qv = 1;
+                mc |= qm << (8 * i);
+                vc |= qv << (8 * i);
+            }
+            if ((threadIdx.x & 63) == 0) {
+                reinterpret_cast<uint8_t *>(c.m_scale)[b] = uint8_t(me);
+                reinterpret_cast<uint8_t *>(c.v_scale)[b] = uint8_t(ve);
             }
         }
-        me = scale_of<M8>(wave_max(mm));
-        ve = scale_of<V8>(wave_max(vm));
-        const uint32_t key = mix(mix(h.seed + uint32_t(h.step) * 0x9E3779B9u) + c.tensor * 0x510E527Fu);
-        mc = vc = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t rnd = mix((c.e0 + uint32_t(at + i)) * 0x9E3779B9u + key);
-            const uint32_t qm = encode<M8>(m[i], me, rnd & 0xffffu) | (m[i] < 0.f ? 0x80u : 0u);
-            uint32_t qv = encode<V8>(v[i], ve, rnd >> 16);
-            if (v[i] > 0.f && qv == 0) qv = 1;
-            mc |= qm << (8 * i);
-            vc |= qv << (8 * i);
+        if (n > 0) {
+            put4(reinterpret_cast<float *>(c.param) + here, p, n);
+            if (c.copy) put4(reinterpret_cast<uint16_t *>(c.copy) + here, p, n);
+            if constexpr (BITS8) {
+                put4(reinterpret_cast<uint8_t *>(c.m) + here, mc, n);
+                put4(reinterpret_cast<uint8_t *>(c.v) + here, vc, n);
+            } else {
+                put4(reinterpret_cast<float *>(c.m) + here, m, n);
+                put4(reinterpret_cast<float *>(c.v) + here, v, n);
+            }
         }
-        if ((threadIdx.x & 63) == 0) {
-            reinterpret_cast<uint8_t *>(c.m_scale)[b] = uint8_t(me);
-            reinterpret_cast<uint8_t *>(c.v_scale)[b] = uint8_t(ve);
-        }
-    }
-    if (!any) return;
-    put4(reinterpret_cast<float *>(c.param) + at, p, n);
-    if (c.copy) put4(reinterpret_cast<uint16_t *>(c.copy) + at, p, n);
-    if constexpr (BITS8) {
-        put4(reinterpret_cast<uint8_t *>(c.m) + at, mc, n);
-        put4(reinterpret_cast<uint8_t *>(c.v) + at, vc, n);
-    } else {
-        put4(reinterpret_cast<float *>(c.m) + at, m, n);
-        put4(reinterpret_cast<float *>(c.v) + at, v, n);
     }
 }
 
@@ -339,10 +360,16 @@ bool sizes_ok(const lora_adam_tensor *t, int32_t n)
     return true;
 }
 
-int64_t chunks_of(const lora_adam_tensor *t, int32_t n)
+int64_t elements_of(const lora_adam_tensor *t, int32_t n)
+{
+    int64_t e = 0;
+    for (int32_t i = 0; i < n; ++i) e += t[i].n;
+    return e;
+}
+int64_t chunks_of(const lora_adam_tensor *t, int32_t n, int chunk)
 {
     int64_t c = 0;
-    for (int32_t i = 0; i < n; ++i) c += (t[i].n + kChunk - 1) / kChunk;
+    for (int32_t i = 0; i < n; ++i) c += (t[i].n + chunk - 1) / chunk;
     return c;
 }
 
@@ -355,8 +382,9 @@ extern "C" {
 
 size_t lora_adamw_plan_bytes(const lora_adam_tensor *tensors, int32_t n_tensors)
 {
+    // the larger of both states' plans: chunks of one row
     if (!sizes_ok(tensors, n_tensors)) return 0;
-    return sizeof(AdamHeader) + sizeof(AdamChunk) * size_t(chunks_of(tensors, n_tensors));
+    return sizeof(AdamHeader) + sizeof(AdamChunk) * size_t(chunks_of(tensors, n_tensors, kRow));
 }
 
 int lora_adamw_plan(const lora_adam_tensor *tensors, int32_t n_tensors, int32_t n_groups, int state, int grad_dtype,
@@ -409,14 +437,16 @@ int lora_adamw_plan(const lora_adam_tensor *tensors, int32_t n_tensors, int32_t 
         if (ranges[k].lo < ranges[k - 1].hi)
             return fail(LORA_ERR_ARG, "tensors %d and %d share memory that is written",
                         std::min(ranges[k].tensor, ranges[k - 1].tensor), std::max(ranges[k].tensor, ranges[k - 1].tensor));
-    const size_t need = lora_adamw_plan_bytes(tensors, n_tensors);
+    const int chunk = chunk_of(elements_of(tensors, n_tensors), eight);
+    const int64_t n_chunks = chunks_of(tensors, n_tensors, chunk);
+    const size_t need = sizeof(AdamHeader) + sizeof(AdamChunk) * size_t(n_chunks);
     if (plan_bytes < need) return fail(LORA_ERR_WORKSPACE, "plan buffer of %zu B < %zu B needed", plan_bytes, need);
     auto *h = static_cast<AdamHeader *>(plan_host);
     auto *ch = reinterpret_cast<AdamChunk *>(h + 1);
     for (int32_t i = 0; i < n_tensors; ++i) {
         const lora_adam_tensor &t = tensors[i];
         const uint64_t gs = grad_dtype == LORA_BF16 ? 2 : 4, es = eight ? 1 : 4;
-        for (int64_t e = 0; e < t.n; e += kChunk, ++ch) {
+        for (int64_t e = 0; e < t.n; e += chunk, ++ch) {
             std::memset(ch, 0, sizeof *ch);
             ch->param = t.param + 4 * uint64_t(e);
             ch->grad = t.grad + gs * uint64_t(e);
@@ -426,7 +456,7 @@ int lora_adamw_plan(const lora_adam_tensor *tensors, int32_t n_tensors, int32_t 
             ch->m_scale = eight ? t.m_scale + uint64_t(e) / kBlock : 0;
             ch->v_scale = eight ? t.v_scale + uint64_t(e) / kBlock : 0;
             ch->e0 = uint32_t(e);
-            ch->n = int32_t(std::min<int64_t>(kChunk, t.n - e));
+            ch->n = int32_t(std::min<int64_t>(chunk, t.n - e));
             ch->group = t.group;
             ch->tensor = uint32_t(i);
         }
@@ -434,7 +464,7 @@ int lora_adamw_plan(const lora_adam_tensor *tensors, int32_t n_tensors, int32_t 
     h->state = state;
     h->grad_dtype = grad_dtype;
     h->n_groups = n_groups;
-    h->n_chunks = chunks_of(tensors, n_tensors);
+    h->n_chunks = n_chunks;
     h->bytes = need;
     h->magic = kAdamMagic;
     return LORA_OK;

@@ -112,6 +112,16 @@ def test_against_numpy(state, gdt, copy):
     c.check()
 
 
+def test_many_elements():
+    """Above 2^22 elements 8-bit chunks hold two rows of 1024: sizes around both."""
+    sizes = [1, 1023, 1025, 2047, 2048, 2049, 3000, 1 << 20, (1 << 20) + 1, 300, (1 << 21) + 77, 5]
+    assert sum(sizes) > 1 << 22
+    c = Case(sizes, "8bit")
+    c.opt.step()
+    torch.cuda.synchronize()
+    c.check()
+
+
 def test_zero_state_and_zero_gradient():
     """From nothing: zeroed states, gradients that are zero in places."""
     for state in ("f32", "8bit"):
