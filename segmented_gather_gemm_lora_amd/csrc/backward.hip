@@ -21,13 +21,20 @@
 //  3. bwd_reduce_kernel: adds those partial sums in span order (a fixed order:
 //     the gradients do not change from run to run).
 //
+// Access shape.  A vector load or store costs the L1 one access per run of lanes
+// with consecutive addresses, so every large access has 8 or more adjacent lanes on one row's
+// consecutive 16 bytes (operands loaded straight into MFMA's lane order, 16 rows
+// x 4 pieces that are 16 lanes apart, cost 51 accesses per load: the shrink
+// of 4096 rows took 27 us so, XX as it is).  Rows go to a wave's own LDS tile and are
+// read back in MFMA's order; u and v are stored in that order by launch 1; results
+// leave with consecutive columns in consecutive lanes.
+//
 // The transposed operands.  MFMA wants, in each lane, consecutive elements of
 // the summed axis.  x, dy (summed over rows for dA, dB), A (summed over its
 // rows for dx) and B (summed over its rows for u) are contiguous along the
-// other axis.  Rows are loaded with 16 bytes per lane into a wave's own LDS
-// tile and read back with ds_read_b64_tr_b16, which hands lane i of every 16
-// lanes column i of 4 rows.  fp32 operands go to v_mfma_f32_16x16x4_f32, which
-// takes one element per lane: they are loaded where they are needed.
+// other axis: their LDS tiles are read with ds_read_b64_tr_b16, which hands lane i
+// of every 16 lanes column i of 4 rows.  fp32 operands go to
+// v_mfma_f32_16x16x4_f32, which takes one element per lane.
 //
 // Precision.  u and v are fp32 sums.  For dA and dB they are fed to bf16 MFMA
 // as three bf16 parts (hi + mid + lo, 24 significant bits: all of an fp32), so the
@@ -87,6 +94,7 @@ template <class T> __device__ __forceinline__ u32x4 load16_any(gptr<T> p) { retu
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 constexpr int kWin = 32; // sorted positions of one step over rows; u and v are stored in windows of it
+constexpr int kPieces = 64 * 16; // bytes of one operand: 16 per lane
 
 template <int DT> struct Elem;
 template <> struct Elem<LORA_BF16> {
@@ -94,16 +102,14 @@ template <> struct Elem<LORA_BF16> {
     using F = bf16x8;              // operand of one MFMA step
     static constexpr int kVec = 8; // elements of the summed axis per lane
     static constexpr int kStep = 32;
-    static constexpr int kParts = 3;  // u and v for dA, dB
-    static constexpr int kPart = 2;   // bytes of a part's element
+    static constexpr int kParts = 3; // operands of a window and 16 ranks: hi, mid, lo of 32 positions
 };
 template <> struct Elem<LORA_F32> {
     using T = float;
     using F = floatx4;
     static constexpr int kVec = 4;
     static constexpr int kStep = 16;
-    static constexpr int kParts = 1;
-    static constexpr int kPart = 4;
+    static constexpr int kParts = 2; // 16 positions each
 };
 
 template <int DT>
@@ -147,9 +153,11 @@ struct BwdArgs {
     const lora_chunk_desc *chunk;
     const int32_t *perm;
     int S, nblk, nchunk;
-    int r16;        // largest rank, rounded up to 16
-    char *ut, *vt;  // u and v in windows: [window][part][rank][32 positions]
-    char *ur;       // u in rows: bf16 [position][16 ranks hi, 16 ranks lo ...], fp32 [position][ranks]
+    int nt;         // 16-rank tiles of the largest rank
+    // u and v as MFMA operands (16 bytes a lane, lane = 16 g + m):
+    char *ut, *vt;  // [window][part][tile]: rank m of the tile, bf16 positions 8 g .. + 7 (fp32 4 g .. + 3)
+    char *ur;       // [16 positions][tile]: position m, bf16 ranks 8 (g % 2) .. + 7 of the hi (g < 2) or lo
+                    // part, fp32 ranks 4 g .. + 3
     Item *items;
     Split *segsplits;
     float *part;
@@ -169,12 +177,12 @@ struct BwdArgs {
 };
 
 // ----------------------------------------------------------------------------
-// Launch 1.  One workgroup: 16 rows, all ranks, one side.
+// Launch 1.  One workgroup: 16 MB rows, all ranks, one side.
 // Side 0: v, K = d_in, W = A (row j is rank j, contiguous along K).
 // Side 1: u, K = d_out, W = B (row k holds the ranks).
 // ----------------------------------------------------------------------------
 // Elements k .. of a row, 0 past K, one by one.
-template <int DT> __device__ __forceinline__ typename Elem<DT>::F load_row(gptr<typename Elem<DT>::T> row, int k, int K)
+template <int DT> __device__ __forceinline__ u32x4 load_row(gptr<typename Elem<DT>::T> row, int k, int K)
 {
     using E = Elem<DT>;
     typename E::F f;
@@ -184,23 +192,7 @@ template <int DT> __device__ __forceinline__ typename Elem<DT>::F load_row(gptr<
         if constexpr (DT == LORA_BF16) f[e] = __builtin_bit_cast(__bf16, uint16_t(k + e < K ? w : 0));
         else f[e] = k + e < K ? w : 0.f;
     }
-    return f;
-}
-
-// Column j of rows k .. k + kVec - 1 of B (row pitch r), element by element.
-template <int DT>
-__device__ __forceinline__ typename Elem<DT>::F load_col(gptr<typename Elem<DT>::T> B, int r, int j, int k, int K)
-{
-    using E = Elem<DT>;
-    typename E::F f;
-    const int jj = j < r ? j : r - 1; // past r: a column that nothing reads
-#pragma unroll
-    for (int e = 0; e < E::kVec; ++e) {
-        const typename E::T w = B[int64_t(k + e < K ? k + e : K - 1) * r + jj];
-        if constexpr (DT == LORA_BF16) f[e] = __builtin_bit_cast(__bf16, uint16_t(k + e < K ? w : 0));
-        else f[e] = k + e < K ? w : 0.f;
-    }
-    return f;
+    return __builtin_bit_cast(u32x4, f);
 }
 
 // Work items: the segments cut at multiples of `span`.  One workgroup.
@@ -248,12 +240,20 @@ __device__ void list_items(const BwdArgs &a, int *scan, int nthreads)
 }
 
 constexpr int kShrinkWaves = 8;
+#define LORA_NP (RT * MB == 1 ? 2 : 1)
 
-// The operands of NS steps of a wave: MB blocks of 16 rows of x (dy), RT rank
-// tiles of A (B).
-template <int DT, int RT, int MB, int NS> struct ShrinkOps {
-    typename Elem<DT>::F xf[NS][MB];
-    typename Elem<DT>::F wf[NS][RT];
+// A wave advances 128 bytes of every row at a time (a pair of steps: 64 elements in
+// bf16, 32 in fp32).  Rows of x (dy) and of A are loaded as 8 rows x 128 bytes per
+// instruction, B as pieces of 16 bytes in the order of its rows, and kept in the
+// wave's LDS tile: rows of 128 bytes with unit (16 bytes) un of row q in slot
+// un ^ (q % 8), B as below.
+template <int DT, int RT, int MB> struct ShrinkTile {
+    static constexpr int kPair = 2 * Elem<DT>::kStep;     // elements of the long axis
+    static constexpr int kX = MB * 2048;                  // bytes: x rows
+    static constexpr int kRowB = DT == LORA_BF16 ? 32 * RT : 64 * RT + 16; // bytes of a row of B's tile
+    static constexpr int kB = kPair * kRowB;
+    static constexpr int kW = kB > RT * 2048 ? kB : RT * 2048;
+    static constexpr int kBytes = kX + kW;
 };
 
 // One side's operands of a workgroup: rows of x or dy, and A or B.
@@ -265,186 +265,184 @@ struct ShrinkSide {
     int n;
 };
 
-// How W is loaded: by elements, by 16 bytes at any alignment, by 16 aligned bytes.
-enum { kByElem = 0, kByAny = 1, kByVec = 2 };
-
-// A lane's rows: byte offsets of its first element of every row (VEC; all below
-// 4 GiB) or the rows' tokens, and the byte offset of its part of A or B.
-template <int RT, int MB> struct ShrinkOffs {
-    uint32_t x[MB], w[RT];
+// A pair's loads, in registers.
+template <int DT, int RT, int MB> struct ShrinkOps {
+    static constexpr int kWs = RT * 2; // loads of W (B: 64 rows of 2 RT pieces, fp32 32 rows of 4 RT)
+    u32x4 x[MB][2], w[kWs];
 };
 
-template <int DT, bool VEC, int SIDE, int RT, int MB>
-__device__ __forceinline__ ShrinkOffs<RT, MB> shrink_offs(const ShrinkSide &sd, int lane)
+// B's place in the tile.  bf16: 32-byte granules (one rank tile of a row), moved so
+// that the 4 rows of a transposing read fall in distinct banks; fp32: padded rows.
+template <int DT, int RT> __device__ __forceinline__ int b_at(int k, int byte)
 {
-    constexpr int es = int(sizeof(typename Elem<DT>::T));
-    const int m = lane & 15, g = lane >> 4;
-    ShrinkOffs<RT, MB> o;
-#pragma unroll
-    for (int b = 0; b < MB; ++b) { // rows past n: never stored
-        const uint32_t t = uint32_t(sd.rows[min(16 * b + m, sd.n - 1)]);
-        o.x[b] = VEC ? t * uint32_t(sd.ld * es) + 16 * g : t;
-    }
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-        if constexpr (SIDE == 1) { // 32 rows x 2 RT pieces of 16 bytes a step, RT pieces a lane
-            const int q = lane + 64 * i, j = 16 * sd.rt0 + 8 * (q % (2 * RT));
-            o.w[i] = uint32_t((q / (2 * RT)) * sd.r + (j < sd.r ? j : 0)) * es;
-        } else {
-            const int j = 16 * (sd.rt0 + i) + m;
-            o.w[i] = uint32_t(j < sd.r ? j : sd.r - 1) * uint32_t(sd.K * es) + 16 * g;
-        }
-    }
-    return o;
+    if constexpr (DT == LORA_BF16)
+        return k * 32 * RT + (((byte >> 5) ^ ((RT == 4 ? k >> 1 : k >> 2) & (RT - 1))) << 5) + (byte & 31);
+    else return k * (64 * RT + 16) + byte;
 }
 
-// The operands of steps k .. (k wave-uniform).  Rows of x (dy) and of A by 16
-// bytes, B (WLOAD kByAny, kByVec) by pieces of 8 ranks; FULL: every element loaded
-// lies inside.  Else element by element (VEC rows: clamped to the row).
-template <int DT, bool VEC, int SIDE, int WLOAD, bool FULL, int RT, int MB, int NS>
-__device__ __forceinline__ void shrink_load(ShrinkOps<DT, RT, MB, NS> &o, const ShrinkSide &sd,
-                                            const ShrinkOffs<RT, MB> &off, int k, int lane)
+// FULL: everything that is loaded lies inside.  VEC: rows are whole aligned 16-byte
+// pieces below 4 GiB (xoff: byte offsets); else at any alignment (xoff: tokens).
+// BANY: B's rows are not whole 16-byte pieces.
+template <int DT, bool VEC, int SIDE, bool BANY, bool FULL, int RT, int MB>
+__device__ __forceinline__ void shrink_load(ShrinkOps<DT, RT, MB> &o, const ShrinkSide &sd, const uint32_t (&xoff)[MB][2],
+                                            int k, int lane)
 {
     using E = Elem<DT>;
     using T = typename E::T;
-    using F = typename E::F;
-    const int m = lane & 15, g = lane >> 4;
+    constexpr int es = int(sizeof(T));
+    const int kl = k + E::kVec * (lane & 7); // this lane's first element of a row
+    const char *xb = static_cast<const char *>(sd.src) + int64_t(k) * es;
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-        const int ks = k + s * E::kStep;
-        // VEC, past K: the row's first unit, replaced by zero
-        const int kc = FULL || ks < sd.K ? ks : 0;
-        const bool in = FULL || ks + E::kVec * g < sd.K;
-        const uint32_t back = in ? 0 : uint32_t(16 * g);
-        const char *xb = static_cast<const char *>(sd.src) + int64_t(kc) * int(sizeof(T));
-        const char *ab = static_cast<const char *>(sd.mat) + int64_t(kc) * int(sizeof(T));
+    for (int b = 0; b < MB; ++b)
 #pragma unroll
-        for (int b = 0; b < MB; ++b) {
-            if constexpr (VEC) {
-                u32x4 w = load16(xb, off.x[b] - back);
-                if (!in) w = u32x4{};
-                o.xf[s][b] = __builtin_bit_cast(F, w);
+        for (int h = 0; h < 2; ++h) {
+            if constexpr (FULL && VEC) {
+                o.x[b][h] = load16(xb, xoff[b][h]);
             } else {
-                const gptr<T> row = as_global<T>(sd.src) + int64_t(off.x[b]) * sd.ld;
-                if constexpr (FULL) o.xf[s][b] = __builtin_bit_cast(F, load16_any(row + (ks + E::kVec * g)));
-                else o.xf[s][b] = load_row<DT>(row, ks + E::kVec * g, sd.K);
+                const gptr<T> row = VEC ? (gptr<T>)(as_global<char>(sd.src) + xoff[b][h]) - E::kVec * (lane & 7)
+                                        : as_global<T>(sd.src) + int64_t(xoff[b][h]) * sd.ld;
+                if constexpr (FULL) o.x[b][h] = load16_any(row + kl);
+                else o.x[b][h] = load_row<DT>(row, kl, sd.K);
             }
         }
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            if constexpr (SIDE == 0 && VEC) {
-                u32x4 w = load16(ab, off.w[i] - back);
-                if (!in) w = u32x4{};
-                o.wf[s][i] = __builtin_bit_cast(F, w);
-            } else if constexpr (SIDE == 0) {
-                const int j = 16 * (sd.rt0 + i) + m;
-                const gptr<T> row = as_global<T>(sd.mat) + int64_t(j < sd.r ? j : sd.r - 1) * sd.K;
-                if constexpr (FULL) o.wf[s][i] = __builtin_bit_cast(F, load16_any(as_global<char>(ab) + off.w[i]));
-                else o.wf[s][i] = load_row<DT>(row, ks + E::kVec * g, sd.K);
-            } else if constexpr (WLOAD != kByElem) {
-                static_assert(FULL || WLOAD == kByElem, "pieces of whole chunks");
-                const char *bb = static_cast<const char *>(sd.mat) + int64_t(ks) * sd.r * 2;
-                if constexpr (WLOAD == kByVec) o.wf[s][i] = __builtin_bit_cast(F, load16(bb, off.w[i]));
-                else o.wf[s][i] = __builtin_bit_cast(F, load16_any(as_global<char>(bb) + off.w[i]));
-            } else {
-                o.wf[s][i] = load_col<DT>(as_global<T>(sd.mat), sd.r, 16 * (sd.rt0 + i) + m, ks + E::kVec * g, sd.K);
+    for (int i = 0; i < o.kWs; ++i) {
+        if constexpr (SIDE == 0) { // rank rows 16 (i / 2) + 8 (i % 2) + lane / 8
+            const int j = 16 * sd.rt0 + 8 * i + (lane >> 3);
+            const gptr<T> row = as_global<T>(sd.mat) + int64_t(j < sd.r ? j : sd.r - 1) * sd.K;
+            if constexpr (FULL && VEC)
+                o.w[i] = load16(static_cast<const char *>(sd.mat) + int64_t(k) * es,
+                                uint32_t(j < sd.r ? j : sd.r - 1) * uint32_t(sd.K * es) + 16 * (lane & 7));
+            else if constexpr (FULL) o.w[i] = load16_any(row + kl);
+            else o.w[i] = load_row<DT>(row, kl, sd.K);
+        } else { // piece lane + 64 i of the pair's rows of B
+            constexpr int kPer = 16 * RT / E::kVec; // pieces of a row
+            const int q = lane + 64 * i, kr = k + q / kPer, j = 16 * sd.rt0 + E::kVec * (q % kPer);
+            const int jj = j < sd.r ? j : 0; // past r: columns that nothing reads
+            const gptr<T> B = as_global<T>(sd.mat);
+            if constexpr (FULL && !BANY)
+                o.w[i] = load16(static_cast<const char *>(sd.mat) + int64_t(k) * sd.r * es, uint32_t((q / kPer) * sd.r + jj) * es);
+            else if constexpr (FULL) o.w[i] = load16_any(B + (int64_t(kr) * sd.r + jj));
+            else {
+                o.w[i] = load_row<DT>(B + int64_t(kr < sd.K ? kr : sd.K - 1) * sd.r, jj, sd.r);
+                if (kr >= sd.K) o.w[i] = u32x4{};
             }
         }
     }
 }
 
-// PIECES: W is B by pieces, to be turned through the wave's LDS tile.
-template <int DT, bool PIECES, int RT, int MB, int NS>
-__device__ __forceinline__ void shrink_mma(const ShrinkOps<DT, RT, MB, NS> &o, floatx4 (&acc)[MB][RT], char *tiles,
-                                           int lane)
+template <int DT, int SIDE, int RT, int MB>
+__device__ __forceinline__ void shrink_put(const ShrinkOps<DT, RT, MB> &o, char *tile, int lane)
 {
-    using F = typename Elem<DT>::F;
+    constexpr int kX = ShrinkTile<DT, RT, MB>::kX;
+    const int q0 = lane >> 3;
+    const int at = q0 * 128 + (((lane & 7) ^ q0) << 4); // rows 8 on: 1024 bytes on, the same slot
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) *reinterpret_cast<u32x4 *>(tile + (2 * b + h) * 1024 + at) = o.x[b][h];
+#pragma unroll
+    for (int i = 0; i < o.kWs; ++i) {
+        if constexpr (SIDE == 0) {
+            *reinterpret_cast<u32x4 *>(tile + kX + i * 1024 + at) = o.w[i];
+        } else {
+            constexpr int kPer = 16 * RT / Elem<DT>::kVec;
+            const int q = lane + 64 * i;
+            *reinterpret_cast<u32x4 *>(tile + kX + b_at<DT, RT>(q / kPer, 16 * (q % kPer))) = o.w[i];
+        }
+    }
+}
+
+template <int DT, int SIDE, int RT, int MB>
+__device__ __forceinline__ void shrink_mma(floatx4 (&acc)[MB][RT], const char *tile, int lane)
+{
+    using E = Elem<DT>;
+    using F = typename E::F;
+    constexpr int kX = ShrinkTile<DT, RT, MB>::kX;
     const int m = lane & 15, g = lane >> 4;
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-        F wf[RT];
-        if constexpr (PIECES) {
-            // 32-byte granules (one rank tile of a row), moved so that 4 rows of a
-            // tile fall in distinct banks
-            char *tile = tiles + (s & 1) * 1024 * RT;
-            auto gran = [](int kr, int t) { return kr * 32 * RT + (t ^ ((RT == 4 ? kr >> 1 : kr >> 2) & (RT - 1))) * 32; };
+    for (int s = 0; s < 2; ++s) {
+        auto row_frag = [&](const char *rows) { // row m, unit 4 s + g
+            return __builtin_bit_cast(F, *reinterpret_cast<const u32x4 *>(rows + m * 128 + (((4 * s + g) ^ (m & 7)) << 4)));
+        };
+        F xf[MB], wf[RT];
 #pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                const int q = lane + 64 * i, kr = q / (2 * RT), pc = q % (2 * RT);
-                *reinterpret_cast<u32x4 *>(tile + gran(kr, pc >> 1) + (pc & 1) * 16) = __builtin_bit_cast(u32x4, o.wf[s][i]);
+        for (int b = 0; b < MB; ++b) xf[b] = row_frag(tile + b * 2048);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            if constexpr (SIDE == 0) {
+                wf[i] = row_frag(tile + kX + i * 2048);
+            } else if constexpr (DT == LORA_BF16) {
+                u32x2 t[2];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) t[b] = read_tr(tile + kX + b_at<DT, RT>(32 * s + 8 * g + 4 * b + (m >> 2), 32 * i + 8 * (m & 3)));
+                wf[i] = join8(t[0], t[1]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    wf[i][e] = *reinterpret_cast<const float *>(tile + kX + b_at<DT, RT>(16 * s + 4 * g + e, 4 * (16 * i + m)));
             }
-#pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                u32x2 h[2];
-#pragma unroll
-                for (int b = 0; b < 2; ++b) h[b] = read_tr(tile + gran(8 * g + 4 * b + (m >> 2), i) + (m & 3) * 8);
-                wf[i] = __builtin_bit_cast(F, u32x4{h[0][0], h[0][1], h[1][0], h[1][1]});
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < RT; ++i) wf[i] = o.wf[s][i];
         }
 #pragma unroll
         for (int b = 0; b < MB; ++b)
 #pragma unroll
-            for (int i = 0; i < RT; ++i) acc[b][i] = mma<DT>(o.xf[s][b], wf[i], acc[b][i]);
+            for (int i = 0; i < RT; ++i) acc[b][i] = mma<DT>(xf[b], wf[i], acc[b][i]);
     }
 }
 
-// This wave's part of the sums: chunks of NS steps, the loads of the next chunk
-// issued before the products of the current one (PIPE).
-template <int DT, bool VEC, int SIDE, int WLOAD, bool PIPE, int RT, int MB, int NS>
-__device__ __forceinline__ void shrink_sum(floatx4 (&acc)[MB][RT], const ShrinkSide &sd, char *tiles, int wave, int lane)
+// This wave's part of the sums: NP pairs at a time, the next ones' loads in flight
+// while the current ones are multiplied.
+template <int DT, bool VEC, int SIDE, bool BANY, int RT, int MB, int NP>
+__device__ __forceinline__ void shrink_sum(floatx4 (&acc)[MB][RT], const ShrinkSide &sd, char *tile, int wave, int lane)
 {
-    constexpr int kChunk = NS * Elem<DT>::kStep, kNext = kShrinkWaves * kChunk;
-    constexpr bool kPieces = SIDE == 1 && WLOAD != kByElem;
-    ShrinkOps<DT, RT, MB, NS> o0, o1;
-    const ShrinkOffs<RT, MB> off = shrink_offs<DT, VEC, SIDE, RT, MB>(sd, lane);
-    // pieces of 8 ranks of rows that hold fewer or others reach up to 7 elements
-    // into the rows after, so they keep 8 rows from B's end
-    const int last = sd.K - kChunk - (WLOAD == kByAny && SIDE == 1 ? 8 : 0);
+    using E = Elem<DT>;
+    using Tl = ShrinkTile<DT, RT, MB>;
+    constexpr int kChunk = NP * Tl::kPair, kNext = kShrinkWaves * kChunk;
+    uint32_t xoff[MB][2];
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) { // rows past n: never stored
+            const uint32_t t = uint32_t(sd.rows[min(16 * b + 8 * h + (lane >> 3), sd.n - 1)]);
+            xoff[b][h] = VEC ? t * uint32_t(sd.ld * int(sizeof(typename E::T))) + 16 * (lane & 7) : t;
+        }
+    // pieces of rows of B that hold fewer or other ranks reach up to kVec - 1
+    // elements into the rows after, so they keep kVec rows from B's end
+    const int last = sd.K - kChunk - (SIDE == 1 && BANY ? E::kVec : 0);
+    ShrinkOps<DT, RT, MB> o[NP];
     int k = wave * kChunk;
-    if constexpr (PIPE) {
-        if (k <= last) {
-            shrink_load<DT, VEC, SIDE, WLOAD, true>(o0, sd, off, k, lane);
-            for (;;) {
-                k += kNext;
-                const bool more0 = k <= last;
-                if (more0) shrink_load<DT, VEC, SIDE, WLOAD, true>(o1, sd, off, k, lane);
-                shrink_mma<DT, kPieces>(o0, acc, tiles, lane);
-                if (!more0) break;
-                k += kNext;
-                const bool more1 = k <= last;
-                if (more1) shrink_load<DT, VEC, SIDE, WLOAD, true>(o0, sd, off, k, lane);
-                shrink_mma<DT, kPieces>(o1, acc, tiles, lane);
-                if (!more1) break;
-            }
-        }
-    } else {
-        for (; k <= last; k += kNext) {
-            shrink_load<DT, VEC, SIDE, WLOAD, true>(o0, sd, off, k, lane);
-            shrink_mma<DT, kPieces>(o0, acc, tiles, lane);
-        }
+    auto load = [&] {
+#pragma unroll
+        for (int q = 0; q < NP; ++q) shrink_load<DT, VEC, SIDE, BANY, true>(o[q], sd, xoff, k + q * Tl::kPair, lane);
+    };
+    if (k <= last) load();
+    while (k <= last) {
+#pragma unroll
+        for (int q = 0; q < NP; ++q) shrink_put<DT, SIDE>(o[q], tile + q * Tl::kBytes, lane);
+        k += kNext;
+        if (k <= last) load();
+#pragma unroll
+        for (int q = 0; q < NP; ++q) shrink_mma<DT, SIDE>(acc, tile + q * Tl::kBytes, lane);
     }
-    for (; k < sd.K; k += kNext) { // the last, partial chunk
-        shrink_load<DT, VEC, SIDE, kByElem, false>(o0, sd, off, k, lane);
-        shrink_mma<DT, false>(o0, acc, tiles, lane);
-    }
+    for (; k < sd.K; k += kNext) // the last, partial chunk
+        for (int q = 0; q < NP && k + q * Tl::kPair < sd.K; ++q) {
+            shrink_load<DT, VEC, SIDE, BANY, false>(o[0], sd, xoff, k + q * Tl::kPair, lane);
+            shrink_put<DT, SIDE>(o[0], tile, lane);
+            shrink_mma<DT, SIDE>(acc, tile, lane);
+        }
 }
 
-// MB = 1: a workgroup takes a block of 16 rows; MB = 4: a chunk of up to 64, so
-// that A and B are read from L2 once for 64 rows.
+// A workgroup takes MB blocks of 16 rows of one segment (MB = 4: a chunk), so that
+// A and B are read once for 16 MB rows.
 template <int DT, bool VEC, int RT, int MB>
 __global__ __launch_bounds__(kShrinkWaves * 64) void bwd_shrink_kernel(BwdArgs a)
 {
-    using E = Elem<DT>;
-    constexpr int W = kShrinkWaves, NS = RT * MB >= 4 ? 2 : 4;
-    constexpr bool kPipe = RT * MB > 1; // one rank tile of 16 rows: no gain
-    constexpr int kTile = 1024 * RT; // LDS of one step's B tile: 32 rows of 16 RT ranks
-    constexpr int kRed = W * RT * 1024, kTiles = W * 2 * kTile;
-    constexpr int kScan = 3 * 4 * W * 64;
-    constexpr int kLds = kRed > kTiles ? kRed : kTiles;
-    __shared__ __attribute__((aligned(16))) char lds[kLds > kScan ? kLds : kScan];
+    constexpr int W = kShrinkWaves, NP = LORA_NP;
+    constexpr int kTile = NP * ShrinkTile<DT, RT, MB>::kBytes;
+    constexpr int kRed = W * RT * 1024, kScan = 3 * 4 * W * 64;
+    constexpr int kLds = std::max(std::max(W * kTile, kRed), kScan);
+    static_assert(kLds <= 160 * 1024, "LDS budget");
+    __shared__ __attribute__((aligned(16))) char lds[kLds];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int units = MB == 1 ? a.nblk : a.nchunk;
     // Workgroup b runs on XCD b % 8: an XCD takes a run of consecutive units, so
@@ -462,18 +460,15 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void bwd_shrink_kernel(BwdArgs a
     int r, n, p0;
     float scale;
     const int32_t *rows;
-    if constexpr (MB == 1) {
-        const lora_blk_desc *d = a.blk + unit;
+    auto take = [&](const auto *d) {
         pA = reinterpret_cast<const void *>(d->A), pB = reinterpret_cast<const void *>(d->B);
         r = d->rank, n = d->n, p0 = d->p0, scale = d->scale, rows = d->rows;
-    } else {
-        const lora_chunk_desc *d = a.chunk + unit;
-        pA = reinterpret_cast<const void *>(d->A), pB = reinterpret_cast<const void *>(d->B);
-        r = d->rank, n = d->n, p0 = d->p0, scale = d->scale, rows = d->rows;
-    }
+    };
+    if constexpr (MB == 1) take(a.blk + unit);
+    else take(a.chunk + unit);
     ShrinkSide sd = side ? ShrinkSide{a.dy, pB, a.lddy, a.d_out, r, 0, rows, n} : ShrinkSide{a.x, pA, a.ldx, a.d_in, r, 0, rows, n};
     const int ntiles = (r + 15) >> 4;
-    char *tiles = lds + wave * 2 * kTile;
+    char *tile = lds + wave * kTile;
 
     for (int rt0 = 0; rt0 < ntiles; rt0 += RT) {
         floatx4 acc[MB][RT];
@@ -482,10 +477,9 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void bwd_shrink_kernel(BwdArgs a
 #pragma unroll
             for (int i = 0; i < RT; ++i) acc[b][i] = floatx4{};
         sd.rt0 = rt0;
-        if (side == 0) shrink_sum<DT, VEC, 0, kByElem, kPipe, RT, MB, NS>(acc, sd, tiles, wave, lane);
-        else if constexpr (DT == LORA_F32) shrink_sum<DT, VEC, 1, kByElem, false, RT, MB, NS>(acc, sd, tiles, wave, lane);
-        else if (r & 7) shrink_sum<DT, VEC, 1, kByAny, false, RT, MB, NS>(acc, sd, tiles, wave, lane);
-        else shrink_sum<DT, VEC, 1, kByVec, kPipe, RT, MB, NS>(acc, sd, tiles, wave, lane);
+        if (side == 0) shrink_sum<DT, VEC, 0, false, RT, MB, NP>(acc, sd, tile, wave, lane);
+        else if (r % Elem<DT>::kVec) shrink_sum<DT, VEC, 1, true, RT, MB, NP>(acc, sd, tile, wave, lane);
+        else shrink_sum<DT, VEC, 1, false, RT, MB, NP>(acc, sd, tile, wave, lane);
         // lane l of tile i holds D[row 4 (l / 16) + q][rank l % 16]
         float *red = reinterpret_cast<float *>(lds);
 #pragma unroll
@@ -495,33 +489,35 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void bwd_shrink_kernel(BwdArgs a
             for (int i = 0; i < RT; ++i) *reinterpret_cast<floatx4 *>(red + ((wave * RT + i) * 64 + lane) * 4) = acc[b][i];
             __syncthreads();
             for (int idx = tid; idx < RT * 256; idx += W * 64) {
-                const int i = idx >> 8, l2 = (idx >> 2) & 63, q = idx & 3;
+                const int i = idx >> 8, l2 = (idx >> 2) & 63, q4 = idx & 3;
                 float sum = 0.f;
 #pragma unroll
-                for (int w = 0; w < W; ++w) sum += red[((w * RT + i) * 64 + l2) * 4 + q];
-                const int mm = 16 * b + 4 * (l2 >> 4) + q, j = 16 * (rt0 + i) + (l2 & 15);
-                if (mm >= n || rt0 + i >= ntiles) continue;
+                for (int w = 0; w < W; ++w) sum += red[((w * RT + i) * 64 + l2) * 4 + q4];
+                const int mm = 16 * b + 4 * (l2 >> 4) + q4, t = rt0 + i, jm = l2 & 15, j = 16 * t + jm;
+                if (mm >= n || t >= ntiles) continue;
                 const int p = p0 + mm;
-                const float t = j < r ? sum * scale : 0.f;
-                char *win = (side ? a.ut : a.vt) + int64_t(p / kWin) * E::kParts * a.r16 * kWin * E::kPart;
-                const int at = j * kWin + p % kWin;
+                const float v = j < r ? sum * scale : 0.f;
+                char *parts = side ? a.ut : a.vt, *ur = a.ur + (int64_t(p >> 4) * a.nt + t) * kPieces;
                 if constexpr (DT == LORA_BF16) {
-                    const uint32_t h = f32_to_bf16(t);
+                    const uint32_t h = f32_to_bf16(v);
                     const bool fin = (h & 0x7f80u) != 0x7f80u; // an infinity or NaN has no rest
-                    const float rest = fin ? t - bf16_to_f32(h) : 0.f;
+                    const float rest = fin ? v - bf16_to_f32(h) : 0.f;
                     const uint32_t mid = f32_to_bf16(rest);
-                    uint16_t *o = reinterpret_cast<uint16_t *>(win) + at;
+                    const int at = (((p & 31) >> 3) * 16 + jm) * 8 + (p & 7);
+                    uint16_t *o = reinterpret_cast<uint16_t *>(parts + (int64_t(p / kWin) * 3 * a.nt + t) * kPieces) + at;
+                    const int64_t part = int64_t(a.nt) * kPieces / 2;
                     o[0] = uint16_t(h);
-                    o[a.r16 * kWin] = uint16_t(mid);
-                    o[2 * a.r16 * kWin] = uint16_t(f32_to_bf16(rest - bf16_to_f32(mid)));
+                    o[part] = uint16_t(mid);
+                    o[2 * part] = uint16_t(f32_to_bf16(rest - bf16_to_f32(mid)));
                     if (side) {
-                        uint16_t *u = reinterpret_cast<uint16_t *>(a.ur) + int64_t(p) * 2 * a.r16 + 32 * (j >> 4) + (j & 15);
+                        uint16_t *u = reinterpret_cast<uint16_t *>(ur) + ((jm >> 3) * 16 + (p & 15)) * 8 + (jm & 7);
                         u[0] = uint16_t(h);
-                        u[16] = uint16_t(mid);
+                        u[2 * 16 * 8] = uint16_t(mid);
                     }
                 } else {
-                    reinterpret_cast<float *>(win)[at] = t;
-                    if (side) reinterpret_cast<float *>(a.ur)[int64_t(p) * a.r16 + j] = t;
+                    float *o = reinterpret_cast<float *>(parts + ((int64_t(p / kWin) * 2 + ((p & 31) >> 4)) * a.nt + t) * kPieces);
+                    o[(((p & 15) >> 2) * 16 + jm) * 4 + (p & 3)] = v;
+                    if (side) reinterpret_cast<float *>(ur)[((jm >> 2) * 16 + (p & 15)) * 4 + (jm & 3)] = v;
                 }
             }
         }
@@ -535,6 +531,7 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void bwd_shrink_kernel(BwdArgs a
 // ----------------------------------------------------------------------------
 constexpr int kGradWaves = 4;
 constexpr int kMaxSpan = 2048;
+constexpr int kOutPitch = 272, kWaveTile = 16 * kOutPitch; // a wave's LDS: 32 rows of 128 bytes, or 16 rows of results
 constexpr int kTileCols = 64 * kGradWaves; // columns of a workgroup
 // Row blocks of a dx workgroup, by the rank tiles of a gradient one (which set the
 // registers that the launch has): with one rank tile, chunks of 64 rows would
@@ -555,26 +552,13 @@ __device__ __forceinline__ bf16x8 tile_frag(const char *tile, int un, int half, 
     return join8(h[0], h[1]);
 }
 
-// Stores 4 consecutive fp32 sums.
-__device__ __forceinline__ void put4(float *dst, floatx4 v, int n, bool vec, bool add)
-{
-    if (vec) {
-        if (add) v += *reinterpret_cast<const floatx4 *>(dst);
-        *reinterpret_cast<floatx4 *>(dst) = v;
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (e < n) dst[e] = add ? dst[e] + v[e] : v[e];
-    }
-}
-
 // Operands of one window.  bf16: rows by 16 bytes, row (lane / 8) + 8 i, column
 // 8 (lane % 8), to be turned through the tile; fp32: the column fragments
 // themselves, in two halves of 16 rows.
 template <int DT, int RT> struct GradOps {
     static constexpr int kHalves = DT == LORA_BF16 ? 1 : 2;
     typename Elem<DT>::F xf[kHalves][4];
-    typename Elem<DT>::F uf[kHalves][RT][Elem<DT>::kParts];
+    typename Elem<DT>::F uf[RT][Elem<DT>::kParts]; // fp32: of the two halves
 };
 
 struct GradSide {
@@ -592,17 +576,13 @@ __device__ __forceinline__ void grad_load(GradOps<DT, RT> &o, const BwdArgs &a, 
     using T = typename E::T;
     const int m = lane & 15, g = lane >> 4;
     const int base = w * kWin;
-    const char *win = static_cast<const char *>(sd.parts) + int64_t(w) * E::kParts * a.r16 * kWin * E::kPart;
-    const uint32_t uoff = uint32_t(m * kWin + E::kVec * g) * E::kPart;
+    const char *win = static_cast<const char *>(sd.parts) + int64_t(w) * E::kParts * a.nt * kPieces;
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-        const int j = min(16 * (rt0 + i), a.r16 - 16); // ranks past r16: clamped, not stored
+        const int t = min(rt0 + i, a.nt - 1); // past the last tile: not stored
 #pragma unroll
-        for (int h = 0; h < o.kHalves; ++h)
-#pragma unroll
-            for (int q = 0; q < E::kParts; ++q)
-                o.uf[h][i][q] = __builtin_bit_cast(
-                    typename E::F, load16(win + ((q * a.r16 + j) * kWin + 16 * h) * E::kPart, uoff));
+        for (int q = 0; q < E::kParts; ++q)
+            o.uf[i][q] = __builtin_bit_cast(typename E::F, load16(win + (q * a.nt + t) * kPieces, 16 * lane));
     }
     auto token = [&](int p) { return tok[min(max(p, begin), end - 1) - begin]; };
     if constexpr (DT == LORA_BF16 && VEC) {
@@ -619,7 +599,7 @@ __device__ __forceinline__ void grad_load(GradOps<DT, RT> &o, const BwdArgs &a, 
         for (int i = 0; i < 4; ++i) {
             const gptr<T> row = src + int64_t(token(base + (lane >> 3) + 8 * i)) * sd.ld;
             if constexpr (WHOLE) o.xf[0][i] = __builtin_bit_cast(bf16x8, load16_any(row + c));
-            else o.xf[0][i] = load_row<DT>(row, c, sd.D);
+            else o.xf[0][i] = __builtin_bit_cast(bf16x8, load_row<DT>(row, c, sd.D));
         }
     } else {
         const gptr<T> src = as_global<T>(sd.src);
@@ -658,7 +638,8 @@ __device__ __forceinline__ void grad_mma(GradOps<DT, RT> &o, floatx4 (&acc)[4][R
 #pragma unroll
             for (int i = 0; i < RT; ++i)
 #pragma unroll
-                for (int q = 0; q < E::kParts; ++q) mask(o.uf[h][i][q]);
+                for (int q = 0; q < E::kParts; ++q)
+                    if (DT == LORA_BF16 || q == h) mask(o.uf[i][q]);
             if constexpr (DT == LORA_BF16) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -686,9 +667,11 @@ __device__ __forceinline__ void grad_mma(GradOps<DT, RT> &o, floatx4 (&acc)[4][R
         for (int i = 0; i < RT; ++i)
 #pragma unroll
             for (int q = 0; q < E::kParts; ++q)
+                if (DT == LORA_BF16 || q == h) {
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    acc[t][i] = side ? mma<DT>(o.uf[h][i][q], xf[t], acc[t][i]) : mma<DT>(xf[t], o.uf[h][i][q], acc[t][i]);
+                    for (int t = 0; t < 4; ++t)
+                        acc[t][i] = side ? mma<DT>(xf[t], o.uf[i][q], acc[t][i]) : mma<DT>(o.uf[i][q], xf[t], acc[t][i]);
+                }
     }
 }
 
@@ -716,22 +699,21 @@ __device__ __forceinline__ void grad_item(const BwdArgs &a, const GradSide &sd, 
         if (RT == 4) o0 = o1;
         else grad_load<DT, VEC, WHOLE>(o0, a, sd, begin, end, w, c0, rt0, tok, lane);
     }
-    // dA (side 0): D rows are columns of x, D columns are ranks.  dB: D rows
-    // are ranks, D columns are columns of dy (rows of dB).
+    // dA (side 0): D rows are ranks, D columns are columns of x; dB: D rows are
+    // columns of dy (rows of dB), D columns are ranks.  Either way the 16 lanes of
+    // a group store 64 consecutive bytes.
     const int m = lane & 15, g = lane >> 4;
-    const bool vec = (reinterpret_cast<uintptr_t>(dst) & 15) == 0 && ((side ? r : sd.D) & 3) == 0;
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            if (side == 0) {
-                const int j = 16 * (rt0 + i) + m, c = c0 + 16 * t + 4 * g;
-                if (j < r && c < sd.D) put4(dst + int64_t(j) * sd.D + c, acc[t][i], sd.D - c, vec, add);
-            } else {
-                const int c = c0 + 16 * t + m, j = 16 * (rt0 + i) + 4 * g;
-                if (c < sd.D && j < r) put4(dst + int64_t(c) * r + j, acc[t][i], r - j, vec, add);
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int j = 16 * (rt0 + i) + (side ? m : 4 * g + q), c = c0 + 16 * t + (side ? 4 * g + q : m);
+                if (j >= r || c >= sd.D) continue;
+                float *o = dst + (side ? int64_t(c) * r + j : int64_t(j) * sd.D + c);
+                *o = add ? *o + acc[t][i][q] : acc[t][i][q];
             }
-        }
 }
 
 // RT: rank tiles that a wave holds (the plan's largest rank, at most 4: higher
@@ -757,7 +739,7 @@ __device__ __forceinline__ void grad_unit(const BwdArgs &a, int id, char *tiles_
         dst = a.part + it.slot * a.part_stride + (side ? int64_t(r) * a.d_in : 0);
         add = false;
     }
-    char *tile = tiles_lds + (DT == LORA_BF16 ? wave * 4096 : 0);
+    char *tile = tiles_lds + wave * kWaveTile;
     auto ranks = [&](auto whole) {
         constexpr bool W = decltype(whole)::value;
         const int left = r - 64 * group;
@@ -799,22 +781,25 @@ __device__ __forceinline__ void dx_unit(const BwdArgs &a, int id, char *tiles_ld
     if constexpr (RB == 4) take(a.chunk + unit);
     else if (!JOIN || unit < a.nblk) take(a.blk + unit);
     else p0 = a.Tp + 16 * (unit - a.nblk), n = min(16, a.T - p0);
-    char *tile = tiles_lds + wave * 4096;
+    char *tile = tiles_lds + wave * kWaveTile;
     // operands of 16 ranks: u of 4 row blocks, and A by rows (bf16: rank
     // (lane / 8) + 8 i, column 8 (lane % 8)) or by column fragments (fp32)
     struct Ops {
         typename E::F uf[RB], af[4];
     };
-    constexpr int kU = DT == LORA_BF16 ? 4 : int(sizeof(float)); // bytes of u in rows per rank
+    // u of row m of block i (past n: not stored), where launch 1 put its position
     uint32_t uoff[RB];
 #pragma unroll
-    for (int i = 0; i < RB; ++i) uoff[i] = uint32_t(min(16 * i + m, n - 1)) * uint32_t(a.r16 * kU) + 16 * g; // past n: not stored
-    const char *ur = a.ur + int64_t(p0) * a.r16 * kU;
+    for (int i = 0; i < RB; ++i) {
+        const int p = p0 + min(16 * i + m, n - 1);
+        uoff[i] = uint32_t((p >> 4) - (p0 >> 4)) * uint32_t(a.nt * kPieces) + uint32_t(g * 16 + (p & 15)) * 16;
+    }
+    const char *ur = a.ur + int64_t(p0 >> 4) * a.nt * kPieces;
     const bool whole = c0 + 64 <= a.d_in; // every piece of this wave lies in its row
     const uint32_t acol = c0 + 8 * (lane & 7) < a.d_in ? 16 * (lane & 7) : 0;
     auto load = [&](Ops &o, int j0) {
 #pragma unroll
-        for (int i = 0; i < RB; ++i) o.uf[i] = __builtin_bit_cast(typename E::F, load16(ur + j0 * kU, uoff[i]));
+        for (int i = 0; i < RB; ++i) o.uf[i] = __builtin_bit_cast(typename E::F, load16(ur + (j0 >> 4) * kPieces, uoff[i]));
         if constexpr (DT == LORA_BF16) {
             const char *base = static_cast<const char *>(A) + (int64_t(j0) * a.d_in + c0) * 2;
 #pragma unroll
@@ -824,7 +809,7 @@ __device__ __forceinline__ void dx_unit(const BwdArgs &a, int id, char *tiles_ld
                 u32x4 w;
                 if constexpr (VEC) w = load16(base, row + acol);
                 else if (whole) w = load16_any(as_global<char>(base) + (row + acol)); // wave-uniform
-                else w = __builtin_bit_cast(u32x4, load_row<DT>(as_global<T>(base + row), 8 * (lane & 7), a.d_in - c0));
+                else w = load_row<DT>(as_global<T>(base + row), 8 * (lane & 7), a.d_in - c0);
                 if (j0 + j >= r) w = u32x4{};
                 o.af[i] = __builtin_bit_cast(bf16x8, w);
             }
@@ -865,40 +850,37 @@ __device__ __forceinline__ void dx_unit(const BwdArgs &a, int id, char *tiles_ld
 #pragma unroll
             for (int i = 0; i < RB; ++i) acc[t][i] = mma<DT>(af[t], o.uf[i], acc[t][i]);
     };
-    // the first operands, then dx's rows (needed last), then each next step's
-    // operands before the products of the current one
+    // The first operands, then what is added to (needed last), then each next step's
+    // operands before the products of the current one.  Results leave through the
+    // wave's tile by rows: bf16 rows (lane / 8) + 8 h of a block, 8 columns at
+    // 8 (lane % 8); fp32 and JOIN rows (lane / 16) + 4 h, 4 columns at 4 (lane % 16).
+    constexpr bool kBy8 = DT == LORA_BF16 && !JOIN;
+    constexpr int H = kBy8 ? 2 : 4, kC = kBy8 ? 8 : 4;
+    const int orow = kBy8 ? lane >> 3 : lane >> 4, oc = c0 + kC * (kBy8 ? lane & 7 : lane & 15);
     Ops o0, o1;
     if (!JOIN || r) load(o0, 0);
-    T *row[RB];      // element by element
-    uint32_t yoff[RB]; // VEC: byte offsets of the row's pieces of this lane
-    u32x4 y[RB][2];
-    char *dxc = reinterpret_cast<char *>(static_cast<T *>(a.dx) + c0);
+    T *out[RB][H];
+    u32x4 y[RB][H];
 #pragma unroll
-    for (int i = 0; i < RB; ++i) {
-        const int t = a.perm[p0 + min(16 * i + m, n - 1)];
-        row[i] = static_cast<T *>(a.dx) + int64_t(t) * a.lddx;
-        yoff[i] = uint32_t(t) * uint32_t(a.lddx * int(sizeof(T))) + 16 * g;
-        if constexpr (!JOIN && DT == LORA_BF16) {
+    for (int i = 0; i < RB; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int c = c0 + col<DT>(g, 8 * h);
-                if constexpr (VEC) y[i][h] = load16(dxc, c < a.d_in ? yoff[i] + 64 * h : yoff[i] - 16 * g); // past d_in: not stored
-                else if (whole) y[i][h] = load16_any(as_global<T>(row[i]) + c);
-                else y[i][h] = __builtin_bit_cast(u32x4, load_row<DT>(as_global<T>(row[i]), c, a.d_in));
+        for (int h = 0; h < H; ++h) {
+            out[i][h] = static_cast<T *>(a.dx) + int64_t(a.perm[p0 + min(16 * i + orow + (16 / H) * h, n - 1)]) * a.lddx;
+            if constexpr (!JOIN) {
+                const gptr<T> row = as_global<T>(out[i][h]);
+                if constexpr (VEC) y[i][h] = *(gptr<u32x4>)(row + (oc < a.d_in ? oc : 0)); // past d_in: not stored
+                else if (whole) y[i][h] = load16_any(row + oc);
+                else y[i][h] = load_row<DT>(row, oc, a.d_in);
             }
         }
-    }
+    floatx4 base[H]; // JOIN: the sums of the parts
     if constexpr (JOIN) {
-        const float *q = a.joins + int64_t(p0) * a.d_in + c0;
+#pragma unroll
+        for (int h = 0; h < H; ++h) base[h] = floatx4{};
+        const float *q = a.joins + int64_t(p0) * a.d_in + (oc < a.d_in ? oc : 0);
         for (int k = 0; k < a.splits; ++k, q += int64_t(a.T) * a.d_in)
 #pragma unroll
-            for (int i = 0; i < RB; ++i)
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const int c = col<DT>(g, 4 * t);
-                    acc[t][i] += *reinterpret_cast<const floatx4 *>(q + int64_t(min(16 * i + m, n - 1)) * a.d_in +
-                                                                    (c0 + c < a.d_in ? c : 0));
-                }
+            for (int h = 0; h < H; ++h) base[h] += *reinterpret_cast<const floatx4 *>(q + int64_t(min(orow + 4 * h, n - 1)) * a.d_in);
     }
     for (int j0 = 0; !JOIN || r;) {
         if (j0 + 16 < r) load(o1, j0 + 16);
@@ -910,42 +892,55 @@ __device__ __forceinline__ void dx_unit(const BwdArgs &a, int id, char *tiles_ld
     }
 #pragma unroll
     for (int i = 0; i < RB; ++i) {
-        if (16 * i + m >= n) continue;
-        if constexpr (DT == LORA_BF16) {
+        // rows of kOutPitch bytes: 16 rows' equal columns fall in distinct banks
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int c = c0 + col<DT>(g, 8 * h);
-                const floatx4 lo = acc[2 * h][i], hi = acc[2 * h + 1][i];
-                if (c >= a.d_in) continue;
+        for (int t = 0; t < 4; ++t)
+            *reinterpret_cast<floatx4 *>(tile + m * kOutPitch + 4 * (DT == LORA_BF16 ? col<DT>(g, 4 * t) : 16 * t + 4 * g)) = acc[t][i];
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            const int row = orow + (16 / H) * h;
+            const floatx4 *f = reinterpret_cast<const floatx4 *>(tile + row * kOutPitch + 4 * (oc - c0));
+            if (16 * i + row >= n || oc >= a.d_in) continue;
+            if constexpr (kBy8) {
+                const floatx4 lo = f[0], hi = f[1];
                 u32x4 o;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float f0 = e < 2 ? lo[2 * e] : hi[2 * e - 4], f1 = e < 2 ? lo[2 * e + 1] : hi[2 * e - 3];
-                    o[e] = JOIN ? pack_bf16x2(f0, f1)
-                                : pack_bf16x2(bf16_to_f32(y[i][h][e] & 0xffffu) + f0, bf16_to_f32(y[i][h][e] >> 16) + f1);
+                    o[e] = pack_bf16x2(bf16_to_f32(y[i][h][e] & 0xffffu) + f0, bf16_to_f32(y[i][h][e] >> 16) + f1);
                 }
-                if constexpr (VEC) *reinterpret_cast<u32x4 *>(dxc + 64 * h + yoff[i]) = o;
-                else if (whole) *reinterpret_cast<u32x4_any *>(row[i] + c) = o;
+                if constexpr (VEC) *reinterpret_cast<u32x4 *>(out[i][h] + oc) = o;
+                else if (whole) *reinterpret_cast<u32x4_any *>(out[i][h] + oc) = o;
                 else
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        if (c + e < a.d_in) row[i][c + e] = uint16_t(o[e >> 1] >> (16 * (e & 1)));
-            }
-        } else {
+                        if (oc + e < a.d_in) out[i][h][oc + e] = uint16_t(o[e >> 1] >> (16 * (e & 1)));
+            } else if constexpr (JOIN) { // d_in is a multiple of 8
+                const floatx4 v = base[h] + f[0];
+                *reinterpret_cast<u32x2 *>(out[i][h] + oc) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+            } else {
+                const floatx4 v = __builtin_bit_cast(floatx4, y[i][h]) + f[0];
+                if constexpr (VEC) *reinterpret_cast<floatx4 *>(out[i][h] + oc) = v;
+                else
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int c = c0 + col<DT>(g, 4 * t);
-                if (c < a.d_in) put4(row[i] + c, acc[t][i], a.d_in - c, VEC, true);
+                    for (int e = 0; e < 4; ++e)
+                        if (oc + e < a.d_in) out[i][h][oc + e] = v[e];
             }
         }
     }
 }
 
 // Launch 2: the gradients' workgroups, then dx's (they read the same u).
-template <int DT, bool VEC, int RT>
-__global__ __launch_bounds__(kGradWaves * 64, RT == 1 ? 5 : RT == 2 && DT == LORA_BF16 ? 4 : 2) void bwd_out_kernel(BwdArgs a)
+// Waves per SIMD that the registers allow without spills.
+constexpr int out_waves(int dt, bool vec, int rt)
 {
-    __shared__ __attribute__((aligned(16))) char tiles_lds[DT == LORA_BF16 ? kGradWaves * 4096 : 16];
+    if (dt == LORA_F32) return rt == 1 ? 4 : rt == 2 ? 3 : 1;
+    return rt == 1 ? 5 : rt == 2 ? (vec ? 4 : 3) : (vec ? 2 : 1);
+}
+template <int DT, bool VEC, int RT>
+__global__ __launch_bounds__(kGradWaves * 64, out_waves(DT, VEC, RT)) void bwd_out_kernel(BwdArgs a)
+{
+    __shared__ __attribute__((aligned(16))) char tiles_lds[kGradWaves * kWaveTile];
     __shared__ int32_t tok[kMaxSpan];
     if (int(blockIdx.x) < a.ngrad) grad_unit<DT, VEC, RT>(a, blockIdx.x, tiles_lds, tok);
     else dx_unit<DT, VEC, false, dx_blocks(RT)>(a, int(blockIdx.x) - a.ngrad, tiles_lds);
@@ -980,7 +975,7 @@ __global__ __launch_bounds__(256) void bwd_reduce_kernel(BwdArgs a)
 // The last launch of the fused layer's backward.
 template <bool VEC> __global__ __launch_bounds__(kDxWaves * 64, 4) void bwd_join_kernel(BwdArgs a)
 {
-    __shared__ __attribute__((aligned(16))) char tiles_lds[kDxWaves * 4096];
+    __shared__ __attribute__((aligned(16))) char tiles_lds[kDxWaves * kWaveTile];
     dx_unit<LORA_BF16, VEC, true, 1>(a, blockIdx.x, tiles_lds);
 }
 
@@ -1017,9 +1012,9 @@ Layout layout_of(int32_t rows, int32_t d_in, int32_t d_out, int32_t max_rank)
     const size_t r16 = size_t(max_rank + 15) / 16 * 16, n = size_t(rows);
     const size_t windows = (n + kWin - 1) / kWin;
     l.ut = 0;
-    l.vt = l.ut + up256(windows * kWin * r16 * 6); // three bf16 parts; fp32 takes 4 of the 6 bytes
-    l.ur = l.vt + up256(windows * kWin * r16 * 6);
-    l.items = l.ur + up256(n * r16 * 4);
+    l.vt = l.ut + windows * 3 * (r16 / 16) * kPieces; // three bf16 parts; fp32 takes two thirds
+    l.ur = l.vt + windows * 3 * (r16 / 16) * kPieces;
+    l.items = l.ur + (n + 15) / 16 * (r16 / 16) * kPieces;
     const size_t borders = most_borders(n);
     l.splits = l.items + up256((n + borders) * sizeof(Item));
     l.part = l.splits + up256(borders * sizeof(Split));
@@ -1031,8 +1026,8 @@ Layout layout_of(int32_t rows, int32_t d_in, int32_t d_out, int32_t max_rank)
 template <int DT, bool VEC, int MB> void run_shrink_mb(hipStream_t s, const BwdArgs &a, unsigned units, unsigned nside)
 {
     const dim3 grid((units + 7) / 8 * nside * 8 + 8), block(kShrinkWaves * 64);
-    if (a.r16 <= 16) launch_kernel(bwd_shrink_kernel<DT, VEC, 1, MB>, grid, block, 0, s, a);
-    else if (a.r16 <= 32) launch_kernel(bwd_shrink_kernel<DT, VEC, 2, MB>, grid, block, 0, s, a);
+    if (a.nt <= 1) launch_kernel(bwd_shrink_kernel<DT, VEC, 1, MB>, grid, block, 0, s, a);
+    else if (a.nt <= 2) launch_kernel(bwd_shrink_kernel<DT, VEC, 2, MB>, grid, block, 0, s, a);
     else launch_kernel(bwd_shrink_kernel<DT, VEC, 4, MB>, grid, block, 0, s, a);
 }
 // 64 rows per workgroup when that still gives every CU two of them.
@@ -1045,8 +1040,8 @@ template <int DT, bool VEC> void run_shrink(hipStream_t s, const BwdArgs &a, int
 template <int DT, bool VEC> void run_out(hipStream_t s, const BwdArgs &a, dim3 grid)
 {
     const dim3 block(kGradWaves * 64);
-    if (a.r16 <= 16) launch_kernel(bwd_out_kernel<DT, VEC, 1>, grid, block, 0, s, a);
-    else if (a.r16 <= 32) launch_kernel(bwd_out_kernel<DT, VEC, 2>, grid, block, 0, s, a);
+    if (a.nt <= 1) launch_kernel(bwd_out_kernel<DT, VEC, 1>, grid, block, 0, s, a);
+    else if (a.nt <= 2) launch_kernel(bwd_out_kernel<DT, VEC, 2>, grid, block, 0, s, a);
     else launch_kernel(bwd_out_kernel<DT, VEC, 4>, grid, block, 0, s, a);
 }
 
@@ -1081,7 +1076,7 @@ static BwdArgs make_args(const BackwardArgs &b, const PlanView &p, const Layout 
     a.S = h->num_segments;
     a.nblk = h->num_blocks;
     a.nchunk = h->num_chunks;
-    a.r16 = (h->max_rank + 15) / 16 * 16;
+    a.nt = (h->max_rank + 15) / 16;
     a.ut = w + l.ut;
     a.vt = w + l.vt;
     a.ur = w + l.ur;
@@ -1110,12 +1105,12 @@ int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p
     a.sides = (b.grad_B ? 1 : 0) | (b.grad_A || b.dx || u_rows ? 2 : 0);
     if (u_rows) {
         *u_rows = reinterpret_cast<const uint16_t *>(a.ur);
-        *ldu = 2 * int64_t(a.r16);
+        *ldu = int64_t(a.nt) * kPieces / 2;
     }
     if (!a.sides) return LORA_OK;
     a.tiles_A = a.grad_A ? (a.d_in + kTileCols - 1) / kTileCols : 0;
     a.tiles = a.tiles_A + (a.grad_B ? (a.d_out + kTileCols - 1) / kTileCols : 0);
-    a.groups = (a.r16 + 63) / 64;
+    a.groups = (a.nt + 3) / 4;
     a.span = span_of(h->num_sorted, h->num_segments, int64_t(a.tiles) * a.groups);
     const lora_seg_desc *hs = reinterpret_cast<const lora_seg_desc *>(reinterpret_cast<const char *>(h) + h->seg_offset);
     for (int i = 0; i < h->num_segments; ++i) {
@@ -1127,7 +1122,7 @@ int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p
     if (a.nsplit > 65535) return fail(LORA_ERR_ARG, "backward: %d segments over several spans (> 65535)", a.nsplit);
 
     const int64_t ngrad = int64_t(a.nitems) * a.tiles * a.groups;
-    const int64_t ndx = a.dx ? int64_t(dx_blocks((a.r16 + 15) / 16) == 4 ? a.nchunk : a.nblk) * a.tiles_x : 0;
+    const int64_t ndx = a.dx ? int64_t(dx_blocks(a.nt) == 4 ? a.nchunk : a.nblk) * a.tiles_x : 0;
     if (ngrad + ndx > (int64_t(1) << 31) - 1) return fail(LORA_ERR_ARG, "backward: too many work items");
     a.ngrad = int(ngrad);
 

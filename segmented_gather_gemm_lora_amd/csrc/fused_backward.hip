@@ -103,8 +103,8 @@ struct DgradArgs {
     const int32_t *perm;
     const int32_t *segidx;
     const lora_seg_desc *seg;
-    const uint16_t *ur; // u in rows: [position][per 16 ranks: 16 hi, 16 lo]
-    int64_t ldu;
+    const uint16_t *ur; // u as MFMA operands: [16 positions][16-rank tile][lane 16 g + position % 16][8 ranks]
+    int64_t ldu;        // elements from 16 positions to the next
     int T, Tp;
     uint16_t *dx;
     int64_t lddx;
@@ -234,7 +234,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
             if (xw) {
 #pragma unroll
                 for (int j = 0; j < kXDma; ++j) {
-                    const char *p = reinterpret_cast<const char *>(a.ur + int64_t(xpos[j]) * a.ldu + 2 * ij + xk[j]);
+                    // unit xk / 8: hi parts of ranks 0 .. 7, 8 .. 15, then lo parts
+                    const char *p = reinterpret_cast<const char *>(a.ur + int64_t(xpos[j] >> 4) * a.ldu + 32 * ij + 16 * xk[j] + 8 * (xpos[j] & 15));
                     dma16(xpos[j] >= first && xpos[j] < last ? p : zeros, xbase + j * 1024);
                 }
             }

@@ -148,8 +148,10 @@ struct BackwardArgs {
     bool vec_x, vec_dy, vec_dx; // rows are whole aligned 16-byte pieces
 };
 size_t sgmv_backward_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out, int32_t max_rank);
-// u_rows / ldu: where the call leaves u in rows (bf16 calls: per position and 16
-// ranks, 16 hi then 16 lo halves), computed when asked for or needed.
+// u_rows / ldu: where the call leaves u for dx, computed when asked for or needed
+// (bf16: operands of 512 elements per 16 positions and 16 ranks, lane 16 g +
+// position % 16 of 8 ranks each, g = 0, 1: hi parts, 2, 3: lo; ldu elements from
+// 16 positions to the next).
 int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p, void *ws,
                          const uint16_t **u_rows = nullptr, int64_t *ldu = nullptr);
 // dx = the sum of `splits` parts [T][d_in] (fp32, plan rows) + u A, every row; after
