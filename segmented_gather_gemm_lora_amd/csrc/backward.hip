@@ -670,7 +670,7 @@ __device__ __forceinline__ void grad_mma(GradOps<DT, RT> &o, floatx4 (&acc)[4][R
                 if (DT == LORA_BF16 || q == h) {
 #pragma unroll
                     for (int t = 0; t < 4; ++t)
-                        acc[t][i] = side ? mma<DT>(xf[t], o.uf[i][q], acc[t][i]) : mma<DT>(o.uf[i][q], xf[t], acc[t][i]);
+                        acc[t][i] = side ? mma<DT>(o.uf[i][q], xf[t], acc[t][i]) : mma<DT>(xf[t], o.uf[i][q], acc[t][i]);
                 }
     }
 }
@@ -699,21 +699,46 @@ __device__ __forceinline__ void grad_item(const BwdArgs &a, const GradSide &sd, 
         if (RT == 4) o0 = o1;
         else grad_load<DT, VEC, WHOLE>(o0, a, sd, begin, end, w, c0, rt0, tok, lane);
     }
-    // dA (side 0): D rows are ranks, D columns are columns of x; dB: D rows are
-    // columns of dy (rows of dB), D columns are ranks.  Either way the 16 lanes of
-    // a group store 64 consecutive bytes.
+    // dA (side 0): D rows are columns of x, D columns ranks; dB: D rows are ranks, D
+    // columns columns of dy (rows of dB).  A lane's 4 sums are consecutive in the
+    // gradient; 16 ranks x 64 columns turn in the wave's tile, so that they leave
+    // with 16 bytes from each of 16 (dB: 4) adjacent lanes for a row.
     const int m = lane & 15, g = lane >> 4;
+    const bool vec = (reinterpret_cast<uintptr_t>(dst) & 15) == 0 && ((side ? r : sd.D) & 3) == 0;
+    auto put4 = [&](float *o, const floatx4 &v, int n) {
+        if (n <= 0) return;
+        if (vec) { // n is a multiple of 4
+            *reinterpret_cast<floatx4 *>(o) = add ? *reinterpret_cast<const floatx4 *>(o) + v : v;
+        } else {
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
+            for (int e = 0; e < 4; ++e)
+                if (e < n) o[e] = add ? o[e] + v[e] : v[e];
+        }
+    };
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+    for (int i = 0; i < RT; ++i) {
+        const int j0 = 16 * (rt0 + i);
+        if (side == 0) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int j = 16 * (rt0 + i) + (side ? m : 4 * g + q), c = c0 + 16 * t + (side ? 4 * g + q : m);
-                if (j >= r || c >= sd.D) continue;
-                float *o = dst + (side ? int64_t(c) * r + j : int64_t(j) * sd.D + c);
-                *o = add ? *o + acc[t][i][q] : acc[t][i][q];
+            for (int t = 0; t < 4; ++t) *reinterpret_cast<floatx4 *>(tile + m * kOutPitch + 4 * (16 * t + 4 * g)) = acc[t][i];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const int j = 4 * h + g, c = c0 + 4 * m;
+                const floatx4 v = *reinterpret_cast<const floatx4 *>(tile + j * kOutPitch + 16 * m);
+                if (j0 + j < r) put4(dst + int64_t(j0 + j) * sd.D + c, v, sd.D - c);
             }
+        } else {
+            // rows of 64 bytes, unit un of row q in slot un ^ (q / 2 % 4)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) *reinterpret_cast<floatx4 *>(tile + (16 * t + m) * 64 + ((g ^ ((m >> 1) & 3)) << 4)) = acc[t][i];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const int q = 16 * h + (lane >> 2), un = lane & 3, j = j0 + 4 * un;
+                const floatx4 v = *reinterpret_cast<const floatx4 *>(tile + q * 64 + ((un ^ ((q >> 1) & 3)) << 4));
+                if (c0 + q < sd.D) put4(dst + int64_t(c0 + q) * r + j, v, r - j);
+            }
+        }
+    }
 }
 
 // RT: rank tiles that a wave holds (the plan's largest rank, at most 4: higher
