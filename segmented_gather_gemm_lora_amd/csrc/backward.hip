@@ -12,7 +12,8 @@
 //  1. bwd_shrink_kernel: u and v of every block of 16 rows (one workgroup per
 //     block and side, its waves split the long axis and are summed in LDS in
 //     wave order), stored in the forms that the next launches multiply with;
-//     one more workgroup lists the work items of launch 2;
+//     one more workgroup lists the work items of launch 2.  Many long segments of
+//     large ranks: bwd_shrink_ring_kernel, 64 rows per workgroup;
 //  2. bwd_out_kernel: dA, dB and dx.  An item of dA and dB is one segment's rows
 //     inside one span of `span` sorted positions; a workgroup takes 256 columns of
 //     x or dy of it.  A segment inside one span is written at once; the sums of a
@@ -22,10 +23,10 @@
 //     the gradients do not change from run to run).
 //
 // Access shape.  A vector load or store costs the L1 one access per run of lanes
-// with consecutive addresses, so every large access has 8 or more adjacent lanes on one row's
-// consecutive 16 bytes (operands loaded straight into MFMA's lane order, 16 rows
-// x 4 pieces that are 16 lanes apart, cost 51 accesses per load: the shrink
-// of 4096 rows took 27 us so, XX as it is).  Rows go to a wave's own LDS tile and are
+// with consecutive addresses, so every large access has 8 or more adjacent lanes on
+// one row's consecutive 16 bytes (operands loaded straight into MFMA's lane order,
+// 16 rows x 4 pieces that are 16 lanes apart, cost 51 accesses per load: the shrink
+// of 4096 rows of rank 16 took 27 us so, 21 as it is).  Rows go to a wave's own LDS tile and are
 // read back in MFMA's order; u and v are stored in that order by launch 1; results
 // leave with consecutive columns in consecutive lanes.
 //
@@ -56,6 +57,8 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 template <typename T> using gptr = const __attribute__((address_space(1))) T *;
+typedef __attribute__((address_space(1))) float *gfloat; // written
+typedef __attribute__((address_space(1))) floatx4 *gfloatx4;
 template <typename T> __device__ __forceinline__ gptr<T> as_global(const void *p) { return (gptr<T>)(p); }
 
 __device__ __forceinline__ float bf16_to_f32(uint32_t h) { return __uint_as_float(h << 16); }
@@ -177,7 +180,7 @@ struct BwdArgs {
 };
 
 // ----------------------------------------------------------------------------
-// Launch 1.  One workgroup: 16 MB rows, all ranks, one side.
+// Launch 1.  One workgroup: 16 rows, all ranks, one side.
 // Side 0: v, K = d_in, W = A (row j is rank j, contiguous along K).
 // Side 1: u, K = d_out, W = B (row k holds the ranks).
 // ----------------------------------------------------------------------------
@@ -239,17 +242,55 @@ __device__ void list_items(const BwdArgs &a, int *scan, int nthreads)
     }
 }
 
+// v = h + mid + low, three bf16 (24 bits); an infinity or NaN has no rest.
+struct Parts {
+    uint32_t h, mid, low;
+};
+__device__ __forceinline__ Parts parts_of(float v)
+{
+    Parts p;
+    p.h = f32_to_bf16(v);
+    const float rest = (p.h & 0x7f80u) != 0x7f80u ? v - bf16_to_f32(p.h) : 0.f;
+    p.mid = f32_to_bf16(rest);
+    p.low = f32_to_bf16(rest - bf16_to_f32(p.mid));
+    return p;
+}
+
+// One value of u (side 1) or v, scaled: position p, rank 16 t + jm (0 past the
+// segment's rank), in the operands that launch 2 reads.
+template <int DT> __device__ __forceinline__ void store_uv(const BwdArgs &a, int side, int p, int t, int jm, float v)
+{
+    char *parts = side ? a.ut : a.vt, *ur = a.ur + (int64_t(p >> 4) * a.nt + t) * kPieces;
+    if constexpr (DT == LORA_BF16) {
+        const Parts f = parts_of(v);
+        const int at = (((p & 31) >> 3) * 16 + jm) * 8 + (p & 7);
+        uint16_t *o = reinterpret_cast<uint16_t *>(parts + (int64_t(p / kWin) * 3 * a.nt + t) * kPieces) + at;
+        const int64_t part = int64_t(a.nt) * kPieces / 2;
+        o[0] = uint16_t(f.h);
+        o[part] = uint16_t(f.mid);
+        o[2 * part] = uint16_t(f.low);
+        if (side) {
+            uint16_t *u = reinterpret_cast<uint16_t *>(ur) + ((jm >> 3) * 16 + (p & 15)) * 8 + (jm & 7);
+            u[0] = uint16_t(f.h);
+            u[2 * 16 * 8] = uint16_t(f.mid);
+        }
+    } else {
+        float *o = reinterpret_cast<float *>(parts + ((int64_t(p / kWin) * 2 + ((p & 31) >> 4)) * a.nt + t) * kPieces);
+        o[(((p & 15) >> 2) * 16 + jm) * 4 + (p & 3)] = v;
+        if (side) reinterpret_cast<float *>(ur)[((jm >> 2) * 16 + (p & 15)) * 4 + (jm & 3)] = v;
+    }
+}
+
 constexpr int kShrinkWaves = 8;
-#define LORA_NP (RT * MB == 1 ? 2 : 1)
 
 // A wave advances 128 bytes of every row at a time (a pair of steps: 64 elements in
 // bf16, 32 in fp32).  Rows of x (dy) and of A are loaded as 8 rows x 128 bytes per
 // instruction, B as pieces of 16 bytes in the order of its rows, and kept in the
 // wave's LDS tile: rows of 128 bytes with unit (16 bytes) un of row q in slot
 // un ^ (q % 8), B as below.
-template <int DT, int RT, int MB> struct ShrinkTile {
+template <int DT, int RT> struct ShrinkTile {
     static constexpr int kPair = 2 * Elem<DT>::kStep;     // elements of the long axis
-    static constexpr int kX = MB * 2048;                  // bytes: x rows
+    static constexpr int kX = 2048;                       // bytes: x rows
     static constexpr int kRowB = DT == LORA_BF16 ? 32 * RT : 64 * RT + 16; // bytes of a row of B's tile
     static constexpr int kB = kPair * kRowB;
     static constexpr int kW = kB > RT * 2048 ? kB : RT * 2048;
@@ -266,9 +307,9 @@ struct ShrinkSide {
 };
 
 // A pair's loads, in registers.
-template <int DT, int RT, int MB> struct ShrinkOps {
+template <int DT, int RT> struct ShrinkOps {
     static constexpr int kWs = RT * 2; // loads of W (B: 64 rows of 2 RT pieces, fp32 32 rows of 4 RT)
-    u32x4 x[MB][2], w[kWs];
+    u32x4 x[2], w[kWs];
 };
 
 // B's place in the tile.  bf16: 32-byte granules (one rank tile of a row), moved so
@@ -283,8 +324,8 @@ template <int DT, int RT> __device__ __forceinline__ int b_at(int k, int byte)
 // FULL: everything that is loaded lies inside.  VEC: rows are whole aligned 16-byte
 // pieces below 4 GiB (xoff: byte offsets); else at any alignment (xoff: tokens).
 // BANY: B's rows are not whole 16-byte pieces.
-template <int DT, bool VEC, int SIDE, bool BANY, bool FULL, int RT, int MB>
-__device__ __forceinline__ void shrink_load(ShrinkOps<DT, RT, MB> &o, const ShrinkSide &sd, const uint32_t (&xoff)[MB][2],
+template <int DT, bool VEC, int SIDE, bool BANY, bool FULL, int RT>
+__device__ __forceinline__ void shrink_load(ShrinkOps<DT, RT> &o, const ShrinkSide &sd, const uint32_t (&xoff)[2],
                                             int k, int lane)
 {
     using E = Elem<DT>;
@@ -293,16 +334,14 @@ __device__ __forceinline__ void shrink_load(ShrinkOps<DT, RT, MB> &o, const Shri
     const int kl = k + E::kVec * (lane & 7); // this lane's first element of a row
     const char *xb = static_cast<const char *>(sd.src) + int64_t(k) * es;
 #pragma unroll
-    for (int b = 0; b < MB; ++b)
-#pragma unroll
         for (int h = 0; h < 2; ++h) {
             if constexpr (FULL && VEC) {
-                o.x[b][h] = load16(xb, xoff[b][h]);
+                o.x[h] = load16(xb, xoff[h]);
             } else {
-                const gptr<T> row = VEC ? (gptr<T>)(as_global<char>(sd.src) + xoff[b][h]) - E::kVec * (lane & 7)
-                                        : as_global<T>(sd.src) + int64_t(xoff[b][h]) * sd.ld;
-                if constexpr (FULL) o.x[b][h] = load16_any(row + kl);
-                else o.x[b][h] = load_row<DT>(row, kl, sd.K);
+                const gptr<T> row = VEC ? (gptr<T>)(as_global<char>(sd.src) + xoff[h]) - E::kVec * (lane & 7)
+                                        : as_global<T>(sd.src) + int64_t(xoff[h]) * sd.ld;
+                if constexpr (FULL) o.x[h] = load16_any(row + kl);
+                else o.x[h] = load_row<DT>(row, kl, sd.K);
             }
         }
 #pragma unroll
@@ -331,16 +370,14 @@ __device__ __forceinline__ void shrink_load(ShrinkOps<DT, RT, MB> &o, const Shri
     }
 }
 
-template <int DT, int SIDE, int RT, int MB>
-__device__ __forceinline__ void shrink_put(const ShrinkOps<DT, RT, MB> &o, char *tile, int lane)
+template <int DT, int SIDE, int RT>
+__device__ __forceinline__ void shrink_put(const ShrinkOps<DT, RT> &o, char *tile, int lane)
 {
-    constexpr int kX = ShrinkTile<DT, RT, MB>::kX;
+    constexpr int kX = ShrinkTile<DT, RT>::kX;
     const int q0 = lane >> 3;
     const int at = q0 * 128 + (((lane & 7) ^ q0) << 4); // rows 8 on: 1024 bytes on, the same slot
 #pragma unroll
-    for (int b = 0; b < MB; ++b)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) *reinterpret_cast<u32x4 *>(tile + (2 * b + h) * 1024 + at) = o.x[b][h];
+        for (int h = 0; h < 2; ++h) *reinterpret_cast<u32x4 *>(tile + h * 1024 + at) = o.x[h];
 #pragma unroll
     for (int i = 0; i < o.kWs; ++i) {
         if constexpr (SIDE == 0) {
@@ -353,21 +390,20 @@ __device__ __forceinline__ void shrink_put(const ShrinkOps<DT, RT, MB> &o, char 
     }
 }
 
-template <int DT, int SIDE, int RT, int MB>
-__device__ __forceinline__ void shrink_mma(floatx4 (&acc)[MB][RT], const char *tile, int lane)
+template <int DT, int SIDE, int RT>
+__device__ __forceinline__ void shrink_mma(floatx4 (&acc)[RT], const char *tile, int lane)
 {
     using E = Elem<DT>;
     using F = typename E::F;
-    constexpr int kX = ShrinkTile<DT, RT, MB>::kX;
+    constexpr int kX = ShrinkTile<DT, RT>::kX;
     const int m = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         auto row_frag = [&](const char *rows) { // row m, unit 4 s + g
             return __builtin_bit_cast(F, *reinterpret_cast<const u32x4 *>(rows + m * 128 + (((4 * s + g) ^ (m & 7)) << 4)));
         };
-        F xf[MB], wf[RT];
-#pragma unroll
-        for (int b = 0; b < MB; ++b) xf[b] = row_frag(tile + b * 2048);
+        F wf[RT];
+        const F xf = row_frag(tile);
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
             if constexpr (SIDE == 0) {
@@ -384,32 +420,29 @@ __device__ __forceinline__ void shrink_mma(floatx4 (&acc)[MB][RT], const char *t
             }
         }
 #pragma unroll
-        for (int b = 0; b < MB; ++b)
-#pragma unroll
-            for (int i = 0; i < RT; ++i) acc[b][i] = mma<DT>(xf[b], wf[i], acc[b][i]);
+        for (int i = 0; i < RT; ++i) acc[i] = mma<DT>(xf, wf[i], acc[i]);
     }
 }
 
-// This wave's part of the sums: NP pairs at a time, the next ones' loads in flight
-// while the current ones are multiplied.
-template <int DT, bool VEC, int SIDE, bool BANY, int RT, int MB, int NP>
-__device__ __forceinline__ void shrink_sum(floatx4 (&acc)[MB][RT], const ShrinkSide &sd, char *tile, int wave, int lane)
+// This wave's part of the sums: NP pairs at a time (one rank tile: 2, else 1; 1 or 3
+// there and 2 for more tiles measured no faster), the next ones' loads in flight while
+// the current ones are multiplied.
+template <int DT, bool VEC, int SIDE, bool BANY, int RT, int NP>
+__device__ __forceinline__ void shrink_sum(floatx4 (&acc)[RT], const ShrinkSide &sd, char *tile, int wave, int lane)
 {
     using E = Elem<DT>;
-    using Tl = ShrinkTile<DT, RT, MB>;
+    using Tl = ShrinkTile<DT, RT>;
     constexpr int kChunk = NP * Tl::kPair, kNext = kShrinkWaves * kChunk;
-    uint32_t xoff[MB][2];
-#pragma unroll
-    for (int b = 0; b < MB; ++b)
+    uint32_t xoff[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) { // rows past n: never stored
-            const uint32_t t = uint32_t(sd.rows[min(16 * b + 8 * h + (lane >> 3), sd.n - 1)]);
-            xoff[b][h] = VEC ? t * uint32_t(sd.ld * int(sizeof(typename E::T))) + 16 * (lane & 7) : t;
+            const uint32_t t = uint32_t(sd.rows[min(8 * h + (lane >> 3), sd.n - 1)]);
+            xoff[h] = VEC ? t * uint32_t(sd.ld * int(sizeof(typename E::T))) + 16 * (lane & 7) : t;
         }
     // pieces of rows of B that hold fewer or other ranks reach up to kVec - 1
     // elements into the rows after, so they keep kVec rows from B's end
     const int last = sd.K - kChunk - (SIDE == 1 && BANY ? E::kVec : 0);
-    ShrinkOps<DT, RT, MB> o[NP];
+    ShrinkOps<DT, RT> o[NP];
     int k = wave * kChunk;
     auto load = [&] {
 #pragma unroll
@@ -432,96 +465,229 @@ __device__ __forceinline__ void shrink_sum(floatx4 (&acc)[MB][RT], const ShrinkS
         }
 }
 
-// A workgroup takes MB blocks of 16 rows of one segment (MB = 4: a chunk), so that
-// A and B are read once for 16 MB rows.
-template <int DT, bool VEC, int RT, int MB>
+// Where the work of launch 1 goes on.  Workgroup b runs on XCD b % 8: an XCD takes a
+// run of consecutive units, so that a segment's A and B are fetched into few L2s;
+// the list of items first (one workgroup), then the longer side.  False: nothing
+// (more) to do here.
+__device__ __forceinline__ bool shrink_unit(const BwdArgs &a, int units, int *scan, int &unit, int &side)
+{
+    const int run = (units + 7) / 8, q = int(blockIdx.x >> 3) - 1;
+    if (q < 0) {
+        if (blockIdx.x == 0) list_items(a, scan, blockDim.x);
+        return false;
+    }
+    unit = int(blockIdx.x % 8) * run + q % run;
+    side = a.sides == 3 ? (q < run) == (a.d_out >= a.d_in) : a.sides - 1;
+    return unit < units;
+}
+
+// A workgroup takes a block of 16 rows; its waves share the long axis.
+template <int DT, bool VEC, int RT>
 __global__ __launch_bounds__(kShrinkWaves * 64) void bwd_shrink_kernel(BwdArgs a)
 {
-    constexpr int W = kShrinkWaves, NP = LORA_NP;
-    constexpr int kTile = NP * ShrinkTile<DT, RT, MB>::kBytes;
+    constexpr int W = kShrinkWaves, NP = RT == 1 ? 2 : 1;
+    constexpr int kTile = NP * ShrinkTile<DT, RT>::kBytes;
     constexpr int kRed = W * RT * 1024, kScan = 3 * 4 * W * 64;
     constexpr int kLds = std::max(std::max(W * kTile, kRed), kScan);
     static_assert(kLds <= 160 * 1024, "LDS budget");
     __shared__ __attribute__((aligned(16))) char lds[kLds];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-    const int units = MB == 1 ? a.nblk : a.nchunk;
-    // Workgroup b runs on XCD b % 8: an XCD takes a run of consecutive units, so
-    // that a segment's A and B are fetched into few L2s; the list of items first
-    // (one workgroup), then the longer side.
-    const int run = (units + 7) / 8, q = int(blockIdx.x >> 3) - 1;
-    if (q < 0) {
-        if (blockIdx.x == 0) list_items(a, reinterpret_cast<int *>(lds), W * 64);
-        return;
-    }
-    const int unit = int(blockIdx.x % 8) * run + q % run;
-    if (unit >= units) return;
-    const int side = a.sides == 3 ? (q < run) == (a.d_out >= a.d_in) : a.sides - 1;
-    const void *pA, *pB;
-    int r, n, p0;
-    float scale;
-    const int32_t *rows;
-    auto take = [&](const auto *d) {
-        pA = reinterpret_cast<const void *>(d->A), pB = reinterpret_cast<const void *>(d->B);
-        r = d->rank, n = d->n, p0 = d->p0, scale = d->scale, rows = d->rows;
-    };
-    if constexpr (MB == 1) take(a.blk + unit);
-    else take(a.chunk + unit);
-    ShrinkSide sd = side ? ShrinkSide{a.dy, pB, a.lddy, a.d_out, r, 0, rows, n} : ShrinkSide{a.x, pA, a.ldx, a.d_in, r, 0, rows, n};
+    int unit, side;
+    if (!shrink_unit(a, a.nblk, reinterpret_cast<int *>(lds), unit, side)) return;
+    const lora_blk_desc *d = a.blk + unit;
+    const int r = d->rank, n = d->n, p0 = d->p0;
+    const float scale = d->scale;
+    const void *mat = reinterpret_cast<const void *>(side ? d->B : d->A);
+    ShrinkSide sd = side ? ShrinkSide{a.dy, mat, a.lddy, a.d_out, r, 0, d->rows, n} : ShrinkSide{a.x, mat, a.ldx, a.d_in, r, 0, d->rows, n};
     const int ntiles = (r + 15) >> 4;
     char *tile = lds + wave * kTile;
 
     for (int rt0 = 0; rt0 < ntiles; rt0 += RT) {
-        floatx4 acc[MB][RT];
+        floatx4 acc[RT];
 #pragma unroll
-        for (int b = 0; b < MB; ++b)
-#pragma unroll
-            for (int i = 0; i < RT; ++i) acc[b][i] = floatx4{};
+        for (int i = 0; i < RT; ++i) acc[i] = floatx4{};
         sd.rt0 = rt0;
-        if (side == 0) shrink_sum<DT, VEC, 0, false, RT, MB, NP>(acc, sd, tile, wave, lane);
-        else if (r % Elem<DT>::kVec) shrink_sum<DT, VEC, 1, true, RT, MB, NP>(acc, sd, tile, wave, lane);
-        else shrink_sum<DT, VEC, 1, false, RT, MB, NP>(acc, sd, tile, wave, lane);
+        if (side == 0) shrink_sum<DT, VEC, 0, false, RT, NP>(acc, sd, tile, wave, lane);
+        else if (r % Elem<DT>::kVec) shrink_sum<DT, VEC, 1, true, RT, NP>(acc, sd, tile, wave, lane);
+        else shrink_sum<DT, VEC, 1, false, RT, NP>(acc, sd, tile, wave, lane);
         // lane l of tile i holds D[row 4 (l / 16) + q][rank l % 16]
         float *red = reinterpret_cast<float *>(lds);
+        __syncthreads(); // every wave is past its tiles, and past the last sums
 #pragma unroll
-        for (int b = 0; b < MB; ++b) {
-            __syncthreads(); // every wave is past its tiles, and past the last sums
+        for (int i = 0; i < RT; ++i) *reinterpret_cast<floatx4 *>(red + ((wave * RT + i) * 64 + lane) * 4) = acc[i];
+        __syncthreads();
+        for (int idx = tid; idx < RT * 256; idx += W * 64) {
+            const int i = idx >> 8, l2 = (idx >> 2) & 63, q4 = idx & 3;
+            float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < RT; ++i) *reinterpret_cast<floatx4 *>(red + ((wave * RT + i) * 64 + lane) * 4) = acc[b][i];
-            __syncthreads();
-            for (int idx = tid; idx < RT * 256; idx += W * 64) {
-                const int i = idx >> 8, l2 = (idx >> 2) & 63, q4 = idx & 3;
-                float sum = 0.f;
+            for (int w = 0; w < W; ++w) sum += red[((w * RT + i) * 64 + l2) * 4 + q4];
+            const int mm = 4 * (l2 >> 4) + q4, t = rt0 + i, jm = l2 & 15, j = 16 * t + jm;
+            if (mm >= n || t >= ntiles) continue;
+            const int p = p0 + mm;
+            const float v = j < r ? sum * scale : 0.f;
+            store_uv<DT>(a, side, p, t, jm, v);
+        }
+        __syncthreads();
+    }
+}
+
+// The same for many long segments (bf16, VEC, ranks above 32, multiples of 8): a
+// workgroup takes a chunk of up to 64 rows, a wave 16 of them and 64 ranks, over the
+// whole long axis.  Stages of 128 bytes of every row come through a ring of LDS tiles
+// filled by direct global-to-LDS loads, kRing - 1 stages ahead, so A and B are read
+// once for 64 rows.  16384 rows of rank 64, d 4096: 98 us (the loads alone 83, the
+// bytes at the copy rate 52; ring of 4: 104), by blocks of 16 rows 125.
+constexpr int kRing = 3;
+
+__device__ const uint32_t g_zeros[4] = {0, 0, 0, 0};
+
+constexpr int waitcnt_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4); } // and lgkmcnt(0)
+
+// 16 bytes per lane to LDS at m0 + 16 lane (published by an explicit vmcnt wait and
+// a barrier; nothing else uses m0).
+__device__ __forceinline__ void dma16(const void *g, uint32_t lds_byte)
+{
+    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(lds_byte) : "memory");
+}
+
+__global__ __launch_bounds__(256) void bwd_shrink_ring_kernel(BwdArgs a)
+{
+    constexpr int RT = 4, kXBytes = 64 * 128, kWBytes = 64 * 128, kStage = kXBytes + kWBytes;
+    constexpr int kDma = 2; // loads of x, and of W, of a wave per stage
+    __shared__ __attribute__((aligned(1024))) char lds[kRing * kStage];
+    static_assert(kRing * kStage >= 3 * 4 * 256, "the list's scan");
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), m = lane & 15, g = lane >> 4;
+    int unit, side;
+    if (!shrink_unit(a, a.nchunk, reinterpret_cast<int *>(lds), unit, side)) return;
+    const lora_chunk_desc *d = a.chunk + unit;
+    const int r = d->rank, n = d->n, p0 = d->p0;
+    const float scale = d->scale;
+    const int K = side ? a.d_out : a.d_in, nst = (K + 63) / 64;
+    const uint32_t lds0 = uint32_t(uintptr_t((__attribute__((address_space(3))) char *)(lds)));
+    const char *zeros = reinterpret_cast<const char *>(g_zeros);
+    // x: instruction 2 wave + j, row 8 i + lane / 8, slot lane % 8 holds unit slot ^ (row % 8)
+    const int un = (lane & 7) ^ (lane >> 3);
+    const char *xp[kDma];
 #pragma unroll
-                for (int w = 0; w < W; ++w) sum += red[((w * RT + i) * 64 + l2) * 4 + q4];
-                const int mm = 16 * b + 4 * (l2 >> 4) + q4, t = rt0 + i, jm = l2 & 15, j = 16 * t + jm;
-                if (mm >= n || t >= ntiles) continue;
-                const int p = p0 + mm;
-                const float v = j < r ? sum * scale : 0.f;
-                char *parts = side ? a.ut : a.vt, *ur = a.ur + (int64_t(p >> 4) * a.nt + t) * kPieces;
-                if constexpr (DT == LORA_BF16) {
-                    const uint32_t h = f32_to_bf16(v);
-                    const bool fin = (h & 0x7f80u) != 0x7f80u; // an infinity or NaN has no rest
-                    const float rest = fin ? v - bf16_to_f32(h) : 0.f;
-                    const uint32_t mid = f32_to_bf16(rest);
-                    const int at = (((p & 31) >> 3) * 16 + jm) * 8 + (p & 7);
-                    uint16_t *o = reinterpret_cast<uint16_t *>(parts + (int64_t(p / kWin) * 3 * a.nt + t) * kPieces) + at;
-                    const int64_t part = int64_t(a.nt) * kPieces / 2;
-                    o[0] = uint16_t(h);
-                    o[part] = uint16_t(mid);
-                    o[2 * part] = uint16_t(f32_to_bf16(rest - bf16_to_f32(mid)));
-                    if (side) {
-                        uint16_t *u = reinterpret_cast<uint16_t *>(ur) + ((jm >> 3) * 16 + (p & 15)) * 8 + (jm & 7);
-                        u[0] = uint16_t(h);
-                        u[2 * 16 * 8] = uint16_t(mid);
+    for (int j = 0; j < kDma; ++j) {
+        const int row = d->rows[min(8 * (2 * wave + j) + (lane >> 3), n - 1)]; // past n: not stored
+        xp[j] = side ? static_cast<const char *>(a.dy) + (int64_t(row) * a.lddy + 8 * un) * 2
+                     : static_cast<const char *>(a.x) + (int64_t(row) * a.ldx + 8 * un) * 2;
+    }
+    for (int rt0 = 0; 16 * rt0 < r; rt0 += RT) {
+        // W: instruction 2 wave + j.  A: as x; B: row k of 8 slots, 32-byte granules
+        // moved as in b_at
+        const char *wp[kDma];
+        int wk[kDma];
+        const int64_t step = side ? int64_t(64) * r * 2 : 128;
+#pragma unroll
+        for (int j = 0; j < kDma; ++j) {
+            const int s = (kDma * wave + j) * 64 + lane;
+            if (side == 0) {
+                const int rank = 16 * rt0 + (s >> 3);
+                wk[j] = 8 * un;
+                wp[j] = reinterpret_cast<const char *>(d->A) + (int64_t(rank < r ? rank : r - 1) * K + 8 * un) * 2;
+            } else {
+                const int k = s >> 3, pos = s & 7, gran = (pos >> 1) ^ ((k >> 1) & 3), rank = 16 * (rt0 + gran) + 8 * (pos & 1);
+                wk[j] = k;
+                wp[j] = reinterpret_cast<const char *>(d->B) + (int64_t(k) * r + (rank < r ? rank : 0)) * 2;
+            }
+        }
+        auto issue = [&](int i) {
+            const uint32_t xbase = lds0 + uint32_t((i % kRing) * kStage + wave * kDma * 1024);
+            const uint32_t wbase = lds0 + uint32_t((i % kRing) * kStage + kXBytes + wave * kDma * 1024);
+            const int k0 = 64 * i;
+            // past K (the last stage, and stages past the last): zeros
+#pragma unroll
+            for (int j = 0; j < kDma; ++j) dma16(k0 + 8 * un < K ? xp[j] + int64_t(k0) * 2 : zeros, xbase + j * 1024);
+#pragma unroll
+            for (int j = 0; j < kDma; ++j) dma16(k0 + wk[j] < K ? wp[j] + i * step : zeros, wbase + j * 1024);
+        };
+        floatx4 acc[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) acc[i] = floatx4{};
+#pragma unroll
+        for (int i = 0; i < kRing - 1; ++i) issue(i);
+        for (int i = 0; i < nst; ++i) {
+            // this wave's loads of stage i are done, then every wave's, and every wave
+            // has read stage i - 1
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(waitcnt_vm(2 * kDma * (kRing - 2)));
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            issue(i + kRing - 1);
+            const char *xt = lds + (i % kRing) * kStage + wave * 2048, *wt = lds + (i % kRing) * kStage + kXBytes;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int at = m * 128 + (((4 * s + g) ^ (m & 7)) << 4);
+                const bf16x8 xf = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(xt + at));
+#pragma unroll
+                for (int q = 0; q < RT; ++q) {
+                    bf16x8 wf;
+                    if (side == 0) {
+                        wf = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(wt + q * 2048 + at));
+                    } else {
+                        u32x2 t[2];
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) t[b] = read_tr(wt + b_at<LORA_BF16, RT>(32 * s + 8 * g + 4 * b + (m >> 2), 32 * q + 8 * (m & 3)));
+                        wf = join8(t[0], t[1]);
                     }
-                } else {
-                    float *o = reinterpret_cast<float *>(parts + ((int64_t(p / kWin) * 2 + ((p & 31) >> 4)) * a.nt + t) * kPieces);
-                    o[(((p & 15) >> 2) * 16 + jm) * 4 + (p & 3)] = v;
-                    if (side) reinterpret_cast<float *>(ur)[((jm >> 2) * 16 + (p & 15)) * 4 + (jm & 3)] = v;
+                    acc[q] = mma<LORA_BF16>(xf, wf, acc[q]);
                 }
             }
         }
+        // no direct load may still be writing the ring, and every wave is past its reads
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        // u or v through LDS, so that whole 16-byte pieces of the operands are stored
+        // (by single values: 14 us more for 16384 rows of rank 64)
+        constexpr int kPitch = 16 * RT + 1;
+        static_assert(64 * kPitch * 4 <= kRing * kStage, "the sums fit the ring");
+        float *sum = reinterpret_cast<float *>(lds);
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                sum[(16 * wave + 4 * g + q) * kPitch + 16 * i + m] = 16 * (rt0 + i) + m < r ? acc[i][q] * scale : 0.f;
         __syncthreads();
+        const int cols = min(16 * RT, ((r + 15) & ~15) - 16 * rt0), oct0 = p0 >> 3, octs = ((p0 + n - 1) >> 3) - oct0 + 1;
+        const int64_t part = int64_t(a.nt) * kPieces / 2;
+        for (int idx = tid; idx < octs * cols; idx += 256) {
+            const int oct = idx / cols, j = idx - oct * cols, p = 8 * (oct0 + oct), row = p - p0;
+            uint16_t *o = reinterpret_cast<uint16_t *>((side ? a.ut : a.vt) + (int64_t(p / kWin) * 3 * a.nt + rt0 + (j >> 4)) * kPieces) +
+                          (((p & 31) >> 3) * 16 + (j & 15)) * 8;
+            if (row >= 0 && row + 8 <= n) {
+                u32x4 w[3];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const Parts f0 = parts_of(sum[(row + 2 * e) * kPitch + j]), f1 = parts_of(sum[(row + 2 * e + 1) * kPitch + j]);
+                    w[0][e] = f0.h | f1.h << 16, w[1][e] = f0.mid | f1.mid << 16, w[2][e] = f0.low | f1.low << 16;
+                }
+#pragma unroll
+                for (int q = 0; q < 3; ++q) *reinterpret_cast<u32x4 *>(o + q * part) = w[q];
+            } else {
+                for (int e = max(0, -row); e < 8 && row + e < n; ++e) {
+                    const Parts f = parts_of(sum[(row + e) * kPitch + j]);
+                    o[e] = uint16_t(f.h), o[part + e] = uint16_t(f.mid), o[2 * part + e] = uint16_t(f.low);
+                }
+            }
+        }
+        if (side)
+            for (int idx = tid; idx < n * (cols >> 3); idx += 256) {
+                const int c8 = idx / n, row = idx - c8 * n, p = p0 + row;
+                uint16_t *u = reinterpret_cast<uint16_t *>(a.ur + (int64_t(p >> 4) * a.nt + rt0 + (c8 >> 1)) * kPieces) +
+                              ((c8 & 1) * 16 + (p & 15)) * 8;
+                u32x4 w[2];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const Parts f0 = parts_of(sum[row * kPitch + 8 * c8 + 2 * e]), f1 = parts_of(sum[row * kPitch + 8 * c8 + 2 * e + 1]);
+                    w[0][e] = f0.h | f1.h << 16, w[1][e] = f0.mid | f1.mid << 16;
+                }
+                *reinterpret_cast<u32x4 *>(u) = w[0];
+                *reinterpret_cast<u32x4 *>(u + 2 * 16 * 8) = w[1];
+            }
+        __syncthreads(); // the next ranks' stages overwrite the sums
     }
 }
 
@@ -677,7 +843,7 @@ __device__ __forceinline__ void grad_mma(GradOps<DT, RT> &o, floatx4 (&acc)[4][R
 
 template <int DT, bool VEC, bool WHOLE, int RT>
 __device__ __forceinline__ void grad_item(const BwdArgs &a, const GradSide &sd, int side, int begin, int end, int c0, int rt0,
-                                          int r, float *dst, bool add, const int32_t *tok, char *tile, int lane)
+                                          int r, float *dst, bool add, bool stream, const int32_t *tok, char *tile, int lane)
 {
     const int w1 = (end - 1) / kWin;
     floatx4 acc[4][RT];
@@ -704,11 +870,23 @@ __device__ __forceinline__ void grad_item(const BwdArgs &a, const GradSide &sd, 
     // gradient; 16 ranks x 64 columns turn in the wave's tile, so that they leave
     // with 16 bytes from each of 16 (dB: 4) adjacent lanes for a row.
     const int m = lane & 15, g = lane >> 4;
+    const gfloat gdst = (gfloat)dst; // (generic stores would be waited for with the tile's reads)
     const bool vec = (reinterpret_cast<uintptr_t>(dst) & 15) == 0 && ((side ? r : sd.D) & 3) == 0;
-    auto put4 = [&](float *o, const floatx4 &v, int n) {
+    auto put4 = [&](gfloat o, const floatx4 &v, int n) {
         if (n <= 0) return;
         if (vec) { // n is a multiple of 4
-            *reinterpret_cast<floatx4 *>(o) = add ? *reinterpret_cast<const floatx4 *>(o) + v : v;
+            const floatx4 f = add ? *(gfloatx4)o + v : v;
+            // Gradients are not read here again, partial sums are (200 adapters of 5
+            // rows, d_out 12288: 55 us with plain stores, 46 so; ranks up to 64 over 128
+            // adapters, 72 and 82: plain there).  The two empty statements keep the
+            // compiler from making the two stores one.
+            if (stream) {
+                asm volatile("");
+                __builtin_nontemporal_store(f, (gfloatx4)o);
+                asm volatile("");
+            } else {
+                *(gfloatx4)o = f;
+            }
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -725,7 +903,7 @@ __device__ __forceinline__ void grad_item(const BwdArgs &a, const GradSide &sd, 
             for (int h = 0; h < 4; ++h) {
                 const int j = 4 * h + g, c = c0 + 4 * m;
                 const floatx4 v = *reinterpret_cast<const floatx4 *>(tile + j * kOutPitch + 16 * m);
-                if (j0 + j < r) put4(dst + int64_t(j0 + j) * sd.D + c, v, sd.D - c);
+                if (j0 + j < r) put4(gdst + int64_t(j0 + j) * sd.D + c, v, sd.D - c);
             }
         } else {
             // rows of 64 bytes, unit un of row q in slot un ^ (q / 2 % 4)
@@ -735,7 +913,7 @@ __device__ __forceinline__ void grad_item(const BwdArgs &a, const GradSide &sd, 
             for (int h = 0; h < 4; ++h) {
                 const int q = 16 * h + (lane >> 2), un = lane & 3, j = j0 + 4 * un;
                 const floatx4 v = *reinterpret_cast<const floatx4 *>(tile + q * 64 + ((un ^ ((q >> 1) & 3)) << 4));
-                if (c0 + q < sd.D) put4(dst + int64_t(c0 + q) * r + j, v, r - j);
+                if (c0 + q < sd.D) put4(gdst + int64_t(c0 + q) * r + j, v, r - j);
             }
         }
     }
@@ -769,10 +947,10 @@ __device__ __forceinline__ void grad_unit(const BwdArgs &a, int id, char *tiles_
         constexpr bool W = decltype(whole)::value;
         const int left = r - 64 * group;
         if (RT >= 4 && left > 32)
-            grad_item<DT, VEC, W, RT >= 4 ? 4 : 1>(a, sd, side, it.begin, it.end, c0, 4 * group, r, dst, add, tok, tile, lane);
+            grad_item<DT, VEC, W, RT >= 4 ? 4 : 1>(a, sd, side, it.begin, it.end, c0, 4 * group, r, dst, add, RT < 4 && it.slot < 0, tok, tile, lane);
         else if (RT >= 2 && left > 16)
-            grad_item<DT, VEC, W, RT >= 2 ? 2 : 1>(a, sd, side, it.begin, it.end, c0, 4 * group, r, dst, add, tok, tile, lane);
-        else grad_item<DT, VEC, W, 1>(a, sd, side, it.begin, it.end, c0, 4 * group, r, dst, add, tok, tile, lane);
+            grad_item<DT, VEC, W, RT >= 2 ? 2 : 1>(a, sd, side, it.begin, it.end, c0, 4 * group, r, dst, add, RT < 4 && it.slot < 0, tok, tile, lane);
+        else grad_item<DT, VEC, W, 1>(a, sd, side, it.begin, it.end, c0, 4 * group, r, dst, add, RT < 4 && it.slot < 0, tok, tile, lane);
     };
     if constexpr (VEC || DT == LORA_F32) ranks(std::true_type{});
     else if (c0 + 64 <= sd.D) ranks(std::true_type{});
@@ -1048,19 +1226,21 @@ Layout layout_of(int32_t rows, int32_t d_in, int32_t d_out, int32_t max_rank)
     return l;
 }
 
-template <int DT, bool VEC, int MB> void run_shrink_mb(hipStream_t s, const BwdArgs &a, unsigned units, unsigned nside)
+template <int DT, bool VEC> void run_shrink(hipStream_t s, const BwdArgs &a, unsigned nside, bool ranks8)
 {
-    const dim3 grid((units + 7) / 8 * nside * 8 + 8), block(kShrinkWaves * 64);
-    if (a.nt <= 1) launch_kernel(bwd_shrink_kernel<DT, VEC, 1, MB>, grid, block, 0, s, a);
-    else if (a.nt <= 2) launch_kernel(bwd_shrink_kernel<DT, VEC, 2, MB>, grid, block, 0, s, a);
-    else launch_kernel(bwd_shrink_kernel<DT, VEC, 4, MB>, grid, block, 0, s, a);
-}
-// 64 rows per workgroup when that still gives every CU two of them.
-template <int DT, bool VEC> void run_shrink(hipStream_t s, const BwdArgs &a, int nside)
-{
-    if (VEC && DT == LORA_BF16 && int64_t(a.nchunk) * nside >= 512)
-        run_shrink_mb<DT, VEC, VEC && DT == LORA_BF16 ? 4 : 1>(s, a, unsigned(a.nchunk), unsigned(nside));
-    else run_shrink_mb<DT, VEC, 1>(s, a, unsigned(a.nblk), unsigned(nside));
+    // The ring where 64-row workgroups fill the chip and are mostly whole: d 4096,
+    // ring / blocks of 16 rows, us.  Rank 64: 4096 rows 41 / 41, 8192 54 / 66, 16384
+    // 98 / 125, 32768 159 / 231; rank 32: 44 / 42, 84 / 80, 146 / 151 from 8192 rows;
+    // rank 16: 78 / 67 for 16384.
+    if (DT == LORA_BF16 && VEC && ranks8 && a.nt > 2 && int64_t(a.nchunk) * nside >= 256 && a.Tp / a.nchunk >= 32) {
+        const dim3 grid((unsigned(a.nchunk) + 7) / 8 * nside * 8 + 8), block(256);
+        launch_kernel(bwd_shrink_ring_kernel, grid, block, 0, s, a);
+        return;
+    }
+    const dim3 grid((unsigned(a.nblk) + 7) / 8 * nside * 8 + 8), block(kShrinkWaves * 64);
+    if (a.nt <= 1) launch_kernel(bwd_shrink_kernel<DT, VEC, 1>, grid, block, 0, s, a);
+    else if (a.nt <= 2) launch_kernel(bwd_shrink_kernel<DT, VEC, 2>, grid, block, 0, s, a);
+    else launch_kernel(bwd_shrink_kernel<DT, VEC, 4>, grid, block, 0, s, a);
 }
 template <int DT, bool VEC> void run_out(hipStream_t s, const BwdArgs &a, dim3 grid)
 {
@@ -1138,10 +1318,12 @@ int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p
     a.groups = (a.nt + 3) / 4;
     a.span = span_of(h->num_sorted, h->num_segments, int64_t(a.tiles) * a.groups);
     const lora_seg_desc *hs = reinterpret_cast<const lora_seg_desc *>(reinterpret_cast<const char *>(h) + h->seg_offset);
+    bool ranks8 = true;
     for (int i = 0; i < h->num_segments; ++i) {
         const int n = (hs[i].start + hs[i].len - 1) / a.span - hs[i].start / a.span + 1;
         a.nitems += n;
         a.nsplit += n > 1;
+        ranks8 = ranks8 && hs[i].rank % 8 == 0;
     }
 
     if (a.nsplit > 65535) return fail(LORA_ERR_ARG, "backward: %d segments over several spans (> 65535)", a.nsplit);
@@ -1153,11 +1335,11 @@ int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p
 
     const bool bf16 = b.dtype == LORA_BF16;
     const bool vec = b.vec_x && b.vec_dy && (!a.dx || b.vec_dx);
-    const int nside = a.sides == 3 ? 2 : 1;
-    if (bf16 && vec) run_shrink<LORA_BF16, true>(s, a, nside);
-    else if (bf16) run_shrink<LORA_BF16, false>(s, a, nside);
-    else if (vec) run_shrink<LORA_F32, true>(s, a, nside);
-    else run_shrink<LORA_F32, false>(s, a, nside);
+    const unsigned nside = a.sides == 3 ? 2 : 1;
+    if (bf16 && vec) run_shrink<LORA_BF16, true>(s, a, nside, ranks8);
+    else if (bf16) run_shrink<LORA_BF16, false>(s, a, nside, ranks8);
+    else if (vec) run_shrink<LORA_F32, true>(s, a, nside, ranks8);
+    else run_shrink<LORA_F32, false>(s, a, nside, ranks8);
     int st = checked("backward shrink");
     if (st || ngrad + ndx == 0) return st;
     const dim3 grid{unsigned(ngrad + ndx)};

@@ -67,6 +67,26 @@ def test_against_64_bits(dtype, T, d_in, d_out, ranks, kind):
     check(p, d, f"{dtype} T={T}")
 
 
+LONG = [  # enough 64-row pieces to fill the chip: ranks of one, two and more tiles
+    (8400, 72, 136, [16, 8], "runs"),
+    (8600, 136, 64, [32, 8, 24], "mixed"),
+    (8777, 200, 72, [64, 8, 40], "runs"),
+    (8500, 64, 264, [72, 128, 256], "mixed"),
+    (8448, 8, 8, [48], "one"),
+    (8300, 128, 192, [20, 64], "runs"),
+]
+
+
+@pytest.mark.parametrize("T,d_in,d_out,ranks,kind", LONG)
+def test_many_long_segments(T, d_in, d_out, ranks, kind):
+    say(f"case backward long T={T} {d_in}->{d_out} ranks={ranks} {kind}")
+    p = Problem("bf16", ids_of(kind, T, len(ranks), T), ranks, d_in, d_out, seed=T)
+    d = p.device()
+    call(p, d)
+    torch.cuda.synchronize()
+    check(p, d, f"long T={T}")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("pad,misalign", [((8, 16, 24), 0), ((3, 1, 2), 0), ((0, 0, 5), 0), ((0, 0, 0), 1), ((8, 8, 8), 8)])
 def test_pitches_and_alignment(dtype, pad, misalign):
