@@ -661,8 +661,8 @@ int lora_fused_linear_e4m3(void *stream, const void *x, int64_t ldx, int32_t d_i
  *     dA_i   = sum over t with a(t) = i of u[t]^T x[t]     [r_i, d_in]
  *     dB_i   = sum over t with a(t) = i of dy[t]^T v[t]    [d_out, r_i]
  *   x, dy            the forward's input and the gradient of its output, of the
- *                    call's dtype, any row pitch; 16-byte aligned rows of whole
- *                    16-byte pieces take the fast loads
+ *                    call's dtype, any row pitch (16-byte aligned rows of whole
+ *                    16-byte pieces are read fastest)
  *   grad_A_dev,      device tables [n_adapters] of fp32 gradient addresses
  *   grad_B_dev       (4-byte aligned; A's gradient contiguous [r_i, d_in], B's
  *                    [d_out, r_i]); an entry of 0 leaves that gradient out, a
@@ -679,7 +679,7 @@ int lora_fused_linear_e4m3(void *stream, const void *x, int64_t ldx, int32_t d_i
  * Every sum has a fixed order: results are the same from run to run.
  * Needs ws_bytes >= lora_workspace_bytes(LORA_OP_SGMV_BACKWARD, T, d_in, d_out,
  * max_rank), T and max_rank as in lora_sgmv; the workspace needs no preparation.
- * Two to four launches; capturable; calls that share a workspace must be ordered
+ * Two or three launches; capturable; calls that share a workspace must be ordered
  * on one stream.
  * Errors: LORA_ERR_ARG, LORA_ERR_DTYPE, LORA_ERR_ALIGN, LORA_ERR_PLAN,
  * LORA_ERR_ADAPTER_ID (the segments use an adapter >= n_adapters),
@@ -757,7 +757,8 @@ size_t lora_adamw_plan_bytes(const lora_adam_tensor *tensors, int32_t n_tensors)
 /* Build the plan of a list of tensors in host memory (16-byte aligned; pinned
  * for the upload).  grad_dtype: LORA_F32 or LORA_BF16, of every gradient.  No
  * GPU call.
- * Errors: LORA_ERR_ARG (also: two tensors share memory that the step writes),
+ * Errors: LORA_ERR_ARG (also: two tensors, or a tensor and a gradient, share
+ * memory that the step writes; gradients may share theirs),
  * LORA_ERR_DTYPE, LORA_ERR_ALIGN, LORA_ERR_WORKSPACE. */
 int lora_adamw_plan(const lora_adam_tensor *tensors, int32_t n_tensors, int32_t n_groups, int state, int grad_dtype,
                     void *plan_host, size_t plan_bytes);

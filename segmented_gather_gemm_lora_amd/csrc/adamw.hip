@@ -437,6 +437,15 @@ int lora_adamw_plan(const lora_adam_tensor *tensors, int32_t n_tensors, int32_t 
         if (ranges[k].lo < ranges[k - 1].hi)
             return fail(LORA_ERR_ARG, "tensors %d and %d share memory that is written",
                         std::min(ranges[k].tensor, ranges[k - 1].tensor), std::max(ranges[k].tensor, ranges[k - 1].tensor));
+    // gradients are read by one workgroup while others write: they may share memory
+    // with each other, not with what is written
+    for (int32_t i = 0; i < n_tensors; ++i) {
+        const uint64_t lo = tensors[i].grad, hi = lo + (grad_dtype == LORA_BF16 ? 2 : 4) * uint64_t(tensors[i].n);
+        // the last written range that starts below hi ends last too
+        auto it = std::lower_bound(ranges.begin(), ranges.end(), hi, [](const Range &r, uint64_t at) { return r.lo < at; });
+        if (hi > lo && it != ranges.begin() && (--it)->hi > lo)
+            return fail(LORA_ERR_ARG, "the gradient of tensor %d shares memory with what is written of tensor %d", i, it->tensor);
+    }
     const int chunk = chunk_of(elements_of(tensors, n_tensors), eight);
     const int64_t n_chunks = chunks_of(tensors, n_tensors, chunk);
     const size_t need = sizeof(AdamHeader) + sizeof(AdamChunk) * size_t(n_chunks);
