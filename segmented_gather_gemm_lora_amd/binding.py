@@ -499,21 +499,21 @@ def _torch():
     return torch
 
 
-def _stream_handle(stream) -> Optional[int]:
+def _stream_handle(stream, device: Optional[int] = None) -> Optional[int]:
     if stream is None:
-        return _current_stream()
+        return _current_stream(device)
     return stream.cuda_stream
 
 
-def _current_stream() -> int:
-    """The current device's current stream, without building a stream object
-    (2.5 us of a call whose kernel takes 4)."""
+def _current_stream(device: Optional[int] = None) -> int:
+    """The current stream of the device (None: the current one), without building a
+    stream object (2.5 us of a call whose kernel takes 4)."""
     global _RAW_STREAM
     torch = _torch()
     if _RAW_STREAM is None:
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _RAW_STREAM = raw if raw is not None else lambda device: torch.cuda.current_stream(device).cuda_stream
-    return _RAW_STREAM(torch.cuda.current_device())
+    return _RAW_STREAM(torch.cuda.current_device() if device is None else device)
 
 
 def _ptr(t) -> Optional[int]:
@@ -1086,13 +1086,39 @@ def fused_linear_e4m3(x, W0, w0_scale: float, plan: Plan, y, ws, stream=None):
            "lora_fused_linear_e4m3")
 
 
+def _gradient_rows(dtype: str, tokens: int, tables, dy, *more) -> int:
+    """Refuses what the C call cannot see: matrices (dy, then pairs of one, or None,
+    and its columns) of another type, shape or device than the call's.  The device."""
+    torch = _torch()
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    device = torch.cuda.current_device() if dy.get_device() >= 0 else -1
+    for t, cols in ((dy, 0), *more):
+        if t is None:
+            continue
+        n, d = t.shape
+        if t.get_device() != device or device < 0:
+            raise ValueError(f"a tensor of {tuple(t.shape)} is not on the current device")
+        if n < tokens or (d != cols and cols) or t.dtype is not dt or (d > 1 and t.stride(1) != 1):
+            raise ValueError(f"{tokens} rows of {cols or d} adjacent elements of {dt} are wanted, not {tuple(t.shape)} of {t.dtype}")
+    if tables is not None and tables.addr_A_dev.get_device() != device:
+        raise ValueError("grads are not on the current device")
+    return device
+
+
 def sgmv_backward(x, dy, plan: Plan, grads: Optional[GradPool], dx, ws, dtype: str, accumulate: bool = False,
                   stream=None):
     """Gradients of sgmv: dx[perm] += u A (dx None: not wanted), grads.A = u^T x,
     grads.B = dy^T v over each adapter's rows (added to them with accumulate;
-    grads None: not wanted)."""
-    d_in = (dx if x is None else x).shape[1]
-    _check(load().lora_sgmv_backward(_stream_handle(stream), DTYPES[dtype], _ptr(x), d_in if x is None else x.stride(0),
+    grads None: not wanted).  The gradients have the shapes of the adapters that
+    the plan was built with."""
+    if x is not None or dx is not None:
+        d_in = (dx if x is None else x).shape[-1]
+    elif grads is not None:
+        raise ValueError("x is None")
+    else:
+        return  # nothing is wanted
+    device = _gradient_rows(dtype, plan.h.batch_tokens, grads, dy, (x, d_in), (dx, d_in))
+    _check(load().lora_sgmv_backward(_stream_handle(stream, device), DTYPES[dtype], _ptr(x), d_in if x is None else x.stride(0),
                                      d_in, _ptr(dy), dy.stride(0), dy.shape[1], plan.seg,
                                      _ptr(grads and grads.addr_A_dev), _ptr(grads and grads.addr_B_dev),
                                      grads.n_adapters if grads else 0, LORA_GRAD_ACCUMULATE if accumulate else 0,
@@ -1105,8 +1131,12 @@ def fused_linear_backward(x, W0, dy, plan: Plan, grads: Optional[GradPool], dx, 
                           accumulate: bool = False, stream=None):
     """Gradients of fused_linear: dx = dy W0 + u A (overwritten, every row), and the
     adapters' gradients as in sgmv_backward (grads None: not wanted; x may then be None)."""
-    d_in = W0.shape[1]
-    _check(load().lora_fused_linear_backward(_stream_handle(stream), DTYPES[dtype], _ptr(x),
+    d_out, d_in = W0.shape
+    if not W0.is_contiguous():
+        raise ValueError("W0 is contiguous [d_out, d_in]")
+    device = _gradient_rows(dtype, plan.h.batch_tokens, grads, dy, (dy, d_out), (x, d_in), (dx, d_in))
+    _gradient_rows(dtype, d_out, None, W0)
+    _check(load().lora_fused_linear_backward(_stream_handle(stream, device), DTYPES[dtype], _ptr(x),
                                              d_in if x is None else x.stride(0), d_in, _ptr(W0), _ptr(dy), dy.stride(0),
                                              dy.shape[1], plan.seg, _ptr(grads and grads.addr_A_dev),
                                              _ptr(grads and grads.addr_B_dev), grads.n_adapters if grads else 0,
@@ -1145,7 +1175,7 @@ class AdamW:
         torch = _torch()
         if state not in ("f32", "8bit"):
             raise ValueError("state is 'f32' or '8bit'")
-        eight, device = state == "8bit", params[0].device if params else "cuda"
+        eight, device = state == "8bit", params[0].device if params else hyper.device
         made = lambda given, size, dt: given if given is not None else [  # noqa: E731
             torch.zeros(size(p.numel()), dtype=dt, device=p.device) for p in params]
         blocks = lambda n: (n + ADAM_BLOCK - 1) // ADAM_BLOCK  # noqa: E731
@@ -1159,6 +1189,8 @@ class AdamW:
             raise ValueError("gradients are fp32 or bf16")
         if hyper.dtype != torch.int32 or hyper.dim() != 2 or hyper.shape[1] != 8 or not hyper.is_contiguous():
             raise ValueError("hyper is the int32 [n_groups, 8] table of adamw_hyper")
+        if not hyper.is_cuda or hyper.device != device or hyper.get_device() != torch.cuda.current_device():
+            raise ValueError("params and hyper are on the current device")
         n = len(self.params)
         sdt = torch.uint8 if eight else torch.float32
         lists = [("params", self.params, torch.float32, None), ("grads", self.grads, gdt, None),
@@ -1170,8 +1202,8 @@ class AdamW:
                 raise ValueError(f"{name} and groups list one entry for each parameter")
             for t, p in zip(ts, self.params):
                 want = size(p.numel()) if size else p.numel()
-                if t.dtype != dt or t.numel() != want or not t.is_contiguous() or t.device != p.device:
-                    raise ValueError(f"{name}: contiguous {dt} tensors of {want} elements on the parameter's device")
+                if t.dtype != dt or t.numel() != want or not t.is_contiguous() or t.device != device:
+                    raise ValueError(f"{name}: contiguous {dt} tensors of {want} elements on the device of hyper")
         arr = (LoraAdamTensor * max(n, 1))()
         for i, p in enumerate(self.params):
             arr[i] = LoraAdamTensor(_ptr(p), _ptr(self.grads[i]), _ptr(copies[i]) if copies is not None else 0,
@@ -1186,12 +1218,14 @@ class AdamW:
                "lora_adamw_plan")
         _check(lib.lora_adamw_upload(_ptr(self._host), _ptr(self._dev), nbytes, _stream_handle(stream)),
                "lora_adamw_upload")
-        self._fn = lib.lora_adamw
+        self._fn, self._device = lib.lora_adamw, hyper.get_device()
         self._args = (_vp(_ptr(self._host)), _vp(_ptr(self._dev)), _vp(_ptr(hyper)), _i32(hyper.shape[0]))
 
     def step(self, stream=None):
         """One step of every tensor, with the numbers that `hyper` holds on the device."""
-        st = self._fn(_stream_handle(stream), *self._args)
+        if self._device != _torch().cuda.current_device():
+            raise ValueError("the tensors are not on the current device")
+        st = self._fn(_stream_handle(stream, self._device), *self._args)
         if st:
             _check(st, "lora_adamw")
 
@@ -1199,7 +1233,17 @@ class AdamW:
 def adamw_state_values(m, m_scale, v, v_scale, m_out, v_out, stream=None):
     """bf16 values of 8-bit states: flat code tensors (uint8), their scales (one
     for each 256 elements) and bf16 outputs; m or v may be None."""
+    torch = _torch()
+    if m is None and v is None:
+        return
     n = (v if m is None else m).numel()
+    sides = [s for s in ((m, m_scale, m_out), (v, v_scale, v_out)) if s[0] is not None]
+    for side in sides:
+        for t, dt, size in zip(side, (torch.uint8, torch.uint8, torch.bfloat16), (n, (n + ADAM_BLOCK - 1) // ADAM_BLOCK, n)):
+            if t is None or t.dtype != dt or t.numel() < size or not t.is_contiguous():
+                raise ValueError(f"contiguous codes (uint8) and values (bf16) of {n} elements, one scale for each {ADAM_BLOCK}")
+    if any(t.get_device() < 0 or t.get_device() != torch.cuda.current_device() for side in sides for t in side):
+        raise ValueError("the states are not on the current device")
     _check(load().lora_adam_state_values(_stream_handle(stream), n, _ptr(m), _ptr(m_scale), _ptr(v), _ptr(v_scale),
                                          _ptr(m_out), _ptr(v_out)), "lora_adam_state_values")
 

@@ -78,6 +78,42 @@ def test_fp32_states_need_no_scales_and_shared_gradients_are_fine():
     assert st == "LORA_OK"
 
 
+@pytest.mark.parametrize("tensors,gdt", [
+    ([tensor(0), tensor(1, grad=FX + 3984)], 0),  # the other's gradient starts in a parameter's last 16 bytes
+    ([tensor(0), tensor(1, grad=FX + 0x30000 - 16)], 0),  # ... ends in the other's m
+    ([tensor(0, grad=FX)], 0),  # its own parameter
+    ([tensor(0), tensor(1, n=9, grad=FX + 0x51000 - 16)], 1),  # 18 bytes of bf16, the last 2 in v's scales
+])
+def test_gradients_in_written_memory(tensors, gdt):
+    st, *_ = plan(tensors, gdt=gdt)
+    assert st == "LORA_ERR_ARG" and "gradient" in B.last_error()
+
+
+def test_gradients_next_to_written_memory():
+    st, *_ = plan([tensor(0), tensor(1, n=8, grad=FX + 0x51000 - 16), tensor(2, n=0, grad=FX)], gdt=1)
+    assert st == "LORA_OK"
+
+
+def test_binding_refuses_host_tensors():
+    import torch
+
+    host = torch.zeros(16)
+    hyper = B.adamw_hyper(1, device="cpu")
+    with pytest.raises(ValueError, match="device"):
+        B.AdamW([host], [host], [0], hyper)
+    with pytest.raises(ValueError, match="device"):
+        B.AdamW([], [], [], hyper)
+    codes, scale, out = torch.zeros(300, dtype=torch.uint8), torch.zeros(2, dtype=torch.uint8), torch.zeros(300).bfloat16()
+    with pytest.raises(ValueError, match="device"):
+        B.adamw_state_values(codes, scale, None, None, out, None)
+    with pytest.raises(ValueError, match="scale"):
+        B.adamw_state_values(codes, scale[:1], None, None, out, None)
+    with pytest.raises(ValueError, match="scale"):
+        B.adamw_state_values(None, None, codes, scale, None, out[:299])
+    with pytest.raises(ValueError, match="scale"):
+        B.adamw_state_values(codes, scale, None, None, out.float(), None)
+
+
 def test_step_refusals():
     L = B.load()
     st, raw, ptr, need = plan([tensor()])

@@ -173,6 +173,59 @@ def test_gradient_pool_checks():
         B.GradPool.from_tensors([None], [])
 
 
+class _Rows:
+    """What the binding looks at of a matrix on a device that is not here."""
+
+    def __init__(self, shape, device=0, dtype=None, inner=1):
+        import torch
+
+        self.shape, self.dtype, self._d, self._inner = shape, dtype or torch.bfloat16, device, inner
+
+    dim = lambda self: len(self.shape)  # noqa: E731
+    get_device = lambda self: self._d  # noqa: E731
+    stride = lambda self, i: self._inner if i else self.shape[1]  # noqa: E731
+    is_contiguous = lambda self: True  # noqa: E731
+
+
+class _Plan:
+    class h:
+        batch_tokens = 4
+
+
+@pytest.mark.parametrize("fused", [False, True])
+@pytest.mark.parametrize("kw", [
+    dict(x=_Rows((4, 64), device=1)), dict(dy=_Rows((4, 32), device=1)), dict(dx=_Rows((4, 64), device=-1)),
+    dict(dy=_Rows((4, 32), device=-1)), dict(x=_Rows((3, 64))), dict(dx=_Rows((3, 64))), dict(dy=_Rows((3, 32))),
+    dict(dx=_Rows((4, 65))), dict(x=_Rows((4, 64, 1))), dict(x=_Rows((4, 64), inner=2)), dict(dtype="f32"),
+])
+def test_binding_refuses_what_the_call_cannot_see(fused, kw, monkeypatch):
+    import torch
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    a = dict(x=_Rows((4, 64)), dy=_Rows((4, 32)), dx=_Rows((4, 64)), W0=_Rows((32, 64)), dtype="bf16")
+    a.update(kw)
+    with pytest.raises(ValueError):
+        if fused:
+            B.fused_linear_backward(a["x"], a["W0"], a["dy"], _Plan, None, a["dx"], None, a["dtype"])
+        else:
+            B.sgmv_backward(a["x"], a["dy"], _Plan, None, a["dx"], None, a["dtype"])
+
+
+def test_binding_refuses_other_weights_and_missing_x(monkeypatch):
+    import torch
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    x, dy = _Rows((4, 64)), _Rows((4, 32))
+    for W0 in (_Rows((31, 64)), _Rows((32, 72)), _Rows((32, 64), device=1), _Rows((32, 64), dtype=torch.float32)):
+        with pytest.raises(ValueError):
+            B.fused_linear_backward(x, W0, dy, _Plan, None, x, None)
+    with pytest.raises(ValueError, match="x is None"):
+        B.sgmv_backward(None, dy, _Plan, B.GradPool([], [], [], x, x), None, None, "bf16")
+    with pytest.raises(ValueError, match="grads"):
+        B.sgmv_backward(x, dy, _Plan, B.GradPool([], [], [], _Rows((1, 1), device=1), x), None, None, "bf16")
+    assert B.sgmv_backward(None, dy, _Plan, None, None, None, "bf16") is None  # nothing wanted
+
+
 def test_header_and_binding_agree():
     assert B.LORA_OP_SGMV_BACKWARD == 7 and B.LORA_GRAD_ACCUMULATE == 1
     assert ctypes.sizeof(ctypes.c_uint) == 4
