@@ -829,7 +829,9 @@ static int make_backward_args(int dtype, const void *x, int64_t ldx, int32_t d_i
 {
     const int es = esize_of(dtype);
     if (flags & ~LORA_GRAD_ACCUMULATE) return fail(LORA_ERR_ARG, "unknown flags %#x", flags);
-    if (d_in < 1 || d_out < 1) return fail(LORA_ERR_ARG, "d_in %d or d_out %d < 1", d_in, d_out);
+    // 16 rows of A or B stay below 2^32 bytes, columns of the last tile below 2^31
+    if (d_in < 1 || d_out < 1 || d_in > (1 << 24) || d_out > (1 << 24))
+        return fail(LORA_ERR_ARG, "d_in %d or d_out %d outside [1, 2^24]", d_in, d_out);
     if (n_adapters < 0) return fail(LORA_ERR_ARG, "n_adapters %d < 0", n_adapters);
     const bool grads = grad_A_dev || grad_B_dev;
     if (!dy) return fail(LORA_ERR_ARG, "dy is NULL");

@@ -35,6 +35,8 @@ def run(plan, **kw):
     (dict(dy=None), "LORA_ERR_ARG"),
     (dict(d_in=0), "LORA_ERR_ARG"),
     (dict(d_out=-1), "LORA_ERR_ARG"),
+    (dict(d_in=(1 << 24) + 1, ldx=1 << 25, lddx=1 << 25), "LORA_ERR_ARG"),
+    (dict(d_out=(1 << 24) + 8, lddy=1 << 25), "LORA_ERR_ARG"),
     (dict(ldx=63), "LORA_ERR_ARG"),
     (dict(lddy=127), "LORA_ERR_ARG"),
     (dict(lddx=63), "LORA_ERR_ARG"),
@@ -83,6 +85,7 @@ def run_fused(plan, **kw):
     (dict(dx=FX + 0x400008), "LORA_ERR_ALIGN"),
     (dict(W0=FX + 0x80008), "LORA_ERR_ALIGN"),
     (dict(d_in=60), "LORA_ERR_ALIGN"),
+    (dict(d_out=1 << 30, lddy=1 << 30), "LORA_ERR_ARG"),
     (dict(n=2), "LORA_ERR_ADAPTER_ID"),
     (dict(flags=4), "LORA_ERR_ARG"),
     (dict(ws_bytes=1000), "LORA_ERR_WORKSPACE"),
