@@ -18,7 +18,7 @@
 // distance, so the stored state is right on average.  The 32 random bits of an
 // element (16 each for m and v) are a hash of the group's seed and step, the
 // tensor's number and the element's index.  A positive v never becomes 0, which
-// would make the next quotient arbitrary large.  A non-finite m or v is stored
+// would make the next quotient arbitrarily large.  A non-finite m or v is stored
 // as NaN and does not enter its block's scale.  The update of p uses m and v
 // before they are rounded.
 //

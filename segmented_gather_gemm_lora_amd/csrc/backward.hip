@@ -18,7 +18,7 @@
 //     inside one span of `span` sorted positions; a workgroup takes 256 columns of
 //     x or dy of it.  A segment inside one span is written at once; the sums of a
 //     segment that crosses spans go to the workspace.  Further workgroups take 256
-//     columns of dx for a block of 16 rows (ranks up to 32) or a chunk of 64;
+//     columns of dx for a block of 16 rows or a chunk of 64;
 //  3. bwd_reduce_kernel: adds those partial sums in span order (a fixed order:
 //     the gradients do not change from run to run).
 //
@@ -172,6 +172,7 @@ struct BwdArgs {
     // launch 2: column tiles of x and of both, groups of 64 ranks, gradient workgroups,
     // column tiles of dx
     int tiles_A, tiles, groups, ngrad, tiles_x;
+    bool chunks; // dx by chunks of 64 rows, else by blocks of 16
     void *dx;
     int64_t lddx;
     // JOIN: the sums of a base product in parts, [splits][T][d_in] by plan rows
@@ -467,9 +468,9 @@ __device__ __forceinline__ void shrink_sum(floatx4 (&acc)[RT], const ShrinkSide 
 
 // Where the work of launch 1 goes on.  Workgroup b runs on XCD b % 8: an XCD takes a
 // run of consecutive units, so that a segment's A and B are fetched into few L2s;
-// the list of items first (one workgroup), then the longer side.  False: nothing
-// (more) to do here.
-__device__ __forceinline__ bool shrink_unit(const BwdArgs &a, int units, int *scan, int &unit, int &side)
+// the list of items first (one workgroup), then the longer side, and each group of
+// 64 ranks by itself.  False: nothing (more) to do here.
+__device__ __forceinline__ bool shrink_unit(const BwdArgs &a, int units, int *scan, int &unit, int &side, int &group)
 {
     const int run = (units + 7) / 8, q = int(blockIdx.x >> 3) - 1;
     if (q < 0) {
@@ -477,13 +478,18 @@ __device__ __forceinline__ bool shrink_unit(const BwdArgs &a, int units, int *sc
         return false;
     }
     unit = int(blockIdx.x % 8) * run + q % run;
-    side = a.sides == 3 ? (q < run) == (a.d_out >= a.d_in) : a.sides - 1;
+    const bool both = a.sides == 3;
+    side = both ? (q / run % 2 == 0) == (a.d_out >= a.d_in) : a.sides - 1;
+    group = both ? q / run / 2 : q / run;
     return unit < units;
 }
 
-// A workgroup takes a block of 16 rows; its waves share the long axis.
+// A workgroup takes a block of 16 rows and 64 ranks (all of them by one workgroup:
+// 517 rows of ranks to 100, 22 us, 10 so); its waves share the long axis.  Four rank
+// tiles: 2 waves per SIMD, so that the loads ahead stay in registers (left to
+// itself the compiler makes 4 fit: mixed ranks 65 us, 58 so).
 template <int DT, bool VEC, int RT>
-__global__ __launch_bounds__(kShrinkWaves * 64) void bwd_shrink_kernel(BwdArgs a)
+__global__ __launch_bounds__(kShrinkWaves * 64) __attribute__((amdgpu_waves_per_eu(2, RT == 4 ? 2 : 8))) void bwd_shrink_kernel(BwdArgs a)
 {
     constexpr int W = kShrinkWaves, NP = RT == 1 ? 2 : 1;
     constexpr int kTile = NP * ShrinkTile<DT, RT>::kBytes;
@@ -492,42 +498,39 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void bwd_shrink_kernel(BwdArgs a
     static_assert(kLds <= 160 * 1024, "LDS budget");
     __shared__ __attribute__((aligned(16))) char lds[kLds];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-    int unit, side;
-    if (!shrink_unit(a, a.nblk, reinterpret_cast<int *>(lds), unit, side)) return;
+    int unit, side, group;
+    if (!shrink_unit(a, a.nblk, reinterpret_cast<int *>(lds), unit, side, group)) return;
     const lora_blk_desc *d = a.blk + unit;
     const int r = d->rank, n = d->n, p0 = d->p0;
     const float scale = d->scale;
     const void *mat = reinterpret_cast<const void *>(side ? d->B : d->A);
-    ShrinkSide sd = side ? ShrinkSide{a.dy, mat, a.lddy, a.d_out, r, 0, d->rows, n} : ShrinkSide{a.x, mat, a.ldx, a.d_in, r, 0, d->rows, n};
+    const int rt0 = RT * group;
+    if (16 * rt0 >= r) return;
+    const ShrinkSide sd = side ? ShrinkSide{a.dy, mat, a.lddy, a.d_out, r, rt0, d->rows, n} : ShrinkSide{a.x, mat, a.ldx, a.d_in, r, rt0, d->rows, n};
     const int ntiles = (r + 15) >> 4;
     char *tile = lds + wave * kTile;
-
-    for (int rt0 = 0; rt0 < ntiles; rt0 += RT) {
-        floatx4 acc[RT];
+    floatx4 acc[RT];
 #pragma unroll
-        for (int i = 0; i < RT; ++i) acc[i] = floatx4{};
-        sd.rt0 = rt0;
-        if (side == 0) shrink_sum<DT, VEC, 0, false, RT, NP>(acc, sd, tile, wave, lane);
-        else if (r % Elem<DT>::kVec) shrink_sum<DT, VEC, 1, true, RT, NP>(acc, sd, tile, wave, lane);
-        else shrink_sum<DT, VEC, 1, false, RT, NP>(acc, sd, tile, wave, lane);
-        // lane l of tile i holds D[row 4 (l / 16) + q][rank l % 16]
-        float *red = reinterpret_cast<float *>(lds);
-        __syncthreads(); // every wave is past its tiles, and past the last sums
+    for (int i = 0; i < RT; ++i) acc[i] = floatx4{};
+    if (side == 0) shrink_sum<DT, VEC, 0, false, RT, NP>(acc, sd, tile, wave, lane);
+    else if (r % Elem<DT>::kVec) shrink_sum<DT, VEC, 1, true, RT, NP>(acc, sd, tile, wave, lane);
+    else shrink_sum<DT, VEC, 1, false, RT, NP>(acc, sd, tile, wave, lane);
+    // lane l of tile i holds D[row 4 (l / 16) + q][rank l % 16]
+    float *red = reinterpret_cast<float *>(lds);
+    __syncthreads(); // every wave is past its tiles, and past the last sums
 #pragma unroll
-        for (int i = 0; i < RT; ++i) *reinterpret_cast<floatx4 *>(red + ((wave * RT + i) * 64 + lane) * 4) = acc[i];
-        __syncthreads();
-        for (int idx = tid; idx < RT * 256; idx += W * 64) {
-            const int i = idx >> 8, l2 = (idx >> 2) & 63, q4 = idx & 3;
-            float sum = 0.f;
+    for (int i = 0; i < RT; ++i) *reinterpret_cast<floatx4 *>(red + ((wave * RT + i) * 64 + lane) * 4) = acc[i];
+    __syncthreads();
+    for (int idx = tid; idx < RT * 256; idx += W * 64) {
+        const int i = idx >> 8, l2 = (idx >> 2) & 63, q4 = idx & 3;
+        float sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < W; ++w) sum += red[((w * RT + i) * 64 + l2) * 4 + q4];
-            const int mm = 4 * (l2 >> 4) + q4, t = rt0 + i, jm = l2 & 15, j = 16 * t + jm;
-            if (mm >= n || t >= ntiles) continue;
-            const int p = p0 + mm;
-            const float v = j < r ? sum * scale : 0.f;
-            store_uv<DT>(a, side, p, t, jm, v);
-        }
-        __syncthreads();
+        for (int w = 0; w < W; ++w) sum += red[((w * RT + i) * 64 + l2) * 4 + q4];
+        const int mm = 4 * (l2 >> 4) + q4, t = rt0 + i, jm = l2 & 15, j = 16 * t + jm;
+        if (mm >= n || t >= ntiles) continue;
+        const int p = p0 + mm;
+        const float v = j < r ? sum * scale : 0.f;
+        store_uv<DT>(a, side, p, t, jm, v);
     }
 }
 
@@ -557,11 +560,13 @@ __global__ __launch_bounds__(256) void bwd_shrink_ring_kernel(BwdArgs a)
     __shared__ __attribute__((aligned(1024))) char lds[kRing * kStage];
     static_assert(kRing * kStage >= 3 * 4 * 256, "the list's scan");
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), m = lane & 15, g = lane >> 4;
-    int unit, side;
-    if (!shrink_unit(a, a.nchunk, reinterpret_cast<int *>(lds), unit, side)) return;
+    int unit, side, group;
+    if (!shrink_unit(a, a.nchunk, reinterpret_cast<int *>(lds), unit, side, group)) return;
     const lora_chunk_desc *d = a.chunk + unit;
     const int r = d->rank, n = d->n, p0 = d->p0;
     const float scale = d->scale;
+    const int rt0 = RT * group;
+    if (16 * rt0 >= r) return;
     const int K = side ? a.d_out : a.d_in, nst = (K + 63) / 64;
     const uint32_t lds0 = uint32_t(uintptr_t((__attribute__((address_space(3))) char *)(lds)));
     const char *zeros = reinterpret_cast<const char *>(g_zeros);
@@ -574,121 +579,118 @@ __global__ __launch_bounds__(256) void bwd_shrink_ring_kernel(BwdArgs a)
         xp[j] = side ? static_cast<const char *>(a.dy) + (int64_t(row) * a.lddy + 8 * un) * 2
                      : static_cast<const char *>(a.x) + (int64_t(row) * a.ldx + 8 * un) * 2;
     }
-    for (int rt0 = 0; 16 * rt0 < r; rt0 += RT) {
-        // W: instruction 2 wave + j.  A: as x; B: row k of 8 slots, 32-byte granules
-        // moved as in b_at
-        const char *wp[kDma];
-        int wk[kDma];
-        const int64_t step = side ? int64_t(64) * r * 2 : 128;
+    // W: instruction 2 wave + j.  A: as x; B: row k of 8 slots, 32-byte granules
+    // moved as in b_at
+    const char *wp[kDma];
+    int wk[kDma];
+    const int64_t step = side ? int64_t(64) * r * 2 : 128;
 #pragma unroll
-        for (int j = 0; j < kDma; ++j) {
-            const int s = (kDma * wave + j) * 64 + lane;
-            if (side == 0) {
-                const int rank = 16 * rt0 + (s >> 3);
-                wk[j] = 8 * un;
-                wp[j] = reinterpret_cast<const char *>(d->A) + (int64_t(rank < r ? rank : r - 1) * K + 8 * un) * 2;
-            } else {
-                const int k = s >> 3, pos = s & 7, gran = (pos >> 1) ^ ((k >> 1) & 3), rank = 16 * (rt0 + gran) + 8 * (pos & 1);
-                wk[j] = k;
-                wp[j] = reinterpret_cast<const char *>(d->B) + (int64_t(k) * r + (rank < r ? rank : 0)) * 2;
-            }
+    for (int j = 0; j < kDma; ++j) {
+        const int s = (kDma * wave + j) * 64 + lane;
+        if (side == 0) {
+            const int rank = 16 * rt0 + (s >> 3);
+            wk[j] = 8 * un;
+            wp[j] = reinterpret_cast<const char *>(d->A) + (int64_t(rank < r ? rank : r - 1) * K + 8 * un) * 2;
+        } else {
+            const int k = s >> 3, pos = s & 7, gran = (pos >> 1) ^ ((k >> 1) & 3), rank = 16 * (rt0 + gran) + 8 * (pos & 1);
+            wk[j] = k;
+            wp[j] = reinterpret_cast<const char *>(d->B) + (int64_t(k) * r + (rank < r ? rank : 0)) * 2;
         }
-        auto issue = [&](int i) {
-            const uint32_t xbase = lds0 + uint32_t((i % kRing) * kStage + wave * kDma * 1024);
-            const uint32_t wbase = lds0 + uint32_t((i % kRing) * kStage + kXBytes + wave * kDma * 1024);
-            const int k0 = 64 * i;
-            // past K (the last stage, and stages past the last): zeros
+    }
+    auto issue = [&](int i) {
+        const uint32_t xbase = lds0 + uint32_t((i % kRing) * kStage + wave * kDma * 1024);
+        const uint32_t wbase = lds0 + uint32_t((i % kRing) * kStage + kXBytes + wave * kDma * 1024);
+        const int k0 = 64 * i;
+        // past K (the last stage, and stages past the last): zeros
 #pragma unroll
-            for (int j = 0; j < kDma; ++j) dma16(k0 + 8 * un < K ? xp[j] + int64_t(k0) * 2 : zeros, xbase + j * 1024);
+        for (int j = 0; j < kDma; ++j) dma16(k0 + 8 * un < K ? xp[j] + int64_t(k0) * 2 : zeros, xbase + j * 1024);
 #pragma unroll
-            for (int j = 0; j < kDma; ++j) dma16(k0 + wk[j] < K ? wp[j] + i * step : zeros, wbase + j * 1024);
-        };
-        floatx4 acc[RT];
+        for (int j = 0; j < kDma; ++j) dma16(k0 + wk[j] < K ? wp[j] + i * step : zeros, wbase + j * 1024);
+    };
+    floatx4 acc[RT];
 #pragma unroll
-        for (int i = 0; i < RT; ++i) acc[i] = floatx4{};
+    for (int i = 0; i < RT; ++i) acc[i] = floatx4{};
 #pragma unroll
-        for (int i = 0; i < kRing - 1; ++i) issue(i);
-        for (int i = 0; i < nst; ++i) {
-            // this wave's loads of stage i are done, then every wave's, and every wave
-            // has read stage i - 1
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_s_waitcnt(waitcnt_vm(2 * kDma * (kRing - 2)));
-            __builtin_amdgcn_s_barrier();
-            asm volatile("" ::: "memory");
-            issue(i + kRing - 1);
-            const char *xt = lds + (i % kRing) * kStage + wave * 2048, *wt = lds + (i % kRing) * kStage + kXBytes;
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const int at = m * 128 + (((4 * s + g) ^ (m & 7)) << 4);
-                const bf16x8 xf = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(xt + at));
-#pragma unroll
-                for (int q = 0; q < RT; ++q) {
-                    bf16x8 wf;
-                    if (side == 0) {
-                        wf = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(wt + q * 2048 + at));
-                    } else {
-                        u32x2 t[2];
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) t[b] = read_tr(wt + b_at<LORA_BF16, RT>(32 * s + 8 * g + 4 * b + (m >> 2), 32 * q + 8 * (m & 3)));
-                        wf = join8(t[0], t[1]);
-                    }
-                    acc[q] = mma<LORA_BF16>(xf, wf, acc[q]);
-                }
-            }
-        }
-        // no direct load may still be writing the ring, and every wave is past its reads
-        __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    for (int i = 0; i < kRing - 1; ++i) issue(i);
+    for (int i = 0; i < nst; ++i) {
+        // this wave's loads of stage i are done, then every wave's, and every wave
+        // has read stage i - 1
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(2 * kDma * (kRing - 2)));
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        // u or v through LDS, so that whole 16-byte pieces of the operands are stored
-        // (by single values: 14 us more for 16384 rows of rank 64)
-        constexpr int kPitch = 16 * RT + 1;
-        static_assert(64 * kPitch * 4 <= kRing * kStage, "the sums fit the ring");
-        float *sum = reinterpret_cast<float *>(lds);
+        issue(i + kRing - 1);
+        const char *xt = lds + (i % kRing) * kStage + wave * 2048, *wt = lds + (i % kRing) * kStage + kXBytes;
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
+        for (int s = 0; s < 2; ++s) {
+            const int at = m * 128 + (((4 * s + g) ^ (m & 7)) << 4);
+            const bf16x8 xf = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(xt + at));
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                sum[(16 * wave + 4 * g + q) * kPitch + 16 * i + m] = 16 * (rt0 + i) + m < r ? acc[i][q] * scale : 0.f;
-        __syncthreads();
-        const int cols = min(16 * RT, ((r + 15) & ~15) - 16 * rt0), oct0 = p0 >> 3, octs = ((p0 + n - 1) >> 3) - oct0 + 1;
-        const int64_t part = int64_t(a.nt) * kPieces / 2;
-        for (int idx = tid; idx < octs * cols; idx += 256) {
-            const int oct = idx / cols, j = idx - oct * cols, p = 8 * (oct0 + oct), row = p - p0;
-            uint16_t *o = reinterpret_cast<uint16_t *>((side ? a.ut : a.vt) + (int64_t(p / kWin) * 3 * a.nt + rt0 + (j >> 4)) * kPieces) +
-                          (((p & 31) >> 3) * 16 + (j & 15)) * 8;
-            if (row >= 0 && row + 8 <= n) {
-                u32x4 w[3];
+            for (int q = 0; q < RT; ++q) {
+                bf16x8 wf;
+                if (side == 0) {
+                    wf = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(wt + q * 2048 + at));
+                } else {
+                    u32x2 t[2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const Parts f0 = parts_of(sum[(row + 2 * e) * kPitch + j]), f1 = parts_of(sum[(row + 2 * e + 1) * kPitch + j]);
-                    w[0][e] = f0.h | f1.h << 16, w[1][e] = f0.mid | f1.mid << 16, w[2][e] = f0.low | f1.low << 16;
+                    for (int b = 0; b < 2; ++b) t[b] = read_tr(wt + b_at<LORA_BF16, RT>(32 * s + 8 * g + 4 * b + (m >> 2), 32 * q + 8 * (m & 3)));
+                    wf = join8(t[0], t[1]);
                 }
-#pragma unroll
-                for (int q = 0; q < 3; ++q) *reinterpret_cast<u32x4 *>(o + q * part) = w[q];
-            } else {
-                for (int e = max(0, -row); e < 8 && row + e < n; ++e) {
-                    const Parts f = parts_of(sum[(row + e) * kPitch + j]);
-                    o[e] = uint16_t(f.h), o[part + e] = uint16_t(f.mid), o[2 * part + e] = uint16_t(f.low);
-                }
+                acc[q] = mma<LORA_BF16>(xf, wf, acc[q]);
             }
         }
-        if (side)
-            for (int idx = tid; idx < n * (cols >> 3); idx += 256) {
-                const int c8 = idx / n, row = idx - c8 * n, p = p0 + row;
-                uint16_t *u = reinterpret_cast<uint16_t *>(a.ur + (int64_t(p >> 4) * a.nt + rt0 + (c8 >> 1)) * kPieces) +
-                              ((c8 & 1) * 16 + (p & 15)) * 8;
-                u32x4 w[2];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const Parts f0 = parts_of(sum[row * kPitch + 8 * c8 + 2 * e]), f1 = parts_of(sum[row * kPitch + 8 * c8 + 2 * e + 1]);
-                    w[0][e] = f0.h | f1.h << 16, w[1][e] = f0.mid | f1.mid << 16;
-                }
-                *reinterpret_cast<u32x4 *>(u) = w[0];
-                *reinterpret_cast<u32x4 *>(u + 2 * 16 * 8) = w[1];
-            }
-        __syncthreads(); // the next ranks' stages overwrite the sums
     }
+    // no direct load may still be writing the ring, and every wave is past its reads
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    // u or v through LDS, so that whole 16-byte pieces of the operands are stored
+    // (by single values: 14 us more for 16384 rows of rank 64)
+    constexpr int kPitch = 16 * RT + 1;
+    static_assert(64 * kPitch * 4 <= kRing * kStage, "the sums fit the ring");
+    float *sum = reinterpret_cast<float *>(lds);
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            sum[(16 * wave + 4 * g + q) * kPitch + 16 * i + m] = 16 * (rt0 + i) + m < r ? acc[i][q] * scale : 0.f;
+    __syncthreads();
+    const int cols = min(16 * RT, ((r + 15) & ~15) - 16 * rt0), oct0 = p0 >> 3, octs = ((p0 + n - 1) >> 3) - oct0 + 1;
+    const int64_t part = int64_t(a.nt) * kPieces / 2;
+    for (int idx = tid; idx < octs * cols; idx += 256) {
+        const int oct = idx / cols, j = idx - oct * cols, p = 8 * (oct0 + oct), row = p - p0;
+        uint16_t *o = reinterpret_cast<uint16_t *>((side ? a.ut : a.vt) + (int64_t(p / kWin) * 3 * a.nt + rt0 + (j >> 4)) * kPieces) +
+                      (((p & 31) >> 3) * 16 + (j & 15)) * 8;
+        if (row >= 0 && row + 8 <= n) {
+            u32x4 w[3];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const Parts f0 = parts_of(sum[(row + 2 * e) * kPitch + j]), f1 = parts_of(sum[(row + 2 * e + 1) * kPitch + j]);
+                w[0][e] = f0.h | f1.h << 16, w[1][e] = f0.mid | f1.mid << 16, w[2][e] = f0.low | f1.low << 16;
+            }
+#pragma unroll
+            for (int q = 0; q < 3; ++q) *reinterpret_cast<u32x4 *>(o + q * part) = w[q];
+        } else {
+            for (int e = max(0, -row); e < 8 && row + e < n; ++e) {
+                const Parts f = parts_of(sum[(row + e) * kPitch + j]);
+                o[e] = uint16_t(f.h), o[part + e] = uint16_t(f.mid), o[2 * part + e] = uint16_t(f.low);
+            }
+        }
+    }
+    if (side)
+        for (int idx = tid; idx < n * (cols >> 3); idx += 256) {
+            const int c8 = idx / n, row = idx - c8 * n, p = p0 + row;
+            uint16_t *u = reinterpret_cast<uint16_t *>(a.ur + (int64_t(p >> 4) * a.nt + rt0 + (c8 >> 1)) * kPieces) +
+                          ((c8 & 1) * 16 + (p & 15)) * 8;
+            u32x4 w[2];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const Parts f0 = parts_of(sum[row * kPitch + 8 * c8 + 2 * e]), f1 = parts_of(sum[row * kPitch + 8 * c8 + 2 * e + 1]);
+                w[0][e] = f0.h | f1.h << 16, w[1][e] = f0.mid | f1.mid << 16;
+            }
+            *reinterpret_cast<u32x4 *>(u) = w[0];
+            *reinterpret_cast<u32x4 *>(u + 2 * 16 * 8) = w[1];
+        }
 }
 
 // ----------------------------------------------------------------------------
@@ -699,10 +701,6 @@ constexpr int kGradWaves = 4;
 constexpr int kMaxSpan = 2048;
 constexpr int kOutPitch = 272, kWaveTile = 16 * kOutPitch; // a wave's LDS: 32 rows of 128 bytes, or 16 rows of results
 constexpr int kTileCols = 64 * kGradWaves; // columns of a workgroup
-// Row blocks of a dx workgroup, by the rank tiles of a gradient one (which set the
-// registers that the launch has): with one rank tile, chunks of 64 rows would
-// take twice its registers (4096 rows of rank 16: 70 us against 29).
-constexpr int dx_blocks(int rank_tiles) { return rank_tiles >= 3 ? 4 : 1; }
 
 // The wave's column fragments of one window, from its LDS tile: 32 rows of 128
 // bytes, unit 16 bytes, unit un of row q in slot un ^ (4 if q & 2): 4 rows
@@ -1146,7 +1144,8 @@ __global__ __launch_bounds__(kGradWaves * 64, out_waves(DT, VEC, RT)) void bwd_o
     __shared__ __attribute__((aligned(16))) char tiles_lds[kGradWaves * kWaveTile];
     __shared__ int32_t tok[kMaxSpan];
     if (int(blockIdx.x) < a.ngrad) grad_unit<DT, VEC, RT>(a, blockIdx.x, tiles_lds, tok);
-    else dx_unit<DT, VEC, false, dx_blocks(RT)>(a, int(blockIdx.x) - a.ngrad, tiles_lds);
+    else if (RT >= 4 && a.chunks) dx_unit<DT, VEC, false, RT >= 4 ? 4 : 1>(a, int(blockIdx.x) - a.ngrad, tiles_lds);
+    else dx_unit<DT, VEC, false, 1>(a, int(blockIdx.x) - a.ngrad, tiles_lds);
 }
 
 // Launch 3: gradient = sum of a split segment's slots, in slot order.
@@ -1233,11 +1232,11 @@ template <int DT, bool VEC> void run_shrink(hipStream_t s, const BwdArgs &a, uns
     // 98 / 125, 32768 159 / 231; rank 32: 44 / 42, 84 / 80, 146 / 151 from 8192 rows;
     // rank 16: 78 / 67 for 16384.
     if (DT == LORA_BF16 && VEC && ranks8 && a.nt > 2 && int64_t(a.nchunk) * nside >= 256 && a.Tp / a.nchunk >= 32) {
-        const dim3 grid((unsigned(a.nchunk) + 7) / 8 * nside * 8 + 8), block(256);
+        const dim3 grid((unsigned(a.nchunk) + 7) / 8 * nside * a.groups * 8 + 8), block(256);
         launch_kernel(bwd_shrink_ring_kernel, grid, block, 0, s, a);
         return;
     }
-    const dim3 grid((unsigned(a.nblk) + 7) / 8 * nside * 8 + 8), block(kShrinkWaves * 64);
+    const dim3 grid((unsigned(a.nblk) + 7) / 8 * nside * a.groups * 8 + 8), block(kShrinkWaves * 64);
     if (a.nt <= 1) launch_kernel(bwd_shrink_kernel<DT, VEC, 1>, grid, block, 0, s, a);
     else if (a.nt <= 2) launch_kernel(bwd_shrink_kernel<DT, VEC, 2>, grid, block, 0, s, a);
     else launch_kernel(bwd_shrink_kernel<DT, VEC, 4>, grid, block, 0, s, a);
@@ -1329,7 +1328,12 @@ int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p
     if (a.nsplit > 65535) return fail(LORA_ERR_ARG, "backward: %d segments over several spans (> 65535)", a.nsplit);
 
     const int64_t ngrad = int64_t(a.nitems) * a.tiles * a.groups;
-    const int64_t ndx = a.dx ? int64_t(dx_blocks(a.nt) == 4 ? a.nchunk : a.nblk) * a.tiles_x : 0;
+    // dx by chunks of 64 rows where they fill the chip (16384 rows of rank 64: launch
+    // 2 takes 149 us so, 217 by blocks; 517 rows of ranks to 100: 19, 14 by blocks),
+    // and not beside gradients of one or two rank tiles, whose launch would take
+    // twice its registers (4096 rows of rank 16: 70 us, 29 by blocks).
+    a.chunks = a.nt >= 3 && int64_t(a.nchunk) * a.tiles_x >= 512;
+    const int64_t ndx = a.dx ? int64_t(a.chunks ? a.nchunk : a.nblk) * a.tiles_x : 0;
     if (ngrad + ndx > (int64_t(1) << 31) - 1) return fail(LORA_ERR_ARG, "backward: too many work items");
     a.ngrad = int(ngrad);
 
