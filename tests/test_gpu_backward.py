@@ -88,6 +88,17 @@ def test_many_long_segments(T, d_in, d_out, ranks, kind):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d_in", [1032, 1029])
+def test_dx_of_many_long_segments(dtype, d_in):
+    say(f"case backward long dx {dtype} {d_in}")
+    p = Problem(dtype, ids_of("mixed", 8450, 3, d_in), [64, 40, 97], d_in, 24, seed=d_in)
+    d = p.device()
+    call(p, d)
+    torch.cuda.synchronize()
+    check(p, d, f"long dx {dtype} {d_in}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("pad,misalign", [((8, 16, 24), 0), ((3, 1, 2), 0), ((0, 0, 5), 0), ((0, 0, 0), 1), ((8, 8, 8), 8)])
 def test_pitches_and_alignment(dtype, pad, misalign):
     say(f"case backward pitches {dtype} {pad} {misalign}")
