@@ -388,8 +388,6 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     }
 }
 
-int rows_of(int32_t T) { return T <= 64 ? 64 : 256; }
-
 // Splits of the summed axis: as many as fill the chip in one round, with at
 // least 16 stages each (GEMM and join, us, at 8 / 16 splits: 64 rows, 4096 columns,
 // d_out 4096 18.7 / 22.5, d_out 14336 39.9 / 35.3; 8 rows, 2048 columns, d_out 8192
@@ -398,6 +396,16 @@ int splits_of(int64_t tiles, int32_t d_out)
 {
     const int64_t stages = (int64_t(d_out) + kBK - 1) / kBK;
     return int(std::max<int64_t>(1, std::min<int64_t>({kFill / tiles, stages / 16, kMaxSplits})));
+}
+
+// Rows of a tile: 256 where such tiles and their splits take more than half of the
+// chip, and not for up to 128 rows, which leave them half empty (64 / 256 rows, GEMM
+// and join, us.  4096 columns, d_out 4096: 128 rows 21 / 28, 256 rows 26 / 35, 512 rows
+// 38 / 42; d_out 14336: 40 / 45, 60 / 55, 103 / 77; 1024 columns, 256 rows 20 / 32).
+int rows_of(int32_t T, int32_t d_in, int32_t d_out)
+{
+    const int64_t tiles = (int64_t(T) + 255) / 256 * ((int64_t(d_in) + kCols - 1) / kCols);
+    return T <= 128 || tiles * splits_of(tiles, d_out) <= kFill / 2 ? 64 : 256;
 }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -423,7 +431,7 @@ int launch_fused_backward(hipStream_t s, const BackwardArgs &b, const void *W0, 
     const int T = h->num_tokens;
     const int max_rank = h->max_rank < 1 ? 1 : h->max_rank;
     DgradArgs a{};
-    const int rows = rows_of(T);
+    const int rows = rows_of(T, b.d_in, b.d_out);
     a.tiles_m = (T + rows - 1) / rows;
     a.tiles_n = (b.d_in + kCols - 1) / kCols;
     const int64_t tiles = int64_t(a.tiles_m) * a.tiles_n;

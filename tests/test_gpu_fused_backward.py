@@ -51,6 +51,37 @@ def test_against_64_bits(T, d_in, d_out, ranks, kind):
     check(p, d, f"T={T}")
 
 
+WIDE = [  # enough tiles of 256 rows: with the summed axis in parts and whole
+    (300, 4104, 2050, [16, 8, 64], "mixed"),
+    (513, 4096, 2048, [16] * 40, "runs"),
+    (2100, 4104, 72, [33, 8, 100], "mixed"),
+    (2305, 3848, 31, [16] * 300, "runs"),
+]
+
+
+@pytest.mark.parametrize("T,d_in,d_out,ranks,kind", WIDE)
+def test_wide_layers(T, d_in, d_out, ranks, kind):
+    test_against_64_bits(T, d_in, d_out, ranks, kind)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_bad_values_stay_with_their_rows_in_large_tiles(value):
+    ids = ids_of("runs", 2100, 4, 12)
+    p, q = (Problem("bf16", ids, [16, 8, 20, 64], 4104, 69, seed=12, w0=True, pad=(0, 3, 0)) for _ in range(2))
+    rows = np.nonzero(ids == 2)[0]
+    p.dy_full[rows] = value
+    p.A[2].fill_(value)
+    p.B[2].fill_(value)
+    d = p.device()
+    call(p, d)
+    torch.cuda.synchronize()
+    keep = np.nonzero(ids != 2)[0]
+    (dx, _, _), (edx, _, _) = q.reference()
+    from backward_ref import worst
+
+    assert worst(d.dx.double().cpu().numpy()[keep], dx[keep], edx[keep]) <= 1
+
+
 @pytest.mark.parametrize("pad", [(8, 16, 24), (0, 8, 16)])
 def test_pitches(pad):
     p = Problem("bf16", ids_of("mixed", 90, 3, 5), [16, 8, 30], 128, 192, seed=5, pad=pad, w0=True)
