@@ -1086,23 +1086,31 @@ def fused_linear_e4m3(x, W0, w0_scale: float, plan: Plan, y, ws, stream=None):
            "lora_fused_linear_e4m3")
 
 
-def _gradient_rows(dtype: str, tokens: int, tables, dy, *more) -> int:
-    """Refuses what the C call cannot see: matrices (dy, then pairs of one, or None,
-    and its columns) of another type, shape or device than the call's.  The device."""
+def _gradient_rows(dtype: str, tokens: int, others, rows):
+    """Refuses what the C call cannot see: matrices (pairs of one, or None, and its
+    columns, None for any; the first is not None) of another type, shape or device than
+    the call's, and other tensors of another device.  Returns the device and, for each
+    matrix, its address and row pitch (its columns for None)."""
     torch = _torch()
     dt = torch.float32 if dtype == "f32" else torch.bfloat16
-    device = torch.cuda.current_device() if dy.get_device() >= 0 else -1
-    for t, cols in ((dy, 0), *more):
+    device = torch.cuda.current_device() if rows[0][0].get_device() >= 0 else -1
+    out = []
+    for t, cols in rows:
         if t is None:
+            out += (None, cols)
             continue
         n, d = t.shape
         if t.get_device() != device or device < 0:
             raise ValueError(f"a tensor of {tuple(t.shape)} is not on the current device")
-        if n < tokens or (d != cols and cols) or t.dtype is not dt or (d > 1 and t.stride(1) != 1):
-            raise ValueError(f"{tokens} rows of {cols or d} adjacent elements of {dt} are wanted, not {tuple(t.shape)} of {t.dtype}")
-    if tables is not None and tables.addr_A_dev.get_device() != device:
-        raise ValueError("grads are not on the current device")
-    return device
+        ld, inner = t.stride()
+        if n < tokens or (cols is not None and d != cols) or t.dtype is not dt or (inner != 1 and d > 1):
+            raise ValueError(f"{tokens} rows of {d if cols is None else cols} adjacent elements of {dt} are wanted, "
+                             f"not {tuple(t.shape)} of {t.dtype}")
+        out += (t.data_ptr(), ld)
+    for t in others:
+        if t.get_device() != device:
+            raise ValueError("the plan, the workspace or grads are not on the current device")
+    return device, out
 
 
 def sgmv_backward(x, dy, plan: Plan, grads: Optional[GradPool], dx, ws, dtype: str, accumulate: bool = False,
@@ -1117,12 +1125,13 @@ def sgmv_backward(x, dy, plan: Plan, grads: Optional[GradPool], dx, ws, dtype: s
         raise ValueError("x is None")
     else:
         return  # nothing is wanted
-    device = _gradient_rows(dtype, plan.h.batch_tokens, grads, dy, (x, d_in), (dx, d_in))
-    _check(load().lora_sgmv_backward(_stream_handle(stream, device), DTYPES[dtype], _ptr(x), d_in if x is None else x.stride(0),
-                                     d_in, _ptr(dy), dy.stride(0), dy.shape[1], plan.seg,
-                                     _ptr(grads and grads.addr_A_dev), _ptr(grads and grads.addr_B_dev),
-                                     grads.n_adapters if grads else 0, LORA_GRAD_ACCUMULATE if accumulate else 0,
-                                     _ptr(dx), d_in if dx is None else dx.stride(0), _ptr(ws),
+    tA, tB, n = (None, None, 0) if grads is None else (grads.addr_A_dev, grads.addr_B_dev, grads.n_adapters)
+    device, (pdy, lddy, px, ldx, pdx, lddx) = _gradient_rows(
+        dtype, plan.h.batch_tokens, (plan.dev, ws) if grads is None else (plan.dev, ws, tA, tB),
+        ((dy, None), (x, d_in), (dx, d_in)))
+    _check(load().lora_sgmv_backward(_stream_handle(stream, device), DTYPES[dtype], px, ldx, d_in, pdy, lddy,
+                                     dy.shape[1], plan.seg, _ptr(tA), _ptr(tB), n,
+                                     LORA_GRAD_ACCUMULATE if accumulate else 0, pdx, lddx, ws.data_ptr(),
                                      ws.numel() * ws.element_size()),
            "lora_sgmv_backward")
 
@@ -1134,14 +1143,15 @@ def fused_linear_backward(x, W0, dy, plan: Plan, grads: Optional[GradPool], dx, 
     d_out, d_in = W0.shape
     if not W0.is_contiguous():
         raise ValueError("W0 is contiguous [d_out, d_in]")
-    device = _gradient_rows(dtype, plan.h.batch_tokens, grads, dy, (dy, d_out), (x, d_in), (dx, d_in))
-    _gradient_rows(dtype, d_out, None, W0)
-    _check(load().lora_fused_linear_backward(_stream_handle(stream, device), DTYPES[dtype], _ptr(x),
-                                             d_in if x is None else x.stride(0), d_in, _ptr(W0), _ptr(dy), dy.stride(0),
-                                             dy.shape[1], plan.seg, _ptr(grads and grads.addr_A_dev),
-                                             _ptr(grads and grads.addr_B_dev), grads.n_adapters if grads else 0,
-                                             LORA_GRAD_ACCUMULATE if accumulate else 0, _ptr(dx), dx.stride(0),
-                                             _ptr(ws), ws.numel() * ws.element_size()),
+    tA, tB, n = (None, None, 0) if grads is None else (grads.addr_A_dev, grads.addr_B_dev, grads.n_adapters)
+    device, (pdy, lddy, px, ldx, pdx, lddx) = _gradient_rows(
+        dtype, plan.h.batch_tokens, (plan.dev, ws) if grads is None else (plan.dev, ws, tA, tB),
+        ((dy, d_out), (x, d_in), (dx, d_in)))
+    _, (pW0, _) = _gradient_rows(dtype, d_out, (), ((W0, d_in),))
+    _check(load().lora_fused_linear_backward(_stream_handle(stream, device), DTYPES[dtype], px, ldx, d_in, pW0, pdy,
+                                             lddy, d_out, plan.seg, _ptr(tA), _ptr(tB), n,
+                                             LORA_GRAD_ACCUMULATE if accumulate else 0, pdx, lddx, ws.data_ptr(),
+                                             ws.numel() * ws.element_size()),
            "lora_fused_linear_backward")
 
 
@@ -1202,7 +1212,7 @@ class AdamW:
                 raise ValueError(f"{name} and groups list one entry for each parameter")
             for t, p in zip(ts, self.params):
                 want = size(p.numel()) if size else p.numel()
-                if t.dtype != dt or t.numel() != want or not t.is_contiguous() or t.device != device:
+                if t is None or t.dtype != dt or t.numel() != want or not t.is_contiguous() or t.device != device:
                     raise ValueError(f"{name}: contiguous {dt} tensors of {want} elements on the device of hyper")
         arr = (LoraAdamTensor * max(n, 1))()
         for i, p in enumerate(self.params):

@@ -1334,7 +1334,8 @@ int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p
     // twice its registers (4096 rows of rank 16: 70 us, 29 by blocks).
     a.chunks = a.nt >= 3 && int64_t(a.nchunk) * a.tiles_x >= 512;
     const int64_t ndx = a.dx ? int64_t(a.chunks ? a.nchunk : a.nblk) * a.tiles_x : 0;
-    if (ngrad + ndx > (int64_t(1) << 31) - 1) return fail(LORA_ERR_ARG, "backward: too many work items");
+    if (ngrad + ndx > (int64_t(1) << 31) - 1 || int64_t(a.nblk) * 2 * a.groups > (int64_t(1) << 30))
+        return fail(LORA_ERR_ARG, "backward: too many work items");
     a.ngrad = int(ngrad);
 
     const bool bf16 = b.dtype == LORA_BF16;

@@ -184,48 +184,55 @@ class _Rows:
 
         self.shape, self.dtype, self._d, self._inner = shape, dtype or torch.bfloat16, device, inner
 
-    dim = lambda self: len(self.shape)  # noqa: E731
     get_device = lambda self: self._d  # noqa: E731
-    stride = lambda self, i: self._inner if i else self.shape[1]  # noqa: E731
+    stride = lambda self: (self.shape[1], self._inner)  # noqa: E731
+    data_ptr = lambda self: FX  # noqa: E731
     is_contiguous = lambda self: True  # noqa: E731
 
 
 class _Plan:
+    dev = _Rows((1, 1))
+
     class h:
         batch_tokens = 4
+
+
+class _PlanElsewhere(_Plan):
+    dev = _Rows((1, 1), device=1)
 
 
 @pytest.mark.parametrize("fused", [False, True])
 @pytest.mark.parametrize("kw", [
     dict(x=_Rows((4, 64), device=1)), dict(dy=_Rows((4, 32), device=1)), dict(dx=_Rows((4, 64), device=-1)),
     dict(dy=_Rows((4, 32), device=-1)), dict(x=_Rows((3, 64))), dict(dx=_Rows((3, 64))), dict(dy=_Rows((3, 32))),
+    dict(plan=_PlanElsewhere), dict(ws=_Rows((1, 1), device=-1)), dict(ws=_Rows((1, 1), device=1)),
+    dict(grads=B.GradPool([], [], [], _Rows((1, 1), device=1), _Rows((1, 1)))),
     dict(dx=_Rows((4, 65))), dict(x=_Rows((4, 64, 1))), dict(x=_Rows((4, 64), inner=2)), dict(dtype="f32"),
 ])
 def test_binding_refuses_what_the_call_cannot_see(fused, kw, monkeypatch):
     import torch
 
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    a = dict(x=_Rows((4, 64)), dy=_Rows((4, 32)), dx=_Rows((4, 64)), W0=_Rows((32, 64)), dtype="bf16")
+    a = dict(x=_Rows((4, 64)), dy=_Rows((4, 32)), dx=_Rows((4, 64)), W0=_Rows((32, 64)), dtype="bf16", plan=_Plan, grads=None,
+             ws=_Rows((1, 1)))
     a.update(kw)
     with pytest.raises(ValueError):
         if fused:
-            B.fused_linear_backward(a["x"], a["W0"], a["dy"], _Plan, None, a["dx"], None, a["dtype"])
+            B.fused_linear_backward(a["x"], a["W0"], a["dy"], a["plan"], a["grads"], a["dx"], a["ws"], a["dtype"])
         else:
-            B.sgmv_backward(a["x"], a["dy"], _Plan, None, a["dx"], None, a["dtype"])
+            B.sgmv_backward(a["x"], a["dy"], a["plan"], a["grads"], a["dx"], a["ws"], a["dtype"])
 
 
 def test_binding_refuses_other_weights_and_missing_x(monkeypatch):
     import torch
 
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    x, dy = _Rows((4, 64)), _Rows((4, 32))
+    x, dy, ws = _Rows((4, 64)), _Rows((4, 32)), _Rows((1, 1))
     for W0 in (_Rows((31, 64)), _Rows((32, 72)), _Rows((32, 64), device=1), _Rows((32, 64), dtype=torch.float32)):
         with pytest.raises(ValueError):
-            B.fused_linear_backward(x, W0, dy, _Plan, None, x, None)
+            B.fused_linear_backward(x, W0, dy, _Plan, None, x, ws)
     with pytest.raises(ValueError, match="x is None"):
         B.sgmv_backward(None, dy, _Plan, B.GradPool([], [], [], x, x), None, None, "bf16")
-    with pytest.raises(ValueError, match="grads"):
-        B.sgmv_backward(x, dy, _Plan, B.GradPool([], [], [], _Rows((1, 1), device=1), x), None, None, "bf16")
     assert B.sgmv_backward(None, dy, _Plan, None, None, None, "bf16") is None  # nothing wanted
 
 
