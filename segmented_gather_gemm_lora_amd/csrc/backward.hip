@@ -218,27 +218,36 @@ __device__ void list_items(const BwdArgs &a, int *scan, int nthreads)
             gB = a.grad_B ? a.grad_B[d.adapter] : 0;
         }
         const int ns = n > 1 ? n : 0, nq = n > 1 ? 1 : 0;
-        int *sc[3] = {scan, scan + nthreads, scan + 2 * nthreads};
-        int val[3] = {n, ns, nq};
-        for (int q = 0; q < 3; ++q) sc[q][tid] = val[q];
+        // sums before this thread: over its wave's lanes, then the waves'
+        const int own[3] = {n, ns, nq}, lane = tid & 63, wave = tid >> 6;
+        int upto[3] = {n, ns, nq}, total[3] = {0, 0, 0};
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1)
+#pragma unroll
+            for (int q = 0; q < 3; ++q) {
+                const int v = __shfl_up(upto[q], d);
+                if (lane >= d) upto[q] += v;
+            }
+        if (lane == 63)
+            for (int q = 0; q < 3; ++q) scan[3 * wave + q] = upto[q];
         __syncthreads();
-        for (int d = 1; d < nthreads; d <<= 1) {
-            int add[3];
-            for (int q = 0; q < 3; ++q) add[q] = tid >= d ? sc[q][tid - d] : 0;
-            __syncthreads();
-            for (int q = 0; q < 3; ++q) sc[q][tid] += add[q];
-            __syncthreads();
-        }
-        const int it = item0 + sc[0][tid] - n, sl = slot0 + sc[1][tid] - ns, sp = split0 + sc[2][tid] - nq;
+        for (int w = 0; w < nthreads >> 6; ++w)
+#pragma unroll
+            for (int q = 0; q < 3; ++q) {
+                const int v = scan[3 * w + q];
+                if (w < wave) upto[q] += v;
+                total[q] += v;
+            }
+        const int it = item0 + upto[0] - own[0], sl = slot0 + upto[1] - own[1], sp = split0 + upto[2] - own[2];
         for (int i = 0; i < n; ++i) {
             const int b = i == 0 ? start : (start / a.span + i) * a.span;
             const int e = i == n - 1 ? end : (start / a.span + i + 1) * a.span;
             a.items[it + i] = Item{gA, gB, b, e, r, n > 1 ? sl + i : -1};
         }
         if (nq) a.segsplits[sp] = Split{s, sl, n, 0};
-        item0 += sc[0][nthreads - 1];
-        slot0 += sc[1][nthreads - 1];
-        split0 += sc[2][nthreads - 1];
+        item0 += total[0];
+        slot0 += total[1];
+        split0 += total[2];
         __syncthreads();
     }
 }
@@ -493,8 +502,7 @@ __global__ __launch_bounds__(kShrinkWaves * 64) __attribute__((amdgpu_waves_per_
 {
     constexpr int W = kShrinkWaves, NP = RT == 1 ? 2 : 1;
     constexpr int kTile = NP * ShrinkTile<DT, RT>::kBytes;
-    constexpr int kRed = W * RT * 1024, kScan = 3 * 4 * W * 64;
-    constexpr int kLds = std::max(std::max(W * kTile, kRed), kScan);
+    constexpr int kLds = std::max(W * kTile, W * RT * 1024); // tiles, or the waves' sums
     static_assert(kLds <= 160 * 1024, "LDS budget");
     __shared__ __attribute__((aligned(16))) char lds[kLds];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
@@ -558,7 +566,6 @@ __global__ __launch_bounds__(256) void bwd_shrink_ring_kernel(BwdArgs a)
     constexpr int RT = 4, kXBytes = 64 * 128, kWBytes = 64 * 128, kStage = kXBytes + kWBytes;
     constexpr int kDma = 2; // loads of x, and of W, of a wave per stage
     __shared__ __attribute__((aligned(1024))) char lds[kRing * kStage];
-    static_assert(kRing * kStage >= 3 * 4 * 256, "the list's scan");
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), m = lane & 15, g = lane >> 4;
     int unit, side, group;
     if (!shrink_unit(a, a.nchunk, reinterpret_cast<int *>(lds), unit, side, group)) return;
