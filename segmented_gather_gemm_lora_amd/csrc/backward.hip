@@ -738,6 +738,23 @@ struct GradSide {
     int D;
 };
 
+// Four rank tiles (bf16): a window's 12 operands of u or v are three times the bytes of a
+// wave's columns, and the same for the 4 waves, which fetch them once for all, by
+// direct loads into LDS (each wave by itself: L1-bound, 16384 rows of rank 64 95 us, 74
+// so).
+template <int DT, int RT> constexpr bool kShareU = DT == LORA_BF16 && RT == 4;
+constexpr int kShareBytes = 12 * kPieces; // one window; two lie in LDS
+
+__device__ __forceinline__ void share_load(const BwdArgs &a, const GradSide &sd, int w, int rt0, uint32_t lds_byte, int wave, int lane)
+{
+    const char *win = static_cast<const char *>(sd.parts) + int64_t(w) * 3 * a.nt * kPieces + 16 * lane;
+#pragma unroll
+    for (int k = 0; k < 12 / kGradWaves; ++k) {
+        const int piece = 12 / kGradWaves * wave + k, t = min(rt0 + (piece & 3), a.nt - 1); // past the last tile: not stored
+        dma16(win + ((piece >> 2) * a.nt + t) * kPieces, lds_byte + uint32_t((w & 1) * kShareBytes + piece * kPieces));
+    }
+}
+
 // WHOLE: all 64 columns lie in the row (not asked for by VEC).
 template <int DT, bool VEC, bool WHOLE, int RT>
 __device__ __forceinline__ void grad_load(GradOps<DT, RT> &o, const BwdArgs &a, const GradSide &sd, int begin, int end,
@@ -747,13 +764,15 @@ __device__ __forceinline__ void grad_load(GradOps<DT, RT> &o, const BwdArgs &a, 
     using T = typename E::T;
     const int m = lane & 15, g = lane >> 4;
     const int base = w * kWin;
-    const char *win = static_cast<const char *>(sd.parts) + int64_t(w) * E::kParts * a.nt * kPieces;
+    if constexpr (!kShareU<DT, RT>) {
+        const char *win = static_cast<const char *>(sd.parts) + int64_t(w) * E::kParts * a.nt * kPieces;
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-        const int t = min(rt0 + i, a.nt - 1); // past the last tile: not stored
+        for (int i = 0; i < RT; ++i) {
+            const int t = min(rt0 + i, a.nt - 1); // past the last tile: not stored
 #pragma unroll
-        for (int q = 0; q < E::kParts; ++q)
-            o.uf[i][q] = __builtin_bit_cast(typename E::F, load16(win + (q * a.nt + t) * kPieces, 16 * lane));
+            for (int q = 0; q < E::kParts; ++q)
+                o.uf[i][q] = __builtin_bit_cast(typename E::F, load16(win + (q * a.nt + t) * kPieces, 16 * lane));
+        }
     }
     auto token = [&](int p) { return tok[min(max(p, begin), end - 1) - begin]; };
     if constexpr (DT == LORA_BF16 && VEC) {
@@ -789,11 +808,18 @@ __device__ __forceinline__ void grad_load(GradOps<DT, RT> &o, const BwdArgs &a, 
 
 template <int DT, int RT>
 __device__ __forceinline__ void grad_mma(GradOps<DT, RT> &o, floatx4 (&acc)[4][RT], int side, int begin, int end, int w,
-                                         char *tile, int lane)
+                                         char *tile, const char *share, int lane)
 {
     using E = Elem<DT>;
     using F = typename E::F;
     const int m = lane & 15, g = lane >> 4, base = w * kWin;
+    if constexpr (kShareU<DT, RT>) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int q = 0; q < E::kParts; ++q)
+                o.uf[i][q] = __builtin_bit_cast(F, *reinterpret_cast<const u32x4 *>(share + (w & 1) * kShareBytes + ((4 * q + i) * 64 + lane) * 16));
+    }
     if (base < begin || base + kWin > end) { // rows outside: zero on both sides (wave-uniform)
         auto in = [&](int p) { return p >= begin && p < end; };
 #pragma unroll
@@ -848,7 +874,8 @@ __device__ __forceinline__ void grad_mma(GradOps<DT, RT> &o, floatx4 (&acc)[4][R
 
 template <int DT, bool VEC, bool WHOLE, int RT>
 __device__ __forceinline__ void grad_item(const BwdArgs &a, const GradSide &sd, int side, int begin, int end, int c0, int rt0,
-                                          int r, float *dst, bool add, bool stream, const int32_t *tok, char *tile, int lane)
+                                          int r, float *dst, bool add, bool stream, bool idle, const int32_t *tok, char *tile,
+                                          char *share, int lane)
 {
     const int w1 = (end - 1) / kWin;
     floatx4 acc[4][RT];
@@ -857,19 +884,31 @@ __device__ __forceinline__ void grad_item(const BwdArgs &a, const GradSide &sd, 
 #pragma unroll
         for (int i = 0; i < RT; ++i) acc[t][i] = floatx4{};
     // Four rank tiles: the next window's loads are issued before the current one's
-    // products (16384 rows of rank 64: 106 us, 118 without).  Fewer: more waves fit
+    // products (16384 rows of rank 64: 106 us, 118 without, before they were shared).  Fewer: more waves fit
     // instead (rank 16, 4096 rows: 17.2 us, 18.8 with).
     GradOps<DT, RT> o0;
     int w = begin / kWin;
+    const int wave = uniform(threadIdx.x >> 6);
+    const uint32_t share_at = uint32_t(uintptr_t((__attribute__((address_space(3))) char *)(share)));
+    if (kShareU<DT, RT>) share_load(a, sd, w, rt0, share_at, wave, lane);
     grad_load<DT, VEC, WHOLE>(o0, a, sd, begin, end, w, c0, rt0, tok, lane);
     for (;;) {
         GradOps<DT, RT> o1;
+        if (kShareU<DT, RT>) {
+            // window w is there, every wave's part of it, and every wave is past the one before
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            if (w < w1) share_load(a, sd, w + 1, rt0, share_at, wave, lane);
+        }
         if (RT == 4 && w < w1) grad_load<DT, VEC, WHOLE>(o1, a, sd, begin, end, w + 1, c0, rt0, tok, lane);
-        grad_mma(o0, acc, side, begin, end, w, tile, lane);
+        grad_mma(o0, acc, side, begin, end, w, tile, share, lane);
         if (++w > w1) break;
         if (RT == 4) o0 = o1;
         else grad_load<DT, VEC, WHOLE>(o0, a, sd, begin, end, w, c0, rt0, tok, lane);
     }
+    if (idle) return;
     // dA (side 0): D rows are columns of x, D columns ranks; dB: D rows are ranks, D
     // columns columns of dy (rows of dB).  A lane's 4 sums are consecutive in the
     // gradient; 16 ranks x 64 columns turn in the wave's tile, so that they leave
@@ -927,7 +966,7 @@ __device__ __forceinline__ void grad_item(const BwdArgs &a, const GradSide &sd, 
 // RT: rank tiles that a wave holds (the plan's largest rank, at most 4: higher
 // ranks are `groups` of 64, a workgroup each).
 template <int DT, bool VEC, int RT>
-__device__ __forceinline__ void grad_unit(const BwdArgs &a, int id, char *tiles_lds, int32_t *tok)
+__device__ __forceinline__ void grad_unit(const BwdArgs &a, int id, char *tiles_lds, int32_t *tok, char *share)
 {
     const int tl = id % a.tiles, group = id / a.tiles % a.groups;
     const Item it = a.items[id / a.tiles / a.groups];
@@ -939,8 +978,13 @@ __device__ __forceinline__ void grad_unit(const BwdArgs &a, int id, char *tiles_
     __syncthreads();
     const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, r = it.rank;
     const GradSide sd = side ? GradSide{a.dy, a.vt, a.lddy, a.d_out} : GradSide{a.x, a.ut, a.ldx, a.d_in};
-    const int c0 = (side ? tl - a.tiles_A : tl) * (64 * kGradWaves) + 64 * wave;
-    if (c0 >= sd.D) return;
+    int c0 = (side ? tl - a.tiles_A : tl) * (64 * kGradWaves) + 64 * wave;
+    const int left = r - 64 * group;
+    // a wave past the columns does its part of shared windows (on the first columns,
+    // which it does not store)
+    const bool idle = c0 >= sd.D;
+    if (idle && !(DT == LORA_BF16 && RT >= 4 && left > 32)) return;
+    if (idle) c0 = 0;
     float *dst = reinterpret_cast<float *>(grad);
     bool add = a.accumulate;
     if (it.slot >= 0) {
@@ -950,12 +994,11 @@ __device__ __forceinline__ void grad_unit(const BwdArgs &a, int id, char *tiles_
     char *tile = tiles_lds + wave * kWaveTile;
     auto ranks = [&](auto whole) {
         constexpr bool W = decltype(whole)::value;
-        const int left = r - 64 * group;
         if (RT >= 4 && left > 32)
-            grad_item<DT, VEC, W, RT >= 4 ? 4 : 1>(a, sd, side, it.begin, it.end, c0, 4 * group, r, dst, add, RT < 4 && it.slot < 0, tok, tile, lane);
+            grad_item<DT, VEC, W, RT >= 4 ? 4 : 1>(a, sd, side, it.begin, it.end, c0, 4 * group, r, dst, add, RT < 4 && it.slot < 0, idle, tok, tile, share, lane);
         else if (RT >= 2 && left > 16)
-            grad_item<DT, VEC, W, RT >= 2 ? 2 : 1>(a, sd, side, it.begin, it.end, c0, 4 * group, r, dst, add, RT < 4 && it.slot < 0, tok, tile, lane);
-        else grad_item<DT, VEC, W, 1>(a, sd, side, it.begin, it.end, c0, 4 * group, r, dst, add, RT < 4 && it.slot < 0, tok, tile, lane);
+            grad_item<DT, VEC, W, RT >= 2 ? 2 : 1>(a, sd, side, it.begin, it.end, c0, 4 * group, r, dst, add, RT < 4 && it.slot < 0, idle, tok, tile, share, lane);
+        else grad_item<DT, VEC, W, 1>(a, sd, side, it.begin, it.end, c0, 4 * group, r, dst, add, RT < 4 && it.slot < 0, idle, tok, tile, share, lane);
     };
     if constexpr (VEC || DT == LORA_F32) ranks(std::true_type{});
     else if (c0 + 64 <= sd.D) ranks(std::true_type{});
@@ -1150,7 +1193,8 @@ __global__ __launch_bounds__(kGradWaves * 64, out_waves(DT, VEC, RT)) void bwd_o
 {
     __shared__ __attribute__((aligned(16))) char tiles_lds[kGradWaves * kWaveTile];
     __shared__ int32_t tok[kMaxSpan];
-    if (int(blockIdx.x) < a.ngrad) grad_unit<DT, VEC, RT>(a, blockIdx.x, tiles_lds, tok);
+    __shared__ __attribute__((aligned(16))) char share[kShareU<DT, RT> ? 2 * kShareBytes : 16];
+    if (int(blockIdx.x) < a.ngrad) grad_unit<DT, VEC, RT>(a, blockIdx.x, tiles_lds, tok, share);
     else if (RT >= 4 && a.chunks) dx_unit<DT, VEC, false, RT >= 4 ? 4 : 1>(a, int(blockIdx.x) - a.ngrad, tiles_lds);
     else dx_unit<DT, VEC, false, 1>(a, int(blockIdx.x) - a.ngrad, tiles_lds);
 }
