@@ -1380,7 +1380,7 @@ int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p
 
     const int64_t ngrad = int64_t(a.nitems) * a.tiles * a.groups;
     // dx by chunks of 64 rows where they fill the chip (16384 rows of rank 64: launch
-    // 2 takes 149 us so, 217 by blocks; 517 rows of ranks to 100: 19, 14 by blocks),
+    // 2 took 149 us so, 217 by blocks; 517 rows of ranks to 100: 19, 14 by blocks),
     // and not beside gradients of one or two rank tiles, whose launch would take
     // twice its registers (4096 rows of rank 16: 70 us, 29 by blocks).
     a.chunks = a.nt >= 3 && int64_t(a.nchunk) * a.tiles_x >= 512;
