@@ -282,6 +282,30 @@ def test_stream_and_repeats():
         assert torch.equal(t, f)
 
 
+def test_two_streams_at_once():
+    """Two batches on two streams, each with its own workspace: the same bits as one after the other."""
+    ps = [Problem("bf16", ids_of("mixed", T, 4, T), [16, 64, 100, 8], 264, 520, seed=T) for T in (700, 900)]
+    ds = [p.device() for p in ps]
+    start = [d.dx.clone() for d in ds]
+    for p, d in zip(ps, ds):
+        call(p, d)
+    torch.cuda.synchronize()
+    want = [(d.dx.clone(), [t.clone() for t in (*d.grads.A, *d.grads.B)]) for d in ds]
+    streams = [torch.cuda.Stream() for _ in ds]
+    for k in range(4):
+        for d, x in zip(ds, start):
+            d.dx.copy_(x)
+            for t in (*d.grads.A, *d.grads.B):
+                t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for p, d, s in zip(ps, ds, streams):
+            call(p, d, stream=s)
+        torch.cuda.synchronize()
+        for d, (dx, grads) in zip(ds, want):
+            assert torch.equal(d.dx, dx), k
+            assert all(torch.equal(a, b) for a, b in zip((*d.grads.A, *d.grads.B), grads)), k
+
+
 def test_captured_and_replayed():
     """A captured call, replayed with new inputs between eager calls that share its workspace."""
     p = Problem("bf16", ids_of("runs", 600, 3, 8), [16, 8, 32], 256, 128, seed=8)
