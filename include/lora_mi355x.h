@@ -674,6 +674,8 @@ int lora_fused_linear_e4m3(void *stream, const void *x, int64_t ldx, int32_t d_i
  *                    left as they were.  dx must not overlap x or dy.
  *   x may be NULL when both tables are (only dx is wanted).  d_in and d_out go up
  *   to 2^24.
+ *   d_in, d_out and the gradients' sizes are the caller's to keep equal to the
+ *   adapters': the segments hold ranks and addresses, no widths.
  * Precision: u and v are fp32 sums of the dtype's products; bf16 calls feed them
  * to the second products as bf16 parts (three for dA and dB, 24 significant
  * bits; two for dx, 16 bits), with fp32 accumulation; dx is rounded once.

@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+import weakref
 from dataclasses import dataclass
 from typing import Optional
 
@@ -812,6 +813,11 @@ class Plan:
         _check(lora_segments_bind(self.host.data_ptr(), self.capacity, ctypes.addressof(self.h)), "lora_segments_bind")
         _check(lora_segments_bind(self.dev.data_ptr(), self.capacity, ctypes.addressof(self.d)), "lora_segments_bind")
 
+    # (d_in, d_out, dtype) of the pool that build() took the adapters from (the segments
+    # do not hold them), and the GradPool that was last found to fit them (weak)
+    made_for = None
+    grads_fit = None
+
     @property
     def seg(self) -> int:
         return ctypes.addressof(self.d)
@@ -820,6 +826,7 @@ class Plan:
         ids = np.ascontiguousarray(ids, dtype=np.int32)
         if ids.shape[0] > self.capacity:
             raise ValueError("batch larger than the segments' capacity")
+        self.made_for, self.grads_fit = (pool.d_in, pool.d_out, pool.dtype), None
         st = lora_build_segments(ids.shape[0], ids.ctypes.data, pool.n_adapters, pool.addr_A.ctypes.data,
                                  pool.addr_B.ctypes.data, pool.rank.ctypes.data, pool.alpha.ctypes.data,
                                  ctypes.addressof(self.h))
@@ -1113,12 +1120,31 @@ def _gradient_rows(dtype: str, tokens: int, others, rows):
     return device, out
 
 
+def _fits_plan(plan: Plan, d_in: int, d_out: int, dtype: str, grads: Optional[GradPool], device: int):
+    """Refuses sizes other than those of the adapters that the plan was built from: the
+    kernels read A and B, and write the gradients, at the call's widths and the plan's
+    ranks.  The gradients are looked at once for each plan built."""
+    if plan.made_for is None or plan.h.num_segments == 0:  # built without a Plan; no adapter is touched
+        return
+    if plan.made_for != (d_in, d_out, dtype):
+        raise ValueError(f"a call of ({d_in}, {d_out}, {dtype}) on a plan of adapters of {plan.made_for}")
+    if grads is None or (plan.grads_fit is not None and plan.grads_fit() is grads):
+        return
+    t = plan.segment_table()
+    for i, r in zip(t["seg_adapter"].tolist(), t["seg_rank"].tolist()):
+        for g, n in ((grads.A, r * d_in), (grads.B, r * d_out)):
+            if i < len(g) and g[i] is not None and (g[i].numel() < n or g[i].get_device() != device):
+                raise ValueError(f"a gradient of adapter {i} of {g[i].numel()} elements on {g[i].device}; {n} on the "
+                                 "current device are wanted")
+    plan.grads_fit = weakref.ref(grads)
+
+
 def sgmv_backward(x, dy, plan: Plan, grads: Optional[GradPool], dx, ws, dtype: str, accumulate: bool = False,
                   stream=None):
     """Gradients of sgmv: dx[perm] += u A (dx None: not wanted), grads.A = u^T x,
     grads.B = dy^T v over each adapter's rows (added to them with accumulate;
-    grads None: not wanted).  The gradients have the shapes of the adapters that
-    the plan was built with."""
+    grads None: not wanted).  Widths, type and gradients are those of the pool that
+    the plan was built from; others are refused."""
     if x is not None or dx is not None:
         d_in = (dx if x is None else x).shape[-1]
     elif grads is not None:
@@ -1129,6 +1155,7 @@ def sgmv_backward(x, dy, plan: Plan, grads: Optional[GradPool], dx, ws, dtype: s
     device, (pdy, lddy, px, ldx, pdx, lddx) = _gradient_rows(
         dtype, plan.h.batch_tokens, (plan.dev, ws) if grads is None else (plan.dev, ws, tA, tB),
         ((dy, None), (x, d_in), (dx, d_in)))
+    _fits_plan(plan, d_in, dy.shape[1], dtype, grads, device)
     _check(load().lora_sgmv_backward(_stream_handle(stream, device), DTYPES[dtype], px, ldx, d_in, pdy, lddy,
                                      dy.shape[1], plan.seg, _ptr(tA), _ptr(tB), n,
                                      LORA_GRAD_ACCUMULATE if accumulate else 0, pdx, lddx, ws.data_ptr(),
@@ -1139,7 +1166,8 @@ def sgmv_backward(x, dy, plan: Plan, grads: Optional[GradPool], dx, ws, dtype: s
 def fused_linear_backward(x, W0, dy, plan: Plan, grads: Optional[GradPool], dx, ws, dtype: str = "bf16",
                           accumulate: bool = False, stream=None):
     """Gradients of fused_linear: dx = dy W0 + u A (overwritten, every row), and the
-    adapters' gradients as in sgmv_backward (grads None: not wanted; x may then be None)."""
+    adapters' gradients as in sgmv_backward (grads None: not wanted; x may then be None;
+    the sizes that are refused are the same)."""
     d_out, d_in = W0.shape
     if not W0.is_contiguous():
         raise ValueError("W0 is contiguous [d_out, d_in]")
@@ -1148,6 +1176,7 @@ def fused_linear_backward(x, W0, dy, plan: Plan, grads: Optional[GradPool], dx, 
         dtype, plan.h.batch_tokens, (plan.dev, ws) if grads is None else (plan.dev, ws, tA, tB),
         ((dy, d_out), (x, d_in), (dx, d_in)))
     _, (pW0, _) = _gradient_rows(dtype, d_out, (), ((W0, d_in),))
+    _fits_plan(plan, d_in, d_out, dtype, grads, device)
     _check(load().lora_fused_linear_backward(_stream_handle(stream, device), DTYPES[dtype], px, ldx, d_in, pW0, pdy,
                                              lddy, d_out, plan.seg, _ptr(tA), _ptr(tB), n,
                                              LORA_GRAD_ACCUMULATE if accumulate else 0, pdx, lddx, ws.data_ptr(),

@@ -239,3 +239,110 @@ def test_binding_refuses_other_weights_and_missing_x(monkeypatch):
 def test_header_and_binding_agree():
     assert B.LORA_OP_SGMV_BACKWARD == 7 and B.LORA_GRAD_ACCUMULATE == 1
     assert ctypes.sizeof(ctypes.c_uint) == 4
+
+
+def _host_plan(ids, pool):
+    """A Plan in plain host memory whose device buffer is a fake address (nothing is launched before a refusal)."""
+    import torch
+
+    p = B.Plan.__new__(B.Plan)
+    p.capacity = max(len(ids), 1)
+    p.nbytes = B.lora_segments_bytes(p.capacity)
+    raw = torch.zeros(p.nbytes + 16, dtype=torch.uint8)
+    off = -raw.data_ptr() % 16
+    p.host, p.dev = raw[off: off + p.nbytes], _Rows((1, 1))
+    p.h, p.d = B.LoraSegments(), B.LoraSegments()
+    assert B.lora_segments_bind(p.host.data_ptr(), p.capacity, ctypes.addressof(p.h)) == 0
+    return p.build(np.asarray(ids, dtype=np.int32), pool)
+
+
+def _pool(ranks=(16, 8, 4), d_in=64, d_out=32, dtype="bf16", cls=B.DevicePool, **kw):
+    A, Bt, r, al = make_tables(len(ranks), np.random.default_rng(0), list(ranks))
+    return cls(n_adapters=len(ranks), dtype=dtype, d_in=d_in, d_out=d_out, addr_A=A, addr_B=Bt, rank=r, alpha=al,
+               **(dict(storage=None) if cls is B.DevicePool else kw))
+
+
+class _Grad:
+    """What the binding looks at of a gradient tensor on a device that is not here."""
+
+    def __init__(self, n, device=0):
+        self._n, self._d, self.device = n, device, f"cuda:{device}"
+
+    numel = lambda self: self._n  # noqa: E731
+    get_device = lambda self: self._d  # noqa: E731
+
+
+def _grads(nA, nB, device=0):
+    one = lambda n: None if n is None else _Grad(n, device)  # noqa: E731
+    return B.GradPool(None, [one(n) for n in nA], [one(n) for n in nB], _Rows((1, 1)), _Rows((1, 1)))
+
+
+def _call(fused, plan, grads, d_in=64, d_out=32, dtype="bf16"):
+    import torch
+
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    x, dy, W0 = _Rows((4, d_in), dtype=dt), _Rows((4, d_out), dtype=dt), _Rows((d_out, d_in), dtype=dt)
+    ws = _Rows((1, 1))
+    ws.numel, ws.element_size = lambda: 1 << 40, lambda: 1
+    if fused:
+        B.fused_linear_backward(x, W0, dy, plan, grads, _Rows((4, d_in), dtype=dt), ws, dtype)
+    else:
+        B.sgmv_backward(x, dy, plan, grads, _Rows((4, d_in), dtype=dt), ws, dtype)
+
+
+@pytest.fixture
+def no_device(monkeypatch):
+    """A current device 0, and a library that only notes that it was reached."""
+    import torch
+
+    reached = []
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(B, "_stream_handle", lambda *a: 0)
+    lib = B.load()
+
+    class L:
+        lora_sgmv_backward = staticmethod(lambda *a: reached.append(a) or 0)
+        lora_fused_linear_backward = staticmethod(lambda *a: reached.append(a) or 0)
+
+        def __getattr__(self, k):
+            return getattr(lib, k)
+
+    monkeypatch.setattr(B, "load", lambda: L())
+    return reached
+
+
+@pytest.mark.parametrize("fused", [False, True])
+@pytest.mark.parametrize("kw", [
+    dict(d_in=72), dict(d_in=56), dict(d_out=40), dict(d_out=24),  # other widths than the adapters': A or B past its end
+    dict(nA=[16 * 64, 0, 4 * 64 - 1]), dict(nB=[16 * 32, 0, 4 * 32 - 1]), dict(nA=[16 * 64 - 1, 0, 4 * 64]),
+    dict(nB=[8, None, None]), dict(nA=[None, None, 0]), dict(device=1), dict(pool_dtype="f32"),
+])
+def test_sizes_of_the_plans_adapters(fused, kw, no_device):
+    """Widths, type and gradients are those of the adapters that the plan was built from."""
+    pool = _pool(dtype=kw.get("pool_dtype", "bf16"))
+    plan = _host_plan([0, 2, 2, -1], pool)
+    nA, nB = kw.get("nA", [16 * 64, 0, 4 * 64]), kw.get("nB", [16 * 32, 0, 4 * 32])
+    with pytest.raises(ValueError):
+        _call(fused, plan, _grads(nA, nB, kw.get("device", 0)), kw.get("d_in", 64), kw.get("d_out", 32))
+    if {"d_in", "d_out", "pool_dtype"} & set(kw):
+        with pytest.raises(ValueError):
+            _call(fused, plan, None, kw.get("d_in", 64), kw.get("d_out", 32))
+    assert not no_device
+
+
+@pytest.mark.parametrize("fused", [False, True])
+def test_sizes_that_fit(fused, no_device):
+    """Gradients left out, larger buffers, adapters without a row, plans without an adapted row of any width; a
+    plan that is built again looks again."""
+    pool = _pool()
+    plan = _host_plan([0, 2, 2, -1], pool)
+    good = [_grads([16 * 64, 0, 4 * 64], [16 * 32, 0, 4 * 32]), _grads([None, 1, 999], [999, 1, None]), None]
+    for g in (*good, *good):
+        _call(fused, plan, g)
+    assert len(no_device) == 6
+    _call(fused, _host_plan([-1, -1], pool), None, 128, 8)
+    plan.build(np.array([1, 1, 1, 1], dtype=np.int32), pool)
+    for g in good[:2]:
+        with pytest.raises(ValueError):
+            _call(fused, plan, g)
+    assert len(no_device) == 7
