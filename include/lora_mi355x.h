@@ -676,6 +676,8 @@ int lora_fused_linear_e4m3(void *stream, const void *x, int64_t ldx, int32_t d_i
  *   to 2^24.
  *   d_in, d_out and the gradients' sizes are the caller's to keep equal to the
  *   adapters': the segments hold ranks and addresses, no widths.
+ *   The adapters are whole matrices: segments built over page tables (lora_sgmv_paged)
+ *   must not be passed, their tables would be read as A and B.
  * Precision: u and v are fp32 sums of the dtype's products; bf16 calls feed them
  * to the second products as bf16 parts (three for dA and dB, 24 significant
  * bits; two for dx, 16 bits), with fp32 accumulation; dx is rounded once.

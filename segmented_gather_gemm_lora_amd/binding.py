@@ -813,9 +813,11 @@ class Plan:
         _check(lora_segments_bind(self.host.data_ptr(), self.capacity, ctypes.addressof(self.h)), "lora_segments_bind")
         _check(lora_segments_bind(self.dev.data_ptr(), self.capacity, ctypes.addressof(self.d)), "lora_segments_bind")
 
-    # (d_in, d_out, dtype) of the pool that build() took the adapters from (the segments
-    # do not hold them), and the GradPool that was last found to fit them (weak)
+    # (d_in, d_out, dtype) of the pool that build() took the adapters from, and whether
+    # that is a PagedPool (the segments do not say); the GradPool that was last found to
+    # fit them (weak)
     made_for = None
+    paged = False
     grads_fit = None
 
     @property
@@ -827,6 +829,7 @@ class Plan:
         if ids.shape[0] > self.capacity:
             raise ValueError("batch larger than the segments' capacity")
         self.made_for, self.grads_fit = (pool.d_in, pool.d_out, pool.dtype), None
+        self.paged = isinstance(pool, PagedPool)
         st = lora_build_segments(ids.shape[0], ids.ctypes.data, pool.n_adapters, pool.addr_A.ctypes.data,
                                  pool.addr_B.ctypes.data, pool.rank.ctypes.data, pool.alpha.ctypes.data,
                                  ctypes.addressof(self.h))
@@ -1123,7 +1126,10 @@ def _gradient_rows(dtype: str, tokens: int, others, rows):
 def _fits_plan(plan: Plan, d_in: int, d_out: int, dtype: str, grads: Optional[GradPool], device: int):
     """Refuses sizes other than those of the adapters that the plan was built from: the
     kernels read A and B, and write the gradients, at the call's widths and the plan's
-    ranks.  The gradients are looked at once for each plan built."""
+    ranks.  The gradients are looked at once for each plan built.  Paged adapters have
+    no gradient calls: their page tables would be read as A and B."""
+    if plan.paged:
+        raise ValueError("the plan's adapters are paged; the gradient calls take whole matrices")
     if plan.made_for is None or plan.h.num_segments == 0:  # built without a Plan; no adapter is touched
         return
     if plan.made_for != (d_in, d_out, dtype):
@@ -1144,7 +1150,7 @@ def sgmv_backward(x, dy, plan: Plan, grads: Optional[GradPool], dx, ws, dtype: s
     """Gradients of sgmv: dx[perm] += u A (dx None: not wanted), grads.A = u^T x,
     grads.B = dy^T v over each adapter's rows (added to them with accumulate;
     grads None: not wanted).  Widths, type and gradients are those of the pool that
-    the plan was built from; others are refused."""
+    the plan was built from; others are refused, and so are plans of a PagedPool."""
     if x is not None or dx is not None:
         d_in = (dx if x is None else x).shape[-1]
     elif grads is not None:
@@ -1167,7 +1173,7 @@ def fused_linear_backward(x, W0, dy, plan: Plan, grads: Optional[GradPool], dx, 
                           accumulate: bool = False, stream=None):
     """Gradients of fused_linear: dx = dy W0 + u A (overwritten, every row), and the
     adapters' gradients as in sgmv_backward (grads None: not wanted; x may then be None;
-    the sizes that are refused are the same)."""
+    what is refused is the same)."""
     d_out, d_in = W0.shape
     if not W0.is_contiguous():
         raise ValueError("W0 is contiguous [d_out, d_in]")

@@ -346,3 +346,18 @@ def test_sizes_that_fit(fused, no_device):
         with pytest.raises(ValueError):
             _call(fused, plan, g)
     assert len(no_device) == 7
+
+
+@pytest.mark.parametrize("fused", [False, True])
+def test_paged_adapters_are_refused(fused, no_device):
+    """A PagedPool's addresses are page tables, not matrices; a plan built again from whole matrices is taken."""
+    none = {k: None for k in ("pages", "tables", "table_host", "frames_A", "frames_B", "alloc")}
+    paged = _pool(cls=B.PagedPool, page_bytes=4096, **none)
+    plan = _host_plan([0, 2, 2, -1], paged)
+    for grads in (None, B.GradPool(None, [None] * 3, [None] * 3, _Rows((1, 1)), _Rows((1, 1)))):
+        with pytest.raises(ValueError, match="paged"):
+            _call(fused, plan, grads)
+    assert not no_device
+    plan.build(np.array([0, 2], dtype=np.int32), _pool())
+    _call(fused, plan, None)
+    assert len(no_device) == 1
