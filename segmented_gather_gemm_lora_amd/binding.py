@@ -1213,13 +1213,18 @@ class AdamW:
     tensors that receive the rounded parameters.  groups[i] is the entry of
     `hyper` (see adamw_hyper) that tensor i goes by.  state: "f32" or "8bit";
     m, v (and m_scale, v_scale for 8-bit states) are lists of state tensors, made
-    here as zeros when not given."""
+    here as zeros when not given.  stream: where the plan is uploaded.  The states
+    and the plan are complete when the constructor returns (it waits for the current
+    stream and for `stream`, so it is not for a captured region), so that steps may go
+    to any stream; they are used until the steps given are done."""
 
     def __init__(self, params, grads, groups, hyper, state: str = "f32", copies=None, m=None, v=None, m_scale=None,
                  v_scale=None, stream=None):
         torch = _torch()
         if state not in ("f32", "8bit"):
             raise ValueError("state is 'f32' or '8bit'")
+        if hyper.is_cuda and torch.cuda.is_current_stream_capturing():
+            raise ValueError("AdamW is built outside of a captured region; its steps may be captured")
         eight, device = state == "8bit", params[0].device if params else hyper.device
         made = lambda given, size, dt: given if given is not None else [  # noqa: E731
             torch.zeros(size(p.numel()), dtype=dt, device=p.device) for p in params]
@@ -1261,8 +1266,14 @@ class AdamW:
         _check(lib.lora_adamw_plan(arr, n, hyper.shape[0], LORA_ADAM_8BIT if eight else LORA_ADAM_F32,
                                    LORA_BF16 if gdt == torch.bfloat16 else LORA_F32, _ptr(self._host), nbytes),
                "lora_adamw_plan")
+        # zeros and the plan's memory belong to the current stream, the upload to `stream`,
+        # the steps to others: each waits for the one before
+        made_on = torch.cuda.current_stream()
+        if stream is not None:
+            made_on.synchronize()
         _check(lib.lora_adamw_upload(_ptr(self._host), _ptr(self._dev), nbytes, _stream_handle(stream)),
                "lora_adamw_upload")
+        (stream or made_on).synchronize()
         self._fn, self._device = lib.lora_adamw, hyper.get_device()
         self._args = (_vp(_ptr(self._host)), _vp(_ptr(self._dev)), _vp(_ptr(hyper)), _i32(hyper.shape[0]))
 

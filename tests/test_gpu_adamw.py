@@ -291,3 +291,47 @@ def test_training_step_of_a_pool():
         want = p.scale[i] * (x[rows] @ A.t()) @ Bm.t()
         err = (y[rows].double().cpu() - want).abs()
         assert (err <= 2e-2 * (want.abs() + 1e-2)).all()
+
+
+@pytest.mark.parametrize("where", ["side", "current", "side twice"])
+@pytest.mark.parametrize("state", ["f32", "8bit"])
+def test_built_on_one_stream_stepped_on_another(state, where):
+    """Built while its stream is busy, stepped at once on another: the plan and the zeroed states are there."""
+    g = [torch.randn(n, device="cuda") for n in (5000, 700)]
+    table = table_of(HYPER[:1])
+    want = [torch.ones_like(t) for t in g]
+    ref = B.AdamW(want, g, [0, 0], table, state=state)
+    ref.step()
+    p = [torch.ones_like(t) for t in g]
+    junk = [torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda") for n in (5000, 20000, 20000, 5000, 700, 700)]
+    torch.cuda.synchronize()
+    del junk  # what the states and the plan are made in
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    busy, step = {"side": (a, None), "current": (torch.cuda.current_stream(), b), "side twice": (a, b)}[where]
+    with torch.cuda.stream(busy):
+        torch.cuda._sleep(20_000_000)
+    o = B.AdamW(p, g, [0, 0], table, state=state, stream=None if where == "current" else a)
+    o.step(stream=step)
+    torch.cuda.synchronize()
+    for t, w in zip((*p, *o.m, *o.v), (*want, *ref.m, *ref.v)):
+        assert torch.equal(t, w)
+
+
+def test_building_in_a_captured_region_is_refused():
+    p, g = torch.zeros(64, device="cuda"), torch.ones(64, device="cuda")
+    table = table_of(HYPER[:1])
+    opt = B.AdamW([p], [g], [0], table)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        with pytest.raises(ValueError, match="captured"):
+            B.AdamW([p], [g], [0], table)
+        opt.step()
+    q = torch.zeros(64, device="cuda")
+    eager = B.AdamW([q], [g], [0], table)
+    for k in range(3):
+        graph.replay()
+        eager.step()
+        torch.cuda.synchronize()
+        assert torch.equal(p, q), k
