@@ -335,3 +335,25 @@ def test_building_in_a_captured_region_is_refused():
         eager.step()
         torch.cuda.synchronize()
         assert torch.equal(p, q), k
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-20])
+@pytest.mark.parametrize("step", [1, 5000])
+@pytest.mark.parametrize("state,size", [("f32", 1e-20), ("f32", 2e-19), ("8bit", 1e-20), ("8bit", 2e-18)])
+def test_subnormal_second_moments(state, size, step, eps):
+    """v / (1 - b2^t) below fp32's normal range is not taken as 0: the root keeps what v has."""
+    r = np.random.default_rng(5)
+    h = dict(HYPER[0], eps=eps, weight_decay=0.0, step=step)
+    g = (np.sign(r.standard_normal(600)) * (1 + r.random(600)) * size).astype(np.float32)
+    m0, v0 = (g, (g.astype(np.float64) ** 2).astype(np.float32)) if state == "f32" else (np.zeros_like(g),) * 2
+    p = torch.zeros(600, device="cuda")
+    more = {} if state == "8bit" else {k: [torch.from_numpy(x.copy()).cuda()] for k, x in (("m", m0), ("v", v0))}
+    o = B.AdamW([p], [torch.from_numpy(g).cuda()], [0], table_of([h]), state=state, **more)
+    o.step()
+    torch.cuda.synchronize()
+    want, bound, _, v = R.step(np.zeros(600), g, m0, v0, h)
+    # the quotient v / bc2 is rounded to a multiple of 2^-149 (half of one off, at most), and its root
+    # moves by half as much, relative to it
+    vhat = v.astype(np.float64) / (1 - float(np.float32(h["beta2"])) ** step)
+    bound = bound + np.abs(want) * 2.0**-150 / vhat
+    assert (v > 0).all() and (np.abs(p.double().cpu().numpy() - want) <= bound).all()
