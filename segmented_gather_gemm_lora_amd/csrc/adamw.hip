@@ -42,12 +42,15 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kBlock = LORA_ADAM_BLOCK; // elements of a state block: 4 per lane of a wave
 constexpr int kAdamThreads = 256;
 constexpr int kRow = 4 * kAdamThreads; // elements that a workgroup takes at a time
-// Elements of a chunk: two rows for many elements with 8-bit states, whose
-// arithmetic shows (the record, the group's numbers and its powers are read and
-// formed once for them: 100 M elements in 345 us, 407 with one row; four and
-// eight rows alike); one row where there are few (131072 elements: 3.5 us, 5.4
-// with four) and with fp32 states (16.8 M elements: 80 us, 88 with two).
-constexpr int64_t kFewElements = 1 << 22;
+// Elements of a chunk: one row, or two where there are many with 8-bit states, whose
+// arithmetic shows (the record, the group's numbers and its powers are read and formed
+// once for both).  8-bit states, one / two rows, us.  fp32 gradients: 0.5 M elements
+// 4.8 / 5.6, 1 M 6.5 / 6.7, 2 M 10.8 / 10.1, 8 M 34 / 31, 24 M 90 / 82, 48 M 171 / 166;
+// from 64 M on 5% the other way for steps one after the other (96 M 330 / 347), nothing
+// with other work between, and the first steps 520 / 480: left alone.  bf16 gradients:
+// 1 M 6.7 / 7.4, 1.5 M 9.0 / 9.2, 24 M 90 / 82, 96 M 308 / 285, 128 M 401 / 373.  fp32
+// states, 16.8 M elements: 80 / 88.
+constexpr int64_t kFewElements = 1 << 21;
 int chunk_of(int64_t elements, bool eight) { return eight && elements > kFewElements ? 2 * kRow : kRow; }
 
 constexpr uint32_t kAdamMagic = 0x4C6F4164u;

@@ -209,3 +209,20 @@ def test_reference_step_against_torch():
         # bound has p's rounding and 24 steps for the update; m and v in fp32 add 4 steps
         # to an update of at most lr (1 + 0.1 |p|)
         assert (np.abs(q.detach().numpy() - new) <= t * (bound + 4 * 2.0**-23 * 1e-2 * (1 + np.abs(new)))).all()
+
+
+@pytest.mark.parametrize("n,state,gdt,chunk", [
+    (1 << 21, 1, 0, 1024), ((1 << 21) + 1, 1, 0, 2048), ((1 << 21) + 1, 1, 1, 2048), (1 << 24, 0, 0, 1024), (1000, 1, 1, 1024),
+])
+def test_elements_of_a_chunk(n, state, gdt, chunk):
+    """Two rows of 1024 for many 8-bit elements; the records cover the tensor once either way."""
+    one = dict(param=FX, grad=FX + (1 << 32), copy=0, m=FX + (2 << 32), v=FX + (3 << 32), m_scale=FX + (4 << 32),
+               v_scale=FX + (5 << 32), n=n, group=0, reserved=0)
+    st, raw, ptr, need = plan([B.LoraAdamTensor(*(one[k] for k, _ in B.LoraAdamTensor._fields_))], state=state, gdt=gdt)
+    assert st == "LORA_OK"
+    off = ptr - raw.ctypes.data
+    rows = (n + chunk - 1) // chunk
+    at = raw[off + 32: off + 32 + 80 * rows].reshape(rows, 80)
+    e0, k = at[:, 56:60].copy().view("<u4")[:, 0], at[:, 60:64].copy().view("<i4")[:, 0]
+    assert np.array_equal(e0, chunk * np.arange(rows)) and k.sum() == n and (k[:-1] == chunk).all()
+    assert not raw[off + 32 + 80 * rows: off + need].any()

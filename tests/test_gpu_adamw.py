@@ -357,3 +357,12 @@ def test_subnormal_second_moments(state, size, step, eps):
     vhat = v.astype(np.float64) / (1 - float(np.float32(h["beta2"])) ** step)
     bound = bound + np.abs(want) * 2.0**-150 / vhat
     assert (v > 0).all() and (np.abs(p.double().cpu().numpy() - want) <= bound).all()
+
+
+def test_many_elements_of_bf16_gradients():
+    """Two rows a chunk, bf16 gradients."""
+    c = Case([1, 1025, 2047, 2049, (1 << 20) + 3, 300, (1 << 20) + 1029, 5], "8bit", torch.bfloat16)
+    assert sum(c.sizes) > 1 << 21
+    c.opt.step()
+    torch.cuda.synchronize()
+    c.check()
