@@ -206,3 +206,57 @@ def test_large_layer():
     bound += 2.0**-8 * np.abs(dx)
     err = np.abs(d.dx.double().cpu().numpy()[rows] - dx)
     assert (err <= bound).all(), float((err / bound).max())
+
+
+def _copies(d):
+    return [t.clone() for t in (d.dx, *d.grads.A, *d.grads.B)]
+
+
+# T 90: the sum over d_out in parts; 2100 rows, 4104 columns: whole
+@pytest.mark.parametrize("T,d_in,d_out", [(90, 264, 2056), (2100, 4104, 72)])
+def test_accumulate_and_partial_requests(T, d_in, d_out):
+    p = Problem("bf16", ids_of("mixed", T, 3, 7), [16, 8, 33], d_in, d_out, seed=7, w0=True)
+    d = p.device()
+    call(p, d)
+    torch.cuda.synchronize()
+    check(p, d, f"T={T}")
+    first = _copies(d)
+    # added to the gradients, not to dx
+    call(p, d, accumulate=True)
+    torch.cuda.synchronize()
+    assert torch.equal(d.dx, first[0])
+    assert all(torch.equal(t, f + f) for t, f in zip((*d.grads.A, *d.grads.B), first[1:]))
+    # single gradients left out, and all of a kind
+    for A, Bm in (([0, None, 2], [None, 1, 2]), ([None] * 3, [0, 1, 2]), ([0, 1, 2], [None] * 3)):
+        e = p.device()
+        g = B.GradPool.from_tensors([None if i is None else e.grads.A[i] for i in A],
+                                    [None if i is None else e.grads.B[i] for i in Bm], device="cuda")
+        for t in (*e.grads.A, *e.grads.B):
+            t.fill_(7.0)
+        call(p, e, grads=g)
+        torch.cuda.synchronize()
+        assert torch.equal(e.dx, first[0])
+        for i in range(3):
+            for at, got, f in ((A[i], e.grads.A[i], first[1 + i]), (Bm[i], e.grads.B[i], first[4 + i])):
+                assert (got == 7).all() if at is None else torch.equal(got, f)
+
+
+def test_two_streams_at_once():
+    """Two batches on two streams, each with its own workspace: the same bits as one after the other."""
+    ps = [Problem("bf16", ids_of("mixed", T, 4, T), [16, 64, 100, 8], 264, 2080, seed=T, w0=True) for T in (70, 900)]
+    ds = [p.device() for p in ps]
+    for p, d in zip(ps, ds):
+        call(p, d)
+    torch.cuda.synchronize()
+    want = [_copies(d) for d in ds]
+    streams = [torch.cuda.Stream() for _ in ds]
+    for k in range(4):
+        for d in ds:
+            for t in (d.dx, *d.grads.A, *d.grads.B):
+                t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for p, d, s in zip(ps, ds, streams):
+            call(p, d, stream=s)
+        torch.cuda.synchronize()
+        for d, w in zip(ds, want):
+            assert all(torch.equal(a, b) for a, b in zip(_copies(d), w)), k
