@@ -681,6 +681,10 @@ int lora_fused_linear_e4m3(void *stream, const void *x, int64_t ldx, int32_t d_i
  * Precision: u and v are fp32 sums of the dtype's products; bf16 calls feed them
  * to the second products as bf16 parts (three for dA and dB, 24 significant
  * bits; two for dx, 16 bits), with fp32 accumulation; dx is rounded once.
+ * An infinity, or a u or v above the largest bf16 (3.39e38), makes the results that
+ * it enters infinite or NaN: the parts' products with an infinity, or of an infinite
+ * part with 0, can be NaN where one product is infinite.  Results that it does not
+ * enter (other adapters' gradients, other rows of dx) are not touched.
  * Every sum has a fixed order: results are the same from run to run.
  * Needs ws_bytes >= lora_workspace_bytes(LORA_OP_SGMV_BACKWARD, T, d_in, d_out,
  * max_rank), T and max_rank as in lora_sgmv; the workspace needs no preparation.
@@ -731,8 +735,14 @@ int lora_fused_linear_backward(void *stream, int dtype, const void *x, int64_t l
  * of all zero bytes is zero.  The 8-bit states are rounded stochastically, with
  * random bits from a hash of the group's seed and step, the tensor's number in
  * the plan and the element's index (the same inputs give the same state); a
- * positive v is never rounded to 0.  A gradient that is not finite makes its own
- * element's p, m and v NaN and touches no other element. */
+ * positive v is never rounded to 0.  Codes are those of the fp32 m and v: where
+ * value and random bits together lie within fp32's rounding of a code, the code of
+ * the exact value can be the neighbour.
+ * What is not finite touches no other element.  A NaN gradient makes its element's
+ * p, m and v NaN; an infinite one p NaN, m and v infinite.  |grad_scale grad| from
+ * 1.85e19 (sqrt(FLT_MAX)) on makes g g, and v, infinite: its element's m / sqrt(v) is
+ * 0 from then on.  8-bit states hold an infinite m or v as NaN, so p is NaN from the
+ * next step on.  eps is 0 or at least 2^-126. */
 #define LORA_ADAM_F32 0
 #define LORA_ADAM_8BIT 1
 #define LORA_ADAM_BLOCK 256

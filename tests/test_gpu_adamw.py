@@ -366,3 +366,59 @@ def test_many_elements_of_bf16_gradients():
     c.opt.step()
     torch.cuda.synchronize()
     c.check()
+
+
+@pytest.mark.parametrize("state", ["f32", "8bit"])
+def test_states_of_bad_and_huge_gradients(state):
+    """m and v of gradients that are not finite, and of finite ones whose square is not."""
+    bad = {3: np.nan, 300: np.inf, 301: -np.inf, 500: 1.9e19, 501: -3e38, 700: 1.8e19}
+
+    def make(n):
+        g = np.random.default_rng(2).standard_normal(n).astype(np.float32)
+        for k, x in bad.items():
+            g[k] = x
+        return g
+
+    h = dict(HYPER[0], step=3)
+    c = Case([1000], state, hs=[h], make_g=make)
+    before = c.host[0]["p"].copy()
+    c.opt.step()
+    torch.cuda.synchronize()
+    d = c.dev[0]
+    p = d["p"].cpu().numpy()
+    if state == "f32":
+        m, v = d["m"].cpu().numpy(), d["v"].cpu().numpy()
+        h0 = c.host[0]
+        _, _, wm, wv = R.step(before, h0["g"], h0["m"], h0["v"], h)
+        assert np.array_equal(m, wm, equal_nan=True) and np.array_equal(v, wv, equal_nan=True)
+        assert np.isnan(m[3]) and m[300] == np.inf and m[301] == -np.inf and np.isfinite(m[[500, 501, 700]]).all()
+        assert np.isnan(v[3]) and (v[[300, 301, 500, 501]] == np.inf).all() and np.isfinite(v[700])
+    else:
+        mo, vo = torch.empty(1000, dtype=torch.bfloat16, device="cuda"), torch.empty(1000, dtype=torch.bfloat16, device="cuda")
+        B.adamw_state_values(d["m"], d["m_scale"], d["v"], d["v_scale"], mo, vo)
+        m, v = mo.float().cpu().numpy(), vo.float().cpu().numpy()
+        assert np.array_equal(np.isnan(m), np.isin(np.arange(1000), [3, 300, 301]))
+        assert np.array_equal(np.isnan(v), np.isin(np.arange(1000), [3, 300, 301, 500, 501]))
+    assert np.array_equal(np.isnan(p), np.isin(np.arange(1000), [3, 300, 301])) and np.isfinite(p[[500, 501, 700]]).all()
+    decay = 1 - float(np.float32(h["lr"])) * float(np.float32(h["weight_decay"]))
+    # m / infinity is 0: the element only decays (24 steps of the decay, half a step of p)
+    want = before[[500, 501]].astype(np.float64) * decay
+    assert (np.abs(p[[500, 501]] - want) <= 2.0**-24 * np.abs(want) + 24 * 2.0**-23 * (1 - decay) * np.abs(want)).all()
+    # the next step, with gradients of order 1
+    d["g"].normal_()
+    c.hyper[:, 6] += 1
+    c.opt.step()
+    torch.cuda.synchronize()
+    lost = [3, 300, 301] if state == "f32" else [3, 300, 301, 500, 501]
+    assert np.array_equal(np.isnan(d["p"].cpu().numpy()), np.isin(np.arange(1000), lost))
+
+
+def test_huge_gradients_by_the_formula():
+    """The same in 64 bits: with g g finite in fp32 nothing is lost."""
+    g = np.array([1.8e19, -1.8e19, 1e19, 3.0], dtype=np.float32)
+    p = torch.ones(4, device="cuda")
+    o = B.AdamW([p], [torch.from_numpy(g).cuda()], [0], table_of(HYPER[:1]))
+    o.step()
+    torch.cuda.synchronize()
+    want, bound, *_ = R.step(np.ones(4), g, np.zeros(4), np.zeros(4), HYPER[0])
+    assert (np.abs(p.double().cpu().numpy() - want) <= bound).all()

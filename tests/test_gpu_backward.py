@@ -342,3 +342,39 @@ def test_larger_workspace_request_covers_smaller_batches():
     call(p, d)
     torch.cuda.synchronize()
     check(p, d)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("where", ["x", "dy", "A", "B"])
+def test_one_infinity_enters_what_the_formulas_say(dtype, where):
+    """A single infinity: results whose sums hold it are infinite or NaN, all others are as without it."""
+    from backward_ref import worst
+
+    ids = ids_of("mixed", 90, 3, 21)
+    p, q = (Problem(dtype, ids, [16, 8, 40], 136, 72, seed=21) for _ in range(2))
+    t = int(np.nonzero(ids == 1)[0][3])
+    dst, at = {"x": (p.x_full, (t, 17)), "dy": (p.dy_full, (t, 33)), "A": (p.A[1], (5, 17)), "B": (p.B[1], (33, 5))}[where]
+    dst[at] = float("inf")
+    d = p.device()
+    call(p, d)
+    torch.cuda.synchronize()
+    (dx, dA, dB), (edx, eA, eB) = q.reference()
+    # u = s dy B, v = s x A^T: rows (of the batch) and ranks that hold the infinity
+    hit = ids == 1 if where in ("A", "B") else np.arange(90) == t
+    in_dx, in_A, in_B = np.zeros(dx.shape, bool), np.zeros(dA[1].shape, bool), np.zeros(dB[1].shape, bool)
+    if where == "x":  # v[t]: every rank; x's own column of dA
+        in_A[:, 17], in_B[:] = True, True
+    elif where == "dy":  # u[t]: every rank; dy's own row of dB
+        in_dx[hit], in_A[:], in_B[33] = True, True, True
+    elif where == "A":  # v's rank 5; u times A's column 17
+        in_dx[np.ix_(hit, [17])] = True
+        in_B[:, 5] = True
+    else:  # u's rank 5
+        in_dx[hit], in_A[5] = True, True
+    for got, want, e, bad in ((d.dx, dx, edx, in_dx), (d.grads.A[1], dA[1], eA[1], in_A), (d.grads.B[1], dB[1], eB[1], in_B)):
+        got = got.double().cpu().numpy().reshape(want.shape)
+        assert not np.isfinite(got[bad]).any()
+        assert worst(got[~bad], want[~bad], e[~bad]) <= 1
+    for i in (0, 2):
+        assert worst(d.grads.A[i].double().cpu().numpy(), dA[i], eA[i]) <= 1
+        assert worst(d.grads.B[i].double().cpu().numpy(), dB[i], eB[i]) <= 1
