@@ -398,14 +398,27 @@ int splits_of(int64_t tiles, int32_t d_out)
     return int(std::max<int64_t>(1, std::min<int64_t>({kFill / tiles, stages / 16, kMaxSplits})));
 }
 
-// Rows of a tile: 256 where such tiles and their splits take more than half of the
-// chip, and not for up to 128 rows, which leave them half empty (64 / 256 rows, GEMM
-// and join, us.  4096 columns, d_out 4096: 128 rows 21 / 28, 256 rows 26 / 35, 512 rows
-// 38 / 42; d_out 14336: 40 / 45, 60 / 55, 103 / 77; 1024 columns, 256 rows 20 / 32).
+// Stages that a CU goes through one after the other: rounds of workgroups, times a
+// workgroup's.
+int64_t stages_of_cu(int64_t tiles, int32_t d_out)
+{
+    const int64_t splits = splits_of(tiles, d_out), stages = (int64_t(d_out) + kBK - 1) / kBK;
+    return (tiles * splits + kFill - 1) / kFill * ((stages + splits - 1) / splits);
+}
+
+// Rows of a tile.  A stage takes 0.39 us with 64 rows and 0.87 with 256, which also
+// begin and end later (by the time of some 40 of the small stages): so 256 where 64
+// rows would go through more than 2 s + 36 stages, s those of 256 rows.  Over 260
+// sizes (T 96 to 2048, d_in and d_out 1024 to 14336) the other choice would have been
+// over 5% faster in 10, by 28% at most.  64 / 256 rows, us, u, GEMM and join.  d 4096 ->
+// 4096: 256 rows 30 / 39, 512 40 / 51, 640 54 / 52, 1024 55 / 64 (256 is taken), 1536
+// 100 / 82; d_in 4096, d_out 14336: 192 rows 68 / 71, 384 117 / 89, 1024 198 / 138; d_in
+// 1024, d_out 8192: 512 rows 33 / 42, 1024 43 / 54.
 int rows_of(int32_t T, int32_t d_in, int32_t d_out)
 {
-    const int64_t tiles = (int64_t(T) + 255) / 256 * ((int64_t(d_in) + kCols - 1) / kCols);
-    return T <= 128 || tiles * splits_of(tiles, d_out) <= kFill / 2 ? 64 : 256;
+    const int64_t cols = (int64_t(d_in) + kCols - 1) / kCols;
+    const int64_t few = stages_of_cu((int64_t(T) + 63) / 64 * cols, d_out);
+    return few <= 2 * stages_of_cu((int64_t(T) + 255) / 256 * cols, d_out) + 36 ? 64 : 256;
 }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }

@@ -260,3 +260,34 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         for d, w in zip(ds, want):
             assert all(torch.equal(a, b) for a, b in zip(_copies(d), w)), k
+
+
+LARGE = [  # long sums over d_out: tiles of 256 rows, the sum in parts (up to 1100 rows) and whole
+    (1100, 4104, 2050, [16, 8, 64], "mixed"),
+    (1061, 4096, 2048, [16] * 40, "runs"),
+    (2100, 4104, 2050, [33, 8, 100], "mixed"),
+    (2305, 3848, 2079, [16] * 300, "runs"),
+]
+
+
+@pytest.mark.parametrize("T,d_in,d_out,ranks,kind", LARGE)
+def test_long_sums(T, d_in, d_out, ranks, kind):
+    test_against_64_bits(T, d_in, d_out, ranks, kind)
+
+
+@pytest.mark.parametrize("T", [1100, 2100])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_bad_values_stay_with_their_rows_in_long_sums(value, T):
+    from backward_ref import worst
+
+    ids = ids_of("runs", T, 4, 12)
+    p, q = (Problem("bf16", ids, [16, 8, 20, 64], 4104, 2053, seed=12, w0=True, pad=(0, 3, 0)) for _ in range(2))
+    p.dy_full[np.nonzero(ids == 2)[0]] = value
+    p.A[2].fill_(value)
+    p.B[2].fill_(value)
+    d = p.device()
+    call(p, d)
+    torch.cuda.synchronize()
+    keep = np.nonzero(ids != 2)[0]
+    (dx, _, _), (edx, _, _) = q.reference()
+    assert worst(d.dx.double().cpu().numpy()[keep], dx[keep], edx[keep]) <= 1
