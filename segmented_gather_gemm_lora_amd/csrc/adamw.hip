@@ -25,6 +25,7 @@
 // One workgroup takes one chunk, described by one record (addresses at the
 // chunk's start), and a wave 256 consecutive elements at a time, so that a
 // state block's maximum is a reduction over one wave.
+#include "device.h"
 #include "internal.h"
 
 #include <algorithm>
@@ -34,10 +35,6 @@
 
 namespace lora {
 namespace {
-
-typedef float floatx4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kBlock = LORA_ADAM_BLOCK; // elements of a state block: 4 per lane of a wave
 constexpr int kAdamThreads = 256;
@@ -72,9 +69,6 @@ struct AdamHeader {
     uint64_t bytes;
 };
 static_assert(sizeof(AdamHeader) == 32, "plan header");
-
-__device__ __forceinline__ uint32_t f32_to_bf16(float f) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f)); }
-__device__ __forceinline__ float bf16_to_f32(uint32_t h) { return __uint_as_float(h << 16); }
 
 // Multiply and xor-shift mixing of 32 bits (the fractions of sqrt 2 and sqrt 3
 // as odd multipliers): every input bit reaches every output bit.

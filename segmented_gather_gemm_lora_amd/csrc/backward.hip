@@ -42,6 +42,7 @@
 // fp32 gradients keep fp32 accuracy; for dx, which is rounded to bf16, as two
 // (16 significant bits, as in the forward's expand).  fp32 calls multiply
 // exactly.
+#include "device.h"
 #include "internal.h"
 
 #include <algorithm>
@@ -50,36 +51,9 @@
 namespace lora {
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float floatx4 __attribute__((ext_vector_type(4)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
-template <typename T> using gptr = const __attribute__((address_space(1))) T *;
 typedef __attribute__((address_space(1))) float *gfloat; // written
 typedef __attribute__((address_space(1))) floatx4 *gfloatx4;
-template <typename T> __device__ __forceinline__ gptr<T> as_global(const void *p) { return (gptr<T>)(p); }
 
-__device__ __forceinline__ float bf16_to_f32(uint32_t h) { return __uint_as_float(h << 16); }
-__device__ __forceinline__ uint32_t f32_to_bf16(float f)
-{
-    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f)); // nearest even, NaN stays NaN
-}
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
-{
-    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-    const bf16x2_t v = {static_cast<__bf16>(lo), static_cast<__bf16>(hi)};
-    return __builtin_bit_cast(uint32_t, v);
-}
-
-// Lane i of every 16 lanes gives the address of 4 elements of row i / 4, at
-// column group i % 4, and receives column i of the 4 rows.
-__device__ __forceinline__ u32x2 read_tr(const char *lds)
-{
-    typedef __attribute__((address_space(3))) s16x4 lds4;
-    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(lds)));
-}
 __device__ __forceinline__ bf16x8 join8(u32x2 a, u32x2 b)
 {
     return __builtin_bit_cast(bf16x8, u32x4{a[0], a[1], b[0], b[1]});
@@ -94,7 +68,6 @@ __device__ __forceinline__ u32x4 load16(const void *base, uint32_t off)
 // 16 bytes from or to a place that is aligned to its elements alone.
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 template <class T> __device__ __forceinline__ u32x4 load16_any(gptr<T> p) { return *(gptr<u32x4_any>)(p); }
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 constexpr int kWin = 32; // sorted positions of one step over rows; u and v are stored in windows of it
 constexpr int kPieces = 64 * 16; // bytes of one operand: 16 per lane
@@ -550,17 +523,6 @@ __global__ __launch_bounds__(kShrinkWaves * 64) __attribute__((amdgpu_waves_per_
 // bytes at the copy rate 52; ring of 4: 104), by blocks of 16 rows 125.
 constexpr int kRing = 3;
 
-__device__ const uint32_t g_zeros[4] = {0, 0, 0, 0};
-
-constexpr int waitcnt_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4); } // and lgkmcnt(0)
-
-// 16 bytes per lane to LDS at m0 + 16 lane (published by an explicit vmcnt wait and
-// a barrier; nothing else uses m0).
-__device__ __forceinline__ void dma16(const void *g, uint32_t lds_byte)
-{
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(lds_byte) : "memory");
-}
-
 __global__ __launch_bounds__(256) void bwd_shrink_ring_kernel(BwdArgs a)
 {
     constexpr int RT = 4, kXBytes = 64 * 128, kWBytes = 64 * 128, kStage = kXBytes + kWBytes;
@@ -623,7 +585,7 @@ __global__ __launch_bounds__(256) void bwd_shrink_ring_kernel(BwdArgs a)
         // this wave's loads of stage i are done, then every wave's, and every wave
         // has read stage i - 1
         asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(waitcnt_vm(2 * kDma * (kRing - 2)));
+        __builtin_amdgcn_s_waitcnt(wait_vm_lds0(2 * kDma * (kRing - 2)));
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         issue(i + kRing - 1);
@@ -648,7 +610,7 @@ __global__ __launch_bounds__(256) void bwd_shrink_ring_kernel(BwdArgs a)
         }
     }
     // no direct load may still be writing the ring, and every wave is past its reads
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    __builtin_amdgcn_s_waitcnt(wait_vm_lds0(0));
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     // u or v through LDS, so that whole 16-byte pieces of the operands are stored
@@ -897,7 +859,7 @@ __device__ __forceinline__ void grad_item(const BwdArgs &a, const GradSide &sd, 
         if (kShareU<DT, RT>) {
             // window w is there, every wave's part of it, and every wave is past the one before
             asm volatile("" ::: "memory");
-            __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+            __builtin_amdgcn_s_waitcnt(wait_vm_lds0(0));
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
             if (w < w1) share_load(a, sd, w + 1, rt0, share_at, wave, lane);
@@ -1231,8 +1193,6 @@ template <bool VEC> __global__ __launch_bounds__(kDxWaves * 64, 4) void bwd_join
     __shared__ __attribute__((aligned(16))) char tiles_lds[kDxWaves * kWaveTile];
     dx_unit<LORA_BF16, VEC, true, 1>(a, blockIdx.x, tiles_lds);
 }
-
-size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Sorted positions of one span, a power of two of windows.  Items of the whole
 // batch are wanted, since a segment over k spans costs k partial sums and a launch:

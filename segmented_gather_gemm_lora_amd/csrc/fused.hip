@@ -44,17 +44,11 @@
 // accumulators hold x q + (scale_s / w0_scale) v B_s, which is multiplied by
 // w0_scale once before the store; the prep pass divides scale_s * v by
 // w0_scale.
+#include "device.h"
 #include "internal.h"
 
 namespace lora {
 namespace {
-
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float floatx4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
-template <typename T> using gptr = const __attribute__((address_space(1))) T *;
-template <typename T> __device__ __forceinline__ gptr<T> as_global(const void *p) { return (gptr<T>)(p); }
 
 constexpr int kBN = 192;                 // output columns per workgroup
 constexpr int kBM = 256;                 // plan rows per workgroup
@@ -99,20 +93,6 @@ template <bool W8> struct Geo {
     static_assert(kStages - 2 - kAhead >= 1, "ring depth");
 };
 
-__device__ __forceinline__ uint32_t f32_to_bf16(float f)
-{
-    // v_cvt_pk_bf16_f32: round to nearest even, NaN stays a (quiet) NaN
-    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f));
-}
-// two fp32 -> packed bf16 (lo in bits 15:0), one conversion instruction
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
-{
-    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-    const bf16x2_t v = {static_cast<__bf16>(lo), static_cast<__bf16>(hi)};
-    return __builtin_bit_cast(uint32_t, v);
-}
-__device__ __forceinline__ float bf16_to_f32(uint32_t h) { return __uint_as_float(h << 16); }
-
 // Wave-tile column of MFMA row m in column tile j: lane group g of the output
 // then holds columns 24 g + 4 j + q (q < 4), i.e. 24 consecutive columns.
 __device__ __forceinline__ int wave_col(int m, int j) { return (m >> 2) * 24 + 4 * j + (m & 3); }
@@ -140,23 +120,7 @@ __device__ __forceinline__ bf16x8 e4m3x8_to_bf16(uint32_t lo, uint32_t hi)
     return __builtin_bit_cast(bf16x8, u);
 }
 
-// s_waitcnt immediate for vmcnt(n) (gfx9 encoding: vmcnt in bits 3:0 and
-// 15:14, expcnt in 6:4, lgkmcnt in 11:8).  Written through the builtin, so that the compiler's
-// own wait insertion knows about them.
-constexpr int waitcnt_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
-// s_waitcnt immediate for lgkmcnt(0) alone
-constexpr int kWaitLgkm0 = 15 | (3 << 14) | (7 << 4);
-
-// 16 bytes per lane from global memory to LDS at m0 + 16 * lane.  The
-// compiler does not see this write to LDS; the kernel waits for it with an
-// explicit vmcnt before the barrier that publishes the stage.  dma16s: the
-// address is a wave-uniform base plus a 32-bit per-lane byte offset.  m0 is
-// a reserved register (never allocated by the compiler) and no other code in
-// these kernels reads it.
-__device__ __forceinline__ void dma16(const void *g, uint32_t lds_byte)
-{
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(lds_byte) : "memory");
-}
+// dma16 from a wave-uniform base plus a 32-bit per-lane byte offset.
 __device__ __forceinline__ void dma16s(const void *base, uint32_t off, uint32_t lds_byte)
 {
     asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds_byte)
@@ -521,12 +485,12 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
         // after the barrier every wave is past its reads of stage kt (and of
         // bf16 tile kt % 2, which stage kt + 2 reuses), so the ring slot of
         // stage kt - 1 is free for stage kt + kStages - 1
-        if (nw == kWDma) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kDma * (kStages - 2 - kAhead)));
-        else __builtin_amdgcn_s_waitcnt(waitcnt_vm((kDma - 1) * (kStages - 2 - kAhead)));
+        if (nw == kWDma) __builtin_amdgcn_s_waitcnt(wait_vm(kDma * (kStages - 2 - kAhead)));
+        else __builtin_amdgcn_s_waitcnt(wait_vm((kDma - 1) * (kStages - 2 - kAhead)));
         // E4M3: this wave's reads of tile kt % 2 (stage kt's fragments,
         // issued in the previous stage) are complete before any wave passes
         // the barrier and widens stage kt + 2 into that tile
-        if (W8) __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+        if (W8) __builtin_amdgcn_s_waitcnt(kWaitLds0);
         __builtin_amdgcn_s_barrier();
         const int nxt = kt + kStages - 1;
         issue(nxt < nk ? nxt : nk - 1);
@@ -544,12 +508,12 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     // operands): the compiler then knows that no load of its own is pending
     // in the loop, and inserts no wait there that would also wait for the
     // direct loads in flight.  The barrier publishes every wave's stage 0.
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    __builtin_amdgcn_s_waitcnt(wait_vm(0));
     __builtin_amdgcn_s_barrier();
     if (W8) { // the first two widened tiles
         widen_store(0, widen_load(0));
         widen_store(1, widen_load(1));
-        __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+        __builtin_amdgcn_s_waitcnt(kWaitLds0);
         __builtin_amdgcn_s_barrier();
     }
     read_frags(0, wa, xa);
@@ -560,7 +524,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     }
     if (kt < nk) stage(kt, wa, xa, wb, xb);
     // no direct load may still be writing this workgroup's LDS when it ends
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    __builtin_amdgcn_s_waitcnt(wait_vm(0));
 
     if (W8) {
 #pragma unroll

@@ -26,18 +26,13 @@
 // dx kernel) adds them in split order, and u A.  With 200 adapters over 1024
 // tokens the correction took 20 us as steps of the split GEMM (117 us, 96
 // without); the last launch, which sums the parts in any case, takes 22 us with it.
+#include "device.h"
 #include "internal.h"
 
 #include <algorithm>
 
 namespace lora {
 namespace {
-
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float floatx4 __attribute__((ext_vector_type(4)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kCols = 256;    // columns per workgroup
 constexpr int kBK = 32;       // summed axis per stage
@@ -46,8 +41,6 @@ constexpr int kStages = 4;
 constexpr int kWBytes = kBK * kCols * 2; // W0 part of a stage: 16 KB
 constexpr int kMaxSplits = 16;
 constexpr int kFill = 256; // workgroups that fill the chip
-
-__device__ const uint32_t g_zeros[4] = {0, 0, 0, 0};
 
 // WC column groups of waves (8 / WC row groups); a wave has TM row tiles and TN
 // column tiles of 16.
@@ -63,35 +56,11 @@ template <> struct Shape<64> {
 // vector load in flight.
 template <typename T> using cptr = const __attribute__((address_space(4))) T *;
 template <typename T> __device__ __forceinline__ cptr<T> as_const(const T *p) { return (cptr<T>)(p); }
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ int wave_sum(int v)
 {
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
     return uniform(v);
-}
-
-// s_waitcnt immediates: vmcnt in bits 3:0 and 15:14, expcnt 6:4, lgkmcnt 11:8; the
-// others at their largest (no wait).
-constexpr int kWaitLgkm0 = ~(15 << 8);
-constexpr int waitcnt_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
-
-// 16 bytes per lane to LDS at m0 + 16 lane (published by an explicit vmcnt wait
-// and a barrier; nothing else uses m0).
-__device__ __forceinline__ void dma16(const void *g, uint32_t lds_byte)
-{
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(lds_byte) : "memory");
-}
-__device__ __forceinline__ u32x2 read_tr(const char *lds)
-{
-    typedef __attribute__((address_space(3))) s16x4 lds4;
-    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(lds)));
-}
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
-{
-    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-    const bf16x2_t v = {static_cast<__bf16>(lo), static_cast<__bf16>(hi)};
-    return __builtin_bit_cast(uint32_t, v);
 }
 
 struct DgradArgs {
@@ -292,8 +261,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     // wave's.  Refills the slot.
     auto next_stage = [&](int i) {
         asm volatile("" ::: "memory");
-        if (xw) __builtin_amdgcn_s_waitcnt(waitcnt_vm((kWDma + kXDma) * (kStages - 2)) & kWaitLgkm0);
-        else __builtin_amdgcn_s_waitcnt(waitcnt_vm(kWDma * (kStages - 2)) & kWaitLgkm0);
+        if (xw) __builtin_amdgcn_s_waitcnt(wait_vm_lds0((kWDma + kXDma) * (kStages - 2)));
+        else __builtin_amdgcn_s_waitcnt(wait_vm_lds0(kWDma * (kStages - 2)));
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         issue(i + kStages);
@@ -321,8 +290,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     };
 #pragma unroll
     for (int i = 0; i < kStages; ++i) issue(i);
-    if (xw) __builtin_amdgcn_s_waitcnt(waitcnt_vm((kWDma + kXDma) * (kStages - 1)));
-    else __builtin_amdgcn_s_waitcnt(waitcnt_vm(kWDma * (kStages - 1)));
+    if (xw) __builtin_amdgcn_s_waitcnt(wait_vm((kWDma + kXDma) * (kStages - 1)));
+    else __builtin_amdgcn_s_waitcnt(wait_vm(kWDma * (kStages - 1)));
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     read_w(lds, wa);
@@ -364,7 +333,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
         next_stage(i);
     }
     // no direct load may still be writing this workgroup's LDS when it ends
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    __builtin_amdgcn_s_waitcnt(wait_vm(0));
 
     // lane: 16 columns (8 for TN = 2) of each of its rows, as 16-byte pieces
 #pragma unroll
@@ -420,8 +389,6 @@ int rows_of(int32_t T, int32_t d_in, int32_t d_out)
     const int64_t few = stages_of_cu((int64_t(T) + 63) / 64 * cols, d_out);
     return few <= 2 * stages_of_cu((int64_t(T) + 255) / 256 * cols, d_out) + 36 ? 64 : 256;
 }
-
-size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // dy's tail columns, and the splits' sums: splits x tiles <= kFill tiles of at most
 // 256 x 256, and at most kMaxSplits of T x d_in.
