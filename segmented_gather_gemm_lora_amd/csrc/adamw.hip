@@ -514,7 +514,8 @@ int lora_adamw(void *stream, const void *plan_host, const void *plan_dev, const 
     if (!plan_dev || !hyper_dev) return fail(LORA_ERR_ARG, "plan_dev or hyper_dev is NULL");
     if (!aligned16(plan_dev) || !aligned16(hyper_dev))
         return fail(LORA_ERR_ALIGN, "plan_dev or hyper_dev is not 16-byte aligned");
-    if (h->n_chunks > (int64_t(1) << 31) - 1) return fail(LORA_ERR_ARG, "too many chunks");
+    if (h->n_chunks > most_workgroups(kAdamThreads))
+        return fail(LORA_ERR_ARG, "%lld chunks of elements are more than one launch has", (long long)h->n_chunks);
     const auto *ch = reinterpret_cast<const AdamChunk *>(static_cast<const AdamHeader *>(plan_dev) + 1);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     const dim3 grid{unsigned(h->n_chunks)}, block(kAdamThreads);
@@ -537,7 +538,7 @@ int lora_adam_state_values(void *stream, int64_t n, const void *m, const void *m
     if ((m && (!aligned16(m) || !aligned16(m_out))) || (v && (!aligned16(v) || !aligned16(v_out))))
         return fail(LORA_ERR_ALIGN, "codes or outputs are not 16-byte aligned");
     const int64_t nwg = (n + 4095) / 4096;
-    if (nwg > (int64_t(1) << 31) - 1) return fail(LORA_ERR_ARG, "n %lld is too large", (long long)n);
+    if (nwg > most_workgroups(256)) return fail(LORA_ERR_ARG, "n %lld is too large", (long long)n);
     launch_kernel(adam_values_kernel, dim3(unsigned(nwg)), dim3(256), 0, static_cast<hipStream_t>(stream), n,
                   static_cast<const uint8_t *>(m), static_cast<const uint8_t *>(m_scale), static_cast<const uint8_t *>(v),
                   static_cast<const uint8_t *>(v_scale), static_cast<uint16_t *>(m_out), static_cast<uint16_t *>(v_out));

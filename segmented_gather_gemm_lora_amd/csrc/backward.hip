@@ -1345,7 +1345,9 @@ int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p
     // twice its registers (4096 rows of rank 16: 70 us, 29 by blocks).
     a.chunks = a.nt >= 3 && int64_t(a.nchunk) * a.tiles_x >= 512;
     const int64_t ndx = a.dx ? int64_t(a.chunks ? a.nchunk : a.nblk) * a.tiles_x : 0;
-    if (ngrad + ndx > (int64_t(1) << 31) - 1 || int64_t(a.nblk) * 2 * a.groups > (int64_t(1) << 30))
+    // launch 1: at most (blocks + 7 and 8 more) workgroups for a side and group of ranks
+    if (ngrad + ndx > most_workgroups(kGradWaves * 64) ||
+        (int64_t(a.nblk) + 15) * 2 * a.groups > most_workgroups(kShrinkWaves * 64))
         return fail(LORA_ERR_ARG, "backward: too many work items");
     a.ngrad = int(ngrad);
 
@@ -1379,7 +1381,7 @@ int launch_dx_join(hipStream_t s, const BackwardArgs &b, const PlanView &p, void
     a.joins = parts;
     a.splits = splits;
     const int64_t nwg = (int64_t(a.nblk) + (a.T - a.Tp + 15) / 16) * a.tiles_x;
-    if (nwg > (int64_t(1) << 31) - 1) return fail(LORA_ERR_ARG, "backward: too many dx tiles");
+    if (nwg > most_workgroups(kDxWaves * 64)) return fail(LORA_ERR_ARG, "backward: too many dx tiles");
     const dim3 grid{unsigned(nwg)}, block(kDxWaves * 64);
     if (b.vec_dx) launch_kernel(bwd_join_kernel<true>, grid, block, 0, s, a);
     else launch_kernel(bwd_join_kernel<false>, grid, block, 0, s, a);

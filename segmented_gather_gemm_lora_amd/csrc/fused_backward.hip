@@ -415,7 +415,7 @@ int launch_fused_backward(hipStream_t s, const BackwardArgs &b, const void *W0, 
     a.tiles_m = (T + rows - 1) / rows;
     a.tiles_n = (b.d_in + kCols - 1) / kCols;
     const int64_t tiles = int64_t(a.tiles_m) * a.tiles_n;
-    if (tiles > (int64_t(1) << 31) - 1) return fail(LORA_ERR_ARG, "fused backward: too many tiles");
+    if (tiles > most_workgroups(kThreads)) return fail(LORA_ERR_ARG, "fused backward: too many tiles");
     a.splits = splits_of(tiles, b.d_out);
     if (T > (1 << 27))
         return fail(LORA_ERR_ARG, "fused backward: too many rows");

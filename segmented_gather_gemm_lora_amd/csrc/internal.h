@@ -160,6 +160,9 @@ int launch_dx_join(hipStream_t s, const BackwardArgs &b, const PlanView &p, void
 size_t fused_backward_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out, int32_t max_rank);
 int launch_fused_backward(hipStream_t s, const BackwardArgs &b, const void *W0, const PlanView &p, void *ws);
 
+// Workgroups that one launch may have: the runtime counts threads in 32 bits.
+constexpr int64_t most_workgroups(int threads) { return 0xFFFFFFFFll / threads; }
+
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Per-thread request to time the next launches (lora_profile_launches).

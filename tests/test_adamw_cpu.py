@@ -226,3 +226,15 @@ def test_elements_of_a_chunk(n, state, gdt, chunk):
     e0, k = at[:, 56:60].copy().view("<u4")[:, 0], at[:, 60:64].copy().view("<i4")[:, 0]
     assert np.array_equal(e0, chunk * np.arange(rows)) and k.sum() == n and (k[:-1] == chunk).all()
     assert not raw[off + 32 + 80 * rows: off + need].any()
+
+
+def test_more_than_one_launch_has():
+    """The runtime counts a launch's threads in 32 bits: 2^24 workgroups of 256 are refused, not cut off."""
+    L = B.load()
+    st, raw, ptr, need = plan([], n_groups=0)
+    off = ptr - raw.ctypes.data
+    for chunks in (1 << 24, 1 << 31):
+        raw[off + 16: off + 24] = np.frombuffer(np.int64(chunks).tobytes(), dtype=np.uint8)
+        assert B.STATUS[L.lora_adamw(None, ptr, FX, FX, 1)] == "LORA_ERR_ARG"
+    n = 4096 * (1 << 24)
+    assert B.STATUS[L.lora_adam_state_values(None, n, FX, FX, None, None, FX, None)] == "LORA_ERR_ARG"

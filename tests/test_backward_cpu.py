@@ -361,3 +361,12 @@ def test_paged_adapters_are_refused(fused, no_device):
     plan.build(np.array([0, 2], dtype=np.int32), _pool())
     _call(fused, plan, None)
     assert len(no_device) == 1
+
+
+def test_more_workgroups_than_one_launch_has():
+    """The runtime counts a launch's threads in 32 bits (2^24 - 1 workgroups of 256): refused before anything runs."""
+    wide = dict(d_in=1 << 24, d_out=1 << 24, ldx=1 << 24, lddy=1 << 24, lddx=1 << 24, n=200)
+    plan = plan_of(range(200), 200, [1] * 200)
+    assert B.STATUS[run(plan, **wide)] == "LORA_ERR_ARG" and "work items" in B.last_error()
+    tall = plan_of([-1] * 70000, 1, [1])  # 64-row tiles of 256 columns: 1094 x 2^16
+    assert B.STATUS[run_fused(tall, **dict(wide, d_out=64, lddy=64))] == "LORA_ERR_ARG" and "tiles" in B.last_error()
