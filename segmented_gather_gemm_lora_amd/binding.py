@@ -1226,9 +1226,11 @@ class AdamW:
         if hyper.is_cuda and torch.cuda.is_current_stream_capturing():
             raise ValueError("AdamW is built outside of a captured region; its steps may be captured")
         eight, device = state == "8bit", params[0].device if params else hyper.device
-        made = lambda given, size, dt: given if given is not None else [  # noqa: E731
+        made = lambda given, size, dt: list(given) if given is not None else [  # noqa: E731
             torch.zeros(size(p.numel()), dtype=dt, device=p.device) for p in params]
         blocks = lambda n: (n + ADAM_BLOCK - 1) // ADAM_BLOCK  # noqa: E731
+        # lists of its own: the plan holds addresses, so every tensor lives as long as this
+        copies = None if copies is None else list(copies)
         self.params, self.grads, self.copies, self.hyper, self.state = list(params), list(grads), copies, hyper, state
         self.m = made(m, lambda n: n, torch.uint8 if eight else torch.float32)
         self.v = made(v, lambda n: n, torch.uint8 if eight else torch.float32)

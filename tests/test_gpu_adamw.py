@@ -422,3 +422,22 @@ def test_huge_gradients_by_the_formula():
     torch.cuda.synchronize()
     want, bound, *_ = R.step(np.ones(4), g, np.zeros(4), np.zeros(4), HYPER[0])
     assert (np.abs(p.double().cpu().numpy() - want) <= bound).all()
+
+
+def test_the_tensors_live_as_long_as_the_optimizer():
+    """The plan holds addresses: emptying the lists that were given frees nothing."""
+    import weakref
+
+    p = [torch.zeros(300, device="cuda")]
+    copies, m, v, ms, vs = ([torch.zeros(n, dtype=dt, device="cuda")] for n, dt in (
+        (300, torch.bfloat16), (300, torch.uint8), (300, torch.uint8), (2, torch.uint8), (2, torch.uint8)))
+    g = [torch.ones(300, device="cuda")]
+    lists = (p, g, copies, m, v, ms, vs)
+    refs = [weakref.ref(t[0]) for t in lists]
+    o = B.AdamW(p, g, [0], table_of(HYPER[:1]), state="8bit", copies=copies, m=m, v=v, m_scale=ms, v_scale=vs)
+    for t in lists:
+        t.clear()
+    assert all(r() is not None for r in refs)
+    o.step()
+    torch.cuda.synchronize()
+    assert torch.equal(o.copies[0], o.params[0].to(torch.bfloat16)) and (o.params[0] < 0).all()
