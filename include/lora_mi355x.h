@@ -73,6 +73,11 @@ typedef enum lora_dtype {
     LORA_BF16 = 1  /* x, A, B, W0, y in bf16 (stored as 16-bit patterns) */
 } lora_dtype;
 
+typedef enum lora_scale_type { /* scales of E4M3 blocks */
+    LORA_SCALE_F32 = 0, /* fp32 */
+    LORA_SCALE_E8M0 = 1 /* one byte e: the scale 2^(e - 127); 255: NaN */
+} lora_scale_type;
+
 #define LORA_MAX_RANK 256     /* largest adapter rank accepted */
 #define LORA_PLAN_ROW_BLOCK 16 /* rows per block in a plan's block list */
 
@@ -230,6 +235,38 @@ int lora_build_segments(int32_t T, const int32_t *ids, int32_t n_adapters,
  * Errors: LORA_ERR_ARG, LORA_ERR_PLAN, LORA_ERR_WORKSPACE (dev too small),
  * LORA_ERR_HIP. */
 int lora_segments_upload(const lora_segments *host, lora_segments *dev, void *stream);
+
+/* Build the segments of one batch on the device, in one launch on the stream,
+ * from arrays that only the device has to know: the plan holds what
+ * lora_build_segments makes of the same batch (same order, same records), at
+ * table offsets that depend on T and n_adapters alone.  Every call that takes
+ * uploaded segments takes these, except the gradient calls (LORA_ERR_PLAN).
+ * Captured into a graph, one recording serves every batch of up to T rows:
+ * lengths, adapters and the pool's tables are read at replay.
+ *   T            rows of the batch's x and y, at most dev->capacity and 65536
+ *   adapters_dev [n_requests] adapter of each request (-1: none)
+ *   lengths_dev  [n_requests] rows of each request, in order from row 0 (0 or less:
+ *                none; rows past T are cut off); NULL: one row each, n_requests <= T.
+ *                Rows that no request owns are padding: the calls neither use
+ *                nor write them (perm holds -1 behind the others)
+ *   n_adapters   entries of the pool's tables, at most LORA_DEVICE_PLAN_MAX_ADAPTERS
+ *   max_rank, rank_multiple   bounds that the host promises: the launches are chosen
+ *                by them.  A request whose adapter is outside [-1, n_adapters),
+ *                or has a rank outside [1, max_rank] or not a multiple of
+ *                rank_multiple, counts as one without an adapter
+ *   geometry     host, 8-byte aligned: the bounds of the counts, which the calls
+ *                read; it must stay unchanged while dev is used
+ * dev's counts are bounds too (num_tokens: T); the counts themselves are in the
+ * header at the start of dev's buffer.  Records past them: segments with adapter
+ * -1 and length 0, blocks and chunks with n = 0 and rows of -1.
+ * The tables' contents are a precondition: addresses of matrices, 16-byte aligned.
+ * Errors: LORA_ERR_ARG, LORA_ERR_RANK, LORA_ERR_ALIGN, LORA_ERR_WORKSPACE,
+ * LORA_ERR_HIP. */
+#define LORA_DEVICE_PLAN_MAX_ADAPTERS 7680
+int lora_build_segments_device(void *stream, int32_t T, int32_t n_requests, const int32_t *adapters_dev,
+                               const int32_t *lengths_dev, int32_t n_adapters, const uint64_t *pool_A_dev,
+                               const uint64_t *pool_B_dev, const int32_t *pool_rank_dev, const float *pool_alpha_dev,
+                               int32_t max_rank, int32_t rank_multiple, lora_plan_header *geometry, lora_segments *dev);
 
 /* ------------------------------------------------------------------ SGMV
  * Segmented shrink, the pages' "Shrink Stage" ("Multi-LoRA Serving in
@@ -651,6 +688,59 @@ int lora_fused_linear_e4m3(void *stream, const void *x, int64_t ldx, int32_t d_i
                            const lora_segments *seg, void *y, int64_t ldy,
                            void *ws, size_t ws_bytes);
 
+/* ------------------------------------------------------------ block-scaled FP8
+ * An FP8 base whose scales belong to blocks of 128 (the pages' FP8 base under
+ * BF16 adapters, "Multi-LoRA serving: the single translator with a thousand
+ * glossaries" (blog.lo0.es), section "Combined pattern with quantisation and
+ * disaggregated serving", with a finer scale than one for each matrix), multiplied
+ * in 8 bits: OCP E4M3 codes on both sides.
+ *
+ * A block is 128 adjacent elements of a row (activations, gradients: block_rows 1)
+ * or 128 x 128 elements (weights: block_rows 128), the last ones ragged.  With amax its
+ * largest magnitude, its scale is
+ *     LORA_SCALE_F32   max(fp32(amax / 448), 2^-126)
+ *     LORA_SCALE_E8M0  2^e, the least e in [-126, 127] with amax <= 448 2^e
+ * and a code is the E4M3 value nearest to x / scale, ties to even, rounded once from
+ * the exact quotient.  A block with an infinity or a NaN has a NaN scale and codes
+ * of 0, so that what it enters becomes NaN. */
+#define LORA_SCALE_BLOCK 128
+
+/* Codes and scales of a matrix x [rows, cols] (bf16 or fp32).
+ *   codes   [rows, ldq] bytes, any pitch and alignment
+ *   scales  block_rows 1: [groups, lds], groups = ceil(cols / 128), lds >= rows: a
+ *           row of `rows` scales for each group of columns (the product reads them
+ *           so); block_rows 128: [ceil(rows / 128), lds], lds >= groups
+ * cols <= 2^22.  One launch; x may not overlap codes or scales.
+ * Errors: LORA_ERR_ARG, LORA_ERR_DTYPE, LORA_ERR_ALIGN, LORA_ERR_HIP. */
+int lora_quantize_e4m3(void *stream, int dtype, const void *x, int64_t ldx, int32_t rows, int32_t cols,
+                       int32_t block_rows, int scale_type, void *codes, int64_t ldq, void *scales, int64_t lds);
+
+/* y[t, n] = sum_b x_scales[b, t] w_scales[n / 128, b] sum_{k in block b} x[t, k] W[n, k],
+ * overwriting y: the block's inner sums on 8-bit MFMA, everything in fp32, rounded once.
+ *   x         codes [T, ldx], 16-byte aligned rows; x_scales [groups, lds], lds >= T, 4-byte
+ *             aligned rows
+ *   W         codes [d_out, d_in], row pitch d_in, 16-byte aligned, d_in % 16 == 0;
+ *             w_scales [ceil(d_out / 128), groups], contiguous
+ *   y         [T, ldy] of out_dtype (bf16 or fp32), any alignment
+ * x (T rows) and W must each span less than 4 GiB.  Needs ws_bytes >=
+ * lora_workspace_bytes(LORA_OP_LINEAR_BLOCK, T, d_in, d_out, 1).
+ * Errors: LORA_ERR_ARG, LORA_ERR_DTYPE, LORA_ERR_ALIGN, LORA_ERR_WORKSPACE, LORA_ERR_HIP. */
+int lora_linear_e4m3_block(void *stream, int32_t T, const void *x, int64_t ldx, const void *x_scales, int64_t lds,
+                           int32_t d_in, const void *W, const void *w_scales, int scale_type, int32_t d_out,
+                           int out_dtype, void *y, int64_t ldy, void *ws, size_t ws_bytes);
+
+/* The fused layer over that base: y[t] = the product of x[t], quantized in groups of
+ * 128 columns with scales of the same type, with W0, + scale_s (x[t] A_s) B_s from x as
+ * given; overwriting y for every token of the plan.  x, y and the adapters are bf16;
+ * x and y rows are 16-byte aligned (ldx, ldy multiples of 8 elements); W0 and w_scales
+ * as W above.  Needs ws_bytes >= lora_workspace_bytes(LORA_OP_FUSED_BLOCK, T, d_in,
+ * d_out, max_rank).  Capturable; calls that share a workspace must be ordered on one
+ * stream.
+ * Errors: as lora_fused_linear_e4m3. */
+int lora_fused_linear_e4m3_block(void *stream, const void *x, int64_t ldx, int32_t d_in, const void *W0,
+                                 const void *w_scales, int scale_type, int32_t d_out, const lora_segments *seg, void *y,
+                                 int64_t ldy, void *ws, size_t ws_bytes);
+
 /* ------------------------------------------------------------------ gradients
  * Training the adapters of many requests at once: the gradients of lora_sgmv's
  * correction y[t] += s_i (x[t] A_i^T) B_i^T (s_i = alpha_i / r_i, i = a(t), A_i
@@ -809,7 +899,10 @@ enum {
     LORA_OP_SGMV = 5,
     LORA_OP_BGMV = 6,
     LORA_OP_SGMV_BACKWARD = 7,
-    LORA_OP_FUSED_BACKWARD = 8
+    LORA_OP_FUSED_BACKWARD = 8,
+    LORA_OP_LINEAR_BLOCK = 9,
+    LORA_OP_FUSED_BLOCK = 10,
+    LORA_OP_FUSED_BLOCK_BACKWARD = 11
 };
 
 /* Workspace bytes an op needs (0 = none; ws may then be NULL); -1 cast to

@@ -11,6 +11,7 @@ from .binding import (  # noqa: F401
     LORA_BF16,
     LORA_F32,
     AdamW,
+    DevicePlan,
     DevicePool,
     GradPool,
     LoraError,
@@ -22,8 +23,11 @@ from .binding import (  # noqa: F401
     bgmv_shrink,
     fused_linear,
     fused_linear_backward,
+    fused_linear_e4m3_block,
     lib_path,
+    linear_e4m3_block,
     load,
+    quantize_e4m3,
     sgmv,
     sgmv_backward,
     sgmv_expand,

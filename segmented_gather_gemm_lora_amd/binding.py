@@ -32,6 +32,14 @@ LORA_OP_SGMV = 5
 LORA_OP_BGMV = 6
 LORA_OP_SGMV_BACKWARD = 7
 LORA_OP_FUSED_BACKWARD = 8
+LORA_OP_LINEAR_BLOCK = 9
+LORA_OP_FUSED_BLOCK = 10
+LORA_OP_FUSED_BLOCK_BACKWARD = 11
+
+LORA_SCALE_F32 = 0
+LORA_SCALE_E8M0 = 1
+SCALE_BLOCK = 128
+DEVICE_PLAN_MAX_ADAPTERS = 7680
 
 LORA_GRAD_ACCUMULATE = 1
 LORA_ADAM_F32 = 0
@@ -57,7 +65,8 @@ EXPORTS = [
     "lora_sgmv_grouped", "lora_sgmv_grouped_workspace_bytes", "lora_probe_empty", "lora_probe_stream",
     "lora_probe_chase", "lora_workspace_clear", "lora_debug_wait_limit", "lora_bgmv_noalloc",
     "lora_sgmv_backward", "lora_fused_linear_backward", "lora_adamw_plan_bytes", "lora_adamw_plan", "lora_adamw_upload", "lora_adamw",
-    "lora_adam_state_values",
+    "lora_adam_state_values", "lora_build_segments_device", "lora_quantize_e4m3", "lora_linear_e4m3_block",
+    "lora_fused_linear_e4m3_block",
 ]
 LORA_CACHE_DRY = 1
 MAX_PROJ = 8
@@ -130,6 +139,14 @@ _SIGS = {
     "lora_adamw_upload": (ctypes.c_int, [_vp, _vp, _sz, _vp]),
     "lora_adamw": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32]),
     "lora_adam_state_values": (ctypes.c_int, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "lora_build_segments_device": (ctypes.c_int, [_vp, _i32, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _vp,
+                                                  _vp]),
+    "lora_quantize_e4m3": (ctypes.c_int, [_vp, ctypes.c_int, _vp, _i64, _i32, _i32, _i32, ctypes.c_int, _vp, _i64, _vp,
+                                          _i64]),
+    "lora_linear_e4m3_block": (ctypes.c_int, [_vp, _i32, _vp, _i64, _vp, _i64, _i32, _vp, _vp, ctypes.c_int, _i32,
+                                              ctypes.c_int, _vp, _i64, _vp, _sz]),
+    "lora_fused_linear_e4m3_block": (ctypes.c_int, [_vp, _vp, _i64, _i32, _vp, _vp, ctypes.c_int, _i32, _vp, _vp, _i64,
+                                                    _vp, _sz]),
     "lora_probe_stream": (ctypes.c_int, [_vp, _vp, _i64, _vp, _i64, _vp, _i32]),
     "lora_probe_chase": (ctypes.c_int, [_vp, _vp, _i32, _vp]),
     "lora_page_alloc_create": (ctypes.c_int, [_i32, _vp]),
@@ -853,6 +870,87 @@ class Plan:
         return segment_table(self.h)
 
 
+class DevicePlan:
+    """A batch's segments built on the device (lora_build_segments_device): build()
+    enqueues one launch that reads the adapters and lengths of the requests, and the
+    pool's tables, from device memory, so it and the calls that take the plan can be
+    captured together and replayed for other batches of up to `rows` rows.  The
+    gradient calls take a Plan.  max_rank and rank_multiple (the pool's, where not given)
+    bound what the tables may hold at any build; requests of adapters outside them count
+    as having none."""
+
+    def __init__(self, rows: int, pool, max_rank: Optional[int] = None, rank_multiple: Optional[int] = None):
+        torch = _torch()
+        self.rows, self.pool = int(rows), pool
+        ranks = np.asarray(pool.rank, dtype=np.int64)
+        self.max_rank = int(max_rank or max(pool.max_rank, 1))
+        step = int(np.gcd.reduce(ranks)) if ranks.size else 1
+        self.rank_multiple = int(rank_multiple or max(min(step & -step, 16), 1))
+        for t, dt in ((pool.addr_A_dev, torch.int64), (pool.addr_B_dev, torch.int64), (pool.rank_dev, torch.int32),
+                      (pool.alpha_dev, torch.float32)):
+            if not isinstance(t, _Raw) and (t is None or t.dtype != dt or not t.is_cuda or not t.is_contiguous()
+                                            or t.numel() < pool.n_adapters):
+                raise ValueError("the pool has no device tables of its adapters")
+        device = pool.rank_dev.device if hasattr(pool.rank_dev, "device") else "cuda"
+        self.dev = torch.empty(lora_segments_bytes(self.rows), dtype=torch.uint8, device=device)
+        self.geometry = (ctypes.c_uint64 * (PLAN_HEADER_BYTES // 8))()
+        self.h = LoraSegments()  # no segment on the host
+        self.h.batch_tokens = self.rows
+        self.d = LoraSegments()
+        self.made_for, self.paged, self.grads_fit = (pool.d_in, pool.d_out, pool.dtype), isinstance(pool, PagedPool), None
+        _check(lora_segments_bind(self.dev.data_ptr(), self.rows, ctypes.addressof(self.d)), "lora_segments_bind")
+
+    @property
+    def seg(self) -> int:
+        return ctypes.addressof(self.d)
+
+    def build(self, adapters, lengths=None, stream=None):
+        """adapters: int32 device tensor, the adapter of each request (-1: none); lengths:
+        int32 device tensor of the requests' rows, or None: one row each."""
+        torch = _torch()
+        device = torch.cuda.current_device()
+        if self.dev.get_device() != device:
+            raise ValueError("the plan is not on the current device")
+        for t in (adapters,) if lengths is None else (adapters, lengths):
+            if t.dtype is not torch.int32 or t.dim() != 1 or t.get_device() != device or t.shape != adapters.shape or (
+                    t.numel() > 1 and t.stride(0) != 1):
+                raise ValueError("adapters and lengths are adjacent int32 elements on the current device, one a request")
+        p = self.pool
+        _check(load().lora_build_segments_device(
+            _stream_handle(stream, device), self.rows, adapters.shape[0], adapters.data_ptr(), _ptr(lengths), p.n_adapters,
+            _ptr(p.addr_A_dev), _ptr(p.addr_B_dev), _ptr(p.rank_dev), _ptr(p.alpha_dev), self.max_rank,
+            self.rank_multiple, self.geometry, ctypes.addressof(self.d)), "lora_build_segments_device")
+        return self
+
+    def bounds(self) -> dict:
+        """The geometry: bounds of the counts, and the tables' offsets."""
+        return plan_header(np.frombuffer(self.geometry, dtype=np.uint8))
+
+    def tables(self) -> dict:
+        """Views of the last build's tables in the device buffer (int32): counts (rows, adapted
+        rows, segments, blocks, largest rank, longest segment, chunks), segments [S, 10], blocks
+        [n, 32], chunks [n, 80] (the records' words), perm and segidx."""
+        h, w = self.bounds(), self.dev[: self.dev.numel() // 4 * 4].view(_torch().int32)
+
+        def at(key, n, width):
+            o = h[key] // 4
+            return w[o: o + n * width].view(n, width)
+
+        T = h["num_tokens"]
+        return {"counts": w[1:8], "segments": at("seg_offset", h["num_segments"], SEG_DESC.itemsize // 4),
+                "blocks": at("blk_offset", h["num_blocks"], BLK_DESC.itemsize // 4),
+                "chunks": at("chunk_offset", h["num_chunks"], CHUNK_DESC.itemsize // 4),
+                "perm": w[h["perm_offset"] // 4:][:T], "segidx": w[h["segidx_offset"] // 4:][: h["num_sorted"]]}
+
+    def header(self) -> dict:
+        """The last build's header, from the device (synchronises)."""
+        return plan_header(self.dev[:PLAN_HEADER_BYTES].cpu().numpy())
+
+    def arrays(self) -> dict:
+        """Host copies of the last build's arrays, cut to its counts (synchronises; for tests)."""
+        return plan_arrays(self.dev.cpu().numpy(), self.header())
+
+
 _NP_OF = {ctypes.c_int32: np.int32, ctypes.c_uint64: np.uint64, ctypes.c_float: np.float32}
 
 
@@ -1094,6 +1192,104 @@ def fused_linear_e4m3(x, W0, w0_scale: float, plan: Plan, y, ws, stream=None):
                                   float(w0_scale), W0.shape[0], plan.seg, _ptr(y), y.stride(0),
                                   _ptr(ws), ws.numel() * ws.element_size()),
            "lora_fused_linear_e4m3")
+
+
+def _scale_type(*scales) -> int:
+    torch = _torch()
+    dt = scales[0].dtype
+    if dt not in (torch.float32, torch.uint8) or any(s.dtype is not dt for s in scales):
+        raise ValueError("scales are float32, or uint8 (E8M0), and the same on both sides")
+    return LORA_SCALE_F32 if dt is torch.float32 else LORA_SCALE_E8M0
+
+
+def _on_device(*tensors) -> int:
+    """The current device, where all of them are."""
+    device = _torch().cuda.current_device()
+    if any(t.get_device() != device for t in tensors):
+        raise ValueError("a tensor is not on the current device")
+    return device
+
+
+def _matrix(t, dtypes, rows=None, cols=None, whole=False):
+    """Refuses what the C call cannot see: another type or shape, columns that are not
+    adjacent (whole: rows neither)."""
+    if t.dim() != 2 or t.dtype not in dtypes or (rows is not None and t.shape[0] < rows) or (
+            cols is not None and t.shape[1] != cols) or (t.stride(1) != 1 and t.shape[1] > 1) or (
+            whole and not t.is_contiguous()):
+        raise ValueError(f"a matrix of {rows} x {cols} adjacent elements of {dtypes[0]} is wanted, not {tuple(t.shape)} "
+                         f"of {t.dtype} at {t.stride()}")
+    return t
+
+
+def _pitch(t) -> int:
+    """Row pitch; of a single row any, so the row's length or more."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def quantize_e4m3(x, codes, scales, block_rows: int = 1, stream=None):
+    """E4M3 codes (uint8, x's shape) of a bf16 or fp32 matrix with a scale for each block of
+    1 x 128 (block_rows 1; scales [groups, rows]) or 128 x 128 elements (block_rows 128;
+    scales [row blocks, groups]).  The scales' type says which: float32, or uint8 for
+    powers of two (E8M0)."""
+    torch = _torch()
+    rows, cols = x.shape
+    _matrix(x, (torch.bfloat16, torch.float32))
+    _matrix(codes, (torch.uint8,), rows, cols)
+    groups = (cols + SCALE_BLOCK - 1) // SCALE_BLOCK
+    want = (groups, rows) if block_rows == 1 else ((rows + SCALE_BLOCK - 1) // SCALE_BLOCK, groups)
+    _matrix(scales, (torch.float32, torch.uint8), *want)
+    device = _on_device(x, codes, scales)
+    _check(load().lora_quantize_e4m3(_stream_handle(stream, device), LORA_BF16 if x.dtype is torch.bfloat16 else LORA_F32,
+                                     x.data_ptr(), _pitch(x), rows, cols, block_rows, _scale_type(scales),
+                                     codes.data_ptr(), _pitch(codes), scales.data_ptr(), _pitch(scales)),
+           "lora_quantize_e4m3")
+
+
+def _block_base(W, w_scales):
+    torch = _torch()
+    d_out, d_in = W.shape
+    _matrix(W, (torch.uint8,), whole=True)
+    _matrix(w_scales, (torch.float32, torch.uint8), (d_out + SCALE_BLOCK - 1) // SCALE_BLOCK,
+            (d_in + SCALE_BLOCK - 1) // SCALE_BLOCK, whole=True)
+    return d_out, d_in
+
+
+def linear_e4m3_block(x, x_scales, W, w_scales, y, ws, stream=None):
+    """y = (x_scales x) (w_scales W)^T for E4M3 codes x [T, d_in] (scales [groups, T]) and W
+    [d_out, d_in] (scales for each 128 x 128 block); y bf16 or fp32, overwritten.  ws: a
+    workspace of LORA_OP_LINEAR_BLOCK."""
+    torch = _torch()
+    d_out, d_in = _block_base(W, w_scales)
+    T = x.shape[0]
+    _matrix(x, (torch.uint8,), None, d_in)
+    _matrix(x_scales, (torch.float32, torch.uint8), w_scales.shape[1], T)
+    _matrix(y, (torch.bfloat16, torch.float32), T, d_out)
+    device = _on_device(x, x_scales, W, w_scales, y, ws)
+    _check(load().lora_linear_e4m3_block(
+        _stream_handle(stream, device), T, x.data_ptr(), _pitch(x), x_scales.data_ptr(), _pitch(x_scales), d_in,
+        W.data_ptr(), w_scales.data_ptr(), _scale_type(x_scales, w_scales), d_out,
+        LORA_BF16 if y.dtype is torch.bfloat16 else LORA_F32, y.data_ptr(), _pitch(y), ws.data_ptr(),
+        ws.numel() * ws.element_size()), "lora_linear_e4m3_block")
+
+
+def fused_linear_e4m3_block(x, W0, w_scales, plan, y, ws, stream=None):
+    """The fused layer over an E4M3 base with a scale for each 128 x 128 block: x (bf16) is
+    quantized by the call, in groups of 128 columns with scales of the same type; the
+    correction is x's own.  plan: a Plan or a DevicePlan; ws: of LORA_OP_FUSED_BLOCK."""
+    torch = _torch()
+    d_out, d_in = _block_base(W0, w_scales)
+    T = plan.h.batch_tokens
+    _matrix(x, (torch.bfloat16,), T, d_in)
+    _matrix(y, (torch.bfloat16,), T, d_out)
+    if plan.paged:
+        raise ValueError("the plan's adapters are paged; this call takes whole matrices")
+    if plan.made_for is not None and plan.made_for != (d_in, d_out, "bf16"):
+        raise ValueError(f"a call of ({d_in}, {d_out}, bf16) on a plan of adapters of {plan.made_for}")
+    device = _on_device(x, W0, w_scales, y, ws, plan.dev)
+    _check(load().lora_fused_linear_e4m3_block(
+        _stream_handle(stream, device), x.data_ptr(), _pitch(x), d_in, W0.data_ptr(), w_scales.data_ptr(),
+        _scale_type(w_scales), d_out, plan.seg, y.data_ptr(), _pitch(y), ws.data_ptr(), ws.numel() * ws.element_size()),
+        "lora_fused_linear_e4m3_block")
 
 
 def _gradient_rows(dtype: str, tokens: int, others, rows):

@@ -23,7 +23,7 @@ LIB_DIR = os.path.join(PKG, "_lib")
 LIB_NAME = "liblora_mi355x.so"
 
 SOURCES = ["sgmv_bgmv.hip", "fused.hip", "abi.cpp", "residency.cpp", "pages.hip", "probes.hip", "noalloc.hip",
-           "backward.hip", "fused_backward.hip", "adamw.hip"]
+           "backward.hip", "fused_backward.hip", "adamw.hip", "plan_device.hip", "e4m3.hip", "block_gemm.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

@@ -237,6 +237,9 @@ size_t lora_workspace_bytes(int op, int32_t T, int32_t d_in, int32_t d_out, int3
     case LORA_OP_BGMV_SHRINK:
     case LORA_OP_BGMV_EXPAND: return 0;
     case LORA_OP_FUSED: return fused_workspace_bytes(T < 0 ? 0 : T, d_in < 1 ? 1 : d_in, max_rank < 1 ? 1 : max_rank);
+    case LORA_OP_LINEAR_BLOCK: return 0;
+    case LORA_OP_FUSED_BLOCK:
+        return fused_block_workspace_bytes(T < 0 ? 0 : T, d_in < 1 ? 1 : d_in, max_rank < 1 ? 1 : max_rank);
     case LORA_OP_SGMV: // control words, fp32 partials (two kernels), tagged partials (one launch)
         return sgmv_ctl_bytes(T < 0 ? 0 : T) +
                3 * combined_workspace_bytes(T < 0 ? 0 : T, d_in < 1 ? 1 : d_in, max_rank < 1 ? 1 : max_rank);
@@ -250,6 +253,24 @@ size_t lora_workspace_bytes(int op, int32_t T, int32_t d_in, int32_t d_out, int3
                                               max_rank < 1 ? 1 : max_rank);
     default: return size_t(-1);
     }
+}
+
+// Counts and table offsets of a plan; everything else of the header is zero.
+static void lay_out_plan(lora_plan_header *h, int32_t T, int32_t sorted, int32_t S, int32_t nblk, int32_t nchunk)
+{
+    std::memset(h, 0, sizeof *h);
+    h->num_tokens = T;
+    h->num_sorted = sorted;
+    h->num_segments = S;
+    h->num_blocks = nblk;
+    h->num_chunks = nchunk;
+    h->seg_offset = sizeof(lora_plan_header);
+    h->blk_offset = (h->seg_offset + sizeof(lora_seg_desc) * size_t(S) + 127) & ~size_t(127);
+    h->perm_offset = align16(h->blk_offset + sizeof(lora_blk_desc) * size_t(nblk));
+    h->chunk_offset = (h->perm_offset + 4 * size_t(T) + 63) & ~size_t(63);
+    h->segidx_offset = align16(h->chunk_offset + sizeof(lora_chunk_desc) * size_t(nchunk));
+    h->soa_offset = align16(h->segidx_offset + 4 * size_t(sorted));
+    h->bytes_used = h->soa_offset + soa_bytes(S);
 }
 
 // The plan of one batch in `plan` (plan_bytes >= segments_bytes(T)): see the
@@ -302,21 +323,9 @@ static int build_plan(int32_t T, const int32_t *ids, int32_t n_adapters, const u
 
     char *base = static_cast<char *>(plan);
     auto *h = reinterpret_cast<lora_plan_header *>(base);
-    std::memset(h, 0, sizeof *h);
-    h->num_tokens = T;
-    h->num_sorted = sorted;
-    h->num_segments = S;
-    h->num_blocks = nblk;
+    lay_out_plan(h, T, sorted, S, nblk, nchunk);
     h->max_rank = max_rank;
     h->max_len = max_len;
-    h->num_chunks = nchunk;
-    h->seg_offset = sizeof(lora_plan_header);
-    h->blk_offset = (h->seg_offset + sizeof(lora_seg_desc) * size_t(S) + 127) & ~size_t(127);
-    h->perm_offset = align16(h->blk_offset + sizeof(lora_blk_desc) * size_t(nblk));
-    h->chunk_offset = (h->perm_offset + 4 * size_t(T) + 63) & ~size_t(63);
-    h->segidx_offset = align16(h->chunk_offset + sizeof(lora_chunk_desc) * size_t(nchunk));
-    h->soa_offset = align16(h->segidx_offset + 4 * size_t(sorted));
-    h->bytes_used = h->soa_offset + soa_bytes(S);
 
     auto *seg = reinterpret_cast<lora_seg_desc *>(base + h->seg_offset);
     auto *blk = reinterpret_cast<lora_blk_desc *>(base + h->blk_offset);
@@ -461,6 +470,7 @@ int lora_segments_upload(const lora_segments *host, lora_segments *dev, void *st
     const lora_plan_header *h = nullptr;
     int st = check_plan(host->buf, &h);
     if (st) return st;
+    if (plan_on_device(h)) return fail(LORA_ERR_PLAN, "host's buffer is the geometry of a plan built on the device");
     if (!dev->buf) return fail(LORA_ERR_ARG, "dev is not bound to a buffer");
     if (dev->buf == host->buf) return fail(LORA_ERR_ARG, "dev and host are bound to the same buffer");
     if (lora_segments_bytes(dev->capacity) < h->bytes_used)
@@ -471,6 +481,43 @@ int lora_segments_upload(const lora_segments *host, lora_segments *dev, void *st
     fill_segments(dev, static_cast<char *>(dev->buf), h);
     dev->host = host->buf;
     return LORA_OK;
+}
+
+int lora_build_segments_device(void *stream, int32_t T, int32_t n_requests, const int32_t *adapters_dev,
+                               const int32_t *lengths_dev, int32_t n_adapters, const uint64_t *pool_A_dev,
+                               const uint64_t *pool_B_dev, const int32_t *pool_rank_dev, const float *pool_alpha_dev,
+                               int32_t max_rank, int32_t rank_multiple, lora_plan_header *geometry, lora_segments *dev)
+{
+    clear_error();
+    if (!geometry || !dev || !dev->buf) return fail(LORA_ERR_ARG, "geometry is NULL or dev is not bound to a buffer");
+    if (reinterpret_cast<uintptr_t>(geometry) & 7u) return fail(LORA_ERR_ALIGN, "geometry is not 8-byte aligned");
+    if (T < 0 || T > 65536) return fail(LORA_ERR_ARG, "T %d outside [0, 65536]", T);
+    if (T > dev->capacity) return fail(LORA_ERR_WORKSPACE, "batch of %d rows > capacity %d", T, dev->capacity);
+    if (n_requests < 0 || (!lengths_dev && n_requests > T))
+        return fail(LORA_ERR_ARG, "%d requests for %d rows", n_requests, T);
+    if (n_adapters < 0 || n_adapters > LORA_DEVICE_PLAN_MAX_ADAPTERS)
+        return fail(LORA_ERR_ARG, "n_adapters %d outside [0, %d]", n_adapters, LORA_DEVICE_PLAN_MAX_ADAPTERS);
+    if (n_requests > 0 && !adapters_dev) return fail(LORA_ERR_ARG, "adapters is NULL");
+    if (n_adapters > 0 && (!pool_A_dev || !pool_B_dev || !pool_rank_dev || !pool_alpha_dev))
+        return fail(LORA_ERR_ARG, "pool tables are NULL");
+    if (max_rank < 1 || max_rank > LORA_MAX_RANK) return fail(LORA_ERR_RANK, "max_rank %d outside [1, 256]", max_rank);
+    if (rank_multiple < 1 || rank_multiple > max_rank)
+        return fail(LORA_ERR_RANK, "rank_multiple %d outside [1, max_rank]", rank_multiple);
+    const int32_t S = std::min(T, n_adapters);
+    lay_out_plan(geometry, T, S ? T : 0, S, S ? std::min(T, T / LORA_PLAN_ROW_BLOCK + S) : 0,
+                 S ? std::min(T, T / LORA_PLAN_CHUNK_ROWS + S) : 0);
+    geometry->max_rank = S ? max_rank : 0;
+    geometry->max_len = T;
+    geometry->magic = LORA_PLAN_MAGIC;
+    geometry->reserved = 1u | uint64_t(std::min(rank_multiple, 255)) << 8;
+    if (lora_segments_bytes(dev->capacity) < geometry->bytes_used)
+        return fail(LORA_ERR_WORKSPACE, "dev holds %d rows; the batch has %d", dev->capacity, T);
+    fill_segments(dev, static_cast<char *>(dev->buf), geometry);
+    dev->host = geometry;
+    if (T == 0) return LORA_OK;
+    const DevicePlanCall c{adapters_dev, lengths_dev, n_requests, n_adapters, max_rank, rank_multiple,
+                           pool_A_dev, pool_B_dev, pool_rank_dev, pool_alpha_dev};
+    return launch_plan_device(static_cast<hipStream_t>(stream), c, *geometry, dev->buf);
 }
 
 int lora_sgmv_shrink(void *stream, int dtype, const void *x, int64_t ldx, int32_t d_in, const lora_segments *seg,
@@ -828,6 +875,7 @@ static int make_backward_args(int dtype, const void *x, int64_t ldx, int32_t d_i
                               BackwardArgs *b)
 {
     const int es = esize_of(dtype);
+    if (plan_on_device(h)) return fail(LORA_ERR_PLAN, "the gradient calls take plans that the host has built");
     if (flags & ~LORA_GRAD_ACCUMULATE) return fail(LORA_ERR_ARG, "unknown flags %#x", flags);
     // 16 rows of A or B stay below 2^32 bytes, columns of the last tile below 2^31
     if (d_in < 1 || d_out < 1 || d_in > (1 << 24) || d_out > (1 << 24))
@@ -929,6 +977,124 @@ int lora_fused_linear_backward(void *stream, int dtype, const void *x, int64_t l
     if (!ws || ws_bytes < need) return fail(LORA_ERR_WORKSPACE, "workspace %zu B < %zu B needed", ws_bytes, need);
     if (!aligned16(ws)) return fail(LORA_ERR_ALIGN, "workspace is not 16-byte aligned");
     return launch_fused_backward(static_cast<hipStream_t>(stream), b, W0, PlanView{h, plan_dev}, ws);
+}
+
+static int check_scale_type(int scale_type)
+{
+    if (scale_type != LORA_SCALE_F32 && scale_type != LORA_SCALE_E8M0)
+        return fail(LORA_ERR_DTYPE, "unknown scale type %d", scale_type);
+    return LORA_OK;
+}
+static bool scale_aligned(const void *p, int scale_type)
+{
+    return elem_aligned(p, scale_type == LORA_SCALE_F32 ? 4 : 1);
+}
+
+int lora_quantize_e4m3(void *stream, int dtype, const void *x, int64_t ldx, int32_t rows, int32_t cols,
+                       int32_t block_rows, int scale_type, void *codes, int64_t ldq, void *scales, int64_t lds)
+{
+    clear_error();
+    int st = check_dtype(dtype);
+    if (st) return st;
+    if ((st = check_scale_type(scale_type))) return st;
+    if (block_rows != 1 && block_rows != LORA_SCALE_BLOCK)
+        return fail(LORA_ERR_ARG, "block_rows %d is not 1 or %d", block_rows, LORA_SCALE_BLOCK);
+    if (rows < 0 || cols < 1 || cols > (1 << 22)) return fail(LORA_ERR_ARG, "rows %d < 0 or cols %d outside [1, 2^22]", rows, cols);
+    if (rows == 0) return LORA_OK;
+    if (!x || !codes || !scales) return fail(LORA_ERR_ARG, "x, codes or scales is NULL");
+    const int32_t groups = (cols + LORA_SCALE_BLOCK - 1) / LORA_SCALE_BLOCK;
+    if (ldx < cols || ldq < cols) return fail(LORA_ERR_ARG, "row pitch smaller than the row");
+    if (lds < (block_rows == 1 ? rows : groups)) return fail(LORA_ERR_ARG, "lds %lld < a row of scales", (long long)lds);
+    if (!elem_aligned(x, esize_of(dtype)) || !scale_aligned(scales, scale_type))
+        return fail(LORA_ERR_ALIGN, "x or scales is not aligned to its element size");
+    QuantCall q{};
+    q.dtype = dtype;
+    q.x = x;
+    q.ldx = ldx;
+    q.rows = rows;
+    q.cols = cols;
+    q.codes = codes;
+    q.ldq = ldq;
+    q.block_rows = block_rows;
+    q.scale_type = scale_type;
+    q.scales = scales;
+    q.lds = lds;
+    return launch_quantize(static_cast<hipStream_t>(stream), q);
+}
+
+// Checks that the products with a block-scaled base share.
+static int check_block_base(int64_t rows, int64_t ldx, int32_t d_in, const void *W, const void *w_scales, int scale_type,
+                            int32_t d_out)
+{
+    if (!W || !w_scales) return fail(LORA_ERR_ARG, "W or its scales are NULL");
+    if (d_in < 1 || d_out < 1) return fail(LORA_ERR_ARG, "d_in %d or d_out %d < 1", d_in, d_out);
+    if (d_in % 16) return fail(LORA_ERR_ALIGN, "an E4M3 base needs d_in %% 16 == 0 (16-byte rows), got %d", d_in);
+    if (!aligned16(W)) return fail(LORA_ERR_ALIGN, "W is not 16-byte aligned");
+    if (!scale_aligned(w_scales, scale_type)) return fail(LORA_ERR_ALIGN, "W's scales are not aligned to their size");
+    // rows are addressed with 32-bit byte offsets
+    if ((rows + 1) * ldx >= int64_t(1) << 32 || (int64_t(d_out) + 1) * d_in >= int64_t(1) << 32)
+        return fail(LORA_ERR_ARG, "the codes of x or W span 4 GiB or more");
+    return LORA_OK;
+}
+
+int lora_linear_e4m3_block(void *stream, int32_t T, const void *x, int64_t ldx, const void *x_scales, int64_t lds,
+                           int32_t d_in, const void *W, const void *w_scales, int scale_type, int32_t d_out,
+                           int out_dtype, void *y, int64_t ldy, void *ws, size_t ws_bytes)
+{
+    (void)ws;
+    (void)ws_bytes;
+    clear_error();
+    int st = check_dtype(out_dtype);
+    if (st) return st;
+    if ((st = check_scale_type(scale_type))) return st;
+    if (T < 0) return fail(LORA_ERR_ARG, "T %d < 0", T);
+    if (T == 0) return LORA_OK;
+    if (!x || !x_scales || !y) return fail(LORA_ERR_ARG, "x, its scales or y is NULL");
+    if (ldx < d_in || ldy < d_out || lds < T) return fail(LORA_ERR_ARG, "row pitch smaller than the row");
+    if ((st = check_block_base(T, ldx, d_in, W, w_scales, scale_type, d_out))) return st;
+    if (!aligned16(x) || ldx % 16) return fail(LORA_ERR_ALIGN, "x needs 16-byte aligned rows");
+    if (reinterpret_cast<uintptr_t>(x_scales) & 3u || (scale_type == LORA_SCALE_E8M0 && lds % 4))
+        return fail(LORA_ERR_ALIGN, "x's scales need 4-byte aligned rows");
+    if (!elem_aligned(y, esize_of(out_dtype))) return fail(LORA_ERR_ALIGN, "y is not aligned to its element size");
+    const LinearBlockCall c{T, x, ldx, x_scales, lds, d_in, W, w_scales, scale_type, d_out, out_dtype, y, ldy};
+    return launch_linear_block(static_cast<hipStream_t>(stream), c);
+}
+
+int lora_fused_linear_e4m3_block(void *stream, const void *x, int64_t ldx, int32_t d_in, const void *W0,
+                                 const void *w_scales, int scale_type, int32_t d_out, const lora_segments *seg, void *y,
+                                 int64_t ldy, void *ws, size_t ws_bytes)
+{
+    clear_error();
+    const lora_plan_header *h = nullptr;
+    const char *plan_dev = nullptr;
+    int st = check_segments(seg, &h, &plan_dev);
+    if (st) return st;
+    if ((st = check_scale_type(scale_type))) return st;
+    const int32_t T = h->num_tokens;
+    if (T == 0) return LORA_OK;
+    if (!x || !y) return fail(LORA_ERR_ARG, "x or y is NULL");
+    if (ldx < d_in || ldy < d_out) return fail(LORA_ERR_ARG, "row pitch smaller than the row");
+    // x's codes are held in rows of whole blocks
+    if ((st = check_block_base(T, int64_t(d_in) + LORA_SCALE_BLOCK, d_in, W0, w_scales, scale_type, d_out))) return st;
+    if (!aligned16(x) || !aligned16(y) || ldx % 8 || ldy % 8)
+        return fail(LORA_ERR_ALIGN, "fused entry needs 16-byte aligned x and y rows");
+    if (!plan_dev) return fail(LORA_ERR_ARG, "the segments' device buffer is NULL");
+    const size_t need = fused_block_workspace_bytes(T, d_in, h->max_rank < 1 ? 1 : h->max_rank);
+    if (!ws || ws_bytes < need) return fail(LORA_ERR_WORKSPACE, "workspace %zu B < %zu B needed", ws_bytes, need);
+    if (!aligned16(ws)) return fail(LORA_ERR_ALIGN, "workspace is not 16-byte aligned");
+    ShrinkArgs sa{};
+    sa.dtype = LORA_BF16;
+    sa.x = x;
+    sa.ldx = ldx;
+    sa.d_in = d_in;
+    sa.vec = true;
+    ExpandArgs ea{};
+    ea.dtype = LORA_BF16;
+    ea.y = y;
+    ea.ldy = ldy;
+    ea.d_out = d_out;
+    return launch_fused_linear_block(static_cast<hipStream_t>(stream), sa, W0, w_scales, scale_type, ea,
+                                     PlanView{h, plan_dev}, ws);
 }
 
 // Checks and launch shared by the bf16 and E4M3 forms of the fused entry.

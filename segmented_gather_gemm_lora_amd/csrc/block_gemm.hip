@@ -1,0 +1,426 @@
+// Products with an E4M3 base that has a scale for each block of 128, on gfx950:
+//
+//     y[t, n] = sum_b sx[b, t] sw[n / 128, b] sum_{k in block b} qx[t, k] qw[n, k]
+//
+// with qx, sx the codes and scales of 1 x 128 groups of the rows and qw, sw those of 128 x
+// 128 blocks of W [d_out, d_in].  lora_linear_e4m3_block is that product;
+// lora_fused_linear_e4m3_block quantizes x itself and adds every token's correction
+// scale_s (x A_s) B_s from the unquantized x, as further steps of the same accumulators.
+//
+// One workgroup computes 16 TN WN columns x 16 TM WM rows with WN x WM waves on
+// v_mfma_f32_16x16x128_f8f6f4, whose 128 is a block: one instruction is the inner sum of 16
+// columns and 16 rows.  fp32 scales: it starts from 0 and its result enters the fp32
+// accumulators with one fma a value (a lane's four values are one row's, so the factor
+// sx sw is one register a row tile).  E8M0 scales: the instruction takes the two scale
+// bytes itself and accumulates.  MFMA rows are columns of W, MFMA columns are rows of x.
+//
+// A stage is a block: 128 bytes of each row of W and of x, and the rows' scales, brought
+// to LDS by direct loads.  16-byte unit u of row r lies in slot u ^ (r % 8), so that 8
+// rows at one unit cover all banks.  Of the 128 a lane takes units g and g + 4 (g = lane /
+// 16) on both sides: within a block the order of k does not matter.  The rows of W are
+// placed so that a lane ends with 4 TN adjacent columns of a row.
+#include "device.h"
+#include "internal.h"
+
+#include <algorithm>
+
+namespace lora {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+constexpr int kG = 128;
+
+// Read-only memory at a wave-uniform address: scalar loads.
+template <typename T> using cptr = const __attribute__((address_space(4))) T *;
+
+struct BlockArgs {
+    const uint8_t *x; // codes [T][ldx]
+    int64_t ldx;
+    const void *sx; // [groups][lds]
+    int64_t lds;
+    const uint8_t *W; // codes [n][k]
+    const void *sw;   // [n / 128][groups]
+    int k, n, T;
+    const int32_t *perm; // output row of each row (-1: none); null: the row itself
+    void *y;
+    int64_t ldy;
+    int vec_y; // whole aligned 16-byte pieces of y
+    int tiles_m, tiles_n;
+    // the correction
+    const int32_t *segidx;
+    const lora_seg_desc *seg;
+    int Tp;
+    const int32_t *tp_dev;
+    const uint16_t *vh;
+    int64_t ldh;
+};
+
+template <int TN_, int TM_, int WN_, int WM_, int STAGES> struct Shape {
+    static constexpr int TN = TN_, TM = TM_, WN = WN_, WM = WM_, kStages = STAGES;
+    static constexpr int kBN = 16 * TN * WN, kBM = 16 * TM * WM, kWaves = WN * WM, kThreads = 64 * kWaves;
+    static constexpr int kWBytes = kBN * kG, kXBytes = kBM * kG;
+    static constexpr int kSBytes = kBM <= 64 ? 256 : 4 * kBM; // the rows' scales
+    static constexpr int kStageBytes = kWBytes + kXBytes + kSBytes;
+    static constexpr int kWDma = kWBytes / 1024 / kWaves, kXDma = kXBytes / 1024 / kWaves;
+    static constexpr int kDma = kWDma + kXDma + 1; // direct loads of a wave in a stage
+    static_assert(kWDma * kWaves * 1024 == kWBytes && kXDma * kWaves * 1024 == kXBytes, "stage split");
+    static_assert(kStages * kStageBytes <= 160 * 1024, "LDS budget");
+    static_assert(kDma * (kStages - 2) <= 63, "vmcnt range");
+    static_assert(16 * TN <= kG && kG % (16 * TN) == 0, "a wave's columns lie in one block");
+};
+
+__device__ __forceinline__ void dma4(const void *g, uint32_t lds_byte)
+{
+    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(lds_byte) : "memory");
+}
+
+// Column of a wave's tile t that MFMA row m stands for: lane group g ends with columns
+// 4 TN g + 4 t + q.
+template <int TN> __device__ __forceinline__ int wave_col(int m, int t) { return (m >> 2) * (4 * TN) + 4 * t + (m & 3); }
+
+// The correction of the segments that meet rows pw0 .. pw0 + 16 TM, on bf16 MFMA: 16
+// ranks a step, B_s against the hi and lo halves of scale_s v.
+template <int TN, int TM>
+__device__ __forceinline__ void correction(const BlockArgs &a, int Tp, int pw0, int cw0, int lane, floatx4 (&acc)[TN][TM])
+{
+    const int m = lane & 15, g = lane >> 4;
+    const int plast = (pw0 + 16 * TM < Tp ? pw0 + 16 * TM : Tp) - 1;
+    const int s0 = uniform(a.segidx[pw0]), s1 = uniform(a.segidx[plast]);
+    for (int s = s0; s <= s1; ++s) {
+        const lora_seg_desc *d = a.seg + s;
+        const gptr<uint16_t> B = as_global<uint16_t>(reinterpret_cast<const void *>(d->B));
+        const int r = d->rank, p0 = d->start, p1 = d->start + d->len;
+        for (int j0 = 0; j0 < r; j0 += 16) {
+            const int jj = j0 + 8 * (g & 1);
+            bf16x8 bf[TN], vf[TM];
+#pragma unroll
+            for (int t = 0; t < TN; ++t) {
+                const int c = cw0 + wave_col<TN>(m, t);
+                const gptr<uint16_t> row = B + int64_t(c < a.n ? c : a.n - 1) * r;
+                if ((r & 7) == 0) {
+                    u32x4 u = *(gptr<u32x4>)(row + (jj < r ? jj : 0));
+                    if (jj >= r) u = u32x4{};
+                    bf[t] = __builtin_bit_cast(bf16x8, u);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int j = jj + e;
+                        const uint16_t h = row[j < r ? j : r - 1];
+                        bf[t][e] = __builtin_bit_cast(__bf16, j < r ? h : uint16_t(0));
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                const int p = pw0 + 16 * i + m;
+                const bool in = p >= p0 && p < p1;
+                u32x4 u = *(gptr<u32x4>)(as_global<uint16_t>(a.vh) + int64_t(in ? p : p0) * a.ldh + 2 * j0 + 8 * g);
+                if (!in) u = u32x4{};
+                vf[i] = __builtin_bit_cast(bf16x8, u);
+            }
+#pragma unroll
+            for (int t = 0; t < TN; ++t)
+#pragma unroll
+                for (int i = 0; i < TM; ++i) acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[t], vf[i], acc[t][i], 0, 0, 0);
+        }
+    }
+}
+
+// Row p's values of columns c0 .. c0 + 4 TN - 1.
+template <int TN, bool F32OUT>
+__device__ __forceinline__ void store_row(const BlockArgs &a, int64_t row, int c0, const float (&v)[4 * TN])
+{
+    constexpr int kPiece = F32OUT ? 4 : 8;
+#pragma unroll
+    for (int h = 0; h < 4 * TN / kPiece; ++h) {
+        const int c = c0 + h * kPiece;
+        const float *f = v + h * kPiece;
+        if (a.vec_y && c + kPiece <= a.n) {
+            u32x4 w;
+            if constexpr (F32OUT) w = u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+            else w = u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
+            *reinterpret_cast<u32x4 *>(static_cast<char *>(a.y) + (row * a.ldy + c) * (F32OUT ? 4 : 2)) = w;
+        } else {
+#pragma unroll
+            for (int q = 0; q < kPiece; ++q)
+                if (c + q < a.n) {
+                    if constexpr (F32OUT) static_cast<float *>(a.y)[row * a.ldy + c + q] = f[q];
+                    else static_cast<uint16_t *>(a.y)[row * a.ldy + c + q] = uint16_t(f32_to_bf16(f[q]));
+                }
+        }
+    }
+}
+
+template <class S, bool E8, bool F32OUT, bool LORA>
+__global__ __launch_bounds__(S::kThreads) __attribute__((amdgpu_waves_per_eu(S::kWaves / 4, S::kWaves / 4 * (S::kStages * S::kStageBytes <= 80 * 1024 ? 2 : 1))))
+void block_gemm_kernel(BlockArgs a)
+{
+    constexpr int TN = S::TN, TM = S::TM;
+    __shared__ __attribute__((aligned(1024))) char lds[S::kStages * S::kStageBytes];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = uniform(tid >> 6);
+    const int m = lane & 15, g = lane >> 4;
+    const int wn = wave / S::WM, wm = wave % S::WM;
+    const uint32_t lds0 = uint32_t(uintptr_t((__attribute__((address_space(3))) char *)(lds)));
+
+    // row tiles fastest, a contiguous run of tiles for each XCD
+    const int nwg = a.tiles_m * a.tiles_n;
+    int tile = blockIdx.x;
+    if ((nwg & 7) == 0) tile = (tile & 7) * (nwg >> 3) + (tile >> 3);
+    const int m0 = tile % a.tiles_m * S::kBM, n0 = tile / a.tiles_m * S::kBN;
+    const int nk = (a.k + kG - 1) / kG;
+
+    // Direct loads: load i of a part fills LDS rows 8 i .. 8 i + 7; this lane row 8 i +
+    // lane / 8, slot lane % 8, which holds unit slot ^ (row % 8).
+    const int unit = (lane & 7) ^ (lane >> 3);
+    uint32_t woff[S::kWDma], xoff[S::kXDma];
+#pragma unroll
+    for (int j = 0; j < S::kWDma; ++j) {
+        const int rho = (wave * S::kWDma + j) * 8 + (lane >> 3), rp = rho % (16 * TN);
+        int c = n0 + rho / (16 * TN) * (16 * TN) + wave_col<TN>(rp & 15, rp >> 4);
+        c = c < a.n ? c : a.n - 1;
+        woff[j] = uint32_t(int64_t(c) * a.k + 16 * unit);
+    }
+#pragma unroll
+    for (int j = 0; j < S::kXDma; ++j) {
+        int p = m0 + (wave * S::kXDma + j) * 8 + (lane >> 3);
+        p = p < a.T ? p : a.T - 1;
+        xoff[j] = uint32_t(p * a.ldx + 16 * unit);
+    }
+    // scales: a wave brings 64 rows' (E8M0: 256 rows', 4 a lane); others repeat them
+    constexpr int kSRows = E8 ? 256 : 64, kSParts = (S::kBM + kSRows - 1) / kSRows;
+    const int spart = wave % kSParts;
+    int sp = m0 + spart * kSRows + (E8 ? 4 : 1) * lane;
+    sp = sp < a.T ? sp : (E8 ? (a.T - 1) & ~3 : a.T - 1);
+    const char *sxp = static_cast<const char *>(a.sx) + int64_t(sp) * (E8 ? 1 : 4);
+    const int64_t sstep = a.lds * (E8 ? 1 : 4);
+
+    auto issue = [&](int kt) {
+        const uint32_t base = lds0 + uint32_t(kt % S::kStages) * S::kStageBytes;
+        const uint8_t *wb = a.W + int64_t(kt) * kG, *xb = a.x + int64_t(kt) * kG;
+        const bool in = kt * kG + 16 * unit < a.k; // units past k are zeros (on both sides)
+#pragma unroll
+        for (int j = 0; j < S::kWDma; ++j)
+            dma16(in ? static_cast<const void *>(wb + woff[j]) : g_zeros, base + uint32_t(wave * S::kWDma + j) * 1024);
+#pragma unroll
+        for (int j = 0; j < S::kXDma; ++j)
+            dma16(in ? static_cast<const void *>(xb + xoff[j]) : g_zeros, base + S::kWBytes + uint32_t(wave * S::kXDma + j) * 1024);
+        dma4(sxp + kt * sstep, base + S::kWBytes + S::kXBytes + uint32_t(spart) * 256);
+    };
+
+    floatx4 acc[TN][TM];
+#pragma unroll
+    for (int t = 0; t < TN; ++t)
+#pragma unroll
+        for (int i = 0; i < TM; ++i) acc[t][i] = floatx4{};
+    const int pw0 = m0 + 16 * TM * wm, cw0 = n0 + 16 * TN * wn;
+    if constexpr (LORA) {
+        const int Tp = a.tp_dev ? uniform(*a.tp_dev) : a.Tp;
+        if (pw0 < Tp) correction<TN, TM>(a, Tp, pw0, cw0, lane, acc);
+    }
+    int64_t yrow[TM];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        const int p = pw0 + 16 * i + m;
+        yrow[i] = p < a.T ? (a.perm ? as_global<int32_t>(a.perm)[p] : p) : -1;
+    }
+    // every load so far is complete: none of the compiler's waits in the loop is for one
+    // of them, and would be for the direct loads behind it too
+    __builtin_amdgcn_s_waitcnt(wait_vm(0));
+#pragma unroll
+    for (int s = 0; s < S::kStages - 1; ++s) issue(s < nk ? s : nk - 1);
+
+    // the wave's block of W: columns past n repeat the last ones, which are not stored
+    const int nb = (cw0 < a.n ? cw0 : a.n - 1) / kG;
+    const int u0 = (g ^ (m & 7)) << 4, u1 = ((g + 4) ^ (m & 7)) << 4;
+    const uint32_t wrow = uint32_t((16 * TN * wn + m) * kG), xrow = uint32_t(S::kWBytes + (16 * TM * wm + m) * kG);
+    auto frag = [&](const char *row) {
+        const u32x4 lo = *reinterpret_cast<const u32x4 *>(row + u0), hi = *reinterpret_cast<const u32x4 *>(row + u1);
+        return i32x8{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]), int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])};
+    };
+    for (int kt = 0; kt < nk; ++kt) {
+        // this wave's loads of stage kt have landed and its reads of stage kt - 1 are
+        // done; past the barrier that holds for every wave
+        __builtin_amdgcn_s_waitcnt(wait_vm_lds0(S::kDma * (S::kStages - 2)));
+        __builtin_amdgcn_s_barrier();
+        const int nxt = kt + S::kStages - 1;
+        issue(nxt < nk ? nxt : nk - 1);
+        const char *st = lds + (kt % S::kStages) * S::kStageBytes;
+        const char *ss = st + S::kWBytes + S::kXBytes;
+        const int r0 = 16 * TM * wm + m;
+        i32x8 xf[TM];
+#pragma unroll
+        for (int i = 0; i < TM; ++i) xf[i] = frag(st + xrow + i * 16 * kG);
+        if constexpr (E8) {
+            // one byte by a scalar load of its aligned word
+            const uintptr_t at = reinterpret_cast<uintptr_t>(a.sw) + size_t(int64_t(nb) * nk + kt);
+            const int ws = int(*(cptr<uint32_t>)(at & ~uintptr_t(3)) >> (8 * (at & 3)) & 255);
+            int xs[TM];
+#pragma unroll
+            for (int i = 0; i < TM; ++i) xs[i] = *reinterpret_cast<const uint8_t *>(ss + r0 + 16 * i);
+#pragma unroll
+            for (int t = 0; t < TN; ++t) {
+                const i32x8 wf = frag(st + wrow + t * 16 * kG);
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+                    acc[t][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf[i], acc[t][i], 0, 0, 0, ws, 0, xs[i]);
+            }
+        } else {
+            const float ws = ((cptr<float>)(a.sw))[int64_t(nb) * nk + kt];
+            float f[TM];
+#pragma unroll
+            for (int i = 0; i < TM; ++i) f[i] = ws * *reinterpret_cast<const float *>(ss + 4 * (r0 + 16 * i));
+#pragma unroll
+            for (int t = 0; t < TN; ++t) {
+                const i32x8 wf = frag(st + wrow + t * 16 * kG);
+#pragma unroll
+                for (int i = 0; i < TM; ++i) {
+                    // scale bytes of 127: 2^0
+                    const floatx4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf[i], floatx4{}, 0, 0, 0, 127, 0, 127);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) acc[t][i][q] = fmaf(p[q], f[i], acc[t][i][q]);
+                }
+            }
+        }
+    }
+    // no direct load may still be writing this workgroup's LDS when it ends
+    __builtin_amdgcn_s_waitcnt(wait_vm(0));
+
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        if (yrow[i] < 0) continue;
+        float v[4 * TN];
+#pragma unroll
+        for (int t = 0; t < TN; ++t)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[4 * t + q] = acc[t][i][q];
+        store_row<TN, F32OUT>(a, yrow[i], cw0 + 4 * TN * g, v);
+    }
+}
+
+typedef Shape<8, 4, 2, 4, 2> Large;  // 256 columns x 256 rows, 8 waves
+typedef Shape<4, 4, 2, 2, 2> Medium; // 128 x 128, 4 waves, two workgroups on a CU
+typedef Shape<2, 2, 4, 2, 3> Small;  // 128 x 64, 8 waves
+
+template <class S> int go(hipStream_t s, BlockArgs &a, bool e8, bool f32out, bool lora)
+{
+    a.tiles_m = (a.T + S::kBM - 1) / S::kBM;
+    a.tiles_n = (a.n + S::kBN - 1) / S::kBN;
+    const int64_t tiles = int64_t(a.tiles_m) * a.tiles_n;
+    if (tiles > most_workgroups(S::kThreads)) return fail(LORA_ERR_ARG, "block product: too many tiles");
+    const dim3 grid{unsigned(tiles)};
+    const dim3 block(S::kThreads);
+    if (lora) {
+        if (e8) launch_kernel(block_gemm_kernel<S, true, false, true>, grid, block, 0, s, a);
+        else launch_kernel(block_gemm_kernel<S, false, false, true>, grid, block, 0, s, a);
+    } else if (f32out) {
+        if (e8) launch_kernel(block_gemm_kernel<S, true, true, false>, grid, block, 0, s, a);
+        else launch_kernel(block_gemm_kernel<S, false, true, false>, grid, block, 0, s, a);
+    } else {
+        if (e8) launch_kernel(block_gemm_kernel<S, true, false, false>, grid, block, 0, s, a);
+        else launch_kernel(block_gemm_kernel<S, false, false, false>, grid, block, 0, s, a);
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return fail(LORA_ERR_HIP, "block product launch: %s", hipGetErrorString(e));
+    return LORA_OK;
+}
+
+int launch_product(hipStream_t s, BlockArgs &a, bool e8, bool f32out, bool lora)
+{
+    if (a.T <= 64) return go<Small>(s, a, e8, f32out, lora);
+    const int64_t large = int64_t(a.T + 255) / 256 * ((a.n + 255) / 256);
+    if (large >= 128) return go<Large>(s, a, e8, f32out, lora);
+    return go<Medium>(s, a, e8, f32out, lora);
+}
+
+// Workspace of the fused call: the shrink's slice partials, v's halves, x's codes (rows of
+// whole blocks) and scales (rows padded to 4).
+int64_t vh_pitch(int32_t max_rank) { return 2 * int64_t((max_rank + 15) / 16 * 16); }
+struct FusedBlockWs {
+    size_t vh, codes, scales, end;
+    int64_t ldq, lds;
+    FusedBlockWs(int32_t T, int32_t d_in, int32_t max_rank)
+    {
+        const int64_t groups = (int64_t(d_in) + kG - 1) / kG;
+        ldq = groups * kG;
+        lds = (int64_t(T) + 3) / 4 * 4;
+        vh = up256(combined_workspace_bytes(T, d_in, max_rank));
+        codes = vh + up256(size_t(T) * size_t(vh_pitch(max_rank)) * 2);
+        scales = codes + up256(size_t(T) * size_t(ldq));
+        end = scales + up256(size_t(groups) * size_t(lds) * 4);
+    }
+};
+
+} // namespace
+
+int launch_linear_block(hipStream_t s, const LinearBlockCall &c)
+{
+    if (c.T == 0) return LORA_OK;
+    BlockArgs a{};
+    a.x = static_cast<const uint8_t *>(c.x);
+    a.ldx = c.ldx;
+    a.sx = c.sx;
+    a.lds = c.lds;
+    a.W = static_cast<const uint8_t *>(c.W);
+    a.sw = c.sw;
+    a.k = c.d_in;
+    a.n = c.d_out;
+    a.T = c.T;
+    a.y = c.y;
+    a.ldy = c.ldy;
+    const int es = c.out_dtype == LORA_F32 ? 4 : 2;
+    a.vec_y = aligned16(c.y) && c.ldy * es % 16 == 0;
+    return launch_product(s, a, c.scale_type == LORA_SCALE_E8M0, c.out_dtype == LORA_F32, false);
+}
+
+size_t fused_block_workspace_bytes(int32_t T, int32_t d_in, int32_t max_rank) { return FusedBlockWs(T, d_in, max_rank).end; }
+
+int launch_fused_linear_block(hipStream_t s, const ShrinkArgs &sa, const void *W0, const void *sw, int scale_type,
+                              const ExpandArgs &ea, const PlanView &p, void *ws)
+{
+    const int T = p.h->num_tokens;
+    const int max_rank = p.h->max_rank < 1 ? 1 : p.h->max_rank;
+    const FusedBlockWs w(T, sa.d_in, max_rank);
+    char *base = static_cast<char *>(ws);
+    BlockArgs a{};
+    a.perm = reinterpret_cast<const int32_t *>(p.dev + p.h->perm_offset);
+    QuantCall q{};
+    q.dtype = LORA_BF16;
+    q.x = sa.x;
+    q.ldx = sa.ldx;
+    q.rows = T;
+    q.cols = sa.d_in;
+    q.perm = a.perm;
+    q.codes = base + w.codes;
+    q.ldq = w.ldq;
+    q.pad = true;
+    q.block_rows = 1;
+    q.scale_type = scale_type;
+    q.scales = base + w.scales;
+    q.lds = w.lds;
+    int st = launch_quantize(s, q);
+    if (st) return st;
+    uint16_t *vh = reinterpret_cast<uint16_t *>(base + w.vh);
+    a.ldh = vh_pitch(max_rank);
+    if (p.h->num_sorted > 0 && (st = launch_v_halves(s, sa, p, ws, vh, a.ldh))) return st;
+    a.x = static_cast<const uint8_t *>(q.codes);
+    a.ldx = w.ldq;
+    a.sx = q.scales;
+    a.lds = w.lds;
+    a.W = static_cast<const uint8_t *>(W0);
+    a.sw = sw;
+    a.k = sa.d_in;
+    a.n = ea.d_out;
+    a.T = T;
+    a.y = ea.y;
+    a.ldy = ea.ldy;
+    a.vec_y = 1;
+    a.segidx = reinterpret_cast<const int32_t *>(p.dev + p.h->segidx_offset);
+    a.seg = reinterpret_cast<const lora_seg_desc *>(p.dev + p.h->seg_offset);
+    a.Tp = p.h->num_sorted;
+    a.tp_dev = plan_sorted_dev(p);
+    a.vh = vh;
+    return launch_product(s, a, scale_type == LORA_SCALE_E8M0, false, true);
+}
+
+} // namespace lora

@@ -138,6 +138,7 @@ struct FusedArgs {
     const int32_t *segidx;    // [T'] sorted position -> segment
     const lora_seg_desc *seg; // [S]
     int T, Tp;
+    const int32_t *tp_dev;    // the device's Tp where the host has a bound (a plan built on the device), else null
     const uint16_t *vh; // split scaled v rows (fused_prep_kernel)
     int64_t ldh;
     uint16_t *y;
@@ -170,9 +171,9 @@ __global__ __launch_bounds__(256) void fused_prep_kernel(const float *__restrict
         f[c][0] = *reinterpret_cast<const floatx4 *>(row + jh);
         f[c][1] = *reinterpret_cast<const floatx4 *>(row + jl);
     }
-    const int s = segidx[p];
-    const int r = seg[s].rank;
-    const float scale = seg[s].scale;
+    const int s = segidx[p]; // -1: past the adapted rows of a plan built on the device
+    const int r = s < 0 ? 0 : seg[s].rank;
+    const float scale = s < 0 ? 0.f : seg[s].scale;
     float val[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -360,7 +361,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
         xk[j] = 8 * ((u & 3) ^ swz(row));
         int p = m0 + row;
         p = p < a.T ? p : a.T - 1;
-        xoff32[j] = uint32_t((int64_t(as_global<int32_t>(a.perm)[p]) * a.ldx + xk[j]) * 2);
+        const int t = as_global<int32_t>(a.perm)[p]; // -1: a row of the padding, not stored
+        xoff32[j] = uint32_t((int64_t(t < 0 ? 0 : t) * a.ldx + xk[j]) * 2);
     }
     const int nk = (a.d_in + kBK - 1) / kBK;
     // stage kt into ring slot kt % kStages.  A full stage adds kt * kBK
@@ -413,8 +415,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     // queue behind them
     const int pw0 = m0 + kWM * wm;
     const int cw0 = n0 + kWN * wn;
-    if (pw0 < a.Tp) {
-        const int plast = (pw0 + kWM < a.Tp ? pw0 + kWM : a.Tp) - 1;
+    const int Tp = a.tp_dev ? uniform(*a.tp_dev) : a.Tp;
+    if (pw0 < Tp) {
+        const int plast = (pw0 + kWM < Tp ? pw0 + kWM : Tp) - 1;
         const int s0 = __builtin_amdgcn_readfirstlane(a.segidx[pw0]);
         const int s1 = __builtin_amdgcn_readfirstlane(a.segidx[plast]);
         lora_correction<VECB>(a, s0, s1, pw0, cw0, lane, acc);
@@ -575,6 +578,33 @@ size_t fused_workspace_bytes(int32_t T, int32_t d_in, int32_t max_rank)
     return vh_offset(T, d_in, max_rank) + size_t(T) * size_t(vh_pitch(max_rank)) * 2 + 256;
 }
 
+int launch_v_halves(hipStream_t s, const ShrinkArgs &sa, const PlanView &p, void *ws, uint16_t *vh, int64_t ldh,
+                    float wdiv)
+{
+    float *v = static_cast<float *>(ws);
+    int64_t ldw = 0, sl_stride = 0;
+    int nsl = 0;
+    const int st = launch_sgmv_shrink_split(s, sa, p, v, &ldw, &sl_stride, &nsl);
+    if (st) return st;
+    if (nsl > kMaxSlicesFused) return fail(LORA_ERR_ARG, "fused layer: %d d_in slices > %d", nsl, kMaxSlicesFused);
+    const int Tp = p.h->num_sorted;
+    if (Tp == 0) return LORA_OK;
+    const int32_t *segidx = reinterpret_cast<const int32_t *>(p.dev + p.h->segidx_offset);
+    const lora_seg_desc *segs = reinterpret_cast<const lora_seg_desc *>(p.dev + p.h->seg_offset);
+    const int units = int(ldh / 16);
+    const int64_t threads = int64_t(Tp) * units;
+    const dim3 grid(unsigned((threads + 255) / 256));
+    if (wdiv != 0.f)
+        launch_kernel(fused_prep_kernel<true>, grid, dim3(256), 0, s, v, ldw, sl_stride, nsl, segidx, segs, Tp, units,
+                      wdiv, vh, ldh);
+    else
+        launch_kernel(fused_prep_kernel<false>, grid, dim3(256), 0, s, v, ldw, sl_stride, nsl, segidx, segs, Tp, units,
+                      1.0f, vh, ldh);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return fail(LORA_ERR_HIP, "fused layer prep launch: %s", hipGetErrorString(e));
+    return LORA_OK;
+}
+
 int launch_fused_linear(hipStream_t s, const ShrinkArgs &sa, const void *W0, const ExpandArgs &ea,
                         const PlanView &p, void *ws, bool w0_e4m3, float w0_scale)
 {
@@ -587,31 +617,13 @@ int launch_fused_linear(hipStream_t s, const ShrinkArgs &sa, const void *W0, con
     const bool off32 = (int64_t(T) * sa.ldx + sa.d_in) * 2 < (int64_t(1) << 32) &&
                        (int64_t(ea.d_out) * sa.d_in + sa.d_in) * wel < (int64_t(1) << 32);
     if (!off32) return fail(LORA_ERR_ARG, "fused layer: x or W0 spans 4 GiB or more");
-    float *v = static_cast<float *>(ws);
-    int64_t ldw = 0, sl_stride = 0;
-    int nsl = 0;
-    int st = launch_sgmv_shrink_split(s, sa, p, v, &ldw, &sl_stride, &nsl);
-    if (st) return st;
-    const int Tp = p.h->num_sorted;
     const int max_rank = p.h->max_rank < 1 ? 1 : p.h->max_rank;
     uint16_t *vh = reinterpret_cast<uint16_t *>(static_cast<char *>(ws) + vh_offset(T, sa.d_in, max_rank));
     const int64_t ldh = vh_pitch(max_rank);
     const int32_t *segidx = reinterpret_cast<const int32_t *>(p.dev + p.h->segidx_offset);
     const lora_seg_desc *segs = reinterpret_cast<const lora_seg_desc *>(p.dev + p.h->seg_offset);
-    if (nsl > kMaxSlicesFused) return fail(LORA_ERR_ARG, "fused layer: %d d_in slices > %d", nsl, kMaxSlicesFused);
-    if (Tp > 0) {
-        const int units = int(ldh / 16);
-        const int64_t threads = int64_t(Tp) * units;
-        const dim3 grid(unsigned((threads + 255) / 256));
-        if (w0_e4m3)
-            launch_kernel(fused_prep_kernel<true>, grid, dim3(256), 0, s, v, ldw, sl_stride, nsl, segidx, segs, Tp,
-                          units, w0_scale, vh, ldh);
-        else
-            launch_kernel(fused_prep_kernel<false>, grid, dim3(256), 0, s, v, ldw, sl_stride, nsl, segidx, segs, Tp,
-                          units, 1.0f, vh, ldh);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return fail(LORA_ERR_HIP, "fused layer prep launch: %s", hipGetErrorString(e));
-    }
+    const int st = launch_v_halves(s, sa, p, ws, vh, ldh, w0_e4m3 ? w0_scale : 0.f);
+    if (st) return st;
     FusedArgs a{};
     a.x = static_cast<const uint16_t *>(sa.x);
     a.ldx = sa.ldx;
@@ -624,6 +636,7 @@ int launch_fused_linear(hipStream_t s, const ShrinkArgs &sa, const void *W0, con
     a.seg = segs;
     a.T = T;
     a.Tp = p.h->num_sorted;
+    a.tp_dev = plan_sorted_dev(p);
     a.vh = vh;
     a.ldh = ldh;
     a.y = static_cast<uint16_t *>(ea.y);
@@ -635,7 +648,9 @@ int launch_fused_linear(hipStream_t s, const ShrinkArgs &sa, const void *W0, con
     bool vecb = true;
     const lora_seg_desc *hseg = reinterpret_cast<const lora_seg_desc *>(reinterpret_cast<const char *>(p.h) +
                                                                         p.h->seg_offset);
-    for (int i = 0; i < p.h->num_segments; ++i) vecb = vecb && (hseg[i].rank & 7) == 0;
+    if (plan_on_device(p.h)) vecb = plan_rank_multiple(p.h) % 8 == 0;
+    else
+        for (int i = 0; i < p.h->num_segments; ++i) vecb = vecb && (hseg[i].rank & 7) == 0;
     const dim3 grid(static_cast<unsigned>(nwg));
     if (w0_e4m3) {
         if (vecb) launch_kernel(fused_linear_kernel<true, true>, grid, dim3(kThreads), 0, s, a);

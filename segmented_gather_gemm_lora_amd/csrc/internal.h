@@ -21,6 +21,24 @@ struct PlanView {
     const char *dev;           // device copy (same layout)
 };
 
+// A plan built on the device: its host header holds bounds of the counts, and there are
+// no host copies of its records.  reserved: bit 0, then the rank multiple in bits 8 .. 15.
+inline bool plan_on_device(const lora_plan_header *h) { return h->reserved & 1; }
+inline int plan_rank_multiple(const lora_plan_header *h) { return int(h->reserved >> 8 & 255); }
+// The device's count of adapted rows where the host has only its bound, else nullptr.
+inline const int32_t *plan_sorted_dev(const PlanView &p)
+{
+    return plan_on_device(p.h) ? &reinterpret_cast<const lora_plan_header *>(p.dev)->num_sorted : nullptr;
+}
+struct DevicePlanCall {
+    const int32_t *adapters, *lengths;
+    int32_t n_requests, n_adapters, max_rank, rank_multiple;
+    const uint64_t *pool_A, *pool_B;
+    const int32_t *pool_rank;
+    const float *pool_alpha;
+};
+int launch_plan_device(hipStream_t s, const DevicePlanCall &c, const lora_plan_header &h, void *dev);
+
 // Launch geometry / path choices made on the host.
 struct ShrinkArgs {
     int dtype;
@@ -159,6 +177,48 @@ int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p
 int launch_dx_join(hipStream_t s, const BackwardArgs &b, const PlanView &p, void *ws, const float *parts, int splits);
 size_t fused_backward_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out, int32_t max_rank);
 int launch_fused_backward(hipStream_t s, const BackwardArgs &b, const void *W0, const PlanView &p, void *ws);
+
+// E4M3 codes and scales of a matrix, in blocks of 1 x 128 or 128 x 128 (block_rows).  perm:
+// row p of the result is row perm[p] of x (-1: zeros).  pad: zero codes up to whole blocks.
+struct QuantCall {
+    int dtype;
+    const void *x;
+    int64_t ldx;
+    int32_t rows, cols;
+    const int32_t *perm;
+    void *codes;
+    int64_t ldq;
+    bool pad;
+    int block_rows, scale_type;
+    void *scales;
+    int64_t lds;
+};
+int launch_quantize(hipStream_t s, const QuantCall &q);
+
+// y = (sx qx) (sw qw)^T
+struct LinearBlockCall {
+    int32_t T;
+    const void *x;
+    int64_t ldx;
+    const void *sx;
+    int64_t lds;
+    int32_t d_in;
+    const void *W, *sw;
+    int scale_type;
+    int32_t d_out;
+    int out_dtype;
+    void *y;
+    int64_t ldy;
+};
+int launch_linear_block(hipStream_t s, const LinearBlockCall &c);
+size_t fused_block_workspace_bytes(int32_t T, int32_t d_in, int32_t max_rank);
+int launch_fused_linear_block(hipStream_t s, const ShrinkArgs &sa, const void *W0, const void *sw, int scale_type,
+                              const ExpandArgs &ea, const PlanView &p, void *ws);
+// The shrink of the plan's rows into ws (combined_workspace_bytes), then scale_s v in
+// two bf16 halves, for 16 ranks each 16 hi and 16 lo, ldh apart from row to row (plan
+// order; zeros past the adapted rows).  The value is divided by wdiv unless that is 0.
+int launch_v_halves(hipStream_t s, const ShrinkArgs &sa, const PlanView &p, void *ws, uint16_t *vh, int64_t ldh,
+                    float wdiv = 0.f);
 
 // Workgroups that one launch may have: the runtime counts threads in 32 bits.
 constexpr int64_t most_workgroups(int threads) { return 0xFFFFFFFFll / threads; }

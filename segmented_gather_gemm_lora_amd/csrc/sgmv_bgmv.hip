@@ -990,6 +990,7 @@ __device__ __forceinline__ void sgmv_shrink_item(const void *__restrict__ x, int
     const int item = int(b & 7) * per + int(b >> 3);
     if (item >= total) return;
     const lora_blk_desc *bd = blks + item % nblk;
+    if (bd->n <= 0) return; // an unused record of a plan built on the device
     shrink_block_slice<DT, VEC, W, NSTEP, RT, M>(x, ldx, d_in, bd->rows, bd->n, bd->p0,
                                                  reinterpret_cast<const void *>(bd->A), bd->rank, item / nblk,
                                                  slice_len, out, ldo, sl_stride, mem);
@@ -1024,6 +1025,7 @@ void sgmv_expand_kernel(const float *__restrict__ v, int64_t ldv, int64_t sl_str
 {
     extern __shared__ floatx4 vl4[];
     const lora_blk_desc *d = blks + blockIdx.y;
+    if (d->n <= 0) return; // an unused record of a plan built on the device
     expand_rows<DT, VECY, false, UPT, M, MAXNCH>(v, ldv, sl_stride, nsl, reinterpret_cast<const void *>(d->B), d->rank,
                                          d->scale, y, ldy, d_out, blockIdx.x * kExpandCols, vec_b, d->rows, d->p0,
                                          d->n, reinterpret_cast<float *>(vl4), ldl, mem);
@@ -1557,6 +1559,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void s
         if (item >= total) return;
         const int blk = item % a.nblk, sl = item / a.nblk;
         const lora_blk_desc *bd = a.blks + blk;
+        if (bd->n <= 0) return; // an unused record of a plan built on the device
         shrink_block_slice<DT, true, 4, NSTEP, RT, DenseMem, 2>(
             a.x, a.ldx, a.d_in, bd->rows, bd->n, bd->p0, reinterpret_cast<const void *>(bd->A), bd->rank, sl,
             a.slice_len, a.part, a.ldw, a.sl_stride, DenseMem{}, tag);
@@ -1567,6 +1570,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void s
     const lora_chunk_desc *cd = a.chunks + ci;
     const int r = cd->rank;
     const int n = min(cd->n, kChunkRB * kRows);
+    if (n <= 0) return; // as above
     const TagWait w{tag, a.status, a.wait_limit};
     const void *B = reinterpret_cast<const void *>(cd->B);
     float *vl = reinterpret_cast<float *>(vl4);
@@ -1768,6 +1772,7 @@ void sgmv_expand_chunk_grouped_kernel(const SGExpandTable tab, int n_proj)
     const lora_chunk_desc *d = P.chunks + ci;
     const int r = d->rank;
     const int n = d->n < kChunkRB * kRows ? d->n : kChunkRB * kRows;
+    if (n <= 0) return; // an unused record of a plan built on the device
     const void *B = reinterpret_cast<const void *>(d->B);
     float *vl = reinterpret_cast<float *>(vl4);
     if (P.vec_b && (r & 3) == 0)
@@ -1788,6 +1793,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(6))) void s
     const SGExpand &P = tab.p[blockIdx.z];
     if (int(blockIdx.y) >= P.nblk || int(blockIdx.x) >= P.ncol) return;
     const lora_blk_desc *d = P.blks + blockIdx.y;
+    if (d->n <= 0) return; // an unused record of a plan built on the device
     expand_rows<DT, VECY, false, UPT>(P.v, P.ldv, P.sl_stride, P.nsl, reinterpret_cast<const void *>(d->B), d->rank,
                                       d->scale, P.y, P.ldy, P.d_out, blockIdx.x * kExpandCols, P.vec_b != 0, d->rows,
                                       d->p0, d->n, reinterpret_cast<float *>(vl4), P.ldl);
@@ -2089,7 +2095,9 @@ void sgmv_expand_launch(hipStream_t s, const ExpandArgs &a, const float *v, int6
     // Plans with ranks up to 64 (dense or paged), except the ones the
     // argument-table chunk kernel serves (ranks <= 32, enough chunk items): one
     // launch whose workgroups choose the block or chunk form per plan chunk.
-    const bool arg_chunks = p.h->num_chunks * ncol >= 1024 && ldl <= 32 && p.h->num_chunks <= kArgChunks;
+    // (a plan built on the device has no host copy of its chunks to pass)
+    const bool arg_chunks =
+        p.h->num_chunks * ncol >= 1024 && ldl <= 32 && p.h->num_chunks <= kArgChunks && !plan_on_device(p.h);
     if (ldl <= 64 && !arg_chunks) {
         const dim3 grid(ncol, p.h->num_chunks);
         const size_t shm = (size_t(kChunkRB * kRows) * 64 + 4) * sizeof(float);
