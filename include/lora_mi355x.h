@@ -806,6 +806,21 @@ int lora_fused_linear_backward(void *stream, int dtype, const void *x, int64_t l
                                const uint64_t *grad_A_dev, const uint64_t *grad_B_dev, int32_t n_adapters,
                                unsigned flags, void *dx, int64_t lddx, void *ws, size_t ws_bytes);
 
+/* Gradients of lora_fused_linear_e4m3_block: as lora_fused_linear_backward, the base's
+ * part of dx being the product of dy[t], quantized in groups of 128 of its columns with
+ * scales of the base's type, with W0:
+ *     dx[t, c] = sum_b dy_scale[b, t] w_scales[b, c / 128] sum_{n in block b} q_dy[t, n] W0[n, c] + u[t] A_i
+ * u, dA and dB are those of the unquantized dy.  The base is frozen: it gets no gradient.
+ * x, W0, dy, dx and the workspace are 16-byte aligned, ldx, lddy and lddx multiples of 8
+ * elements, d_in a multiple of 16 (d_out is free).  Needs ws_bytes >=
+ * lora_workspace_bytes(LORA_OP_FUSED_BLOCK_BACKWARD, T, d_in, d_out, max_rank).
+ * Errors: as lora_fused_linear_backward; LORA_ERR_DTYPE for an unknown scale type. */
+int lora_fused_linear_e4m3_block_backward(void *stream, const void *x, int64_t ldx, int32_t d_in, const void *W0,
+                                          const void *w_scales, int scale_type, const void *dy, int64_t lddy,
+                                          int32_t d_out, const lora_segments *seg, const uint64_t *grad_A_dev,
+                                          const uint64_t *grad_B_dev, int32_t n_adapters, unsigned flags, void *dx,
+                                          int64_t lddx, void *ws, size_t ws_bytes);
+
 /* ------------------------------------------------------------------ optimizer
  * AdamW (Loshchilov and Hutter, "Decoupled Weight Decay Regularization") over
  * many tensors in one launch: the step that uses the gradients above, for the

@@ -24,6 +24,7 @@ from .binding import (  # noqa: F401
     fused_linear,
     fused_linear_backward,
     fused_linear_e4m3_block,
+    fused_linear_e4m3_block_backward,
     lib_path,
     linear_e4m3_block,
     load,

@@ -66,7 +66,7 @@ EXPORTS = [
     "lora_probe_chase", "lora_workspace_clear", "lora_debug_wait_limit", "lora_bgmv_noalloc",
     "lora_sgmv_backward", "lora_fused_linear_backward", "lora_adamw_plan_bytes", "lora_adamw_plan", "lora_adamw_upload", "lora_adamw",
     "lora_adam_state_values", "lora_build_segments_device", "lora_quantize_e4m3", "lora_linear_e4m3_block",
-    "lora_fused_linear_e4m3_block",
+    "lora_fused_linear_e4m3_block", "lora_fused_linear_e4m3_block_backward",
 ]
 LORA_CACHE_DRY = 1
 MAX_PROJ = 8
@@ -147,6 +147,9 @@ _SIGS = {
                                               ctypes.c_int, _vp, _i64, _vp, _sz]),
     "lora_fused_linear_e4m3_block": (ctypes.c_int, [_vp, _vp, _i64, _i32, _vp, _vp, ctypes.c_int, _i32, _vp, _vp, _i64,
                                                     _vp, _sz]),
+    "lora_fused_linear_e4m3_block_backward": (ctypes.c_int, [_vp, _vp, _i64, _i32, _vp, _vp, ctypes.c_int, _vp, _i64,
+                                                             _i32, _vp, _vp, _vp, _i32, ctypes.c_uint, _vp, _i64, _vp,
+                                                             _sz]),
     "lora_probe_stream": (ctypes.c_int, [_vp, _vp, _i64, _vp, _i64, _vp, _i32]),
     "lora_probe_chase": (ctypes.c_int, [_vp, _vp, _i32, _vp]),
     "lora_page_alloc_create": (ctypes.c_int, [_i32, _vp]),
@@ -1384,6 +1387,23 @@ def fused_linear_backward(x, W0, dy, plan: Plan, grads: Optional[GradPool], dx, 
                                              LORA_GRAD_ACCUMULATE if accumulate else 0, pdx, lddx, ws.data_ptr(),
                                              ws.numel() * ws.element_size()),
            "lora_fused_linear_backward")
+
+
+def fused_linear_e4m3_block_backward(x, W0, w_scales, dy, plan: Plan, grads: Optional[GradPool], dx, ws,
+                                     accumulate: bool = False, stream=None):
+    """Gradients of fused_linear_e4m3_block: dx = Q(dy) W0 + u A (overwritten, every row; Q quantizes
+    groups of 128 columns with scales of the base's type), and the adapters' gradients as in
+    sgmv_backward (grads None: not wanted; x may then be None; what is refused is the same)."""
+    d_out, d_in = _block_base(W0, w_scales)
+    tA, tB, n = (None, None, 0) if grads is None else (grads.addr_A_dev, grads.addr_B_dev, grads.n_adapters)
+    device, (pdy, lddy, px, ldx, pdx, lddx) = _gradient_rows(
+        "bf16", plan.h.batch_tokens, (plan.dev, ws, W0, w_scales) if grads is None else (plan.dev, ws, W0, w_scales, tA, tB),
+        ((dy, d_out), (x, d_in), (dx, d_in)))
+    _fits_plan(plan, d_in, d_out, "bf16", grads, device)
+    _check(load().lora_fused_linear_e4m3_block_backward(
+        _stream_handle(stream, device), px, ldx, d_in, W0.data_ptr(), w_scales.data_ptr(), _scale_type(w_scales), pdy, lddy,
+        d_out, plan.seg, _ptr(tA), _ptr(tB), n, LORA_GRAD_ACCUMULATE if accumulate else 0, pdx, lddx, ws.data_ptr(),
+        ws.numel() * ws.element_size()), "lora_fused_linear_e4m3_block_backward")
 
 
 def adamw_hyper(n_groups: int, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, grad_scale=1.0, step=1,

@@ -240,6 +240,9 @@ size_t lora_workspace_bytes(int op, int32_t T, int32_t d_in, int32_t d_out, int3
     case LORA_OP_LINEAR_BLOCK: return 0;
     case LORA_OP_FUSED_BLOCK:
         return fused_block_workspace_bytes(T < 0 ? 0 : T, d_in < 1 ? 1 : d_in, max_rank < 1 ? 1 : max_rank);
+    case LORA_OP_FUSED_BLOCK_BACKWARD:
+        return fused_block_backward_workspace_bytes(T < 0 ? 0 : T, d_in < 1 ? 1 : d_in, d_out < 1 ? 1 : d_out,
+                                                    max_rank < 1 ? 1 : max_rank);
     case LORA_OP_SGMV: // control words, fp32 partials (two kernels), tagged partials (one launch)
         return sgmv_ctl_bytes(T < 0 ? 0 : T) +
                3 * combined_workspace_bytes(T < 0 ? 0 : T, d_in < 1 ? 1 : d_in, max_rank < 1 ? 1 : max_rank);
@@ -1095,6 +1098,39 @@ int lora_fused_linear_e4m3_block(void *stream, const void *x, int64_t ldx, int32
     ea.d_out = d_out;
     return launch_fused_linear_block(static_cast<hipStream_t>(stream), sa, W0, w_scales, scale_type, ea,
                                      PlanView{h, plan_dev}, ws);
+}
+
+int lora_fused_linear_e4m3_block_backward(void *stream, const void *x, int64_t ldx, int32_t d_in, const void *W0,
+                                          const void *w_scales, int scale_type, const void *dy, int64_t lddy,
+                                          int32_t d_out, const lora_segments *seg, const uint64_t *grad_A_dev,
+                                          const uint64_t *grad_B_dev, int32_t n_adapters, unsigned flags, void *dx,
+                                          int64_t lddx, void *ws, size_t ws_bytes)
+{
+    clear_error();
+    const lora_plan_header *h = nullptr;
+    const char *plan_dev = nullptr;
+    int st = check_segments(seg, &h, &plan_dev);
+    if (st) return st;
+    if ((st = check_scale_type(scale_type))) return st;
+    if (h->num_tokens == 0) return LORA_OK;
+    if (!plan_dev) return fail(LORA_ERR_ARG, "the segments' device buffer is NULL");
+    if (!dx) return fail(LORA_ERR_ARG, "dx is NULL");
+    BackwardArgs b{};
+    if ((st = make_backward_args(LORA_BF16, x, ldx, d_in, dy, lddy, d_out, h, grad_A_dev, grad_B_dev, n_adapters, flags,
+                                 dx, lddx, &b)))
+        return st;
+    // dy's codes are held in rows of whole blocks
+    if ((st = check_block_base(1, 0, d_in, W0, w_scales, scale_type, d_out))) return st;
+    if ((int64_t(h->num_tokens) + 1) * (int64_t(d_out) + LORA_SCALE_BLOCK) >= int64_t(1) << 32)
+        return fail(LORA_ERR_ARG, "the codes of dy span 4 GiB or more");
+    const bool grads = grad_A_dev || grad_B_dev;
+    if ((grads && (!aligned16(x) || ldx % 8)) || !aligned16(dy) || !aligned16(dx) || lddy % 8 || lddx % 8)
+        return fail(LORA_ERR_ALIGN, "fused entry needs 16-byte aligned x, dy and dx rows");
+    const size_t need = fused_block_backward_workspace_bytes(h->num_tokens, d_in, d_out, h->max_rank < 1 ? 1 : h->max_rank);
+    if (!ws || ws_bytes < need) return fail(LORA_ERR_WORKSPACE, "workspace %zu B < %zu B needed", ws_bytes, need);
+    if (!aligned16(ws)) return fail(LORA_ERR_ALIGN, "workspace is not 16-byte aligned");
+    return launch_fused_block_backward(static_cast<hipStream_t>(stream), b, W0, w_scales, scale_type,
+                                       PlanView{h, plan_dev}, ws);
 }
 
 // Checks and launch shared by the bf16 and E4M3 forms of the fused entry.

@@ -19,6 +19,20 @@
 // rows at one unit cover all banks.  Of the 128 a lane takes units g and g + 4 (g = lane /
 // 16) on both sides: within a block the order of k does not matter.  The rows of W are
 // placed so that a lane ends with 4 TN adjacent columns of a row.
+//
+// Precision.  The 8-bit instructions add the products of 8 adjacent k at a fixed point,
+// 2^-13 below the power of two of the largest, and the eights in fp32 (measured with exact
+// powers of two: 2^16 + 2^3 is kept, 2^16 + 2^2 gives 2^16).  On hidden states that is 4e-5 of a
+// result, 50 times below the rounding to bf16, so bf16 results and dx take them.  fp32 results
+// do not: their codes are widened to bf16 (exactly: 4 significant bits) and multiplied on
+// v_mfma_f32_16x16x32_bf16, whose sums are fp32's, at half the rate and a conversion for
+// each operand.
+//
+// The rows' gradient, dx = (sdy qdy) (sw qw), sums over d_out, along which W is not
+// contiguous: a stage is then 128 rows of 16 TN WN bytes of W, read with
+// ds_read_b64_tr_b8, which hands a lane one column of 8 rows; unit u of row r lies in
+// slot u ^ (r % 8), so that those 8 rows cover all banks.  It writes fp32 sums (few tiles are
+// split along d_out), which the gradient's last launch adds, with u A.
 #include "device.h"
 #include "internal.h"
 
@@ -28,6 +42,7 @@ namespace lora {
 namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
 constexpr int kG = 128;
 
 // Read-only memory at a wave-uniform address: scalar loads.
@@ -53,6 +68,7 @@ struct BlockArgs {
     const int32_t *tp_dev;
     const uint16_t *vh;
     int64_t ldh;
+    int per; // gradient: stages of a split; split i writes rows i T .. of y
 };
 
 template <int TN_, int TM_, int WN_, int WM_, int STAGES> struct Shape {
@@ -61,6 +77,7 @@ template <int TN_, int TM_, int WN_, int WM_, int STAGES> struct Shape {
     static constexpr int kWBytes = kBN * kG, kXBytes = kBM * kG;
     static constexpr int kSBytes = kBM <= 64 ? 256 : 4 * kBM; // the rows' scales
     static constexpr int kStageBytes = kWBytes + kXBytes + kSBytes;
+    static constexpr int kWavesPerSimd = kWaves * (160 * 1024 / (kStages * kStageBytes)) / 4;
     static constexpr int kWDma = kWBytes / 1024 / kWaves, kXDma = kXBytes / 1024 / kWaves;
     static constexpr int kDma = kWDma + kXDma + 1; // direct loads of a wave in a stage
     static_assert(kWDma * kWaves * 1024 == kWBytes && kXDma * kWaves * 1024 == kXBytes, "stage split");
@@ -151,11 +168,66 @@ __device__ __forceinline__ void store_row(const BlockArgs &a, int64_t row, int c
     }
 }
 
-template <class S, bool E8, bool F32OUT, bool LORA>
-__global__ __launch_bounds__(S::kThreads) __attribute__((amdgpu_waves_per_eu(S::kWaves / 4, S::kWaves / 4 * (S::kStages * S::kStageBytes <= 80 * 1024 ? 2 : 1))))
+// 32 codes as four operands of 8 bf16, exactly.
+struct Wide {
+    bf16x8 v[4];
+};
+__device__ __forceinline__ Wide widen(const i32x8 &c)
+{
+    typedef float floatx2 __attribute__((ext_vector_type(2)));
+    Wide w;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        u32x4 u;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const floatx2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(c[2 * h + q], false);
+            const floatx2 hi = __builtin_amdgcn_cvt_pk_f32_fp8(c[2 * h + q], true);
+            u[2 * q] = pack_bf16x2(lo[0], lo[1]);
+            u[2 * q + 1] = pack_bf16x2(hi[0], hi[1]);
+        }
+        w.v[h] = __builtin_bit_cast(bf16x8, u);
+    }
+    return w;
+}
+
+// One block with fp32 sums: acc += f (W x) on bf16 MFMA.
+template <int TN, int TM, class WF>
+__device__ __forceinline__ void exact_block(const i32x8 (&xf)[TM], const float (&f)[TM], floatx4 (&acc)[TN][TM], const WF &wfrag)
+{
+    Wide x[TM];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) x[i] = widen(xf[i]);
+#pragma unroll
+    for (int t = 0; t < TN; ++t) {
+        const Wide w = widen(wfrag(t));
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            floatx4 p{};
+#pragma unroll
+            for (int h = 0; h < 4; ++h) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[h], x[i].v[h], p, 0, 0, 0);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[t][i][q] = fmaf(p[q], f[i], acc[t][i][q]);
+        }
+    }
+}
+
+// What a kernel computes: the product into bf16 or fp32, the fused layer, or the rows'
+// gradient.
+enum Form { kBf16, kF32, kFused, kGradient };
+
+__device__ __forceinline__ float e8m0(int e)
+{
+    return e == 255 ? __uint_as_float(0x7FC00000u) : e ? __uint_as_float(uint32_t(e) << 23) : 0x1p-127f;
+}
+
+// k is the summed axis and n the columns of W [n][k], or of W [k][n] (kGradient).
+template <class S, bool E8, Form F>
+__global__ __launch_bounds__(S::kThreads) __attribute__((amdgpu_waves_per_eu(S::kWavesPerSimd, S::kWavesPerSimd)))
 void block_gemm_kernel(BlockArgs a)
 {
     constexpr int TN = S::TN, TM = S::TM;
+    constexpr bool WT = F == kGradient;
     __shared__ __attribute__((aligned(1024))) char lds[S::kStages * S::kStageBytes];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = uniform(tid >> 6);
@@ -163,29 +235,39 @@ void block_gemm_kernel(BlockArgs a)
     const int wn = wave / S::WM, wm = wave % S::WM;
     const uint32_t lds0 = uint32_t(uintptr_t((__attribute__((address_space(3))) char *)(lds)));
 
-    // row tiles fastest, a contiguous run of tiles for each XCD
-    const int nwg = a.tiles_m * a.tiles_n;
+    // row tiles fastest, then columns, then splits; a contiguous run of tiles for each XCD
+    const int nwg = gridDim.x;
     int tile = blockIdx.x;
     if ((nwg & 7) == 0) tile = (tile & 7) * (nwg >> 3) + (tile >> 3);
-    const int m0 = tile % a.tiles_m * S::kBM, n0 = tile / a.tiles_m * S::kBN;
-    const int nk = (a.k + kG - 1) / kG;
+    const int m0 = tile % a.tiles_m * S::kBM;
+    tile /= a.tiles_m;
+    const int n0 = tile % a.tiles_n * S::kBN, split = tile / a.tiles_n;
+    const int blocks = (a.k + kG - 1) / kG; // of the summed axis
+    const int k0 = WT ? split * a.per : 0, k1 = WT ? min(k0 + a.per, blocks) : blocks;
 
-    // Direct loads: load i of a part fills LDS rows 8 i .. 8 i + 7; this lane row 8 i +
-    // lane / 8, slot lane % 8, which holds unit slot ^ (row % 8).
+    // Direct loads: load i of a part fills 64 units of 16 bytes, this lane the one in row
+    // (64 i + lane) / units-of-a-row, slot (64 i + lane) % units-of-a-row, which holds unit
+    // slot ^ (row % 8).
+    constexpr int kWUnits = WT ? S::kBN / 16 : 8;
     const int unit = (lane & 7) ^ (lane >> 3);
     uint32_t woff[S::kWDma], xoff[S::kXDma];
+    int wrow[S::kWDma]; // WT: row of the stage
 #pragma unroll
     for (int j = 0; j < S::kWDma; ++j) {
-        const int rho = (wave * S::kWDma + j) * 8 + (lane >> 3), rp = rho % (16 * TN);
-        int c = n0 + rho / (16 * TN) * (16 * TN) + wave_col<TN>(rp & 15, rp >> 4);
-        c = c < a.n ? c : a.n - 1;
-        woff[j] = uint32_t(int64_t(c) * a.k + 16 * unit);
+        const int rho = ((wave * S::kWDma + j) * 64 + lane) / kWUnits, rp = rho % (16 * TN);
+        wrow[j] = rho;
+        if constexpr (WT) {
+            const int c = n0 + 16 * ((lane % kWUnits) ^ (rho & 7)); // n is a multiple of 16
+            woff[j] = uint32_t(int64_t(rho) * a.n + (c < a.n ? c : a.n - 16));
+        } else {
+            const int c = n0 + rho / (16 * TN) * (16 * TN) + wave_col<TN>(rp & 15, rp >> 4);
+            woff[j] = uint32_t(int64_t(c < a.n ? c : a.n - 1) * a.k + 16 * unit);
+        }
     }
 #pragma unroll
     for (int j = 0; j < S::kXDma; ++j) {
-        int p = m0 + (wave * S::kXDma + j) * 8 + (lane >> 3);
-        p = p < a.T ? p : a.T - 1;
-        xoff[j] = uint32_t(p * a.ldx + 16 * unit);
+        const int p = m0 + (wave * S::kXDma + j) * 8 + (lane >> 3);
+        xoff[j] = uint32_t((p < a.T ? p : a.T - 1) * a.ldx + 16 * unit);
     }
     // scales: a wave brings 64 rows' (E8M0: 256 rows', 4 a lane); others repeat them
     constexpr int kSRows = E8 ? 256 : 64, kSParts = (S::kBM + kSRows - 1) / kSRows;
@@ -195,13 +277,18 @@ void block_gemm_kernel(BlockArgs a)
     const char *sxp = static_cast<const char *>(a.sx) + int64_t(sp) * (E8 ? 1 : 4);
     const int64_t sstep = a.lds * (E8 ? 1 : 4);
 
+    // Stage kt to its slot of the ring (past the last one, the last one's data again, so
+    // that every stage has the same number of loads).
     auto issue = [&](int kt) {
-        const uint32_t base = lds0 + uint32_t(kt % S::kStages) * S::kStageBytes;
-        const uint8_t *wb = a.W + int64_t(kt) * kG, *xb = a.x + int64_t(kt) * kG;
-        const bool in = kt * kG + 16 * unit < a.k; // units past k are zeros (on both sides)
+        const uint32_t base = lds0 + uint32_t((kt - k0) % S::kStages) * S::kStageBytes;
+        kt = kt < k1 ? kt : k1 - 1;
+        const uint8_t *wb = a.W + int64_t(kt) * kG * (WT ? a.n : 1), *xb = a.x + int64_t(kt) * kG;
+        const bool in = kt * kG + 16 * unit < a.k; // what lies past k is zeros, on both sides
 #pragma unroll
-        for (int j = 0; j < S::kWDma; ++j)
-            dma16(in ? static_cast<const void *>(wb + woff[j]) : g_zeros, base + uint32_t(wave * S::kWDma + j) * 1024);
+        for (int j = 0; j < S::kWDma; ++j) {
+            const bool win = WT ? kt * kG + wrow[j] < a.k : in;
+            dma16(win ? static_cast<const void *>(wb + woff[j]) : g_zeros, base + uint32_t(wave * S::kWDma + j) * 1024);
+        }
 #pragma unroll
         for (int j = 0; j < S::kXDma; ++j)
             dma16(in ? static_cast<const void *>(xb + xoff[j]) : g_zeros, base + S::kWBytes + uint32_t(wave * S::kXDma + j) * 1024);
@@ -214,7 +301,7 @@ void block_gemm_kernel(BlockArgs a)
 #pragma unroll
         for (int i = 0; i < TM; ++i) acc[t][i] = floatx4{};
     const int pw0 = m0 + 16 * TM * wm, cw0 = n0 + 16 * TN * wn;
-    if constexpr (LORA) {
+    if constexpr (F == kFused) {
         const int Tp = a.tp_dev ? uniform(*a.tp_dev) : a.Tp;
         if (pw0 < Tp) correction<TN, TM>(a, Tp, pw0, cw0, lane, acc);
     }
@@ -228,54 +315,70 @@ void block_gemm_kernel(BlockArgs a)
     // of them, and would be for the direct loads behind it too
     __builtin_amdgcn_s_waitcnt(wait_vm(0));
 #pragma unroll
-    for (int s = 0; s < S::kStages - 1; ++s) issue(s < nk ? s : nk - 1);
+    for (int s = 0; s < S::kStages - 1; ++s) issue(k0 + s);
 
-    // the wave's block of W: columns past n repeat the last ones, which are not stored
+    // the wave's block of columns: those past n repeat the last ones and are not stored
     const int nb = (cw0 < a.n ? cw0 : a.n - 1) / kG;
+    const int64_t sw0 = WT ? nb : int64_t(nb) * blocks, sw1 = WT ? (a.n + kG - 1) / kG : 1;
     const int u0 = (g ^ (m & 7)) << 4, u1 = ((g + 4) ^ (m & 7)) << 4;
-    const uint32_t wrow = uint32_t((16 * TN * wn + m) * kG), xrow = uint32_t(S::kWBytes + (16 * TM * wm + m) * kG);
     auto frag = [&](const char *row) {
         const u32x4 lo = *reinterpret_cast<const u32x4 *>(row + u0), hi = *reinterpret_cast<const u32x4 *>(row + u1);
         return i32x8{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]), int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])};
     };
-    for (int kt = 0; kt < nk; ++kt) {
+    auto wfrag = [&](const char *st, int t) {
+        if constexpr (WT) { // 16 rows at 16 g and 16 at 64 + 16 g, 8 at a time
+            const char *p = st + (16 * g + (m >> 1)) * S::kBN + (((TN * wn + t) ^ (m >> 1)) << 4) + 8 * (m & 1);
+            typedef __attribute__((address_space(3))) i32x2 lds2;
+            i32x2 r[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                r[h] = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds2 *)(p + (8 * (h & 1) + 64 * (h >> 1)) * S::kBN));
+            return i32x8{r[0][0], r[0][1], r[1][0], r[1][1], r[2][0], r[2][1], r[3][0], r[3][1]};
+        } else {
+            return frag(st + (16 * (TN * wn + t) + m) * kG);
+        }
+    };
+    for (int kt = k0; kt < k1; ++kt) {
         // this wave's loads of stage kt have landed and its reads of stage kt - 1 are
         // done; past the barrier that holds for every wave
         __builtin_amdgcn_s_waitcnt(wait_vm_lds0(S::kDma * (S::kStages - 2)));
         __builtin_amdgcn_s_barrier();
-        const int nxt = kt + S::kStages - 1;
-        issue(nxt < nk ? nxt : nk - 1);
-        const char *st = lds + (kt % S::kStages) * S::kStageBytes;
+        issue(kt + S::kStages - 1);
+        const char *st = lds + ((kt - k0) % S::kStages) * S::kStageBytes;
         const char *ss = st + S::kWBytes + S::kXBytes;
         const int r0 = 16 * TM * wm + m;
+        const int64_t swi = sw0 + kt * sw1;
         i32x8 xf[TM];
 #pragma unroll
-        for (int i = 0; i < TM; ++i) xf[i] = frag(st + xrow + i * 16 * kG);
+        for (int i = 0; i < TM; ++i) xf[i] = frag(st + S::kWBytes + (r0 + 16 * i) * kG);
+        int wb = 0, xb[TM]; // E8M0 bytes
+        float f[TM];        // the product of both scales
         if constexpr (E8) {
             // one byte by a scalar load of its aligned word
-            const uintptr_t at = reinterpret_cast<uintptr_t>(a.sw) + size_t(int64_t(nb) * nk + kt);
-            const int ws = int(*(cptr<uint32_t>)(at & ~uintptr_t(3)) >> (8 * (at & 3)) & 255);
-            int xs[TM];
+            const uintptr_t at = reinterpret_cast<uintptr_t>(a.sw) + size_t(swi);
+            wb = int(*(cptr<uint32_t>)(at & ~uintptr_t(3)) >> (8 * (at & 3)) & 255);
 #pragma unroll
-            for (int i = 0; i < TM; ++i) xs[i] = *reinterpret_cast<const uint8_t *>(ss + r0 + 16 * i);
-#pragma unroll
-            for (int t = 0; t < TN; ++t) {
-                const i32x8 wf = frag(st + wrow + t * 16 * kG);
-#pragma unroll
-                for (int i = 0; i < TM; ++i)
-                    acc[t][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf[i], acc[t][i], 0, 0, 0, ws, 0, xs[i]);
+            for (int i = 0; i < TM; ++i) {
+                xb[i] = *reinterpret_cast<const uint8_t *>(ss + r0 + 16 * i);
+                if (F == kF32) f[i] = e8m0(wb) * e8m0(xb[i]);
             }
         } else {
-            const float ws = ((cptr<float>)(a.sw))[int64_t(nb) * nk + kt];
-            float f[TM];
+            const float ws = ((cptr<float>)(a.sw))[swi];
 #pragma unroll
             for (int i = 0; i < TM; ++i) f[i] = ws * *reinterpret_cast<const float *>(ss + 4 * (r0 + 16 * i));
+        }
+        if constexpr (F == kF32) {
+            exact_block<TN, TM>(xf, f, acc, [&](int t) { return wfrag(st, t); });
+            continue;
+        }
 #pragma unroll
-            for (int t = 0; t < TN; ++t) {
-                const i32x8 wf = frag(st + wrow + t * 16 * kG);
+        for (int t = 0; t < TN; ++t) {
+            const i32x8 wf = wfrag(st, t);
 #pragma unroll
-                for (int i = 0; i < TM; ++i) {
-                    // scale bytes of 127: 2^0
+            for (int i = 0; i < TM; ++i) {
+                if constexpr (E8) {
+                    acc[t][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf[i], acc[t][i], 0, 0, 0, wb, 0, xb[i]);
+                } else { // scale bytes of 127: 2^0
                     const floatx4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf[i], floatx4{}, 0, 0, 0, 127, 0, 127);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) acc[t][i][q] = fmaf(p[q], f[i], acc[t][i][q]);
@@ -289,12 +392,19 @@ void block_gemm_kernel(BlockArgs a)
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
         if (yrow[i] < 0) continue;
-        float v[4 * TN];
+        if constexpr (WT) { // lane: columns 16 t + 4 g .. + 3
+            float *o = static_cast<float *>(a.y) + (int64_t(split) * a.T + yrow[i]) * a.n + cw0 + 4 * g;
 #pragma unroll
-        for (int t = 0; t < TN; ++t)
+            for (int t = 0; t < TN; ++t)
+                if (cw0 + 16 * t < a.n) *reinterpret_cast<floatx4 *>(o + 16 * t) = acc[t][i];
+        } else {
+            float v[4 * TN];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[4 * t + q] = acc[t][i][q];
-        store_row<TN, F32OUT>(a, yrow[i], cw0 + 4 * TN * g, v);
+            for (int t = 0; t < TN; ++t)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[4 * t + q] = acc[t][i][q];
+            store_row<TN, F == kF32>(a, yrow[i], cw0 + 4 * TN * g, v);
+        }
     }
 }
 
@@ -302,36 +412,49 @@ typedef Shape<8, 4, 2, 4, 2> Large;  // 256 columns x 256 rows, 8 waves
 typedef Shape<4, 4, 2, 2, 2> Medium; // 128 x 128, 4 waves, two workgroups on a CU
 typedef Shape<2, 2, 4, 2, 3> Small;  // 128 x 64, 8 waves
 
-template <class S> int go(hipStream_t s, BlockArgs &a, bool e8, bool f32out, bool lora)
+template <class S, Form F> int go(hipStream_t s, BlockArgs &a, bool e8, int splits = 1)
 {
     a.tiles_m = (a.T + S::kBM - 1) / S::kBM;
     a.tiles_n = (a.n + S::kBN - 1) / S::kBN;
-    const int64_t tiles = int64_t(a.tiles_m) * a.tiles_n;
+    const int64_t tiles = int64_t(a.tiles_m) * a.tiles_n * splits;
     if (tiles > most_workgroups(S::kThreads)) return fail(LORA_ERR_ARG, "block product: too many tiles");
-    const dim3 grid{unsigned(tiles)};
-    const dim3 block(S::kThreads);
-    if (lora) {
-        if (e8) launch_kernel(block_gemm_kernel<S, true, false, true>, grid, block, 0, s, a);
-        else launch_kernel(block_gemm_kernel<S, false, false, true>, grid, block, 0, s, a);
-    } else if (f32out) {
-        if (e8) launch_kernel(block_gemm_kernel<S, true, true, false>, grid, block, 0, s, a);
-        else launch_kernel(block_gemm_kernel<S, false, true, false>, grid, block, 0, s, a);
-    } else {
-        if (e8) launch_kernel(block_gemm_kernel<S, true, false, false>, grid, block, 0, s, a);
-        else launch_kernel(block_gemm_kernel<S, false, false, false>, grid, block, 0, s, a);
-    }
+    const dim3 grid{unsigned(tiles)}, block(S::kThreads);
+    if (e8) launch_kernel(block_gemm_kernel<S, true, F>, grid, block, 0, s, a);
+    else launch_kernel(block_gemm_kernel<S, false, F>, grid, block, 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return fail(LORA_ERR_HIP, "block product launch: %s", hipGetErrorString(e));
     return LORA_OK;
 }
 
-int launch_product(hipStream_t s, BlockArgs &a, bool e8, bool f32out, bool lora)
+template <Form F> int launch_product(hipStream_t s, BlockArgs &a, bool e8)
 {
-    if (a.T <= 64) return go<Small>(s, a, e8, f32out, lora);
-    const int64_t large = int64_t(a.T + 255) / 256 * ((a.n + 255) / 256);
-    if (large >= 128) return go<Large>(s, a, e8, f32out, lora);
-    return go<Medium>(s, a, e8, f32out, lora);
+    if (a.T <= 64) return go<Small, F>(s, a, e8);
+    // fp32 results hold the rows' widened operands too: tiles of 128 x 128
+    if (F != kF32 && int64_t(a.T + 255) / 256 * ((a.n + 255) / 256) >= 128) return go<Large, F>(s, a, e8);
+    return go<Medium, F>(s, a, e8);
 }
+
+// Tile and splits of the rows' gradient: as many splits of the summed axis as fill the
+// chip once, with at least 4 blocks each.
+struct GradientPlan {
+    bool large;
+    int splits, per;
+    GradientPlan(int32_t T, int32_t d_in, int32_t d_out)
+    {
+        large = int64_t(T + 255) / 256 * ((d_in + 255) / 256) >= 128;
+        const int64_t tiles = large ? int64_t(T + 255) / 256 * ((d_in + 255) / 256) : int64_t(T + 63) / 64 * ((d_in + 127) / 128);
+        const int blocks = (d_out + kG - 1) / kG;
+        const int most = int(std::max<int64_t>(1, std::min<int64_t>({256 / tiles, blocks / 4, 16})));
+        per = (blocks + most - 1) / most;
+        splits = (blocks + per - 1) / per;
+    }
+    // floats of the sums of a batch of up to T rows: a batch of fewer has more splits
+    static size_t sums(int32_t T, int32_t d_in)
+    {
+        const size_t one = size_t(T) * size_t(d_in);
+        return std::max(one, std::min(16 * one, size_t(256) * 256 * 256));
+    }
+};
 
 // Workspace of the fused call: the shrink's slice partials, v's halves, x's codes (rows of
 // whole blocks) and scales (rows padded to 4).
@@ -348,6 +471,23 @@ struct FusedBlockWs {
         codes = vh + up256(size_t(T) * size_t(vh_pitch(max_rank)) * 2);
         scales = codes + up256(size_t(T) * size_t(ldq));
         end = scales + up256(size_t(groups) * size_t(lds) * 4);
+    }
+};
+
+// Workspace of the gradient call: the adapters' gradients', then dy's codes and scales and
+// the fp32 sums of dx.
+struct GradientWs {
+    size_t codes, scales, parts, end;
+    int64_t ldq, lds;
+    GradientWs(int32_t T, int32_t d_in, int32_t d_out, int32_t max_rank)
+    {
+        const int64_t groups = (int64_t(d_out) + kG - 1) / kG;
+        ldq = groups * kG;
+        lds = (int64_t(T) + 3) / 4 * 4;
+        codes = up256(sgmv_backward_workspace_bytes(T, d_in, d_out, max_rank));
+        scales = codes + up256(size_t(T) * size_t(ldq));
+        parts = scales + up256(size_t(groups) * size_t(lds) * 4);
+        end = parts + GradientPlan::sums(T, d_in) * 4;
     }
 };
 
@@ -370,7 +510,8 @@ int launch_linear_block(hipStream_t s, const LinearBlockCall &c)
     a.ldy = c.ldy;
     const int es = c.out_dtype == LORA_F32 ? 4 : 2;
     a.vec_y = aligned16(c.y) && c.ldy * es % 16 == 0;
-    return launch_product(s, a, c.scale_type == LORA_SCALE_E8M0, c.out_dtype == LORA_F32, false);
+    const bool e8 = c.scale_type == LORA_SCALE_E8M0;
+    return c.out_dtype == LORA_F32 ? launch_product<kF32>(s, a, e8) : launch_product<kBf16>(s, a, e8);
 }
 
 size_t fused_block_workspace_bytes(int32_t T, int32_t d_in, int32_t max_rank) { return FusedBlockWs(T, d_in, max_rank).end; }
@@ -420,7 +561,61 @@ int launch_fused_linear_block(hipStream_t s, const ShrinkArgs &sa, const void *W
     a.Tp = p.h->num_sorted;
     a.tp_dev = plan_sorted_dev(p);
     a.vh = vh;
-    return launch_product(s, a, scale_type == LORA_SCALE_E8M0, false, true);
+    return launch_product<kFused>(s, a, scale_type == LORA_SCALE_E8M0);
+}
+
+size_t fused_block_backward_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out, int32_t max_rank)
+{
+    return GradientWs(T, d_in, d_out, max_rank).end;
+}
+
+int launch_fused_block_backward(hipStream_t s, const BackwardArgs &b, const void *W0, const void *sw, int scale_type,
+                                const PlanView &p, void *ws)
+{
+    const lora_plan_header *h = p.h;
+    const int T = h->num_tokens;
+    const GradientWs w(T, b.d_in, b.d_out, h->max_rank < 1 ? 1 : h->max_rank);
+    const GradientPlan g(T, b.d_in, b.d_out);
+    char *base = static_cast<char *>(ws);
+    int st;
+    if (h->num_sorted > 0) { // the adapters' gradients, and u
+        BackwardArgs q = b;
+        q.dx = nullptr;
+        const uint16_t *ur;
+        int64_t ldu;
+        if ((st = launch_sgmv_backward(s, q, p, ws, &ur, &ldu))) return st;
+    }
+    QuantCall q{};
+    q.dtype = LORA_BF16;
+    q.x = b.dy;
+    q.ldx = b.lddy;
+    q.rows = T;
+    q.cols = b.d_out;
+    q.perm = reinterpret_cast<const int32_t *>(p.dev + h->perm_offset);
+    q.codes = base + w.codes;
+    q.ldq = w.ldq;
+    q.pad = true;
+    q.block_rows = 1;
+    q.scale_type = scale_type;
+    q.scales = base + w.scales;
+    q.lds = w.lds;
+    if ((st = launch_quantize(s, q))) return st;
+    BlockArgs a{};
+    a.x = static_cast<const uint8_t *>(q.codes);
+    a.ldx = w.ldq;
+    a.sx = q.scales;
+    a.lds = w.lds;
+    a.W = static_cast<const uint8_t *>(W0);
+    a.sw = sw;
+    a.k = b.d_out;
+    a.n = b.d_in;
+    a.T = T;
+    a.y = base + w.parts;
+    a.per = g.per;
+    const bool e8 = scale_type == LORA_SCALE_E8M0;
+    st = g.large ? go<Large, kGradient>(s, a, e8, g.splits) : go<Small, kGradient>(s, a, e8, g.splits);
+    if (st) return st;
+    return launch_dx_join(s, b, p, ws, reinterpret_cast<const float *>(base + w.parts), g.splits);
 }
 
 } // namespace lora

@@ -214,6 +214,9 @@ int launch_linear_block(hipStream_t s, const LinearBlockCall &c);
 size_t fused_block_workspace_bytes(int32_t T, int32_t d_in, int32_t max_rank);
 int launch_fused_linear_block(hipStream_t s, const ShrinkArgs &sa, const void *W0, const void *sw, int scale_type,
                               const ExpandArgs &ea, const PlanView &p, void *ws);
+size_t fused_block_backward_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out, int32_t max_rank);
+int launch_fused_block_backward(hipStream_t s, const BackwardArgs &b, const void *W0, const void *sw, int scale_type,
+                                const PlanView &p, void *ws);
 // The shrink of the plan's rows into ws (combined_workspace_bytes), then scale_s v in
 // two bf16 halves, for 16 ranks each 16 hi and 16 lo, ldh apart from row to row (plan
 // order; zeros past the adapted rows).  The value is divided by wdiv unless that is 0.

@@ -217,3 +217,73 @@ def test_fused_without_adapters():
     plan = B.Plan(40).build(prob.ids, pool).upload()
     ref, bound = fused_reference(prob, W, ws, "f32")
     check(run_fused(prob, W, ws, plan), ref, bound, "no adapter")
+
+
+# ---- gradients
+def grad_reference(prob, W, ws, kind, x, dy):
+    """dx, dA, dB in 64 bits, and bounds.  dx: the product's bound with dy's codes, u's two halves (2^-16) and fp32 sums, one
+    rounding.  dA, dB: fp32 sums of products with u and v, themselves fp32 sums (2^-23 for each addition, and 2^-22
+    for u and v in three bf16 parts)."""
+    T, d_in, d_out = prob.T, prob.d_in, prob.d_out
+    q, s, _ = R.quantize(dy, 1, kind)
+    w = R.dequantize(W, ws, 128)
+    d = R.dequantize(q, s, 1)
+    dx = d @ w
+    tops = np.repeat(R._tops(q, s, 1), 8, 1)[:, : d_out]  # eights along d_out on both sides
+    wt = np.abs(R.decode(W))
+    with np.errstate(divide="ignore"):
+        e = np.where(wt >= 2.0**-6, np.exp2(np.floor(np.log2(np.maximum(wt, 2.0**-6)))), 2.0**-6) * R.spread(R.scale_values(ws), 128, W.shape)
+    e = np.pad(e, ((0, -d_out % 8), (0, 0))).reshape(-1, 8, d_in).max(1)
+    bound = (d_out + -(-d_out // 128) + 20) * 2.0**-23 * (np.abs(d) @ np.abs(w)) + 8 * 2.0**-13 * tops[:, ::8] @ e
+    dA, dB, bA, bB = {}, {}, {}, {}
+    for i in range(prob.n_adapters):
+        rows = np.nonzero(prob.ids == i)[0]
+        if not rows.size:
+            continue
+        A = bf16_bits_to_f32(prob.A(i)).astype(np.float64).reshape(-1, d_in)
+        Bm = bf16_bits_to_f32(prob.B(i)).astype(np.float64).reshape(d_out, -1)
+        c = float(np.float32(prob.alphas[i]) / np.float32(A.shape[0]))
+        u, um = c * dy[rows] @ Bm, c * np.abs(dy[rows]) @ np.abs(Bm)
+        v, vm = c * x[rows] @ A.T, c * np.abs(x[rows]) @ np.abs(A).T
+        dx[rows] += u @ A
+        bound[rows] += (um * (d_out + 4) * 2.0**-23 + np.abs(u) * 2.0**-16 + um * 256 * 2.0**-23) @ np.abs(A)
+        dA[i], dB[i] = u.T @ x[rows], dy[rows].T @ v
+        n = rows.size
+        bA[i] = (um * (d_out + n + 16) * 2.0**-23).T @ np.abs(x[rows])
+        bB[i] = np.abs(dy[rows]).T @ (vm * (d_in + n + 16) * 2.0**-23)
+    return dx, bound + 2.0**-8 * 1.01 * np.abs(dx) + 2.0**-133, dA, bA, dB, bB
+
+
+GRADS = [(1, 128, 128, [16]), (40, 256, 264, [8, 8, 3]), (64, 1024, 512, [16] * 8), (65, 528, 136, [3, 17]), (130, 400, 1000, [8, 64, 1]),
+         (300, 512, 2049, [16, 32, 5, 100]), (64, 256, 8192, [16] * 3), (2100, 4096, 384, [8, 16, 256]), (4200, 2064, 250, [16] * 4)]
+
+
+@pytest.mark.parametrize("kind", ["f32", "e8m0"])
+@pytest.mark.parametrize("T,d_in,d_out,ranks", GRADS)
+def test_gradients(kind, T, d_in, d_out, ranks):
+    say(f"gradients {kind} {T} {d_in}->{d_out} {ranks[:4]}")
+    rng = np.random.default_rng(T + d_in)
+    prob = fused_problem(T, d_in, d_out, ranks, T, layout="random" if T < 500 else "runs")
+    W, ws = base(rng, d_out, d_in, kind)
+    pool = B.DevicePool.from_problem(prob)
+    plan = B.Plan(T).build(prob.ids, pool).upload()
+    dyh, dy = bf16(hidden(rng, T, d_out) * 1e-3)
+    x = bf16_bits_to_f32(prob.x).reshape(prob.x.shape).astype(np.float64)
+    dx, bound, dA, bA, dB, bB = grad_reference(prob, W, ws, kind, x, dy)
+    lddy = (d_out + 7) // 8 * 8
+    dyd = torch.zeros(T, lddy, dtype=torch.bfloat16, device="cuda")[:, :d_out]
+    dyd.copy_(dyh)
+    out = torch.full((T, d_in + 8), 5.0, dtype=torch.bfloat16, device="cuda")
+    grads = B.GradPool.like(pool)
+    work = B.workspace(B.LORA_OP_FUSED_BLOCK_BACKWARD, T, d_in, d_out, prob.max_rank)
+    call = lambda g, acc=False: B.fused_linear_e4m3_block_backward(  # noqa: E731
+        B.to_device(prob.x, "bf16"), torch.from_numpy(W).cuda(), torch.from_numpy(ws).cuda(), dyd, plan, g, out[:, :d_in], work, accumulate=acc)
+    call(grads)
+    check(out[:, :d_in].double().cpu().numpy(), dx, bound, "dx")
+    assert (out[:, d_in:] == 5.0).all()
+    for i in dA:
+        check(grads.A[i].double().cpu().numpy(), dA[i], bA[i] + 1e-30, f"dA {i}")
+        check(grads.B[i].double().cpu().numpy(), dB[i], bB[i] + 1e-30, f"dB {i}")
+    first = out.clone()
+    call(None)  # dx alone
+    assert torch.equal(out, first)
