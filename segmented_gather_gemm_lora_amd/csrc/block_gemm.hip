@@ -95,51 +95,88 @@ __device__ __forceinline__ void dma4(const void *g, uint32_t lds_byte)
 // 4 TN g + 4 t + q.
 template <int TN> __device__ __forceinline__ int wave_col(int m, int t) { return (m >> 2) * (4 * TN) + 4 * t + (m & 3); }
 
-// The correction of the segments that meet rows pw0 .. pw0 + 16 TM, on bf16 MFMA: 16
-// ranks a step, B_s against the hi and lo halves of scale_s v.
-template <int TN, int TM>
-__device__ __forceinline__ void correction(const BlockArgs &a, int Tp, int pw0, int cw0, int lane, floatx4 (&acc)[TN][TM])
+// Operands of one correction step: 16 ranks (from j0) of segment s for a wave's rows and
+// columns.  A = B_s rows (lane groups 0, 2: ranks j0 .. j0 + 7, groups 1, 3: j0 + 8 .. j0 +
+// 15), B = scale_s v in two halves (groups 0, 1: hi, 2, 3: lo), zero on rows of others.
+template <int TN, int TM> struct Step {
+    u32x4 b[TN], v[TM];
+};
+struct Segment {
+    gptr<uint16_t> B;
+    int r, p0, p1;
+};
+__device__ __forceinline__ Segment segment(const BlockArgs &a, int s)
+{
+    const lora_seg_desc *d = a.seg + s;
+    return Segment{as_global<uint16_t>(reinterpret_cast<const void *>(d->B)), d->rank, d->start, d->start + d->len};
+}
+
+// RV: every rank is a multiple of 8, so 8 ranks of a row are one aligned load.
+template <int TN, int TM, bool RV>
+__device__ __forceinline__ void load_step(const BlockArgs &a, const Segment &sg, int j0, int pw0, int cw0, int lane, Step<TN, TM> &f)
 {
     const int m = lane & 15, g = lane >> 4;
-    const int plast = (pw0 + 16 * TM < Tp ? pw0 + 16 * TM : Tp) - 1;
-    const int s0 = uniform(a.segidx[pw0]), s1 = uniform(a.segidx[plast]);
-    for (int s = s0; s <= s1; ++s) {
-        const lora_seg_desc *d = a.seg + s;
-        const gptr<uint16_t> B = as_global<uint16_t>(reinterpret_cast<const void *>(d->B));
-        const int r = d->rank, p0 = d->start, p1 = d->start + d->len;
-        for (int j0 = 0; j0 < r; j0 += 16) {
-            const int jj = j0 + 8 * (g & 1);
-            bf16x8 bf[TN], vf[TM];
+    const int r = sg.r, jj = j0 + 8 * (g & 1);
 #pragma unroll
-            for (int t = 0; t < TN; ++t) {
-                const int c = cw0 + wave_col<TN>(m, t);
-                const gptr<uint16_t> row = B + int64_t(c < a.n ? c : a.n - 1) * r;
-                if ((r & 7) == 0) {
-                    u32x4 u = *(gptr<u32x4>)(row + (jj < r ? jj : 0));
-                    if (jj >= r) u = u32x4{};
-                    bf[t] = __builtin_bit_cast(bf16x8, u);
-                } else {
+    for (int t = 0; t < TN; ++t) {
+        const int c = cw0 + wave_col<TN>(m, t);
+        const gptr<uint16_t> row = sg.B + int64_t(c < a.n ? c : a.n - 1) * r;
+        if constexpr (RV) {
+            f.b[t] = *(gptr<u32x4>)(row + (jj < r ? jj : 0));
+            if (jj >= r) f.b[t] = u32x4{};
+        } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int j = jj + e;
-                        const uint16_t h = row[j < r ? j : r - 1];
-                        bf[t][e] = __builtin_bit_cast(__bf16, j < r ? h : uint16_t(0));
-                    }
-                }
+            for (int e = 0; e < 4; ++e) {
+                const int j = jj + 2 * e;
+                const uint32_t lo = row[j < r ? j : 0], hi = row[j + 1 < r ? j + 1 : 0];
+                f.b[t][e] = (j < r ? lo : 0) | (j + 1 < r ? hi << 16 : 0);
             }
-#pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                const int p = pw0 + 16 * i + m;
-                const bool in = p >= p0 && p < p1;
-                u32x4 u = *(gptr<u32x4>)(as_global<uint16_t>(a.vh) + int64_t(in ? p : p0) * a.ldh + 2 * j0 + 8 * g);
-                if (!in) u = u32x4{};
-                vf[i] = __builtin_bit_cast(bf16x8, u);
-            }
-#pragma unroll
-            for (int t = 0; t < TN; ++t)
-#pragma unroll
-                for (int i = 0; i < TM; ++i) acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[t], vf[i], acc[t][i], 0, 0, 0);
         }
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        const int p = pw0 + 16 * i + m;
+        const bool in = p >= sg.p0 && p < sg.p1;
+        f.v[i] = *(gptr<u32x4>)(as_global<uint16_t>(a.vh) + int64_t(in ? p : sg.p0) * a.ldh + 2 * j0 + 8 * g);
+        if (!in) f.v[i] = u32x4{};
+    }
+}
+
+// The correction of the segments that meet rows pw0 .. pw0 + 16 TM, on bf16 MFMA, 16
+// ranks a step; with RV the operands of a step are loaded before the products of the one before.
+template <int TN, int TM, bool RV>
+__device__ __forceinline__ void correction(const BlockArgs &a, int Tp, int pw0, int cw0, int lane, floatx4 (&acc)[TN][TM])
+{
+    auto add = [&](const Step<TN, TM> &f) {
+#pragma unroll
+        for (int t = 0; t < TN; ++t)
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+                acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f.b[t]), __builtin_bit_cast(bf16x8, f.v[i]),
+                                                                    acc[t][i], 0, 0, 0);
+    };
+    const int plast = (pw0 + 16 * TM < Tp ? pw0 + 16 * TM : Tp) - 1;
+    const int s1 = uniform(a.segidx[plast]);
+    int s = uniform(a.segidx[pw0]), j0 = 0;
+    Segment sg = segment(a, s);
+    Step<TN, TM> f[2];
+    load_step<TN, TM, RV>(a, sg, j0, pw0, cw0, lane, f[0]);
+    // two steps a round, so that no operand is copied
+    for (;;) {
+        bool more = true;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (!more) break;
+            j0 += 16;
+            if (j0 >= sg.r) {
+                j0 = 0;
+                more = ++s <= s1;
+                if (more) sg = segment(a, s);
+            }
+            if (more) load_step<TN, TM, RV>(a, sg, j0, pw0, cw0, lane, f[h ^ 1]);
+            add(f[h]);
+        }
+        if (!more) break;
     }
 }
 
@@ -214,118 +251,134 @@ __device__ __forceinline__ void exact_block(const i32x8 (&xf)[TM], const float (
 
 // What a kernel computes: the product into bf16 or fp32, the fused layer, or the rows'
 // gradient.
-enum Form { kBf16, kF32, kFused, kGradient };
+enum Form { kBf16, kF32, kFused, kFusedAnyRank, kGradient };
+constexpr bool is_fused(Form f) { return f == kFused || f == kFusedAnyRank; }
 
 __device__ __forceinline__ float e8m0(int e)
 {
     return e == 255 ? __uint_as_float(0x7FC00000u) : e ? __uint_as_float(uint32_t(e) << 23) : 0x1p-127f;
 }
 
-// k is the summed axis and n the columns of W [n][k], or of W [k][n] (kGradient).
-template <class S, bool E8, Form F>
-__global__ __launch_bounds__(S::kThreads) __attribute__((amdgpu_waves_per_eu(S::kWavesPerSimd, S::kWavesPerSimd)))
-void block_gemm_kernel(BlockArgs a)
+// dma16 from a wave-uniform base plus a 32-bit per-lane byte offset.
+__device__ __forceinline__ void dma16s(const void *base, uint32_t off, uint32_t lds_byte)
 {
-    constexpr int TN = S::TN, TM = S::TM;
-    constexpr bool WT = F == kGradient;
-    __shared__ __attribute__((aligned(1024))) char lds[S::kStages * S::kStageBytes];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = uniform(tid >> 6);
-    const int m = lane & 15, g = lane >> 4;
-    const int wn = wave / S::WM, wm = wave % S::WM;
-    const uint32_t lds0 = uint32_t(uintptr_t((__attribute__((address_space(3))) char *)(lds)));
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds_byte) : "memory");
+}
 
-    // row tiles fastest, then columns, then splits; a contiguous run of tiles for each XCD
-    const int nwg = gridDim.x;
-    int tile = blockIdx.x;
-    if ((nwg & 7) == 0) tile = (tile & 7) * (nwg >> 3) + (tile >> 3);
-    const int m0 = tile % a.tiles_m * S::kBM;
-    tile /= a.tiles_m;
-    const int n0 = tile % a.tiles_n * S::kBN, split = tile / a.tiles_n;
-    const int blocks = (a.k + kG - 1) / kG; // of the summed axis
-    const int k0 = WT ? split * a.per : 0, k1 = WT ? min(k0 + a.per, blocks) : blocks;
-
-    // Direct loads: load i of a part fills 64 units of 16 bytes, this lane the one in row
+// A workgroup's tile: its place, the loads of its stages and the fragments in them.
+// k is the summed axis and n the columns of W [n][k], or of W [k][n] (kGradient).
+template <class S, bool E8, Form F> struct Tile {
+    static constexpr int TN = S::TN, TM = S::TM;
+    static constexpr bool WT = F == kGradient;
+    // Direct loads: load i of a part fills 64 units of 16 bytes, a lane the one in row
     // (64 i + lane) / units-of-a-row, slot (64 i + lane) % units-of-a-row, which holds unit
     // slot ^ (row % 8).
-    constexpr int kWUnits = WT ? S::kBN / 16 : 8;
-    const int unit = (lane & 7) ^ (lane >> 3);
+    static constexpr int kWUnits = WT ? S::kBN / 16 : 8;
+    const BlockArgs &a;
+    char *lds;
+    uint32_t lds0;
+    int lane, wave, m, g, wn, wm;
+    int m0, n0, split, blocks, k0, k1, pw0, cw0;
+    int unit, spart;
     uint32_t woff[S::kWDma], xoff[S::kXDma];
-    int wrow[S::kWDma]; // WT: row of the stage
-#pragma unroll
-    for (int j = 0; j < S::kWDma; ++j) {
-        const int rho = ((wave * S::kWDma + j) * 64 + lane) / kWUnits, rp = rho % (16 * TN);
-        wrow[j] = rho;
-        if constexpr (WT) {
-            const int c = n0 + 16 * ((lane % kWUnits) ^ (rho & 7)); // n is a multiple of 16
-            woff[j] = uint32_t(int64_t(rho) * a.n + (c < a.n ? c : a.n - 16));
-        } else {
-            const int c = n0 + rho / (16 * TN) * (16 * TN) + wave_col<TN>(rp & 15, rp >> 4);
-            woff[j] = uint32_t(int64_t(c < a.n ? c : a.n - 1) * a.k + 16 * unit);
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < S::kXDma; ++j) {
-        const int p = m0 + (wave * S::kXDma + j) * 8 + (lane >> 3);
-        xoff[j] = uint32_t((p < a.T ? p : a.T - 1) * a.ldx + 16 * unit);
-    }
-    // scales: a wave brings 64 rows' (E8M0: 256 rows', 4 a lane); others repeat them
-    constexpr int kSRows = E8 ? 256 : 64, kSParts = (S::kBM + kSRows - 1) / kSRows;
-    const int spart = wave % kSParts;
-    int sp = m0 + spart * kSRows + (E8 ? 4 : 1) * lane;
-    sp = sp < a.T ? sp : (E8 ? (a.T - 1) & ~3 : a.T - 1);
-    const char *sxp = static_cast<const char *>(a.sx) + int64_t(sp) * (E8 ? 1 : 4);
-    const int64_t sstep = a.lds * (E8 ? 1 : 4);
+    const char *sxp;
+    int64_t sstep, sw0, sw1;
+    int u0, u1;
 
-    // Stage kt to its slot of the ring (past the last one, the last one's data again, so
-    // that every stage has the same number of loads).
-    auto issue = [&](int kt) {
+    __device__ __forceinline__ Tile(const BlockArgs &args, char *l) : a(args), lds(l)
+    {
+        const int tid = threadIdx.x;
+        lane = tid & 63;
+        wave = uniform(tid >> 6);
+        m = lane & 15;
+        g = lane >> 4;
+        wn = wave / S::WM;
+        wm = wave % S::WM;
+        lds0 = uint32_t(uintptr_t((__attribute__((address_space(3))) char *)(lds)));
+        // row tiles fastest, then columns, then splits; a contiguous run of tiles for each XCD
+        const int nwg = gridDim.x;
+        int tile = blockIdx.x;
+        if ((nwg & 7) == 0) tile = (tile & 7) * (nwg >> 3) + (tile >> 3);
+        m0 = tile % a.tiles_m * S::kBM;
+        tile /= a.tiles_m;
+        n0 = tile % a.tiles_n * S::kBN;
+        split = tile / a.tiles_n;
+        blocks = (a.k + kG - 1) / kG; // of the summed axis
+        k0 = WT ? split * a.per : 0;
+        k1 = WT ? min(k0 + a.per, blocks) : blocks;
+        pw0 = m0 + 16 * TM * wm;
+        cw0 = n0 + 16 * TN * wn;
+        // the wave's block of columns: those past n repeat the last ones and are not stored
+        const int nb = (cw0 < a.n ? cw0 : a.n - 1) / kG;
+        sw0 = WT ? nb : int64_t(nb) * blocks;
+        sw1 = WT ? (a.n + kG - 1) / kG : 1;
+        u0 = (g ^ (m & 7)) << 4;
+        u1 = ((g + 4) ^ (m & 7)) << 4;
+        unit = (lane & 7) ^ (lane >> 3);
+#pragma unroll
+        for (int j = 0; j < S::kWDma; ++j) {
+            const int rho = wrow(j), rp = rho % (16 * TN);
+            if constexpr (WT) {
+                const int c = n0 + 16 * ((lane % kWUnits) ^ (rho & 7)); // n is a multiple of 16
+                woff[j] = uint32_t(int64_t(rho) * a.n + (c < a.n ? c : a.n - 16));
+            } else {
+                const int c = n0 + rho / (16 * TN) * (16 * TN) + wave_col<TN>(rp & 15, rp >> 4);
+                woff[j] = uint32_t(int64_t(c < a.n ? c : a.n - 1) * a.k + 16 * unit);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < S::kXDma; ++j) {
+            const int p = m0 + (wave * S::kXDma + j) * 8 + (lane >> 3);
+            xoff[j] = uint32_t((p < a.T ? p : a.T - 1) * a.ldx + 16 * unit);
+        }
+        // scales: a wave brings 64 rows' (E8M0: 256 rows', 4 a lane); others repeat them
+        constexpr int kSRows = E8 ? 256 : 64, kSParts = (S::kBM + kSRows - 1) / kSRows;
+        spart = wave % kSParts;
+        int sp = m0 + spart * kSRows + (E8 ? 4 : 1) * lane;
+        sp = sp < a.T ? sp : (E8 ? (a.T - 1) & ~3 : a.T - 1);
+        sxp = static_cast<const char *>(a.sx) + int64_t(sp) * (E8 ? 1 : 4);
+        sstep = a.lds * (E8 ? 1 : 4);
+    }
+    __device__ __forceinline__ int wrow(int j) const { return ((wave * S::kWDma + j) * 64 + lane) / kWUnits; }
+
+    // Loads part, part + parts, ... of stage kt, to its slot of the ring (past the last stage, the
+    // last one's data again, so that every stage has the same number of loads).  No branches: they
+    // would keep the matrix instructions around them apart.  Of what lies past k, x's codes
+    // are zeros (the fused forms pad them, else the lane loads zeros), and W's are others of the same
+    // column, so that a NaN code reaches only results that are NaN in any case.
+    __device__ __forceinline__ void issue(int kt, int part = 0, int parts = 1) const
+    {
         const uint32_t base = lds0 + uint32_t((kt - k0) % S::kStages) * S::kStageBytes;
         kt = kt < k1 ? kt : k1 - 1;
         const uint8_t *wb = a.W + int64_t(kt) * kG * (WT ? a.n : 1), *xb = a.x + int64_t(kt) * kG;
-        const bool in = kt * kG + 16 * unit < a.k; // what lies past k is zeros, on both sides
+        const uint32_t wl = base + uint32_t(wave * S::kWDma) * 1024, xl = base + S::kWBytes + uint32_t(wave * S::kXDma) * 1024;
+        const bool in = kt * kG + 16 * unit < a.k;
 #pragma unroll
         for (int j = 0; j < S::kWDma; ++j) {
-            const bool win = WT ? kt * kG + wrow[j] < a.k : in;
-            dma16(win ? static_cast<const void *>(wb + woff[j]) : g_zeros, base + uint32_t(wave * S::kWDma + j) * 1024);
+            if (j % parts != part) continue;
+            uint32_t off = woff[j];
+            if constexpr (WT) off -= uint32_t(max(kt * kG + wrow(j) - (a.k - 1), 0)) * uint32_t(a.n);
+            else off -= in ? 0u : uint32_t(16 * unit);
+            dma16s(wb, off, wl + 1024 * j);
         }
 #pragma unroll
-        for (int j = 0; j < S::kXDma; ++j)
-            dma16(in ? static_cast<const void *>(xb + xoff[j]) : g_zeros, base + S::kWBytes + uint32_t(wave * S::kXDma + j) * 1024);
-        dma4(sxp + kt * sstep, base + S::kWBytes + S::kXBytes + uint32_t(spart) * 256);
-    };
-
-    floatx4 acc[TN][TM];
-#pragma unroll
-    for (int t = 0; t < TN; ++t)
-#pragma unroll
-        for (int i = 0; i < TM; ++i) acc[t][i] = floatx4{};
-    const int pw0 = m0 + 16 * TM * wm, cw0 = n0 + 16 * TN * wn;
-    if constexpr (F == kFused) {
-        const int Tp = a.tp_dev ? uniform(*a.tp_dev) : a.Tp;
-        if (pw0 < Tp) correction<TN, TM>(a, Tp, pw0, cw0, lane, acc);
+        for (int j = 0; j < S::kXDma; ++j) {
+            if ((S::kWDma + j) % parts != part) continue;
+            if constexpr (is_fused(F) || F == kGradient) dma16s(xb, xoff[j], xl + 1024 * j);
+            else dma16(in ? static_cast<const void *>(xb + xoff[j]) : g_zeros, xl + 1024 * j);
+        }
+        if ((S::kWDma + S::kXDma) % parts == part)
+            dma4(sxp + kt * sstep, base + S::kWBytes + S::kXBytes + uint32_t(spart) * 256);
     }
-    int64_t yrow[TM];
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        const int p = pw0 + 16 * i + m;
-        yrow[i] = p < a.T ? (a.perm ? as_global<int32_t>(a.perm)[p] : p) : -1;
-    }
-    // every load so far is complete: none of the compiler's waits in the loop is for one
-    // of them, and would be for the direct loads behind it too
-    __builtin_amdgcn_s_waitcnt(wait_vm(0));
-#pragma unroll
-    for (int s = 0; s < S::kStages - 1; ++s) issue(k0 + s);
 
-    // the wave's block of columns: those past n repeat the last ones and are not stored
-    const int nb = (cw0 < a.n ? cw0 : a.n - 1) / kG;
-    const int64_t sw0 = WT ? nb : int64_t(nb) * blocks, sw1 = WT ? (a.n + kG - 1) / kG : 1;
-    const int u0 = (g ^ (m & 7)) << 4, u1 = ((g + 4) ^ (m & 7)) << 4;
-    auto frag = [&](const char *row) {
+    __device__ __forceinline__ const char *stage(int kt) const { return lds + ((kt - k0) % S::kStages) * S::kStageBytes; }
+    __device__ __forceinline__ i32x8 frag(const char *row) const
+    {
         const u32x4 lo = *reinterpret_cast<const u32x4 *>(row + u0), hi = *reinterpret_cast<const u32x4 *>(row + u1);
         return i32x8{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]), int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])};
-    };
-    auto wfrag = [&](const char *st, int t) {
+    }
+    __device__ __forceinline__ i32x8 wfrag(const char *st, int t) const
+    {
         if constexpr (WT) { // 16 rows at 16 g and 16 at 64 + 16 g, 8 at a time
             const char *p = st + (16 * g + (m >> 1)) * S::kBN + (((TN * wn + t) ^ (m >> 1)) << 4) + 8 * (m & 1);
             typedef __attribute__((address_space(3))) i32x2 lds2;
@@ -337,75 +390,154 @@ void block_gemm_kernel(BlockArgs a)
         } else {
             return frag(st + (16 * (TN * wn + t) + m) * kG);
         }
+    }
+    __device__ __forceinline__ i32x8 xfrag(const char *st, int i) const { return frag(st + S::kWBytes + (16 * (TM * wm + i) + m) * kG); }
+
+    // The scales of block kt: E8M0 bytes, or the products of both sides' scales.
+    struct Scales {
+        int wb, xb[TM];
+        float f[TM];
     };
-    for (int kt = k0; kt < k1; ++kt) {
+    // W's scale of block kt: fp32 bits, or the aligned word that holds its byte.
+    __device__ __forceinline__ uint32_t wscale(int kt) const
+    {
+        const int64_t at = sw0 + (kt < k1 ? kt : k1 - 1) * sw1;
+        if constexpr (!E8) return ((cptr<uint32_t>)(a.sw))[at];
+        return *(cptr<uint32_t>)((reinterpret_cast<uintptr_t>(a.sw) + size_t(at)) & ~uintptr_t(3));
+    }
+    __device__ __forceinline__ Scales scales(int kt, uint32_t word) const
+    {
+        Scales r;
+        const char *ss = stage(kt) + S::kWBytes + S::kXBytes;
+        const int r0 = 16 * TM * wm + m;
+        if constexpr (E8) {
+            r.wb = int(word >> (8 * uint32_t((reinterpret_cast<uintptr_t>(a.sw) + size_t(sw0 + kt * sw1)) & 3)) & 255);
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                r.xb[i] = *reinterpret_cast<const uint8_t *>(ss + r0 + 16 * i);
+                if (F == kF32) r.f[i] = e8m0(r.wb) * e8m0(r.xb[i]);
+            }
+        } else {
+            const float ws = __uint_as_float(word);
+#pragma unroll
+            for (int i = 0; i < TM; ++i) r.f[i] = ws * *reinterpret_cast<const float *>(ss + 4 * (r0 + 16 * i));
+        }
+        return r;
+    }
+
+    // acc += the block's product of one column tile with every row tile
+    __device__ __forceinline__ void multiply(const i32x8 &wf, const i32x8 (&xf)[TM], const Scales &sc, floatx4 (&acc)[TM]) const
+    {
+        if constexpr (E8) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+                acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf[i], acc[i], 0, 0, 0, sc.wb, 0, sc.xb[i]);
+        } else {
+            floatx4 p[TM];
+#pragma unroll
+            for (int i = 0; i < TM; ++i) // scale bytes of 127: 2^0
+                p[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf[i], floatx4{}, 0, 0, 0, 127, 0, 127);
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[i][q] = fmaf(p[i][q], sc.f[i], acc[i][q]);
+        }
+    }
+
+    __device__ __forceinline__ void correct(floatx4 (&acc)[TN][TM]) const
+    {
+        if constexpr (is_fused(F)) {
+            const int Tp = a.tp_dev ? uniform(*a.tp_dev) : a.Tp;
+            if (pw0 < Tp) {
+                correction<TN, TM, F == kFused>(a, Tp, pw0, cw0, lane, acc);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void store(const floatx4 (&acc)[TN][TM]) const
+    {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int p = pw0 + 16 * i + m;
+            if (p >= a.T) continue;
+            if constexpr (WT) { // lane: columns 16 t + 4 g .. + 3
+                float *o = static_cast<float *>(a.y) + (int64_t(split) * a.T + p) * a.n + cw0 + 4 * g;
+#pragma unroll
+                for (int t = 0; t < TN; ++t)
+                    if (cw0 + 16 * t < a.n) *reinterpret_cast<floatx4 *>(o + 16 * t) = acc[t][i];
+            } else {
+                const int row = a.perm ? as_global<int32_t>(a.perm)[p] : p;
+                if (row < 0) continue;
+                float v[4 * TN];
+#pragma unroll
+                for (int t = 0; t < TN; ++t)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[4 * t + q] = acc[t][i][q];
+                store_row<TN, F == kF32>(a, row, cw0 + 4 * TN * g, v);
+            }
+        }
+    }
+};
+
+template <class S, bool E8, Form F>
+__global__ __launch_bounds__(S::kThreads) __attribute__((amdgpu_waves_per_eu(S::kWavesPerSimd, S::kWavesPerSimd)))
+void block_gemm_kernel(BlockArgs a)
+{
+    constexpr int TN = S::TN, TM = S::TM;
+    __shared__ __attribute__((aligned(1024))) char lds[S::kStages * S::kStageBytes];
+    Tile<S, E8, F> T(a, lds);
+    floatx4 acc[TN][TM];
+#pragma unroll
+    for (int t = 0; t < TN; ++t)
+#pragma unroll
+        for (int i = 0; i < TM; ++i) acc[t][i] = floatx4{};
+#pragma unroll
+    for (int s = 0; s < S::kStages - 1; ++s) T.issue(T.k0 + s);
+    uint32_t word = T.wscale(T.k0);
+    for (int kt = T.k0; kt < T.k1; ++kt) {
         // this wave's loads of stage kt have landed and its reads of stage kt - 1 are
         // done; past the barrier that holds for every wave
         __builtin_amdgcn_s_waitcnt(wait_vm_lds0(S::kDma * (S::kStages - 2)));
         __builtin_amdgcn_s_barrier();
-        issue(kt + S::kStages - 1);
-        const char *st = lds + ((kt - k0) % S::kStages) * S::kStageBytes;
-        const char *ss = st + S::kWBytes + S::kXBytes;
-        const int r0 = 16 * TM * wm + m;
-        const int64_t swi = sw0 + kt * sw1;
+        const char *st = T.stage(kt);
         i32x8 xf[TM];
 #pragma unroll
-        for (int i = 0; i < TM; ++i) xf[i] = frag(st + S::kWBytes + (r0 + 16 * i) * kG);
-        int wb = 0, xb[TM]; // E8M0 bytes
-        float f[TM];        // the product of both scales
-        if constexpr (E8) {
-            // one byte by a scalar load of its aligned word
-            const uintptr_t at = reinterpret_cast<uintptr_t>(a.sw) + size_t(swi);
-            wb = int(*(cptr<uint32_t>)(at & ~uintptr_t(3)) >> (8 * (at & 3)) & 255);
-#pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                xb[i] = *reinterpret_cast<const uint8_t *>(ss + r0 + 16 * i);
-                if (F == kF32) f[i] = e8m0(wb) * e8m0(xb[i]);
-            }
-        } else {
-            const float ws = ((cptr<float>)(a.sw))[swi];
-#pragma unroll
-            for (int i = 0; i < TM; ++i) f[i] = ws * *reinterpret_cast<const float *>(ss + 4 * (r0 + 16 * i));
-        }
+        for (int i = 0; i < TM; ++i) xf[i] = T.xfrag(st, i);
+        const i32x8 w0 = T.wfrag(st, 0);
+        const auto sc = T.scales(kt, word);
+        const i32x8 w1 = T.wfrag(st, 1);
+        // the next stage's loads go out while these reads come back
+        T.issue(kt + S::kStages - 1);
+        word = T.wscale(kt + 1);
         if constexpr (F == kF32) {
-            exact_block<TN, TM>(xf, f, acc, [&](int t) { return wfrag(st, t); });
-            continue;
-        }
+            exact_block<TN, TM>(xf, sc.f, acc, [&](int t) { return t ? T.wfrag(st, t) : w0; });
+        } else if constexpr (E8) {
 #pragma unroll
-        for (int t = 0; t < TN; ++t) {
-            const i32x8 wf = wfrag(st, t);
+            for (int t = 0; t < TN; ++t) T.multiply(t ? t == 1 ? w1 : T.wfrag(st, t) : w0, xf, sc, acc[t]);
+        } else {
+            // the fmas of a column tile go between the matrix instructions of the next
+            constexpr int NW = 3;
+            i32x8 w[NW] = {w0, w1};
+            floatx4 q[2][TM];
 #pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                if constexpr (E8) {
-                    acc[t][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf[i], acc[t][i], 0, 0, 0, wb, 0, xb[i]);
-                } else { // scale bytes of 127: 2^0
-                    const floatx4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf[i], floatx4{}, 0, 0, 0, 127, 0, 127);
+            for (int t = 0; t <= TN; ++t) {
+                __builtin_amdgcn_sched_barrier(0);
+                if (NW > 2 ? t + 2 < TN : t > 0 && t + 1 < TN) w[(t + NW - 1) % NW] = T.wfrag(st, t + NW - 1);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) acc[t][i][q] = fmaf(p[q], f[i], acc[t][i][q]);
+                for (int i = 0; i < TM; ++i) {
+                    if (t < TN)
+                        q[t & 1][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[t % NW], xf[i], floatx4{}, 0, 0, 0, 127, 0, 127);
+                    if (t > 0)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[t - 1][i][e] = fmaf(q[(t - 1) & 1][i][e], sc.f[i], acc[t - 1][i][e]);
                 }
             }
         }
     }
     // no direct load may still be writing this workgroup's LDS when it ends
     __builtin_amdgcn_s_waitcnt(wait_vm(0));
-
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        if (yrow[i] < 0) continue;
-        if constexpr (WT) { // lane: columns 16 t + 4 g .. + 3
-            float *o = static_cast<float *>(a.y) + (int64_t(split) * a.T + yrow[i]) * a.n + cw0 + 4 * g;
-#pragma unroll
-            for (int t = 0; t < TN; ++t)
-                if (cw0 + 16 * t < a.n) *reinterpret_cast<floatx4 *>(o + 16 * t) = acc[t][i];
-        } else {
-            float v[4 * TN];
-#pragma unroll
-            for (int t = 0; t < TN; ++t)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) v[4 * t + q] = acc[t][i][q];
-            store_row<TN, F == kF32>(a, yrow[i], cw0 + 4 * TN * g, v);
-        }
-    }
+    T.correct(acc);
+    T.store(acc);
 }
 
 typedef Shape<8, 4, 2, 4, 2> Large;  // 256 columns x 256 rows, 8 waves
@@ -561,7 +693,8 @@ int launch_fused_linear_block(hipStream_t s, const ShrinkArgs &sa, const void *W
     a.Tp = p.h->num_sorted;
     a.tp_dev = plan_sorted_dev(p);
     a.vh = vh;
-    return launch_product<kFused>(s, a, scale_type == LORA_SCALE_E8M0);
+    const bool e8 = scale_type == LORA_SCALE_E8M0;
+    return ranks_of_8(p) ? launch_product<kFused>(s, a, e8) : launch_product<kFusedAnyRank>(s, a, e8);
 }
 
 size_t fused_block_backward_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out, int32_t max_rank)

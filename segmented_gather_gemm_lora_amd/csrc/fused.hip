@@ -645,12 +645,7 @@ int launch_fused_linear(hipStream_t s, const ShrinkArgs &sa, const void *W0, con
     a.tiles_n = (ea.d_out + kBN - 1) / kBN;
     const int64_t nwg = int64_t(a.tiles_m) * a.tiles_n;
     if (nwg > (int64_t(1) << 31) - 1) return fail(LORA_ERR_ARG, "fused layer: too many tiles");
-    bool vecb = true;
-    const lora_seg_desc *hseg = reinterpret_cast<const lora_seg_desc *>(reinterpret_cast<const char *>(p.h) +
-                                                                        p.h->seg_offset);
-    if (plan_on_device(p.h)) vecb = plan_rank_multiple(p.h) % 8 == 0;
-    else
-        for (int i = 0; i < p.h->num_segments; ++i) vecb = vecb && (hseg[i].rank & 7) == 0;
+    const bool vecb = ranks_of_8(p);
     const dim3 grid(static_cast<unsigned>(nwg));
     if (w0_e4m3) {
         if (vecb) launch_kernel(fused_linear_kernel<true, true>, grid, dim3(kThreads), 0, s, a);

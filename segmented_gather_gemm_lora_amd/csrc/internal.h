@@ -30,6 +30,15 @@ inline const int32_t *plan_sorted_dev(const PlanView &p)
 {
     return plan_on_device(p.h) ? &reinterpret_cast<const lora_plan_header *>(p.dev)->num_sorted : nullptr;
 }
+// Whether every rank of the plan is a multiple of 8.
+inline bool ranks_of_8(const PlanView &p)
+{
+    if (plan_on_device(p.h)) return plan_rank_multiple(p.h) % 8 == 0;
+    const auto *seg = reinterpret_cast<const lora_seg_desc *>(reinterpret_cast<const char *>(p.h) + p.h->seg_offset);
+    for (int i = 0; i < p.h->num_segments; ++i)
+        if (seg[i].rank & 7) return false;
+    return true;
+}
 struct DevicePlanCall {
     const int32_t *adapters, *lengths;
     int32_t n_requests, n_adapters, max_rank, rank_multiple;
