@@ -91,92 +91,137 @@ __device__ __forceinline__ void dma4(const void *g, uint32_t lds_byte)
     asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(lds_byte) : "memory");
 }
 
+// dma16 from a wave-uniform base plus a 32-bit per-lane byte offset.
+__device__ __forceinline__ void dma16s(const void *base, uint32_t off, uint32_t lds_byte)
+{
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds_byte) : "memory");
+}
+
 // Column of a wave's tile t that MFMA row m stands for: lane group g ends with columns
 // 4 TN g + 4 t + q.
 template <int TN> __device__ __forceinline__ int wave_col(int m, int t) { return (m >> 2) * (4 * TN) + 4 * t + (m & 3); }
 
-// Operands of one correction step: 16 ranks (from j0) of segment s for a wave's rows and
-// columns.  A = B_s rows (lane groups 0, 2: ranks j0 .. j0 + 7, groups 1, 3: j0 + 8 .. j0 +
-// 15), B = scale_s v in two halves (groups 0, 1: hi, 2, 3: lo), zero on rows of others.
-template <int TN, int TM> struct Step {
-    u32x4 b[TN], v[TM];
-};
-struct Segment {
-    gptr<uint16_t> B;
-    int r, p0, p1;
-};
-__device__ __forceinline__ Segment segment(const BlockArgs &a, int s)
+// The correction of the segments that meet a wave's rows (at most one a row), on bf16
+// MFMA: a step is 16 ranks of one segment, A = B_s rows (lane groups 0, 2: the first 8 ranks,
+// 1, 3: the others), B = scale_s v in two halves (groups 0, 1: hi, 2, 3: lo).  Only the row tiles that the
+// segment meets are multiplied, and of those only its own rows take the result: what is
+// not finite in one adapter stays with its rows.  Ranks are the outer loop: the rows' v of 16
+// ranks is then loaded once for all segments.
+//
+// kRing (every rank is a multiple of 8): B_s comes by direct loads through a ring of
+// steps in LDS that is the wave's own, several steps ahead: short segments are chains of
+// loads that depend on nothing but their segment, and one step at a time took over 2 us.
+template <int TN, int TM, bool kRing, int kBytes>
+__device__ __forceinline__ void correction(const BlockArgs &a, int Tp, int pw0, int cw0, int lane, char *mine, uint32_t mine_lds,
+                                           floatx4 (&acc)[TN][TM])
 {
-    const lora_seg_desc *d = a.seg + s;
-    return Segment{as_global<uint16_t>(reinterpret_cast<const void *>(d->B)), d->rank, d->start, d->start + d->len};
-}
-
-// RV: every rank is a multiple of 8, so 8 ranks of a row are one aligned load.
-template <int TN, int TM, bool RV>
-__device__ __forceinline__ void load_step(const BlockArgs &a, const Segment &sg, int j0, int pw0, int cw0, int lane, Step<TN, TM> &f)
-{
+    constexpr int kSlot = 512 * TN, kLoads = TN / 2, kDepth = kBytes / kSlot < 4 ? kBytes / kSlot : 4;
+    static_assert(kDepth >= 2 && 16 * TM <= 64, "ring, segments of a wave");
     const int m = lane & 15, g = lane >> 4;
-    const int r = sg.r, jj = j0 + 8 * (g & 1);
-#pragma unroll
-    for (int t = 0; t < TN; ++t) {
-        const int c = cw0 + wave_col<TN>(m, t);
-        const gptr<uint16_t> row = sg.B + int64_t(c < a.n ? c : a.n - 1) * r;
-        if constexpr (RV) {
-            f.b[t] = *(gptr<u32x4>)(row + (jj < r ? jj : 0));
-            if (jj >= r) f.b[t] = u32x4{};
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int j = jj + 2 * e;
-                const uint32_t lo = row[j < r ? j : 0], hi = row[j + 1 < r ? j + 1 : 0];
-                f.b[t][e] = (j < r ? lo : 0) | (j + 1 < r ? hi << 16 : 0);
-            }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        const int p = pw0 + 16 * i + m;
-        const bool in = p >= sg.p0 && p < sg.p1;
-        f.v[i] = *(gptr<u32x4>)(as_global<uint16_t>(a.vh) + int64_t(in ? p : sg.p0) * a.ldh + 2 * j0 + 8 * g);
-        if (!in) f.v[i] = u32x4{};
-    }
-}
-
-// The correction of the segments that meet rows pw0 .. pw0 + 16 TM, on bf16 MFMA, 16
-// ranks a step; with RV the operands of a step are loaded before the products of the one before.
-template <int TN, int TM, bool RV>
-__device__ __forceinline__ void correction(const BlockArgs &a, int Tp, int pw0, int cw0, int lane, floatx4 (&acc)[TN][TM])
-{
-    auto add = [&](const Step<TN, TM> &f) {
-#pragma unroll
-        for (int t = 0; t < TN; ++t)
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-                acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f.b[t]), __builtin_bit_cast(bf16x8, f.v[i]),
-                                                                    acc[t][i], 0, 0, 0);
-    };
     const int plast = (pw0 + 16 * TM < Tp ? pw0 + 16 * TM : Tp) - 1;
-    const int s1 = uniform(a.segidx[plast]);
-    int s = uniform(a.segidx[pw0]), j0 = 0;
-    Segment sg = segment(a, s);
-    Step<TN, TM> f[2];
-    load_step<TN, TM, RV>(a, sg, j0, pw0, cw0, lane, f[0]);
-    // two steps a round, so that no operand is copied
-    for (;;) {
-        bool more = true;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (!more) break;
-            j0 += 16;
-            if (j0 >= sg.r) {
-                j0 = 0;
-                more = ++s <= s1;
-                if (more) sg = segment(a, s);
-            }
-            if (more) load_step<TN, TM, RV>(a, sg, j0, pw0, cw0, lane, f[h ^ 1]);
-            add(f[h]);
+    const int s0 = uniform(a.segidx[pw0]), n = uniform(a.segidx[plast]) - s0 + 1;
+    // lane l: the wave's segment l
+    const lora_seg_desc *d = a.seg + s0 + (lane < n ? lane : n - 1);
+    const uint64_t dB = d->B;
+    const uint32_t Blo = uint32_t(dB), Bhi = uint32_t(dB >> 32);
+    const int start = d->start, len = d->len, rank = lane < n ? d->rank : 0;
+    auto lane_of = [](int v, int l) { return __builtin_amdgcn_readlane(v, l); };
+    auto base_of = [&](int l) {
+        return reinterpret_cast<const void *>(uint64_t(uint32_t(lane_of(int(Blo), l))) | uint64_t(uint32_t(lane_of(int(Bhi), l))) << 32);
+    };
+    auto next = [&](int &q, uint64_t &left) { // the next step (16 ranks q, segment), or -1
+        while (left == 0) {
+            left = __ballot(rank > 16 * ++q);
+            if (left == 0) return -1;
         }
-        if (!more) break;
+        const int l = __builtin_ctzll(left);
+        left &= left - 1;
+        return l;
+    };
+    int pq = -1, issued = 0, done = 0; // steps whose loads are out
+    uint64_t pleft = 0;
+    bool more = true;
+    int col[kLoads];
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) { // LDS row 32 k + lane / 2 of a step, half lane % 2
+        const int rho = 32 * k + (lane >> 1), c = cw0 + wave_col<TN>(rho & 15, rho >> 4);
+        col[k] = c < a.n ? c : a.n - 1;
+    }
+    auto issue = [&] {
+        const int l = next(pq, pleft);
+        if (l < 0) {
+            more = false;
+            return;
+        }
+        const int r = lane_of(rank, l), half = 16 * pq + 8 < r ? lane & 1 : 0;
+        const void *B = base_of(l);
+        const uint32_t to = mine_lds + uint32_t(issued % kDepth) * kSlot;
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) dma16s(B, uint32_t(col[k]) * uint32_t(2 * r) + uint32_t(32 * pq + 16 * half), to + 1024 * k);
+        ++issued;
+    };
+    if constexpr (kRing)
+        for (int i = 0; i < kDepth && more; ++i) issue();
+    int q = -1, vq = -1;
+    uint64_t left = 0;
+    u32x4 v[TM];
+    for (;;) {
+        const int l = next(q, left);
+        if (l < 0) break;
+        if (q != vq) {
+            vq = q;
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                const int p = pw0 + 16 * i + m;
+                v[i] = *(gptr<u32x4>)(as_global<uint16_t>(a.vh) + int64_t(p < Tp ? p : Tp - 1) * a.ldh + 32 * q + 8 * g);
+            }
+        }
+        const int r = lane_of(rank, l), p0 = lane_of(start, l), p1 = p0 + lane_of(len, l);
+        const int jj = 16 * q + 8 * (g & 1);
+        bf16x8 b[TN];
+        if constexpr (kRing) {
+            // this step's loads have landed: with a full ring all but those of the later ones
+            if (issued - done == kDepth) __builtin_amdgcn_s_waitcnt(wait_vm(kLoads * (kDepth - 1)));
+            else __builtin_amdgcn_s_waitcnt(wait_vm(0));
+            const char *at = mine + (done % kDepth) * kSlot + m * 32 + (g & 1) * 16;
+#pragma unroll
+            for (int t = 0; t < TN; ++t) {
+                u32x4 u = *reinterpret_cast<const u32x4 *>(at + 512 * t);
+                if (jj >= r) u = u32x4{};
+                b[t] = __builtin_bit_cast(bf16x8, u);
+            }
+            ++done;
+            __builtin_amdgcn_s_waitcnt(kWaitLds0); // read before the place is filled again
+            if (more) issue();
+        } else {
+            const gptr<uint16_t> B = as_global<uint16_t>(base_of(l));
+#pragma unroll
+            for (int t = 0; t < TN; ++t) {
+                const int c = cw0 + wave_col<TN>(m, t);
+                const gptr<uint16_t> row = B + int64_t(c < a.n ? c : a.n - 1) * r;
+                u32x4 u;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = jj + 2 * e;
+                    const uint32_t lo = row[j < r ? j : 0], hi = row[j + 1 < r ? j + 1 : 0];
+                    u[e] = (j < r ? lo : 0) | (j + 1 < r ? hi << 16 : 0);
+                }
+                b[t] = __builtin_bit_cast(bf16x8, u);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int t0 = pw0 + 16 * i;
+            if (p0 >= t0 + 16 || p1 <= t0) continue; // wave-uniform
+            const bool in = t0 + m >= p0 && t0 + m < p1;
+            const bf16x8 vi = __builtin_bit_cast(bf16x8, v[i]);
+#pragma unroll
+            for (int t = 0; t < TN; ++t) {
+                const floatx4 y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[t], vi, acc[t][i], 0, 0, 0);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[t][i][e] = in ? y[e] : acc[t][i][e];
+            }
+        }
     }
 }
 
@@ -257,12 +302,6 @@ constexpr bool is_fused(Form f) { return f == kFused || f == kFusedAnyRank; }
 __device__ __forceinline__ float e8m0(int e)
 {
     return e == 255 ? __uint_as_float(0x7FC00000u) : e ? __uint_as_float(uint32_t(e) << 23) : 0x1p-127f;
-}
-
-// dma16 from a wave-uniform base plus a 32-bit per-lane byte offset.
-__device__ __forceinline__ void dma16s(const void *base, uint32_t off, uint32_t lds_byte)
-{
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds_byte) : "memory");
 }
 
 // A workgroup's tile: its place, the loads of its stages and the fragments in them.
@@ -444,13 +483,16 @@ template <class S, bool E8, Form F> struct Tile {
         }
     }
 
+    // Behind the last stage: its place in LDS is free when every wave is past its reads.
     __device__ __forceinline__ void correct(floatx4 (&acc)[TN][TM]) const
     {
         if constexpr (is_fused(F)) {
+            __builtin_amdgcn_s_waitcnt(kWaitLds0);
+            __builtin_amdgcn_s_barrier();
+            constexpr int kBytes = S::kStages * S::kStageBytes / S::kWaves / 1024 * 1024;
             const int Tp = a.tp_dev ? uniform(*a.tp_dev) : a.Tp;
-            if (pw0 < Tp) {
-                correction<TN, TM, F == kFused>(a, Tp, pw0, cw0, lane, acc);
-            }
+            if (pw0 < Tp)
+                correction<TN, TM, F == kFused, kBytes>(a, Tp, pw0, cw0, lane, lds + wave * kBytes, lds0 + uint32_t(wave) * kBytes, acc);
         }
     }
 
