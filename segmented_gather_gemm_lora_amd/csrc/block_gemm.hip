@@ -68,6 +68,9 @@ struct BlockArgs {
     const int32_t *tp_dev;
     const uint16_t *vh;
     int64_t ldh;
+    const float *v; // up to 64 rows: the shrink's slices of v, and their layout
+    int64_t ldw, sl_stride;
+    int nsl;
     int per; // gradient: stages of a split; split i writes rows i T .. of y
 };
 
@@ -582,6 +585,321 @@ void block_gemm_kernel(BlockArgs a)
     T.store(acc);
 }
 
+// Up to 64 rows: bound by reading W once.  A workgroup has 16 TN columns and all rows; its 8 waves
+// take every eighth block each, straight from memory in MFMA order (a wave's 16 columns of a
+// block are whole 128-byte lines), with 8 KB of W a wave on the way: 64 KB a CU, which
+// is what HBM's latency takes.  The waves' sums meet in LDS.  x's codes (at most 64 rows) are
+// read by every workgroup from L2; TN grows with the columns, so that there are about 256.
+constexpr int kFew = 64;
+constexpr int kMaxSlices = 4; // of the shrink
+constexpr int kFewWaves = 8;
+template <int TN, int TM, bool E8, Form F> __global__ __launch_bounds__(64 * kFewWaves) void block_few_kernel(BlockArgs a)
+{
+    constexpr int D = 4 / TN; // blocks of a group
+    constexpr int kPitch = 16 * TN + 4;
+    constexpr int kSum = kFewWaves * 16 * TM * kPitch * 4;
+    constexpr int kV = is_fused(F) ? 16 * TM * 2 * LORA_MAX_RANK * 2 : 0;
+    __shared__ __attribute__((aligned(16))) char lds[kSum > kV ? kSum : kV];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int m = lane & 15, g = lane >> 4;
+    const int c0 = int(blockIdx.x) * 16 * TN;
+    const int blocks = (a.k + kG - 1) / kG;
+    const int nb = (c0 < a.n ? c0 : a.n - 1) / kG;
+
+    const gptr<char> W = as_global<char>(a.W), X = as_global<char>(a.x), SX = as_global<char>(a.sx);
+    uint32_t woff[TN];
+    int64_t xoff[TM];
+    int xrow[TM];
+#pragma unroll
+    for (int t = 0; t < TN; ++t) {
+        const int c = c0 + 16 * t + m;
+        woff[t] = uint32_t(int64_t(c < a.n ? c : a.n - 1) * a.k);
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        const int p = 16 * i + m;
+        xrow[i] = p < a.T ? p : a.T - 1;
+        xoff[i] = xrow[i] * a.ldx;
+    }
+    struct Row {
+        u32x4 lo, hi;
+    };
+    // units g and g + 4 of a row's block; past k those of another place of the row
+    auto load = [&](gptr<char> row, int kb) {
+        const int k = kb * kG + 16 * g;
+        return Row{*(gptr<u32x4>)(row + (k < a.k ? k : 0)), *(gptr<u32x4>)(row + (k + 64 < a.k ? k + 64 : 0))};
+    };
+    auto operand = [](const Row &r) {
+        return i32x8{int(r.lo[0]), int(r.lo[1]), int(r.lo[2]), int(r.lo[3]), int(r.hi[0]), int(r.hi[1]), int(r.hi[2]), int(r.hi[3])};
+    };
+    struct Group {
+        Row w[D][TN];
+    };
+    struct Rows {
+        Row x[TM];
+        uint32_t sx[TM]; // fp32 bits or a byte
+    };
+    auto block_of = [&](int j) { return wave + kFewWaves * j; }; // the wave's block j
+    auto load_group = [&](int j, Group &G) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            const int kb = block_of(j + d);
+#pragma unroll
+            for (int t = 0; t < TN; ++t) G.w[d][t] = load(W + woff[t], kb < blocks ? kb : blocks - 1);
+        }
+    };
+    auto load_rows = [&](int j, Rows &R) {
+        int kb = block_of(j);
+        kb = kb < blocks ? kb : blocks - 1;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            R.x[i] = load(X + xoff[i], kb);
+            const int64_t at = kb * a.lds + xrow[i];
+            if constexpr (E8) R.sx[i] = *(gptr<uint8_t>)(SX + at);
+            else R.sx[i] = *(gptr<uint32_t>)(SX + 4 * at);
+        }
+    };
+    floatx4 acc[TN][TM];
+#pragma unroll
+    for (int t = 0; t < TN; ++t)
+#pragma unroll
+        for (int i = 0; i < TM; ++i) acc[t][i] = floatx4{};
+    auto multiply = [&](int j, const Row (&w)[TN], Rows &R) {
+        const int kb = block_of(j);
+        if (kb >= blocks) return; // wave-uniform
+        const int64_t at = int64_t(nb) * blocks + kb;
+        i32x8 xf[TM];
+        float f[TM];
+        int wb = 0;
+        if constexpr (E8) {
+            const uintptr_t p = reinterpret_cast<uintptr_t>(a.sw) + size_t(at);
+            wb = int(*(cptr<uint32_t>)(p & ~uintptr_t(3)) >> (8 * (p & 3)) & 255);
+        }
+        const int k = kb * kG + 16 * g;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) { // past k x's codes are zeros
+            if (k >= a.k) R.x[i].lo = u32x4{};
+            if (k + 64 >= a.k) R.x[i].hi = u32x4{};
+            xf[i] = operand(R.x[i]);
+            if constexpr (E8) f[i] = F == kF32 ? e8m0(wb) * e8m0(int(R.sx[i])) : 0.f;
+            else f[i] = ((cptr<float>)(a.sw))[at] * __uint_as_float(R.sx[i]);
+        }
+        if constexpr (F == kF32) {
+            exact_block<TN, TM>(xf, f, acc, [&](int t) { return operand(w[t]); });
+        } else {
+#pragma unroll
+            for (int t = 0; t < TN; ++t)
+#pragma unroll
+                for (int i = 0; i < TM; ++i) {
+                    if constexpr (E8) {
+                        acc[t][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w[t]), xf[i], acc[t][i], 0, 0, 0, wb, 0,
+                                                                                     int(R.sx[i]));
+                    } else {
+                        const floatx4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w[t]), xf[i], floatx4{}, 0, 0, 0,
+                                                                                           127, 0, 127);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) acc[t][i][q] = fmaf(p[q], f[i], acc[t][i][q]);
+                    }
+                }
+        }
+    };
+    // one group: the next one's loads go out first
+    const int mine = wave < blocks ? (blocks - wave + kFewWaves - 1) / kFewWaves : 0; // blocks of this wave
+    Group A, B;
+    Rows R0, R1;
+    auto group = [&](int j, Group &cur, Group &nxt) {
+        if (j + D < mine) load_group(j + D, nxt);
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            Rows &now = d & 1 ? R1 : R0, &then = d & 1 ? R0 : R1;
+            if (j + d + 1 < mine) load_rows(j + d + 1, then);
+            multiply(j + d, cur.w[d], now);
+            if (D == 1) R0 = R1;
+        }
+    };
+    load_group(0, A);
+    load_rows(0, R0);
+
+    // The correction.  v = the sum of the shrink's slices, in two bf16 halves in the order of
+    // v_halves(), goes to LDS; the segments are dealt to the waves, and kAhead steps of 16 ranks
+    // are loaded at a time, the first before the products.
+    constexpr int kAhead = 4 / TN;
+    struct Step {
+        u32x4 b[TN];
+        int r, p0, p1, j0; // p1 = 0: none
+        float scale;
+    };
+    const int pitch = int(a.ldh);
+    int s_at = wave, j_at = 0, S = 0;
+    Step step[kAhead];
+    auto load_steps = [&] {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            Step &f = step[i];
+            f.p1 = 0;
+            if (s_at >= S) continue;
+            const auto *d = (cptr<lora_seg_desc>)(a.seg + s_at);
+            const gptr<uint16_t> Bs = as_global<uint16_t>(reinterpret_cast<const void *>(d->B));
+            f.r = d->rank;
+            f.p0 = d->start;
+            f.p1 = f.p0 + d->len;
+            f.scale = d->scale;
+            f.j0 = j_at;
+            const int r = f.r, jj = f.j0 + 8 * (g & 1);
+#pragma unroll
+            for (int t = 0; t < TN; ++t) {
+                const int c = c0 + 16 * t + m;
+                const gptr<uint16_t> row = Bs + int64_t(c < a.n ? c : a.n - 1) * r;
+                u32x4 u{};
+                if ((r & 7) == 0) {
+                    u = *(gptr<u32x4>)(row + (jj < r ? jj : 0));
+                    if (jj >= r) u = u32x4{};
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = jj + 2 * e;
+                        const uint32_t x0 = row[j < r ? j : 0], x1 = row[j + 1 < r ? j + 1 : 0];
+                        u[e] = (j < r ? x0 : 0) | (j + 1 < r ? x1 << 16 : 0);
+                    }
+                }
+                f.b[t] = u;
+            }
+            j_at += 16;
+            if (j_at >= r) {
+                j_at = 0;
+                s_at += kFewWaves;
+            }
+        }
+    };
+    auto add_steps = [&] {
+#pragma unroll
+        for (int h = 0; h < kAhead; ++h) {
+            const Step &f = step[h];
+            if (f.p1 == 0) continue;
+            const int left = f.r - (f.j0 + 8 * (g & 1)); // ranks of this lane's 8 (LDS holds any bits past r)
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                if (f.p0 >= 16 * i + 16 || f.p1 <= 16 * i) continue; // wave-uniform
+                const bool in = 16 * i + m >= f.p0 && 16 * i + m < f.p1;
+                u32x4 v = *reinterpret_cast<const u32x4 *>(lds + ((16 * i + m) * pitch + 2 * f.j0 + 8 * g) * 2);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] &= (2 * e < left ? 0xFFFFu : 0u) | (2 * e + 1 < left ? 0xFFFF0000u : 0u);
+#pragma unroll
+                for (int t = 0; t < TN; ++t) {
+                    const floatx4 y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f.b[t]),
+                                                                              __builtin_bit_cast(bf16x8, v), floatx4{}, 0, 0, 0);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[t][i][e] = in ? fmaf(f.scale, y[e], acc[t][i][e]) : acc[t][i][e];
+                }
+            }
+        }
+    };
+    if constexpr (is_fused(F)) {
+        const int Tp = a.tp_dev ? *(cptr<int32_t>)(a.tp_dev) : a.Tp;
+        S = Tp > 0 ? *((cptr<int32_t>)(a.segidx) + (Tp - 1)) + 1 : 0;
+        for (int e = tid; e < Tp * (pitch / 8); e += 64 * kFewWaves) { // 4 ranks of a row a thread
+            const int p = e / (pitch / 8), j = e % (pitch / 8) * 4;
+            const int64_t at = p * a.ldw + (j < a.ldw ? j : 0);
+            floatx4 v{};
+#pragma unroll
+            for (int c = 0; c < kMaxSlices; ++c) {
+                const floatx4 u = *reinterpret_cast<const floatx4 *>(a.v + (c < a.nsl ? c : 0) * a.sl_stride + at);
+                if (c < a.nsl)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) v[x] += u[x];
+            }
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                hi[x] = f32_to_bf16(v[x]);
+                lo[x] = f32_to_bf16(v[x] - bf16_to_f32(hi[x]));
+            }
+            char *to = lds + (p * pitch + 32 * (j >> 4) + (j & 15)) * 2;
+            *reinterpret_cast<u32x2 *>(to) = u32x2{hi[0] | hi[1] << 16, hi[2] | hi[3] << 16};
+            *reinterpret_cast<u32x2 *>(to + 32) = u32x2{lo[0] | lo[1] << 16, lo[2] | lo[3] << 16};
+        }
+        load_steps();
+    }
+    for (int j = 0; j < mine; j += 2 * D) {
+        group(j, A, B);
+        if (j + D < mine) group(j + D, B, A);
+    }
+    if constexpr (is_fused(F)) {
+        __syncthreads();
+        for (;;) {
+            add_steps();
+            if (s_at >= S) break;
+            load_steps();
+        }
+        __syncthreads(); // v's place is the sums' now
+    }
+
+    // the waves' sums, in wave order
+    float *sums = reinterpret_cast<float *>(lds);
+#pragma unroll
+    for (int t = 0; t < TN; ++t)
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            *reinterpret_cast<floatx4 *>(sums + (wave * 16 * TM + 16 * i + m) * kPitch + 16 * t + 4 * g) = acc[t][i];
+    __syncthreads();
+    for (int e = tid; e < a.T * 4 * TN; e += 64 * kFewWaves) {
+        const int p = e / (4 * TN), c = e % (4 * TN) * 4;
+        floatx4 y{};
+#pragma unroll
+        for (int w = 0; w < kFewWaves; ++w) {
+            const floatx4 u = *reinterpret_cast<const floatx4 *>(sums + (w * 16 * TM + p) * kPitch + c);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) y[x] += u[x];
+        }
+        const int row = a.perm ? a.perm[p] : p;
+        if (row < 0) continue;
+        const int n = c0 + c;
+        if constexpr (F == kF32) {
+            float *o = static_cast<float *>(a.y) + row * a.ldy + n;
+            if (a.vec_y && n + 4 <= a.n) *reinterpret_cast<floatx4 *>(o) = y;
+            else
+                for (int x = 0; x < 4; ++x)
+                    if (n + x < a.n) o[x] = y[x];
+        } else {
+            uint16_t *o = static_cast<uint16_t *>(a.y) + row * a.ldy + n;
+            if (a.vec_y && n + 4 <= a.n) *reinterpret_cast<u32x2 *>(o) = u32x2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+            else
+                for (int x = 0; x < 4; ++x)
+                    if (n + x < a.n) o[x] = uint16_t(f32_to_bf16(y[x]));
+        }
+    }
+}
+
+template <int TN, Form F> void go_few_rows(hipStream_t s, const BlockArgs &a, bool e8, dim3 grid)
+{
+    const dim3 block(64 * kFewWaves);
+    const int tm = a.T <= 16 ? 1 : a.T <= 32 ? 2 : 4;
+    if (e8) {
+        if (tm == 1) launch_kernel(block_few_kernel<TN, 1, true, F>, grid, block, 0, s, a);
+        else if (tm == 2) launch_kernel(block_few_kernel<TN, 2, true, F>, grid, block, 0, s, a);
+        else if constexpr (TN <= (F == kF32 ? 1 : 2)) launch_kernel(block_few_kernel<TN, 4, true, F>, grid, block, 0, s, a);
+    } else {
+        if (tm == 1) launch_kernel(block_few_kernel<TN, 1, false, F>, grid, block, 0, s, a);
+        else if (tm == 2) launch_kernel(block_few_kernel<TN, 2, false, F>, grid, block, 0, s, a);
+        else if constexpr (TN <= (F == kF32 ? 1 : 2)) launch_kernel(block_few_kernel<TN, 4, false, F>, grid, block, 0, s, a);
+    }
+}
+
+template <Form F> int go_few(hipStream_t s, const BlockArgs &a, bool e8)
+{
+    // about a workgroup for each CU
+    // (the registers of 64 rows hold fewer columns)
+    const int tiles = (a.n + 15) / 16, most = a.T <= 32 ? 4 : F == kF32 ? 1 : 2;
+    const int tn = std::min(most, tiles <= 256 ? 1 : tiles <= 512 ? 2 : 4);
+    const dim3 grid{unsigned((tiles + tn - 1) / tn)};
+    if (tn == 1) go_few_rows<1, F>(s, a, e8, grid);
+    else if (tn == 2) go_few_rows<2, F>(s, a, e8, grid);
+    else go_few_rows<4, F>(s, a, e8, grid); // up to 32 rows
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return fail(LORA_ERR_HIP, "block product launch: %s", hipGetErrorString(e));
+    return LORA_OK;
+}
+
 typedef Shape<8, 4, 2, 4, 2> Large;  // 256 columns x 256 rows, 8 waves
 typedef Shape<4, 4, 2, 2, 2> Medium; // 128 x 128, 4 waves, two workgroups on a CU
 typedef Shape<2, 2, 4, 2, 3> Small;  // 128 x 64, 8 waves
@@ -602,7 +920,7 @@ template <class S, Form F> int go(hipStream_t s, BlockArgs &a, bool e8, int spli
 
 template <Form F> int launch_product(hipStream_t s, BlockArgs &a, bool e8)
 {
-    if (a.T <= 64) return go<Small, F>(s, a, e8);
+    if (a.T <= kFew) return go_few<F == kFusedAnyRank ? kFused : F>(s, a, e8);
     // fp32 results hold the rows' widened operands too: tiles of 128 x 128
     if (F != kF32 && int64_t(a.T + 255) / 256 * ((a.n + 255) / 256) >= 128) return go<Large, F>(s, a, e8);
     return go<Medium, F>(s, a, e8);
@@ -717,7 +1035,14 @@ int launch_fused_linear_block(hipStream_t s, const ShrinkArgs &sa, const void *W
     if (st) return st;
     uint16_t *vh = reinterpret_cast<uint16_t *>(base + w.vh);
     a.ldh = vh_pitch(max_rank);
-    if (p.h->num_sorted > 0 && (st = launch_v_halves(s, sa, p, ws, vh, a.ldh))) return st;
+    a.nsl = 0;
+    if (p.h->num_sorted > 0) {
+        a.v = static_cast<const float *>(ws);
+        st = T <= kFew ? launch_sgmv_shrink_split(s, sa, p, static_cast<float *>(ws), &a.ldw, &a.sl_stride, &a.nsl)
+                       : launch_v_halves(s, sa, p, ws, vh, a.ldh);
+        if (st) return st;
+        if (a.nsl > kMaxSlices) return fail(LORA_ERR_ARG, "block product: %d d_in slices > %d", a.nsl, kMaxSlices);
+    }
     a.x = static_cast<const uint8_t *>(q.codes);
     a.ldx = w.ldq;
     a.sx = q.scales;
