@@ -595,7 +595,8 @@ constexpr int kMaxSlices = 4; // of the shrink
 constexpr int kFewWaves = 8;
 template <int TN, int TM, bool E8, Form F> __global__ __launch_bounds__(64 * kFewWaves) void block_few_kernel(BlockArgs a)
 {
-    constexpr int D = 4 / TN; // blocks of a group
+    // blocks of the wave whose loads are out: four where the registers hold them
+    constexpr int D = TN * TM <= 4 && !(F == kF32 && TM == 4) ? 4 : 2;
     constexpr int kPitch = 16 * TN + 4;
     constexpr int kSum = kFewWaves * 16 * TM * kPitch * 4;
     constexpr int kV = is_fused(F) ? 16 * TM * 2 * LORA_MAX_RANK * 2 : 0;
@@ -632,31 +633,22 @@ template <int TN, int TM, bool E8, Form F> __global__ __launch_bounds__(64 * kFe
     auto operand = [](const Row &r) {
         return i32x8{int(r.lo[0]), int(r.lo[1]), int(r.lo[2]), int(r.lo[3]), int(r.hi[0]), int(r.hi[1]), int(r.hi[2]), int(r.hi[3])};
     };
-    struct Group {
-        Row w[D][TN];
-    };
-    struct Rows {
-        Row x[TM];
+    struct Operands {
+        Row w[TN], x[TM];
         uint32_t sx[TM]; // fp32 bits or a byte
     };
     auto block_of = [&](int j) { return wave + kFewWaves * j; }; // the wave's block j
-    auto load_group = [&](int j, Group &G) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            const int kb = block_of(j + d);
-#pragma unroll
-            for (int t = 0; t < TN; ++t) G.w[d][t] = load(W + woff[t], kb < blocks ? kb : blocks - 1);
-        }
-    };
-    auto load_rows = [&](int j, Rows &R) {
+    auto load_block = [&](int j, Operands &o) {
         int kb = block_of(j);
         kb = kb < blocks ? kb : blocks - 1;
 #pragma unroll
+        for (int t = 0; t < TN; ++t) o.w[t] = load(W + woff[t], kb);
+#pragma unroll
         for (int i = 0; i < TM; ++i) {
-            R.x[i] = load(X + xoff[i], kb);
+            o.x[i] = load(X + xoff[i], kb);
             const int64_t at = kb * a.lds + xrow[i];
-            if constexpr (E8) R.sx[i] = *(gptr<uint8_t>)(SX + at);
-            else R.sx[i] = *(gptr<uint32_t>)(SX + 4 * at);
+            if constexpr (E8) o.sx[i] = *(gptr<uint8_t>)(SX + at);
+            else o.sx[i] = *(gptr<uint32_t>)(SX + 4 * at);
         }
     };
     floatx4 acc[TN][TM];
@@ -664,7 +656,7 @@ template <int TN, int TM, bool E8, Form F> __global__ __launch_bounds__(64 * kFe
     for (int t = 0; t < TN; ++t)
 #pragma unroll
         for (int i = 0; i < TM; ++i) acc[t][i] = floatx4{};
-    auto multiply = [&](int j, const Row (&w)[TN], Rows &R) {
+    auto multiply = [&](int j, Operands &o) {
         const int kb = block_of(j);
         if (kb >= blocks) return; // wave-uniform
         const int64_t at = int64_t(nb) * blocks + kb;
@@ -678,24 +670,24 @@ template <int TN, int TM, bool E8, Form F> __global__ __launch_bounds__(64 * kFe
         const int k = kb * kG + 16 * g;
 #pragma unroll
         for (int i = 0; i < TM; ++i) { // past k x's codes are zeros
-            if (k >= a.k) R.x[i].lo = u32x4{};
-            if (k + 64 >= a.k) R.x[i].hi = u32x4{};
-            xf[i] = operand(R.x[i]);
-            if constexpr (E8) f[i] = F == kF32 ? e8m0(wb) * e8m0(int(R.sx[i])) : 0.f;
-            else f[i] = ((cptr<float>)(a.sw))[at] * __uint_as_float(R.sx[i]);
+            if (k >= a.k) o.x[i].lo = u32x4{};
+            if (k + 64 >= a.k) o.x[i].hi = u32x4{};
+            xf[i] = operand(o.x[i]);
+            if constexpr (E8) f[i] = F == kF32 ? e8m0(wb) * e8m0(int(o.sx[i])) : 0.f;
+            else f[i] = ((cptr<float>)(a.sw))[at] * __uint_as_float(o.sx[i]);
         }
         if constexpr (F == kF32) {
-            exact_block<TN, TM>(xf, f, acc, [&](int t) { return operand(w[t]); });
+            exact_block<TN, TM>(xf, f, acc, [&](int t) { return operand(o.w[t]); });
         } else {
 #pragma unroll
             for (int t = 0; t < TN; ++t)
 #pragma unroll
                 for (int i = 0; i < TM; ++i) {
                     if constexpr (E8) {
-                        acc[t][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w[t]), xf[i], acc[t][i], 0, 0, 0, wb, 0,
-                                                                                     int(R.sx[i]));
+                        acc[t][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(o.w[t]), xf[i], acc[t][i], 0, 0, 0, wb, 0,
+                                                                                     int(o.sx[i]));
                     } else {
-                        const floatx4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w[t]), xf[i], floatx4{}, 0, 0, 0,
+                        const floatx4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(o.w[t]), xf[i], floatx4{}, 0, 0, 0,
                                                                                            127, 0, 127);
 #pragma unroll
                         for (int q = 0; q < 4; ++q) acc[t][i][q] = fmaf(p[q], f[i], acc[t][i][q]);
@@ -703,22 +695,10 @@ template <int TN, int TM, bool E8, Form F> __global__ __launch_bounds__(64 * kFe
                 }
         }
     };
-    // one group: the next one's loads go out first
     const int mine = wave < blocks ? (blocks - wave + kFewWaves - 1) / kFewWaves : 0; // blocks of this wave
-    Group A, B;
-    Rows R0, R1;
-    auto group = [&](int j, Group &cur, Group &nxt) {
-        if (j + D < mine) load_group(j + D, nxt);
+    Operands ring[D];
 #pragma unroll
-        for (int d = 0; d < D; ++d) {
-            Rows &now = d & 1 ? R1 : R0, &then = d & 1 ? R0 : R1;
-            if (j + d + 1 < mine) load_rows(j + d + 1, then);
-            multiply(j + d, cur.w[d], now);
-            if (D == 1) R0 = R1;
-        }
-    };
-    load_group(0, A);
-    load_rows(0, R0);
+    for (int d = 0; d < D; ++d) load_block(d, ring[d]);
 
     // The correction.  v = the sum of the shrink's slices, in two bf16 halves in the order of
     // v_halves(), goes to LDS; the segments are dealt to the waves, and kAhead steps of 16 ranks
@@ -820,9 +800,12 @@ template <int TN, int TM, bool E8, Form F> __global__ __launch_bounds__(64 * kFe
         }
         load_steps();
     }
-    for (int j = 0; j < mine; j += 2 * D) {
-        group(j, A, B);
-        if (j + D < mine) group(j + D, B, A);
+    for (int j = 0; j < mine; j += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            multiply(j + d, ring[d]);
+            if (j + d + D < mine) load_block(j + d + D, ring[d]);
+        }
     }
     if constexpr (is_fused(F)) {
         __syncthreads();
