@@ -637,7 +637,13 @@ template <int TN, int TM, bool E8, Form F> __global__ __launch_bounds__(64 * kFe
         Row w[TN], x[TM];
         uint32_t sx[TM]; // fp32 bits or a byte
     };
-    auto block_of = [&](int j) { return wave + kFewWaves * j; }; // the wave's block j
+    // The wave's block j, from another place in each workgroup of an XCD: rows are often a
+    // power of two apart, so that one block of all rows lies in few channels of the L2.
+    const int turn = int(blockIdx.x >> 3) % blocks;
+    auto block_of = [&](int j) {
+        const int kb = wave + kFewWaves * j + turn;
+        return wave + kFewWaves * j >= blocks ? blocks : kb < blocks ? kb : kb - blocks;
+    };
     auto load_block = [&](int j, Operands &o) {
         int kb = block_of(j);
         kb = kb < blocks ? kb : blocks - 1;

@@ -24,6 +24,9 @@ namespace {
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kRows = 256; // rows that a workgroup ranks and scatters
+// Blocks, and chunks, of a workgroup: its share of T / 16 + min(T, N) and less than 16 more.
+constexpr int kRecords = 512;
+static_assert(kRows / 16 + kRows + 16 <= kRecords && 2 * kRecords <= kThreads, "a thread for each record");
 static_assert(sizeof(lora_blk_desc) == 128 && sizeof(lora_chunk_desc) == 320 && sizeof(lora_seg_desc) == 40, "records");
 
 struct DevicePlanArgs {
@@ -61,6 +64,7 @@ __global__ __launch_bounds__(kThreads) void plan_device_kernel(DevicePlanArgs a)
     extern __shared__ int32_t dyn[];
     __shared__ int32_t part[4][kWaves];
     __shared__ int32_t mark[kRows], last[kRows / 64];
+    __shared__ int32_t rows_of[2][kRecords];
     __shared__ int32_t sums[8]; // rows before this workgroup's without an adapter, rows of all requests
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int t0 = blockIdx.x * kRows;
@@ -296,50 +300,40 @@ __global__ __launch_bounds__(kThreads) void plan_device_kernel(DevicePlanArgs a)
         }
         return lo;
     };
-    // header word i of a block's (chunk's) record: 16 lanes write one each
-    auto word = [&](int i, int ad, int n, int p0, int w9, int w10) -> uint32_t {
-        const uint64_t A = a.A[ad], B = a.B[ad];
-        const int r = a.rank[ad];
-        switch (i) {
-        case 0: return uint32_t(A);
-        case 1: return uint32_t(A >> 32);
-        case 2: return uint32_t(B);
-        case 3: return uint32_t(B >> 32);
-        case 4: return __float_as_uint(a.alpha[ad] / float(r));
-        case 5: return uint32_t(r);
-        case 6: return uint32_t(n);
-        case 7: return uint32_t(p0);
-        case 8: return tb.sc[ad] & 0xFFFF;
-        case 9: return uint32_t(w9);
-        case 10: return uint32_t(w10);
-        default: return 0;
-        }
-    };
-    for (int x = wg * (kThreads / 16) + (tid >> 4); x < a.nb; x += wgs * (kThreads / 16)) {
-        const int i = tid & 15;
-        uint32_t w = 0;
+    // This workgroup's blocks x0 + i and chunks y0 + i: a thread each writes the record's head (its
+    // first 64 bytes) and leaves its rows' count, then the waves fill the places past it.
+    const int per_b = (a.nb + wgs - 1) / wgs, per_c = (a.nc + wgs - 1) / wgs;
+    const int x0 = wg * per_b, y0 = wg * per_c;
+    const bool is_chunk = tid >= kRecords;
+    const int i = is_chunk ? tid - kRecords : tid, x = (is_chunk ? y0 : x0) + i;
+    if (i < (is_chunk ? per_c : per_b) && x < (is_chunk ? a.nc : a.nb)) {
+        u32x4 w[4] = {};
         int n = 0;
-        if (x < n_blk) {
-            const int ad = find([&](int j) { return tb.blk0[j]; }, x);
-            const int q = (x - tb.blk0[ad]) * 16;
-            n = min(tb.len[ad] - q, 16);
-            w = word(i, ad, n, tb.start[ad] + q, 0, 0);
+        if (x < (is_chunk ? n_chunk : n_blk)) {
+            const int ad = is_chunk ? find([&](int j) { return int(tb.sc[j] >> 16); }, x) : find([&](int j) { return tb.blk0[j]; }, x);
+            const int c = x - (is_chunk ? int(tb.sc[ad] >> 16) : tb.blk0[ad]), rows = is_chunk ? 64 : 16;
+            const uint64_t A = a.A[ad], B = a.B[ad];
+            const int r = a.rank[ad];
+            const float scale = a.alpha[ad] / float(r);
+            n = min(tb.len[ad] - c * rows, rows);
+            w[0] = u32x4{uint32_t(A), uint32_t(A >> 32), uint32_t(B), uint32_t(B >> 32)};
+            w[1] = u32x4{__float_as_uint(scale), uint32_t(r), uint32_t(n), uint32_t(tb.start[ad] + c * rows)};
+            w[2][0] = tb.sc[ad] & 0xFFFF;
+            if (is_chunk) {
+                w[2][1] = uint32_t(tb.blk0[ad] + 4 * c);
+                w[2][2] = uint32_t((n + 15) >> 4);
+            }
         }
-        reinterpret_cast<uint32_t *>(blk + x)[i] = w;
-        if (i >= n) blk[x].rows[i] = -1;
+        auto *to = is_chunk ? reinterpret_cast<u32x4 *>(chunk + x) : reinterpret_cast<u32x4 *>(blk + x);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) to[k] = w[k];
+        rows_of[is_chunk][i] = n;
     }
-    for (int x = wg * kWaves + wave; x < a.nc; x += wgs * kWaves) {
-        uint32_t w = 0;
-        int n = 0;
-        if (x < n_chunk) {
-            const int ad = find([&](int j) { return int(tb.sc[j] >> 16); }, x);
-            const int c = x - int(tb.sc[ad] >> 16);
-            n = min(tb.len[ad] - c * 64, 64);
-            if (lane < 16) w = word(lane, ad, n, tb.start[ad] + c * 64, tb.blk0[ad] + c * 4, (n + 15) >> 4);
-        }
-        if (lane < 16) reinterpret_cast<uint32_t *>(chunk + x)[lane] = w;
-        if (lane >= n) chunk[x].rows[lane] = -1;
-    }
+    __syncthreads();
+    for (int k = tid >> 4; k < per_b && x0 + k < a.nb; k += kThreads / 16)
+        if ((tid & 15) >= rows_of[0][k]) blk[x0 + k].rows[tid & 15] = -1;
+    for (int k = wave; k < per_c && y0 + k < a.nc; k += kWaves)
+        if (lane >= rows_of[1][k]) chunk[y0 + k].rows[lane] = -1;
 
     // ---- the header
     if (wg != 0) return;
