@@ -262,7 +262,7 @@ int lora_segments_upload(const lora_segments *host, lora_segments *dev, void *st
  * The tables' contents are a precondition: addresses of matrices, 16-byte aligned.
  * Errors: LORA_ERR_ARG, LORA_ERR_RANK, LORA_ERR_ALIGN, LORA_ERR_WORKSPACE,
  * LORA_ERR_HIP. */
-#define LORA_DEVICE_PLAN_MAX_ADAPTERS 7680
+#define LORA_DEVICE_PLAN_MAX_ADAPTERS 7168
 int lora_build_segments_device(void *stream, int32_t T, int32_t n_requests, const int32_t *adapters_dev,
                                const int32_t *lengths_dev, int32_t n_adapters, const uint64_t *pool_A_dev,
                                const uint64_t *pool_B_dev, const int32_t *pool_rank_dev, const float *pool_alpha_dev,

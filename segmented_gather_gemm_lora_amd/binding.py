@@ -39,7 +39,7 @@ LORA_OP_FUSED_BLOCK_BACKWARD = 11
 LORA_SCALE_F32 = 0
 LORA_SCALE_E8M0 = 1
 SCALE_BLOCK = 128
-DEVICE_PLAN_MAX_ADAPTERS = 7680
+DEVICE_PLAN_MAX_ADAPTERS = 7168
 
 LORA_GRAD_ACCUMULATE = 1
 LORA_ADAM_F32 = 0

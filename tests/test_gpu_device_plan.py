@@ -77,7 +77,7 @@ CASES = [  # rows, requests, mean length (0: one row each, no lengths), adapters
     (1, 1, 0, 1, 0.0), (1, 1, 1, 1, 1.0), (64, 64, 0, 32, 0.0), (64, 50, 0, 5, 0.2), (100, 7, 20, 3, 0.0), (255, 40, 3, 4, 0.1),
     (256, 256, 0, 1, 0.0), (257, 257, 0, 300, 0.0), (1000, 1, 1200, 3, 0.0), (1000, 30, 50, 1000, 0.3), (2304, 260, 8, 128, 0.0),
     (4096, 4096, 0, 16, 0.05), (4096, 3000, 1, 4000, 0.0), (16384, 600, 27, 2000, 0.05), (16385, 2, 5000, 7, 0.0),
-    (20000, 20000, 0, 7680, 0.1), (65536, 65536, 0, 3, 0.0), (65536, 1500, 50, 1000, 0.0), (512, 5000, 1, 64, 0.0)]
+    (20000, 20000, 0, 7168, 0.1), (65536, 65536, 0, 3, 0.0), (65536, 1500, 50, 1000, 0.0), (512, 5000, 1, 64, 0.0)]
 
 
 @pytest.mark.parametrize("T,R,mean,N,none", CASES)
