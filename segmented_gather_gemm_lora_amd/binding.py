@@ -902,6 +902,9 @@ class DevicePlan:
         self.d = LoraSegments()
         self.made_for, self.paged, self.grads_fit = (pool.d_in, pool.d_out, pool.dtype), isinstance(pool, PagedPool), None
         _check(lora_segments_bind(self.dev.data_ptr(), self.rows, ctypes.addressof(self.d)), "lora_segments_bind")
+        self._device, self._fn, self._tables = self.dev.get_device(), load().lora_build_segments_device, None
+        self._pool_args = (pool.n_adapters, *(_ptr(t) for t in (pool.addr_A_dev, pool.addr_B_dev, pool.rank_dev, pool.alpha_dev)),
+                           self.max_rank, self.rank_multiple, self.geometry, ctypes.addressof(self.d))
 
     @property
     def seg(self) -> int:
@@ -912,17 +915,20 @@ class DevicePlan:
         int32 device tensor of the requests' rows, or None: one row each."""
         torch = _torch()
         device = torch.cuda.current_device()
-        if self.dev.get_device() != device:
-            raise ValueError("the plan is not on the current device")
-        for t in (adapters,) if lengths is None else (adapters, lengths):
-            if t.dtype is not torch.int32 or t.dim() != 1 or t.get_device() != device or t.shape != adapters.shape or (
-                    t.numel() > 1 and t.stride(0) != 1):
-                raise ValueError("adapters and lengths are adjacent int32 elements on the current device, one a request")
-        p = self.pool
-        _check(load().lora_build_segments_device(
-            _stream_handle(stream, device), self.rows, adapters.shape[0], adapters.data_ptr(), _ptr(lengths), p.n_adapters,
-            _ptr(p.addr_A_dev), _ptr(p.addr_B_dev), _ptr(p.rank_dev), _ptr(p.alpha_dev), self.max_rank,
-            self.rank_multiple, self.geometry, ctypes.addressof(self.d)), "lora_build_segments_device")
+        n, = adapters.shape
+        if self._device != device or adapters.get_device() != device:
+            raise ValueError("the plan or adapters are not on the current device")
+        if adapters.dtype is not torch.int32 or (n > 1 and adapters.stride(0) != 1):
+            raise ValueError("adapters are adjacent int32 elements, one a request")
+        at = None
+        if lengths is not None:
+            if lengths.dtype is not torch.int32 or lengths.shape != adapters.shape or lengths.get_device() != device or (
+                    n > 1 and lengths.stride(0) != 1):
+                raise ValueError("lengths are adjacent int32 elements on the current device, one a request")
+            at = lengths.data_ptr()
+        st = self._fn(_stream_handle(stream, device), self.rows, n, adapters.data_ptr(), at, *self._pool_args)
+        if st:
+            _check(st, "lora_build_segments_device")
         return self
 
     def bounds(self) -> dict:
@@ -933,17 +939,22 @@ class DevicePlan:
         """Views of the last build's tables in the device buffer (int32): counts (rows, adapted
         rows, segments, blocks, largest rank, longest segment, chunks), segments [S, 10], blocks
         [n, 32], chunks [n, 80] (the records' words), perm and segidx."""
+        if self._tables is not None:  # their places do not change from build to build
+            return self._tables
         h, w = self.bounds(), self.dev[: self.dev.numel() // 4 * 4].view(_torch().int32)
+        if h["magic"] != PLAN_MAGIC:
+            raise ValueError("nothing has been built")
 
         def at(key, n, width):
             o = h[key] // 4
             return w[o: o + n * width].view(n, width)
 
         T = h["num_tokens"]
-        return {"counts": w[1:8], "segments": at("seg_offset", h["num_segments"], SEG_DESC.itemsize // 4),
-                "blocks": at("blk_offset", h["num_blocks"], BLK_DESC.itemsize // 4),
-                "chunks": at("chunk_offset", h["num_chunks"], CHUNK_DESC.itemsize // 4),
-                "perm": w[h["perm_offset"] // 4:][:T], "segidx": w[h["segidx_offset"] // 4:][: h["num_sorted"]]}
+        self._tables = {"counts": w[1:8], "segments": at("seg_offset", h["num_segments"], SEG_DESC.itemsize // 4),
+                        "blocks": at("blk_offset", h["num_blocks"], BLK_DESC.itemsize // 4),
+                        "chunks": at("chunk_offset", h["num_chunks"], CHUNK_DESC.itemsize // 4),
+                        "perm": w[h["perm_offset"] // 4:][:T], "segidx": w[h["segidx_offset"] // 4:][: h["num_sorted"]]}
+        return self._tables
 
     def header(self) -> dict:
         """The last build's header, from the device (synchronises)."""
@@ -1197,36 +1208,32 @@ def fused_linear_e4m3(x, W0, w0_scale: float, plan: Plan, y, ws, stream=None):
            "lora_fused_linear_e4m3")
 
 
-def _scale_type(*scales) -> int:
-    torch = _torch()
-    dt = scales[0].dtype
-    if dt not in (torch.float32, torch.uint8) or any(s.dtype is not dt for s in scales):
-        raise ValueError("scales are float32, or uint8 (E8M0), and the same on both sides")
-    return LORA_SCALE_F32 if dt is torch.float32 else LORA_SCALE_E8M0
+_SCALE_TYPES = None
 
 
-def _on_device(*tensors) -> int:
-    """The current device, where all of them are."""
-    device = _torch().cuda.current_device()
-    if any(t.get_device() != device for t in tensors):
-        raise ValueError("a tensor is not on the current device")
-    return device
+def _scale_type(scales) -> int:
+    """LORA_SCALE_F32 or LORA_SCALE_E8M0 by the tensor's type."""
+    global _SCALE_TYPES
+    if _SCALE_TYPES is None:
+        torch = _torch()
+        _SCALE_TYPES = {torch.float32: LORA_SCALE_F32, torch.uint8: LORA_SCALE_E8M0}
+    kind = _SCALE_TYPES.get(scales.dtype)
+    if kind is None:
+        raise ValueError(f"scales are float32, or uint8 (E8M0), not {scales.dtype}")
+    return kind
 
 
-def _matrix(t, dtypes, rows=None, cols=None, whole=False):
-    """Refuses what the C call cannot see: another type or shape, columns that are not
-    adjacent (whole: rows neither)."""
-    if t.dim() != 2 or t.dtype not in dtypes or (rows is not None and t.shape[0] < rows) or (
-            cols is not None and t.shape[1] != cols) or (t.stride(1) != 1 and t.shape[1] > 1) or (
-            whole and not t.is_contiguous()):
-        raise ValueError(f"a matrix of {rows} x {cols} adjacent elements of {dtypes[0]} is wanted, not {tuple(t.shape)} "
-                         f"of {t.dtype} at {t.stride()}")
-    return t
-
-
-def _pitch(t) -> int:
-    """Row pitch; of a single row any, so the row's length or more."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+def _rows_of(t, dtype, rows, cols, device, least=False):
+    """Address and row pitch of a matrix of `rows` (least: or more) x `cols` adjacent elements on the
+    device; refuses what the C call cannot see.  The pitch of a single row is any."""
+    n, d = t.shape
+    ld, inner = t.stride()
+    if (n != rows and not (least and n > rows)) or d != cols or t.dtype is not dtype or (inner != 1 and d > 1):
+        raise ValueError(f"{rows} rows of {cols} adjacent elements of {dtype} are wanted, not {tuple(t.shape)} of {t.dtype} "
+                         f"at strides {t.stride()}")
+    if t.get_device() != device:
+        raise ValueError(f"a tensor of {tuple(t.shape)} is not on the current device")
+    return t.data_ptr(), ld if n > 1 else max(ld, d)
 
 
 def quantize_e4m3(x, codes, scales, block_rows: int = 1, stream=None):
@@ -1235,44 +1242,58 @@ def quantize_e4m3(x, codes, scales, block_rows: int = 1, stream=None):
     scales [row blocks, groups]).  The scales' type says which: float32, or uint8 for
     powers of two (E8M0)."""
     torch = _torch()
+    device = torch.cuda.current_device()
     rows, cols = x.shape
-    _matrix(x, (torch.bfloat16, torch.float32))
-    _matrix(codes, (torch.uint8,), rows, cols)
-    groups = (cols + SCALE_BLOCK - 1) // SCALE_BLOCK
-    want = (groups, rows) if block_rows == 1 else ((rows + SCALE_BLOCK - 1) // SCALE_BLOCK, groups)
-    _matrix(scales, (torch.float32, torch.uint8), *want)
-    device = _on_device(x, codes, scales)
-    _check(load().lora_quantize_e4m3(_stream_handle(stream, device), LORA_BF16 if x.dtype is torch.bfloat16 else LORA_F32,
-                                     x.data_ptr(), _pitch(x), rows, cols, block_rows, _scale_type(scales),
-                                     codes.data_ptr(), _pitch(codes), scales.data_ptr(), _pitch(scales)),
-           "lora_quantize_e4m3")
+    dt = x.dtype
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise ValueError(f"x is bf16 or fp32, not {dt}")
+    groups = (cols + 127) // SCALE_BLOCK
+    px, ldx = _rows_of(x, dt, rows, cols, device)
+    pc, ldc = _rows_of(codes, torch.uint8, rows, cols, device)
+    kind = _scale_type(scales)
+    if block_rows == 1:
+        ps, lds = _rows_of(scales, scales.dtype, groups, rows, device)
+    else:
+        ps, lds = _rows_of(scales, scales.dtype, (rows + 127) // SCALE_BLOCK, groups, device)
+    st = load().lora_quantize_e4m3(_stream_handle(stream, device), LORA_BF16 if dt is torch.bfloat16 else LORA_F32, px, ldx,
+                                   rows, cols, block_rows, kind, pc, ldc, ps, lds)
+    if st:
+        _check(st, "lora_quantize_e4m3")
 
 
-def _block_base(W, w_scales):
+def _block_base(W, w_scales, device):
+    """d_out, d_in, addresses of codes and scales, and the scales' type of a block-scaled base."""
     torch = _torch()
     d_out, d_in = W.shape
-    _matrix(W, (torch.uint8,), whole=True)
-    _matrix(w_scales, (torch.float32, torch.uint8), (d_out + SCALE_BLOCK - 1) // SCALE_BLOCK,
-            (d_in + SCALE_BLOCK - 1) // SCALE_BLOCK, whole=True)
-    return d_out, d_in
+    kind = _scale_type(w_scales)
+    if not W.is_contiguous() or not w_scales.is_contiguous():
+        raise ValueError("W and its scales are contiguous")
+    pW, _ = _rows_of(W, torch.uint8, d_out, d_in, device)
+    ps, _ = _rows_of(w_scales, w_scales.dtype, (d_out + 127) // SCALE_BLOCK, (d_in + 127) // SCALE_BLOCK, device)
+    return d_out, d_in, pW, ps, kind
 
 
 def linear_e4m3_block(x, x_scales, W, w_scales, y, ws, stream=None):
     """y = (x_scales x) (w_scales W)^T for E4M3 codes x [T, d_in] (scales [groups, T]) and W
-    [d_out, d_in] (scales for each 128 x 128 block); y bf16 or fp32, overwritten.  ws: a
-    workspace of LORA_OP_LINEAR_BLOCK."""
+    [d_out, d_in] (scales for each 128 x 128 block, of the same type); y bf16 or fp32,
+    overwritten.  ws: a workspace of LORA_OP_LINEAR_BLOCK."""
     torch = _torch()
-    d_out, d_in = _block_base(W, w_scales)
+    device = torch.cuda.current_device()
+    d_out, d_in, pW, pws, kind = _block_base(W, w_scales, device)
     T = x.shape[0]
-    _matrix(x, (torch.uint8,), None, d_in)
-    _matrix(x_scales, (torch.float32, torch.uint8), w_scales.shape[1], T)
-    _matrix(y, (torch.bfloat16, torch.float32), T, d_out)
-    device = _on_device(x, x_scales, W, w_scales, y, ws)
-    _check(load().lora_linear_e4m3_block(
-        _stream_handle(stream, device), T, x.data_ptr(), _pitch(x), x_scales.data_ptr(), _pitch(x_scales), d_in,
-        W.data_ptr(), w_scales.data_ptr(), _scale_type(x_scales, w_scales), d_out,
-        LORA_BF16 if y.dtype is torch.bfloat16 else LORA_F32, y.data_ptr(), _pitch(y), ws.data_ptr(),
-        ws.numel() * ws.element_size()), "lora_linear_e4m3_block")
+    dt = y.dtype
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise ValueError(f"y is bf16 or fp32, not {dt}")
+    px, ldx = _rows_of(x, torch.uint8, T, d_in, device)
+    ps, lds = _rows_of(x_scales, w_scales.dtype, (d_in + 127) // SCALE_BLOCK, T, device)
+    py, ldy = _rows_of(y, dt, T, d_out, device)
+    if ws.get_device() != device:
+        raise ValueError("the workspace is not on the current device")
+    st = load().lora_linear_e4m3_block(_stream_handle(stream, device), T, px, ldx, ps, lds, d_in, pW, pws, kind, d_out,
+                                       LORA_BF16 if dt is torch.bfloat16 else LORA_F32, py, ldy, ws.data_ptr(),
+                                       ws.numel() * ws.element_size())
+    if st:
+        _check(st, "lora_linear_e4m3_block")
 
 
 def fused_linear_e4m3_block(x, W0, w_scales, plan, y, ws, stream=None):
@@ -1280,19 +1301,21 @@ def fused_linear_e4m3_block(x, W0, w_scales, plan, y, ws, stream=None):
     quantized by the call, in groups of 128 columns with scales of the same type; the
     correction is x's own.  plan: a Plan or a DevicePlan; ws: of LORA_OP_FUSED_BLOCK."""
     torch = _torch()
-    d_out, d_in = _block_base(W0, w_scales)
+    device = torch.cuda.current_device()
+    d_out, d_in, pW, pws, kind = _block_base(W0, w_scales, device)
     T = plan.h.batch_tokens
-    _matrix(x, (torch.bfloat16,), T, d_in)
-    _matrix(y, (torch.bfloat16,), T, d_out)
+    px, ldx = _rows_of(x, torch.bfloat16, T, d_in, device, least=True)
+    py, ldy = _rows_of(y, torch.bfloat16, T, d_out, device, least=True)
     if plan.paged:
         raise ValueError("the plan's adapters are paged; this call takes whole matrices")
     if plan.made_for is not None and plan.made_for != (d_in, d_out, "bf16"):
         raise ValueError(f"a call of ({d_in}, {d_out}, bf16) on a plan of adapters of {plan.made_for}")
-    device = _on_device(x, W0, w_scales, y, ws, plan.dev)
-    _check(load().lora_fused_linear_e4m3_block(
-        _stream_handle(stream, device), x.data_ptr(), _pitch(x), d_in, W0.data_ptr(), w_scales.data_ptr(),
-        _scale_type(w_scales), d_out, plan.seg, y.data_ptr(), _pitch(y), ws.data_ptr(), ws.numel() * ws.element_size()),
-        "lora_fused_linear_e4m3_block")
+    if ws.get_device() != device or plan.dev.get_device() != device:
+        raise ValueError("the plan or the workspace is not on the current device")
+    st = load().lora_fused_linear_e4m3_block(_stream_handle(stream, device), px, ldx, d_in, pW, pws, kind, d_out, plan.seg, py,
+                                             ldy, ws.data_ptr(), ws.numel() * ws.element_size())
+    if st:
+        _check(st, "lora_fused_linear_e4m3_block")
 
 
 def _gradient_rows(dtype: str, tokens: int, others, rows):
@@ -1394,14 +1417,14 @@ def fused_linear_e4m3_block_backward(x, W0, w_scales, dy, plan: Plan, grads: Opt
     """Gradients of fused_linear_e4m3_block: dx = Q(dy) W0 + u A (overwritten, every row; Q quantizes
     groups of 128 columns with scales of the base's type), and the adapters' gradients as in
     sgmv_backward (grads None: not wanted; x may then be None; what is refused is the same)."""
-    d_out, d_in = _block_base(W0, w_scales)
+    d_out, d_in, pW, pws, kind = _block_base(W0, w_scales, _torch().cuda.current_device())
     tA, tB, n = (None, None, 0) if grads is None else (grads.addr_A_dev, grads.addr_B_dev, grads.n_adapters)
     device, (pdy, lddy, px, ldx, pdx, lddx) = _gradient_rows(
-        "bf16", plan.h.batch_tokens, (plan.dev, ws, W0, w_scales) if grads is None else (plan.dev, ws, W0, w_scales, tA, tB),
+        "bf16", plan.h.batch_tokens, (plan.dev, ws) if grads is None else (plan.dev, ws, tA, tB),
         ((dy, d_out), (x, d_in), (dx, d_in)))
     _fits_plan(plan, d_in, d_out, "bf16", grads, device)
     _check(load().lora_fused_linear_e4m3_block_backward(
-        _stream_handle(stream, device), px, ldx, d_in, W0.data_ptr(), w_scales.data_ptr(), _scale_type(w_scales), pdy, lddy,
+        _stream_handle(stream, device), px, ldx, d_in, pW, pws, kind, pdy, lddy,
         d_out, plan.seg, _ptr(tA), _ptr(tB), n, LORA_GRAD_ACCUMULATE if accumulate else 0, pdx, lddx, ws.data_ptr(),
         ws.numel() * ws.element_size()), "lora_fused_linear_e4m3_block_backward")
 
