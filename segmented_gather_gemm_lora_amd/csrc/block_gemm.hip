@@ -1020,17 +1020,18 @@ int launch_fused_linear_block(hipStream_t s, const ShrinkArgs &sa, const void *W
     q.scale_type = scale_type;
     q.scales = base + w.scales;
     q.lds = w.lds;
-    int st = launch_quantize(s, q);
-    if (st) return st;
+    int st = LORA_OK;
     uint16_t *vh = reinterpret_cast<uint16_t *>(base + w.vh);
     a.ldh = vh_pitch(max_rank);
     a.nsl = 0;
     if (p.h->num_sorted > 0) {
         a.v = static_cast<const float *>(ws);
-        st = T <= kFew ? launch_sgmv_shrink_split(s, sa, p, static_cast<float *>(ws), &a.ldw, &a.sl_stride, &a.nsl)
-                       : launch_v_halves(s, sa, p, ws, vh, a.ldh);
+        st = T <= kFew ? launch_sgmv_shrink_quantize(s, sa, p, static_cast<float *>(ws), &a.ldw, &a.sl_stride, &a.nsl, q)
+                       : launch_v_halves(s, sa, p, ws, vh, a.ldh, 0.f, &q);
         if (st) return st;
         if (a.nsl > kMaxSlices) return fail(LORA_ERR_ARG, "block product: %d d_in slices > %d", a.nsl, kMaxSlices);
+    } else if ((st = launch_quantize(s, q))) {
+        return st;
     }
     a.x = static_cast<const uint8_t *>(q.codes);
     a.ldx = w.ldq;

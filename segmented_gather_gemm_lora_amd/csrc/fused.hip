@@ -579,12 +579,13 @@ size_t fused_workspace_bytes(int32_t T, int32_t d_in, int32_t max_rank)
 }
 
 int launch_v_halves(hipStream_t s, const ShrinkArgs &sa, const PlanView &p, void *ws, uint16_t *vh, int64_t ldh,
-                    float wdiv)
+                    float wdiv, const QuantCall *quant)
 {
     float *v = static_cast<float *>(ws);
     int64_t ldw = 0, sl_stride = 0;
     int nsl = 0;
-    const int st = launch_sgmv_shrink_split(s, sa, p, v, &ldw, &sl_stride, &nsl);
+    const int st = quant ? launch_sgmv_shrink_quantize(s, sa, p, v, &ldw, &sl_stride, &nsl, *quant)
+                         : launch_sgmv_shrink_split(s, sa, p, v, &ldw, &sl_stride, &nsl);
     if (st) return st;
     if (nsl > kMaxSlicesFused) return fail(LORA_ERR_ARG, "fused layer: %d d_in slices > %d", nsl, kMaxSlicesFused);
     const int Tp = p.h->num_sorted;

@@ -203,6 +203,9 @@ struct QuantCall {
     int64_t lds;
 };
 int launch_quantize(hipStream_t s, const QuantCall &q);
+// launch_sgmv_shrink_split, and the quantization of x's rows, in one launch where the shapes allow it.
+int launch_sgmv_shrink_quantize(hipStream_t s, const ShrinkArgs &sa, const PlanView &p, float *ws, int64_t *ldw,
+                                int64_t *sl_stride, int *nsl, const QuantCall &q);
 
 // y = (sx qx) (sw qw)^T
 struct LinearBlockCall {
@@ -228,9 +231,9 @@ int launch_fused_block_backward(hipStream_t s, const BackwardArgs &b, const void
                                 const PlanView &p, void *ws);
 // The shrink of the plan's rows into ws (combined_workspace_bytes), then scale_s v in
 // two bf16 halves, for 16 ranks each 16 hi and 16 lo, ldh apart from row to row (plan
-// order; zeros past the adapted rows).  The value is divided by wdiv unless that is 0.
+// order; zeros past the adapted rows).  The value is divided by wdiv unless that is 0.  quant: done along with the shrink.
 int launch_v_halves(hipStream_t s, const ShrinkArgs &sa, const PlanView &p, void *ws, uint16_t *vh, int64_t ldh,
-                    float wdiv = 0.f);
+                    float wdiv = 0.f, const QuantCall *quant = nullptr);
 
 // Workgroups that one launch may have: the runtime counts threads in 32 bits.
 constexpr int64_t most_workgroups(int threads) { return 0xFFFFFFFFll / threads; }

@@ -34,6 +34,7 @@
 // Latency: every load a workgroup needs depends on at most one earlier load
 // (the block descriptor, or the decode ids), so a kernel costs about two
 // memory round trips plus its streaming time.
+#include "e4m3.h"
 #include "internal.h"
 
 #include <cstring>
@@ -42,36 +43,16 @@
 namespace lora {
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float floatx4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
 constexpr int kRows = LORA_PLAN_ROW_BLOCK; // rows per block (MFMA M)
 // s_waitcnt immediate for vmcnt(0) with the other counters left alone (gfx9
 // encoding: vmcnt in bits 3:0 and 15:14, expcnt 6:4, lgkmcnt 11:8)
 
 constexpr int kExpandCols = 256;          // output columns per expand workgroup (4 waves x 64)
 
-__device__ __forceinline__ float bf16_to_f32(uint32_t h) { return __uint_as_float(h << 16); }
-
 // Adapter addresses come from descriptors and pool tables, so the compiler
 // cannot tell that they point to global memory and would use flat loads (which
 // also occupy the LDS/scalar counter and force extra waits).  Say so.
-template <typename T> using global_ptr = const __attribute__((address_space(1))) T *;
-template <typename T> __device__ __forceinline__ global_ptr<T> as_global(const void *p)
-{
-    return (global_ptr<T>)(p);
-}
-
-// two fp32 -> packed bf16 (lo in bits 15:0) with one v_cvt_pk_bf16_f32: round to
-// nearest even, NaN stays a (quiet) NaN
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
-{
-    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-    const bf16x2_t v = {static_cast<__bf16>(lo), static_cast<__bf16>(hi)};
-    return __builtin_bit_cast(uint32_t, v);
-}
+template <typename T> using global_ptr = gptr<T>;
 
 // Where adapter elements live.  The kernels address A_i and B_i as element
 // offsets from the adapter's table entry:
@@ -1014,6 +995,35 @@ void sgmv_shrink_kernel(const void *__restrict__ x, int64_t ldx, int d_in,
 {
     sgmv_shrink_item<DT, VEC, W, NSTEP, RT>(x, ldx, d_in, blks, nblk, kc, slice_len, out, ldo, sl_stride, blockIdx.x,
                                             mem);
+}
+
+// The shrink, and in workgroups behind it the quantization of the same x, of which it needs
+// nothing: one launch of both instead of two after each other (bf16 rows of whole 16-byte pieces).
+struct QuantAlong {
+    QuantArgs q;
+    unsigned first, gx; // first workgroup, workgroups along the rows
+    int groups;
+    bool e8;
+};
+template <int NSTEP, int RT>
+__global__ __launch_bounds__(256) void sgmv_shrink_quantize_kernel(const void *__restrict__ x, int64_t ldx, int d_in,
+                                                                   const lora_blk_desc *__restrict__ blks, int nblk, int kc,
+                                                                   int slice_len, float *__restrict__ out, int64_t ldo,
+                                                                   int64_t sl_stride, const QuantAlong along)
+{
+    if (blockIdx.x < along.first) {
+        sgmv_shrink_item<LORA_BF16, true, 4, NSTEP, RT>(x, ldx, d_in, blks, nblk, kc, slice_len, out, ldo, sl_stride,
+                                                        blockIdx.x, DenseMem{});
+        return;
+    }
+    const unsigned b = blockIdx.x - along.first, bx = b % along.gx, by = b / along.gx;
+    if (along.groups == 4) {
+        if (along.e8) quantize_rows<LORA_BF16, true, 4>(along.q, bx, by);
+        else quantize_rows<LORA_BF16, false, 4>(along.q, bx, by);
+    } else {
+        if (along.e8) quantize_rows<LORA_BF16, true, 1>(along.q, bx, by);
+        else quantize_rows<LORA_BF16, false, 1>(along.q, bx, by);
+    }
 }
 
 template <int DT, bool VECY, int UPT, class M, int MAXNCH>
@@ -2330,6 +2340,41 @@ int launch_sgmv_shrink_split(hipStream_t s, const ShrinkArgs &sa, const PlanView
                              int64_t *sl_stride, int *nsl)
 {
     return shrink_split(s, sa, p, ws, ldw, sl_stride, nsl, DenseMem{});
+}
+
+int launch_sgmv_shrink_quantize(hipStream_t s, const ShrinkArgs &sa, const PlanView &p, float *ws, int64_t *ldw,
+                                int64_t *sl_stride, int *nsl, const QuantCall &q)
+{
+    const int nblk = p.h->num_blocks;
+    QuantAlong along{};
+    along.q = quant_args(q);
+    along.groups = quant_groups(along.q);
+    along.e8 = q.scale_type == LORA_SCALE_E8M0;
+    along.gx = unsigned((int64_t(q.rows) + 15) / 16);
+    const int64_t gy = (int64_t(along.q.qcols) / kScaleGroup + along.groups - 1) / along.groups;
+    const Split sp = choose_split(sa.d_in, nblk, sa.dtype);
+    const int64_t first = (int64_t(nblk) * sp.kc + 7) / 8 * 8, grid = first + gy * along.gx;
+    if (nblk == 0 || sa.dtype != LORA_BF16 || !sa.vec || !q.pad || grid > most_workgroups(256)) {
+        const int st = launch_quantize(s, q);
+        return st ? st : shrink_split(s, sa, p, ws, ldw, sl_stride, nsl, DenseMem{});
+    }
+    along.first = unsigned(first);
+    *ldw = (p.h->max_rank + 3) / 4 * 4;
+    *sl_stride = int64_t(p.h->num_sorted) * *ldw;
+    *nsl = sp.kc;
+    const int rt = rank_tiles(p.h->max_rank);
+    const dim3 g(static_cast<unsigned>(grid));
+    auto go = [&](auto kernel) {
+        launch_kernel(kernel, g, dim3(256), 0, s, sa.x, sa.ldx, sa.d_in, plan_blocks(p), nblk, sp.kc, sp.slice_len, ws, *ldw,
+                      *sl_stride, along);
+    };
+    // the forms of the shrink alone
+    if (sp.nstep == 2 && rt == 1) go(sgmv_shrink_quantize_kernel<2, 1>);
+    else if (sp.nstep == 2 && rt == 2) go(sgmv_shrink_quantize_kernel<2, 2>);
+    else if (rt == 1) go(sgmv_shrink_quantize_kernel<1, 1>);
+    else if (rt == 2) go(sgmv_shrink_quantize_kernel<1, 2>);
+    else go(sgmv_shrink_quantize_kernel<1, 4>);
+    return check_launch("sgmv shrink and quantize");
 }
 
 int launch_sgmv(hipStream_t s, const ShrinkArgs &sa, const ExpandArgs &ea, const PlanView &p, void *ws, int32_t *ctl)
