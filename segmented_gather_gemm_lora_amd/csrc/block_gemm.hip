@@ -440,12 +440,14 @@ template <class S, bool E8, Form F> struct Tile {
         int wb, xb[TM];
         float f[TM];
     };
-    // W's scale of block kt: fp32 bits, or the aligned word that holds its byte.
-    __device__ __forceinline__ uint32_t wscale(int kt) const
+    // W's scales of the 64 stages from kt, one a lane (fp32 bits or a byte).  A scalar load in each
+    // stage would make every wait for LDS in it a wait for that load too (they return out of
+    // order): 0.7 us a stage.
+    __device__ __forceinline__ uint32_t wscales(int kt) const
     {
-        const int64_t at = sw0 + (kt < k1 ? kt : k1 - 1) * sw1;
-        if constexpr (!E8) return ((cptr<uint32_t>)(a.sw))[at];
-        return *(cptr<uint32_t>)((reinterpret_cast<uintptr_t>(a.sw) + size_t(at)) & ~uintptr_t(3));
+        const int64_t at = sw0 + (kt + lane < k1 ? kt + lane : k1 - 1) * sw1;
+        if constexpr (E8) return as_global<uint8_t>(a.sw)[at];
+        return as_global<uint32_t>(a.sw)[at];
     }
     __device__ __forceinline__ Scales scales(int kt, uint32_t word) const
     {
@@ -453,7 +455,7 @@ template <class S, bool E8, Form F> struct Tile {
         const char *ss = stage(kt) + S::kWBytes + S::kXBytes;
         const int r0 = 16 * TM * wm + m;
         if constexpr (E8) {
-            r.wb = int(word >> (8 * uint32_t((reinterpret_cast<uintptr_t>(a.sw) + size_t(sw0 + kt * sw1)) & 3)) & 255);
+            r.wb = int(word);
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
                 r.xb[i] = *reinterpret_cast<const uint8_t *>(ss + r0 + 16 * i);
@@ -538,8 +540,10 @@ void block_gemm_kernel(BlockArgs a)
         for (int i = 0; i < TM; ++i) acc[t][i] = floatx4{};
 #pragma unroll
     for (int s = 0; s < S::kStages - 1; ++s) T.issue(T.k0 + s);
-    uint32_t word = T.wscale(T.k0);
+    uint32_t ws = 0;
     for (int kt = T.k0; kt < T.k1; ++kt) {
+        if (((kt - T.k0) & 63) == 0) ws = T.wscales(kt);
+        const uint32_t word = uint32_t(__builtin_amdgcn_readlane(int(ws), (kt - T.k0) & 63));
         // this wave's loads of stage kt have landed and its reads of stage kt - 1 are
         // done; past the barrier that holds for every wave
         __builtin_amdgcn_s_waitcnt(wait_vm_lds0(S::kDma * (S::kStages - 2)));
@@ -553,7 +557,6 @@ void block_gemm_kernel(BlockArgs a)
         const i32x8 w1 = T.wfrag(st, 1);
         // the next stage's loads go out while these reads come back
         T.issue(kt + S::kStages - 1);
-        word = T.wscale(kt + 1);
         if constexpr (F == kF32) {
             exact_block<TN, TM>(xf, sc.f, acc, [&](int t) { return t ? T.wfrag(st, t) : w0; });
         } else if constexpr (E8) {
@@ -662,17 +665,20 @@ template <int TN, int TM, bool E8, Form F> __global__ __launch_bounds__(64 * kFe
     for (int t = 0; t < TN; ++t)
 #pragma unroll
         for (int i = 0; i < TM; ++i) acc[t][i] = floatx4{};
+    // W's scales of the wave's next 64 blocks, one a lane
+    uint32_t wsv = 0;
+    auto load_scales = [&](int j) {
+        const int kb = block_of(j + lane);
+        const int64_t at = int64_t(nb) * blocks + (kb < blocks ? kb : 0);
+        if constexpr (E8) wsv = as_global<uint8_t>(a.sw)[at];
+        else wsv = as_global<uint32_t>(a.sw)[at];
+    };
     auto multiply = [&](int j, Operands &o) {
         const int kb = block_of(j);
         if (kb >= blocks) return; // wave-uniform
-        const int64_t at = int64_t(nb) * blocks + kb;
         i32x8 xf[TM];
         float f[TM];
-        int wb = 0;
-        if constexpr (E8) {
-            const uintptr_t p = reinterpret_cast<uintptr_t>(a.sw) + size_t(at);
-            wb = int(*(cptr<uint32_t>)(p & ~uintptr_t(3)) >> (8 * (p & 3)) & 255);
-        }
+        const int wb = __builtin_amdgcn_readlane(int(wsv), j & 63); // fp32 bits, or a byte
         const int k = kb * kG + 16 * g;
 #pragma unroll
         for (int i = 0; i < TM; ++i) { // past k x's codes are zeros
@@ -680,7 +686,7 @@ template <int TN, int TM, bool E8, Form F> __global__ __launch_bounds__(64 * kFe
             if (k + 64 >= a.k) o.x[i].hi = u32x4{};
             xf[i] = operand(o.x[i]);
             if constexpr (E8) f[i] = F == kF32 ? e8m0(wb) * e8m0(int(o.sx[i])) : 0.f;
-            else f[i] = ((cptr<float>)(a.sw))[at] * __uint_as_float(o.sx[i]);
+            else f[i] = __uint_as_float(uint32_t(wb)) * __uint_as_float(o.sx[i]);
         }
         if constexpr (F == kF32) {
             exact_block<TN, TM>(xf, f, acc, [&](int t) { return operand(o.w[t]); });
@@ -703,6 +709,7 @@ template <int TN, int TM, bool E8, Form F> __global__ __launch_bounds__(64 * kFe
     };
     const int mine = wave < blocks ? (blocks - wave + kFewWaves - 1) / kFewWaves : 0; // blocks of this wave
     Operands ring[D];
+    load_scales(0);
 #pragma unroll
     for (int d = 0; d < D; ++d) load_block(d, ring[d]);
 
@@ -807,6 +814,7 @@ template <int TN, int TM, bool E8, Form F> __global__ __launch_bounds__(64 * kFe
         load_steps();
     }
     for (int j = 0; j < mine; j += D) {
+        if (j && (j & 63) == 0) load_scales(j);
 #pragma unroll
         for (int d = 0; d < D; ++d) {
             multiply(j + d, ring[d]);
