@@ -442,7 +442,7 @@ template <class S, bool E8, Form F> struct Tile {
     };
     // W's scales of the 64 stages from kt, one a lane (fp32 bits or a byte).  A scalar load in each
     // stage would make every wait for LDS in it a wait for that load too (they return out of
-    // order): 0.7 us a stage.
+    // order): fp32 results of 65 x 1024, summed axis 4096, 53 -> 42 us; one row, 12288 columns, 12.5 -> 11.1.
     __device__ __forceinline__ uint32_t wscales(int kt) const
     {
         const int64_t at = sw0 + (kt + lane < k1 ? kt + lane : k1 - 1) * sw1;
@@ -915,23 +915,43 @@ template <class S, Form F> int go(hipStream_t s, BlockArgs &a, bool e8, int spli
     return LORA_OK;
 }
 
+template <class S> int64_t tiles_of(int32_t T, int32_t n) { return (int64_t(T) + S::kBM - 1) / S::kBM * ((int64_t(n) + S::kBN - 1) / S::kBN); }
+
+// The tile of a product of T rows and n columns.  A round of Large, Medium and Small tiles
+// over the chip takes about 1.6, 0.8 and 0.5 us for each block of the summed axis (Medium
+// and Small 0.9 and 0.8 with two workgroups on a CU), so the smallest tile whose workgroups
+// run all at once is taken, two of them on a CU, and the largest where none does.  Summed
+// axis 4096, rows x columns, us of Small / Medium / Large:
+//    128 x  4096   17 / 26 / 51      517 x 12288   58 /  40 /  62     4096 x 4096  131 /  97 /  80
+//   1024 x  4096   28 / 30 / 57     1024 x 12288   90 /  73 /  69    2304 x 12288    - / 171 / 160
+// An fp32 result takes four times the matrix instructions and widens each code that it reads, which
+// larger tiles do less often; Large ones do not fit the registers.  Small / Medium, 517 x 1531 (summed axis 1008)
+// 12 / 16, 517 x 4096 61 / 50, 1024 x 4096 67 / 60.
+enum Size { kSmall, kMedium, kLarge };
+inline Size size_of(int32_t T, int32_t n, bool f32)
+{
+    if (tiles_of<Small>(T, n) <= (f32 ? 256 : 512)) return kSmall;
+    return f32 || tiles_of<Medium>(T, n) <= 512 ? kMedium : kLarge;
+}
+
 template <Form F> int launch_product(hipStream_t s, BlockArgs &a, bool e8)
 {
     if (a.T <= kFew) return go_few<F == kFusedAnyRank ? kFused : F>(s, a, e8);
-    // fp32 results hold the rows' widened operands too: tiles of 128 x 128
-    if (F != kF32 && int64_t(a.T + 255) / 256 * ((a.n + 255) / 256) >= 128) return go<Large, F>(s, a, e8);
-    return go<Medium, F>(s, a, e8);
+    const Size size = size_of(a.T, a.n, F == kF32);
+    if constexpr (F != kF32)
+        if (size == kLarge) return go<Large, F>(s, a, e8);
+    return size == kMedium ? go<Medium, F>(s, a, e8) : go<Small, F>(s, a, e8);
 }
 
 // Tile and splits of the rows' gradient: as many splits of the summed axis as fill the
 // chip once, with at least 4 blocks each.
 struct GradientPlan {
-    bool large;
+    Size size;
     int splits, per;
     GradientPlan(int32_t T, int32_t d_in, int32_t d_out)
     {
-        large = int64_t(T + 255) / 256 * ((d_in + 255) / 256) >= 128;
-        const int64_t tiles = large ? int64_t(T + 255) / 256 * ((d_in + 255) / 256) : int64_t(T + 63) / 64 * ((d_in + 127) / 128);
+        size = size_of(T, d_in, false);
+        const int64_t tiles = size == kLarge ? tiles_of<Large>(T, d_in) : size == kMedium ? tiles_of<Medium>(T, d_in) : tiles_of<Small>(T, d_in);
         const int blocks = (d_out + kG - 1) / kG;
         const int most = int(std::max<int64_t>(1, std::min<int64_t>({256 / tiles, blocks / 4, 16})));
         per = (blocks + most - 1) / most;
@@ -1111,7 +1131,9 @@ int launch_fused_block_backward(hipStream_t s, const BackwardArgs &b, const void
     a.y = base + w.parts;
     a.per = g.per;
     const bool e8 = scale_type == LORA_SCALE_E8M0;
-    st = g.large ? go<Large, kGradient>(s, a, e8, g.splits) : go<Small, kGradient>(s, a, e8, g.splits);
+    if (g.size == kLarge) st = go<Large, kGradient>(s, a, e8, g.splits);
+    else if (g.size == kMedium) st = go<Medium, kGradient>(s, a, e8, g.splits);
+    else st = go<Small, kGradient>(s, a, e8, g.splits);
     if (st) return st;
     return launch_dx_join(s, b, p, ws, reinterpret_cast<const float *>(base + w.parts), g.splits);
 }
