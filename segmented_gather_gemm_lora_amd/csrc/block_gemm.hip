@@ -114,20 +114,26 @@ template <int TN> __device__ __forceinline__ int wave_col(int m, int t) { return
 // kRing (every rank is a multiple of 8): B_s comes by direct loads through a ring of
 // steps in LDS that is the wave's own, several steps ahead: short segments are chains of
 // loads that depend on nothing but their segment, and one step at a time took over 2 us.
-template <int TN, int TM, bool kRing, int kBytes>
+template <int TN, int TM, int SR, bool kRing, int kBytes>
 __device__ __forceinline__ void correction(const BlockArgs &a, int Tp, int pw0, int cw0, int lane, char *mine, uint32_t mine_lds,
                                            floatx4 (&acc)[TN][TM])
 {
     constexpr int kSlot = 512 * TN, kLoads = TN / 2, kDepth = kBytes / kSlot < 4 ? kBytes / kSlot : 4;
     static_assert(kDepth >= 2 && 16 * TM <= 64, "ring, segments of a wave");
     const int m = lane & 15, g = lane >> 4;
-    const int plast = (pw0 + 16 * TM < Tp ? pw0 + 16 * TM : Tp) - 1;
-    const int s0 = uniform(a.segidx[pw0]), n = uniform(a.segidx[plast]) - s0 + 1;
-    // lane l: the wave's segment l
-    const lora_seg_desc *d = a.seg + s0 + (lane < n ? lane : n - 1);
+    // lane l: the segment of row l % 16 of the wave's row tile l / 16, if that is the first of the
+    // wave's rows in it
+    const int mt = lane >> 4 < TM ? lane >> 4 : TM - 1, mp = pw0 + SR * mt + m;
+    const lora_seg_desc *d = a.seg + as_global<int32_t>(a.segidx)[mp < Tp ? mp : Tp - 1];
     const uint64_t dB = d->B;
     const uint32_t Blo = uint32_t(dB), Bhi = uint32_t(dB >> 32);
-    const int start = d->start, len = d->len, rank = lane < n ? d->rank : 0;
+    const int start = d->start, len = d->len, drank = d->rank;
+    const bool first = mp == start || (m == 0 && (mt == 0 || start >= mp - SR + 16));
+    const int rank = first && mp < Tp && lane < 16 * TM ? drank : 0;
+    // Here, and below, what the compiler loaded has landed before the ring's loads, which it does not
+    // count: else it would wait for all of them in every step (2304 rows, 288 of them by 128
+    // adapters: 62 us of correction).
+    __builtin_amdgcn_s_waitcnt(wait_vm(0));
     auto lane_of = [](int v, int l) { return __builtin_amdgcn_readlane(v, l); };
     auto base_of = [&](int l) {
         return reinterpret_cast<const void *>(uint64_t(uint32_t(lane_of(int(Blo), l))) | uint64_t(uint32_t(lane_of(int(Bhi), l))) << 32);
@@ -175,9 +181,10 @@ __device__ __forceinline__ void correction(const BlockArgs &a, int Tp, int pw0, 
             vq = q;
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
-                const int p = pw0 + 16 * i + m;
+                const int p = pw0 + SR * i + m;
                 v[i] = *(gptr<u32x4>)(as_global<uint16_t>(a.vh) + int64_t(p < Tp ? p : Tp - 1) * a.ldh + 32 * q + 8 * g);
             }
+            if constexpr (kRing) __builtin_amdgcn_s_waitcnt(wait_vm(0));
         }
         const int r = lane_of(rank, l), p0 = lane_of(start, l), p1 = p0 + lane_of(len, l);
         const int jj = 16 * q + 8 * (g & 1);
@@ -214,15 +221,21 @@ __device__ __forceinline__ void correction(const BlockArgs &a, int Tp, int pw0, 
         }
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-            const int t0 = pw0 + 16 * i;
+            const int t0 = pw0 + SR * i;
             if (p0 >= t0 + 16 || p1 <= t0) continue; // wave-uniform
             const bool in = t0 + m >= p0 && t0 + m < p1;
             const bf16x8 vi = __builtin_bit_cast(bf16x8, v[i]);
+            constexpr int kAtOnce = TN < 4 ? TN : 4; // so many results wait for their choice together
 #pragma unroll
-            for (int t = 0; t < TN; ++t) {
-                const floatx4 y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[t], vi, acc[t][i], 0, 0, 0);
+            for (int t = 0; t < TN; t += kAtOnce) {
+                floatx4 y[kAtOnce];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[t][i][e] = in ? y[e] : acc[t][i][e];
+                for (int h = 0; h < kAtOnce; ++h) y[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[t + h], vi, acc[t + h][i], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int h = 0; h < kAtOnce; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[t + h][i][e] = in ? y[h][e] : acc[t + h][i][e];
             }
         }
     }
@@ -316,6 +329,9 @@ template <class S, bool E8, Form F> struct Tile {
     // (64 i + lane) / units-of-a-row, slot (64 i + lane) % units-of-a-row, which holds unit
     // slot ^ (row % 8).
     static constexpr int kWUnits = WT ? S::kBN / 16 : 8;
+    // Row tile i of a wave is kStrips * i below its first: neighbouring rows, which may be many short
+    // segments, are every wave's.
+    static constexpr int kStrips = 16 * S::WM;
     const BlockArgs &a;
     char *lds;
     uint32_t lds0;
@@ -348,7 +364,7 @@ template <class S, bool E8, Form F> struct Tile {
         blocks = (a.k + kG - 1) / kG; // of the summed axis
         k0 = WT ? split * a.per : 0;
         k1 = WT ? min(k0 + a.per, blocks) : blocks;
-        pw0 = m0 + 16 * TM * wm;
+        pw0 = m0 + 16 * wm;
         cw0 = n0 + 16 * TN * wn;
         // the wave's block of columns: those past n repeat the last ones and are not stored
         const int nb = (cw0 < a.n ? cw0 : a.n - 1) / kG;
@@ -433,7 +449,7 @@ template <class S, bool E8, Form F> struct Tile {
             return frag(st + (16 * (TN * wn + t) + m) * kG);
         }
     }
-    __device__ __forceinline__ i32x8 xfrag(const char *st, int i) const { return frag(st + S::kWBytes + (16 * (TM * wm + i) + m) * kG); }
+    __device__ __forceinline__ i32x8 xfrag(const char *st, int i) const { return frag(st + S::kWBytes + (16 * wm + kStrips * i + m) * kG); }
 
     // The scales of block kt: E8M0 bytes, or the products of both sides' scales.
     struct Scales {
@@ -453,18 +469,18 @@ template <class S, bool E8, Form F> struct Tile {
     {
         Scales r;
         const char *ss = stage(kt) + S::kWBytes + S::kXBytes;
-        const int r0 = 16 * TM * wm + m;
+        const int r0 = 16 * wm + m;
         if constexpr (E8) {
             r.wb = int(word);
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
-                r.xb[i] = *reinterpret_cast<const uint8_t *>(ss + r0 + 16 * i);
+                r.xb[i] = *reinterpret_cast<const uint8_t *>(ss + r0 + kStrips * i);
                 if (F == kF32) r.f[i] = e8m0(r.wb) * e8m0(r.xb[i]);
             }
         } else {
             const float ws = __uint_as_float(word);
 #pragma unroll
-            for (int i = 0; i < TM; ++i) r.f[i] = ws * *reinterpret_cast<const float *>(ss + 4 * (r0 + 16 * i));
+            for (int i = 0; i < TM; ++i) r.f[i] = ws * *reinterpret_cast<const float *>(ss + 4 * (r0 + kStrips * i));
         }
         return r;
     }
@@ -497,7 +513,7 @@ template <class S, bool E8, Form F> struct Tile {
             constexpr int kBytes = S::kStages * S::kStageBytes / S::kWaves / 1024 * 1024;
             const int Tp = a.tp_dev ? uniform(*a.tp_dev) : a.Tp;
             if (pw0 < Tp)
-                correction<TN, TM, F == kFused, kBytes>(a, Tp, pw0, cw0, lane, lds + wave * kBytes, lds0 + uint32_t(wave) * kBytes, acc);
+                correction<TN, TM, kStrips, F == kFused, kBytes>(a, Tp, pw0, cw0, lane, lds + wave * kBytes, lds0 + uint32_t(wave) * kBytes, acc);
         }
     }
 
@@ -505,7 +521,7 @@ template <class S, bool E8, Form F> struct Tile {
     {
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-            const int p = pw0 + 16 * i + m;
+            const int p = pw0 + kStrips * i + m;
             if (p >= a.T) continue;
             if constexpr (WT) { // lane: columns 16 t + 4 g .. + 3
                 float *o = static_cast<float *>(a.y) + (int64_t(split) * a.T + p) * a.n + cw0 + 4 * g;
