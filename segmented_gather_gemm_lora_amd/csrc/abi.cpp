@@ -1035,7 +1035,7 @@ static int check_block_base(int64_t rows, int64_t ldx, int32_t d_in, const void 
     if (!aligned16(W)) return fail(LORA_ERR_ALIGN, "W is not 16-byte aligned");
     if (!scale_aligned(w_scales, scale_type)) return fail(LORA_ERR_ALIGN, "W's scales are not aligned to their size");
     // rows are addressed with 32-bit byte offsets
-    if ((rows + 1) * ldx >= int64_t(1) << 32 || (int64_t(d_out) + 1) * d_in >= int64_t(1) << 32)
+    if (ldx >= int64_t(1) << 31 || (rows + 1) * ldx >= int64_t(1) << 32 || (int64_t(d_out) + 1) * d_in >= int64_t(1) << 32)
         return fail(LORA_ERR_ARG, "the codes of x or W span 4 GiB or more");
     return LORA_OK;
 }

@@ -42,8 +42,7 @@
 // fp32 gradients keep fp32 accuracy; for dx, which is rounded to bf16, as two
 // (16 significant bits, as in the forward's expand).  fp32 calls multiply
 // exactly.
-#include "device.h"
-#include "internal.h"
+#include "e4m3.h"
 
 #include <algorithm>
 #include <type_traits>
@@ -470,8 +469,7 @@ __device__ __forceinline__ bool shrink_unit(const BwdArgs &a, int units, int *sc
 // 517 rows of ranks to 100, 22 us, 10 so); its waves share the long axis.  Four rank
 // tiles: 2 waves per SIMD, so that the loads ahead stay in registers (left to
 // itself the compiler makes 4 fit: mixed ranks 65 us, 58 so).
-template <int DT, bool VEC, int RT>
-__global__ __launch_bounds__(kShrinkWaves * 64) __attribute__((amdgpu_waves_per_eu(2, RT == 4 ? 2 : 8))) void bwd_shrink_kernel(BwdArgs a)
+template <int DT, bool VEC, int RT> __device__ __forceinline__ void shrink_block(const BwdArgs &a)
 {
     constexpr int W = kShrinkWaves, NP = RT == 1 ? 2 : 1;
     constexpr int kTile = NP * ShrinkTile<DT, RT>::kBytes;
@@ -513,6 +511,20 @@ __global__ __launch_bounds__(kShrinkWaves * 64) __attribute__((amdgpu_waves_per_
         const float v = j < r ? sum * scale : 0.f;
         store_uv<DT>(a, side, p, t, jm, v);
     }
+}
+template <int DT, bool VEC, int RT>
+__global__ __launch_bounds__(kShrinkWaves * 64) __attribute__((amdgpu_waves_per_eu(2, RT == 4 ? 2 : 8))) void bwd_shrink_kernel(BwdArgs a)
+{
+    shrink_block<DT, VEC, RT>(a);
+}
+// And dy's rows quantized by further workgroups, a launch less and dy read from memory once: 64 rows of
+// 4096 columns 6.6 us (6.8 and 3.2 in two), 4096 rows 37 (24.4 and 17.9).
+template <int RT>
+__global__ __launch_bounds__(kShrinkWaves * 64) __attribute__((amdgpu_waves_per_eu(2, RT == 4 ? 2 : 8)))
+void bwd_shrink_quantize_kernel(BwdArgs a, QuantAlong along)
+{
+    if (blockIdx.x < along.first) shrink_block<LORA_BF16, true, RT>(a);
+    else quantize_along<kShrinkWaves / 4>(along, blockIdx.x);
 }
 
 // The same for many long segments (bf16, VEC, ranks above 32, multiples of 8): a
@@ -1236,21 +1248,44 @@ Layout layout_of(int32_t rows, int32_t d_in, int32_t d_out, int32_t max_rank)
     return l;
 }
 
-template <int DT, bool VEC> void run_shrink(hipStream_t s, const BwdArgs &a, unsigned nside, bool ranks8)
+int checked(const char *what)
 {
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? LORA_OK : fail(LORA_ERR_HIP, "%s launch: %s", what, hipGetErrorString(e));
+}
+
+template <int DT, bool VEC> int run_shrink(hipStream_t s, const BwdArgs &a, unsigned nside, bool ranks8, const QuantCall *quant)
+{
+    int st = LORA_OK;
     // The ring where 64-row workgroups fill the chip and are mostly whole: d 4096,
     // ring / blocks of 16 rows, us.  Rank 64: 4096 rows 41 / 41, 8192 54 / 66, 16384
     // 98 / 125, 32768 159 / 231; rank 32: 44 / 42, 84 / 80, 146 / 151 from 8192 rows;
     // rank 16: 78 / 67 for 16384.
     if (DT == LORA_BF16 && VEC && ranks8 && a.nt > 2 && int64_t(a.nchunk) * nside >= 256 && a.Tp / a.nchunk >= 32) {
         const dim3 grid((unsigned(a.nchunk) + 7) / 8 * nside * a.groups * 8 + 8), block(256);
+        if (quant) st = launch_quantize(s, *quant);
+        if (st) return st;
         launch_kernel(bwd_shrink_ring_kernel, grid, block, 0, s, a);
-        return;
+        return checked("backward shrink");
     }
     const dim3 grid((unsigned(a.nblk) + 7) / 8 * nside * a.groups * 8 + 8), block(kShrinkWaves * 64);
+    if (quant) {
+        int64_t both;
+        const QuantAlong along = quant_along(*quant, grid.x, kShrinkWaves / 4, &both);
+        if (DT == LORA_BF16 && VEC && quant->pad && both <= most_workgroups(kShrinkWaves * 64)) {
+            const dim3 all{unsigned(both)};
+            if (a.nt <= 1) launch_kernel(bwd_shrink_quantize_kernel<1>, all, block, 0, s, a, along);
+            else if (a.nt <= 2) launch_kernel(bwd_shrink_quantize_kernel<2>, all, block, 0, s, a, along);
+            else launch_kernel(bwd_shrink_quantize_kernel<4>, all, block, 0, s, a, along);
+            return checked("backward shrink and quantize");
+        }
+        st = launch_quantize(s, *quant);
+        if (st) return st;
+    }
     if (a.nt <= 1) launch_kernel(bwd_shrink_kernel<DT, VEC, 1>, grid, block, 0, s, a);
     else if (a.nt <= 2) launch_kernel(bwd_shrink_kernel<DT, VEC, 2>, grid, block, 0, s, a);
     else launch_kernel(bwd_shrink_kernel<DT, VEC, 4>, grid, block, 0, s, a);
+    return checked("backward shrink");
 }
 template <int DT, bool VEC> void run_out(hipStream_t s, const BwdArgs &a, dim3 grid)
 {
@@ -1258,12 +1293,6 @@ template <int DT, bool VEC> void run_out(hipStream_t s, const BwdArgs &a, dim3 g
     if (a.nt <= 1) launch_kernel(bwd_out_kernel<DT, VEC, 1>, grid, block, 0, s, a);
     else if (a.nt <= 2) launch_kernel(bwd_out_kernel<DT, VEC, 2>, grid, block, 0, s, a);
     else launch_kernel(bwd_out_kernel<DT, VEC, 4>, grid, block, 0, s, a);
-}
-
-int checked(const char *what)
-{
-    const hipError_t e = hipGetLastError();
-    return e == hipSuccess ? LORA_OK : fail(LORA_ERR_HIP, "%s launch: %s", what, hipGetErrorString(e));
 }
 
 } // namespace
@@ -1312,7 +1341,7 @@ static BwdArgs make_args(const BackwardArgs &b, const PlanView &p, const Layout 
 }
 
 int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p, void *ws, const uint16_t **u_rows,
-                         int64_t *ldu)
+                         int64_t *ldu, const QuantCall *quant)
 {
     const lora_plan_header *h = p.h;
     const Layout l = layout_of(h->num_sorted, b.d_in, b.d_out, h->max_rank);
@@ -1354,11 +1383,11 @@ int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p
     const bool bf16 = b.dtype == LORA_BF16;
     const bool vec = b.vec_x && b.vec_dy && (!a.dx || b.vec_dx);
     const unsigned nside = a.sides == 3 ? 2 : 1;
-    if (bf16 && vec) run_shrink<LORA_BF16, true>(s, a, nside, ranks8);
-    else if (bf16) run_shrink<LORA_BF16, false>(s, a, nside, ranks8);
-    else if (vec) run_shrink<LORA_F32, true>(s, a, nside, ranks8);
-    else run_shrink<LORA_F32, false>(s, a, nside, ranks8);
-    int st = checked("backward shrink");
+    int st;
+    if (bf16 && vec) st = run_shrink<LORA_BF16, true>(s, a, nside, ranks8, quant);
+    else if (bf16) st = run_shrink<LORA_BF16, false>(s, a, nside, ranks8, quant);
+    else if (vec) st = run_shrink<LORA_F32, true>(s, a, nside, ranks8, quant);
+    else st = run_shrink<LORA_F32, false>(s, a, nside, ranks8, quant);
     if (st || ngrad + ndx == 0) return st;
     const dim3 grid{unsigned(ngrad + ndx)};
     if (bf16 && vec) run_out<LORA_BF16, true>(s, a, grid);

@@ -135,8 +135,10 @@ __device__ __forceinline__ void correction(const BlockArgs &a, int Tp, int pw0, 
     // adapters: 62 us of correction).
     __builtin_amdgcn_s_waitcnt(wait_vm(0));
     auto lane_of = [](int v, int l) { return __builtin_amdgcn_readlane(v, l); };
-    auto base_of = [&](int l) {
-        return reinterpret_cast<const void *>(uint64_t(uint32_t(lane_of(int(Blo), l))) | uint64_t(uint32_t(lane_of(int(Bhi), l))) << 32);
+    const int c00 = cw0 < a.n ? cw0 : a.n - 1; // columns are counted from here: B may span more than 4 GiB
+    auto base_of = [&](int l, int r) {
+        const uint64_t B = uint64_t(uint32_t(lane_of(int(Blo), l))) | uint64_t(uint32_t(lane_of(int(Bhi), l))) << 32;
+        return reinterpret_cast<const uint16_t *>(B) + int64_t(c00) * r;
     };
     auto next = [&](int &q, uint64_t &left) { // the next step (16 ranks q, segment), or -1
         while (left == 0) {
@@ -154,7 +156,7 @@ __device__ __forceinline__ void correction(const BlockArgs &a, int Tp, int pw0, 
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) { // LDS row 32 k + lane / 2 of a step, half lane % 2
         const int rho = 32 * k + (lane >> 1), c = cw0 + wave_col<TN>(rho & 15, rho >> 4);
-        col[k] = c < a.n ? c : a.n - 1;
+        col[k] = (c < a.n ? c : a.n - 1) - c00;
     }
     auto issue = [&] {
         const int l = next(pq, pleft);
@@ -163,7 +165,7 @@ __device__ __forceinline__ void correction(const BlockArgs &a, int Tp, int pw0, 
             return;
         }
         const int r = lane_of(rank, l), half = 16 * pq + 8 < r ? lane & 1 : 0;
-        const void *B = base_of(l);
+        const void *B = base_of(l, r);
         const uint32_t to = mine_lds + uint32_t(issued % kDepth) * kSlot;
 #pragma unroll
         for (int k = 0; k < kLoads; ++k) dma16s(B, uint32_t(col[k]) * uint32_t(2 * r) + uint32_t(32 * pq + 16 * half), to + 1024 * k);
@@ -204,11 +206,11 @@ __device__ __forceinline__ void correction(const BlockArgs &a, int Tp, int pw0, 
             __builtin_amdgcn_s_waitcnt(kWaitLds0); // read before the place is filled again
             if (more) issue();
         } else {
-            const gptr<uint16_t> B = as_global<uint16_t>(base_of(l));
+            const gptr<uint16_t> B = as_global<uint16_t>(base_of(l, r));
 #pragma unroll
             for (int t = 0; t < TN; ++t) {
                 const int c = cw0 + wave_col<TN>(m, t);
-                const gptr<uint16_t> row = B + int64_t(c < a.n ? c : a.n - 1) * r;
+                const gptr<uint16_t> row = B + ((c < a.n ? c : a.n - 1) - c00) * r;
                 u32x4 u;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -1112,13 +1114,6 @@ int launch_fused_block_backward(hipStream_t s, const BackwardArgs &b, const void
     const GradientPlan g(T, b.d_in, b.d_out);
     char *base = static_cast<char *>(ws);
     int st;
-    if (h->num_sorted > 0) { // the adapters' gradients, and u
-        BackwardArgs q = b;
-        q.dx = nullptr;
-        const uint16_t *ur;
-        int64_t ldu;
-        if ((st = launch_sgmv_backward(s, q, p, ws, &ur, &ldu))) return st;
-    }
     QuantCall q{};
     q.dtype = LORA_BF16;
     q.x = b.dy;
@@ -1133,7 +1128,16 @@ int launch_fused_block_backward(hipStream_t s, const BackwardArgs &b, const void
     q.scale_type = scale_type;
     q.scales = base + w.scales;
     q.lds = w.lds;
-    if ((st = launch_quantize(s, q))) return st;
+    if (h->num_sorted > 0) { // the adapters' gradients, and u
+        BackwardArgs adapters = b;
+        adapters.dx = nullptr;
+        const uint16_t *ur;
+        int64_t ldu;
+        st = launch_sgmv_backward(s, adapters, p, ws, &ur, &ldu, &q);
+    } else {
+        st = launch_quantize(s, q);
+    }
+    if (st) return st;
     BlockArgs a{};
     a.x = static_cast<const uint8_t *>(q.codes);
     a.ldx = w.ldq;

@@ -132,11 +132,15 @@ __device__ __forceinline__ void store8(uint8_t *p, int c, int cols, u32x2 w)
         if (c + i < cols) p[c + i] = uint8_t(w[i >> 2] >> (8 * (i & 3)));
 }
 
-// 16 rows (from 16 bx) x U groups (from U by) by a workgroup of 256 threads.
-template <int DT, bool E8, int U> __device__ __forceinline__ void quantize_rows(const QuantArgs &a, unsigned bx, unsigned by)
+// 16 rows (from 16 bx) x U groups (from U by) by 256 threads; a workgroup of NW times as many
+// takes the groups from U NW by.
+template <int DT, bool E8, int U, int NW = 1>
+__device__ __forceinline__ void quantize_rows(const QuantArgs &a, unsigned bx, unsigned by)
 {
-    __shared__ uint32_t sc_lds[U][16];
-    const int tid = threadIdx.x, l = tid & 15, i = tid >> 4;
+    __shared__ uint32_t sc_all[NW][U][16];
+    const int part = threadIdx.x >> 8, tid = threadIdx.x & 255, l = tid & 15, i = tid >> 4;
+    auto &sc_lds = sc_all[part];
+    by = by * NW + part;
     const int64_t p = int64_t(bx) * 16 + i;
     const int groups = (a.cols + kScaleGroup - 1) / kScaleGroup;
     int64_t row = p < a.rows ? p : -1;
@@ -160,7 +164,7 @@ template <int DT, bool E8, int U> __device__ __forceinline__ void quantize_rows(
         if (l == 0) sc_lds[u][i] = sc.stored;
     }
     __syncthreads();
-    const int u = tid >> 4, g = int(by) * U + u;
+    const int u = i, g = int(by) * U + u;
     const int64_t q = int64_t(bx) * 16 + l;
     if (u < U && g < groups && q < a.rows) {
         if constexpr (E8) static_cast<uint8_t *>(a.scales)[g * a.lds + q] = uint8_t(sc_lds[u][l]);
@@ -189,6 +193,38 @@ inline int quant_groups(const QuantArgs &a)
 {
     const int64_t rt = (int64_t(a.rows) + 15) / 16, qg = (a.qcols + kScaleGroup - 1) / kScaleGroup;
     return rt * qg >= 4 * 512 ? 4 : 1;
+}
+
+// Rows that another launch of bf16 rows quantizes along: its workgroups from `first` on, each of 256 NW threads.
+struct QuantAlong {
+    QuantArgs q;
+    unsigned first, gx; // first workgroup, workgroups along the rows
+    int groups;
+    bool e8;
+};
+template <int NW> __device__ __forceinline__ void quantize_along(const QuantAlong &along, unsigned workgroup)
+{
+    const unsigned b = workgroup - along.first, bx = b % along.gx, by = b / along.gx;
+    if (along.groups == 4) {
+        if (along.e8) quantize_rows<LORA_BF16, true, 4, NW>(along.q, bx, by);
+        else quantize_rows<LORA_BF16, false, 4, NW>(along.q, bx, by);
+    } else {
+        if (along.e8) quantize_rows<LORA_BF16, true, 1, NW>(along.q, bx, by);
+        else quantize_rows<LORA_BF16, false, 1, NW>(along.q, bx, by);
+    }
+}
+// q behind `first` workgroups of the launch; *grid: workgroups of both.
+inline QuantAlong quant_along(const QuantCall &q, int64_t first, int nw, int64_t *grid)
+{
+    QuantAlong along{};
+    along.q = quant_args(q);
+    along.groups = quant_groups(along.q);
+    along.e8 = q.scale_type == LORA_SCALE_E8M0;
+    along.gx = unsigned((int64_t(q.rows) + 15) / 16);
+    along.first = unsigned(first);
+    const int64_t each = int64_t(along.groups) * nw, qg = along.q.qcols / kScaleGroup;
+    *grid = first + (qg + each - 1) / each * along.gx;
+    return along;
 }
 
 } // namespace

@@ -179,8 +179,10 @@ size_t sgmv_backward_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out, int
 // (bf16: operands of 512 elements per 16 positions and 16 ranks, lane 16 g +
 // position % 16 of 8 ranks each, g = 0, 1: hi parts, 2, 3: lo; ldu elements from
 // 16 positions to the next).
+// quant: rows of dy to quantize too, in the first launch where the shapes allow it.
+struct QuantCall;
 int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p, void *ws,
-                         const uint16_t **u_rows = nullptr, int64_t *ldu = nullptr);
+                         const uint16_t **u_rows = nullptr, int64_t *ldu = nullptr, const QuantCall *quant = nullptr);
 // dx = the sum of `splits` parts [T][d_in] (fp32, plan rows) + u A, every row; after
 // launch_sgmv_backward with u_rows on the same workspace (bf16).
 int launch_dx_join(hipStream_t s, const BackwardArgs &b, const PlanView &p, void *ws, const float *parts, int splits);

@@ -999,12 +999,6 @@ void sgmv_shrink_kernel(const void *__restrict__ x, int64_t ldx, int d_in,
 
 // The shrink, and in workgroups behind it the quantization of the same x, of which it needs
 // nothing: one launch of both instead of two after each other (bf16 rows of whole 16-byte pieces).
-struct QuantAlong {
-    QuantArgs q;
-    unsigned first, gx; // first workgroup, workgroups along the rows
-    int groups;
-    bool e8;
-};
 template <int NSTEP, int RT>
 __global__ __launch_bounds__(256) void sgmv_shrink_quantize_kernel(const void *__restrict__ x, int64_t ldx, int d_in,
                                                                    const lora_blk_desc *__restrict__ blks, int nblk, int kc,
@@ -1016,14 +1010,7 @@ __global__ __launch_bounds__(256) void sgmv_shrink_quantize_kernel(const void *_
                                                         blockIdx.x, DenseMem{});
         return;
     }
-    const unsigned b = blockIdx.x - along.first, bx = b % along.gx, by = b / along.gx;
-    if (along.groups == 4) {
-        if (along.e8) quantize_rows<LORA_BF16, true, 4>(along.q, bx, by);
-        else quantize_rows<LORA_BF16, false, 4>(along.q, bx, by);
-    } else {
-        if (along.e8) quantize_rows<LORA_BF16, true, 1>(along.q, bx, by);
-        else quantize_rows<LORA_BF16, false, 1>(along.q, bx, by);
-    }
+    quantize_along<1>(along, blockIdx.x);
 }
 
 template <int DT, bool VECY, int UPT, class M, int MAXNCH>
@@ -2346,19 +2333,13 @@ int launch_sgmv_shrink_quantize(hipStream_t s, const ShrinkArgs &sa, const PlanV
                                 int64_t *sl_stride, int *nsl, const QuantCall &q)
 {
     const int nblk = p.h->num_blocks;
-    QuantAlong along{};
-    along.q = quant_args(q);
-    along.groups = quant_groups(along.q);
-    along.e8 = q.scale_type == LORA_SCALE_E8M0;
-    along.gx = unsigned((int64_t(q.rows) + 15) / 16);
-    const int64_t gy = (int64_t(along.q.qcols) / kScaleGroup + along.groups - 1) / along.groups;
     const Split sp = choose_split(sa.d_in, nblk, sa.dtype);
-    const int64_t first = (int64_t(nblk) * sp.kc + 7) / 8 * 8, grid = first + gy * along.gx;
+    int64_t grid;
+    const QuantAlong along = quant_along(q, (int64_t(nblk) * sp.kc + 7) / 8 * 8, 1, &grid);
     if (nblk == 0 || sa.dtype != LORA_BF16 || !sa.vec || !q.pad || grid > most_workgroups(256)) {
         const int st = launch_quantize(s, q);
         return st ? st : shrink_split(s, sa, p, ws, ldw, sl_stride, nsl, DenseMem{});
     }
-    along.first = unsigned(first);
     *ldw = (p.h->max_rank + 3) / 4 * 4;
     *sl_stride = int64_t(p.h->num_sorted) * *ldw;
     *nsl = sp.kc;
