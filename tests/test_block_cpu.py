@@ -82,11 +82,11 @@ def test_backward():
     need = B.lora_workspace_bytes(B.LORA_OP_FUSED_BLOCK_BACKWARD, 4, 256, 104, 16)
     assert need > 0
     good = dict(stream=None, x=P, ldx=256, d_in=256, W=P, ws=P, scale_type=F32, dy=P, lddy=104, d_out=104, seg=plan.dev(), gA=P,
-                gB=P, n=2, flags=0, dx=P, lddx=256, work=P, work_bytes=need)
+                gB=P, n=2, flags=0, dx=P + (1 << 24), lddx=256, work=P, work_bytes=need)
     refused("lora_fused_linear_e4m3_block_backward", good, [
         (dict(seg=None), ARG), (dict(scale_type=3), DTYPE), (dict(x=None), ARG), (dict(dy=None), ARG), (dict(dx=None), ARG),
         (dict(W=None), ARG), (dict(ws=None), ARG), (dict(ldx=248), ARG), (dict(lddy=96), ARG), (dict(lddx=248), ARG), (dict(n=1), ADAPTER),
-        (dict(d_in=248), ALIGN), (dict(x=P + 8), ALIGN), (dict(dy=P + 8), ALIGN), (dict(dx=P + 8), ALIGN), (dict(lddy=108), ALIGN),
+        (dict(d_in=248), ALIGN), (dict(x=P + 8), ALIGN), (dict(dy=P + 8), ALIGN), (dict(dx=P + 8 + (1 << 24)), ALIGN), (dict(dx=P), ARG), (dict(lddy=108), ALIGN),
         (dict(lddx=260), ALIGN), (dict(W=P + 4), ALIGN), (dict(ws=P + 2), ALIGN), (dict(work=None), WORKSPACE),
         (dict(work_bytes=need - 1), WORKSPACE), (dict(work=P + 8), ALIGN), (dict(flags=1 << 20), ARG), (dict(seg=plan.dev(buf=None)), ARG)])
 
