@@ -1233,7 +1233,7 @@ def _rows_of(t, dtype, rows, cols, device, least=False):
                          f"at strides {t.stride()}")
     if t.get_device() != device:
         raise ValueError(f"a tensor of {tuple(t.shape)} is not on the current device")
-    return t.data_ptr(), ld if n > 1 else max(ld, d)
+    return t.data_ptr(), ld if n > 1 else (d + 15) // 16 * 16
 
 
 def quantize_e4m3(x, codes, scales, block_rows: int = 1, stream=None):
