@@ -61,6 +61,7 @@ struct BlockArgs {
     int64_t ldy;
     int vec_y; // whole aligned 16-byte pieces of y
     int tiles_m, tiles_n;
+    int whole; // tiles that are not halved
     // the correction
     const int32_t *segidx;
     const lora_seg_desc *seg;
@@ -87,6 +88,8 @@ template <int TN_, int TM_, int WN_, int WM_, int STAGES> struct Shape {
     static_assert(kStages * kStageBytes <= 160 * 1024, "LDS budget");
     static_assert(kDma * (kStages - 2) <= 63, "vmcnt range");
     static_assert(16 * TN <= kG && kG % (16 * TN) == 0, "a wave's columns lie in one block");
+    static constexpr bool kHalved = TN == 8; // its last tiles may be halves
+    typedef Shape<TN / 2, TM, WN, WM, STAGES> Half;
 };
 
 __device__ __forceinline__ void dma4(const void *g, uint32_t lds_byte)
@@ -345,7 +348,8 @@ template <class S, bool E8, Form F> struct Tile {
     int64_t sstep, sw0, sw1;
     int u0, u1;
 
-    __device__ __forceinline__ Tile(const BlockArgs &args, char *l) : a(args), lds(l)
+    // tile: its number; half: columns it starts behind its first
+    __device__ __forceinline__ Tile(const BlockArgs &args, char *l, int tile, int cols, int half) : a(args), lds(l)
     {
         const int tid = threadIdx.x;
         lane = tid & 63;
@@ -355,13 +359,10 @@ template <class S, bool E8, Form F> struct Tile {
         wn = wave / S::WM;
         wm = wave % S::WM;
         lds0 = uint32_t(uintptr_t((__attribute__((address_space(3))) char *)(lds)));
-        // row tiles fastest, then columns, then splits; a contiguous run of tiles for each XCD
-        const int nwg = gridDim.x;
-        int tile = blockIdx.x;
-        if ((nwg & 7) == 0) tile = (tile & 7) * (nwg >> 3) + (tile >> 3);
+        // row tiles fastest, then columns, then splits
         m0 = tile % a.tiles_m * S::kBM;
         tile /= a.tiles_m;
-        n0 = tile % a.tiles_n * S::kBN;
+        n0 = tile % a.tiles_n * cols + half;
         split = tile / a.tiles_n;
         blocks = (a.k + kG - 1) / kG; // of the summed axis
         k0 = WT ? split * a.per : 0;
@@ -544,13 +545,10 @@ template <class S, bool E8, Form F> struct Tile {
     }
 };
 
-template <class S, bool E8, Form F>
-__global__ __launch_bounds__(S::kThreads) __attribute__((amdgpu_waves_per_eu(S::kWavesPerSimd, S::kWavesPerSimd)))
-void block_gemm_kernel(BlockArgs a)
+template <class S, bool E8, Form F> __device__ __forceinline__ void multiply_tile(const BlockArgs &a, char *lds, int tile, int cols, int half)
 {
     constexpr int TN = S::TN, TM = S::TM;
-    __shared__ __attribute__((aligned(1024))) char lds[S::kStages * S::kStageBytes];
-    Tile<S, E8, F> T(a, lds);
+    Tile<S, E8, F> T(a, lds, tile, cols, half);
     floatx4 acc[TN][TM];
 #pragma unroll
     for (int t = 0; t < TN; ++t)
@@ -604,6 +602,27 @@ void block_gemm_kernel(BlockArgs a)
     __builtin_amdgcn_s_waitcnt(wait_vm(0));
     T.correct(acc);
     T.store(acc);
+}
+
+// A contiguous run of n tiles for each XCD.
+__device__ __forceinline__ int own_run(int b, int n) { return (n & 7) == 0 ? (b & 7) * (n >> 3) + (b >> 3) : b; }
+
+template <class S, bool E8, Form F>
+__global__ __launch_bounds__(S::kThreads) __attribute__((amdgpu_waves_per_eu(S::kWavesPerSimd, S::kWavesPerSimd)))
+void block_gemm_kernel(BlockArgs a)
+{
+    __shared__ __attribute__((aligned(1024))) char lds[S::kStages * S::kStageBytes];
+    const int b = blockIdx.x;
+    if constexpr (S::kHalved) {
+        if (b >= a.whole) {
+            const int c = own_run(b - a.whole, int(gridDim.x) - a.whole);
+            multiply_tile<typename S::Half, E8, F>(a, lds, a.whole + c / 2, S::kBN, c % 2 * (S::kBN / 2));
+            return;
+        }
+        multiply_tile<S, E8, F>(a, lds, own_run(b, a.whole), S::kBN, 0);
+    } else {
+        multiply_tile<S, E8, F>(a, lds, own_run(b, gridDim.x), S::kBN, 0);
+    }
 }
 
 // Up to 64 rows: bound by reading W once.  A workgroup has 16 TN columns and all rows; its 8 waves
@@ -925,7 +944,12 @@ template <class S, Form F> int go(hipStream_t s, BlockArgs &a, bool e8, int spli
     a.tiles_n = (a.n + S::kBN - 1) / S::kBN;
     const int64_t tiles = int64_t(a.tiles_m) * a.tiles_n * splits;
     if (tiles > most_workgroups(S::kThreads)) return fail(LORA_ERR_ARG, "block product: too many tiles");
-    const dim3 grid{unsigned(tiles)}, block(S::kThreads);
+    // Where whole rounds of workgroups (one on a CU) leave at most half a round of tiles, those
+    // are halves of 128 columns (summed axis 4096, fp32 scales / E8M0, us: 4096 x 4352 128 -> 113 / 115 -> 104,
+    // 2304 x 8192 130 -> 115 / 112 -> 108, 4096 x 14336 340 -> 330 / 265 -> 259).
+    const int rest = S::kHalved && tiles > 256 && splits == 1 && tiles % 256 <= 128 ? int(tiles % 256) : 0;
+    a.whole = int(tiles) - rest;
+    const dim3 grid{unsigned(tiles + rest)}, block(S::kThreads);
     if (e8) launch_kernel(block_gemm_kernel<S, true, F>, grid, block, 0, s, a);
     else launch_kernel(block_gemm_kernel<S, false, F>, grid, block, 0, s, a);
     const hipError_t e = hipGetLastError();

@@ -112,7 +112,7 @@ def check(got, ref, bound, what):
 
 SHAPES = [(1, 16, 1), (1, 4096, 130), (2, 128, 128), (3, 144, 100), (15, 256, 272), (16, 1024, 384), (17, 1008, 1531),
           (33, 400, 129), (64, 2048, 512), (65, 2048, 512), (100, 272, 700), (128, 128, 4096), (200, 512, 300),
-          (257, 1040, 520), (517, 1008, 1531), (1030, 640, 2064), (2049, 256, 4100)]
+          (257, 1040, 520), (517, 1008, 1531), (1030, 640, 2064), (2049, 256, 4100), (2100, 144, 8300)]
 
 
 @pytest.mark.parametrize("kind", ["f32", "e8m0"])
@@ -195,7 +195,8 @@ def run_fused(prob, W, ws, plan, T=None):
 
 
 FUSED = [(1, 128, 256, [16]), (8, 256, 264, [8, 8]), (64, 1024, 512, [16] * 8), (65, 528, 136, [3, 17]), (130, 400, 1000, [8, 64, 1]),
-         (300, 512, 2048, [16, 32, 5, 100]), (1000, 1024, 2304, [16] * 20), (2100, 384, 4096, [8, 16, 256])]
+         (300, 512, 2048, [16, 32, 5, 100]), (1000, 1024, 2304, [16] * 20), (2100, 384, 4096, [8, 16, 256]), (2100, 144, 8304, [8, 16] * 40),
+         (2100, 144, 8304, [5, 17])]
 
 
 @pytest.mark.parametrize("kind", ["f32", "e8m0"])
@@ -255,7 +256,7 @@ def grad_reference(prob, W, ws, kind, x, dy):
 
 
 GRADS = [(1, 128, 128, [16]), (40, 256, 264, [8, 8, 3]), (64, 1024, 512, [16] * 8), (65, 528, 136, [3, 17]), (130, 400, 1000, [8, 64, 1]),
-         (300, 512, 2049, [16, 32, 5, 100]), (64, 256, 8192, [16] * 3), (2100, 4096, 384, [8, 16, 256]), (4200, 2064, 250, [16] * 4)]
+         (300, 512, 2049, [16, 32, 5, 100]), (64, 256, 8192, [16] * 3), (2100, 4096, 384, [8, 16, 256]), (4200, 2064, 250, [16] * 4), (4200, 4368, 130, [8, 16])]
 
 
 @pytest.mark.parametrize("kind", ["f32", "e8m0"])
