@@ -710,15 +710,14 @@ int lora_fused_linear_e4m3(void *stream, const void *x, int64_t ldx, int32_t d_i
  *   scales  block_rows 1: [groups, lds], groups = ceil(cols / 128), lds >= rows: a
  *           row of `rows` scales for each group of columns (the product reads them
  *           so); block_rows 128: [ceil(rows / 128), lds], lds >= groups
- * cols <= 2^22.  One launch; x may not overlap codes or scales.
+ * rows <= 2^27, cols <= 2^22.  One launch; x may not overlap codes or scales.
  * Errors: LORA_ERR_ARG, LORA_ERR_DTYPE, LORA_ERR_ALIGN, LORA_ERR_HIP. */
 int lora_quantize_e4m3(void *stream, int dtype, const void *x, int64_t ldx, int32_t rows, int32_t cols,
                        int32_t block_rows, int scale_type, void *codes, int64_t ldq, void *scales, int64_t lds);
 
 /* y[t, n] = sum_b x_scales[b, t] w_scales[n / 128, b] sum_{k in block b} x[t, k] W[n, k],
  * overwriting y: the block's inner sums on 8-bit MFMA, everything in fp32, rounded once.
- *   x         codes [T, ldx], 16-byte aligned rows; x_scales [groups, lds], lds >= T, 4-byte
- *             aligned rows
+ *   x         codes [T, ldx], 16-byte aligned rows; x_scales [groups, lds], lds >= T
  *   W         codes [d_out, d_in], row pitch d_in, 16-byte aligned, d_in % 16 == 0;
  *             w_scales [ceil(d_out / 128), groups], contiguous
  *   y         [T, ldy] of out_dtype (bf16 or fp32), any alignment

@@ -1002,7 +1002,8 @@ int lora_quantize_e4m3(void *stream, int dtype, const void *x, int64_t ldx, int3
     if ((st = check_scale_type(scale_type))) return st;
     if (block_rows != 1 && block_rows != LORA_SCALE_BLOCK)
         return fail(LORA_ERR_ARG, "block_rows %d is not 1 or %d", block_rows, LORA_SCALE_BLOCK);
-    if (rows < 0 || cols < 1 || cols > (1 << 22)) return fail(LORA_ERR_ARG, "rows %d < 0 or cols %d outside [1, 2^22]", rows, cols);
+    if (rows < 0 || rows > (1 << 27) || cols < 1 || cols > (1 << 22))
+        return fail(LORA_ERR_ARG, "rows %d outside [0, 2^27] or cols %d outside [1, 2^22]", rows, cols);
     if (rows == 0) return LORA_OK;
     if (!x || !codes || !scales) return fail(LORA_ERR_ARG, "x, codes or scales is NULL");
     const int32_t groups = (cols + LORA_SCALE_BLOCK - 1) / LORA_SCALE_BLOCK;
@@ -1056,8 +1057,7 @@ int lora_linear_e4m3_block(void *stream, int32_t T, const void *x, int64_t ldx, 
     if (ldx < d_in || ldy < d_out || lds < T) return fail(LORA_ERR_ARG, "row pitch smaller than the row");
     if ((st = check_block_base(T, ldx, d_in, W, w_scales, scale_type, d_out))) return st;
     if (!aligned16(x) || ldx % 16) return fail(LORA_ERR_ALIGN, "x needs 16-byte aligned rows");
-    if (reinterpret_cast<uintptr_t>(x_scales) & 3u || (scale_type == LORA_SCALE_E8M0 && lds % 4))
-        return fail(LORA_ERR_ALIGN, "x's scales need 4-byte aligned rows");
+    if (!scale_aligned(x_scales, scale_type)) return fail(LORA_ERR_ALIGN, "x's scales are not aligned to their size");
     if (!elem_aligned(y, esize_of(out_dtype))) return fail(LORA_ERR_ALIGN, "y is not aligned to its element size");
     const LinearBlockCall c{T, x, ldx, x_scales, lds, d_in, W, w_scales, scale_type, d_out, out_dtype, y, ldy};
     return launch_linear_block(static_cast<hipStream_t>(stream), c);

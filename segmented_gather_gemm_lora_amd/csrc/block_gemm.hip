@@ -98,6 +98,12 @@ __device__ __forceinline__ void dma4(const void *g, uint32_t lds_byte)
     asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(lds_byte) : "memory");
 }
 
+// A byte per lane, which becomes a word in LDS.
+__device__ __forceinline__ void dma1(const void *g, uint32_t lds_byte)
+{
+    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_ubyte %0, off" ::"v"(g), "s"(lds_byte) : "memory");
+}
+
 // dma16 from a wave-uniform base plus a 32-bit per-lane byte offset.
 __device__ __forceinline__ void dma16s(const void *base, uint32_t off, uint32_t lds_byte)
 {
@@ -393,11 +399,12 @@ template <class S, bool E8, Form F> struct Tile {
             const int p = m0 + (wave * S::kXDma + j) * 8 + (lane >> 3);
             xoff[j] = uint32_t((p < a.T ? p : a.T - 1) * a.ldx + 16 * unit);
         }
-        // scales: a wave brings 64 rows' (E8M0: 256 rows', 4 a lane); others repeat them
-        constexpr int kSRows = E8 ? 256 : 64, kSParts = (S::kBM + kSRows - 1) / kSRows;
+        // scales: a wave brings 64 rows', a word each (rows of E8M0 scales may start at any byte); others
+        // repeat them
+        constexpr int kSParts = (S::kBM + 63) / 64;
         spart = wave % kSParts;
-        int sp = m0 + spart * kSRows + (E8 ? 4 : 1) * lane;
-        sp = sp < a.T ? sp : (E8 ? (a.T - 1) & ~3 : a.T - 1);
+        int sp = m0 + spart * 64 + lane;
+        sp = sp < a.T ? sp : a.T - 1;
         sxp = static_cast<const char *>(a.sx) + int64_t(sp) * (E8 ? 1 : 4);
         sstep = a.lds * (E8 ? 1 : 4);
     }
@@ -429,8 +436,11 @@ template <class S, bool E8, Form F> struct Tile {
             if constexpr (is_fused(F) || F == kGradient) dma16s(xb, xoff[j], xl + 1024 * j);
             else dma16(in ? static_cast<const void *>(xb + xoff[j]) : g_zeros, xl + 1024 * j);
         }
-        if ((S::kWDma + S::kXDma) % parts == part)
-            dma4(sxp + kt * sstep, base + S::kWBytes + S::kXBytes + uint32_t(spart) * 256);
+        if ((S::kWDma + S::kXDma) % parts == part) {
+            const uint32_t to = base + S::kWBytes + S::kXBytes + uint32_t(spart) * 256;
+            if constexpr (E8) dma1(sxp + kt * sstep, to);
+            else dma4(sxp + kt * sstep, to);
+        }
     }
 
     __device__ __forceinline__ const char *stage(int kt) const { return lds + ((kt - k0) % S::kStages) * S::kStageBytes; }
@@ -478,7 +488,7 @@ template <class S, bool E8, Form F> struct Tile {
             r.wb = int(word);
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
-                r.xb[i] = *reinterpret_cast<const uint8_t *>(ss + r0 + kStrips * i);
+                r.xb[i] = *reinterpret_cast<const int *>(ss + 4 * (r0 + kStrips * i));
                 if (F == kF32) r.f[i] = e8m0(r.wb) * e8m0(r.xb[i]);
             }
         } else {

@@ -127,7 +127,7 @@ def test_linear(kind, out, T, d_in, d_out):
     dt = torch.bfloat16 if out == "bf16" else torch.float32
     pad = T % 3  # y at odd pitches too
     ydev, y = pitched(T, d_out, dt, pad, 7)
-    sdev, s = pitched(xs.shape[0], T, np_dtype(kind), (-T) % 4 + 4)
+    sdev, s = pitched(xs.shape[0], T, np_dtype(kind), T % 5)
     s.copy_(torch.from_numpy(xs))
     ws_dev = B.workspace(B.LORA_OP_LINEAR_BLOCK, T, d_in, d_out, 1)
     B.linear_e4m3_block(torch.from_numpy(xq).cuda(), s, torch.from_numpy(W).cuda(), torch.from_numpy(ws).cuda(), y, ws_dev)
