@@ -33,6 +33,11 @@
 // ds_read_b64_tr_b8, which hands a lane one column of 8 rows; unit u of row r lies in
 // slot u ^ (r % 8), so that those 8 rows cover all banks.  It writes fp32 sums (few tiles are
 // split along d_out), which the gradient's last launch adds, with u A.
+//
+// What bounds it: a stage's loads.  4096 rows, 4096 -> 14336, E8M0 scales: 240 us (2.0
+// PFLOP/s), the matrix units busy 44% of the cycles, no LDS conflicts; 64 KB a stage come
+// from the L2 while the stage before is multiplied, and LDS holds two.  fp32 scales: 330
+// us, the fmas beside the matrix instructions.
 #include "device.h"
 #include "internal.h"
 
@@ -141,8 +146,7 @@ __device__ __forceinline__ void correction(const BlockArgs &a, int Tp, int pw0, 
     const bool first = mp == start || (m == 0 && (mt == 0 || start >= mp - SR + 16));
     const int rank = first && mp < Tp && lane < 16 * TM ? drank : 0;
     // Here, and below, what the compiler loaded has landed before the ring's loads, which it does not
-    // count: else it would wait for all of them in every step (2304 rows, 288 of them by 128
-    // adapters: 62 us of correction).
+    // count: else it would wait for all of them in every step.
     __builtin_amdgcn_s_waitcnt(wait_vm(0));
     auto lane_of = [](int v, int l) { return __builtin_amdgcn_readlane(v, l); };
     const int c00 = cw0 < a.n ? cw0 : a.n - 1; // columns are counted from here: B may span more than 4 GiB
@@ -342,7 +346,8 @@ template <class S, bool E8, Form F> struct Tile {
     // slot ^ (row % 8).
     static constexpr int kWUnits = WT ? S::kBN / 16 : 8;
     // Row tile i of a wave is kStrips * i below its first: neighbouring rows, which may be many short
-    // segments, are every wave's.
+    // segments, are every wave's (2304 rows, the 288 last of 70 adapters of ranks 8 to 64: 121 us with
+    // a wave's tiles side by side, 90 so).
     static constexpr int kStrips = 16 * S::WM;
     const BlockArgs &a;
     char *lds;
@@ -641,6 +646,7 @@ void block_gemm_kernel(BlockArgs a)
 // block are whole 128-byte lines), with 8 KB of W a wave on the way: 64 KB a CU, which
 // is what HBM's latency takes.  The waves' sums meet in LDS.  x's codes (at most 64 rows) are
 // read by every workgroup from L2; TN grows with the columns, so that there are about 256.
+// 4096 -> 4096: 1 row 5.3 us (3.2 TB/s), 16 6.7, 32 8.7, 64 12.4: 64 rows' codes are 64 MB from the L2.
 constexpr int kFew = 64;
 constexpr int kMaxSlices = 4; // of the shrink
 constexpr int kFewWaves = 8;

