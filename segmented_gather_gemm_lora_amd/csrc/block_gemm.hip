@@ -119,6 +119,44 @@ __device__ __forceinline__ void dma16s(const void *base, uint32_t off, uint32_t 
 // 4 TN g + 4 t + q.
 template <int TN> __device__ __forceinline__ int wave_col(int m, int t) { return (m >> 2) * (4 * TN) + 4 * t + (m & 3); }
 
+// Ranks jj .. jj + 7 of a row of B whose rank r is any: the 16 bytes from element `at` of the matrix (its
+// elements go on in the next row), or at the matrix's end those before it.  n r >= 8 elements.
+// Ranks one by one: 201 rows of ranks 5, 24 and 100, 4224 -> 4880, 49 us, 29 so; 64 rows of 32 such adapters
+// 31 and 25.
+typedef u32x4 u32x4_half __attribute__((aligned(2)));
+__device__ __forceinline__ u32x4 eight_of(gptr<uint16_t> B, int64_t at, int64_t elements)
+{
+    return *(gptr<u32x4_half>)(B + (at < elements - 8 ? at : elements - 8));
+}
+// What eight_of() has brought, moved to its place, and zeros for what are not the row's ranks (`left` of them).
+__device__ __forceinline__ u32x4 own_eight(u32x4 u, int64_t at, int64_t elements, int left)
+{
+    const int late = at > elements - 8 ? int(at - (elements - 8)) : 0; // only in the matrix's last rows
+    if (__any(late > 0)) {
+        uint64_t lo = uint64_t(u[0]) | uint64_t(u[1]) << 32, hi = uint64_t(u[2]) | uint64_t(u[3]) << 32;
+        const int by = 16 * (late & 3);
+        if (late & 4) lo = hi, hi = 0;
+        if (by) lo = lo >> by | hi << (64 - by), hi >>= by;
+        if (late > 7) lo = 0;
+        u = u32x4{uint32_t(lo), uint32_t(lo >> 32), uint32_t(hi), uint32_t(hi >> 32)};
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u[e] &= (2 * e < left ? 0xFFFFu : 0u) | (2 * e + 1 < left ? 0xFFFF0000u : 0u);
+    return u;
+}
+// The same one by one, of a matrix of fewer than 8 elements.
+__device__ __forceinline__ u32x4 few_ranks(gptr<uint16_t> row, int jj, int r)
+{
+    u32x4 u;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int j = jj + 2 * e;
+        const uint32_t lo = row[j < r ? j : 0], hi = row[j + 1 < r ? j + 1 : 0];
+        u[e] = (j < r ? lo : 0) | (j + 1 < r ? hi << 16 : 0);
+    }
+    return u;
+}
+
 // The correction of the segments that meet a wave's rows (at most one a row), on bf16
 // MFMA: a step is 16 ranks of one segment, A = B_s rows (lane groups 0, 2: the first 8 ranks,
 // 1, 3: the others), B = scale_s v in two halves (groups 0, 1: hi, 2, 3: lo).  Only the row tiles that the
@@ -150,10 +188,10 @@ __device__ __forceinline__ void correction(const BlockArgs &a, int Tp, int pw0, 
     __builtin_amdgcn_s_waitcnt(wait_vm(0));
     auto lane_of = [](int v, int l) { return __builtin_amdgcn_readlane(v, l); };
     const int c00 = cw0 < a.n ? cw0 : a.n - 1; // columns are counted from here: B may span more than 4 GiB
-    auto base_of = [&](int l, int r) {
-        const uint64_t B = uint64_t(uint32_t(lane_of(int(Blo), l))) | uint64_t(uint32_t(lane_of(int(Bhi), l))) << 32;
-        return reinterpret_cast<const uint16_t *>(B) + int64_t(c00) * r;
+    auto whole_of = [&](int l) {
+        return reinterpret_cast<const uint16_t *>(uint64_t(uint32_t(lane_of(int(Blo), l))) | uint64_t(uint32_t(lane_of(int(Bhi), l))) << 32);
     };
+    auto base_of = [&](int l, int r) { return whole_of(l) + int64_t(c00) * r; };
     auto next = [&](int &q, uint64_t &left) { // the next step (16 ranks q, segment), or -1
         while (left == 0) {
             left = __ballot(rank > 16 * ++q);
@@ -220,20 +258,24 @@ __device__ __forceinline__ void correction(const BlockArgs &a, int Tp, int pw0, 
             __builtin_amdgcn_s_waitcnt(kWaitLds0); // read before the place is filled again
             if (more) issue();
         } else {
-            const gptr<uint16_t> B = as_global<uint16_t>(base_of(l, r));
-#pragma unroll
-            for (int t = 0; t < TN; ++t) {
+            const gptr<uint16_t> B = as_global<uint16_t>(whole_of(l));
+            const int64_t elements = int64_t(a.n) * r;
+            auto at = [&](int t) {
                 const int c = cw0 + wave_col<TN>(m, t);
-                const gptr<uint16_t> row = B + ((c < a.n ? c : a.n - 1) - c00) * r;
-                u32x4 u;
+                return int64_t(c < a.n ? c : a.n - 1) * r;
+            };
+            u32x4 raw[TN];
+            if (elements >= 8) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = jj + 2 * e;
-                    const uint32_t lo = row[j < r ? j : 0], hi = row[j + 1 < r ? j + 1 : 0];
-                    u[e] = (j < r ? lo : 0) | (j + 1 < r ? hi << 16 : 0);
-                }
-                b[t] = __builtin_bit_cast(bf16x8, u);
+                for (int t = 0; t < TN; ++t) raw[t] = eight_of(B, at(t) + jj, elements);
+#pragma unroll
+                for (int t = 0; t < TN; ++t) raw[t] = own_eight(raw[t], at(t) + jj, elements, r - jj);
+            } else {
+#pragma unroll
+                for (int t = 0; t < TN; ++t) raw[t] = few_ranks(B + at(t), jj, r);
             }
+#pragma unroll
+            for (int t = 0; t < TN; ++t) b[t] = __builtin_bit_cast(bf16x8, raw[t]);
         }
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
@@ -809,19 +851,8 @@ template <int TN, int TM, bool E8, Form F> __global__ __launch_bounds__(64 * kFe
 #pragma unroll
             for (int t = 0; t < TN; ++t) {
                 const int c = c0 + 16 * t + m;
-                const gptr<uint16_t> row = Bs + int64_t(c < a.n ? c : a.n - 1) * r;
-                u32x4 u{};
-                if ((r & 7) == 0) {
-                    u = *(gptr<u32x4>)(row + (jj < r ? jj : 0));
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int j = jj + 2 * e;
-                        const uint32_t x0 = row[j < r ? j : 0], x1 = row[j + 1 < r ? j + 1 : 0];
-                        u[e] = (j < r ? x0 : 0) | (j + 1 < r ? x1 << 16 : 0);
-                    }
-                }
-                f.b[t] = u;
+                const int64_t at = int64_t(c < a.n ? c : a.n - 1) * r, elements = int64_t(a.n) * r;
+                f.b[t] = elements >= 8 ? eight_of(Bs, at + jj, elements) : few_ranks(Bs + at, jj, r);
             }
             j_at += 16;
             if (j_at >= r) {
@@ -836,10 +867,15 @@ template <int TN, int TM, bool E8, Form F> __global__ __launch_bounds__(64 * kFe
             if (f.l < 0) continue;
             const int p0 = lane_of(sstart, f.l), p1 = p0 + lane_of(slen, f.l);
             const float scale = __uint_as_float(uint32_t(lane_of(int(__float_as_uint(sscale)), f.l)));
-            const int left = lane_of(srank, f.l) - (f.j0 + 8 * (g & 1)); // ranks of this lane's 8 (LDS holds any bits past r)
+            const int jj = f.j0 + 8 * (g & 1);
+            const int left = lane_of(srank, f.l) - jj; // ranks of this lane's 8 (LDS holds any bits past r)
             u32x4 b[TN];
 #pragma unroll
-            for (int t = 0; t < TN; ++t) b[t] = left > 0 ? f.b[t] : u32x4{};
+            for (int t = 0; t < TN; ++t) {
+                const int c = c0 + 16 * t + m;
+                const int64_t elements = int64_t(a.n) * (left + jj);
+                b[t] = elements >= 8 ? own_eight(f.b[t], int64_t(c < a.n ? c : a.n - 1) * (left + jj) + jj, elements, left) : f.b[t];
+            }
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
                 if (p0 >= 16 * i + 16 || p1 <= 16 * i) continue; // wave-uniform

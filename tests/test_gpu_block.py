@@ -185,7 +185,7 @@ def fused_reference(prob, W, ws, kind):
 
 def run_fused(prob, W, ws, plan, T=None):
     T = T or prob.T
-    y = torch.full((T, prob.d_out + 8), 5.0, dtype=torch.bfloat16, device="cuda")
+    y = torch.full((T, (prob.d_out + 7) // 8 * 8 + 8), 5.0, dtype=torch.bfloat16, device="cuda")
     work = B.workspace(B.LORA_OP_FUSED_BLOCK, T, prob.d_in, prob.d_out, max(prob.max_rank, 1))
     x = torch.zeros(T, prob.d_in, dtype=torch.bfloat16, device="cuda")
     x[: prob.T] = B.to_device(prob.x, "bf16")
@@ -196,7 +196,7 @@ def run_fused(prob, W, ws, plan, T=None):
 
 FUSED = [(1, 128, 256, [16]), (8, 256, 264, [8, 8]), (64, 1024, 512, [16] * 8), (65, 528, 136, [3, 17]), (130, 400, 1000, [8, 64, 1]),
          (300, 512, 2048, [16, 32, 5, 100]), (1000, 1024, 2304, [16] * 20), (2100, 384, 4096, [8, 16, 256]), (2100, 144, 8304, [8, 16] * 40),
-         (2100, 144, 8304, [5, 17])]
+         (2100, 144, 8304, [5, 17]), (3, 32, 5, [1, 2]), (70, 32, 5, [1, 1, 2]), (40, 64, 1, [7, 9]), (90, 64, 3, [3, 33])]
 
 
 @pytest.mark.parametrize("kind", ["f32", "e8m0"])

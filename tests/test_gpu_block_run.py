@@ -163,6 +163,30 @@ def test_an_adapter_that_is_not_finite_stays_with_its_rows():
             assert torch.isnan(y[mine].float()).all() and torch.equal(y[~mine], clean[~mine])
 
 
+@pytest.mark.parametrize("T", [30, 200, 2100])
+@pytest.mark.parametrize("r", [1, 3, 4, 5, 8, 17, 20])
+def test_a_column_that_is_not_finite_stays_alone(T, r):
+    """One row of B (a column of y) holds NaN: its neighbours, whose ranks lie beside it, do not change."""
+    d_out = 8312 if T > 1000 else 264
+    prob = fused_problem(T, 128, d_out, [r], T, none=0.0)
+    W, ws = base(np.random.default_rng(1), d_out, 128, "f32")
+    pool = B.DevicePool.from_problem(prob)
+    plan = B.Plan(T).build(prob.ids, pool).upload()
+    x, work = B.to_device(prob.x, "bf16"), B.workspace(B.LORA_OP_FUSED_BLOCK, T, 128, d_out, r)
+    y, z = (torch.empty(T, d_out, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    Wd, wsd = dev(W), dev(ws)
+    B.fused_linear_e4m3_block(x, Wd, wsd, plan, y, work)
+    store = pool.storage if pool.storage.dtype == torch.bfloat16 else pool.storage.view(torch.bfloat16)
+    at = (int(pool.addr_B[0]) - store.data_ptr()) // 2
+    cols = [0, 100, 257, d_out - 1]
+    for c in cols:
+        store.view(-1)[at + c * r: at + (c + 1) * r] = float("nan")
+    B.fused_linear_e4m3_block(x, Wd, wsd, plan, z, work)
+    keep = torch.ones(d_out, dtype=torch.bool, device="cuda")
+    keep[cols] = False
+    assert torch.isnan(z[:, ~keep].float()).all() and torch.equal(z[:, keep], y[:, keep])
+
+
 def test_an_infinite_row_stays_alone():
     """Its codes have a NaN scale: the row's results are NaN and no other's change."""
     lay = Layer(384, 520, [16, 8], "f32", 9)
