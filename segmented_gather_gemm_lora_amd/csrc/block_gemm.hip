@@ -100,19 +100,19 @@ template <int TN_, int TM_, int WN_, int WM_, int STAGES> struct Shape {
 
 __device__ __forceinline__ void dma4(const void *g, uint32_t lds_byte)
 {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(lds_byte) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(lds_byte) : "memory");
 }
 
 // A byte per lane, which becomes a word in LDS.
 __device__ __forceinline__ void dma1(const void *g, uint32_t lds_byte)
 {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_ubyte %0, off" ::"v"(g), "s"(lds_byte) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_ubyte %0, off" ::"v"(g), "s"(lds_byte) : "memory");
 }
 
 // dma16 from a wave-uniform base plus a 32-bit per-lane byte offset.
 __device__ __forceinline__ void dma16s(const void *base, uint32_t off, uint32_t lds_byte)
 {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds_byte) : "memory");
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds_byte) : "memory");
 }
 
 // Column of a wave's tile t that MFMA row m stands for: lane group g ends with columns

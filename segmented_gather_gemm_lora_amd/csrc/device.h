@@ -44,10 +44,12 @@ constexpr int kWaitLds0 = 15 | (3 << 14) | (7 << 4);                            
 // 16 bytes per lane from global memory to LDS at m0 + 16 lane.  The compiler does
 // not see this write to LDS; the kernel waits for it with an explicit vmcnt before
 // the barrier that publishes the data.  m0 is a reserved register (never allocated
-// by the compiler) and no other code in these kernels reads it.
+// by the compiler) and no other code in these kernels reads it.  A load to LDS needs a
+// wait state behind a scalar write of m0, which the compiler does not add inside an asm
+// statement: hence the s_nop, here and wherever else m0 is written.
 __device__ __forceinline__ void dma16(const void *g, uint32_t lds_byte)
 {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(lds_byte) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(lds_byte) : "memory");
 }
 // What direct loads take for places outside.
 __device__ const uint32_t g_zeros[4] = {0, 0, 0, 0};
