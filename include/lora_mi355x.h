@@ -718,8 +718,8 @@ int lora_quantize_e4m3(void *stream, int dtype, const void *x, int64_t ldx, int3
 /* y[t, n] = sum_b x_scales[b, t] w_scales[n / 128, b] sum_{k in block b} x[t, k] W[n, k],
  * overwriting y: the block's inner sums on 8-bit MFMA, everything in fp32, rounded once.
  *   x         codes [T, ldx], 16-byte aligned rows; x_scales [groups, lds], lds >= T
- *   W         codes [d_out, d_in], row pitch d_in, 16-byte aligned, d_in % 16 == 0;
- *             w_scales [ceil(d_out / 128), groups], contiguous
+ *   W         codes [d_out, d_in], row pitch d_in, 16-byte aligned, d_in % 16 == 0,
+ *             at most 2^31 - 128; w_scales [ceil(d_out / 128), groups], contiguous
  *   y         [T, ldy] of out_dtype (bf16 or fp32), any alignment
  * x (T rows) and W must each span less than 4 GiB.  Needs ws_bytes >=
  * lora_workspace_bytes(LORA_OP_LINEAR_BLOCK, T, d_in, d_out, 1).

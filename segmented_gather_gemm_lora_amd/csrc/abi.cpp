@@ -1035,6 +1035,9 @@ static int check_block_base(int64_t rows, int64_t ldx, int32_t d_in, const void 
     if (d_in % 16) return fail(LORA_ERR_ALIGN, "an E4M3 base needs d_in %% 16 == 0 (16-byte rows), got %d", d_in);
     if (!aligned16(W)) return fail(LORA_ERR_ALIGN, "W is not 16-byte aligned");
     if (!scale_aligned(w_scales, scale_type)) return fail(LORA_ERR_ALIGN, "W's scales are not aligned to their size");
+    // the last block's end is counted in 32 bits
+    if (d_in > INT32_MAX - (LORA_SCALE_BLOCK - 1))
+        return fail(LORA_ERR_ARG, "d_in %d > 2^31 - %d", d_in, LORA_SCALE_BLOCK);
     // rows are addressed with 32-bit byte offsets
     if (ldx >= int64_t(1) << 31 || (rows + 1) * ldx >= int64_t(1) << 32 || (int64_t(d_out) + 1) * d_in >= int64_t(1) << 32)
         return fail(LORA_ERR_ARG, "the codes of x or W span 4 GiB or more");
