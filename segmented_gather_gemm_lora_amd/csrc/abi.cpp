@@ -1080,6 +1080,8 @@ int lora_fused_linear_e4m3_block(void *stream, const void *x, int64_t ldx, int32
     if (T == 0) return LORA_OK;
     if (!x || !y) return fail(LORA_ERR_ARG, "x or y is NULL");
     if (ldx < d_in || ldy < d_out) return fail(LORA_ERR_ARG, "row pitch smaller than the row");
+    // the shrink counts the ends of its slices of a row in 32 bits
+    if (d_in > 1 << 30) return fail(LORA_ERR_ARG, "d_in %d > 2^30", d_in);
     // x's codes are held in rows of whole blocks
     if ((st = check_block_base(T, int64_t(d_in) + LORA_SCALE_BLOCK, d_in, W0, w_scales, scale_type, d_out))) return st;
     if (!aligned16(x) || !aligned16(y) || ldx % 8 || ldy % 8)
