@@ -988,15 +988,26 @@ template <int TN, Form F> void go_few_rows(hipStream_t s, const BlockArgs &a, bo
     }
 }
 
+// Columns, in sixteens, of a workgroup of up to 64 rows, and the workgroups.
+struct FewGrid {
+    int tn;
+    int64_t workgroups;
+    FewGrid(int32_t T, int32_t n, bool f32)
+    {
+        // about a workgroup for each CU
+        // (the registers of 64 rows hold fewer columns)
+        const int tiles = (n + 15) / 16, most = T <= 32 ? 4 : f32 ? 1 : 2;
+        tn = std::min(most, tiles <= 256 ? 1 : tiles <= 512 ? 2 : 4);
+        workgroups = (int64_t(tiles) + tn - 1) / tn;
+    }
+};
+
 template <Form F> int go_few(hipStream_t s, const BlockArgs &a, bool e8)
 {
-    // about a workgroup for each CU
-    // (the registers of 64 rows hold fewer columns)
-    const int tiles = (a.n + 15) / 16, most = a.T <= 32 ? 4 : F == kF32 ? 1 : 2;
-    const int tn = std::min(most, tiles <= 256 ? 1 : tiles <= 512 ? 2 : 4);
-    const dim3 grid{unsigned((tiles + tn - 1) / tn)};
-    if (tn == 1) go_few_rows<1, F>(s, a, e8, grid);
-    else if (tn == 2) go_few_rows<2, F>(s, a, e8, grid);
+    const FewGrid f(a.T, a.n, F == kF32);
+    const dim3 grid{unsigned(f.workgroups)};
+    if (f.tn == 1) go_few_rows<1, F>(s, a, e8, grid);
+    else if (f.tn == 2) go_few_rows<2, F>(s, a, e8, grid);
     else go_few_rows<4, F>(s, a, e8, grid); // up to 32 rows
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return fail(LORA_ERR_HIP, "block product launch: %s", hipGetErrorString(e));
@@ -1012,7 +1023,6 @@ template <class S, Form F> int go(hipStream_t s, BlockArgs &a, bool e8, int spli
     a.tiles_m = (a.T + S::kBM - 1) / S::kBM;
     a.tiles_n = (a.n + S::kBN - 1) / S::kBN;
     const int64_t tiles = int64_t(a.tiles_m) * a.tiles_n * splits;
-    if (tiles > most_workgroups(S::kThreads)) return fail(LORA_ERR_ARG, "block product: too many tiles");
     // Where whole rounds of workgroups (one on a CU) leave at most half a round of tiles, those
     // are halves of 128 columns (summed axis 4096, fp32 scales / E8M0, us: 4096 x 4352 128 -> 113 / 115 -> 104,
     // 2304 x 8192 130 -> 115 / 112 -> 108, 4096 x 14336 340 -> 330 / 265 -> 259).
@@ -1043,6 +1053,24 @@ inline Size size_of(int32_t T, int32_t n, bool f32)
 {
     if (tiles_of<Small>(T, n) <= (f32 ? 256 : 512)) return kSmall;
     return f32 || tiles_of<Medium>(T, n) <= 512 ? kMedium : kLarge;
+}
+
+// More workgroups than a launch has are refused, before anything of the call runs.  A rest of
+// halved tiles is at most 128 more.
+inline int check_tiles(int64_t tiles, int threads)
+{
+    if (tiles + 128 > most_workgroups(threads)) return fail(LORA_ERR_ARG, "block product: too many tiles");
+    return LORA_OK;
+}
+template <class S> int check_shape(int32_t T, int32_t n, int splits) { return check_tiles(tiles_of<S>(T, n) * splits, S::kThreads); }
+inline int check_size(Size size, int32_t T, int32_t n, int splits)
+{
+    return size == kLarge ? check_shape<Large>(T, n, splits) : size == kMedium ? check_shape<Medium>(T, n, splits) : check_shape<Small>(T, n, splits);
+}
+inline int check_product(int32_t T, int32_t n, bool f32)
+{
+    if (T <= kFew) return check_tiles(FewGrid(T, n, f32).workgroups, 64 * kFewWaves);
+    return check_size(size_of(T, n, f32), T, n, 1);
 }
 
 template <Form F> int launch_product(hipStream_t s, BlockArgs &a, bool e8)
@@ -1131,6 +1159,8 @@ int launch_linear_block(hipStream_t s, const LinearBlockCall &c)
     const int es = c.out_dtype == LORA_F32 ? 4 : 2;
     a.vec_y = aligned16(c.y) && c.ldy * es % 16 == 0;
     const bool e8 = c.scale_type == LORA_SCALE_E8M0;
+    const int st = check_product(c.T, c.d_out, c.out_dtype == LORA_F32);
+    if (st) return st;
     return c.out_dtype == LORA_F32 ? launch_product<kF32>(s, a, e8) : launch_product<kBf16>(s, a, e8);
 }
 
@@ -1159,7 +1189,8 @@ int launch_fused_linear_block(hipStream_t s, const ShrinkArgs &sa, const void *W
     q.scale_type = scale_type;
     q.scales = base + w.scales;
     q.lds = w.lds;
-    int st = LORA_OK;
+    int st = check_product(T, ea.d_out, false);
+    if (st) return st;
     uint16_t *vh = reinterpret_cast<uint16_t *>(base + w.vh);
     a.ldh = vh_pitch(max_rank);
     a.nsl = 0;
@@ -1207,7 +1238,8 @@ int launch_fused_block_backward(hipStream_t s, const BackwardArgs &b, const void
     const GradientWs w(T, b.d_in, b.d_out, h->max_rank < 1 ? 1 : h->max_rank);
     const GradientPlan g(T, b.d_in, b.d_out);
     char *base = static_cast<char *>(ws);
-    int st;
+    int st = check_size(g.size, T, b.d_in, g.splits);
+    if (st) return st;
     QuantCall q{};
     q.dtype = LORA_BF16;
     q.x = b.dy;

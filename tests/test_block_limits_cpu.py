@@ -25,3 +25,31 @@ def test_the_fused_layer_past_2_to_the_30():
     good = dict(stream=None, x=P, ldx=k, d_in=k, W=P, ws=P, scale_type=F32, d_out=1, seg=plan.dev(), y=P, ldy=8, work=P, work_bytes=1 << 62)
     refused("lora_fused_linear_e4m3_block", good,
             [(dict(d_in=k, ldx=k), ARG) for k in ((1 << 30) + 16, (1 << 31) - 512, (1 << 31) - 144)])
+
+
+def test_more_workgroups_than_a_launch_has():
+    """Threads of a launch are counted in 32 bits: up to 64 rows, workgroups of 512 threads have 16 columns
+    (fp32 results of more than 32 rows) or 32 (bf16)."""
+    good = dict(stream=None, T=33, x=P, ldx=16, xs=P, lds=33, d_in=16, W=P, ws=P, scale_type=F32, d_out=1, out=B.LORA_F32, y=P, ldy=1 << 28,
+                work=None, work_bytes=0)
+    refused("lora_linear_e4m3_block", good, [(dict(d_out=1 << 27), ARG), (dict(d_out=(1 << 28) - 2), ARG), (dict(T=64, lds=64, d_out=1 << 27), ARG),
+                                             (dict(out=B.LORA_BF16, d_out=(1 << 28) - 2), ARG)])
+    assert "tiles" in B.last_error()
+
+
+def test_the_fused_layer_refuses_them_before_anything_runs():
+    """Not as the failure of a first launch (here: without a GPU)."""
+    plan = host_plan([0] * 40, [8])
+    good = dict(stream=None, x=P, ldx=16, d_in=16, W=P, ws=P, scale_type=F32, d_out=8, seg=plan.dev(), y=P, ldy=1 << 28, work=P, work_bytes=1 << 62)
+    refused("lora_fused_linear_e4m3_block", good, [(dict(d_out=(1 << 28) - 8), ARG)])
+    plan = host_plan([0] * 70000, [8])
+    refused("lora_fused_linear_e4m3_block", dict(good, seg=plan.dev()), [(dict(d_out=(1 << 28) - 8), ARG)])
+
+
+def test_the_gradients_refuse_them_before_anything_runs():
+    plan = host_plan([0] * 400000, [8])
+    n = 1 << 24
+    good = dict(stream=None, x=P, ldx=n, d_in=n, W=P, ws=P, scale_type=F32, dy=P, lddy=16, d_out=8, seg=plan.dev(), gA=P, gB=P, n=1, flags=0,
+                dx=P + (1 << 46), lddx=n, work=P, work_bytes=1 << 62)
+    refused("lora_fused_linear_e4m3_block_backward", good, [(dict(), ARG)])
+    assert "tiles" in B.last_error()
