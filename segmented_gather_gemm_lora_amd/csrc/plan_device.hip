@@ -277,7 +277,7 @@ __global__ __launch_bounds__(kThreads) void plan_device_kernel(DevicePlanArgs a)
         } else {
             const int p = live ? sorted + pos : t;
             perm[p] = live ? t : -1;
-            segidx[p] = -1;
+            if (a.S > 0) segidx[p] = -1; // without adapters the plan has no such table
         }
     }
 

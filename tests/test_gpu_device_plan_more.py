@@ -1,0 +1,37 @@
+"""Plans built on the device at their ends: pools without adapters, and what lies behind the tables."""
+
+import numpy as np
+import pytest
+
+from gpu_helpers import require_gpu, say
+from segmented_gather_gemm_lora_amd import binding as B
+from test_gpu_device_plan import dev32, fake_pool
+
+pytestmark = pytest.mark.gpu
+torch = None
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _gpu():
+    global torch
+    import test_gpu_device_plan
+
+    torch = test_gpu_device_plan.torch = require_gpu()
+
+
+@pytest.mark.parametrize("T,N", [(1, 0), (33, 0), (1000, 0), (33, 1), (300, 40)])
+def test_nothing_is_written_behind_the_tables(T, N):
+    """The buffer from bytes_used on is as it was, with a pool of no adapters too, whose plan has
+    no table of segments by row; its one word of seg_indptr is 0."""
+    say(f"plan {T} rows of {N} adapters")
+    plan = B.DevicePlan(T, fake_pool([16] * N))
+    plan.dev.fill_(0x5A)
+    rng = np.random.default_rng(T)
+    plan.build(dev32(rng.integers(-1, max(N, 3), T)))
+    torch.cuda.synchronize()
+    b, raw = plan.bounds(), plan.dev.cpu().numpy()
+    assert (raw[b["bytes_used"]:] == 0x5A).all()
+    if N == 0:
+        assert b["num_sorted"] == 0 and b["soa_offset"] == b["segidx_offset"]
+        assert raw[b["soa_offset"]:][:4].view(np.int32)[0] == 0
+        assert plan.header()["num_tokens"] == T and plan.tables()["perm"].tolist() == list(range(T))
