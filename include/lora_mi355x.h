@@ -244,7 +244,7 @@ int lora_segments_upload(const lora_segments *host, lora_segments *dev, void *st
  * Captured into a graph, one recording serves every batch of up to T rows:
  * lengths, adapters and the pool's tables are read at replay.
  *   T            rows of the batch's x and y, at most dev->capacity and 65536
- *   adapters_dev [n_requests] adapter of each request (-1: none)
+ *   adapters_dev [n_requests] adapter of each request (-1: none); n_requests <= 2^30
  *   lengths_dev  [n_requests] rows of each request, in order from row 0 (0 or less:
  *                none; rows past T are cut off); NULL: one row each, n_requests <= T.
  *                Rows that no request owns are padding: the calls neither use

@@ -496,7 +496,8 @@ int lora_build_segments_device(void *stream, int32_t T, int32_t n_requests, cons
     if (reinterpret_cast<uintptr_t>(geometry) & 7u) return fail(LORA_ERR_ALIGN, "geometry is not 8-byte aligned");
     if (T < 0 || T > 65536) return fail(LORA_ERR_ARG, "T %d outside [0, 65536]", T);
     if (T > dev->capacity) return fail(LORA_ERR_WORKSPACE, "batch of %d rows > capacity %d", T, dev->capacity);
-    if (n_requests < 0 || (!lengths_dev && n_requests > T))
+    // the kernel counts requests in steps of a workgroup in 32 bits
+    if (n_requests < 0 || n_requests > 1 << 30 || (!lengths_dev && n_requests > T))
         return fail(LORA_ERR_ARG, "%d requests for %d rows", n_requests, T);
     if (n_adapters < 0 || n_adapters > LORA_DEVICE_PLAN_MAX_ADAPTERS)
         return fail(LORA_ERR_ARG, "n_adapters %d outside [0, %d]", n_adapters, LORA_DEVICE_PLAN_MAX_ADAPTERS);

@@ -4,7 +4,7 @@ anything is launched."""
 import pytest
 
 from segmented_gather_gemm_lora_amd import binding as B
-from test_block_cpu import ARG, E8, F32, P, host_plan, refused
+from test_block_cpu import ARG, E8, F32, DevicePlanArgs, P, host_plan, refused
 
 
 @pytest.mark.parametrize("scale_type", [F32, E8])
@@ -53,3 +53,8 @@ def test_the_gradients_refuse_them_before_anything_runs():
                 dx=P + (1 << 46), lddx=n, work=P, work_bytes=1 << 62)
     refused("lora_fused_linear_e4m3_block_backward", good, [(dict(), ARG)])
     assert "tiles" in B.last_error()
+
+
+def test_requests_of_a_device_plan():
+    """Its loop over them adds 1024 to a 32-bit count: past 2^31 - 1024 it would not have ended."""
+    refused("lora_build_segments_device", DevicePlanArgs(64).good(64), [(dict(R=(1 << 30) + 1), ARG), (dict(R=(1 << 31) - 1), ARG)])
