@@ -920,6 +920,8 @@ class DevicePlan:
             raise ValueError("the plan or adapters are not on the current device")
         if adapters.dtype is not torch.int32 or (n > 1 and adapters.stride(0) != 1):
             raise ValueError("adapters are adjacent int32 elements, one a request")
+        if n >> 31:  # the C call's count has 32 bits
+            raise ValueError(f"{n} requests")
         at = None
         if lengths is not None:
             if lengths.dtype is not torch.int32 or lengths.shape != adapters.shape or lengths.get_device() != device or (
@@ -1233,6 +1235,8 @@ def _rows_of(t, dtype, rows, cols, device, least=False):
                          f"at strides {t.stride()}")
     if t.get_device() != device:
         raise ValueError(f"a tensor of {tuple(t.shape)} is not on the current device")
+    if n >> 31 or d >> 31:  # the C call's counts have 32 bits
+        raise ValueError(f"a tensor of {tuple(t.shape)} has 2^31 rows or columns or more")
     return t.data_ptr(), ld if n > 1 else (d + 15) // 16 * 16
 
 

@@ -57,4 +57,26 @@ def test_the_gradients_refuse_them_before_anything_runs():
 
 def test_requests_of_a_device_plan():
     """Its loop over them adds 1024 to a 32-bit count: past 2^31 - 1024 it would not have ended."""
-    refused("lora_build_segments_device", DevicePlanArgs(64).good(64), [(dict(R=(1 << 30) + 1), ARG), (dict(R=(1 << 31) - 1), ARG)])
+    d = DevicePlanArgs(64)
+    refused("lora_build_segments_device", d.good(64), [(dict(R=(1 << 30) + 1), ARG), (dict(R=(1 << 31) - 1), ARG)])
+
+
+def test_the_binding_refuses_counts_past_32_bits(monkeypatch):
+    """ctypes would cut them: 2^32 + 1 rows are not one row.  Tensors without memory stand for large ones."""
+    import torch
+
+    new = lambda *shape, dtype=torch.uint8: torch.empty(*shape, dtype=dtype, device="meta")  # noqa: E731
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: new(1).get_device())
+    monkeypatch.setattr(B, "_stream_handle", lambda *a: None)
+    n, bf16, f32 = (1 << 32) + 1, torch.bfloat16, torch.float32
+    for rows, cols in ((n, 1), (1, n), ((1 << 31), 16)):
+        with pytest.raises(ValueError, match=r"2\^31"):
+            B.quantize_e4m3(new(rows, cols, dtype=bf16), new(rows, cols), new((cols + 127) // 128, rows, dtype=f32))
+    for T, d_in, d_out in ((n, 16, 8), (1, 16, n), (1, n + 15, 1)):
+        with pytest.raises(ValueError, match=r"2\^31"):
+            B.linear_e4m3_block(new(T, d_in), new((d_in + 127) // 128, T, dtype=f32), new(d_out, d_in),
+                                new((d_out + 127) // 128, (d_in + 127) // 128, dtype=f32), new(T, d_out, dtype=bf16), new(0))
+    plan = B.DevicePlan.__new__(B.DevicePlan)  # of the constructor's work, what build() asks for first
+    plan._device, plan._fn, plan._pool_args, plan.rows = new(1).get_device(), lambda *a: 0, (), 8
+    with pytest.raises(ValueError, match="requests"):
+        plan.build(new(n, dtype=torch.int32), new(n, dtype=torch.int32))
