@@ -895,7 +895,8 @@ class DevicePlan:
                                             or t.numel() < pool.n_adapters):
                 raise ValueError("the pool has no device tables of its adapters")
         device = pool.rank_dev.device if hasattr(pool.rank_dev, "device") else "cuda"
-        self.dev = torch.empty(lora_segments_bytes(self.rows), dtype=torch.uint8, device=device)
+        # a plan of no rows is built without a launch: its counts on the device are these zeros
+        self.dev = (torch.empty if self.rows else torch.zeros)(lora_segments_bytes(self.rows), dtype=torch.uint8, device=device)
         self.geometry = (ctypes.c_uint64 * (PLAN_HEADER_BYTES // 8))()
         self.h = LoraSegments()  # no segment on the host
         self.h.batch_tokens = self.rows

@@ -35,3 +35,15 @@ def test_nothing_is_written_behind_the_tables(T, N):
         assert b["num_sorted"] == 0 and b["soa_offset"] == b["segidx_offset"]
         assert raw[b["soa_offset"]:][:4].view(np.int32)[0] == 0
         assert plan.header()["num_tokens"] == T and plan.tables()["perm"].tolist() == list(range(T))
+
+
+def test_a_plan_of_no_rows_has_counts():
+    """Nothing is launched for it; header() and tables() read zeros, not what the memory held."""
+    pool = fake_pool([16] * 4)
+    held = torch.full((B.lora_segments_bytes(0),), 0x5A, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    del held
+    plan = B.DevicePlan(0, pool).build(dev32(np.zeros(0)), dev32(np.zeros(0)))
+    h = plan.header()
+    assert all(h[k] == 0 for k in ("num_tokens", "num_sorted", "num_segments", "num_blocks", "num_chunks", "max_rank", "max_len"))
+    assert plan.tables()["counts"].tolist() == [0] * 7 and len(plan.arrays()["perm"]) == 0
