@@ -9,10 +9,10 @@
 //
 // One workgroup computes 16 TN WN columns x 16 TM WM rows with WN x WM waves on
 // v_mfma_f32_16x16x128_f8f6f4, whose 128 is a block: one instruction is the inner sum of 16
-// columns and 16 rows.  fp32 scales: it starts from 0 and its result enters the fp32
-// accumulators with one fma a value (a lane's four values are one row's, so the factor
-// sx sw is one register a row tile).  E8M0 scales: the instruction takes the two scale
-// bytes itself and accumulates.  MFMA rows are columns of W, MFMA columns are rows of x.
+// columns and 16 rows.  E8M0 scales: the instruction takes the two scale bytes itself and
+// accumulates.  fp32 scales: it takes their powers of two, starts from 0, and its result enters the
+// fp32 accumulators with one fma a value by the product of their factors in [1, 2) (a lane's four values are one
+// row's, so that is one register a row tile).  MFMA rows are columns of W, MFMA columns are rows of x.
 //
 // A stage is a block: 128 bytes of each row of W and of x, and the rows' scales, brought
 // to LDS by direct loads.  16-byte unit u of row r lies in slot u ^ (r % 8), so that 8
@@ -347,9 +347,35 @@ __device__ __forceinline__ Wide widen(const i32x8 &c)
     return w;
 }
 
-// One block with fp32 sums: acc += f (W x) on bf16 MFMA.
+// A scale as the byte of a power of two and a factor: value = f 2^(e - 127).  The product of two
+// scales may leave fp32's range where their products with a block's sum do not (or the sum is 0), so it is never
+// formed: the powers of two go to the matrix instruction (or to an ldexp) and only the factors, in
+// [1, 2), are multiplied.  A zero or subnormal factor is in units of 2^-127; e = 255 (infinity, NaN) makes NaN.
+struct Parts {
+    int e; // its low 8 bits
+    float f;
+};
+template <bool E8> __device__ __forceinline__ Parts parts_of(uint32_t word)
+{
+    if constexpr (E8) return Parts{int(word), 1.f};
+    const bool small = __builtin_amdgcn_classf(__uint_as_float(word), 0xF0); // zero or subnormal, of either sign
+    return Parts{int(word >> 23), small ? __uint_as_float(word) * 0x1p127f : __uint_as_float((word & 0x807FFFFFu) | 0x3F800000u)};
+}
+// The exponent of the product of two scales, and its factor: what the matrix instruction does with the bytes.
+struct Product {
+    int e;
+    float f;
+};
+__device__ __forceinline__ Product product_of(const Parts &w, const Parts &x)
+{
+    const int we = w.e & 255, xe = x.e & 255;
+    return Product{we + xe - 254, max(we, xe) == 255 ? __uint_as_float(0x7FC00000u) : w.f * x.f};
+}
+
+// One block with fp32 sums: acc += f 2^e (W x) on bf16 MFMA.
 template <int TN, int TM, class WF>
-__device__ __forceinline__ void exact_block(const i32x8 (&xf)[TM], const float (&f)[TM], floatx4 (&acc)[TN][TM], const WF &wfrag)
+__device__ __forceinline__ void exact_block(const i32x8 (&xf)[TM], const int (&e)[TM], const float (&f)[TM], floatx4 (&acc)[TN][TM],
+                                            const WF &wfrag)
 {
     Wide x[TM];
 #pragma unroll
@@ -363,7 +389,7 @@ __device__ __forceinline__ void exact_block(const i32x8 (&xf)[TM], const float (
 #pragma unroll
             for (int h = 0; h < 4; ++h) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[h], x[i].v[h], p, 0, 0, 0);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) acc[t][i][q] = fmaf(p[q], f[i], acc[t][i][q]);
+            for (int q = 0; q < 4; ++q) acc[t][i][q] = fmaf(ldexpf(p[q], e[i]), f[i], acc[t][i][q]);
         }
     }
 }
@@ -372,11 +398,6 @@ __device__ __forceinline__ void exact_block(const i32x8 (&xf)[TM], const float (
 // gradient.
 enum Form { kBf16, kF32, kFused, kFusedAnyRank, kGradient };
 constexpr bool is_fused(Form f) { return f == kFused || f == kFusedAnyRank; }
-
-__device__ __forceinline__ float e8m0(int e)
-{
-    return e == 255 ? __uint_as_float(0x7FC00000u) : e ? __uint_as_float(uint32_t(e) << 23) : 0x1p-127f;
-}
 
 // A workgroup's tile: its place, the loads of its stages and the fragments in them.
 // k is the summed axis and n the columns of W [n][k], or of W [k][n] (kGradient).
@@ -512,7 +533,8 @@ template <class S, bool E8, Form F> struct Tile {
     }
     __device__ __forceinline__ i32x8 xfrag(const char *st, int i) const { return frag(st + S::kWBytes + (16 * wm + kStrips * i + m) * kG); }
 
-    // The scales of block kt: E8M0 bytes, or the products of both sides' scales.
+    // The scales of block kt: bytes of powers of two (kF32: the exponents' sum), and the product of both
+    // sides' factors where the matrix instruction does not do it all.
     struct Scales {
         int wb, xb[TM];
         float f[TM];
@@ -531,17 +553,14 @@ template <class S, bool E8, Form F> struct Tile {
         Scales r;
         const char *ss = stage(kt) + S::kWBytes + S::kXBytes;
         const int r0 = 16 * wm + m;
-        if constexpr (E8) {
-            r.wb = int(word);
+        const Parts w = parts_of<E8>(word);
+        r.wb = w.e;
 #pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                r.xb[i] = *reinterpret_cast<const int *>(ss + 4 * (r0 + kStrips * i));
-                if (F == kF32) r.f[i] = e8m0(r.wb) * e8m0(r.xb[i]);
-            }
-        } else {
-            const float ws = __uint_as_float(word);
-#pragma unroll
-            for (int i = 0; i < TM; ++i) r.f[i] = ws * *reinterpret_cast<const float *>(ss + 4 * (r0 + kStrips * i));
+        for (int i = 0; i < TM; ++i) {
+            const Parts x = parts_of<E8>(*reinterpret_cast<const uint32_t *>(ss + 4 * (r0 + kStrips * i)));
+            const Product p = product_of(w, x);
+            r.xb[i] = F == kF32 ? p.e : x.e;
+            r.f[i] = F == kF32 ? p.f : w.f * x.f;
         }
         return r;
     }
@@ -549,20 +568,10 @@ template <class S, bool E8, Form F> struct Tile {
     // acc += the block's product of one column tile with every row tile
     __device__ __forceinline__ void multiply(const i32x8 &wf, const i32x8 (&xf)[TM], const Scales &sc, floatx4 (&acc)[TM]) const
     {
-        if constexpr (E8) {
+        static_assert(E8, "the instruction's own scales");
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
-                acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf[i], acc[i], 0, 0, 0, sc.wb, 0, sc.xb[i]);
-        } else {
-            floatx4 p[TM];
-#pragma unroll
-            for (int i = 0; i < TM; ++i) // scale bytes of 127: 2^0
-                p[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf[i], floatx4{}, 0, 0, 0, 127, 0, 127);
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) acc[i][q] = fmaf(p[i][q], sc.f[i], acc[i][q]);
-        }
+        for (int i = 0; i < TM; ++i)
+            acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf[i], acc[i], 0, 0, 0, sc.wb, 0, sc.xb[i]);
     }
 
     // Behind the last stage: its place in LDS is free when every wave is past its reads.
@@ -623,16 +632,16 @@ template <class S, bool E8, Form F> __device__ __forceinline__ void multiply_til
         __builtin_amdgcn_s_waitcnt(wait_vm_lds0(S::kDma * (S::kStages - 2)));
         __builtin_amdgcn_s_barrier();
         const char *st = T.stage(kt);
+        const auto sc = T.scales(kt, word); // first: the matrix instructions take them
         i32x8 xf[TM];
 #pragma unroll
         for (int i = 0; i < TM; ++i) xf[i] = T.xfrag(st, i);
         const i32x8 w0 = T.wfrag(st, 0);
-        const auto sc = T.scales(kt, word);
         const i32x8 w1 = T.wfrag(st, 1);
         // the next stage's loads go out while these reads come back
         T.issue(kt + S::kStages - 1);
         if constexpr (F == kF32) {
-            exact_block<TN, TM>(xf, sc.f, acc, [&](int t) { return t ? T.wfrag(st, t) : w0; });
+            exact_block<TN, TM>(xf, sc.xb, sc.f, acc, [&](int t) { return t ? T.wfrag(st, t) : w0; });
         } else if constexpr (E8) {
 #pragma unroll
             for (int t = 0; t < TN; ++t) T.multiply(t ? t == 1 ? w1 : T.wfrag(st, t) : w0, xf, sc, acc[t]);
@@ -648,7 +657,8 @@ template <class S, bool E8, Form F> __device__ __forceinline__ void multiply_til
 #pragma unroll
                 for (int i = 0; i < TM; ++i) {
                     if (t < TN)
-                        q[t & 1][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[t % NW], xf[i], floatx4{}, 0, 0, 0, 127, 0, 127);
+                        q[t & 1][i] =
+                            __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[t % NW], xf[i], floatx4{}, 0, 0, 0, sc.wb, 0, sc.xb[i]);
                     if (t > 0)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) acc[t - 1][i][e] = fmaf(q[(t - 1) & 1][i][e], sc.f[i], acc[t - 1][i][e]);
@@ -772,35 +782,38 @@ template <int TN, int TM, bool E8, Form F> __global__ __launch_bounds__(64 * kFe
     auto multiply = [&](int j, Operands &o) {
         const int kb = block_of(j);
         if (kb >= blocks) return; // wave-uniform
-        i32x8 xf[TM];
-        float f[TM];
-        const int wb = __builtin_amdgcn_readlane(int(wsv), j & 63); // fp32 bits, or a byte
+        const Parts w = parts_of<E8>(uint32_t(__builtin_amdgcn_readlane(int(wsv), j & 63)));
         const int k = kb * kG + 16 * g;
-#pragma unroll
-        for (int i = 0; i < TM; ++i) { // past k x's codes are zeros
+        auto xfrag = [&](int i) { // past k x's codes are zeros
             if (k >= a.k) o.x[i].lo = u32x4{};
             if (k + 64 >= a.k) o.x[i].hi = u32x4{};
-            xf[i] = operand(o.x[i]);
-            if constexpr (E8) f[i] = F == kF32 ? e8m0(wb) * e8m0(int(o.sx[i])) : 0.f;
-            else f[i] = __uint_as_float(uint32_t(wb)) * __uint_as_float(o.sx[i]);
-        }
+            return operand(o.x[i]);
+        };
         if constexpr (F == kF32) {
-            exact_block<TN, TM>(xf, f, acc, [&](int t) { return operand(o.w[t]); });
+            i32x8 xf[TM];
+            int e[TM];
+            float f[TM];
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                xf[i] = xfrag(i);
+                const Product p = product_of(w, parts_of<E8>(o.sx[i]));
+                e[i] = p.e;
+                f[i] = p.f;
+            }
+            exact_block<TN, TM>(xf, e, f, acc, [&](int t) { return operand(o.w[t]); });
         } else {
 #pragma unroll
-            for (int t = 0; t < TN; ++t)
+            for (int i = 0; i < TM; ++i) {
+                const i32x8 xf = xfrag(i);
+                const Parts x = parts_of<E8>(o.sx[i]);
 #pragma unroll
-                for (int i = 0; i < TM; ++i) {
-                    if constexpr (E8) {
-                        acc[t][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(o.w[t]), xf[i], acc[t][i], 0, 0, 0, wb, 0,
-                                                                                     int(o.sx[i]));
-                    } else {
-                        const floatx4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(o.w[t]), xf[i], floatx4{}, 0, 0, 0,
-                                                                                           127, 0, 127);
+                for (int t = 0; t < TN; ++t) {
+                    const floatx4 p =
+                        __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(o.w[t]), xf, E8 ? acc[t][i] : floatx4{}, 0, 0, 0, w.e, 0, x.e);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) acc[t][i][q] = fmaf(p[q], f[i], acc[t][i][q]);
-                    }
+                    for (int q = 0; q < 4; ++q) acc[t][i][q] = E8 ? p[q] : fmaf(p[q], w.f * x.f, acc[t][i][q]);
                 }
+            }
         }
     };
     const int mine = wave < blocks ? (blocks - wave + kFewWaves - 1) / kFewWaves : 0; // blocks of this wave
