@@ -94,6 +94,18 @@ def test_zero_and_subnormal_scales(T, d_out):
         check(linear(xq, xs, W, ws, out), ref, bound, f"{T} x {d_out} {out}")
 
 
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d_out", SHAPES)
+def test_an_infinite_scale_counts_as_nan(out, T, d_out):
+    rng = np.random.default_rng(T + 3)
+    xq, W = codes(rng, (T, 144)), codes(rng, (d_out, 144))
+    xs, ws = stored(rng, np.full((2, T), -5), "f32"), stored(rng, np.full((-(-d_out // 128), 2), -6), "f32")
+    clean = linear(xq, xs, W, ws, out)
+    xs[0, 2] = np.inf
+    got = linear(xq, xs, W, ws, out)
+    assert np.isnan(got[2]).all() and np.array_equal(np.delete(got, 2, 0), np.delete(clean, 2, 0))
+
+
 @pytest.mark.parametrize("kind", ["f32", "e8m0"])
 @pytest.mark.parametrize("ranks", [[8, 16], [5, 17]])
 @pytest.mark.parametrize("T,d_out", SHAPES)

@@ -5,7 +5,7 @@ import pytest
 
 from gpu_helpers import require_gpu, say
 from segmented_gather_gemm_lora_amd import binding as B
-from test_gpu_device_plan import dev32, fake_pool
+from test_gpu_device_plan import check_plan, dev32, fake_pool, tokens
 
 pytestmark = pytest.mark.gpu
 torch = None
@@ -47,3 +47,29 @@ def test_a_plan_of_no_rows_has_counts():
     h = plan.header()
     assert all(h[k] == 0 for k in ("num_tokens", "num_sorted", "num_segments", "num_blocks", "num_chunks", "max_rank", "max_len"))
     assert plan.tables()["counts"].tolist() == [0] * 7 and len(plan.arrays()["perm"]) == 0
+
+
+@pytest.mark.parametrize("N", [2457, 2458, 4000, 7168])
+def test_many_adapters_captured(N):
+    """Past 2457 adapters the tables need more LDS than a launch has unasked: built inside a capture, as the
+    first build of that size, and replayed for other batches."""
+    say(f"captured plan of {N} adapters")
+    rng = np.random.default_rng(N)
+    T, R = 700, 60
+    pool = fake_pool(rng.choice([8, 16, 64], N))
+    adapters, lengths = dev32(np.zeros(R)), dev32(np.zeros(R))
+    plan = B.DevicePlan(T, pool)
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=stream):
+        plan.build(adapters, lengths)
+    for i in range(4):
+        a = rng.integers(-1, N, R).astype(np.int32)
+        a[0] = N - 1
+        ln = rng.integers(0, 30, R).astype(np.int32)
+        adapters.copy_(torch.from_numpy(a))
+        lengths.copy_(torch.from_numpy(ln))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        check_plan(plan, pool, tokens(a, ln, T), T)
