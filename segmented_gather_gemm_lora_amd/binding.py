@@ -1278,10 +1278,10 @@ def _block_base(W, w_scales, device):
     return d_out, d_in, pW, ps, kind
 
 
-def linear_e4m3_block(x, x_scales, W, w_scales, y, ws, stream=None):
+def linear_e4m3_block(x, x_scales, W, w_scales, y, ws=None, stream=None):
     """y = (x_scales x) (w_scales W)^T for E4M3 codes x [T, d_in] (scales [groups, T]) and W
     [d_out, d_in] (scales for each 128 x 128 block, of the same type); y bf16 or fp32,
-    overwritten.  ws: a workspace of LORA_OP_LINEAR_BLOCK."""
+    overwritten.  ws: a workspace of LORA_OP_LINEAR_BLOCK, which needs none (None)."""
     torch = _torch()
     device = torch.cuda.current_device()
     d_out, d_in, pW, pws, kind = _block_base(W, w_scales, device)
@@ -1292,11 +1292,11 @@ def linear_e4m3_block(x, x_scales, W, w_scales, y, ws, stream=None):
     px, ldx = _rows_of(x, torch.uint8, T, d_in, device)
     ps, lds = _rows_of(x_scales, w_scales.dtype, (d_in + 127) // SCALE_BLOCK, T, device)
     py, ldy = _rows_of(y, dt, T, d_out, device)
-    if ws.get_device() != device:
+    if ws is not None and ws.get_device() != device:
         raise ValueError("the workspace is not on the current device")
     st = load().lora_linear_e4m3_block(_stream_handle(stream, device), T, px, ldx, ps, lds, d_in, pW, pws, kind, d_out,
-                                       LORA_BF16 if dt is torch.bfloat16 else LORA_F32, py, ldy, ws.data_ptr(),
-                                       ws.numel() * ws.element_size())
+                                       LORA_BF16 if dt is torch.bfloat16 else LORA_F32, py, ldy, _ptr(ws),
+                                       0 if ws is None else ws.numel() * ws.element_size())
     if st:
         _check(st, "lora_linear_e4m3_block")
 

@@ -85,3 +85,14 @@ def test_nan_stays_in_its_rows_and_columns(kind, out, d_in, T, d_out):
     keep = np.ones((T, d_out), bool)
     keep[rows], keep[:, cols] = False, False
     assert np.isnan(got[~keep]).all() and np.array_equal(got[keep], clean[keep])
+
+
+@pytest.mark.parametrize("T", [1, 70])
+def test_the_product_needs_no_workspace(T):
+    assert B.lora_workspace_bytes(B.LORA_OP_LINEAR_BLOCK, T, 256, 100, 1) == 0
+    rng = np.random.default_rng(T)
+    xq, xs, _ = R.quantize(rng.standard_normal((T, 256)), 1, "f32")
+    W, ws, _ = R.quantize(rng.standard_normal((100, 256)), 128, "f32")
+    y = torch.zeros(T, 100, device="cuda")
+    B.linear_e4m3_block(dev(xq), dev(xs), dev(W), dev(ws), y)
+    assert np.array_equal(y.double().cpu().numpy(), linear(xq, xs, W, ws, "f32"))
