@@ -1403,15 +1403,25 @@ int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p
     return LORA_OK;
 }
 
+static int64_t join_workgroups(const BackwardArgs &b, const lora_plan_header *h)
+{
+    return (int64_t(h->num_blocks) + (h->num_tokens - h->num_sorted + 15) / 16) * ((b.d_in + kTileCols - 1) / kTileCols);
+}
+int check_dx_join(const BackwardArgs &b, const PlanView &p)
+{
+    if (join_workgroups(b, p.h) > most_workgroups(kDxWaves * 64)) return fail(LORA_ERR_ARG, "backward: too many dx tiles");
+    return LORA_OK;
+}
+
 int launch_dx_join(hipStream_t s, const BackwardArgs &b, const PlanView &p, void *ws, const float *parts, int splits)
 {
     const lora_plan_header *h = p.h;
     BwdArgs a = make_args(b, p, layout_of(h->num_sorted, b.d_in, b.d_out, h->max_rank), ws);
     a.joins = parts;
     a.splits = splits;
-    const int64_t nwg = (int64_t(a.nblk) + (a.T - a.Tp + 15) / 16) * a.tiles_x;
-    if (nwg > most_workgroups(kDxWaves * 64)) return fail(LORA_ERR_ARG, "backward: too many dx tiles");
-    const dim3 grid{unsigned(nwg)}, block(kDxWaves * 64);
+    const int st = check_dx_join(b, p);
+    if (st) return st;
+    const dim3 grid{unsigned(join_workgroups(b, h))}, block(kDxWaves * 64);
     if (b.vec_dx) launch_kernel(bwd_join_kernel<true>, grid, block, 0, s, a);
     else launch_kernel(bwd_join_kernel<false>, grid, block, 0, s, a);
     return checked("backward join");

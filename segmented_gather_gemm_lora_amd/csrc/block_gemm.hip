@@ -1252,6 +1252,7 @@ int launch_fused_block_backward(hipStream_t s, const BackwardArgs &b, const void
     const GradientPlan g(T, b.d_in, b.d_out);
     char *base = static_cast<char *>(ws);
     int st = check_size(g.size, T, b.d_in, g.splits);
+    if (!st) st = check_dx_join(b, p);
     if (st) return st;
     QuantCall q{};
     q.dtype = LORA_BF16;

@@ -186,6 +186,7 @@ int launch_sgmv_backward(hipStream_t s, const BackwardArgs &b, const PlanView &p
 // dx = the sum of `splits` parts [T][d_in] (fp32, plan rows) + u A, every row; after
 // launch_sgmv_backward with u_rows on the same workspace (bf16).
 int launch_dx_join(hipStream_t s, const BackwardArgs &b, const PlanView &p, void *ws, const float *parts, int splits);
+int check_dx_join(const BackwardArgs &b, const PlanView &p); // refuses what it would
 size_t fused_backward_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out, int32_t max_rank);
 int launch_fused_backward(hipStream_t s, const BackwardArgs &b, const void *W0, const PlanView &p, void *ws);
 

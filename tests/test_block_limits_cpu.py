@@ -46,8 +46,9 @@ def test_the_fused_layer_refuses_them_before_anything_runs():
     refused("lora_fused_linear_e4m3_block", dict(good, seg=plan.dev()), [(dict(d_out=(1 << 28) - 8), ARG)])
 
 
-def test_the_gradients_refuse_them_before_anything_runs():
-    plan = host_plan([0] * 400000, [8])
+@pytest.mark.parametrize("T", [8192, 400000])  # of the last launch; of the product
+def test_the_gradients_refuse_them_before_anything_runs(T):
+    plan = host_plan([0] * T, [8])
     n = 1 << 24
     good = dict(stream=None, x=P, ldx=n, d_in=n, W=P, ws=P, scale_type=F32, dy=P, lddy=16, d_out=8, seg=plan.dev(), gA=P, gB=P, n=1, flags=0,
                 dx=P + (1 << 46), lddx=n, work=P, work_bytes=1 << 62)
