@@ -880,7 +880,7 @@ class DevicePlan:
     captured together and replayed for other batches of up to `rows` rows.  The
     gradient calls take a Plan.  max_rank and rank_multiple (the pool's, where not given)
     bound what the tables may hold at any build; requests of adapters outside them count
-    as having none."""
+    as having none.  Every build reads the table tensors that the pool has now: changes go into them."""
 
     def __init__(self, rows: int, pool, max_rank: Optional[int] = None, rank_multiple: Optional[int] = None):
         torch = _torch()
@@ -904,7 +904,8 @@ class DevicePlan:
         self.made_for, self.paged, self.grads_fit = (pool.d_in, pool.d_out, pool.dtype), isinstance(pool, PagedPool), None
         _check(lora_segments_bind(self.dev.data_ptr(), self.rows, ctypes.addressof(self.d)), "lora_segments_bind")
         self._device, self._fn, self._tables = self.dev.get_device(), load().lora_build_segments_device, None
-        self._pool_args = (pool.n_adapters, *(_ptr(t) for t in (pool.addr_A_dev, pool.addr_B_dev, pool.rank_dev, pool.alpha_dev)),
+        self._held = (pool.addr_A_dev, pool.addr_B_dev, pool.rank_dev, pool.alpha_dev)  # builds, and graphs, read these
+        self._pool_args = (pool.n_adapters, *map(_ptr, self._held),
                            self.max_rank, self.rank_multiple, self.geometry, ctypes.addressof(self.d))
 
     @property

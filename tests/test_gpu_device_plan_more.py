@@ -73,3 +73,21 @@ def test_many_adapters_captured(N):
         graph.replay()
         torch.cuda.synchronize()
         check_plan(plan, pool, tokens(a, ln, T), T)
+
+
+def test_the_tables_stay_while_the_plan_does():
+    """Changes inside the pool's tables are seen; the tensors themselves may be let go."""
+    pool, T = fake_pool([16] * 8), 40
+    ids = (np.arange(T) % 8).astype(np.int32)
+    plan = B.DevicePlan(T, pool)
+    first = [getattr(pool, k) for k in ("addr_A_dev", "addr_B_dev", "rank_dev", "alpha_dev")]
+    at = [t.data_ptr() for t in first]
+    first[3].mul_(2)
+    pool.alpha *= 2
+    for k in ("addr_A_dev", "addr_B_dev", "rank_dev", "alpha_dev"):
+        setattr(pool, k, None)
+    del first
+    others = [torch.full((8,), 3, dtype=dt, device="cuda") for dt in (torch.int64, torch.int64, torch.int32, torch.float32)]
+    assert not set(t.data_ptr() for t in others) & set(at)
+    plan.build(dev32(ids))
+    check_plan(plan, pool, ids, T)
