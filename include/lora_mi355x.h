@@ -703,7 +703,9 @@ int lora_fused_linear_e4m3(void *stream, const void *x, int64_t ldx, int32_t d_i
  * and a code is the E4M3 value nearest to x / scale, ties to even, rounded once from
  * the exact quotient.  A block with an infinity or a NaN has a NaN scale and codes
  * of 0, so that what it enters becomes NaN.  The products below take any scales: two whose
- * product leaves fp32's range count by what they make of a block's sum, an infinite one as NaN. */
+ * product leaves fp32's range count by what they make of a block's sum (below 2^228; past that
+ * a sum of 0 may become NaN), and of a subnormal fp32 scale of x, below those given here, bits
+ * are lost. */
 #define LORA_SCALE_BLOCK 128
 
 /* Codes and scales of a matrix x [rows, cols] (bf16 or fp32).

@@ -10,9 +10,9 @@
 // One workgroup computes 16 TN WN columns x 16 TM WM rows with WN x WM waves on
 // v_mfma_f32_16x16x128_f8f6f4, whose 128 is a block: one instruction is the inner sum of 16
 // columns and 16 rows.  E8M0 scales: the instruction takes the two scale bytes itself and
-// accumulates.  fp32 scales: it takes their powers of two, starts from 0, and its result enters the
-// fp32 accumulators with one fma a value by the product of their factors in [1, 2) (a lane's four values are one
-// row's, so that is one register a row tile).  MFMA rows are columns of W, MFMA columns are rows of x.
+// accumulates.  fp32 scales: it takes the power of two of W's, starts from 0, and its result enters the fp32
+// accumulators with one fma a value (a lane's four values are one row's, so the rest of W's scale and the row's
+// scale are one factor in a register a row tile).  MFMA rows are columns of W, MFMA columns are rows of x.
 //
 // A stage is a block: 128 bytes of each row of W and of x, and the rows' scales, brought
 // to LDS by direct loads.  16-byte unit u of row r lies in slot u ^ (r % 8), so that 8
@@ -324,72 +324,63 @@ __device__ __forceinline__ void store_row(const BlockArgs &a, int64_t row, int c
     }
 }
 
-// 32 codes as four operands of 8 bf16, exactly.
+// 32 codes as four operands of 8 bf16, times a power of two, exactly (2^-100 to 2^100 of 4 significant bits).
 struct Wide {
     bf16x8 v[4];
 };
-__device__ __forceinline__ Wide widen(const i32x8 &c)
+__device__ __forceinline__ Wide widen(const i32x8 &c, float power)
 {
-    typedef float floatx2 __attribute__((ext_vector_type(2)));
     Wide w;
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
         u32x4 u;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            const floatx2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(c[2 * h + q], false);
-            const floatx2 hi = __builtin_amdgcn_cvt_pk_f32_fp8(c[2 * h + q], true);
-            u[2 * q] = pack_bf16x2(lo[0], lo[1]);
-            u[2 * q + 1] = pack_bf16x2(hi[0], hi[1]);
+            u[2 * q] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(uint32_t(c[2 * h + q]), power, false));
+            u[2 * q + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(uint32_t(c[2 * h + q]), power, true));
         }
         w.v[h] = __builtin_bit_cast(bf16x8, u);
     }
     return w;
 }
 
-// A scale as the byte of a power of two and a factor: value = f 2^(e - 127).  The product of two
-// scales may leave fp32's range where their products with a block's sum do not (or the sum is 0), so it is never
-// formed: the powers of two go to the matrix instruction (or to an ldexp) and only the factors, in
-// [1, 2), are multiplied.  A zero or subnormal factor is in units of 2^-127; e = 255 (infinity, NaN) makes NaN.
-struct Parts {
-    int e; // its low 8 bits
-    float f;
-};
-template <bool E8> __device__ __forceinline__ Parts parts_of(uint32_t word)
-{
-    if constexpr (E8) return Parts{int(word), 1.f};
-    const bool small = __builtin_amdgcn_classf(__uint_as_float(word), 0xF0); // zero or subnormal, of either sign
-    return Parts{int(word >> 23), small ? __uint_as_float(word) * 0x1p127f : __uint_as_float((word & 0x807FFFFFu) | 0x3F800000u)};
-}
-// The exponent of the product of two scales, and its factor: what the matrix instruction does with the bytes.
-struct Product {
+// W's scale as the byte of a power of two and a factor: value = f 2^(e - 127).  The product of two scales may
+// leave fp32's range where its product with a block's sum does not (or the sum is 0), so it is never formed: 2^(e - 127)
+// goes into the sum, through the matrix instruction or the widened codes, and f with the row's scale into the
+// accumulators.  e is held in 2^-100 .. 2^100, where no sum of a block (2^-18 to 2^25) leaves the range; f is in [1, 2)
+// there.  So the factor f sx overflows for scales whose product is 2^228 and more alone, and loses bits
+// where sx is subnormal.
+struct WScale {
     int e;
     float f;
 };
-__device__ __forceinline__ Product product_of(const Parts &w, const Parts &x)
+__device__ __forceinline__ float e8m0(int e)
 {
-    const int we = w.e & 255, xe = x.e & 255;
-    return Product{we + xe - 254, max(we, xe) == 255 ? __uint_as_float(0x7FC00000u) : w.f * x.f};
+    return e == 255 ? __uint_as_float(0x7FC00000u) : e ? __uint_as_float(uint32_t(e) << 23) : 0x1p-127f;
+}
+template <bool E8> __device__ __forceinline__ WScale wscale_of(uint32_t word)
+{
+    const int e = min(max(E8 ? int(word) : int(word >> 23 & 255), 27), 227);
+    return WScale{e, ldexpf(E8 ? e8m0(int(word)) : __uint_as_float(word), 127 - e)};
 }
 
-// One block with fp32 sums: acc += f 2^e (W x) on bf16 MFMA.
+// One block with fp32 sums: acc += f (power W x) on bf16 MFMA.
 template <int TN, int TM, class WF>
-__device__ __forceinline__ void exact_block(const i32x8 (&xf)[TM], const int (&e)[TM], const float (&f)[TM], floatx4 (&acc)[TN][TM],
-                                            const WF &wfrag)
+__device__ __forceinline__ void exact_block(const i32x8 (&xf)[TM], float power, const float (&f)[TM], floatx4 (&acc)[TN][TM], const WF &wfrag)
 {
     Wide x[TM];
 #pragma unroll
-    for (int i = 0; i < TM; ++i) x[i] = widen(xf[i]);
+    for (int i = 0; i < TM; ++i) x[i] = widen(xf[i], 1.f);
 #pragma unroll
     for (int t = 0; t < TN; ++t) {
-        const Wide w = widen(wfrag(t));
+        const Wide w = widen(wfrag(t), power);
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
             floatx4 p{};
 #pragma unroll
             for (int h = 0; h < 4; ++h) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[h], x[i].v[h], p, 0, 0, 0);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) acc[t][i][q] = fmaf(ldexpf(p[q], e[i]), f[i], acc[t][i][q]);
+            for (int q = 0; q < 4; ++q) acc[t][i][q] = fmaf(p[q], f[i], acc[t][i][q]);
         }
     }
 }
@@ -398,6 +389,28 @@ __device__ __forceinline__ void exact_block(const i32x8 (&xf)[TM], const int (&e
 // gradient.
 enum Form { kBf16, kF32, kFused, kFusedAnyRank, kGradient };
 constexpr bool is_fused(Form f) { return f == kFused || f == kFusedAnyRank; }
+// Whether the matrix instruction takes both scales whole.
+constexpr bool own_scales(bool e8, Form f) { return e8 && f != kF32; }
+
+// The scales of W that a wave meets in 64 blocks, one a lane: a byte, and where the instruction does not take
+// it all a factor.
+struct WScales {
+    uint32_t e;
+    float f;
+};
+template <bool E8, Form F> __device__ __forceinline__ WScales wscales_at(const void *sw, int64_t at)
+{
+    if constexpr (own_scales(E8, F)) return WScales{as_global<uint8_t>(sw)[at], 1.f};
+    const WScale w = wscale_of<E8>(E8 ? as_global<uint8_t>(sw)[at] : as_global<uint32_t>(sw)[at]);
+    return WScales{uint32_t(w.e), w.f};
+}
+__device__ __forceinline__ WScale wscale_from(const WScales &all, int l)
+{
+    return WScale{__builtin_amdgcn_readlane(int(all.e), l),
+                  __uint_as_float(uint32_t(__builtin_amdgcn_readlane(int(__float_as_uint(all.f)), l)))};
+}
+// A row's factor: what is left of W's scale, and its own (a byte or fp32 bits).
+template <bool E8> __device__ __forceinline__ float factor(const WScale &w, uint32_t sx) { return w.f * (E8 ? e8m0(int(sx)) : __uint_as_float(sx)); }
 
 // A workgroup's tile: its place, the loads of its stages and the fragments in them.
 // k is the summed axis and n the columns of W [n][k], or of W [k][n] (kGradient).
@@ -533,34 +546,27 @@ template <class S, bool E8, Form F> struct Tile {
     }
     __device__ __forceinline__ i32x8 xfrag(const char *st, int i) const { return frag(st + S::kWBytes + (16 * wm + kStrips * i + m) * kG); }
 
-    // The scales of block kt: bytes of powers of two (kF32: the exponents' sum), and the product of both
-    // sides' factors where the matrix instruction does not do it all.
+    // The scales of block kt: bytes, and the rows' factors where the instruction does not take both.
     struct Scales {
         int wb, xb[TM];
         float f[TM];
     };
-    // W's scales of the 64 stages from kt, one a lane (fp32 bits or a byte).  A scalar load in each
+    // W's scales of the 64 stages from kt, one a lane.  A scalar load in each
     // stage would make every wait for LDS in it a wait for that load too (they return out of
     // order): fp32 results of 65 x 1024, summed axis 4096, 53 -> 42 us; one row, 12288 columns, 12.5 -> 11.1.
-    __device__ __forceinline__ uint32_t wscales(int kt) const
+    __device__ __forceinline__ WScales wscales(int kt) const
     {
-        const int64_t at = sw0 + (kt + lane < k1 ? kt + lane : k1 - 1) * sw1;
-        if constexpr (E8) return as_global<uint8_t>(a.sw)[at];
-        return as_global<uint32_t>(a.sw)[at];
+        return wscales_at<E8, F>(a.sw, sw0 + (kt + lane < k1 ? kt + lane : k1 - 1) * sw1);
     }
-    __device__ __forceinline__ Scales scales(int kt, uint32_t word) const
+    __device__ __forceinline__ Scales scales(const char *st, const WScale &w) const
     {
         Scales r;
-        const char *ss = stage(kt) + S::kWBytes + S::kXBytes;
-        const int r0 = 16 * wm + m;
-        const Parts w = parts_of<E8>(word);
         r.wb = w.e;
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-            const Parts x = parts_of<E8>(*reinterpret_cast<const uint32_t *>(ss + 4 * (r0 + kStrips * i)));
-            const Product p = product_of(w, x);
-            r.xb[i] = F == kF32 ? p.e : x.e;
-            r.f[i] = F == kF32 ? p.f : w.f * x.f;
+            const uint32_t sx = *reinterpret_cast<const uint32_t *>(st + S::kWBytes + S::kXBytes + 4 * (16 * wm + m + kStrips * i));
+            if constexpr (own_scales(E8, F)) r.xb[i] = int(sx);
+            else r.f[i] = factor<E8>(w, sx);
         }
         return r;
     }
@@ -623,42 +629,42 @@ template <class S, bool E8, Form F> __device__ __forceinline__ void multiply_til
         for (int i = 0; i < TM; ++i) acc[t][i] = floatx4{};
 #pragma unroll
     for (int s = 0; s < S::kStages - 1; ++s) T.issue(T.k0 + s);
-    uint32_t ws = 0;
+    WScales ws{};
     for (int kt = T.k0; kt < T.k1; ++kt) {
         if (((kt - T.k0) & 63) == 0) ws = T.wscales(kt);
-        const uint32_t word = uint32_t(__builtin_amdgcn_readlane(int(ws), (kt - T.k0) & 63));
+        const WScale w = wscale_from(ws, (kt - T.k0) & 63);
         // this wave's loads of stage kt have landed and its reads of stage kt - 1 are
         // done; past the barrier that holds for every wave
         __builtin_amdgcn_s_waitcnt(wait_vm_lds0(S::kDma * (S::kStages - 2)));
         __builtin_amdgcn_s_barrier();
         const char *st = T.stage(kt);
-        const auto sc = T.scales(kt, word); // first: the matrix instructions take them
         i32x8 xf[TM];
 #pragma unroll
         for (int i = 0; i < TM; ++i) xf[i] = T.xfrag(st, i);
         const i32x8 w0 = T.wfrag(st, 0);
+        const auto sc = T.scales(st, w);
         const i32x8 w1 = T.wfrag(st, 1);
         // the next stage's loads go out while these reads come back
         T.issue(kt + S::kStages - 1);
         if constexpr (F == kF32) {
-            exact_block<TN, TM>(xf, sc.xb, sc.f, acc, [&](int t) { return t ? T.wfrag(st, t) : w0; });
+            exact_block<TN, TM>(xf, e8m0(sc.wb), sc.f, acc, [&](int t) { return t ? T.wfrag(st, t) : w0; });
         } else if constexpr (E8) {
 #pragma unroll
             for (int t = 0; t < TN; ++t) T.multiply(t ? t == 1 ? w1 : T.wfrag(st, t) : w0, xf, sc, acc[t]);
         } else {
             // the fmas of a column tile go between the matrix instructions of the next
             constexpr int NW = 3;
-            i32x8 w[NW] = {w0, w1};
+            i32x8 wf[NW] = {w0, w1};
             floatx4 q[2][TM];
 #pragma unroll
             for (int t = 0; t <= TN; ++t) {
                 __builtin_amdgcn_sched_barrier(0);
-                if (NW > 2 ? t + 2 < TN : t > 0 && t + 1 < TN) w[(t + NW - 1) % NW] = T.wfrag(st, t + NW - 1);
+                if (NW > 2 ? t + 2 < TN : t > 0 && t + 1 < TN) wf[(t + NW - 1) % NW] = T.wfrag(st, t + NW - 1);
 #pragma unroll
                 for (int i = 0; i < TM; ++i) {
                     if (t < TN)
                         q[t & 1][i] =
-                            __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[t % NW], xf[i], floatx4{}, 0, 0, 0, sc.wb, 0, sc.xb[i]);
+                            __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[t % NW], xf[i], floatx4{}, 0, 0, 0, sc.wb, 0, 127);
                     if (t > 0)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) acc[t - 1][i][e] = fmaf(q[(t - 1) & 1][i][e], sc.f[i], acc[t - 1][i][e]);
@@ -772,17 +778,15 @@ template <int TN, int TM, bool E8, Form F> __global__ __launch_bounds__(64 * kFe
 #pragma unroll
         for (int i = 0; i < TM; ++i) acc[t][i] = floatx4{};
     // W's scales of the wave's next 64 blocks, one a lane
-    uint32_t wsv = 0;
+    WScales wsv{};
     auto load_scales = [&](int j) {
         const int kb = block_of(j + lane);
-        const int64_t at = int64_t(nb) * blocks + (kb < blocks ? kb : 0);
-        if constexpr (E8) wsv = as_global<uint8_t>(a.sw)[at];
-        else wsv = as_global<uint32_t>(a.sw)[at];
+        wsv = wscales_at<E8, F>(a.sw, int64_t(nb) * blocks + (kb < blocks ? kb : 0));
     };
     auto multiply = [&](int j, Operands &o) {
         const int kb = block_of(j);
         if (kb >= blocks) return; // wave-uniform
-        const Parts w = parts_of<E8>(uint32_t(__builtin_amdgcn_readlane(int(wsv), j & 63)));
+        const WScale w = wscale_from(wsv, j & 63);
         const int k = kb * kG + 16 * g;
         auto xfrag = [&](int i) { // past k x's codes are zeros
             if (k >= a.k) o.x[i].lo = u32x4{};
@@ -791,27 +795,24 @@ template <int TN, int TM, bool E8, Form F> __global__ __launch_bounds__(64 * kFe
         };
         if constexpr (F == kF32) {
             i32x8 xf[TM];
-            int e[TM];
             float f[TM];
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
                 xf[i] = xfrag(i);
-                const Product p = product_of(w, parts_of<E8>(o.sx[i]));
-                e[i] = p.e;
-                f[i] = p.f;
+                f[i] = factor<E8>(w, o.sx[i]);
             }
-            exact_block<TN, TM>(xf, e, f, acc, [&](int t) { return operand(o.w[t]); });
+            exact_block<TN, TM>(xf, e8m0(w.e), f, acc, [&](int t) { return operand(o.w[t]); });
         } else {
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
                 const i32x8 xf = xfrag(i);
-                const Parts x = parts_of<E8>(o.sx[i]);
+                const float f = E8 ? 1.f : factor<E8>(w, o.sx[i]);
 #pragma unroll
                 for (int t = 0; t < TN; ++t) {
-                    const floatx4 p =
-                        __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(o.w[t]), xf, E8 ? acc[t][i] : floatx4{}, 0, 0, 0, w.e, 0, x.e);
+                    const floatx4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(o.w[t]), xf, E8 ? acc[t][i] : floatx4{}, 0,
+                                                                                       0, 0, w.e, 0, E8 ? int(o.sx[i]) : 127);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) acc[t][i][q] = E8 ? p[q] : fmaf(p[q], w.f * x.f, acc[t][i][q]);
+                    for (int q = 0; q < 4; ++q) acc[t][i][q] = E8 ? p[q] : fmaf(p[q], f, acc[t][i][q]);
                 }
             }
         }

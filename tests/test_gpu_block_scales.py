@@ -79,7 +79,8 @@ def test_factors_whose_product_is_subnormal(kind, out, T, d_out):
 
 @pytest.mark.parametrize("T,d_out", SHAPES)
 def test_zero_and_subnormal_scales(T, d_out):
-    """fp32 scales of 0 make 0, subnormal ones count by their value."""
+    """fp32 scales of 0 make 0.  A subnormal one of a row meets W's in one rounding: with W's scale f 2^e, f in [1, 2), the product f sx is off by up to half of 2^-149, which is 2^-150 2^e,
+    at most 2^-150 W's scale, of the block's sum."""
     rng = np.random.default_rng(T + 2)
     d_in = 384
     xq, W = codes(rng, (T, d_in), 56), codes(rng, (d_out, d_in), 56)
@@ -88,22 +89,35 @@ def test_zero_and_subnormal_scales(T, d_out):
     xs[0], ws[:, 1] = 0.0, 0.0
     xs[2, ::2] = np.float32(2.0**-149) * rng.integers(1, 1 << 20, xs[2, ::2].shape).astype(np.float32)
     ws[:, 2] = stored(rng, np.full(nb, 100), "f32")
+    half = np.where((xs > 0) & (xs < 2.0**-126), 2.0**-150, 0.0)
+    _, off, _ = R.linear(xq, half, W, ws)
     for out in ("bf16", "f32"):
         ref, mag, tops = R.linear(xq, xs, W, ws)
         bound = R.linear_bound(ref, mag, tops, d_in, "bf16") if out == "bf16" else f32_bound(ref, mag, d_in)
-        check(linear(xq, xs, W, ws, out), ref, bound, f"{T} x {d_out} {out}")
+        check(linear(xq, xs, W, ws, out), ref, bound + off, f"{T} x {d_out} {out}")
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [5, 20, 50, 70, 300])
+def test_subnormal_scales_of_w(out, T):
+    """They count by their value, to the last bit."""
+    rng = np.random.default_rng(T)
+    xq, W = codes(rng, (T, 256), 56), codes(rng, (100, 256), 56)
+    xs, ws = stored(rng, np.full((2, T), 100), "f32"), np.array([[1001, 3]], np.float32) * np.float32(2.0**-149)
+    ref, mag, tops = R.linear(xq, xs, W, ws)
+    check(linear(xq, xs, W, ws, out), ref, R.linear_bound(ref, mag, tops, 256, "bf16") if out == "bf16" else f32_bound(ref, mag, 256), f"{T}")
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 @pytest.mark.parametrize("T,d_out", SHAPES)
-def test_an_infinite_scale_counts_as_nan(out, T, d_out):
+def test_an_infinite_scale_stays_in_its_row(out, T, d_out):
     rng = np.random.default_rng(T + 3)
     xq, W = codes(rng, (T, 144)), codes(rng, (d_out, 144))
     xs, ws = stored(rng, np.full((2, T), -5), "f32"), stored(rng, np.full((-(-d_out // 128), 2), -6), "f32")
     clean = linear(xq, xs, W, ws, out)
     xs[0, 2] = np.inf
     got = linear(xq, xs, W, ws, out)
-    assert np.isnan(got[2]).all() and np.array_equal(np.delete(got, 2, 0), np.delete(clean, 2, 0))
+    assert not np.isfinite(got[2]).any() and np.array_equal(np.delete(got, 2, 0), np.delete(clean, 2, 0))
 
 
 @pytest.mark.parametrize("kind", ["f32", "e8m0"])
