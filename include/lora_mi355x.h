@@ -739,8 +739,8 @@ int lora_linear_e4m3_block(void *stream, int32_t T, const void *x, int64_t ldx, 
 /* The fused layer over that base: y[t] = the product of x[t], quantized in groups of
  * 128 columns with scales of the same type, with W0 (by 8-bit matrix instructions, as a bf16
  * result above), + scale_s (x[t] A_s) B_s from x as given; overwriting y for every token of
- * the plan.  x, y and the adapters are bf16; x and y rows are 16-byte aligned (ldx, ldy multiples of 8 elements), d_in <= 2^30; W0
- * and w_scales as W above.  Needs ws_bytes >= lora_workspace_bytes(LORA_OP_FUSED_BLOCK, T, d_in,
+ * the plan.  x, y and the adapters are bf16; x and y rows are 16-byte aligned (ldx, ldy
+ * multiples of 8 elements), d_in <= 2^30; W0 and w_scales as W above.  Needs ws_bytes >= lora_workspace_bytes(LORA_OP_FUSED_BLOCK, T, d_in,
  * d_out, max_rank).  Capturable; calls that share a workspace must be ordered on one
  * stream.
  * Errors: as lora_fused_linear_e4m3. */

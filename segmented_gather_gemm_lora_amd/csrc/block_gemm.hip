@@ -34,10 +34,10 @@
 // slot u ^ (r % 8), so that those 8 rows cover all banks.  It writes fp32 sums (few tiles are
 // split along d_out), which the gradient's last launch adds, with u A.
 //
-// What bounds it: a stage's loads.  4096 rows, 4096 -> 14336, E8M0 scales: 240 us (2.0
+// What bounds it: a stage's loads.  4096 rows, 4096 -> 14336, E8M0 scales: 236 us (2.0
 // PFLOP/s), the matrix units busy 44% of the cycles, no LDS conflicts; 64 KB a stage come
-// from the L2 while the stage before is multiplied, and LDS holds two.  fp32 scales: 330
-// us, the fmas beside the matrix instructions.
+// from the L2 while the stage before is multiplied, and LDS holds two.  fp32 scales: 265
+// us, with fresh results and four fmas for each matrix instruction.
 #include "device.h"
 #include "internal.h"
 
@@ -553,7 +553,8 @@ template <class S, bool E8, Form F> struct Tile {
     };
     // W's scales of the 64 stages from kt, one a lane.  A scalar load in each
     // stage would make every wait for LDS in it a wait for that load too (they return out of
-    // order): fp32 results of 65 x 1024, summed axis 4096, 53 -> 42 us; one row, 12288 columns, 12.5 -> 11.1.
+    // order): fp32 results of 65 x 1024, summed axis 4096, took 53 us with them and 42 without (27.5 since codes
+    // are widened in one instruction), one row of 12288 columns 12.5 and 11.1.
     __device__ __forceinline__ WScales wscales(int kt) const
     {
         return wscales_at<E8, F>(a.sw, sw0 + (kt + lane < k1 ? kt + lane : k1 - 1) * sw1);
@@ -704,7 +705,7 @@ void block_gemm_kernel(BlockArgs a)
 // block are whole 128-byte lines), with 8 KB of W a wave on the way: 64 KB a CU, which
 // is what HBM's latency takes.  The waves' sums meet in LDS.  x's codes (at most 64 rows) are
 // read by every workgroup from L2; TN grows with the columns, so that there are about 256.
-// 4096 -> 4096: 1 row 5.3 us (3.2 TB/s), 16 6.7, 32 8.7, 64 12.4: 64 rows' codes are 64 MB from the L2.
+// 4096 -> 4096, fp32 scales: 1 row 5.8 us (2.9 TB/s), 16 6.7, 32 8.6, 64 12.3: 64 rows' codes are 64 MB from the L2.
 constexpr int kFew = 64;
 constexpr int kMaxSlices = 4; // of the shrink
 constexpr int kFewWaves = 8;
@@ -1038,8 +1039,8 @@ template <class S, Form F> int go(hipStream_t s, BlockArgs &a, bool e8, int spli
     a.tiles_n = (a.n + S::kBN - 1) / S::kBN;
     const int64_t tiles = int64_t(a.tiles_m) * a.tiles_n * splits;
     // Where whole rounds of workgroups (one on a CU) leave at most half a round of tiles, those
-    // are halves of 128 columns (summed axis 4096, fp32 scales / E8M0, us: 4096 x 4352 128 -> 113 / 115 -> 104,
-    // 2304 x 8192 130 -> 115 / 112 -> 108, 4096 x 14336 340 -> 330 / 265 -> 259).
+    // are halves of 128 columns (summed axis 4096, fp32 scales / E8M0, us: 4096 x 4352 119 -> 100 / 103 -> 89,
+    // 2304 x 8192 119 -> 100 / 104 -> 89, 4096 x 14336 280 -> 265 / 248 -> 236).
     const int rest = S::kHalved && tiles > 256 && splits == 1 && tiles % 256 <= 128 ? int(tiles % 256) : 0;
     a.whole = int(tiles) - rest;
     const dim3 grid{unsigned(tiles + rest)}, block(S::kThreads);
@@ -1057,11 +1058,11 @@ template <class S> int64_t tiles_of(int32_t T, int32_t n) { return (int64_t(T) +
 // and Small 0.9 and 0.8 with two workgroups on a CU), so the smallest tile whose workgroups
 // run all at once is taken, two of them on a CU, and the largest where none does.  Summed
 // axis 4096, rows x columns, us of Small / Medium / Large:
-//    128 x  4096   17 / 26 / 51      517 x 12288   58 /  40 /  62     4096 x 4096  131 /  97 /  80
-//   1024 x  4096   28 / 30 / 57     1024 x 12288   90 /  73 /  69    2304 x 12288    - / 171 / 160
+//    128 x  4096   17 / 27 / 53      517 x 12288   52 /  41 /  59     4096 x 4096  108 /  83 /  71
+//   1024 x  4096   28 / 29 / 56     1024 x 12288   79 /  64 /  62    2304 x 12288  186 / 151 / 136
 // An fp32 result takes four times the matrix instructions and widens each code that it reads, which
 // larger tiles do less often; Large ones do not fit the registers.  Small / Medium, 517 x 1531 (summed axis 1008)
-// 12 / 16, 517 x 4096 61 / 50, 1024 x 4096 67 / 60.
+// 13 / 21, 517 x 4096 44 / 42, 1024 x 4096 47 / 45.
 enum Size { kSmall, kMedium, kLarge };
 inline Size size_of(int32_t T, int32_t n, bool f32)
 {
